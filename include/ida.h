@@ -1,5 +1,6 @@
 /*
- * ida.h -- C ABI of the GB300 (sm_103a) Interdomain Attention token mixer.
+ * ida.h -- C ABI of the GB300 (sm_103a) Interdomain Attention token mixer, and of the
+ * selective mixer and the residual pre-norm that go with it in a decoder.
  *
  * The operation is the token mixer of "Interdomain Attention: Beyond
  * Token-Level Key-Value Memory" (arXiv 2605.24330) in its scalable form, as
@@ -37,8 +38,8 @@
  *   - Kernels never trap.  A device-side fault detected by a kernel (e.g. a
  *     bounded wait that ran out) is recorded in a device error word and
  *     returned as IDA_ERR_DEVICE by the next call (or by ida_device_error).
- *   - Outputs must not alias inputs.
- *   - Supported: 8 <= R,d <= 256 with R % 8 == 0 and d % 8 == 0,
+ *   - Outputs must not alias inputs, but where a call says so.
+ *   - Supported by the mixer's own calls: 8 <= R,d <= 256 with R % 8 == 0 and d % 8 == 0,
  *     1 <= M <= 128, 1 <= W <= 4.  Other shapes return IDA_ERR_UNSUPPORTED.
  */
 #ifndef IDA_H
@@ -369,6 +370,131 @@ IDA_API ida_status ida_forward_ideal(const void *q, const void *k, const void *v
 IDA_API ida_status ida_rope(void *q, void *k, int B, int N, int H, int R,
                             int pos0, float base, int dtype,
                             ida_stream_t stream);
+
+/*
+ * The selective mixer.  (Beyond the pages: the input-dependent sibling of the mixer's
+ * recurrence, for layers of the same decoder.)  Per row, head h of H and group
+ * g = h / (H / G) of G, with a state X [M][d] in fp32:
+ *   [x_t | b_t | c_t] = SiLU(conv_b + causal depthwise conv of width W)     ida_ssm_conv
+ *   D_t = softplus(dt_t + dt_bias_h),  a_t = exp(-exp(a_log_h) D_t),
+ *   X_t = a_t X_{t-1} + D_t b_t x_t^T,  y_t = X_t^T c_t + D_h x_t            ida_ssm_scan
+ * ida_ssm_conv and ida_ssm_scan run a prompt, ida_ssm_step one further position of both,
+ * and the two backward calls give the gradients of a loss for training.
+ *
+ * Layouts.  The C = H d + 2 G M convolved channels of a position lie in one row,
+ * [x (H d) | b (G M) | c (G M)].  Inputs are rows inside wider ones (a slice of a
+ * projection's output): position t of row r starts ld elements behind the one before it,
+ * (r N + t) ld elements behind the pointer.  x, b, c and the convolution's rows start on
+ * 16-byte boundaries and their strides are multiples of 8; dt needs its element's alignment
+ * only.  y, out and dout are dense.
+ *   a_log, dt_bias, D  [H] float;  conv_w [C, W] (tap W-1 on the current position),
+ *   conv_b [C] float;  scan states [B, H, M, d] float;  conv states [B, W-1, C] float, the
+ *   raw rows of the last W-1 positions, oldest first (zero before the first position).
+ * Supported: d a multiple of 8 up to 256, M a multiple of 8 up to 128, G dividing H, W <= 4,
+ * B*H <= 2^24, B*N <= 2^28.  States, sums and gradients of parameters are fp32 for both
+ * dtypes.  Non-finite inputs make the outputs of their own row and head (the row and group's
+ * heads for b and c) unspecified, earlier positions included; no others.
+ */
+
+/*
+ * The convolution with SiLU over N positions of B rows of C channels (C % 8 == 0, any C up to
+ * 2^20; the C above for the mixer).  x rows of stride ldx, out [B, N, C] dtype.  state_in
+ * (NULL: zero rows) and final_state (NULL: not wanted) must not overlap.  N == 0 hands the
+ * state on.
+ */
+IDA_API ida_status ida_ssm_conv(const void *x, const float *conv_w, const float *conv_b, const float *state_in,
+                        void *out, float *final_state, int B, int N, int C, long long ldx,
+                        int dtype, int W, ida_stream_t stream);
+
+/*
+ * Gradients of ida_ssm_conv from a zero state, given dout [B, N, C]: dx (rows of stride lddx),
+ * dconv_w [C, W] and dconv_b [C] (written, not accumulated; zero when B*N == 0).  The
+ * workspace is required when B*N > 0.  Deterministic.
+ */
+IDA_API ida_status ida_ssm_conv_backward(const void *x, const void *dout, const float *conv_w, const float *conv_b,
+                                 void *dx, float *dconv_w, float *dconv_b, int B, int N, int C,
+                                 long long ldx, long long lddx, int dtype, int W, void *workspace,
+                                 size_t workspace_bytes, ida_stream_t stream);
+
+/* Workspace bytes of ida_ssm_conv_backward (0 for invalid sizes or no positions); host arithmetic. */
+IDA_API size_t ida_ssm_conv_backward_workspace_bytes(int B, int N, int C, int W);
+
+/*
+ * The scan over N positions: x [B, N, H, d] (rows of stride ldx), b and c [B, N, G, M]
+ * (strides ldb and ldc), dt [B, N, H] (stride lddt), y [B, N, H, d] dense.  state_in (NULL: zero) and
+ * final_state (NULL: not wanted) must not overlap.  workspace as in ida_forward_ws: with at
+ * least ida_ssm_scan_workspace_bytes(...) bytes a sequence is split across SMs, with less (or
+ * NULL) it is not; results differ by rounding only.  N == 0 hands the state on.
+ */
+IDA_API ida_status ida_ssm_scan(const void *x, const void *b, const void *c, const void *dt, const float *a_log,
+                        const float *dt_bias, const float *D, const float *state_in, void *y,
+                        float *final_state, int B, int H, int N, int d, int G, int M,
+                        long long ldx, long long ldb, long long ldc, long long lddt, int dtype, void *workspace,
+                        size_t workspace_bytes, ida_stream_t stream);
+
+/* Workspace bytes that let ida_ssm_scan split sequences on the current device; 0: no split applies. */
+IDA_API size_t ida_ssm_scan_workspace_bytes(int B, int H, int N, int d, int G, int M, int dtype);
+
+/*
+ * Gradients of ida_ssm_scan from a zero state, given dy [B, N, H, d] dense: dx, db, dc, ddt in
+ * dtype with row strides lddx, lddb, lddc and ldddt, db and dc summed over the heads of a
+ * group; da_log, ddt_bias, dD [H] float, summed over rows and positions (written; zero when
+ * B*N == 0).  The workspace is required when B*N > 0.  Deterministic.
+ */
+IDA_API ida_status ida_ssm_scan_backward(const void *x, const void *b, const void *c, const void *dt,
+                                 const float *a_log, const float *dt_bias, const float *D,
+                                 const void *dy, void *dx, void *db, void *dc, void *ddt,
+                                 float *da_log, float *ddt_bias, float *dD, int B, int H, int N,
+                                 int d, int G, int M, long long ldx, long long ldb,
+                                 long long ldc, long long lddt, long long lddx,
+                                 long long lddb, long long lddc, long long ldddt,
+                                 int dtype, void *workspace,
+                                 size_t workspace_bytes, ida_stream_t stream);
+
+/* Workspace bytes of ida_ssm_scan_backward (0 for invalid sizes or no positions); host arithmetic. */
+IDA_API size_t ida_ssm_scan_backward_workspace_bytes(int B, int H, int N, int d, int G, int M, int dtype);
+
+/*
+ * One position of conv and scan: xbc [B, C] raw rows (stride ldx), dt [B, H] (stride lddt),
+ * conv_state (unused when W == 1) and state read and updated in place, y [B, H, d] dtype.  The
+ * convolved values are not rounded between the two.
+ */
+IDA_API ida_status ida_ssm_step(const void *xbc, const void *dt, const float *conv_w, const float *conv_b,
+                        const float *a_log, const float *dt_bias, const float *D,
+                        float *conv_state, float *state, void *y, int B, int H, int d, int G,
+                        int M, long long ldx, long long lddt, int dtype, int W,
+                        ida_stream_t stream);
+
+/*
+ * Root-mean-square norm of the residual stream, the pre-norm of the decoder the pages embed the
+ * mixer in ("Interdomain Attention: Beyond Token-Level Key-Value Memory", German technical
+ * summary, "Skalierbare Implementierung", "Architektur").  Per row of D channels:
+ *   r = x + residual, rounded to dtype (x itself without one),  y = r / sqrt(mean r^2 + eps) * w.
+ *   x, residual (NULL: none) [rows, D] dtype;  w [D] float;
+ *   res_out   NULL, or [rows, D] dtype: receives r; may be x or residual itself;
+ *   out       [rows, D] dtype: receives y (NULL allowed when group > 0);
+ *   group     0, or the channels that share a scale: 32, 64, 128 (dividing D) or D.  Then
+ *             out_e4m3 [rows, D] receives y / scale in e4m3 (round to nearest even, saturating)
+ *             and scale [rows, D / group] float max |y| / 448 of the group (1 if all are zero).
+ * Supported: 8 <= D <= 8192, D % 8 == 0.  Arithmetic in fp32.
+ */
+IDA_API ida_status ida_rmsnorm(const void *x, const void *residual, const float *w, void *res_out, void *out,
+                       void *out_e4m3, float *scale, int rows, int D, int group, float eps,
+                       int dtype, ida_stream_t stream);
+
+/*
+ * Gradients of ida_rmsnorm's y: r [rows, D] the normalised rows (res_out, or x without a
+ * residual), dy [rows, D], dres NULL or [rows, D] (what reaches r from elsewhere); dx [rows, D]
+ * dtype, the gradient of x and of residual alike, dres included; dw [D] float, summed over the
+ * rows (zero when rows == 0).  The workspace is required when rows > 0.  dx may be dy or dres
+ * itself.  Deterministic.
+ */
+IDA_API ida_status ida_rmsnorm_backward(const void *r, const float *w, const void *dy, const void *dres, void *dx,
+                                float *dw, int rows, int D, float eps, int dtype, void *workspace,
+                                size_t workspace_bytes, ida_stream_t stream);
+
+/* Workspace bytes of ida_rmsnorm_backward (0 for invalid sizes or no rows); host arithmetic. */
+IDA_API size_t ida_rmsnorm_backward_workspace_bytes(int rows, int D);
 
 /*
  * Self-test of the failure reporting (no counterpart in the paper: a property

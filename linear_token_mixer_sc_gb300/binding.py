@@ -7,6 +7,7 @@ if the library is missing or a call fails, an exception is raised.
 from __future__ import annotations
 
 import ctypes
+import functools
 import threading
 from pathlib import Path
 
@@ -23,7 +24,10 @@ IDA_PATH_SEQUENTIAL = 256
 EXPORTED = ("ida_state_floats", "ida_forward", "ida_forward_ws", "ida_forward_from", "ida_forward_workspace_bytes",
             "ida_forward_noalloc", "ida_decode_step", "ida_device_error", "ida_status_str",
             "ida_last_error", "ida_selftest_bounded_wait", "ida_backward", "ida_backward_workspace_bytes",
-            "ida_forward_ideal", "ida_rope", "ida_forward_host", "ida_forward_host_staging_bytes")
+            "ida_forward_ideal", "ida_rope", "ida_forward_host", "ida_forward_host_staging_bytes",
+            "ida_ssm_conv", "ida_ssm_conv_backward", "ida_ssm_conv_backward_workspace_bytes", "ida_ssm_scan",
+            "ida_ssm_scan_workspace_bytes", "ida_ssm_scan_backward", "ida_ssm_scan_backward_workspace_bytes",
+            "ida_ssm_step", "ida_rmsnorm", "ida_rmsnorm_backward", "ida_rmsnorm_backward_workspace_bytes")
 
 _lock = threading.Lock()
 _lib = None
@@ -79,6 +83,21 @@ def load() -> ctypes.CDLL:
             L.ida_forward_ideal.argtypes = [_vp, _vp, _vp, _fp, _fp, _fp, _vp, _i, _i, _i, _i, _i, _i, _i, _i, _vp]
             L.ida_rope.restype = _i
             L.ida_rope.argtypes = [_vp, _vp, _i, _i, _i, _i, _i, ctypes.c_float, _i, _vp]
+            ll, sz = ctypes.c_longlong, ctypes.c_size_t
+            for name, args in (
+                    ("ida_ssm_conv", [_vp] * 6 + [_i] * 3 + [ll] + [_i] * 2 + [_vp]),
+                    ("ida_ssm_conv_backward", [_vp] * 7 + [_i] * 3 + [ll] * 2 + [_i] * 2 + [_vp, sz, _vp]),
+                    ("ida_ssm_scan", [_vp] * 10 + [_i] * 6 + [ll] * 4 + [_i, _vp, sz, _vp]),
+                    ("ida_ssm_scan_backward", [_vp] * 15 + [_i] * 6 + [ll] * 8 + [_i, _vp, sz, _vp]),
+                    ("ida_ssm_step", [_vp] * 10 + [_i] * 5 + [ll] * 2 + [_i] * 2 + [_vp]),
+                    ("ida_rmsnorm", [_vp] * 7 + [_i] * 3 + [ctypes.c_float, _i, _vp]),
+                    ("ida_rmsnorm_backward", [_vp] * 6 + [_i] * 2 + [ctypes.c_float, _i, _vp, sz, _vp])):
+                getattr(L, name).restype = _i
+                getattr(L, name).argtypes = args
+            for name, n in (("ida_ssm_conv_backward_workspace_bytes", 4), ("ida_ssm_scan_workspace_bytes", 7),
+                            ("ida_ssm_scan_backward_workspace_bytes", 7), ("ida_rmsnorm_backward_workspace_bytes", 2)):
+                getattr(L, name).restype = sz
+                getattr(L, name).argtypes = [_i] * n
             L.ida_selftest_bounded_wait.restype = _i
             L.ida_selftest_bounded_wait.argtypes = [ctypes.c_longlong, _vp]
             L.ida_device_error.restype = _i
@@ -398,6 +417,301 @@ def ida_rope(q: torch.Tensor, k: torch.Tensor | None = None, pos0: int = 0, base
     B, N, H, R = q.shape
     st = load().ida_rope(_p(q), _p(k), B, N, H, R, int(pos0), float(base), _dtype_code(q), _stream_handle(stream))
     _check(st, "ida_rope")
+
+
+# ---- the selective mixer and the residual pre-norm --------------------------------------------
+
+def _placed(fn):
+    """Run ``fn`` with its first tensor's device and the given stream current, so that what it
+    allocates belongs to the stream its kernels run on."""
+    @functools.wraps(fn)
+    def call(first, *args, stream=None, **kw):
+        if not first.is_cuda:
+            raise ValueError(f"{fn.__name__}: expected CUDA tensors")
+        dev = first.get_device()
+        if stream is not None:
+            if stream.device_index != dev:
+                raise ValueError(f"{fn.__name__}: the stream is on another device than the tensors")
+            with torch.cuda.stream(stream):
+                return fn(first, *args, **kw)
+        if dev != torch.cuda.current_device():
+            with torch.cuda.device(dev):
+                return fn(first, *args, **kw)
+        return fn(first, *args, **kw)
+    return call
+
+
+def _dense(name: str, t: torch.Tensor, shape, dtype, dev: int) -> int:
+    """The address of a contiguous tensor of this shape, dtype and device."""
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.get_device() != dev or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous and on the inputs' CUDA device")
+    return t.data_ptr()
+
+
+def _rows(name: str, t: torch.Tensor, shape, dtype, dev: int, lead: int):
+    """(address, row stride) of a tensor whose last dimensions are dense rows and whose ``lead``
+    first ones (1 or 2) count rows at one stride."""
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} must be on the inputs' CUDA device")
+    strides, row = t.stride(), 1
+    for i in range(len(shape) - 1, lead - 1, -1):
+        if shape[i] > 1 and strides[i] != row and t.numel():
+            raise ValueError(f"the rows of {name} must be dense")
+        row *= shape[i]
+    ld = (row + 7) // 8 * 8  # a single row has no stride
+    n = shape[lead - 1]
+    if not t.numel():
+        return t.data_ptr(), ld
+    if lead == 2 and n > 1:
+        ld = strides[1]
+        if shape[0] > 1 and strides[0] != n * ld:
+            raise ValueError(f"the rows of {name} must lie at one stride")
+    elif shape[0] > 1:
+        ld = strides[0]
+    return t.data_ptr(), ld
+
+
+def _raw_stream() -> int:
+    return torch.cuda.current_stream().cuda_stream
+
+
+def _work_buffer(given: torch.Tensor | None, nbytes: int, dev: int):
+    """(tensor kept alive, address, bytes) of the given workspace or of a new one."""
+    if given is None:
+        given = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+    elif given.get_device() != dev or not given.is_contiguous():
+        raise ValueError("workspace must be a contiguous tensor on the inputs' CUDA device")
+    return given, given.data_ptr(), given.numel() * given.element_size()
+
+
+def ida_ssm_conv_backward_workspace_bytes(B: int, N: int, C: int, W: int) -> int:
+    return int(load().ida_ssm_conv_backward_workspace_bytes(B, N, C, W))
+
+
+def ida_ssm_scan_workspace_bytes(B: int, H: int, N: int, d: int, G: int, M: int, dtype: int) -> int:
+    return int(load().ida_ssm_scan_workspace_bytes(B, H, N, d, G, M, dtype))
+
+
+def ida_ssm_scan_backward_workspace_bytes(B: int, H: int, N: int, d: int, G: int, M: int, dtype: int) -> int:
+    return int(load().ida_ssm_scan_backward_workspace_bytes(B, H, N, d, G, M, dtype))
+
+
+def ida_rmsnorm_backward_workspace_bytes(rows: int, D: int) -> int:
+    return int(load().ida_rmsnorm_backward_workspace_bytes(rows, D))
+
+
+@_placed
+def ida_ssm_conv(x: torch.Tensor, conv_w: torch.Tensor, conv_b: torch.Tensor, state_in: torch.Tensor | None = None,
+                 final_state: torch.Tensor | bool | None = None, out: torch.Tensor | None = None):
+    """Short causal convolution and SiLU of the selective mixer.  x [B,N,C] (a slice of wider rows
+    is taken as it is), conv_w [C,W] and conv_b [C] float32; ``state_in`` [B,W-1,C] float32 or None
+    (zero); ``final_state``: a tensor to fill, True to allocate one, or None.
+    Returns (out [B,N,C], final_state)."""
+    dt, dev = _dtype_code(x), x.get_device()
+    B, N, C = x.shape
+    W = conv_w.shape[1]
+    xp, ldx = _rows("x", x, x.shape, x.dtype, dev, 2)
+    if out is None:
+        out = torch.empty((B, N, C), dtype=x.dtype, device=x.device)
+    if final_state is True:
+        final_state = torch.empty((B, W - 1, C), dtype=torch.float32, device=x.device)
+    elif final_state is False:
+        final_state = None
+    S, f32 = (B, W - 1, C), torch.float32
+    st = load().ida_ssm_conv(xp, _dense("conv_w", conv_w, (C, W), f32, dev), _dense("conv_b", conv_b, (C,), f32, dev),
+                             None if state_in is None else _dense("state_in", state_in, S, f32, dev),
+                             _dense("out", out, x.shape, x.dtype, dev),
+                             None if final_state is None else _dense("final_state", final_state, S, f32, dev),
+                             B, N, C, ldx, dt, W, _raw_stream())
+    _check(st, "ida_ssm_conv")
+    return out, final_state
+
+
+@_placed
+def ida_ssm_conv_backward(x: torch.Tensor, dout: torch.Tensor, conv_w: torch.Tensor, conv_b: torch.Tensor,
+                          dx: torch.Tensor | None = None, workspace: torch.Tensor | None = None) -> dict:
+    """Gradients of ``ida_ssm_conv`` from a zero state: dict x (written into ``dx`` when given, which
+    may be a slice of wider rows), conv_w, conv_b.  dout [B,N,C] dense.  ``workspace``: a tensor of at
+    least ``ida_ssm_conv_backward_workspace_bytes`` bytes (allocated here when None)."""
+    dt, dev = _dtype_code(x), x.get_device()
+    B, N, C = x.shape
+    W = conv_w.shape[1]
+    f32 = torch.float32
+    xp, ldx = _rows("x", x, x.shape, x.dtype, dev, 2)
+    wp, bp = _dense("conv_w", conv_w, (C, W), f32, dev), _dense("conv_b", conv_b, (C,), f32, dev)
+    dp = _dense("dout", dout, x.shape, x.dtype, dev)
+    if dx is None:
+        dx = torch.empty((B, N, C), dtype=x.dtype, device=x.device)
+    dxp, lddx = _rows("dx", dx, x.shape, x.dtype, dev, 2)
+    dw, db = torch.empty_like(conv_w), torch.empty_like(conv_b)
+    L = load()
+    ws, wsp, n = _work_buffer(workspace, L.ida_ssm_conv_backward_workspace_bytes(B, N, C, W), dev)
+    st = L.ida_ssm_conv_backward(xp, dp, wp, bp, dxp, dw.data_ptr(), db.data_ptr(), B, N, C, ldx, lddx, dt, W, wsp, n,
+                                 _raw_stream())
+    _check(st, "ida_ssm_conv_backward")
+    return {"x": dx, "conv_w": dw, "conv_b": db}
+
+
+def _scan_inputs(x, b, c, dt, params):
+    """Addresses, strides and sizes of the scan's inputs."""
+    dev, f32 = x.get_device(), torch.float32
+    B, N, H, d = x.shape
+    G, M = b.shape[2:]
+    xp, ldx = _rows("x", x, x.shape, x.dtype, dev, 2)
+    bp, ldb = _rows("b", b, (B, N, G, M), x.dtype, dev, 2)
+    cp, ldc = _rows("c", c, (B, N, G, M), x.dtype, dev, 2)
+    tp, ldt = _rows("dt", dt, (B, N, H), x.dtype, dev, 2)
+    ptrs = [xp, bp, cp, tp] + [_dense(k, params[k], (H,), f32, dev) for k in ("a_log", "dt_bias", "D")]
+    return dev, ptrs, (B, H, N, d, G, M), (ldx, ldb, ldc, ldt)
+
+
+@_placed
+def ida_ssm_scan(x: torch.Tensor, b: torch.Tensor, c: torch.Tensor, dt: torch.Tensor, params: dict,
+                 state_in: torch.Tensor | None = None, final_state: torch.Tensor | bool | None = None,
+                 out: torch.Tensor | None = None, workspace: torch.Tensor | None = None):
+    """Selective scan over a prompt.  x [B,N,H,d], b and c [B,N,G,M], dt [B,N,H] of one dtype, each a
+    slice of wider rows if need be; ``params``: dict of float32 [H] tensors a_log, dt_bias, D.
+    ``state_in`` [B,H,M,d] float32 or None (zero); ``final_state``: a tensor to fill, True to
+    allocate one, or None.  ``workspace``: a tensor of ``ida_ssm_scan_workspace_bytes`` bytes
+    (allocated here when None).  Returns (y [B,N,H,d], final_state)."""
+    code = _dtype_code(x)
+    dev, ptrs, sizes, strides = _scan_inputs(x, b, c, dt, params)
+    B, H, N, d, G, M = sizes
+    if out is None:
+        out = torch.empty((B, N, H, d), dtype=x.dtype, device=x.device)
+    if final_state is True:
+        final_state = torch.empty((B, H, M, d), dtype=torch.float32, device=x.device)
+    elif final_state is False:
+        final_state = None
+    S, f32 = (B, H, M, d), torch.float32
+    sip = None if state_in is None else _dense("state_in", state_in, S, f32, dev)
+    fsp = None if final_state is None else _dense("final_state", final_state, S, f32, dev)
+    L = load()
+    ws, wsp, n = _work_buffer(workspace, L.ida_ssm_scan_workspace_bytes(B, H, N, d, G, M, code)
+                              if workspace is None else 0, dev)
+    st = L.ida_ssm_scan(*ptrs, sip, _dense("out", out, x.shape, x.dtype, dev), fsp, *sizes, *strides, code, wsp, n,
+                        _raw_stream())
+    _check(st, "ida_ssm_scan")
+    return out, final_state
+
+
+@_placed
+def ida_ssm_scan_backward(x: torch.Tensor, b: torch.Tensor, c: torch.Tensor, dt: torch.Tensor, params: dict,
+                          dy: torch.Tensor, workspace: torch.Tensor | None = None) -> dict:
+    """Gradients of ``ida_ssm_scan`` from a zero state, given dy [B,N,H,d]: dict x, b, c, dt (input
+    dtype; x, b and c are slices of the dense rows ``xbc`` [B,N,H d + 2 G M], what
+    ``ida_ssm_conv_backward`` takes as dout) and a_log, dt_bias, D (float32 [H]).  ``workspace``: a
+    tensor of at least ``ida_ssm_scan_backward_workspace_bytes`` bytes (allocated here when None)."""
+    code = _dtype_code(x)
+    dev, ptrs, sizes, strides = _scan_inputs(x, b, c, dt, params)
+    B, H, N, d, G, M = sizes
+    dyp = _dense("dy", dy, x.shape, x.dtype, dev)
+    C = H * d + 2 * G * M
+    xbc = torch.empty((B, N, C), dtype=x.dtype, device=x.device)
+    ddt = torch.empty((B, N, H), dtype=x.dtype, device=x.device)
+    par = torch.empty((3, H), dtype=torch.float32, device=x.device)
+    L = load()
+    ws, wsp, n = _work_buffer(workspace, L.ida_ssm_scan_backward_workspace_bytes(B, H, N, d, G, M, code)
+                              if workspace is None else 0, dev)
+    e, p, pp = xbc.element_size(), xbc.data_ptr(), par.data_ptr()
+    st = L.ida_ssm_scan_backward(*ptrs, dyp, p, p + H * d * e, p + (H * d + G * M) * e, ddt.data_ptr(),
+                                 pp, pp + 4 * H, pp + 8 * H, *sizes, *strides, C, C, C, H, code, wsp, n, _raw_stream())
+    _check(st, "ida_ssm_scan_backward")
+    gx, gb, gc = xbc.split((H * d, G * M, G * M), dim=2)
+    return {"x": gx.view(B, N, H, d), "b": gb.view(B, N, G, M), "c": gc.view(B, N, G, M), "xbc": xbc, "dt": ddt,
+            "a_log": par[0], "dt_bias": par[1], "D": par[2]}
+
+
+@_placed
+def ida_ssm_step(xbc: torch.Tensor, dt: torch.Tensor, params: dict, conv_state: torch.Tensor, state: torch.Tensor,
+                 groups: int, out: torch.Tensor | None = None) -> torch.Tensor:
+    """One position of the selective mixer, convolution included.  xbc [B, H d + 2 G M] raw rows and
+    dt [B,H] of one dtype, each a slice of wider rows if need be; ``params``: dict of float32 tensors
+    conv_w [C,W], conv_b [C], a_log, dt_bias, D [H]; ``conv_state`` [B,W-1,C] and ``state`` [B,H,M,d]
+    float32, updated in place; ``groups``: G.  Returns y [B,H,d]."""
+    code, dev, f32 = _dtype_code(xbc), xbc.get_device(), torch.float32
+    B, C = xbc.shape
+    _, H, M, d = state.shape
+    conv_w = params["conv_w"]
+    W = conv_w.shape[1]
+    if C != H * d + 2 * groups * M:
+        raise ValueError("xbc must have H d + 2 G M channels")
+    xp, ldx = _rows("xbc", xbc, (B, C), xbc.dtype, dev, 1)
+    tp, ldt = _rows("dt", dt, (B, H), xbc.dtype, dev, 1)
+    if out is None:
+        out = torch.empty((B, H, d), dtype=xbc.dtype, device=xbc.device)
+    st = load().ida_ssm_step(xp, tp, _dense("conv_w", conv_w, (C, W), f32, dev),
+                             _dense("conv_b", params["conv_b"], (C,), f32, dev),
+                             *[_dense(k, params[k], (H,), f32, dev) for k in ("a_log", "dt_bias", "D")],
+                             _dense("conv_state", conv_state, (B, W - 1, C), f32, dev),
+                             _dense("state", state, (B, H, M, d), f32, dev),
+                             _dense("out", out, (B, H, d), xbc.dtype, dev), B, H, d, groups, M, ldx, ldt, code, W,
+                             _raw_stream())
+    _check(st, "ida_ssm_step")
+    return out
+
+
+@_placed
+def ida_rmsnorm(x: torch.Tensor, w: torch.Tensor, residual: torch.Tensor | None = None, eps: float = 1e-6,
+                group: int = 0, res_out: torch.Tensor | None = None, out: torch.Tensor | None = None):
+    """Root-mean-square norm of r = x + residual, rows of D channels (any leading dimensions, dense);
+    w [D] float32.  Returns (out, r, q, scale): r is the new residual stream (written into
+    ``res_out`` when given, which may be x or residual; x itself without a residual).  With
+    ``group`` = 0 out is r / rms * w in x's dtype and q, scale are None.  With 32, 64, 128 or D
+    channels per scale, q is the result divided by scale [..., D / group] in float8_e4m3fn and out
+    is None unless passed in."""
+    dt, dev = _dtype_code(x), x.get_device()
+    D = x.shape[-1]
+    rows = x.numel() // D if D else 0
+    xp, wp = _dense("x", x, x.shape, x.dtype, dev), _dense("w", w, (D,), torch.float32, dev)
+    rp = None if residual is None else _dense("residual", residual, x.shape, x.dtype, dev)
+    if residual is not None and res_out is None:
+        res_out = torch.empty_like(x)
+    q = scale = None
+    if group:
+        if group < 0 or D % group:
+            raise ValueError("group must divide the channels")
+        q = torch.empty(x.shape, dtype=torch.float8_e4m3fn, device=x.device)
+        scale = torch.empty((*x.shape[:-1], D // group), dtype=torch.float32, device=x.device)
+    elif out is None:
+        out = torch.empty_like(x)
+    st = load().ida_rmsnorm(xp, rp, wp, None if res_out is None else _dense("res_out", res_out, x.shape, x.dtype, dev),
+                            None if out is None else _dense("out", out, x.shape, x.dtype, dev),
+                            None if q is None else q.data_ptr(), None if scale is None else scale.data_ptr(),
+                            rows, D, group, eps, dt, _raw_stream())
+    _check(st, "ida_rmsnorm")
+    return out, x if res_out is None else res_out, q, scale
+
+
+@_placed
+def ida_rmsnorm_backward(r: torch.Tensor, w: torch.Tensor, dy: torch.Tensor, dres: torch.Tensor | None = None,
+                         eps: float = 1e-6, dx: torch.Tensor | None = None,
+                         workspace: torch.Tensor | None = None) -> dict:
+    """Gradients of ``ida_rmsnorm``'s out, given the r it returned, dy and what reaches r from elsewhere
+    (``dres`` or None): dict x (the gradient of x and of residual alike; into ``dx`` when given) and w."""
+    dt, dev = _dtype_code(r), r.get_device()
+    D = r.shape[-1]
+    rows = r.numel() // D if D else 0
+    rp, wp = _dense("r", r, r.shape, r.dtype, dev), _dense("w", w, (D,), torch.float32, dev)
+    gp = _dense("dy", dy, r.shape, r.dtype, dev)
+    sp = None if dres is None else _dense("dres", dres, r.shape, r.dtype, dev)
+    if dx is None:
+        dx = torch.empty_like(r)
+    dw = torch.empty_like(w)
+    L = load()
+    ws, wsp, n = _work_buffer(workspace, L.ida_rmsnorm_backward_workspace_bytes(rows, D) if workspace is None else 0, dev)
+    st = L.ida_rmsnorm_backward(rp, wp, gp, sp, _dense("dx", dx, r.shape, r.dtype, dev), dw.data_ptr(), rows, D, eps,
+                                dt, wsp, n, _raw_stream())
+    _check(st, "ida_rmsnorm_backward")
+    return {"x": dx, "w": dw}
 
 
 def ida_selftest_bounded_wait(limit_cycles: int, stream=None) -> None:

@@ -1,0 +1,71 @@
+// ida_ssm.cuh -- what the kernels of the selective scan share.
+//
+// Per row b and head h (group g = h / (H / G)), with D_t = softplus(dt_t + dt_bias):
+//   X_t = a_t X_{t-1} + D_t b_t x_t^T,   a_t = exp(-e^{a_log} D_t),   y_t = X_t^T c_t + D x_t,
+// X [M][d] in fp32.
+#pragma once
+
+#include "ida_vec.cuh"
+
+namespace ida {
+
+struct ScanArgs {
+    const void *x, *b, *c, *dt;
+    const float *a_log, *dt_bias, *D, *state_in;
+    void *y;
+    float *final_state;
+    int B, H, N, d, G, M;
+    long long ldx, ldb, ldc, lddt;
+    int seg, segs;      // positions per segment, segments per sequence
+    float *seg_state;   // [B H][segs][M][d]: each segment's last state from zero
+    float *seg_log;     // [B H][segs]: the sum of log a over the segment
+    unsigned *err;
+};
+
+struct ScanBwdArgs {
+    const void *x, *b, *c, *dt, *dy;
+    const float *a_log, *dt_bias, *D;
+    void *dx, *db, *dc, *ddt;
+    float *da_log, *ddt_bias, *dD;
+    int B, H, N, d, G, M;
+    long long ldx, ldb, ldc, lddt, lddx, lddb, lddc, ldddt;
+    int chunk, chunks;
+    float *state0;   // [B H][chunks][M][d]: the state before each chunk
+    float *adj;      // [B H][chunks][M][d]: a Z of the first position behind each chunk
+    float *chunk_log;  // [B H][chunks]: the sum of log a over the chunk
+    float *db_head, *dc_head;  // [B][N][H][M] per head, or NULL when G == H
+    float *part;     // [B H][chunks][4]: the chunk's parts of da_log, ddt_bias, dD
+    unsigned *err;
+};
+
+// Two fp32 in one 64-bit register for the packed fp32x2 instructions (each lane rounded like
+// the scalar instruction).
+typedef unsigned long long ssm_f2;
+__device__ __forceinline__ ssm_f2 ssm_pack(float lo, float hi) {
+    ssm_f2 v;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(lo), "f"(hi));
+    return v;
+}
+__device__ __forceinline__ void ssm_unpack(ssm_f2 v, float &lo, float &hi) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ ssm_f2 ssm_fma(ssm_f2 a, ssm_f2 b, ssm_f2 c) {
+    ssm_f2 d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+__device__ __forceinline__ ssm_f2 ssm_mul(ssm_f2 a, ssm_f2 b) {
+    ssm_f2 d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+
+__device__ __forceinline__ void cp_async16(void *smem, const void *gmem, bool ok) {
+    const uint32_t s = static_cast<uint32_t>(__cvta_generic_to_shared(smem));
+    const int n = ok ? 16 : 0;  // 0: the 16 bytes are zero-filled and nothing is read
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(s), "l"(gmem), "r"(n) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+__device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_group 0;" ::: "memory"); }
+
+}  // namespace ida

@@ -1,0 +1,96 @@
+// ida_vec.cuh -- 16-byte vectors of fp32 or bf16 elements, and what the entry points of the
+// selective mixer and of the pre-norm share on the host side.
+#pragma once
+
+#include <string>
+
+#include "ida_common.cuh"
+
+namespace ida {
+
+// 16 bytes of elements of type E: n elements, unpacked to and packed from fp32.
+template <typename E>
+struct Vec16;
+
+template <>
+struct Vec16<float> {
+    static constexpr int n = 4;
+    static __device__ __forceinline__ void unpack(const uint4 &u, float *x) {
+        x[0] = __uint_as_float(u.x);
+        x[1] = __uint_as_float(u.y);
+        x[2] = __uint_as_float(u.z);
+        x[3] = __uint_as_float(u.w);
+    }
+    static __device__ __forceinline__ uint4 pack(const float *x) {
+        return make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3]));
+    }
+    static __device__ __forceinline__ float round(float x) { return x; }
+};
+
+template <>
+struct Vec16<__nv_bfloat16> {
+    static constexpr int n = 8;
+    static __device__ __forceinline__ void unpack(const uint4 &u, float *x) {
+        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            x[2 * e] = __uint_as_float(w[e] << 16);
+            x[2 * e + 1] = __uint_as_float(w[e] & 0xFFFF0000u);
+        }
+    }
+    static __device__ __forceinline__ uint4 pack(const float *x) {
+        uint32_t w[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const __nv_bfloat162 h = __floats2bfloat162_rn(x[2 * e], x[2 * e + 1]);
+            w[e] = *reinterpret_cast<const uint32_t *>(&h);
+        }
+        return make_uint4(w[0], w[1], w[2], w[3]);
+    }
+    static __device__ __forceinline__ float round(float x) { return __bfloat162float(__float2bfloat16_rn(x)); }
+};
+
+__device__ __forceinline__ float to_float(float x) { return x; }
+__device__ __forceinline__ float to_float(__nv_bfloat16 x) { return __bfloat162float(x); }
+__device__ __forceinline__ void from_float(float *p, float x) { *p = x; }
+__device__ __forceinline__ void from_float(__nv_bfloat16 *p, float x) { *p = __float2bfloat16_rn(x); }
+
+// log(1 + e^z) without overflow; its derivative is 1 / (1 + e^-z).
+__device__ __forceinline__ float softplus(float z) { return fmaxf(z, 0.f) + log1pf(expf(-fabsf(z))); }
+
+// ---- host side ---------------------------------------------------------------------------
+
+ida_status fail_with(ida_status s, const std::string &why);
+ida_status check_call(int d, int R, int M, int W, int dtype, int flags, int *num_sms, std::string &why);
+
+inline bool misaligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) != 0; }
+
+// [a, a + na) and [b, b + nb) share a byte
+inline bool overlap(const void *a, size_t na, const void *b, size_t nb) {
+    const char *pa = static_cast<const char *>(a), *pb = static_cast<const char *>(b);
+    return a && b && pa < pb + nb && pb < pa + na;
+}
+
+// Device set-up of a call whose own arguments have been checked: the number of SMs, and any
+// pending device error.
+inline ida_status device_ready(int *num_sms, std::string &why) {
+    return check_call(8, 8, 1, 1, IDA_F32, 0, num_sms, why);
+}
+
+// Head layout of the selective mixer: H heads of d channels, G groups of M state channels.
+inline ida_status check_ssm(int H, int d, int G, int M, int dtype) {
+    if (d < 1 || M < 1 || G < 1) return fail_with(IDA_ERR_ARG, "d, G and M must be >= 1");
+    if (dtype != IDA_F32 && dtype != IDA_BF16) return fail_with(IDA_ERR_ARG, "dtype must be IDA_F32 or IDA_BF16");
+    if (d < 8 || d > 256 || (d % 8) || M < 8 || M > 128 || (M % 8))
+        return fail_with(IDA_ERR_UNSUPPORTED, "supported: 8 <= d <= 256 and 8 <= M <= 128, multiples of 8");
+    if (H % G) return fail_with(IDA_ERR_ARG, "G must divide H");
+    if (H > (1 << 16)) return fail_with(IDA_ERR_UNSUPPORTED, "H above 2^16");
+    return IDA_OK;
+}
+
+inline ida_status launched(const char *what) {
+    cudaError_t e = cudaGetLastError();
+    return e == cudaSuccess ? IDA_OK : fail_with(IDA_ERR_CUDA, std::string(what) + " launch: " + cudaGetErrorString(e));
+}
+
+}  // namespace ida
