@@ -17,6 +17,9 @@
 namespace ida {
 
 ida_status device_error_word(unsigned **err, std::string &why);
+ida_status launch_ssm_chunk(const ScanArgs &a, cudaStream_t st);
+void ssm_chunk_segments(int B, int H, int N, int d, int M, int num_sms, int &seg, int &segs);
+size_t ssm_chunk_workspace_bytes(int B, int H, int N, int d, int M, int num_sms);
 
 constexpr int SEQ_T = 16;  // positions per tile
 
@@ -289,7 +292,8 @@ size_t ida_ssm_scan_workspace_bytes(int B, int H, int N, int d, int G, int M, in
     if (cudaGetDevice(&dev) != cudaSuccess ||
         cudaDeviceGetAttribute(&num_sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
         return 0;
-    return ssm_seq_workspace_bytes(B, H, N, d, M, num_sms);
+    return dtype == IDA_BF16 ? ssm_chunk_workspace_bytes(B, H, N, d, M, num_sms)
+                             : ssm_seq_workspace_bytes(B, H, N, d, M, num_sms);
 }
 
 ida_status ida_ssm_scan(const void *x, const void *b, const void *c, const void *dt, const float *a_log,
@@ -328,15 +332,20 @@ ida_status ida_ssm_scan(const void *x, const void *b, const void *c, const void 
                   0, 0, nullptr, nullptr, nullptr};
     s = device_error_word(&a.err, why);
     if (s != IDA_OK) return fail_with(s, why);
-    seq_segments(B, H, N, d, num_sms, a.seg, a.segs);
-    if (a.segs > 1 && workspace && workspace_bytes >= ssm_seq_workspace_bytes(B, H, N, d, M, num_sms)) {
+    const bool chunked = dtype == IDA_BF16;
+    if (chunked)
+        ssm_chunk_segments(B, H, N, d, M, num_sms, a.seg, a.segs);
+    else
+        seq_segments(B, H, N, d, num_sms, a.seg, a.segs);
+    const size_t need = (size_t)B * H * a.segs * ((size_t)M * d + 4) * sizeof(float);
+    if (a.segs > 1 && workspace && workspace_bytes >= need) {
         a.seg_state = static_cast<float *>(workspace);
         a.seg_log = a.seg_state + (size_t)B * H * a.segs * M * d;
     } else {
-        a.seg = (N + SEQ_T - 1) / SEQ_T * SEQ_T;
+        a.seg = (N + 127) / 128 * 128;
         a.segs = 1;
     }
-    return dtype == IDA_F32 ? launch_seq_m<float>(a, st) : launch_seq_m<__nv_bfloat16>(a, st);
+    return chunked ? launch_ssm_chunk(a, st) : launch_seq_m<float>(a, st);
 }
 
 }  // extern "C"
