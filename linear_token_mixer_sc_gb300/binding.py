@@ -426,61 +426,62 @@ def _placed(fn):
     allocates belongs to the stream its kernels run on."""
     @functools.wraps(fn)
     def call(first, *args, stream=None, **kw):
-        if not first.is_cuda:
-            raise ValueError(f"{fn.__name__}: expected CUDA tensors")
         dev = first.get_device()
+        if dev < 0:
+            raise ValueError(f"{fn.__name__}: expected CUDA tensors")
         if stream is not None:
             if stream.device_index != dev:
                 raise ValueError(f"{fn.__name__}: the stream is on another device than the tensors")
             with torch.cuda.stream(stream):
                 return fn(first, *args, **kw)
-        if dev != torch.cuda.current_device():
+        if dev != _current_device():
             with torch.cuda.device(dev):
                 return fn(first, *args, **kw)
         return fn(first, *args, **kw)
     return call
 
 
-def _dense(name: str, t: torch.Tensor, shape, dtype, dev: int) -> int:
-    """The address of a contiguous tensor of this shape, dtype and device."""
+# What torch.cuda.current_device() and current_stream().cuda_stream return, without building a
+# Stream object: the calls below are a few microseconds long.
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                      lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+
+
+def _misfit(name: str, t: torch.Tensor, shape, dtype):
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    if t.get_device() != dev or not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous and on the inputs' CUDA device")
+    raise ValueError(f"{name} must be contiguous and on the inputs' CUDA device")
+
+
+def _dense(name: str, t: torch.Tensor, shape, dtype, dev: int) -> int:
+    """The address of a contiguous tensor of this shape, dtype and device."""
+    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous() or t.get_device() != dev:
+        _misfit(name, t, shape, dtype)
     return t.data_ptr()
 
 
 def _rows(name: str, t: torch.Tensor, shape, dtype, dev: int, lead: int):
     """(address, row stride) of a tensor whose last dimensions are dense rows and whose ``lead``
     first ones (1 or 2) count rows at one stride."""
-    if t.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.shape != shape:
-        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    if t.get_device() != dev:
-        raise ValueError(f"{name} must be on the inputs' CUDA device")
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != dev:
+        _misfit(name, t, shape, dtype)
     strides, row = t.stride(), 1
     for i in range(len(shape) - 1, lead - 1, -1):
         if shape[i] > 1 and strides[i] != row and t.numel():
             raise ValueError(f"the rows of {name} must be dense")
         row *= shape[i]
-    ld = (row + 7) // 8 * 8  # a single row has no stride
     n = shape[lead - 1]
-    if not t.numel():
-        return t.data_ptr(), ld
-    if lead == 2 and n > 1:
+    if lead == 2 and n > 1 and t.numel():
         ld = strides[1]
         if shape[0] > 1 and strides[0] != n * ld:
             raise ValueError(f"the rows of {name} must lie at one stride")
-    elif shape[0] > 1:
-        ld = strides[0]
-    return t.data_ptr(), ld
-
-
-def _raw_stream() -> int:
-    return torch.cuda.current_stream().cuda_stream
+        return t.data_ptr(), ld
+    if shape[0] > 1 and t.numel():
+        return t.data_ptr(), strides[0]
+    return t.data_ptr(), (row + 7) // 8 * 8  # a single row has no stride
 
 
 def _work_buffer(given: torch.Tensor | None, nbytes: int, dev: int):
@@ -530,7 +531,7 @@ def ida_ssm_conv(x: torch.Tensor, conv_w: torch.Tensor, conv_b: torch.Tensor, st
                              None if state_in is None else _dense("state_in", state_in, S, f32, dev),
                              _dense("out", out, x.shape, x.dtype, dev),
                              None if final_state is None else _dense("final_state", final_state, S, f32, dev),
-                             B, N, C, ldx, dt, W, _raw_stream())
+                             B, N, C, ldx, dt, W, _raw_stream(dev))
     _check(st, "ida_ssm_conv")
     return out, final_state
 
@@ -555,7 +556,7 @@ def ida_ssm_conv_backward(x: torch.Tensor, dout: torch.Tensor, conv_w: torch.Ten
     L = load()
     ws, wsp, n = _work_buffer(workspace, L.ida_ssm_conv_backward_workspace_bytes(B, N, C, W), dev)
     st = L.ida_ssm_conv_backward(xp, dp, wp, bp, dxp, dw.data_ptr(), db.data_ptr(), B, N, C, ldx, lddx, dt, W, wsp, n,
-                                 _raw_stream())
+                                 _raw_stream(dev))
     _check(st, "ida_ssm_conv_backward")
     return {"x": dx, "conv_w": dw, "conv_b": db}
 
@@ -598,7 +599,7 @@ def ida_ssm_scan(x: torch.Tensor, b: torch.Tensor, c: torch.Tensor, dt: torch.Te
     ws, wsp, n = _work_buffer(workspace, L.ida_ssm_scan_workspace_bytes(B, H, N, d, G, M, code)
                               if workspace is None else 0, dev)
     st = L.ida_ssm_scan(*ptrs, sip, _dense("out", out, x.shape, x.dtype, dev), fsp, *sizes, *strides, code, wsp, n,
-                        _raw_stream())
+                        _raw_stream(dev))
     _check(st, "ida_ssm_scan")
     return out, final_state
 
@@ -623,7 +624,7 @@ def ida_ssm_scan_backward(x: torch.Tensor, b: torch.Tensor, c: torch.Tensor, dt:
                               if workspace is None else 0, dev)
     e, p, pp = xbc.element_size(), xbc.data_ptr(), par.data_ptr()
     st = L.ida_ssm_scan_backward(*ptrs, dyp, p, p + H * d * e, p + (H * d + G * M) * e, ddt.data_ptr(),
-                                 pp, pp + 4 * H, pp + 8 * H, *sizes, *strides, C, C, C, H, code, wsp, n, _raw_stream())
+                                 pp, pp + 4 * H, pp + 8 * H, *sizes, *strides, C, C, C, H, code, wsp, n, _raw_stream(dev))
     _check(st, "ida_ssm_scan_backward")
     gx, gb, gc = xbc.split((H * d, G * M, G * M), dim=2)
     return {"x": gx.view(B, N, H, d), "b": gb.view(B, N, G, M), "c": gc.view(B, N, G, M), "xbc": xbc, "dt": ddt,
@@ -654,7 +655,7 @@ def ida_ssm_step(xbc: torch.Tensor, dt: torch.Tensor, params: dict, conv_state: 
                              _dense("conv_state", conv_state, (B, W - 1, C), f32, dev),
                              _dense("state", state, (B, H, M, d), f32, dev),
                              _dense("out", out, (B, H, d), xbc.dtype, dev), B, H, d, groups, M, ldx, ldt, code, W,
-                             _raw_stream())
+                             _raw_stream(dev))
     _check(st, "ida_ssm_step")
     return out
 
@@ -686,7 +687,7 @@ def ida_rmsnorm(x: torch.Tensor, w: torch.Tensor, residual: torch.Tensor | None 
     st = load().ida_rmsnorm(xp, rp, wp, None if res_out is None else _dense("res_out", res_out, x.shape, x.dtype, dev),
                             None if out is None else _dense("out", out, x.shape, x.dtype, dev),
                             None if q is None else q.data_ptr(), None if scale is None else scale.data_ptr(),
-                            rows, D, group, eps, dt, _raw_stream())
+                            rows, D, group, eps, dt, _raw_stream(dev))
     _check(st, "ida_rmsnorm")
     return out, x if res_out is None else res_out, q, scale
 
@@ -709,7 +710,7 @@ def ida_rmsnorm_backward(r: torch.Tensor, w: torch.Tensor, dy: torch.Tensor, dre
     L = load()
     ws, wsp, n = _work_buffer(workspace, L.ida_rmsnorm_backward_workspace_bytes(rows, D) if workspace is None else 0, dev)
     st = L.ida_rmsnorm_backward(rp, wp, gp, sp, _dense("dx", dx, r.shape, r.dtype, dev), dw.data_ptr(), rows, D, eps,
-                                dt, wsp, n, _raw_stream())
+                                dt, wsp, n, _raw_stream(dev))
     _check(st, "ida_rmsnorm_backward")
     return {"x": dx, "w": dw}
 

@@ -287,25 +287,18 @@ __global__ void __launch_bounds__(512) rmsnorm_bwd_kernel(NormBwdArgs a) {
     }
 }
 
-// out[c] = sum over rows of part[row][c], rows in 8 interleaved parts summed in a fixed order.
-__global__ void __launch_bounds__(256) sum_rows_kernel(const float *part, float *out, int rows, long long C) {
-    __shared__ float s[8][33];
-    const long long c = blockIdx.x * 32LL + threadIdx.x;
+// out[c] = sum over rows of part[row][c], rows in 32 interleaved parts summed in a fixed order.
+__global__ void __launch_bounds__(1024) sum_rows_kernel(const float *part, float *out, int rows, int C) {
+    __shared__ float s[32][33];
+    const int c = blockIdx.x * 32 + threadIdx.x;
     float v = 0.f;
     if (c < C)
-#pragma unroll 8
-        for (int r = threadIdx.y; r < rows; r += 8) v += part[(size_t)r * C + c];
+#pragma unroll 4
+        for (int r = threadIdx.y; r < rows; r += 32) v += __ldcs(part + (size_t)r * C + c);
     s[threadIdx.y][threadIdx.x] = v;
     __syncthreads();
-    if (threadIdx.y == 0 && c < C) {
-#pragma unroll
-        for (int i = 1; i < 8; ++i) v += s[i][threadIdx.x];
-        out[c] = v;
-    }
-}
-
-void launch_sum_rows(const float *part, float *out, int rows, long long C, cudaStream_t st) {
-    sum_rows_kernel<<<(unsigned)((C + 31) / 32), dim3(32, 8), 0, st>>>(part, out, rows, C);
+    v = warp_sum(s[threadIdx.x][threadIdx.y]);  // warp y: the 32 parts of column y
+    if (threadIdx.x == 0 && blockIdx.x * 32 + threadIdx.y < C) out[blockIdx.x * 32 + threadIdx.y] = v;
 }
 
 // Blocks of the backward pass: as many rows per block as its sums of dw are worth, four blocks
@@ -411,7 +404,7 @@ ida_status ida_rmsnorm_backward(const void *r, const float *w, const void *dy, c
     const int blocks = dtype == IDA_F32 ? launch_norm_bwd<float>(a, st) : launch_norm_bwd<__nv_bfloat16>(a, st);
     s = launched("rmsnorm backward");
     if (s != IDA_OK) return s;
-    launch_sum_rows(a.part, dw, blocks, D, st);
+    sum_rows_kernel<<<(unsigned)((D + 31) / 32), dim3(32, 32), 0, st>>>(a.part, dw, blocks, D);
     return launched("rmsnorm weight gradient");
 }
 

@@ -17,6 +17,7 @@ struct ScanArgs {
     int B, H, N, d, G, M;
     long long ldx, ldb, ldc, lddt;
     int seg, segs;      // positions per segment, segments per sequence
+    int state_segs;     // segments whose last state from zero a first launch leaves in seg_state
     float *seg_state;   // [B H][segs][M][d]: each segment's last state from zero
     float *seg_log;     // [B H][segs]: the sum of log a over the segment
     unsigned *err;

@@ -19,7 +19,6 @@ namespace ida {
 ida_status device_error_word(unsigned **err, std::string &why);
 ida_status launch_ssm_chunk(const ScanArgs &a, cudaStream_t st);
 void ssm_chunk_segments(int B, int H, int N, int d, int M, int num_sms, int &seg, int &segs);
-size_t ssm_chunk_workspace_bytes(int B, int H, int N, int d, int M, int num_sms);
 
 constexpr int SEQ_T = 16;  // positions per tile
 
@@ -42,7 +41,7 @@ __global__ void __launch_bounds__(128) scan_seq_kernel(ScanArgs a) {
     extern __shared__ __align__(16) unsigned char smem[];
     const int M = a.M, d = a.d, H = a.H, N = a.N, rep = H / a.G;
     const int nt = blockDim.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, cols = nt;
-    const int slices = (d + cols - 1) / cols, nseg = STATE ? a.segs - 1 : a.segs;
+    const int slices = (d + cols - 1) / cols, nseg = STATE ? a.state_segs : a.segs;
     int id = blockIdx.x;
     const int seg = id % nseg;
     id /= nseg;
@@ -231,11 +230,13 @@ static void seq_segments(int B, int H, int N, int d, int num_sms, int &seg, int 
     segs = (N + seg - 1) / seg;
 }
 
-size_t ssm_seq_workspace_bytes(int B, int H, int N, int d, int M, int num_sms) {
-    int seg, segs;
-    seq_segments(B, H, N, d, num_sms, seg, segs);
-    if (segs < 2) return 0;
-    return (size_t)B * H * segs * ((size_t)M * d + 4) * sizeof(float);
+// The split of a call and the bytes of its segment states.
+static size_t scan_plan(int B, int H, int N, int d, int M, bool chunked, int num_sms, int &seg, int &segs) {
+    if (chunked)
+        ssm_chunk_segments(B, H, N, d, M, num_sms, seg, segs);
+    else
+        seq_segments(B, H, N, d, num_sms, seg, segs);
+    return segs < 2 ? 0 : (size_t)B * H * segs * ((size_t)M * d + 4) * sizeof(float);
 }
 
 template <typename E, int MT>
@@ -248,8 +249,8 @@ static ida_status launch_seq(const ScanArgs &a, cudaStream_t st) {
     if (e == cudaSuccess)
         e = cudaFuncSetAttribute(scan_seq_kernel<E, MT, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return fail_with(IDA_ERR_CUDA, cudaGetErrorString(e));
-    if (a.segs > 1) {
-        scan_seq_kernel<E, MT, true><<<(unsigned)(units * (a.segs - 1)), cols, smem, st>>>(a);
+    if (a.state_segs > 0) {
+        scan_seq_kernel<E, MT, true><<<(unsigned)(units * a.state_segs), cols, smem, st>>>(a);
         const ida_status s = launched("ssm segment states");
         if (s != IDA_OK) return s;
     }
@@ -292,8 +293,8 @@ size_t ida_ssm_scan_workspace_bytes(int B, int H, int N, int d, int G, int M, in
     if (cudaGetDevice(&dev) != cudaSuccess ||
         cudaDeviceGetAttribute(&num_sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
         return 0;
-    return dtype == IDA_BF16 ? ssm_chunk_workspace_bytes(B, H, N, d, M, num_sms)
-                             : ssm_seq_workspace_bytes(B, H, N, d, M, num_sms);
+    int seg, segs;
+    return scan_plan(B, H, N, d, M, dtype == IDA_BF16, num_sms, seg, segs);
 }
 
 ida_status ida_ssm_scan(const void *x, const void *b, const void *c, const void *dt, const float *a_log,
@@ -329,22 +330,20 @@ ida_status ida_ssm_scan(const void *x, const void *b, const void *c, const void 
         return e == cudaSuccess ? IDA_OK : fail_with(IDA_ERR_CUDA, cudaGetErrorString(e));
     }
     ScanArgs a = {x, b, c, dt, a_log, dt_bias, D, state_in, y, final_state, B, H, N, d, G, M, ldx, ldb, ldc, lddt,
-                  0, 0, nullptr, nullptr, nullptr};
+                  0, 0, 0, nullptr, nullptr, nullptr};
     s = device_error_word(&a.err, why);
     if (s != IDA_OK) return fail_with(s, why);
     const bool chunked = dtype == IDA_BF16;
-    if (chunked)
-        ssm_chunk_segments(B, H, N, d, M, num_sms, a.seg, a.segs);
-    else
-        seq_segments(B, H, N, d, num_sms, a.seg, a.segs);
-    const size_t need = (size_t)B * H * a.segs * ((size_t)M * d + 4) * sizeof(float);
-    if (a.segs > 1 && workspace && workspace_bytes >= need) {
+    const size_t need = scan_plan(B, H, N, d, M, chunked, num_sms, a.seg, a.segs);
+    if (need > 0 && workspace && workspace_bytes >= need) {
         a.seg_state = static_cast<float *>(workspace);
         a.seg_log = a.seg_state + (size_t)B * H * a.segs * M * d;
     } else {
         a.seg = (N + 127) / 128 * 128;
         a.segs = 1;
     }
+    // the tensor-core kernel takes a final state from segment states, the other one from its own
+    a.state_segs = chunked && final_state ? a.segs : a.segs - 1;
     return chunked ? launch_ssm_chunk(a, st) : launch_seq_m<float>(a, st);
 }
 
