@@ -19,7 +19,7 @@ struct ScanArgs {
     int seg, segs;      // positions per segment, segments per sequence
     int state_segs;     // segments whose last state from zero a first launch leaves in seg_state
     float *seg_state;   // [B H][segs][M][d]: each segment's last state from zero
-    float *seg_log;     // [B H][segs]: the sum of log a over the segment
+    float *seg_log;     // [B H][segs]: the sum of log a over the segment (of log2 a on the tensor cores)
     unsigned *err;
 };
 
@@ -33,8 +33,8 @@ struct ScanBwdArgs {
     int chunk, chunks;
     float *state0;   // [B H][chunks][M][d]: the state before each chunk
     float *adj;      // [B H][chunks][M][d]: a Z of the first position behind each chunk
-    float *chunk_log;  // [B H][chunks]: the sum of log a over the chunk
-    float *db_head, *dc_head;  // [B][N][H][M] per head, or NULL when G == H
+    float *chunk_log;  // [B H][chunks]: the sum of log2 a over the chunk
+    float *db_head, *dc_head;  // [B][N][H][M] per head, or NULL where nothing is left to sum
     float *part;     // [B H][chunks][4]: the chunk's parts of da_log, ddt_bias, dD
     unsigned *err;
 };

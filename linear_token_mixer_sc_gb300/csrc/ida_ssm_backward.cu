@@ -1,4 +1,5 @@
-// ida_ssm_backward.cu -- the backward pass of the selective scan.
+// ida_ssm_backward.cu -- the backward pass of the selective scan: its entry point, and its kernels on
+// the CUDA cores (fp32 inputs, and the sizes ida_ssm_bwd_tc.cu does not take).
 //
 // With Z_t the adjoint of the state X_t (per row and head; see ida_ssm.cuh for the forward):
 //   Z_t = c_t dy_t^T + a_{t+1} Z_{t+1},
@@ -25,6 +26,9 @@ namespace ida {
 ida_status check_scan(int B, int H, int N, int d, int G, int M, long long ldx, long long ldb, long long ldc,
                       long long lddt, int dtype);
 ida_status device_error_word(unsigned **err, std::string &why);
+int ssm_bwd_tc_splits(int B, int H, int N, int G, int M);
+ida_status launch_bwd_tc_states(const ScanBwdArgs &a, cudaStream_t st);
+ida_status launch_bwd_tc(const ScanBwdArgs &a, int splits, cudaStream_t st);
 
 constexpr int BT = 8;  // positions between two sums across warps
 
@@ -244,7 +248,7 @@ __global__ void __launch_bounds__(256) bwd_chunk_kernel(ScanBwdArgs s) {
         }
     if (!rev && warp == 0) {
         float la = 0.f;
-        const float rate = expf(s.a_log[unit % s.H]);
+        const float rate = expf(s.a_log[unit % s.H]) * 1.4426950408889634f;
         for (int t = lane; t < Q; t += 32) la -= rate * r.delta[t];
         la = warp_sum(la);
         if (lane == 0) s.chunk_log[(size_t)unit * s.chunks + ch] = la;
@@ -276,7 +280,7 @@ __global__ void __launch_bounds__(256) bwd_carry_kernel(ScanBwdArgs s) {
             if (k0 + k < s.chunks) {
                 const int c = rev ? s.chunks - 1 - (k0 + k) : k0 + k;
                 p[(size_t)c * n] = X;
-                const float e = expf(f[k]);
+                const float e = exp2f(f[k]);
                 X = make_float4(fmaf(e, X.x, v[k].x), fmaf(e, X.y, v[k].y), fmaf(e, X.z, v[k].z), fmaf(e, X.w, v[k].w));
             }
     }
@@ -435,18 +439,19 @@ __global__ void __launch_bounds__(256) bwd_main_kernel(ScanBwdArgs s) {
     }
 }
 
-// db and dc of a group: the sum over its heads, in head order.  One thread per four channels.
+// db and dc of a group: the sum over the `n` parts its heads were taken in, in their order.  One
+// thread per four channels.
 template <typename E>
-__global__ void __launch_bounds__(256) bwd_group_kernel(ScanBwdArgs s) {
-    const int rep = s.H / s.G, vpr = s.G * s.M / 4;
+__global__ void __launch_bounds__(256) bwd_group_kernel(ScanBwdArgs s, int n) {
+    const int vpr = s.G * s.M / 4;
     const long long i = (long long)blockIdx.x * 256 + threadIdx.x;
     if (i >= (long long)s.B * s.N * vpr) return;
     const long long row = i / vpr;
     const int v = (int)(i % vpr), g = v / (s.M / 4), m = v % (s.M / 4) * 4;
-    const float *src = (blockIdx.y ? s.dc_head : s.db_head) + ((size_t)row * s.H + (size_t)g * rep) * s.M + m;
+    const float *src = (blockIdx.y ? s.dc_head : s.db_head) + ((size_t)row * s.G + g) * n * s.M + m;
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
-    for (int r = 0; r < rep; ++r) {
+    for (int r = 0; r < n; ++r) {
         const float4 u = __ldcs(reinterpret_cast<const float4 *>(src + (size_t)r * s.M));
         o.x += u.x;
         o.y += u.y;
@@ -496,15 +501,18 @@ static int bwd_chunk_len(int d, int M) {
 }
 
 struct BwdPlan {
-    int chunk, chunks;
+    bool tc;
+    int chunk, chunks, parts;                      // parts: those a group's db and dc are summed from
     size_t state0, adj, log, db, dc, part, total;  // float offsets
 };
-static BwdPlan bwd_plan(int B, int H, int N, int d, int G, int M) {
+static BwdPlan bwd_plan(int B, int H, int N, int d, int G, int M, int dtype) {
     BwdPlan p;
-    p.chunk = bwd_chunk_len(d, M);
+    p.tc = dtype == IDA_BF16 && d <= 128 && M <= 64;
+    p.chunk = p.tc ? 128 : bwd_chunk_len(d, M);
     p.chunks = (N + p.chunk - 1) / p.chunk;
+    p.parts = p.tc ? ssm_bwd_tc_splits(B, H, N, G, M) : H / G;
     const size_t units = (size_t)B * H, states = units * p.chunks * M * d;
-    const size_t heads = G == H ? 0 : (size_t)B * N * H * M;
+    const size_t heads = p.parts == 1 ? 0 : (size_t)B * N * G * p.parts * M;
     p.state0 = 0;
     p.adj = p.state0 + states;
     p.db = p.adj + states;
@@ -513,6 +521,34 @@ static BwdPlan bwd_plan(int B, int H, int N, int d, int G, int M) {
     p.log = p.part + units * p.chunks * 4;
     p.total = p.log + (units * p.chunks + 3) / 4 * 4;
     return p;
+}
+
+// The running sums over the chunks: a launch per 65535 units.
+static ida_status launch_bwd_carry(const ScanBwdArgs &s, cudaStream_t st) {
+    for (int u0 = 0; u0 < s.B * s.H; u0 += 65535) {
+        ScanBwdArgs t = s;
+        t.state0 += (size_t)u0 * s.chunks * s.M * s.d;
+        t.adj += (size_t)u0 * s.chunks * s.M * s.d;
+        t.chunk_log += (size_t)u0 * s.chunks;
+        const int units = s.B * s.H - u0 < 65535 ? s.B * s.H - u0 : 65535;
+        bwd_carry_kernel<<<dim3((s.M * s.d / 4 + 255) / 256, units, 2), 256, 0, st>>>(t);
+        const ida_status r = launched("ssm chunk sums");
+        if (r != IDA_OK) return r;
+    }
+    return IDA_OK;
+}
+
+// The sums over a group's parts and over the chunks.
+template <typename E>
+static ida_status launch_bwd_sums(const ScanBwdArgs &s, int parts, cudaStream_t st) {
+    if (s.db_head) {
+        const long long n = ((long long)s.B * s.N * s.G * s.M / 4 + 255) / 256;
+        bwd_group_kernel<E><<<dim3((unsigned)n, 2), 256, 0, st>>>(s, parts);
+        const ida_status r = launched("ssm group sums");
+        if (r != IDA_OK) return r;
+    }
+    bwd_params_kernel<<<s.H, 128, 0, st>>>(s);
+    return launched("ssm parameter gradients");
 }
 
 template <typename E, int MT>
@@ -526,28 +562,11 @@ static ida_status launch_bwd(const ScanBwdArgs &s, cudaStream_t st) {
     const long long blocks = (long long)s.B * s.H * s.chunks;
     bwd_chunk_kernel<E, MT><<<dim3((unsigned)blocks, 2), cols, smem, st>>>(s);
     ida_status r = launched("ssm chunk states");
+    if (r == IDA_OK) r = launch_bwd_carry(s, st);
     if (r != IDA_OK) return r;
-    for (int u0 = 0; u0 < s.B * s.H; u0 += 65535) {
-        ScanBwdArgs t = s;
-        t.state0 += (size_t)u0 * s.chunks * s.M * s.d;
-        t.adj += (size_t)u0 * s.chunks * s.M * s.d;
-        t.chunk_log += (size_t)u0 * s.chunks;
-        const int units = s.B * s.H - u0 < 65535 ? s.B * s.H - u0 : 65535;
-        bwd_carry_kernel<<<dim3((s.M * s.d / 4 + 255) / 256, units, 2), 256, 0, st>>>(t);
-        r = launched("ssm chunk sums");
-        if (r != IDA_OK) return r;
-    }
     bwd_main_kernel<E, MT><<<(unsigned)blocks, cols, smem, st>>>(s);
     r = launched("ssm scan backward");
-    if (r != IDA_OK) return r;
-    if (s.db_head) {
-        const long long n = ((long long)s.B * s.N * s.G * s.M / 4 + 255) / 256;
-        bwd_group_kernel<E><<<dim3((unsigned)n, 2), 256, 0, st>>>(s);
-        r = launched("ssm group sums");
-        if (r != IDA_OK) return r;
-    }
-    bwd_params_kernel<<<s.H, 128, 0, st>>>(s);
-    return launched("ssm parameter gradients");
+    return r == IDA_OK ? launch_bwd_sums<E>(s, s.H / s.G, st) : r;
 }
 
 template <typename E>
@@ -568,7 +587,7 @@ size_t ida_ssm_scan_backward_workspace_bytes(int B, int H, int N, int d, int G, 
     using namespace ida;
     if (check_scan(B, H, N, d, G, M, (long long)H * d, (long long)G * M, (long long)G * M, H, dtype) != IDA_OK) return 0;
     if ((long long)B * H * N == 0) return 0;
-    return bwd_plan(B, H, N, d, G, M).total * sizeof(float);
+    return bwd_plan(B, H, N, d, G, M, dtype).total * sizeof(float);
 }
 
 ida_status ida_ssm_scan_backward(const void *x, const void *b, const void *c, const void *dt, const float *a_log,
@@ -609,15 +628,19 @@ ida_status ida_ssm_scan_backward(const void *x, const void *b, const void *c, co
         if (e == cudaSuccess) e = cudaMemsetAsync(dD, 0, H * sizeof(float), st);
         return e == cudaSuccess ? IDA_OK : fail_with(IDA_ERR_CUDA, cudaGetErrorString(e));
     }
-    const BwdPlan p = bwd_plan(B, H, N, d, G, M);
+    const BwdPlan p = bwd_plan(B, H, N, d, G, M, dtype);
     if ((long long)B * H * p.chunks > 0x7FFFFFFFLL) return fail_with(IDA_ERR_UNSUPPORTED, "too many positions and heads");
     float *ws = static_cast<float *>(workspace);
     ScanBwdArgs a = {x, b, c, dt, dy, a_log, dt_bias, D, dx, db, dc, ddt, da_log, ddt_bias, dD, B, H, N, d, G, M,
                      ldx, ldb, ldc, lddt, lddx, lddb, lddc, ldddt, p.chunk, p.chunks, ws + p.state0, ws + p.adj, ws + p.log,
-                     G == H ? nullptr : ws + p.db, G == H ? nullptr : ws + p.dc, ws + p.part, nullptr};
+                     p.parts == 1 ? nullptr : ws + p.db, p.parts == 1 ? nullptr : ws + p.dc, ws + p.part, nullptr};
     s = device_error_word(&a.err, why);
     if (s != IDA_OK) return fail_with(s, why);
-    return dtype == IDA_F32 ? launch_bwd_m<float>(a, st) : launch_bwd_m<__nv_bfloat16>(a, st);
+    if (!p.tc) return dtype == IDA_F32 ? launch_bwd_m<float>(a, st) : launch_bwd_m<__nv_bfloat16>(a, st);
+    s = launch_bwd_tc_states(a, st);
+    if (s == IDA_OK) s = launch_bwd_carry(a, st);
+    if (s == IDA_OK) s = launch_bwd_tc(a, p.parts, st);
+    return s == IDA_OK ? launch_bwd_sums<__nv_bfloat16>(a, p.parts, st) : s;
 }
 
 }  // extern "C"

@@ -1,0 +1,574 @@
+// ida_ssm_bwd_tc.cu -- the backward pass of the selective scan on the tcgen05 tensor cores (bf16
+// inputs, d <= 128, M <= 64).
+//
+// Over a chunk of Q = 128 positions, with X_0 the state before it, Z the adjoint that reaches it
+// from behind (a Z of the next position), S_t the running sum of log2 a, W_ts = 2^(S_t - S_s) for
+// t >= s, f_s = 2^(S_Q - S_s), and the transposed products of positions
+//   G [s][t] = b_s . c_t,   E [s][t] = x_s . dy_t          (MMAs, K = M and K = d)
+// the gradients of ida_ssm_backward.cu's header are
+//   dx_s = D dy_s + D_s (sum_t W G dy_t + f_s Z^T b_s)      P = D_s W G (+ D at s = t) as A, dy as B
+//   db_s = D_s (sum_t W E c_t + f_s Z x_s)                  R = D_s W E as A, c as B
+//   dc_t = sum_s R b_s + 2^(S_t) X_0 dy_t                   R^T as A (the same tile read MN-major)
+// and, from the fp32 K_st = D_s W G E (t > s, never rounded, never stored) and the inter-chunk
+// products, the gradient of log a_t, the sum over all pairs (s < t <= u) of positions:
+//   w_t = sum_{s < t <= u} K_su + sum_{u >= t} 2^(S_u) c_u^T X_0 dy_u + sum_{s < t} D_s f_s b_s^T Z x_s
+//         + 2^(S_Q) <Z, X_0>.
+// Its first sum is a running difference of K's row and column sums, the same K in both, added in
+// fp64; the other terms have no differences.  So dt's and the parameters' gradients come out to
+// fp32 rounding although P and R are rounded to bf16 for the MMAs.  What enters w through MMAs is
+// exact in its operands: b, c, x, dy are bf16, X_0 and Z are kept as the sum of three bf16 tiles.
+//
+// Chunks are independent: X_0 and Z of every chunk come from launch_ssm_states (forwards and
+// backwards) and a running sum over the chunks.  One CTA of 512 threads takes the heads of one
+// group (or a part of them) over one chunk: b, c and G once, db and dc added over the heads in TMEM,
+// so that no per-head rows go to memory where a group's heads stay in one CTA.  Per head: E, then
+// K, P and R on the CUDA cores (thread s of a lane quarter has row s; a warp sums K over its 32 rows
+// by recursive halving), then the MMAs of dx, the inter-chunk products (read back, scaled by
+// 2^S or f and added into db and dc) and the rest of db and dc.
+//
+// Waits are bounded as in ida_ssm_chunk.cu.
+#include "ida_ssm_tc.cuh"
+
+namespace ida {
+
+using namespace tc;
+
+constexpr int BTH = 512;  // threads per CTA
+
+template <int DP>
+struct BwdSmem {
+    static constexpr int XB = DP / 64 * SSLAB;
+    static constexpr int X = 0;                    // [DP / 64][128 s][64] bf16
+    static constexpr int DY = X + XB;              // [DP / 64][128 t][64]
+    static constexpr int B = DY + XB;              // [128 s][64]
+    static constexpr int C = B + SSLAB;            // [128 t][64]
+    static constexpr int R = C + SSLAB;            // [2][128 s][64 t]
+    static constexpr int P = R + 2 * SSLAB;        // [2][128 s][64 t], later dx [DP / 64][128 s][64]
+    static constexpr int PART = DP * 128;          // bytes of one part of a state [DP / 64][64 m][64]
+    static constexpr int ST = P + 2 * SSLAB;       // [3] parts of Z, later of X_0
+    static constexpr int MISC = ST + 3 * PART;
+    static constexpr int ARR = MISC + 64;
+    // S in two floats, 2^S, f, D, z, column factors, row and column sums of K in 4 parts each, the
+    // inter-chunk products in 4 parts each, G and E of a position with itself
+    static constexpr int NARR = 7 + 8 + 8 + 2;
+    static constexpr int RED = ARR + NARR * SQ * 4;  // <Z, X_0> per warp, 2^S_Q, parameters' parts; 8 doubles
+    static constexpr int TOT = RED + 128 + 64;
+    static constexpr int TOTAL = TOT + 32;
+};
+
+struct BwdTmem {
+    static constexpr uint32_t G = 0, E = 128, DBI = 128, DCI = 192, DX = 256, DB = 384, DC = 448, COLS = 512;
+};
+
+struct BwdTcArgs {
+    ScanBwdArgs s;
+    int splits;  // CTAs that share a group's heads; above 1, s.db_head and s.dc_head are [B][N][G][splits][M]
+};
+
+// three bf16 parts of 8 values
+__device__ __forceinline__ void split3(const float *x, uint4 (&p)[3]) {
+    float v[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = x[e];
+#pragma unroll
+    for (int k = 0; k < 3; ++k) {
+        p[k] = Vec16<__nv_bfloat16>::pack(v);
+        float h[8];
+        Vec16<__nv_bfloat16>::unpack(p[k], h);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] -= h[e];
+    }
+}
+
+template <int DP>
+__global__ void __launch_bounds__(BTH, 1)
+    ssm_bwd_tc_kernel(BwdTcArgs ba, const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_dy,
+                      const __grid_constant__ CUtensorMap tm_b, const __grid_constant__ CUtensorMap tm_c,
+                      const __grid_constant__ CUtensorMap tm_dx) {
+    using L = BwdSmem<DP>;
+    using T = BwdTmem;
+    extern __shared__ __align__(1024) unsigned char sm[];
+    const ScanBwdArgs &a = ba.s;
+    const uint32_t s0 = smem_u32(sm);
+    uint64_t *bar = reinterpret_cast<uint64_t *>(sm + L::MISC);  // 0 b, c; 1 x, dy; 2 E and Z^T b; 3 dx, Z x; 4 the rest
+    uint32_t *tslot = reinterpret_cast<uint32_t *>(sm + L::MISC + 48);
+    float *arr = reinterpret_cast<float *>(sm + L::ARR);
+    float *Sh = arr, *Sl = Sh + SQ, *et = Sl + SQ, *fs = et + SQ, *dl = fs + SQ, *zz = dl + SQ, *rt = zz + SQ;
+    float *ksum_t = rt + SQ;        // [4 lane quarters][128]: sum over the quarter's s of K, per t
+    float *ksum_s = ksum_t + 4 * SQ;  // [4 warps of a quarter][128]: sum over their t of K / D_s, per s
+    float *zin = ksum_s + 4 * SQ;   // [4][128]: b_s^T Z x_s
+    float *xin = zin + 4 * SQ;      // [4][128]: c_t^T X_0 dy_t
+    float *gs = xin + 4 * SQ, *es = gs + SQ;  // G and E at s = t
+    float *red = reinterpret_cast<float *>(sm + L::RED);
+    double *dred = reinterpret_cast<double *>(sm + L::RED + 128);
+    long long *tot = reinterpret_cast<long long *>(sm + L::TOT);
+    const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
+    const int q4 = warp & 3, wj = warp >> 2, row = 32 * q4 + lane;  // my lane of TMEM: position s or t
+    const uint32_t lane_base = (uint32_t)(32 * q4) << 16;
+    const int H = a.H, N = a.N, M = a.M, d = a.d, rep = H / a.G;
+    int id = blockIdx.x;
+    const int split = id % ba.splits;
+    id /= ba.splits;
+    const int g = id % a.G;
+    id /= a.G;
+    const int ch = id % a.chunks, b = id / a.chunks;
+    const int t0 = ch * SQ, len = min(SQ, N - t0);
+    const int per = (rep + ba.splits - 1) / ba.splits, r0 = split * per, r1 = min(rep, r0 + per);
+
+    if ((s0 & 1023u) != 0u) {
+        if (tid == 0) report_error(a.err, kErrShape);
+        return;
+    }
+    if (tid == 0) {
+        for (int i = 0; i < 5; ++i) mbar_init(&bar[i], 1);
+        fence_mbar_init();
+        tma_prefetch_desc(&tm_x);
+        tma_prefetch_desc(&tm_dy);
+        tma_prefetch_desc(&tm_b);
+        tma_prefetch_desc(&tm_c);
+        tma_prefetch_desc(&tm_dx);
+    }
+    if (warp == 0) {
+        tmem_alloc(tslot, T::COLS);
+        tmem_relinquish();
+    }
+    const auto fetch = [&](int h) {  // one thread
+        mbar_arrive_expect_tx(&bar[1], 2 * L::XB);
+#pragma unroll
+        for (int i = 0; i < DP / 64; ++i) {
+            tma_load_4d(sm + L::X + i * SSLAB, &tm_x, 64 * i, h, t0, b, &bar[1]);
+            tma_load_4d(sm + L::DY + i * SSLAB, &tm_dy, 64 * i, h, t0, b, &bar[1]);
+        }
+    };
+    // one state [M][d], its three parts as tiles [m][j]; with `other`, returns my share of <st, other>
+    const auto load_state = [&](const float *st, const float *other) {
+        float dot = 0.f;
+#pragma unroll
+        for (int i = tid; i < 64 * DP / 8; i += BTH) {
+            const int m = i / (DP / 8), j = i % (DP / 8) * 8;
+            float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+            if (m < M && j < d) {
+                *reinterpret_cast<float4 *>(v) = __ldg(reinterpret_cast<const float4 *>(st + (size_t)m * d + j));
+                *reinterpret_cast<float4 *>(v + 4) = __ldg(reinterpret_cast<const float4 *>(st + (size_t)m * d + j + 4));
+                if (other) {
+                    float u[8];
+                    *reinterpret_cast<float4 *>(u) = __ldg(reinterpret_cast<const float4 *>(other + (size_t)m * d + j));
+                    *reinterpret_cast<float4 *>(u + 4) = __ldg(reinterpret_cast<const float4 *>(other + (size_t)m * d + j + 4));
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) dot = fmaf(u[e], v[e], dot);
+                }
+            }
+            uint4 p[3];
+            split3(v, p);
+#pragma unroll
+            for (int k = 0; k < 3; ++k)
+                *reinterpret_cast<uint4 *>(sm + L::ST + k * L::PART + j / 64 * 8192 + sw_off(m, j % 64 / 8)) = p[k];
+        }
+        return dot;
+    };
+    __syncthreads();
+    if (tid == 0 && r0 < r1) {
+        mbar_arrive_expect_tx(&bar[0], 2 * SSLAB);
+        tma_load_4d(sm + L::B, &tm_b, 0, g, t0, b, &bar[0]);
+        tma_load_4d(sm + L::C, &tm_c, 0, g, t0, b, &bar[0]);
+        fetch(g * rep + r0);
+    }
+    tc_fence_after();
+    const uint32_t tm = *tslot;
+    bool ok = true;
+    int r = r0;
+    for (; r < r1; ++r) {
+        const int h = g * rep + r, unit = b * H + h;
+        const uint32_t par = (r - r0) & 1;
+        const size_t so = ((size_t)unit * a.chunks + ch) * M * d;
+        const float rate = expf(a.a_log[h]);
+        // step sizes and decays of the head, by the first four warps
+        if (tid < SQ) {
+            float delta = 0.f, z = 0.f;
+            if (tid < len) {
+                z = __bfloat162float(static_cast<const __nv_bfloat16 *>(a.dt)[((size_t)b * N + t0 + tid) * a.lddt + h]) + a.dt_bias[h];
+                delta = softplus(z);
+            }
+            long long all;
+            const long long fx = chunk_sum(rate * 1.4426950408889634f, delta, tid, tot, all);
+            const float hi = (float)fx * kUnfix;
+            // S at the end of the block of 16 before mine
+            const int edge = (lane & 16) - 1;
+            long long ref = __shfl_sync(0xffffffffu, fx, edge < 0 ? 0 : edge);
+            if (edge < 0) ref = tid < 32 ? 0 : tid < 64 ? tot[0] : tid < 96 ? tot[0] + tot[1] : tot[0] + tot[1] + tot[2];
+            Sh[tid] = hi;
+            Sl[tid] = (float)(fx - (long long)(hi * kFix)) * kUnfix;
+            et[tid] = ex2_fix(fx);
+            fs[tid] = ex2_fix(all - fx);
+            dl[tid] = delta;
+            zz[tid] = z;
+            rt[tid] = ex2_fix(fx - ref);
+            if (tid == 0) red[16] = ex2_fix(all);
+        }
+        load_state(a.adj + so, nullptr);
+        fence_proxy_async_smem();
+        if (r == r0) ok = mbar_wait(&bar[0], 0) && ok;
+        ok = mbar_wait(&bar[1], par) && ok;
+        if (__syncthreads_or(!ok)) break;
+        if (warp == 0 && elect_one()) {
+            tc_fence_after();
+            const SmemDesc dxk = sw_desc(s0 + L::X, 16), dyk = sw_desc(s0 + L::DY, 16);
+            const SmemDesc db = sw_desc(s0 + L::B, 16), dc = sw_desc(s0 + L::C, 16), dz = sw_desc(s0 + L::ST, 8192);
+            constexpr uint32_t id_q = idesc(128, 128, 1, 1), id_x = idesc(128, DP, 1, 1, 0, 1);
+#pragma unroll
+            for (int k = 0; k < DP / 16; ++k)
+                mma_f16(tm + T::E, sw_step(dxk, k / 4 * SSLAB + k % 4 * 32), sw_step(dyk, k / 4 * SSLAB + k % 4 * 32), id_q, k > 0);
+            if (r == r0)
+#pragma unroll
+                for (int k = 0; k < 4; ++k) mma_f16(tm + T::G, sw_step(db, k * 32), sw_step(dc, k * 32), id_q, k > 0);
+            // Z^T b: Z's high part [K = m][j] as an MN-major B
+#pragma unroll
+            for (int k = 0; k < 4; ++k) mma_f16(tm + T::DX, sw_step(db, k * 32), sw_step(dz, k * 2048), id_x, k > 0);
+            mma_commit(&bar[2]);
+        }
+        __syncwarp();
+        if (tid == 0) bulk_wait_read_all();  // dx of the last head has left P's place
+        ok = mbar_wait(&bar[2], par);
+        if (__syncthreads_or(!ok)) break;
+        tc_fence_after();
+        {  // Z^T b D_s f_s: my row, a quarter of the channels
+            const float f = dl[row] * fs[row];
+            constexpr int CW = DP / 4;
+#pragma unroll
+            for (int c = 0; c < CW; c += 16) {
+                float v[16];
+                tmem_ld16(tm + lane_base + T::DX + wj * CW + c, v);
+                tmem_wait_ld();
+#pragma unroll
+                for (int e = 0; e < 16; ++e) v[e] *= f;
+                tmem_st16(tm + lane_base + T::DX + wj * CW + c, v);
+            }
+        }
+        {
+            // K, P, R: row s, every fourth block of 16 columns t
+            const float sh = Sh[row], sl = Sl[row], delta = dl[row], skip = a.D[h];
+            float ks = 0.f;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int kb = wj + 4 * i;
+                uint4 pp[2], rr[2];
+                if (kb < 2 * q4) {  // wholly before my rows
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) pp[e] = rr[e] = make_uint4(0, 0, 0, 0);
+                    if (lane < 16) ksum_t[q4 * SQ + 16 * kb + lane] = 0.f;
+                } else {
+                    float gv[16], ev[16], kk[16];
+                    tmem_ld16(tm + lane_base + T::G + 16 * kb, gv);
+                    tmem_ld16(tm + lane_base + T::E + 16 * kb, ev);
+                    tmem_wait_ld();
+                    if (kb >= 2 * q4 + 2) {  // wholly behind my rows: decay to the block's start, then inside it
+                        const float f = ex2((Sh[16 * kb - 1] - sh) + (Sl[16 * kb - 1] - sl));
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) {
+                            const float w = f * rt[16 * kb + e], we = w * ev[e], k1 = we * gv[e];
+                            ks += k1;
+                            kk[e] = k1 * delta;
+                            gv[e] *= w * delta;
+                            ev[e] = we * delta;
+                        }
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) {
+                            const int t = 16 * kb + e;
+                            float w = t > row ? ex2((Sh[t] - sh) + (Sl[t] - sl)) : 0.f;
+                            const float k1 = t > row ? w * ev[e] * gv[e] : 0.f;
+                            ks += k1;
+                            kk[e] = k1 * delta;
+                            if (t == row) {
+                                gs[t] = gv[e];
+                                es[t] = ev[e];
+                                w = 1.f;
+                            }
+                            gv[e] = t >= row ? gv[e] * (w * delta) + (t == row ? skip : 0.f) : 0.f;
+                            ev[e] = t >= row ? ev[e] * (w * delta) : 0.f;
+                        }
+                    }
+                    pp[0] = Vec16<__nv_bfloat16>::pack(gv);
+                    pp[1] = Vec16<__nv_bfloat16>::pack(gv + 8);
+                    rr[0] = Vec16<__nv_bfloat16>::pack(ev);
+                    rr[1] = Vec16<__nv_bfloat16>::pack(ev + 8);
+                    const float v = warp_reduce_scatter<16>(kk, lane);
+                    ksum_t[q4 * SQ + 16 * kb + rs_index<16>(lane)] = v;
+                }
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int off = kb / 4 * SSLAB + sw_off(row, kb % 4 * 2 + e);
+                    *reinterpret_cast<uint4 *>(sm + L::P + off) = pp[e];
+                    *reinterpret_cast<uint4 *>(sm + L::R + off) = rr[e];
+                }
+            }
+            ksum_s[wj * SQ + row] = ks;
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        fence_proxy_async_smem();
+        __syncthreads();
+        if (warp == 0 && elect_one()) {
+            tc_fence_after();
+            const SmemDesc dp = sw_desc(s0 + L::P, 16), dyn = sw_desc(s0 + L::DY, SSLAB), dxk = sw_desc(s0 + L::X, 16);
+            constexpr uint32_t id_x = idesc(128, DP, 1, 1, 0, 1), id_m = idesc(128, 64, 1, 1);
+#pragma unroll
+            for (int k = 0; k < SQ / 16; ++k)
+                mma_f16(tm + T::DX, sw_step(dp, k / 4 * SSLAB + k % 4 * 32), sw_step(dyn, k * 2048), id_x, 1);
+#pragma unroll
+            for (int part = 0; part < 3; ++part) {
+                const SmemDesc dz = sw_desc(s0 + L::ST + part * L::PART, 16);
+#pragma unroll
+                for (int k = 0; k < DP / 16; ++k)
+                    mma_f16(tm + T::DBI, sw_step(dxk, k / 4 * SSLAB + k % 4 * 32), sw_step(dz, k / 4 * 8192 + k % 4 * 32),
+                            id_m, part > 0 || k > 0);
+            }
+            mma_commit(&bar[3]);
+        }
+        __syncwarp();
+        ok = mbar_wait(&bar[3], par);
+        if (__syncthreads_or(!ok)) break;
+        tc_fence_after();
+        {  // X_0's parts take the place of Z's
+            const float dot = warp_sum(load_state(a.state0 + so, a.adj + so));
+            if (lane == 0) red[warp] = dot;
+        }
+        {  // dx out: my row, a quarter of the channels, over P
+            constexpr int CW = DP / 4;
+#pragma unroll
+            for (int c = 0; c < CW; c += 16) {
+                const int j = wj * CW + c;
+                float v[16];
+                tmem_ld16(tm + lane_base + T::DX + j, v);
+                tmem_wait_ld();
+                unsigned char *out = sm + L::P + j / 64 * SSLAB;
+                *reinterpret_cast<uint4 *>(out + sw_off(row, j % 64 / 8)) = Vec16<__nv_bfloat16>::pack(v);
+                *reinterpret_cast<uint4 *>(out + sw_off(row, j % 64 / 8 + 1)) = Vec16<__nv_bfloat16>::pack(v + 8);
+            }
+        }
+        {  // Z x: its product with b, and D_s f_s of it into db
+            float v[16], u[16], w[16];
+            tmem_ld16(tm + lane_base + T::DBI + 16 * wj, v);
+            if (r > r0) tmem_ld16(tm + lane_base + T::DB + 16 * wj, w);
+            tmem_wait_ld();
+            Vec16<__nv_bfloat16>::unpack(*reinterpret_cast<const uint4 *>(sm + L::B + sw_off(row, 2 * wj)), u);
+            Vec16<__nv_bfloat16>::unpack(*reinterpret_cast<const uint4 *>(sm + L::B + sw_off(row, 2 * wj + 1)), u + 8);
+            const float f = dl[row] * fs[row];
+            float dot = 0.f;
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+                dot = fmaf(u[e], v[e], dot);
+                v[e] = r > r0 ? fmaf(f, v[e], w[e]) : f * v[e];
+            }
+            zin[wj * SQ + row] = dot;
+            tmem_st16(tm + lane_base + T::DB + 16 * wj, v);
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        fence_proxy_async_smem();
+        __syncthreads();
+        if (warp == 0 && elect_one()) {
+            tc_fence_after();
+            const SmemDesc dyk = sw_desc(s0 + L::DY, 16), dr = sw_desc(s0 + L::R, 16), drt = sw_desc(s0 + L::R, SSLAB);
+            const SmemDesc dbn = sw_desc(s0 + L::B, SSLAB), dcn = sw_desc(s0 + L::C, SSLAB);
+            constexpr uint32_t id_m = idesc(128, 64, 1, 1), id_b = idesc(128, 64, 1, 1, 0, 1), id_c = idesc(128, 64, 1, 1, 1, 1);
+#pragma unroll
+            for (int part = 0; part < 3; ++part) {
+                const SmemDesc dz = sw_desc(s0 + L::ST + part * L::PART, 16);
+#pragma unroll
+                for (int k = 0; k < DP / 16; ++k)
+                    mma_f16(tm + T::DCI, sw_step(dyk, k / 4 * SSLAB + k % 4 * 32), sw_step(dz, k / 4 * 8192 + k % 4 * 32),
+                            id_m, part > 0 || k > 0);
+            }
+#pragma unroll
+            for (int k = 0; k < SQ / 16; ++k)
+                mma_f16(tm + T::DB, sw_step(dr, k / 4 * SSLAB + k % 4 * 32), sw_step(dcn, k * 2048), id_b, 1);
+#pragma unroll
+            for (int k = 0; k < SQ / 16; ++k)
+                mma_f16(tm + T::DC, sw_step(drt, k * 2048), sw_step(dbn, k * 2048), id_c, r > r0 || k > 0);
+            mma_commit(&bar[4]);
+        }
+        __syncwarp();
+        if (tid == 0) {
+#pragma unroll
+            for (int s = 0; s < DP / 64; ++s)
+                if (64 * s < d) tma_store_4d(&tm_dx, 64 * s, h, t0, b, sm + L::P + s * SSLAB);
+            bulk_commit();
+        }
+        ok = mbar_wait(&bar[4], par);
+        if (__syncthreads_or(!ok)) break;
+        tc_fence_after();
+        if (tid == 0 && r + 1 < r1) fetch(h + 1);
+        {  // X_0 dy: its product with c, and 2^S_t of it into dc
+            float v[16], u[16], w[16];
+            tmem_ld16(tm + lane_base + T::DCI + 16 * wj, v);
+            tmem_ld16(tm + lane_base + T::DC + 16 * wj, w);
+            tmem_wait_ld();
+            Vec16<__nv_bfloat16>::unpack(*reinterpret_cast<const uint4 *>(sm + L::C + sw_off(row, 2 * wj)), u);
+            Vec16<__nv_bfloat16>::unpack(*reinterpret_cast<const uint4 *>(sm + L::C + sw_off(row, 2 * wj + 1)), u + 8);
+            const float f = et[row];
+            float dot = 0.f;
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+                dot = fmaf(u[e], v[e], dot);
+                v[e] = fmaf(f, v[e], w[e]);
+            }
+            xin[wj * SQ + row] = dot;
+            tmem_st16(tm + lane_base + T::DC + 16 * wj, v);
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        __syncthreads();
+        // w, dt's gradient and the chunk's parts of the parameters': position tid
+        if (tid < SQ) {
+            const int t = tid;
+            float kt = 0.f, ks = 0.f, zi = 0.f, xi = 0.f;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                kt += ksum_t[k * SQ + t];
+                ks += ksum_s[k * SQ + t];
+                zi += zin[k * SQ + t];
+                xi += xin[k * SQ + t];
+            }
+            const float delta = dl[t], zf = zi * fs[t];
+            const double up = (double)kt - (double)(delta * ks) + (double)(et[t] * xi), before = (double)(delta * zf);
+            double su = up, sb = before;  // sums from my position on in the warp, and up to it
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const double u = __shfl_down_sync(0xffffffffu, su, o), v = __shfl_up_sync(0xffffffffu, sb, o);
+                if (lane + o < 32) su += u;
+                if (lane >= o) sb += v;
+            }
+            if (lane == 0) dred[warp] = su;
+            if (lane == 31) dred[4 + warp] = sb;
+            named_sync(1, 128);
+            double w = su + (sb - before);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) w += k > warp ? dred[k] : k < warp ? dred[4 + k] : 0.0;
+            float cross = 0.f;
+#pragma unroll
+            for (int k = 0; k < BTH / 32; ++k) cross += red[k];
+            const float wt = (float)(w + (double)(cross * red[16]));
+            float ga = 0.f, gb = 0.f, gd = 0.f;
+            if (t < len) {
+                const float ddt = (ks + gs[t] * es[t] + zf - rate * wt) / (1.f + expf(-zz[t]));
+                static_cast<__nv_bfloat16 *>(a.ddt)[((size_t)b * N + t0 + t) * a.ldddt + h] = __float2bfloat16_rn(ddt);
+                ga = -rate * delta * wt;
+                gb = ddt;
+                gd = es[t];
+            }
+            ga = warp_sum(ga);
+            gb = warp_sum(gb);
+            gd = warp_sum(gd);
+            if (lane == 0) {
+                red[17 + 3 * warp] = ga;
+                red[18 + 3 * warp] = gb;
+                red[19 + 3 * warp] = gd;
+            }
+            named_sync(1, 128);
+            if (tid < 3)
+                a.part[((size_t)unit * a.chunks + ch) * 4 + tid] = red[17 + tid] + red[20 + tid] + red[23 + tid] + red[26 + tid];
+        }
+    }
+    if (r < r1) {  // a wait ran out
+        if (tid == 0) {
+            report_error(a.err, kErrWaitTimeout);
+            mbar_wait(&bar[0], 0);
+            mbar_wait(&bar[1], (r - r0) & 1);
+        }
+    } else {
+        // db and dc of the group (or of this CTA's heads): my row, a quarter of the state rows
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            float v[16];
+            tmem_ld16(tm + lane_base + (k ? T::DC : T::DB) + 16 * wj, v);
+            tmem_wait_ld();
+            if (row < len) {
+                const size_t at = (size_t)b * N + t0 + row;
+#pragma unroll
+                for (int e = 0; e < 16; e += 8) {
+                    const int m = 16 * wj + e;
+                    if (m >= M) break;
+                    if (ba.splits == 1) {
+                        __nv_bfloat16 *o = static_cast<__nv_bfloat16 *>(k ? a.dc : a.db) + at * (k ? a.lddc : a.lddb) + g * M + m;
+                        *reinterpret_cast<uint4 *>(o) = Vec16<__nv_bfloat16>::pack(v + e);
+                    } else {
+                        float4 *o = reinterpret_cast<float4 *>((k ? a.dc_head : a.db_head) + ((at * a.G + g) * ba.splits + split) * M + m);
+                        o[0] = make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
+                        o[1] = make_float4(v[e + 4], v[e + 5], v[e + 6], v[e + 7]);
+                    }
+                }
+            }
+        }
+    }
+    if (tid == 0) bulk_wait_all();
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 0) {
+        tc_fence_after();
+        tmem_dealloc(tm, T::COLS);
+    }
+}
+
+// ---- host side ---------------------------------------------------------------------------
+
+// CTAs that share a group's heads: the fewest passes over the SMs, a head and chunk taking about 4 us
+// and a CTA's start 4 more; the partial rows of a shared group cost their traffic at about 5 TB/s.
+int ssm_bwd_tc_splits(int B, int H, int N, int G, int M) {
+    const int rep = H / G;
+    const long long base = (long long)B * ((N + SQ - 1) / SQ) * G;
+    int best = 1;
+    double cost = 0;
+    for (int s = 1; s <= rep; ++s) {
+        const int per = (rep + s - 1) / s;
+        if ((rep + per - 1) / per != s) continue;  // some CTA would have no head
+        const double c = (double)((base * s + 151) / 152) * (4.0 * per + 4.0) +
+                         (s > 1 ? 5.0 + 16.0 * (double)B * N * G * s * M / 5e6 : 0.0);
+        if (s == 1 || c < cost) {
+            best = s;
+            cost = c;
+        }
+    }
+    return best;
+}
+
+template <int DP>
+static ida_status launch_bwd_tc_d(const BwdTcArgs &ba, cudaStream_t st) {
+    const ScanBwdArgs &a = ba.s;
+    constexpr int smem = BwdSmem<DP>::TOTAL;
+    static_assert(smem <= 227 * 1024, "shared memory budget");
+    CUtensorMap mx, mdy, mb, mc, mdx;
+    ida_status s = ssm_map(&mx, a.x, a.B, a.N, a.H, a.d, a.ldx);
+    if (s == IDA_OK) s = ssm_map(&mdy, a.dy, a.B, a.N, a.H, a.d, (long long)a.H * a.d);
+    if (s == IDA_OK) s = ssm_map(&mb, a.b, a.B, a.N, a.G, a.M, a.ldb);
+    if (s == IDA_OK) s = ssm_map(&mc, a.c, a.B, a.N, a.G, a.M, a.ldc);
+    if (s == IDA_OK) s = ssm_map(&mdx, a.dx, a.B, a.N, a.H, a.d, a.lddx);
+    if (s != IDA_OK) return s;
+    cudaError_t e = cudaFuncSetAttribute(ssm_bwd_tc_kernel<DP>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return fail_with(IDA_ERR_CUDA, cudaGetErrorString(e));
+    const long long ctas = (long long)a.B * a.chunks * a.G * ba.splits;
+    if (ctas > 0x7FFFFFFFLL) return fail_with(IDA_ERR_UNSUPPORTED, "too many positions and groups");
+    ssm_bwd_tc_kernel<DP><<<(unsigned)ctas, BTH, smem, st>>>(ba, mx, mdy, mb, mc, mdx);
+    return launched("ssm scan backward");
+}
+
+// The chunk states, forwards and backwards, from zero.
+ida_status launch_bwd_tc_states(const ScanBwdArgs &a, cudaStream_t st) {
+    ScanArgs f = {a.x, a.b, a.c, a.dt, a.a_log, a.dt_bias, a.D, nullptr, nullptr, nullptr, a.B, a.H, a.N, a.d, a.G, a.M,
+                  a.ldx, a.ldb, a.ldc, a.lddt, SQ, a.chunks, a.chunks, a.state0, a.chunk_log, a.err};
+    ida_status s = launch_ssm_states(f, true, false, st);
+    if (s != IDA_OK) return s;
+    f.x = a.dy;
+    f.b = a.c;
+    f.ldx = (long long)a.H * a.d;
+    f.ldb = a.ldc;
+    f.seg_state = a.adj;
+    return launch_ssm_states(f, true, true, st);
+}
+
+ida_status launch_bwd_tc(const ScanBwdArgs &a, int splits, cudaStream_t st) {
+    const BwdTcArgs ba = {a, splits};
+    return a.d <= 64 ? launch_bwd_tc_d<64>(ba, st) : launch_bwd_tc_d<128>(ba, st);
+}
+
+}  // namespace ida

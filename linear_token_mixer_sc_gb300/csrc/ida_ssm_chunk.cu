@@ -32,20 +32,15 @@
 //
 // Every wait is bounded.  On a timeout all threads of the CTA leave the loop together, the kernel
 // records kErrWaitTimeout, waits (bounded) for its copy in flight, frees its TMEM and returns.
-#include <cuda.h>
-
 #include <mutex>
 
-#include "ida_ssm.cuh"
-#include "tc_sm103.cuh"
+#include "ida_ssm_tc.cuh"
 
 namespace ida {
 
 using namespace tc;
 
-constexpr int SQ = 128;         // positions per chunk
-constexpr int SSLAB = SQ * 128; // bytes of 128 rows of 64 bf16
-constexpr int STH = 256;        // threads per CTA
+constexpr int STH = 256;  // threads per CTA
 
 // Shared memory map; DP, MP: channels and state rows rounded up to 64 or 128.
 constexpr int SARR = 5 * SQ + 16;  // floats of one chunk's arrays (StepArrays)
@@ -86,44 +81,6 @@ struct SsmTmem {
     static constexpr uint32_t COLS = MP == 64 ? 256 : 512;
 };
 
-// Shared-memory descriptor of a 128-byte-swizzled operand whose 64-element rows are 128 bytes
-// apart: `sbo` 1024 between groups of 8 rows; `lbo` between 64-element slabs (MN-major operands).
-__device__ __forceinline__ SmemDesc sw_desc(uint32_t addr, uint32_t lbo) {
-    return {((addr >> 4) & 0x3FFFu) | ((lbo >> 4) << 16), (1024u >> 4) | (1u << 14) | (2u << 29)};
-}
-__device__ __forceinline__ SmemDesc sw_step(SmemDesc d, uint32_t bytes) {
-    d.lo += bytes >> 4;
-    return d;
-}
-// byte offset of 16-byte piece `c` of row `r` in such a slab
-__device__ __forceinline__ int sw_off(int r, int c) { return r * 128 + ((c ^ (r & 7)) << 4); }
-
-__device__ __forceinline__ void mma_f16_t(uint32_t d, uint32_t a_tmem, SmemDesc b, uint32_t id, uint32_t acc) {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t.reg .b64 db;\n\tmov.b64 db, {%2, %3};\n\t"
-        "setp.ne.b32 p, %5, 0;\n\ttcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %4, p;\n\t}" ::"r"(d),
-        "r"(a_tmem), "r"(b.lo), "r"(b.hi), "r"(id), "r"(acc)
-        : "memory");
-}
-__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&v)[8]) {
-    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(v[0]),
-                 "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
-                 : "memory");
-}
-__device__ __forceinline__ float ex2(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
-    const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t *>(&h);
-}
-
-constexpr float kFix = 4294967296.f, kUnfix = 1.f / 4294967296.f;  // 2^32
-
-__device__ __forceinline__ void named_sync(int id, int n) { asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(n) : "memory"); }
-
 // What a chunk's step sizes give, for the positions s of the chunk.
 struct StepArrays {
     float *cumf;  // S_s
@@ -135,24 +92,6 @@ struct StepArrays {
     __device__ __forceinline__ StepArrays(float *p)
         : cumf(p), uf(p + SQ), rs(p + 2 * SQ), wst(p + 3 * SQ), et(p + 4 * SQ), cref(p + 5 * SQ) {}
 };
-
-// Running sum of log2 a over a chunk by 128 threads (four warps, named barrier 1), position k of
-// it in thread k; returns the inclusive sum, and the chunk's in `all`.
-__device__ __forceinline__ long long chunk_sum(float rate2, float delta, int k, long long *tot, long long &all) {
-    const int lane = k & 31, w = k >> 5;
-    long long fx = __float2ll_rn(fmaxf(-rate2 * delta, -1048576.f) * kFix);
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const long long u = __shfl_up_sync(0xffffffffu, fx, o);
-        if (lane >= o) fx += u;
-    }
-    if (lane == 31) tot[w] = fx;
-    named_sync(1, 128);
-    const long long t1 = tot[0], t2 = t1 + tot[1], t3 = t2 + tot[2];
-    all = t3 + tot[3];
-    named_sync(1, 128);  // the totals have been read
-    return fx + (w == 0 ? 0 : w == 1 ? t1 : w == 2 ? t2 : t3);
-}
 
 template <int DP, int MP>
 __global__ void __launch_bounds__(STH, MP == 64 ? 2 : 1)
@@ -438,8 +377,10 @@ __global__ void __launch_bounds__(STH, MP == 64 ? 2 : 1)
 }
 
 // A segment's last state from zero (the first segment's: from state_in) and its log2 decay; a
-// single segment's is the final state.  Chunks from the last to the first.
-template <int DP, int MP, int PARTS>
+// single segment's is the final state.  Chunks from the last to the first.  REV: what a segment
+// passes on of its own adjoint, sum_t a_first .. a_t c_t dy_t^T, from dy and c in the places of x
+// and b; there the sum up to a chunk is needed, so chunks go from the first to the last.
+template <int DP, int MP, int PARTS, bool REV>
 __global__ void __launch_bounds__(STH, MP == 64 ? 2 : 1)
     ssm_state_kernel(ScanArgs a, const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_b) {
     using L = SsmStateSmem<DP, MP, PARTS>;
@@ -476,8 +417,9 @@ __global__ void __launch_bounds__(STH, MP == 64 ? 2 : 1)
         tmem_alloc(tslot, MP);
         tmem_relinquish();
     }
-    const auto fetch = [&](int n) {  // one thread: the n-th chunk from the end
-        const int buf = n % L::NB, t0 = t_begin + (nch - 1 - n) * SQ;
+    const auto start_of = [&](int n) { return t_begin + (REV ? n : nch - 1 - n) * SQ; };  // the n-th chunk walked
+    const auto fetch = [&](int n) {  // one thread
+        const int buf = n % L::NB, t0 = start_of(n);
         mbar_arrive_expect_tx(&bar[buf], (uint32_t)SSLAB * (DP / 64 + MP / 64));
 #pragma unroll
         for (int i = 0; i < MP / 64; ++i)
@@ -488,7 +430,7 @@ __global__ void __launch_bounds__(STH, MP == 64 ? 2 : 1)
     };
     float dt_next = 0.f;
     const auto fetch_dt = [&](int n) {
-        const int k = tid - SQ, p = t_begin + (nch - 1 - n) * SQ + k;
+        const int k = tid - SQ, p = start_of(n) + k;
         if (k >= 0) dt_next = n < nch && p < t_end ? __bfloat162float(gdt[(size_t)p * a.lddt]) : 0.f;
     };
     long long behind = 0;  // log2 a summed over the chunks done, in warps 4 .. 7
@@ -496,10 +438,10 @@ __global__ void __launch_bounds__(STH, MP == 64 ? 2 : 1)
         const int k = tid - SQ;
         if (k < 0) return;
         float delta = 0.f;
-        if (t_begin + (nch - 1 - n) * SQ + k < t_end) delta = softplus(dt_next + dt_bias);
+        if (start_of(n) + k < t_end) delta = softplus(dt_next + dt_bias);
         long long all;
         const long long fx = chunk_sum(rate2, delta, k, tot, all);
-        arrays[(n & 1) * SQ + k] = ex2((float)(all - fx + behind) * kUnfix) * delta;
+        arrays[(n & 1) * SQ + k] = REV ? ex2_fix(fx + behind) : ex2_fix(all - fx + behind) * delta;
         behind += all;
     };
     fetch_dt(0);
@@ -585,11 +527,11 @@ __global__ void __launch_bounds__(STH, MP == 64 ? 2 : 1)
         }
     } else {
         // a single segment's last state is the final state
-        float *out = a.segs == 1 ? a.final_state + (size_t)unit * M * d
-                                 : a.seg_state + ((size_t)unit * a.segs + seg) * M * d;
+        float *out = a.segs == 1 && a.final_state ? a.final_state + (size_t)unit * M * d
+                                                  : a.seg_state + ((size_t)unit * a.segs + seg) * M * d;
         if (tid >= SQ && tid < SQ + 1) arrays[0] = (float)behind * kUnfix;
         __syncthreads();
-        const float *in = seg == 0 && a.state_in ? a.state_in + (size_t)unit * M * d : nullptr;
+        const float *in = !REV && seg == 0 && a.state_in ? a.state_in + (size_t)unit * M * d : nullptr;
         const float total = arrays[0], f = ex2(total);
         constexpr int MH = MP / 2;
         if (DP == 128 || tl < DP) {
@@ -608,7 +550,7 @@ __global__ void __launch_bounds__(STH, MP == 64 ? 2 : 1)
                         }
             }
         }
-        if (tid == 0 && j0 == 0 && a.segs > 1) a.seg_log[(size_t)unit * a.segs + seg] = total;
+        if (!REV && tid == 0 && j0 == 0 && a.segs > 1) a.seg_log[(size_t)unit * a.segs + seg] = total;
     }
     tc_fence_before();
     __syncthreads();
@@ -674,16 +616,16 @@ static SsmEncodeFn ssm_encode_fn() {
     return fn;
 }
 
-// Rows of B x N positions, ld elements apart, of K units of w channels each, as a map
-// (channel, unit, position, row) with boxes of 64 channels of one unit over 128 positions.  Channels
-// behind w and positions behind N are read as zero and not written.
-static bool ssm_map(SsmEncodeFn fn, CUtensorMap *m, const void *p, int B, int N, int K, int w, long long ld) {
+ida_status ssm_map(CUtensorMap *m, const void *p, int B, int N, int K, int w, long long ld) {
+    const SsmEncodeFn fn = ssm_encode_fn();
+    if (!fn) return fail_with(IDA_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
     const cuuint64_t dims[4] = {(cuuint64_t)w, (cuuint64_t)K, (cuuint64_t)N, (cuuint64_t)B};
     const cuuint64_t strides[3] = {(cuuint64_t)w * 2, (cuuint64_t)ld * 2, (cuuint64_t)N * ld * 2};
     const cuuint32_t box[4] = {64, 1, SQ, 1}, one[4] = {1, 1, 1, 1};
-    return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(p), dims, strides, box, one,
-              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    const CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(p), dims, strides, box, one,
+                          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? IDA_OK : fail_with(IDA_ERR_CUDA, "cuTensorMapEncodeTiled failed");
 }
 
 // Segments: the split that the two launches' chunk counts per SM favour.
@@ -707,15 +649,31 @@ void ssm_chunk_segments(int B, int H, int N, int d, int M, int num_sms, int &seg
     segs = (N + seg - 1) / seg;
 }
 
-template <int DP, int MP, int PARTS>
-static ida_status launch_states(const ScanArgs &a, const CUtensorMap &mx, const CUtensorMap &mb, cudaStream_t st) {
+template <int DP, int MP, int PARTS, bool REV>
+static ida_status launch_states(const ScanArgs &a, cudaStream_t st) {
     constexpr int smem = SsmStateSmem<DP, MP, PARTS>::TOTAL;
     static_assert(smem <= (MP == 64 ? 113 : 227) * 1024, "shared memory budget");
-    cudaError_t e = cudaFuncSetAttribute(ssm_state_kernel<DP, MP, PARTS>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    CUtensorMap mx, mb;
+    ida_status s = ssm_map(&mx, a.x, a.B, a.N, a.H, a.d, a.ldx);
+    if (s == IDA_OK) s = ssm_map(&mb, a.b, a.B, a.N, a.G, a.M, a.ldb);
+    if (s != IDA_OK) return s;
+    const auto kernel = ssm_state_kernel<DP, MP, PARTS, REV>;
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return fail_with(IDA_ERR_CUDA, cudaGetErrorString(e));
     const long long units = (long long)a.B * a.H * ((a.d + DP - 1) / DP);
-    ssm_state_kernel<DP, MP, PARTS><<<(unsigned)(units * a.state_segs), STH, smem, st>>>(a, mx, mb);
+    kernel<<<(unsigned)(units * a.state_segs), STH, smem, st>>>(a, mx, mb);
     return launched("ssm segment states");
+}
+
+template <int DP, int MP>
+static ida_status launch_states_of(const ScanArgs &a, bool exact, bool rev, cudaStream_t st) {
+    if (rev) return launch_states<DP, MP, 3, true>(a, st);
+    return exact ? launch_states<DP, MP, 3, false>(a, st) : launch_states<DP, MP, 1, false>(a, st);
+}
+
+ida_status launch_ssm_states(const ScanArgs &a, bool exact, bool rev, cudaStream_t st) {
+    if (a.d <= 64) return a.M <= 64 ? launch_states_of<64, 64>(a, exact, rev, st) : launch_states_of<64, 128>(a, exact, rev, st);
+    return a.M <= 64 ? launch_states_of<128, 64>(a, exact, rev, st) : launch_states_of<128, 128>(a, exact, rev, st);
 }
 
 template <int DP, int MP>
@@ -728,7 +686,7 @@ static ida_status launch_chunk(const ScanArgs &a, const CUtensorMap &mx, const C
     const long long units = (long long)a.B * a.H * ((a.d + DP - 1) / DP);
     if (units * a.segs > 0x7FFFFFFFLL) return fail_with(IDA_ERR_UNSUPPORTED, "too many rows and heads");
     ida_status s = IDA_OK;
-    if (a.state_segs > 0) s = a.final_state ? launch_states<DP, MP, 3>(a, mx, mb, st) : launch_states<DP, MP, 1>(a, mx, mb, st);
+    if (a.state_segs > 0) s = launch_ssm_states(a, a.final_state != nullptr, false, st);
     if (s == IDA_OK && a.segs > 1) {
         const long long n = (long long)a.B * a.H * (a.M * a.d / 4);
         ssm_carry_kernel<<<(unsigned)((n + 255) / 256), 256, 0, st>>>(a);
@@ -740,13 +698,12 @@ static ida_status launch_chunk(const ScanArgs &a, const CUtensorMap &mx, const C
 }
 
 ida_status launch_ssm_chunk(const ScanArgs &a, cudaStream_t st) {
-    const SsmEncodeFn fn = ssm_encode_fn();
-    if (!fn) return fail_with(IDA_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
     CUtensorMap mx, mb, mc, my;
-    if (!ssm_map(fn, &mx, a.x, a.B, a.N, a.H, a.d, a.ldx) || !ssm_map(fn, &mb, a.b, a.B, a.N, a.G, a.M, a.ldb) ||
-        !ssm_map(fn, &mc, a.c, a.B, a.N, a.G, a.M, a.ldc) ||
-        !ssm_map(fn, &my, a.y, a.B, a.N, a.H, a.d, (long long)a.H * a.d))
-        return fail_with(IDA_ERR_CUDA, "cuTensorMapEncodeTiled failed");
+    ida_status s = ssm_map(&mx, a.x, a.B, a.N, a.H, a.d, a.ldx);
+    if (s == IDA_OK) s = ssm_map(&mb, a.b, a.B, a.N, a.G, a.M, a.ldb);
+    if (s == IDA_OK) s = ssm_map(&mc, a.c, a.B, a.N, a.G, a.M, a.ldc);
+    if (s == IDA_OK) s = ssm_map(&my, a.y, a.B, a.N, a.H, a.d, (long long)a.H * a.d);
+    if (s != IDA_OK) return s;
     if (a.d <= 64)
         return a.M <= 64 ? launch_chunk<64, 64>(a, mx, mb, mc, my, st) : launch_chunk<64, 128>(a, mx, mb, mc, my, st);
     return a.M <= 64 ? launch_chunk<128, 64>(a, mx, mb, mc, my, st) : launch_chunk<128, 128>(a, mx, mb, mc, my, st);
