@@ -13,10 +13,12 @@
 // products, the gradient of log a_t, the sum over all pairs (s < t <= u) of positions:
 //   w_t = sum_{s < t <= u} K_su + sum_{u >= t} 2^(S_u) c_u^T X_0 dy_u + sum_{s < t} D_s f_s b_s^T Z x_s
 //         + 2^(S_Q) <Z, X_0>.
-// Its first sum is a running difference of K's row and column sums, the same K in both, added in
-// fp64; the other terms have no differences.  So dt's and the parameters' gradients come out to
-// fp32 rounding although P and R are rounded to bf16 for the MMAs.  What enters w through MMAs is
-// exact in its operands: b, c, x, dy are bf16, X_0 and Z are kept as the sum of three bf16 tiles.
+// Its first sum is taken over groups of 16 positions, without differences but inside t's own group:
+// there it is the running difference of K's row and column sums.  (One running difference over the
+// whole chunk loses 3e-6 of a_log's gradient in heads that forget within a few positions.)  So dt's
+// and the parameters' gradients come out to fp32 rounding although P and R are rounded to bf16 for
+// the MMAs.  What enters w through MMAs is exact in its operands: b, c, x, dy are bf16, X_0 and Z are
+// kept as the sum of three bf16 tiles.
 //
 // Chunks are independent: X_0 and Z of every chunk come from launch_ssm_states (forwards and
 // backwards) and a running sum over the chunks.  One CTA of 512 threads takes the heads of one
@@ -48,11 +50,12 @@ struct BwdSmem {
     static constexpr int ST = P + 2 * SSLAB;       // [3] parts of Z, later of X_0
     static constexpr int MISC = ST + 3 * PART;
     static constexpr int ARR = MISC + 64;
-    // S in two floats, 2^S, f, D, z, column factors, row and column sums of K in 4 parts each, the
-    // inter-chunk products in 4 parts each, G and E of a position with itself
-    static constexpr int NARR = 7 + 8 + 8 + 2;
-    static constexpr int RED = ARR + NARR * SQ * 4;  // <Z, X_0> per warp, 2^S_Q, parameters' parts; 8 doubles
-    static constexpr int TOT = RED + 128 + 64;
+    // S in two floats, 2^S, f, D, z, column factors, column sums of K in 8 parts and row sums in 4 + 1,
+    // the inter-chunk products in 4 parts each, G and E of a position with itself
+    static constexpr int NARR = 7 + 8 + 5 + 8 + 2;
+    // <Z, X_0> per warp, 2^S_Q, parameters' parts; sums per warp; sums of K per pair of groups
+    static constexpr int RED = ARR + NARR * SQ * 4;
+    static constexpr int TOT = RED + 128 + 32 + 256;
     static constexpr int TOTAL = TOT + 32;
 };
 
@@ -94,13 +97,14 @@ __global__ void __launch_bounds__(BTH, 1)
     uint32_t *tslot = reinterpret_cast<uint32_t *>(sm + L::MISC + 48);
     float *arr = reinterpret_cast<float *>(sm + L::ARR);
     float *Sh = arr, *Sl = Sh + SQ, *et = Sl + SQ, *fs = et + SQ, *dl = fs + SQ, *zz = dl + SQ, *rt = zz + SQ;
-    float *ksum_t = rt + SQ;        // [4 lane quarters][128]: sum over the quarter's s of K, per t
-    float *ksum_s = ksum_t + 4 * SQ;  // [4 warps of a quarter][128]: sum over their t of K / D_s, per s
-    float *zin = ksum_s + 4 * SQ;   // [4][128]: b_s^T Z x_s
+    float *ksum_t = rt + SQ;          // [8 groups of 16][128]: sum over the group's s of K, per t
+    float *ksum_s = ksum_t + 8 * SQ;  // [4 warps of a quarter][128]: sum over their t of K / D_s, per s, ...
+    float *kown = ksum_s + 4 * SQ;    // [128]: ... and over the t of s's own group
+    float *zin = kown + SQ;           // [4][128]: b_s^T Z x_s
     float *xin = zin + 4 * SQ;      // [4][128]: c_t^T X_0 dy_t
     float *gs = xin + 4 * SQ, *es = gs + SQ;  // G and E at s = t
     float *red = reinterpret_cast<float *>(sm + L::RED);
-    double *dred = reinterpret_cast<double *>(sm + L::RED + 128);
+    float *wsum = red + 32, *blk = wsum + 8;  // [8] and [8][8]
     long long *tot = reinterpret_cast<long long *>(sm + L::TOT);
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
     const int q4 = warp & 3, wj = warp >> 2, row = 32 * q4 + lane;  // my lane of TMEM: position s or t
@@ -190,7 +194,7 @@ __global__ void __launch_bounds__(BTH, 1)
                 delta = softplus(z);
             }
             long long all;
-            const long long fx = chunk_sum(rate * 1.4426950408889634f, delta, tid, tot, all);
+            const long long fx = chunk_sum(log2_rate(a.a_log[h]), delta, tid, tot, all);
             const float hi = (float)fx * kUnfix;
             // S at the end of the block of 16 before mine
             const int edge = (lane & 16) - 1;
@@ -255,7 +259,7 @@ __global__ void __launch_bounds__(BTH, 1)
                 if (kb < 2 * q4) {  // wholly before my rows
 #pragma unroll
                     for (int e = 0; e < 2; ++e) pp[e] = rr[e] = make_uint4(0, 0, 0, 0);
-                    if (lane < 16) ksum_t[q4 * SQ + 16 * kb + lane] = 0.f;
+                    ksum_t[(2 * q4 + (lane >> 4)) * SQ + 16 * kb + (lane & 15)] = 0.f;
                 } else {
                     float gv[16], ev[16], kk[16];
                     tmem_ld16(tm + lane_base + T::G + 16 * kb, gv);
@@ -272,12 +276,13 @@ __global__ void __launch_bounds__(BTH, 1)
                             ev[e] = we * delta;
                         }
                     } else {
+                        float ko = 0.f;
 #pragma unroll
                         for (int e = 0; e < 16; ++e) {
                             const int t = 16 * kb + e;
                             float w = t > row ? ex2((Sh[t] - sh) + (Sl[t] - sl)) : 0.f;
                             const float k1 = t > row ? w * ev[e] * gv[e] : 0.f;
-                            ks += k1;
+                            ko += k1;
                             kk[e] = k1 * delta;
                             if (t == row) {
                                 gs[t] = gv[e];
@@ -287,13 +292,26 @@ __global__ void __launch_bounds__(BTH, 1)
                             gv[e] = t >= row ? gv[e] * (w * delta) + (t == row ? skip : 0.f) : 0.f;
                             ev[e] = t >= row ? ev[e] * (w * delta) : 0.f;
                         }
+                        if (kb == row >> 4)
+                            kown[row] = ko;
+                        else
+                            ks += ko;
                     }
                     pp[0] = Vec16<__nv_bfloat16>::pack(gv);
                     pp[1] = Vec16<__nv_bfloat16>::pack(gv + 8);
                     rr[0] = Vec16<__nv_bfloat16>::pack(ev);
                     rr[1] = Vec16<__nv_bfloat16>::pack(ev + 8);
-                    const float v = warp_reduce_scatter<16>(kk, lane);
-                    ksum_t[q4 * SQ + 16 * kb + rs_index<16>(lane)] = v;
+                    // summed over my half warp's rows: lane l ends with column l % 16 of the block
+#pragma unroll
+                    for (int n = 8; n >= 1; n >>= 1) {
+                        const bool up = (lane & n) != 0;
+#pragma unroll
+                        for (int k = 0; k < n; ++k) {
+                            const float send = up ? kk[k] : kk[k + n], keep = up ? kk[k + n] : kk[k];
+                            kk[k] = keep + __shfl_xor_sync(0xffffffffu, send, n);
+                        }
+                    }
+                    ksum_t[(2 * q4 + (lane >> 4)) * SQ + 16 * kb + (lane & 15)] = kk[0];
                 }
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
@@ -316,12 +334,12 @@ __global__ void __launch_bounds__(BTH, 1)
             for (int k = 0; k < SQ / 16; ++k)
                 mma_f16(tm + T::DX, sw_step(dp, k / 4 * SSLAB + k % 4 * 32), sw_step(dyn, k * 2048), id_x, 1);
 #pragma unroll
-            for (int part = 0; part < 3; ++part) {
+            for (int part = 2; part >= 0; --part) {  // the small parts first: fewer roundings of the large sum
                 const SmemDesc dz = sw_desc(s0 + L::ST + part * L::PART, 16);
 #pragma unroll
                 for (int k = 0; k < DP / 16; ++k)
                     mma_f16(tm + T::DBI, sw_step(dxk, k / 4 * SSLAB + k % 4 * 32), sw_step(dz, k / 4 * 8192 + k % 4 * 32),
-                            id_m, part > 0 || k > 0);
+                            id_m, part < 2 || k > 0);
             }
             mma_commit(&bar[3]);
         }
@@ -373,12 +391,12 @@ __global__ void __launch_bounds__(BTH, 1)
             const SmemDesc dbn = sw_desc(s0 + L::B, SSLAB), dcn = sw_desc(s0 + L::C, SSLAB);
             constexpr uint32_t id_m = idesc(128, 64, 1, 1), id_b = idesc(128, 64, 1, 1, 0, 1), id_c = idesc(128, 64, 1, 1, 1, 1);
 #pragma unroll
-            for (int part = 0; part < 3; ++part) {
+            for (int part = 2; part >= 0; --part) {  // the small parts first: fewer roundings of the large sum
                 const SmemDesc dz = sw_desc(s0 + L::ST + part * L::PART, 16);
 #pragma unroll
                 for (int k = 0; k < DP / 16; ++k)
                     mma_f16(tm + T::DCI, sw_step(dyk, k / 4 * SSLAB + k % 4 * 32), sw_step(dz, k / 4 * 8192 + k % 4 * 32),
-                            id_m, part > 0 || k > 0);
+                            id_m, part < 2 || k > 0);
             }
 #pragma unroll
             for (int k = 0; k < SQ / 16; ++k)
@@ -422,36 +440,54 @@ __global__ void __launch_bounds__(BTH, 1)
         // w, dt's gradient and the chunk's parts of the parameters': position tid
         if (tid < SQ) {
             const int t = tid;
-            float kt = 0.f, ks = 0.f, zi = 0.f, xi = 0.f;
+            const int J = t >> 4;
+            if (t < 64) {  // sums of K per pair of groups
+                float v = 0.f;
+#pragma unroll
+                for (int e = 0; e < 16; ++e) v += ksum_t[(t >> 3) * SQ + 16 * (t & 7) + e];
+                blk[t] = v;
+            }
+            float ks = 0.f, zi = 0.f, xi = 0.f, kt = 0.f;  // kt: K of s in earlier groups
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-                kt += ksum_t[k * SQ + t];
                 ks += ksum_s[k * SQ + t];
                 zi += zin[k * SQ + t];
                 xi += xin[k * SQ + t];
             }
-            const float delta = dl[t], zf = zi * fs[t];
-            const double up = (double)kt - (double)(delta * ks) + (double)(et[t] * xi), before = (double)(delta * zf);
-            double su = up, sb = before;  // sums from my position on in the warp, and up to it
+#pragma unroll
+            for (int k = 0; k < 7; ++k) kt += k < J ? ksum_t[k * SQ + t] : 0.f;
+            const float delta = dl[t], zf = zi * fs[t], ko = kown[t];
+            // over my group, from my position on: K from earlier groups, and inside the group the running
+            // difference; before my position: K to later groups.  Over the warp: the inter-chunk terms
+            float su = kt + (ksum_t[J * SQ + t] - delta * ko), sb = delta * ks;
+            float iu = et[t] * xi, ib = delta * zf;
+            const float own_b = sb, own_ib = ib;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
-                const double u = __shfl_down_sync(0xffffffffu, su, o), v = __shfl_up_sync(0xffffffffu, sb, o);
-                if (lane + o < 32) su += u;
-                if (lane >= o) sb += v;
+                const float u = __shfl_down_sync(0xffffffffu, su, o), v = __shfl_up_sync(0xffffffffu, sb, o);
+                const float x = __shfl_down_sync(0xffffffffu, iu, o), y = __shfl_up_sync(0xffffffffu, ib, o);
+                if (o < 16) {
+                    if ((lane & 15) + o < 16) su += u;
+                    if ((lane & 15) >= o) sb += v;
+                }
+                if (lane + o < 32) iu += x;
+                if (lane >= o) ib += y;
             }
-            if (lane == 0) dred[warp] = su;
-            if (lane == 31) dred[4 + warp] = sb;
+            if (lane == 0) wsum[warp] = iu;
+            if (lane == 31) wsum[4 + warp] = ib;
             named_sync(1, 128);
-            double w = su + (sb - before);
+            float wt = su + (sb - own_b) + (iu + (ib - own_ib));
 #pragma unroll
-            for (int k = 0; k < 4; ++k) w += k > warp ? dred[k] : k < warp ? dred[4 + k] : 0.0;
+            for (int k = 0; k < 4; ++k) wt += k > warp ? wsum[k] : k < warp ? wsum[4 + k] : 0.f;
+            for (int i = 0; i < J; ++i)  // pairs of groups around mine
+                for (int k = J + 1; k < 8; ++k) wt += blk[8 * i + k];
             float cross = 0.f;
 #pragma unroll
             for (int k = 0; k < BTH / 32; ++k) cross += red[k];
-            const float wt = (float)(w + (double)(cross * red[16]));
+            wt = fmaf(cross, red[16], wt);
             float ga = 0.f, gb = 0.f, gd = 0.f;
             if (t < len) {
-                const float ddt = (ks + gs[t] * es[t] + zf - rate * wt) / (1.f + expf(-zz[t]));
+                const float ddt = (ks + ko + gs[t] * es[t] + zf - rate * wt) / (1.f + expf(-zz[t]));
                 static_cast<__nv_bfloat16 *>(a.ddt)[((size_t)b * N + t0 + t) * a.ldddt + h] = __float2bfloat16_rn(ddt);
                 ga = -rate * delta * wt;
                 gb = ddt;

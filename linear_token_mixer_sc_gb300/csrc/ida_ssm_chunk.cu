@@ -116,7 +116,8 @@ __global__ void __launch_bounds__(STH, MP == 64 ? 2 : 1)
     const int j0 = id % slices * DP, unit = id / slices, b = unit / H, h = unit % H, g = h / (H / a.G);
     const int t_begin = seg * a.seg, t_end = min(N, t_begin + a.seg), nch = (t_end - t_begin + SQ - 1) / SQ;
     const __nv_bfloat16 *gdt = static_cast<const __nv_bfloat16 *>(a.dt) + (size_t)b * N * a.lddt + h;
-    const float rate2 = expf(a.a_log[h]) * 1.4426950408889634f, dt_bias = a.dt_bias[h], skip = a.D[h];
+    const float dt_bias = a.dt_bias[h], skip = a.D[h];
+    const double rate2 = log2_rate(a.a_log[h]);
     constexpr uint32_t TILE_BYTES = (uint32_t)SSLAB * (DP / 64 + 2 * (MP / 64));
 
     if ((s0 & 1023u) != 0u) {  // the swizzle repeats every 1024 bytes
@@ -401,7 +402,8 @@ __global__ void __launch_bounds__(STH, MP == 64 ? 2 : 1)
     const int j0 = id % slices * DP, unit = id / slices, b = unit / H, h = unit % H, g = h / (H / a.G);
     const int t_begin = seg * a.seg, t_end = min(N, t_begin + a.seg), nch = (t_end - t_begin + SQ - 1) / SQ;
     const __nv_bfloat16 *gdt = static_cast<const __nv_bfloat16 *>(a.dt) + (size_t)b * N * a.lddt + h;
-    const float rate2 = expf(a.a_log[h]) * 1.4426950408889634f, dt_bias = a.dt_bias[h];
+    const float dt_bias = a.dt_bias[h];
+    const double rate2 = log2_rate(a.a_log[h]);
 
     if ((s0 & 1023u) != 0u) {
         if (tid == 0) report_error(a.err, kErrShape);
@@ -495,11 +497,11 @@ __global__ void __launch_bounds__(STH, MP == 64 ? 2 : 1)
             const SmemDesc da = sw_desc(s0 + L::X + buf * L::XB, DP == 64 ? 0 : SSLAB);
             constexpr uint32_t id_x = idesc(128, MP, 1, 1, 1, 1);
 #pragma unroll
-            for (int part = 0; part < PARTS; ++part) {
+            for (int part = PARTS - 1; part >= 0; --part) {  // the small parts first: fewer roundings of the large sum
                 const SmemDesc dh = sw_desc(s0 + L::B + buf * L::BB + part * (MP / 64) * SSLAB, SSLAB);
 #pragma unroll
                 for (int k = 0; k < SQ / 16; ++k)
-                    mma_f16(tm, sw_step(da, k * 2048), sw_step(dh, k * 2048), id_x, n > 0 || part > 0 || k > 0);
+                    mma_f16(tm, sw_step(da, k * 2048), sw_step(dh, k * 2048), id_x, n > 0 || part < PARTS - 1 || k > 0);
             }
             mma_commit(&bar[2 + buf]);
         }

@@ -58,10 +58,12 @@ __device__ __forceinline__ float ex2_fix(long long x) {
 }
 
 // Running sum of log2 a over a chunk by 128 threads (four warps, named barrier 1), position k of
-// it in thread k; returns the inclusive sum, and the chunk's in `all`.
-__device__ __forceinline__ long long chunk_sum(float rate2, float delta, int k, long long *tot, long long &all) {
+// it in thread k; returns the inclusive sum, and the chunk's in `all`.  fp64 for the rate and its
+// product: an error in the rate would be the same in every position of a head.
+__device__ __forceinline__ double log2_rate(float a_log) { return exp((double)a_log) * 1.4426950408889634; }
+__device__ __forceinline__ long long chunk_sum(double rate2, float delta, int k, long long *tot, long long &all) {
     const int lane = k & 31, w = k >> 5;
-    long long fx = __float2ll_rn(fmaxf(-rate2 * delta, -1048576.f) * kFix);
+    long long fx = __double2ll_rn(fmax(-rate2 * (double)delta, -1048576.0) * (double)kFix);
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
         const long long u = __shfl_up_sync(0xffffffffu, fx, o);
