@@ -10,8 +10,9 @@
 // <Z_t, X_t> is c_t^T X_t dy_t + w_{t+1} by Z's recurrence and w_t + D_t b_t^T Z_t x_t by X's, and
 // without the term of position t itself that both hold,
 //   w_t = w_{t+1} + c_t^T (a_t X_{t-1}) dy_t - D_t b_t^T (a_{t+1} Z_{t+1}) x_t,
-// from the product of the two states at the end of the chunk.  Chunks are short so that this sum
-// of differences loses little: its rounding is 2^-24 of the terms of one chunk.
+// from the product of the two states at the end of t's group of 8 positions.  Groups are short so
+// that this sum of differences loses little: its rounding is 2^-24 of the terms of one group.  (Over
+// whole chunks it cost 4e-6 of a_log's gradient in heads that forget within a few positions.)
 //
 // Sequences are cut into chunks of 64 positions (32 where the rows would not fit shared memory).
 // Launches: each chunk's last state from zero and, backwards, what it passes on of its own
@@ -26,11 +27,12 @@ namespace ida {
 ida_status check_scan(int B, int H, int N, int d, int G, int M, long long ldx, long long ldb, long long ldc,
                       long long lddt, int dtype);
 ida_status device_error_word(unsigned **err, std::string &why);
+int ssm_bwd_tc_chunk(int M);
 int ssm_bwd_tc_splits(int B, int H, int N, int G, int M);
 ida_status launch_bwd_tc_states(const ScanBwdArgs &a, cudaStream_t st);
 ida_status launch_bwd_tc(const ScanBwdArgs &a, int splits, cudaStream_t st);
 
-constexpr int BT = 8;  // positions between two sums across warps
+constexpr int BT = 8;  // positions between two sums across warps, and of a group (w above)
 
 // floats of a quarter row of b or c and of a row (the four quarters on their own banks)
 template <int MT>
@@ -306,8 +308,8 @@ __global__ void __launch_bounds__(256) bwd_main_kernel(ScanBwdArgs s) {
     const int km = lane & 3, jl = warp * 32 + (lane >> 2) * 4, col = warp * 32 + lane;
     const size_t so = ((size_t)unit * s.chunks + ch) * M * d;
     ssm_f2 X[MT / 2][4];
-    const auto load_tile = [&](const float *src, bool product) {
-        float dot = 0.f;  // with the tile that was there
+    const auto load_tile = [&](const float *src, bool product) {  // product: with the tile that was there
+        float dot = 0.f;
 #pragma unroll
         for (int i = 0; i < MT / 2; ++i) {
             const int m = km * MT + 2 * i;
@@ -327,6 +329,39 @@ __global__ void __launch_bounds__(256) bwd_main_kernel(ScanBwdArgs s) {
             X[i][2] = ssm_pack(u.z, v.z);
             X[i][3] = ssm_pack(u.w, v.w);
         }
+        return dot;
+    };
+    // the state behind a group of BT, kept for the walk backwards
+    float *kept = s.kept + ((size_t)unit * s.chunks + ch) * (Q / BT) * M * d;
+    const auto keep_tile = [&](float *dst) {
+        if (jl < d)
+#pragma unroll
+            for (int i = 0; i < MT / 2; ++i) {
+                const int m = km * MT + 2 * i;
+                if (m < M) {
+                    float u[4], v[4];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) ssm_unpack(X[i][j], u[j], v[j]);
+                    *reinterpret_cast<float4 *>(dst + (size_t)m * d + jl) = make_float4(u[0], u[1], u[2], u[3]);
+                    *reinterpret_cast<float4 *>(dst + (size_t)(m + 1) * d + jl) = make_float4(v[0], v[1], v[2], v[3]);
+                }
+            }
+    };
+    const auto kept_product = [&](const float *src) {  // of this thread's own part
+        float dot = 0.f;
+        if (jl < d)
+#pragma unroll
+            for (int i = 0; i < MT / 2; ++i) {
+                const int m = km * MT + 2 * i;
+                if (m < M) {
+                    const float4 u = *reinterpret_cast<const float4 *>(src + (size_t)m * d + jl);
+                    const float4 v = *reinterpret_cast<const float4 *>(src + (size_t)(m + 1) * d + jl);
+                    float x[4], y[4];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) ssm_unpack(X[i][j], x[j], y[j]);
+                    dot += x[0] * u.x + x[1] * u.y + x[2] * u.z + x[3] * u.w + y[0] * v.x + y[1] * v.y + y[2] * v.z + y[3] * v.w;
+                }
+            }
         return dot;
     };
     load_tile(s.state0 + so, false);
@@ -384,16 +419,20 @@ __global__ void __launch_bounds__(256) bwd_main_kernel(ScanBwdArgs s) {
             tile_add<MT>(X, r.b + t * MS + km * QS, r.delta[t], *reinterpret_cast<const float4 *>(r.x + t * cols + jl));
         }
         flush_rows(tb, nb, true, pw);
+        if (tb + BT < len) keep_tile(kept + (size_t)(tb / BT) * M * d);
     }
-    // w behind the chunk: <a Z of the next position, X of the last>
-    float end = load_tile(s.adj + so, true);
-    end = warp_sum(end);
-    if (lane == 0) misc[warp] = end;
+    // w behind a group: <a Z of the next position, X of the last>; here the chunk's last group
+    const float end = warp_sum(load_tile(s.adj + so, true));
+    if (lane == 0) misc[(len - 1) / BT * 8 + warp] = end;
 
     // backwards: a_{t+1} Z_{t+1} for db_t and dx_t, then Z_t
     const float skip = s.D[h];
     for (int tb = (len - 1) / BT * BT; tb >= 0; tb -= BT) {
         const int nb = min(BT, len - tb);
+        if (tb + BT < len) {
+            const float v = warp_sum(kept_product(kept + (size_t)(tb / BT) * M * d));
+            if (lane == 0) misc[tb / BT * 8 + warp] = v;
+        }
         for (int tt = nb - 1; tt >= 0; --tt) {
             const int t = tb + tt;
             tile_rows<MT>(X, *reinterpret_cast<const float4 *>(r.x + t * cols + jl), lane, rows + (warp * BT + tt) * MP);
@@ -408,21 +447,19 @@ __global__ void __launch_bounds__(256) bwd_main_kernel(ScanBwdArgs s) {
     }
     // w, and the gradients of dt and of the head's parameters: one warp, two positions a lane
     if (warp == 0) {
-        float tail = 0.f;
-        for (int w = 0; w < warps; ++w) tail += misc[w];
         const float rate = expf(s.a_log[h]);
         float ga = 0.f, gb = 0.f, gd = 0.f;
-        for (int base = (len - 1) / 32 * 32; base >= 0; base -= 32) {
+        for (int base = 0; base < len; base += 32) {
             const int t = base + lane;
             const bool ok = t < len;
-            float v = ok ? pw[t] - r.delta[t] * rw[t] : 0.f;
+            float w = ok ? pw[t] - r.delta[t] * rw[t] : 0.f;
 #pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {  // sum of the lanes from mine on
-                const float u = __shfl_down_sync(0xffffffffu, v, o);
-                if (lane + o < 32) v += u;
+            for (int o = 1; o < BT; o <<= 1) {  // sum of the group's positions from mine on
+                const float u = __shfl_down_sync(0xffffffffu, w, o);
+                if ((lane & (BT - 1)) + o < BT) w += u;
             }
-            const float w = v + tail;
-            tail = __shfl_sync(0xffffffffu, w, 0);
+            if (ok)
+                for (int i = 0; i < warps; ++i) w += misc[t / BT * 8 + i];
             if (ok) {
                 const float sig = 1.f / (1.f + expf(-r.z[t]));
                 const float ddt = (fmaf(bc[t], xdy[t], rw[t]) - rate * w) * sig;
@@ -503,19 +540,20 @@ static int bwd_chunk_len(int d, int M) {
 struct BwdPlan {
     bool tc;
     int chunk, chunks, parts;                      // parts: those a group's db and dc are summed from
-    size_t state0, adj, log, db, dc, part, total;  // float offsets
+    size_t state0, adj, kept, log, db, dc, part, total;  // float offsets
 };
 static BwdPlan bwd_plan(int B, int H, int N, int d, int G, int M, int dtype) {
     BwdPlan p;
-    p.tc = dtype == IDA_BF16 && d <= 128 && M <= 64;
-    p.chunk = p.tc ? 128 : bwd_chunk_len(d, M);
+    p.tc = dtype == IDA_BF16 && d <= 128;
+    p.chunk = p.tc ? ssm_bwd_tc_chunk(M) : bwd_chunk_len(d, M);
     p.chunks = (N + p.chunk - 1) / p.chunk;
     p.parts = p.tc ? ssm_bwd_tc_splits(B, H, N, G, M) : H / G;
     const size_t units = (size_t)B * H, states = units * p.chunks * M * d;
     const size_t heads = p.parts == 1 ? 0 : (size_t)B * N * G * p.parts * M;
     p.state0 = 0;
     p.adj = p.state0 + states;
-    p.db = p.adj + states;
+    p.kept = p.adj + states;
+    p.db = p.kept + (p.tc ? 0 : states * (p.chunk / BT));
     p.dc = p.db + heads;
     p.part = p.dc + heads;
     p.log = p.part + units * p.chunks * 4;
@@ -633,7 +671,7 @@ ida_status ida_ssm_scan_backward(const void *x, const void *b, const void *c, co
     float *ws = static_cast<float *>(workspace);
     ScanBwdArgs a = {x, b, c, dt, dy, a_log, dt_bias, D, dx, db, dc, ddt, da_log, ddt_bias, dD, B, H, N, d, G, M,
                      ldx, ldb, ldc, lddt, lddx, lddb, lddc, ldddt, p.chunk, p.chunks, ws + p.state0, ws + p.adj, ws + p.log,
-                     p.parts == 1 ? nullptr : ws + p.db, p.parts == 1 ? nullptr : ws + p.dc, ws + p.part, nullptr};
+                     p.parts == 1 ? nullptr : ws + p.db, p.parts == 1 ? nullptr : ws + p.dc, ws + p.part, ws + p.kept, nullptr};
     s = device_error_word(&a.err, why);
     if (s != IDA_OK) return fail_with(s, why);
     if (!p.tc) return dtype == IDA_F32 ? launch_bwd_m<float>(a, st) : launch_bwd_m<__nv_bfloat16>(a, st);

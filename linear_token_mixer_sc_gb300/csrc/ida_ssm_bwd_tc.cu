@@ -1,7 +1,7 @@
 // ida_ssm_bwd_tc.cu -- the backward pass of the selective scan on the tcgen05 tensor cores (bf16
-// inputs, d <= 128, M <= 64).
+// inputs, d <= 128).
 //
-// Over a chunk of Q = 128 positions, with X_0 the state before it, Z the adjoint that reaches it
+// Over a chunk of Q = 128 positions (64 where M > 64), with X_0 the state before it, Z the adjoint that reaches it
 // from behind (a Z of the next position), S_t the running sum of log2 a, W_ts = 2^(S_t - S_s) for
 // t >= s, f_s = 2^(S_Q - S_s), and the transposed products of positions
 //   G [s][t] = b_s . c_t,   E [s][t] = x_s . dy_t          (MMAs, K = M and K = d)
@@ -37,17 +37,19 @@ using namespace tc;
 
 constexpr int BTH = 512;  // threads per CTA
 
-template <int DP>
+// Shared memory map; Q: positions, DP, MP: channels and state rows rounded up to 64 or 128.
+template <int Q, int DP, int MP>
 struct BwdSmem {
-    static constexpr int XB = DP / 64 * SSLAB;
-    static constexpr int X = 0;                    // [DP / 64][128 s][64] bf16
-    static constexpr int DY = X + XB;              // [DP / 64][128 t][64]
-    static constexpr int B = DY + XB;              // [128 s][64]
-    static constexpr int C = B + SSLAB;            // [128 t][64]
-    static constexpr int R = C + SSLAB;            // [2][128 s][64 t]
-    static constexpr int P = R + 2 * SSLAB;        // [2][128 s][64 t], later dx [DP / 64][128 s][64]
-    static constexpr int PART = DP * 128;          // bytes of one part of a state [DP / 64][64 m][64]
-    static constexpr int ST = P + 2 * SSLAB;       // [3] parts of Z, later of X_0
+    static constexpr int SLAB = Q * 128;           // bytes of Q rows of 64 bf16
+    static constexpr int XB = DP / 64 * SLAB, BB = MP / 64 * SLAB, QB = Q / 64 * SLAB;
+    static constexpr int X = 0;                    // [DP / 64][Q s][64] bf16
+    static constexpr int DY = X + XB;              // [DP / 64][Q t][64]
+    static constexpr int B = DY + XB;              // [MP / 64][Q s][64]
+    static constexpr int C = B + BB;               // [MP / 64][Q t][64]
+    static constexpr int R = C + BB;               // [Q / 64][Q s][64 t]
+    static constexpr int P = R + QB;               // [Q / 64][Q s][64 t], later dx [DP / 64][Q s][64]
+    static constexpr int PSLAB = MP * 128, PART = DP / 64 * PSLAB;  // a part of a state [DP / 64][MP m][64]
+    static constexpr int ST = P + (QB > XB ? QB : XB);  // [3] parts of Z, later of X_0
     static constexpr int MISC = ST + 3 * PART;
     static constexpr int ARR = MISC + 64;
     // S in two floats, 2^S, f, D, z, column factors, column sums of K in 8 parts and row sums in 4 + 1,
@@ -59,8 +61,13 @@ struct BwdSmem {
     static constexpr int TOTAL = TOT + 32;
 };
 
+// Columns.  With M <= 64 G stays for all heads and the inter-chunk products take E's place; with
+// 64 positions and M > 64 they take G's and E's, and G is made again for every head.
+template <int Q, int DP, int MP>
 struct BwdTmem {
-    static constexpr uint32_t G = 0, E = 128, DBI = 128, DCI = 192, DX = 256, DB = 384, DC = 448, COLS = 512;
+    static constexpr bool KEEP_G = MP == 64;
+    static constexpr uint32_t G = 0, E = KEEP_G ? 128 : 64, DBI = KEEP_G ? 128 : 0, DCI = KEEP_G ? 192 : 0;
+    static constexpr uint32_t DX = KEEP_G ? 256 : 128, DB = KEEP_G ? 384 : 256, DC = KEEP_G ? 448 : 384, COLS = 512;
 };
 
 struct BwdTcArgs {
@@ -83,13 +90,14 @@ __device__ __forceinline__ void split3(const float *x, uint4 (&p)[3]) {
     }
 }
 
-template <int DP>
+template <int Q, int DP, int MP>
 __global__ void __launch_bounds__(BTH, 1)
     ssm_bwd_tc_kernel(BwdTcArgs ba, const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_dy,
                       const __grid_constant__ CUtensorMap tm_b, const __grid_constant__ CUtensorMap tm_c,
                       const __grid_constant__ CUtensorMap tm_dx) {
-    using L = BwdSmem<DP>;
-    using T = BwdTmem;
+    using L = BwdSmem<Q, DP, MP>;
+    using T = BwdTmem<Q, DP, MP>;
+    constexpr int NG = Q / 16, MW = MP / 4;  // groups of 16 positions; state rows of a warp
     extern __shared__ __align__(1024) unsigned char sm[];
     const ScanBwdArgs &a = ba.s;
     const uint32_t s0 = smem_u32(sm);
@@ -116,7 +124,7 @@ __global__ void __launch_bounds__(BTH, 1)
     const int g = id % a.G;
     id /= a.G;
     const int ch = id % a.chunks, b = id / a.chunks;
-    const int t0 = ch * SQ, len = min(SQ, N - t0);
+    const int t0 = ch * Q, len = min(Q, N - t0);
     const int per = (rep + ba.splits - 1) / ba.splits, r0 = split * per, r1 = min(rep, r0 + per);
 
     if ((s0 & 1023u) != 0u) {
@@ -140,15 +148,15 @@ __global__ void __launch_bounds__(BTH, 1)
         mbar_arrive_expect_tx(&bar[1], 2 * L::XB);
 #pragma unroll
         for (int i = 0; i < DP / 64; ++i) {
-            tma_load_4d(sm + L::X + i * SSLAB, &tm_x, 64 * i, h, t0, b, &bar[1]);
-            tma_load_4d(sm + L::DY + i * SSLAB, &tm_dy, 64 * i, h, t0, b, &bar[1]);
+            tma_load_4d(sm + L::X + i * L::SLAB, &tm_x, 64 * i, h, t0, b, &bar[1]);
+            tma_load_4d(sm + L::DY + i * L::SLAB, &tm_dy, 64 * i, h, t0, b, &bar[1]);
         }
     };
     // one state [M][d], its three parts as tiles [m][j]; with `other`, returns my share of <st, other>
     const auto load_state = [&](const float *st, const float *other) {
         float dot = 0.f;
 #pragma unroll
-        for (int i = tid; i < 64 * DP / 8; i += BTH) {
+        for (int i = tid; i < MP * DP / 8; i += BTH) {
             const int m = i / (DP / 8), j = i % (DP / 8) * 8;
             float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
             if (m < M && j < d) {
@@ -166,19 +174,25 @@ __global__ void __launch_bounds__(BTH, 1)
             split3(v, p);
 #pragma unroll
             for (int k = 0; k < 3; ++k)
-                *reinterpret_cast<uint4 *>(sm + L::ST + k * L::PART + j / 64 * 8192 + sw_off(m, j % 64 / 8)) = p[k];
+                *reinterpret_cast<uint4 *>(sm + L::ST + k * L::PART + j / 64 * L::PSLAB + sw_off(m, j % 64 / 8)) = p[k];
         }
         return dot;
     };
     __syncthreads();
     if (tid == 0 && r0 < r1) {
-        mbar_arrive_expect_tx(&bar[0], 2 * SSLAB);
-        tma_load_4d(sm + L::B, &tm_b, 0, g, t0, b, &bar[0]);
-        tma_load_4d(sm + L::C, &tm_c, 0, g, t0, b, &bar[0]);
+        mbar_arrive_expect_tx(&bar[0], 2 * L::BB);
+#pragma unroll
+        for (int i = 0; i < MP / 64; ++i) {
+            tma_load_4d(sm + L::B + i * L::SLAB, &tm_b, 64 * i, g, t0, b, &bar[0]);
+            tma_load_4d(sm + L::C + i * L::SLAB, &tm_c, 64 * i, g, t0, b, &bar[0]);
+        }
         fetch(g * rep + r0);
     }
     tc_fence_after();
     const uint32_t tm = *tslot;
+    // 64 positions fill half the lanes: rows 64 .. 127 of the operands are whatever lies behind them in
+    // shared memory, and the lanes that get them are not read
+    const bool mine = row < Q;
     bool ok = true;
     int r = r0;
     for (; r < r1; ++r) {
@@ -217,17 +231,19 @@ __global__ void __launch_bounds__(BTH, 1)
         if (warp == 0 && elect_one()) {
             tc_fence_after();
             const SmemDesc dxk = sw_desc(s0 + L::X, 16), dyk = sw_desc(s0 + L::DY, 16);
-            const SmemDesc db = sw_desc(s0 + L::B, 16), dc = sw_desc(s0 + L::C, 16), dz = sw_desc(s0 + L::ST, 8192);
-            constexpr uint32_t id_q = idesc(128, 128, 1, 1), id_x = idesc(128, DP, 1, 1, 0, 1);
+            const SmemDesc db = sw_desc(s0 + L::B, 16), dc = sw_desc(s0 + L::C, 16), dz = sw_desc(s0 + L::ST, L::PSLAB);
+            constexpr uint32_t id_q = idesc(128, Q, 1, 1), id_x = idesc(128, DP, 1, 1, 0, 1);
 #pragma unroll
             for (int k = 0; k < DP / 16; ++k)
-                mma_f16(tm + T::E, sw_step(dxk, k / 4 * SSLAB + k % 4 * 32), sw_step(dyk, k / 4 * SSLAB + k % 4 * 32), id_q, k > 0);
-            if (r == r0)
+                mma_f16(tm + T::E, sw_step(dxk, k / 4 * L::SLAB + k % 4 * 32), sw_step(dyk, k / 4 * L::SLAB + k % 4 * 32), id_q, k > 0);
+            if (r == r0 || !T::KEEP_G)
 #pragma unroll
-                for (int k = 0; k < 4; ++k) mma_f16(tm + T::G, sw_step(db, k * 32), sw_step(dc, k * 32), id_q, k > 0);
+                for (int k = 0; k < MP / 16; ++k)
+                    mma_f16(tm + T::G, sw_step(db, k / 4 * L::SLAB + k % 4 * 32), sw_step(dc, k / 4 * L::SLAB + k % 4 * 32), id_q, k > 0);
             // Z^T b: Z's high part [K = m][j] as an MN-major B
 #pragma unroll
-            for (int k = 0; k < 4; ++k) mma_f16(tm + T::DX, sw_step(db, k * 32), sw_step(dz, k * 2048), id_x, k > 0);
+            for (int k = 0; k < MP / 16; ++k)
+                mma_f16(tm + T::DX, sw_step(db, k / 4 * L::SLAB + k % 4 * 32), sw_step(dz, k * 2048), id_x, k > 0);
             mma_commit(&bar[2]);
         }
         __syncwarp();
@@ -235,7 +251,7 @@ __global__ void __launch_bounds__(BTH, 1)
         ok = mbar_wait(&bar[2], par);
         if (__syncthreads_or(!ok)) break;
         tc_fence_after();
-        {  // Z^T b D_s f_s: my row, a quarter of the channels
+        if (mine) {  // Z^T b D_s f_s: my row, a quarter of the channels
             const float f = dl[row] * fs[row];
             constexpr int CW = DP / 4;
 #pragma unroll
@@ -248,12 +264,12 @@ __global__ void __launch_bounds__(BTH, 1)
                 tmem_st16(tm + lane_base + T::DX + wj * CW + c, v);
             }
         }
-        {
+        if (mine) {
             // K, P, R: row s, every fourth block of 16 columns t
             const float sh = Sh[row], sl = Sl[row], delta = dl[row], skip = a.D[h];
             float ks = 0.f;
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
+            for (int i = 0; i < NG / 4; ++i) {
                 const int kb = wj + 4 * i;
                 uint4 pp[2], rr[2];
                 if (kb < 2 * q4) {  // wholly before my rows
@@ -315,7 +331,7 @@ __global__ void __launch_bounds__(BTH, 1)
                 }
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    const int off = kb / 4 * SSLAB + sw_off(row, kb % 4 * 2 + e);
+                    const int off = kb / 4 * L::SLAB + sw_off(row, kb % 4 * 2 + e);
                     *reinterpret_cast<uint4 *>(sm + L::P + off) = pp[e];
                     *reinterpret_cast<uint4 *>(sm + L::R + off) = rr[e];
                 }
@@ -328,18 +344,18 @@ __global__ void __launch_bounds__(BTH, 1)
         __syncthreads();
         if (warp == 0 && elect_one()) {
             tc_fence_after();
-            const SmemDesc dp = sw_desc(s0 + L::P, 16), dyn = sw_desc(s0 + L::DY, SSLAB), dxk = sw_desc(s0 + L::X, 16);
-            constexpr uint32_t id_x = idesc(128, DP, 1, 1, 0, 1), id_m = idesc(128, 64, 1, 1);
+            const SmemDesc dp = sw_desc(s0 + L::P, 16), dyn = sw_desc(s0 + L::DY, L::SLAB), dxk = sw_desc(s0 + L::X, 16);
+            constexpr uint32_t id_x = idesc(128, DP, 1, 1, 0, 1), id_m = idesc(128, MP, 1, 1);
 #pragma unroll
-            for (int k = 0; k < SQ / 16; ++k)
-                mma_f16(tm + T::DX, sw_step(dp, k / 4 * SSLAB + k % 4 * 32), sw_step(dyn, k * 2048), id_x, 1);
+            for (int k = 0; k < Q / 16; ++k)
+                mma_f16(tm + T::DX, sw_step(dp, k / 4 * L::SLAB + k % 4 * 32), sw_step(dyn, k * 2048), id_x, 1);
 #pragma unroll
             for (int part = 2; part >= 0; --part) {  // the small parts first: fewer roundings of the large sum
                 const SmemDesc dz = sw_desc(s0 + L::ST + part * L::PART, 16);
 #pragma unroll
                 for (int k = 0; k < DP / 16; ++k)
-                    mma_f16(tm + T::DBI, sw_step(dxk, k / 4 * SSLAB + k % 4 * 32), sw_step(dz, k / 4 * 8192 + k % 4 * 32),
-                            id_m, part < 2 || k > 0);
+                    mma_f16(tm + T::DBI, sw_step(dxk, k / 4 * L::SLAB + k % 4 * 32),
+                            sw_step(dz, k / 4 * L::PSLAB + k % 4 * 32), id_m, part < 2 || k > 0);
             }
             mma_commit(&bar[3]);
         }
@@ -351,7 +367,7 @@ __global__ void __launch_bounds__(BTH, 1)
             const float dot = warp_sum(load_state(a.state0 + so, a.adj + so));
             if (lane == 0) red[warp] = dot;
         }
-        {  // dx out: my row, a quarter of the channels, over P
+        if (mine) {  // dx out: my row, a quarter of the channels, over P
             constexpr int CW = DP / 4;
 #pragma unroll
             for (int c = 0; c < CW; c += 16) {
@@ -359,27 +375,32 @@ __global__ void __launch_bounds__(BTH, 1)
                 float v[16];
                 tmem_ld16(tm + lane_base + T::DX + j, v);
                 tmem_wait_ld();
-                unsigned char *out = sm + L::P + j / 64 * SSLAB;
+                unsigned char *out = sm + L::P + j / 64 * L::SLAB;
                 *reinterpret_cast<uint4 *>(out + sw_off(row, j % 64 / 8)) = Vec16<__nv_bfloat16>::pack(v);
                 *reinterpret_cast<uint4 *>(out + sw_off(row, j % 64 / 8 + 1)) = Vec16<__nv_bfloat16>::pack(v + 8);
             }
         }
-        {  // Z x: its product with b, and D_s f_s of it into db
-            float v[16], u[16], w[16];
-            tmem_ld16(tm + lane_base + T::DBI + 16 * wj, v);
-            if (r > r0) tmem_ld16(tm + lane_base + T::DB + 16 * wj, w);
-            tmem_wait_ld();
-            Vec16<__nv_bfloat16>::unpack(*reinterpret_cast<const uint4 *>(sm + L::B + sw_off(row, 2 * wj)), u);
-            Vec16<__nv_bfloat16>::unpack(*reinterpret_cast<const uint4 *>(sm + L::B + sw_off(row, 2 * wj + 1)), u + 8);
+        if (mine) {  // Z x: its product with b, and D_s f_s of it into db
             const float f = dl[row] * fs[row];
             float dot = 0.f;
 #pragma unroll
-            for (int e = 0; e < 16; ++e) {
-                dot = fmaf(u[e], v[e], dot);
-                v[e] = r > r0 ? fmaf(f, v[e], w[e]) : f * v[e];
+            for (int c = 0; c < MW; c += 16) {
+                const int m = MW * wj + c;
+                float v[16], u[16], w[16];
+                tmem_ld16(tm + lane_base + T::DBI + m, v);
+                if (r > r0) tmem_ld16(tm + lane_base + T::DB + m, w);
+                tmem_wait_ld();
+                const unsigned char *pb = sm + L::B + m / 64 * L::SLAB;
+                Vec16<__nv_bfloat16>::unpack(*reinterpret_cast<const uint4 *>(pb + sw_off(row, m % 64 / 8)), u);
+                Vec16<__nv_bfloat16>::unpack(*reinterpret_cast<const uint4 *>(pb + sw_off(row, m % 64 / 8 + 1)), u + 8);
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                    dot = fmaf(u[e], v[e], dot);
+                    v[e] = r > r0 ? fmaf(f, v[e], w[e]) : f * v[e];
+                }
+                tmem_st16(tm + lane_base + T::DB + m, v);
             }
             zin[wj * SQ + row] = dot;
-            tmem_st16(tm + lane_base + T::DB + 16 * wj, v);
         }
         tmem_wait_st();
         tc_fence_before();
@@ -387,22 +408,23 @@ __global__ void __launch_bounds__(BTH, 1)
         __syncthreads();
         if (warp == 0 && elect_one()) {
             tc_fence_after();
-            const SmemDesc dyk = sw_desc(s0 + L::DY, 16), dr = sw_desc(s0 + L::R, 16), drt = sw_desc(s0 + L::R, SSLAB);
-            const SmemDesc dbn = sw_desc(s0 + L::B, SSLAB), dcn = sw_desc(s0 + L::C, SSLAB);
-            constexpr uint32_t id_m = idesc(128, 64, 1, 1), id_b = idesc(128, 64, 1, 1, 0, 1), id_c = idesc(128, 64, 1, 1, 1, 1);
+            const SmemDesc dyk = sw_desc(s0 + L::DY, 16), dr = sw_desc(s0 + L::R, 16);
+            const SmemDesc drt = sw_desc(s0 + L::R, Q == 64 ? 0 : L::SLAB);  // 64 positions: rows 64.. repeat them
+            const SmemDesc dbn = sw_desc(s0 + L::B, L::SLAB), dcn = sw_desc(s0 + L::C, L::SLAB);
+            constexpr uint32_t id_m = idesc(128, MP, 1, 1), id_b = idesc(128, MP, 1, 1, 0, 1), id_c = idesc(128, MP, 1, 1, 1, 1);
 #pragma unroll
-            for (int part = 2; part >= 0; --part) {  // the small parts first: fewer roundings of the large sum
+            for (int part = 2; part >= 0; --part) {
                 const SmemDesc dz = sw_desc(s0 + L::ST + part * L::PART, 16);
 #pragma unroll
                 for (int k = 0; k < DP / 16; ++k)
-                    mma_f16(tm + T::DCI, sw_step(dyk, k / 4 * SSLAB + k % 4 * 32), sw_step(dz, k / 4 * 8192 + k % 4 * 32),
-                            id_m, part < 2 || k > 0);
+                    mma_f16(tm + T::DCI, sw_step(dyk, k / 4 * L::SLAB + k % 4 * 32),
+                            sw_step(dz, k / 4 * L::PSLAB + k % 4 * 32), id_m, part < 2 || k > 0);
             }
 #pragma unroll
-            for (int k = 0; k < SQ / 16; ++k)
-                mma_f16(tm + T::DB, sw_step(dr, k / 4 * SSLAB + k % 4 * 32), sw_step(dcn, k * 2048), id_b, 1);
+            for (int k = 0; k < Q / 16; ++k)
+                mma_f16(tm + T::DB, sw_step(dr, k / 4 * L::SLAB + k % 4 * 32), sw_step(dcn, k * 2048), id_b, 1);
 #pragma unroll
-            for (int k = 0; k < SQ / 16; ++k)
+            for (int k = 0; k < Q / 16; ++k)
                 mma_f16(tm + T::DC, sw_step(drt, k * 2048), sw_step(dbn, k * 2048), id_c, r > r0 || k > 0);
             mma_commit(&bar[4]);
         }
@@ -410,56 +432,65 @@ __global__ void __launch_bounds__(BTH, 1)
         if (tid == 0) {
 #pragma unroll
             for (int s = 0; s < DP / 64; ++s)
-                if (64 * s < d) tma_store_4d(&tm_dx, 64 * s, h, t0, b, sm + L::P + s * SSLAB);
+                if (64 * s < d) tma_store_4d(&tm_dx, 64 * s, h, t0, b, sm + L::P + s * L::SLAB);
             bulk_commit();
         }
         ok = mbar_wait(&bar[4], par);
         if (__syncthreads_or(!ok)) break;
         tc_fence_after();
         if (tid == 0 && r + 1 < r1) fetch(h + 1);
-        {  // X_0 dy: its product with c, and 2^S_t of it into dc
-            float v[16], u[16], w[16];
-            tmem_ld16(tm + lane_base + T::DCI + 16 * wj, v);
-            tmem_ld16(tm + lane_base + T::DC + 16 * wj, w);
-            tmem_wait_ld();
-            Vec16<__nv_bfloat16>::unpack(*reinterpret_cast<const uint4 *>(sm + L::C + sw_off(row, 2 * wj)), u);
-            Vec16<__nv_bfloat16>::unpack(*reinterpret_cast<const uint4 *>(sm + L::C + sw_off(row, 2 * wj + 1)), u + 8);
+        if (mine) {  // X_0 dy: its product with c, and 2^S_t of it into dc
             const float f = et[row];
             float dot = 0.f;
 #pragma unroll
-            for (int e = 0; e < 16; ++e) {
-                dot = fmaf(u[e], v[e], dot);
-                v[e] = fmaf(f, v[e], w[e]);
+            for (int c = 0; c < MW; c += 16) {
+                const int m = MW * wj + c;
+                float v[16], u[16], w[16];
+                tmem_ld16(tm + lane_base + T::DCI + m, v);
+                tmem_ld16(tm + lane_base + T::DC + m, w);
+                tmem_wait_ld();
+                const unsigned char *pc = sm + L::C + m / 64 * L::SLAB;
+                Vec16<__nv_bfloat16>::unpack(*reinterpret_cast<const uint4 *>(pc + sw_off(row, m % 64 / 8)), u);
+                Vec16<__nv_bfloat16>::unpack(*reinterpret_cast<const uint4 *>(pc + sw_off(row, m % 64 / 8 + 1)), u + 8);
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                    dot = fmaf(u[e], v[e], dot);
+                    v[e] = fmaf(f, v[e], w[e]);
+                }
+                tmem_st16(tm + lane_base + T::DC + m, v);
             }
             xin[wj * SQ + row] = dot;
-            tmem_st16(tm + lane_base + T::DC + 16 * wj, v);
         }
         tmem_wait_st();
         tc_fence_before();
         __syncthreads();
         // w, dt's gradient and the chunk's parts of the parameters': position tid
         if (tid < SQ) {
-            const int t = tid;
-            const int J = t >> 4;
-            if (t < 64) {  // sums of K per pair of groups
+            const int t = tid, J = t >> 4;
+            if (t < NG * NG) {  // sums of K per pair of groups
                 float v = 0.f;
 #pragma unroll
-                for (int e = 0; e < 16; ++e) v += ksum_t[(t >> 3) * SQ + 16 * (t & 7) + e];
+                for (int e = 0; e < 16; ++e) v += ksum_t[t / NG * SQ + 16 * (t % NG) + e];
                 blk[t] = v;
             }
             float ks = 0.f, zi = 0.f, xi = 0.f, kt = 0.f;  // kt: K of s in earlier groups
+            float ko = 0.f, kd = 0.f;
+            if (t < Q) {
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                ks += ksum_s[k * SQ + t];
-                zi += zin[k * SQ + t];
-                xi += xin[k * SQ + t];
+                for (int k = 0; k < 4; ++k) {
+                    ks += ksum_s[k * SQ + t];
+                    zi += zin[k * SQ + t];
+                    xi += xin[k * SQ + t];
+                }
+#pragma unroll
+                for (int k = 0; k < NG - 1; ++k) kt += k < J ? ksum_t[k * SQ + t] : 0.f;
+                ko = kown[t];
+                kd = ksum_t[J * SQ + t];
             }
-#pragma unroll
-            for (int k = 0; k < 7; ++k) kt += k < J ? ksum_t[k * SQ + t] : 0.f;
-            const float delta = dl[t], zf = zi * fs[t], ko = kown[t];
+            const float delta = dl[t], zf = zi * fs[t];
             // over my group, from my position on: K from earlier groups, and inside the group the running
             // difference; before my position: K to later groups.  Over the warp: the inter-chunk terms
-            float su = kt + (ksum_t[J * SQ + t] - delta * ko), sb = delta * ks;
+            float su = kt + (kd - delta * ko), sb = delta * ks;
             float iu = et[t] * xi, ib = delta * zf;
             const float own_b = sb, own_ib = ib;
 #pragma unroll
@@ -479,8 +510,8 @@ __global__ void __launch_bounds__(BTH, 1)
             float wt = su + (sb - own_b) + (iu + (ib - own_ib));
 #pragma unroll
             for (int k = 0; k < 4; ++k) wt += k > warp ? wsum[k] : k < warp ? wsum[4 + k] : 0.f;
-            for (int i = 0; i < J; ++i)  // pairs of groups around mine
-                for (int k = J + 1; k < 8; ++k) wt += blk[8 * i + k];
+            for (int i = 0; i < (J < NG ? J : 0); ++i)  // pairs of groups around mine
+                for (int k = J + 1; k < NG; ++k) wt += blk[NG * i + k];
             float cross = 0.f;
 #pragma unroll
             for (int k = 0; k < BTH / 32; ++k) cross += red[k];
@@ -514,28 +545,31 @@ __global__ void __launch_bounds__(BTH, 1)
         }
     } else {
         // db and dc of the group (or of this CTA's heads): my row, a quarter of the state rows
+        if (mine)
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-            float v[16];
-            tmem_ld16(tm + lane_base + (k ? T::DC : T::DB) + 16 * wj, v);
-            tmem_wait_ld();
-            if (row < len) {
-                const size_t at = (size_t)b * N + t0 + row;
+            for (int k = 0; k < 2 * MW / 16; ++k) {
+                const bool is_c = k >= MW / 16;
+                const int m0 = MW * wj + k % (MW / 16) * 16;
+                float v[16];
+                tmem_ld16(tm + lane_base + (is_c ? T::DC : T::DB) + m0, v);
+                tmem_wait_ld();
+                if (row < len) {
+                    const size_t at = (size_t)b * N + t0 + row;
 #pragma unroll
-                for (int e = 0; e < 16; e += 8) {
-                    const int m = 16 * wj + e;
-                    if (m >= M) break;
-                    if (ba.splits == 1) {
-                        __nv_bfloat16 *o = static_cast<__nv_bfloat16 *>(k ? a.dc : a.db) + at * (k ? a.lddc : a.lddb) + g * M + m;
-                        *reinterpret_cast<uint4 *>(o) = Vec16<__nv_bfloat16>::pack(v + e);
-                    } else {
-                        float4 *o = reinterpret_cast<float4 *>((k ? a.dc_head : a.db_head) + ((at * a.G + g) * ba.splits + split) * M + m);
-                        o[0] = make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
-                        o[1] = make_float4(v[e + 4], v[e + 5], v[e + 6], v[e + 7]);
+                    for (int e = 0; e < 16; e += 8) {
+                        const int m = m0 + e;
+                        if (m >= M) break;
+                        if (ba.splits == 1) {
+                            __nv_bfloat16 *o = static_cast<__nv_bfloat16 *>(is_c ? a.dc : a.db) + at * (is_c ? a.lddc : a.lddb) + g * M + m;
+                            *reinterpret_cast<uint4 *>(o) = Vec16<__nv_bfloat16>::pack(v + e);
+                        } else {
+                            float4 *o = reinterpret_cast<float4 *>((is_c ? a.dc_head : a.db_head) + ((at * a.G + g) * ba.splits + split) * M + m);
+                            o[0] = make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
+                            o[1] = make_float4(v[e + 4], v[e + 5], v[e + 6], v[e + 7]);
+                        }
                     }
                 }
             }
-        }
     }
     if (tid == 0) bulk_wait_all();
     tc_fence_before();
@@ -550,9 +584,10 @@ __global__ void __launch_bounds__(BTH, 1)
 
 // CTAs that share a group's heads: the fewest passes over the SMs, a head and chunk taking about 4 us
 // and a CTA's start 4 more; the partial rows of a shared group cost their traffic at about 5 TB/s.
+int ssm_bwd_tc_chunk(int M) { return M <= 64 ? 128 : 64; }
 int ssm_bwd_tc_splits(int B, int H, int N, int G, int M) {
-    const int rep = H / G;
-    const long long base = (long long)B * ((N + SQ - 1) / SQ) * G;
+    const int rep = H / G, q = ssm_bwd_tc_chunk(M);
+    const long long base = (long long)B * ((N + q - 1) / q) * G;
     int best = 1;
     double cost = 0;
     for (int s = 1; s <= rep; ++s) {
@@ -568,30 +603,30 @@ int ssm_bwd_tc_splits(int B, int H, int N, int G, int M) {
     return best;
 }
 
-template <int DP>
+template <int Q, int DP, int MP>
 static ida_status launch_bwd_tc_d(const BwdTcArgs &ba, cudaStream_t st) {
     const ScanBwdArgs &a = ba.s;
-    constexpr int smem = BwdSmem<DP>::TOTAL;
+    constexpr int smem = BwdSmem<Q, DP, MP>::TOTAL;
     static_assert(smem <= 227 * 1024, "shared memory budget");
     CUtensorMap mx, mdy, mb, mc, mdx;
-    ida_status s = ssm_map(&mx, a.x, a.B, a.N, a.H, a.d, a.ldx);
-    if (s == IDA_OK) s = ssm_map(&mdy, a.dy, a.B, a.N, a.H, a.d, (long long)a.H * a.d);
-    if (s == IDA_OK) s = ssm_map(&mb, a.b, a.B, a.N, a.G, a.M, a.ldb);
-    if (s == IDA_OK) s = ssm_map(&mc, a.c, a.B, a.N, a.G, a.M, a.ldc);
-    if (s == IDA_OK) s = ssm_map(&mdx, a.dx, a.B, a.N, a.H, a.d, a.lddx);
+    ida_status s = ssm_map(&mx, a.x, a.B, a.N, a.H, a.d, a.ldx, Q);
+    if (s == IDA_OK) s = ssm_map(&mdy, a.dy, a.B, a.N, a.H, a.d, (long long)a.H * a.d, Q);
+    if (s == IDA_OK) s = ssm_map(&mb, a.b, a.B, a.N, a.G, a.M, a.ldb, Q);
+    if (s == IDA_OK) s = ssm_map(&mc, a.c, a.B, a.N, a.G, a.M, a.ldc, Q);
+    if (s == IDA_OK) s = ssm_map(&mdx, a.dx, a.B, a.N, a.H, a.d, a.lddx, Q);
     if (s != IDA_OK) return s;
-    cudaError_t e = cudaFuncSetAttribute(ssm_bwd_tc_kernel<DP>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    cudaError_t e = cudaFuncSetAttribute(ssm_bwd_tc_kernel<Q, DP, MP>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return fail_with(IDA_ERR_CUDA, cudaGetErrorString(e));
     const long long ctas = (long long)a.B * a.chunks * a.G * ba.splits;
     if (ctas > 0x7FFFFFFFLL) return fail_with(IDA_ERR_UNSUPPORTED, "too many positions and groups");
-    ssm_bwd_tc_kernel<DP><<<(unsigned)ctas, BTH, smem, st>>>(ba, mx, mdy, mb, mc, mdx);
+    ssm_bwd_tc_kernel<Q, DP, MP><<<(unsigned)ctas, BTH, smem, st>>>(ba, mx, mdy, mb, mc, mdx);
     return launched("ssm scan backward");
 }
 
 // The chunk states, forwards and backwards, from zero.
 ida_status launch_bwd_tc_states(const ScanBwdArgs &a, cudaStream_t st) {
     ScanArgs f = {a.x, a.b, a.c, a.dt, a.a_log, a.dt_bias, a.D, nullptr, nullptr, nullptr, a.B, a.H, a.N, a.d, a.G, a.M,
-                  a.ldx, a.ldb, a.ldc, a.lddt, SQ, a.chunks, a.chunks, a.state0, a.chunk_log, a.err};
+                  a.ldx, a.ldb, a.ldc, a.lddt, a.chunk, a.chunks, a.chunks, a.state0, a.chunk_log, a.err};
     ida_status s = launch_ssm_states(f, true, false, st);
     if (s != IDA_OK) return s;
     f.x = a.dy;
@@ -604,7 +639,8 @@ ida_status launch_bwd_tc_states(const ScanBwdArgs &a, cudaStream_t st) {
 
 ida_status launch_bwd_tc(const ScanBwdArgs &a, int splits, cudaStream_t st) {
     const BwdTcArgs ba = {a, splits};
-    return a.d <= 64 ? launch_bwd_tc_d<64>(ba, st) : launch_bwd_tc_d<128>(ba, st);
+    if (a.M <= 64) return a.d <= 64 ? launch_bwd_tc_d<128, 64, 64>(ba, st) : launch_bwd_tc_d<128, 128, 64>(ba, st);
+    return a.d <= 64 ? launch_bwd_tc_d<64, 64, 128>(ba, st) : launch_bwd_tc_d<64, 128, 128>(ba, st);
 }
 
 }  // namespace ida

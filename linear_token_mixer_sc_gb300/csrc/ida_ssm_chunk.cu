@@ -443,7 +443,7 @@ __global__ void __launch_bounds__(STH, MP == 64 ? 2 : 1)
         if (start_of(n) + k < t_end) delta = softplus(dt_next + dt_bias);
         long long all;
         const long long fx = chunk_sum(rate2, delta, k, tot, all);
-        arrays[(n & 1) * SQ + k] = REV ? ex2_fix(fx + behind) : ex2_fix(all - fx + behind) * delta;
+        arrays[(n & 1) * SQ + k] = REV ? (start_of(n) + k < t_end ? ex2_fix(fx + behind) : 0.f) : ex2_fix(all - fx + behind) * delta;
         behind += all;
     };
     fetch_dt(0);
@@ -618,12 +618,12 @@ static SsmEncodeFn ssm_encode_fn() {
     return fn;
 }
 
-ida_status ssm_map(CUtensorMap *m, const void *p, int B, int N, int K, int w, long long ld) {
+ida_status ssm_map(CUtensorMap *m, const void *p, int B, int N, int K, int w, long long ld, int rows) {
     const SsmEncodeFn fn = ssm_encode_fn();
     if (!fn) return fail_with(IDA_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
     const cuuint64_t dims[4] = {(cuuint64_t)w, (cuuint64_t)K, (cuuint64_t)N, (cuuint64_t)B};
     const cuuint64_t strides[3] = {(cuuint64_t)w * 2, (cuuint64_t)ld * 2, (cuuint64_t)N * ld * 2};
-    const cuuint32_t box[4] = {64, 1, SQ, 1}, one[4] = {1, 1, 1, 1};
+    const cuuint32_t box[4] = {64, 1, (cuuint32_t)rows, 1}, one[4] = {1, 1, 1, 1};
     const CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(p), dims, strides, box, one,
                           CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);

@@ -80,9 +80,9 @@ __device__ __forceinline__ long long chunk_sum(double rate2, float delta, int k,
 // ---- host side ---------------------------------------------------------------------------
 
 // Rows of B x N positions, ld elements apart, of K units of w bf16 channels each, as a tensor map
-// (channel, unit, position, row) with boxes of 64 channels of one unit over 128 positions.  Channels
+// (channel, unit, position, row) with boxes of 64 channels of one unit over `rows` positions.  Channels
 // behind w and positions behind N are read as zero and not written.
-ida_status ssm_map(CUtensorMap *m, const void *p, int B, int N, int K, int w, long long ld);
+ida_status ssm_map(CUtensorMap *m, const void *p, int B, int N, int K, int w, long long ld, int rows = SQ);
 
 // Each segment's last state from zero (from state_in for the first), with rev the sum
 // sum_t a_first .. a_t c_t dy_t^T of the adjoint it passes on; a.x, a.b and their strides then are

@@ -261,6 +261,8 @@ GRADS = [
     (1, 128, 2, 128, 1, 128, "bf16", False, False), (1, 77, 4, 40, 2, 24, "f32", False, False),
     (2, 190, 2, 72, 1, 40, "bf16", False, False), (1, 100, 2, 64, 1, 64, "bf16", False, True),
     (1, 90, 2, 32, 2, 32, "f32", False, True), (1, 140, 1, 256, 1, 128, "bf16", False, False),
+    (2, 150, 4, 64, 2, 128, "bf16", False, False), (1, 200, 6, 128, 1, 104, "bf16", False, False),
+    (1, 260, 3, 16, 3, 72, "bf16", False, True), (1, 300, 5, 64, 1, 16, "bf16", False, False),
 ]
 NAMES = ("x", "b", "c", "dt", "a_log", "dt_bias", "D")
 
