@@ -17,9 +17,10 @@ struct ScanArgs {
     int B, H, N, d, G, M;
     long long ldx, ldb, ldc, lddt;
     int seg, segs;      // positions per segment, segments per sequence
-    int state_segs;     // segments whose last state from zero a first launch leaves in seg_state
-    float *seg_state;   // [B H][segs][M][d]: each segment's last state from zero
-    float *seg_log;     // [B H][segs]: the sum of log a over the segment (of log2 a on the tensor cores)
+    int fine;           // parts of a segment that a first launch takes by themselves (tensor cores)
+    int state_segs;     // parts whose last state from zero that launch leaves in seg_state
+    float *seg_state;   // [B H][segs fine][M][d]: each part's last state from zero
+    float *seg_log;     // [B H][segs fine]: the sum of log a over the part (of log2 a on the tensor cores)
     unsigned *err;
 };
 

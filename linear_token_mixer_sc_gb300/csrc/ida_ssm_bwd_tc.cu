@@ -208,7 +208,7 @@ __global__ void __launch_bounds__(BTH, 1)
                 delta = softplus(z);
             }
             long long all;
-            const long long fx = chunk_sum(log2_rate(a.a_log[h]), delta, tid, tot, all);
+            const long long fx = chunk_sum(Rate2(a.a_log[h]), delta, tid, tot, all);
             const float hi = (float)fx * kUnfix;
             // S at the end of the block of 16 before mine
             const int edge = (lane & 16) - 1;
@@ -626,7 +626,7 @@ static ida_status launch_bwd_tc_d(const BwdTcArgs &ba, cudaStream_t st) {
 // The chunk states, forwards and backwards, from zero.
 ida_status launch_bwd_tc_states(const ScanBwdArgs &a, cudaStream_t st) {
     ScanArgs f = {a.x, a.b, a.c, a.dt, a.a_log, a.dt_bias, a.D, nullptr, nullptr, nullptr, a.B, a.H, a.N, a.d, a.G, a.M,
-                  a.ldx, a.ldb, a.ldc, a.lddt, a.chunk, a.chunks, a.chunks, a.state0, a.chunk_log, a.err};
+                  a.ldx, a.ldb, a.ldc, a.lddt, a.chunk, a.chunks, 1, a.chunks, a.state0, a.chunk_log, a.err};
     ida_status s = launch_ssm_states(f, true, false, st);
     if (s != IDA_OK) return s;
     f.x = a.dy;

@@ -4,34 +4,41 @@
 // state before it and X_Q the state behind it (see ida_ssm.cuh for the recurrence):
 //   G    [t][s]  = c_t . b_s                                   MMA, K = M
 //   P    [t][s]  = G 2^(S_t - S_s) D_s (s <= t), + D at s = t  CUDA cores, G from TMEM, P to TMEM
-//   Y    [t][j]  = P x + (c_t 2^S_t) X_0                       MMA, K = Q and K = M
+//   Y    [t][j]  = P x + 2^S_t (c_t X_0)                       MMAs, K = Q and K = M
 //   X_Q^T [j][m] = 2^S_Q X_0^T + x^T (b_s 2^(S_Q - S_s) D_s)   scaled in TMEM, then MMA, K = Q
 // No factor exceeds 1 (but D_s): decays are differences of S taken before the exponential.
 //
-// Precision.  Everything accumulates in fp32.  P, c 2^S, the X_0 operand and, where only y comes
-// of it, the scaled b are rounded to bf16 (each 2^-9 of a term on average, below y's own
-// rounding).  States that leave the kernel (the final state, and a segment's last state, which the
+// Precision.  Everything accumulates in fp32.  P, the X_0 operand and, where only y comes of it, the
+// scaled b are rounded to bf16 (each 2^-9 of a term on average, as y's own rounding); c is not:
+// 2^S_t scales the rows of c X_0.  States that leave the kernel (the final state, and a segment's last state, which the
 // next one starts from) are fp32 results: for them the scaled b is kept as the sum of three bf16
 // tiles, all 24 bits.  S is summed in 2^-32 fixed point: it is exact over any chunk or segment.
 //
-// One CTA of 256 threads walks the chunks of one (row, head, up to 128 channels, segment).  x, b
-// and c tiles arrive by TMA with the 128-byte swizzle that the MMA descriptors name, so one copy
-// serves as a K-major operand (b, c in G) and as an MN-major one (x, b in the state update, whose K
-// is the position).  P is an A operand in TMEM: thread t of a lane quarter makes row t of it from
-// row t of G.  The state stays in TMEM; y leaves through shared memory that is dead by then, by TMA.
-// With M <= 64 two CTAs share an SM (256 TMEM columns and 75 or 101 KB each) and fill each other's
-// waits: a chunk is a chain of copy, MMA, CUDA-core stage, MMA, epilogue.  The lower triangle gives
-// the lane quarters of P 1 to 4 blocks of columns per warp; the scaling of b and c is dealt out so
-// that all warps have the same total.
+// One CTA per SM walks the chunks of one (row, head, up to 128 channels, segment), its warps in
+// roles that hand chunks on through mbarriers, so that a chunk's copy, MMAs, CUDA-core stages and
+// output overlap its neighbours':
+//   warp 0      copies: x, b and c by TMA, two chunks ahead where shared memory allows
+//   warp 1      issues all MMAs
+//   warps 4-7   the step sizes' sums and exponentials of the next chunk
+//   warps 8-15  P: thread t of a lane quarter makes row t from row t of G, in G's own place in TMEM
+//               (each half of a row is read and replaced by one warp), an A operand there
+//   warps 16-19 the rows of (c X_0) in Y scaled by 2^S_t before P x is added to them, y out by TMA
+//   warps 20-23 b scaled in place; the state's bf16 copy for Y and its decay in TMEM
+// (All stages in one group of 256 threads, two CTAs per SM: 45 us for 4 x 4096 positions of 16
+// heads of 128, 8500 cycles a chunk, most of them waits for the next stage.)
+// The tiles have the 128-byte swizzle that the MMA descriptors name, so one copy serves as a
+// K-major operand (b, c in G) and as an MN-major one (x, b in the state update, whose K is the
+// position).  The state stays in TMEM.
 //
 // Few (row, head) units do not fill the SMs: sequences are cut into segments.  A first launch
-// (ssm_state_kernel: x and b only) leaves each segment's last state from zero, a second the states
-// the segments start from, and the final state.  The state kernel walks a segment backwards, where
-// the decay from a position to the segment's end is known without a look ahead, so its MMAs only
-// accumulate and the copies and the scaling of the next chunk run beside them.
+// (ssm_state_kernel: x and b only) leaves the last states from zero of parts of the segments, a
+// second the states the segments start from, and the final state.  The state kernel walks a part
+// backwards, where the decay from a position to the part's end is known without a look ahead, so its
+// MMAs only accumulate and the copies and the scaling of the next chunk run beside them.
 //
-// Every wait is bounded.  On a timeout all threads of the CTA leave the loop together, the kernel
-// records kErrWaitTimeout, waits (bounded) for its copy in flight, frees its TMEM and returns.
+// Every wait is bounded.  On a timeout the warps of a role leave their loop together (the others
+// run out of waits of their own), the kernel records kErrWaitTimeout, waits (bounded) for its copies
+// in flight, frees its TMEM and returns.
 #include <mutex>
 
 #include "ida_ssm_tc.cuh"
@@ -40,24 +47,44 @@ namespace ida {
 
 using namespace tc;
 
-constexpr int STH = 256;  // threads per CTA
+constexpr int STH = 256;   // threads per CTA of the state kernel
+constexpr int CTH = 768;   // threads per CTA of the chunk kernel
+
+// The chunk kernel's mbarriers: those of chunk i, or of chunks i with the same i % 2.
+enum {
+    kFullBC = 0,   // [2] b and c are there
+    kFreeBC = 2,   // [2] their buffer may be overwritten
+    kFullX = 4,    // [2] x
+    kFreeX = 6,    // [2]
+    kG = 8,        // [2] G is complete
+    kArr = 10,     // [2] the chunk's arrays are there
+    kP = 12,       // [2] P is complete
+    kY = 14,       // [2] Y is complete
+    kScaled = 16,  // scaled b, the state's bf16 copy and its decay
+    kState = 17,   // the state update is complete
+    kCX = 18,      // c X_0 is complete
+    kRows = 19,    // its rows are scaled
+    kFreeY = 20,   // Y has been read
+    kOut = 21,     // the output tile has left shared memory
+    kBars = 22
+};
 
 // Shared memory map; DP, MP: channels and state rows rounded up to 64 or 128.
-constexpr int SARR = 5 * SQ + 16;  // floats of one chunk's arrays (StepArrays)
+constexpr int SARR = 5 * SQ + 32;  // floats of one chunk's arrays (StepArrays)
 template <int DP, int MP>
 struct SsmSmem {
-    static constexpr int X = 0;                            // [DP / 64][128 s][64] bf16
-    static constexpr int B = X + DP / 64 * SSLAB;          // [MP / 64][128 s][64]: b, then scaled
-    static constexpr int C = B + MP / 64 * SSLAB;          // [MP / 64][128 t][64]: c, then scaled
-    static constexpr int SBS = DP * 128;                   // bytes of one slab of SB
-    static constexpr int SB = C + MP / 64 * SSLAB;         // [MP / 64][DP j][64]: X_0^T
-    // the output tile [DP / 64][128 t][64]: over SB, and a slab of its own where SB is smaller
-    static constexpr int SB_BYTES = MP / 64 * SBS, OUT_BYTES = DP / 64 * SSLAB;
-    static constexpr int OUT0 = DP == 64 && MP == 64 ? SB + SB_BYTES : SB;
-    static constexpr int OUT1 = SB + SSLAB;
-    static constexpr int MISC = OUT_BYTES > SB_BYTES ? SB + SB_BYTES + SSLAB : SB + SB_BYTES;
-    static constexpr int ARR = MISC + 64;                  // two chunks' arrays
-    static constexpr int TOT = ARR + 2 * SARR * 4;         // 4 64-bit totals
+    static constexpr int NX = DP == 128 && MP == 128 ? 1 : 2;  // buffers of x
+    static constexpr int XB = DP / 64 * SSLAB, BB = MP / 64 * SSLAB;
+    static constexpr int X = 0;                    // [NX][DP / 64][128 s][64] bf16
+    static constexpr int B = X + NX * XB;          // [2][MP / 64][128 s][64]: b, then scaled
+    static constexpr int C = B + 2 * BB;           // [2][MP / 64][128 t][64]
+    static constexpr int SBS = DP * 128;           // bytes of one slab of SB
+    static constexpr int SB = C + 2 * BB;          // [MP / 64][DP j][64]: X_0^T
+    static constexpr bool OUT_OVER_SB = NX == 1;   // the output tile [DP / 64][128 t][64], where it does not fit beside SB
+    static constexpr int OUT = OUT_OVER_SB ? SB : SB + MP / 64 * SBS;
+    static constexpr int MISC = OUT + XB;
+    static constexpr int ARR = MISC + 256;         // two chunks' arrays
+    static constexpr int TOT = ARR + 2 * SARR * 4; // 4 64-bit totals
     static constexpr int TOTAL = TOT + 32;
 };
 // PARTS: bf16 tiles that the scaled b is kept in.  With one, two chunks are in flight.
@@ -73,40 +100,53 @@ struct SsmStateSmem {
     static constexpr int TOTAL = TOT + 32;
 };
 
-template <int DP, int MP>
-struct SsmTmem {
-    static constexpr uint32_t G = 0;    // [t][s], later Y [t][j]
-    static constexpr uint32_t P = 128;  // [t][s] bf16 pairs
-    static constexpr uint32_t S = 192;  // [j][m]; with DP = 64 lanes 64.. repeat 0..63
-    static constexpr uint32_t COLS = MP == 64 ? 256 : 512;
-};
+// TMEM columns: G of two chunks ([t][s]; P of each in its place, bf16 pairs of s 64 h .. at 64 h ..),
+// Y [t][j], the state [j][m] (with DP = 64 lanes 64.. repeat 0..63).
+constexpr uint32_t TG = 0, TY = 256, TS = 384, TCOLS = 512;
 
 // What a chunk's step sizes give, for the positions s of the chunk.
 struct StepArrays {
     float *cumf;  // S_s
     float *uf;    // S_s - log2 D_s
     float *rs;    // 2^(S at the end of s's block of 16 - uf)
-    float *wst;   // 2^(S_Q - S_s) D_s
     float *et;    // 2^S_s
-    float *cref;  // S at the end of each block of 16; [8]: 2^S_Q
+    float *wst;   // 2^(S_Q - S_s) D_s
+    float *cref;  // S at the end of each block of 16
+    float *span;  // how far S falls from the first to the last position of each block
+    float *decay; // 2^S_Q
     __device__ __forceinline__ StepArrays(float *p)
-        : cumf(p), uf(p + SQ), rs(p + 2 * SQ), wst(p + 3 * SQ), et(p + 4 * SQ), cref(p + 5 * SQ) {}
+        : cumf(p), uf(p + SQ), rs(p + 2 * SQ), et(p + 3 * SQ), wst(p + 4 * SQ), cref(p + 5 * SQ), span(p + 5 * SQ + 8),
+          decay(p + 5 * SQ + 16) {}
 };
 
+__device__ __forceinline__ void mbar_arrive(uint64_t *bar) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+// whether `p` holds in any of n threads, which all get the answer
+__device__ __forceinline__ bool named_any(int id, int n, bool p) {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %3, 0;\n\tbarrier.cta.red.or.pred q, %1, %2, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(r)
+        : "r"(id), "r"(n), "r"((uint32_t)p)
+        : "memory");
+    return r != 0;
+}
+
 template <int DP, int MP>
-__global__ void __launch_bounds__(STH, MP == 64 ? 2 : 1)
+__global__ void __launch_bounds__(CTH, 1)
     ssm_chunk_kernel(ScanArgs a, const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_b,
                      const __grid_constant__ CUtensorMap tm_c, const __grid_constant__ CUtensorMap tm_y) {
     using L = SsmSmem<DP, MP>;
-    using T = SsmTmem<DP, MP>;
     extern __shared__ __align__(1024) unsigned char sm[];
     const uint32_t s0 = smem_u32(sm);
-    uint64_t *bar = reinterpret_cast<uint64_t *>(sm + L::MISC);  // 0 copies, 1 G, 2 Y, 3 state
-    uint32_t *tslot = reinterpret_cast<uint32_t *>(sm + L::MISC + 48);
+    uint64_t *bar = reinterpret_cast<uint64_t *>(sm + L::MISC);
+    uint32_t *tslot = reinterpret_cast<uint32_t *>(sm + L::MISC + 8 * kBars);
+    uint32_t *failed = tslot + 1;
     float *arrays = reinterpret_cast<float *>(sm + L::ARR);
     long long *tot = reinterpret_cast<long long *>(sm + L::TOT);
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
-    const int q4 = warp & 3, half = warp >> 2, tl = 32 * q4 + lane;
+    const int q4 = warp & 3, tl = 32 * q4 + lane;  // the lane quarter of TMEM this warp reaches, and its lane
     const uint32_t lane_base = (uint32_t)(32 * q4) << 16;
     const int H = a.H, N = a.N, M = a.M, d = a.d;
     const int slices = (d + DP - 1) / DP;
@@ -115,265 +155,374 @@ __global__ void __launch_bounds__(STH, MP == 64 ? 2 : 1)
     id /= a.segs;
     const int j0 = id % slices * DP, unit = id / slices, b = unit / H, h = unit % H, g = h / (H / a.G);
     const int t_begin = seg * a.seg, t_end = min(N, t_begin + a.seg), nch = (t_end - t_begin + SQ - 1) / SQ;
-    const __nv_bfloat16 *gdt = static_cast<const __nv_bfloat16 *>(a.dt) + (size_t)b * N * a.lddt + h;
-    const float dt_bias = a.dt_bias[h], skip = a.D[h];
-    const double rate2 = log2_rate(a.a_log[h]);
-    constexpr uint32_t TILE_BYTES = (uint32_t)SSLAB * (DP / 64 + 2 * (MP / 64));
 
     if ((s0 & 1023u) != 0u) {  // the swizzle repeats every 1024 bytes
         if (tid == 0) report_error(a.err, kErrShape);
         return;
     }
     if (tid == 0) {
-        for (int i = 0; i < 4; ++i) mbar_init(&bar[i], 1);
+        for (int i = 0; i < kBars; ++i)
+            mbar_init(&bar[i], i == kP || i == kP + 1 ? 8 : i == kArr || i == kArr + 1 || i == kScaled || i == kRows || i == kFreeY ? 4 : 1);
         fence_mbar_init();
+        *failed = 0;
         tma_prefetch_desc(&tm_x);
         tma_prefetch_desc(&tm_b);
         tma_prefetch_desc(&tm_c);
         tma_prefetch_desc(&tm_y);
     }
-    if (warp == 0) {
-        tmem_alloc(tslot, T::COLS);
+    if (warp == 1) {
+        tmem_alloc(tslot, TCOLS);
         tmem_relinquish();
     }
-    const auto fetch = [&](int t0) {  // one thread
-        mbar_arrive_expect_tx(&bar[0], TILE_BYTES);
-#pragma unroll
-        for (int i = 0; i < MP / 64; ++i) {
-            tma_load_4d(sm + L::B + i * SSLAB, &tm_b, 64 * i, g, t0, b, &bar[0]);
-            tma_load_4d(sm + L::C + i * SSLAB, &tm_c, 64 * i, g, t0, b, &bar[0]);
-        }
-#pragma unroll
-        for (int i = 0; i < DP / 64; ++i) tma_load_4d(sm + L::X + i * SSLAB, &tm_x, j0 + 64 * i, h, t0, b, &bar[0]);
-    };
-    // the arrays of the chunk at t0, by warps 4 .. 7, into buffer `buf`; its raw steps were read before
-    float dt_next = 0.f;
-    const auto fetch_dt = [&](int t0) {
-        const int k = tid - SQ;
-        if (k >= 0) dt_next = t0 + k < t_end ? __bfloat162float(gdt[(size_t)(t0 + k) * a.lddt]) : 0.f;
-    };
-    const auto make_arrays = [&](int t0, int buf) {
-        const int k = tid - SQ;
-        if (k < 0) return;
-        float delta = 0.f;
-        if (t0 + k < t_end) delta = softplus(dt_next + dt_bias);  // behind the end nothing decays or is added
-        long long all;
-        const long long fx = chunk_sum(rate2, delta, k, tot, all);
-        const StepArrays A(arrays + buf * SARR);
-        const float s = (float)fx * kUnfix, u = s - log2f(delta);  // D = 0: +inf, and 2^(.. - u) = 0
-        const float ref = __shfl_sync(0xffffffffu, s, lane | 15);
-        A.cumf[k] = s;
-        A.uf[k] = u;
-        A.rs[k] = ex2(ref - u);
-        A.wst[k] = ex2((float)(all - fx) * kUnfix) * delta;
-        A.et[k] = ex2(s);
-        if ((lane & 15) == 15) A.cref[k >> 4] = s;
-        if (k == 0) A.cref[8] = ex2((float)all * kUnfix);
-    };
-    fetch_dt(t_begin);
     __syncthreads();
-    if (tid == 0) fetch(t_begin);
-    make_arrays(t_begin, 0);
-    fetch_dt(t_begin + SQ);
     tc_fence_after();
     const uint32_t tm = *tslot;
-    constexpr int MH = MP / 2;  // state rows of a warp half
-    {
-        // the state before the segment
-        const int ch = DP == 64 ? (tl & 63) : tl;  // my channel; with DP = 64 lanes 64.. repeat 0..63
-        const float *p = a.segs > 1 ? a.seg_state + ((size_t)unit * a.segs + seg) * M * d
-                                    : (a.state_in ? a.state_in + (size_t)unit * M * d : nullptr);
-        const bool mine = p && j0 + ch < d;
-#pragma unroll
-        for (int blk = 0; blk < MH / 16; ++blk) {
-            const int m0 = half * MH + 16 * blk;
-            float v[16];
-#pragma unroll
-            for (int e = 0; e < 16; ++e)
-                v[e] = mine && m0 + e < M ? __ldg(p + (size_t)(m0 + e) * d + j0 + ch) : 0.f;
-            tmem_st16(tm + lane_base + T::S + m0, v);
-        }
-        tmem_wait_st();
-    }
+    const auto wait = [&](int k, uint32_t parity) { return mbar_wait(&bar[k], parity); };
     bool ok = true;
-    int i = 0;
-    for (; i < nch; ++i) {
-        const int t0 = t_begin + i * SQ;
-        const uint32_t par = i & 1;
-        const StepArrays A(arrays + par * SARR);
-        ok = mbar_wait(&bar[0], par) && ok;
-        if (__syncthreads_or(!ok)) break;  // the tiles and this chunk's arrays are there, the last state update is done
-        tc_fence_after();
-        if (warp == 0 && elect_one()) {
-            const SmemDesc da = sw_desc(s0 + L::C, 16), db = sw_desc(s0 + L::B, 16);
+
+    if (warp == 0) {
+        if (lane == 0) {
+            int i = 0;
+            for (; i < nch && ok; ++i) {
+                const int t0 = t_begin + i * SQ, c = i & 1, x = i % L::NX;
+                if (i >= 2) ok = wait(kFreeBC + c, ((i >> 1) - 1) & 1);
+                if (!ok) break;
+                mbar_arrive_expect_tx(&bar[kFullBC + c], 2 * L::BB);
+#pragma unroll
+                for (int k = 0; k < MP / 64; ++k) {
+                    tma_load_4d(sm + L::B + c * L::BB + k * SSLAB, &tm_b, 64 * k, g, t0, b, &bar[kFullBC + c]);
+                    tma_load_4d(sm + L::C + c * L::BB + k * SSLAB, &tm_c, 64 * k, g, t0, b, &bar[kFullBC + c]);
+                }
+                if (i >= L::NX) ok = wait(kFreeX + x, (i / L::NX - 1) & 1);
+                if (!ok) break;
+                mbar_arrive_expect_tx(&bar[kFullX + x], L::XB);
+#pragma unroll
+                for (int k = 0; k < DP / 64; ++k)
+                    tma_load_4d(sm + L::X + x * L::XB + k * SSLAB, &tm_x, j0 + 64 * k, h, t0, b, &bar[kFullX + x]);
+            }
+            if (!ok) {  // the copies in flight: this chunk's b and c, and the two before it
+                wait(kFullBC + (i & 1), (i >> 1) & 1);
+                if (i > 0) {
+                    wait(kFullBC + ((i - 1) & 1), ((i - 1) >> 1) & 1);
+                    wait(kFullX + (i - 1) % L::NX, ((i - 1) / L::NX) & 1);
+                }
+            }
+        }
+    } else if (warp == 1) {
+        // all lanes wait, one issues: a uniform branch, which the MMAs' operands want (issued from a branch
+        // on the lane they took three times as long)
+        const auto issue_g = [&](int i) {
+            const SmemDesc dc = sw_desc(s0 + L::C + (i & 1) * L::BB, 16), db = sw_desc(s0 + L::B + (i & 1) * L::BB, 16);
             constexpr uint32_t id_g = idesc(128, 128, 1, 1);
 #pragma unroll
             for (int k = 0; k < MP / 16; ++k) {
                 const uint32_t off = (k / 4) * SSLAB + (k % 4) * 32;
-                mma_f16(tm + T::G, sw_step(da, off), sw_step(db, off), id_g, k > 0);
+                mma_f16(tm + TG + 128 * (i & 1), sw_step(dc, off), sw_step(db, off), id_g, k > 0);
             }
-            mma_commit(&bar[1]);
-        }
-        __syncwarp();
-        // the state: its bf16 copy for Y, kept until SB is free, and its decay over the chunk
-        uint32_t sb[MH / 2];
-        const float decay = A.cref[8];
+            mma_commit(&bar[kG + (i & 1)]);
+        };
+        const auto all_wait = [&](int k, uint32_t parity) { return !__any_sync(0xffffffffu, !wait(k, parity)); };
+        ok = all_wait(kFullBC, 0);
+        if (ok && elect_one()) issue_g(0);
+        for (int i = 0; i < nch && ok; ++i) {
+            const int c = i & 1, x = i % L::NX;
+            const uint32_t par = i & 1;
+            ok = all_wait(kScaled, par) && all_wait(kFullX + x, (i / L::NX) & 1);
+            if (!ok) break;
+            if (elect_one()) {
+                tc_fence_after();
+                // x^T as A: with DP = 64 its second 64 rows repeat the first
+                const SmemDesc da = sw_desc(s0 + L::X + x * L::XB, DP == 64 ? 0 : SSLAB);
+                const SmemDesc dh = sw_desc(s0 + L::B + c * L::BB, SSLAB);
+                constexpr uint32_t id_x = idesc(128, MP, 1, 1, 1, 1);
 #pragma unroll
-        for (int blk = 0; blk < MH / 32; ++blk) {
-            const uint32_t at = tm + lane_base + T::S + half * MH + 32 * blk;
-            float v[32];
-            tmem_ld16(at, v);
-            tmem_ld16(at + 16, v + 16);
-            tmem_wait_ld();
-#pragma unroll
-            for (int e = 0; e < 16; ++e) sb[16 * blk + e] = pack_bf16(v[2 * e], v[2 * e + 1]);
-#pragma unroll
-            for (int e = 0; e < 32; ++e) v[e] *= decay;
-            tmem_st16(at, v);
-            tmem_st16(at + 16, v + 16);
-        }
-        if (tid == 0) bulk_wait_read_all();  // y of the last chunk has left shared memory
-        ok = mbar_wait(&bar[1], par);
-        if (__syncthreads_or(!ok)) break;
-        tc_fence_after();
-        if (tl < DP)
-#pragma unroll
-            for (int c = 0; c < MH / 8; ++c) {
-                const int p = half * (MH / 8) + c;  // 16-byte piece of row tl
-                *reinterpret_cast<uint4 *>(sm + L::SB + p / 8 * L::SBS + sw_off(tl, p % 8)) =
-                    make_uint4(sb[4 * c], sb[4 * c + 1], sb[4 * c + 2], sb[4 * c + 3]);
+                for (int k = 0; k < SQ / 16; ++k) mma_f16(tm + TS, sw_step(da, k * 2048), sw_step(dh, k * 2048), id_x, 1);
+                mma_commit(&bar[kState]);
             }
+            __syncwarp();
+            if (i + 1 < nch) {  // in the place of P of chunk i - 1, which the MMAs before have read
+                ok = all_wait(kFullBC + (c ^ 1), ((i + 1) >> 1) & 1);
+                if (!ok) break;
+                if (elect_one()) issue_g(i + 1);
+                __syncwarp();
+            }
+            if (i > 0) ok = all_wait(kFreeY, par ^ 1);
+            if (!ok) break;
+            if (elect_one()) {
+                tc_fence_after();
+                const SmemDesc dc = sw_desc(s0 + L::C + c * L::BB, 16), ds = sw_desc(s0 + L::SB, 16);
+                constexpr uint32_t id_s = idesc(128, DP, 1, 1);
+#pragma unroll
+                for (int k = 0; k < MP / 16; ++k)
+                    mma_f16(tm + TY, sw_step(dc, k / 4 * SSLAB + k % 4 * 32), sw_step(ds, k / 4 * L::SBS + k % 4 * 32), id_s, k > 0);
+                mma_commit(&bar[kCX]);
+                mma_commit(&bar[kFreeBC + c]);
+            }
+            __syncwarp();
+            ok = all_wait(kRows, par) && all_wait(kP + c, (i >> 1) & 1);
+            if (!ok) break;
+            if (elect_one()) {
+                tc_fence_after();
+                const SmemDesc dx = sw_desc(s0 + L::X + x * L::XB, SSLAB);  // [K = s][j]
+                constexpr uint32_t id_p = idesc(128, DP, 1, 1, 0, 1);
+#pragma unroll
+                for (int k = 0; k < SQ / 16; ++k)
+                    mma_f16_t(tm + TY, tm + TG + 128 * c + 64 * (k / 4) + 8 * (k % 4), sw_step(dx, k * 2048), id_p, 1);
+                mma_commit(&bar[kY + c]);
+                mma_commit(&bar[kFreeX + x]);
+            }
+            __syncwarp();
+        }
+    } else if (warp >= 4 && warp < 8) {
+        const int k = tid - 128;  // position of the chunk
+        const __nv_bfloat16 *gdt = static_cast<const __nv_bfloat16 *>(a.dt) + (size_t)b * N * a.lddt + h;
+        const float dt_bias = a.dt_bias[h];
+        const Rate2 rate(a.a_log[h]);
+        const auto dt_of = [&](int i) {
+            const int p = t_begin + i * SQ + k;
+            return p < t_end ? __bfloat162float(gdt[(size_t)p * a.lddt]) : 0.f;
+        };
+        float dt_next = dt_of(0);
+        for (int i = 0; i < nch; ++i) {
+            const float dt_now = dt_next;
+            if (i + 1 < nch) dt_next = dt_of(i + 1);
+            if (i >= 2) ok = wait(kY + (i & 1), ((i - 2) >> 1) & 1);  // the arrays of chunk i - 2 have been used
+            if (named_any(1, 128, !ok)) {
+                ok = false;
+                break;
+            }
+            float delta = 0.f;
+            if (t_begin + i * SQ + k < t_end) delta = softplus(dt_now + dt_bias);  // behind the end nothing decays or is added
+            long long all;
+            const long long fx = chunk_sum(rate, delta, k, tot, all);
+            const StepArrays A(arrays + (i & 1) * SARR);
+            const float s = (float)fx * kUnfix, u = s - log2f(delta);  // D = 0: +inf, and 2^(.. - u) = 0
+            const float ref = __shfl_sync(0xffffffffu, s, lane | 15), first = __shfl_sync(0xffffffffu, s, lane & 16);
+            A.cumf[k] = s;
+            A.uf[k] = u;
+            A.rs[k] = ex2(ref - u);
+            A.et[k] = ex2(s);
+            A.wst[k] = ex2((float)(all - fx) * kUnfix) * delta;
+            if ((lane & 15) == 15) {
+                A.cref[k >> 4] = s;
+                A.span[k >> 4] = first - s;
+            }
+            if (k == 0) *A.decay = ex2((float)all * kUnfix);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bar[kArr + (i & 1)]);
+        }
+    } else if (warp >= 20) {
+        const int k = tid - 640;  // row of b
         {
-            // P: row tl; the two warps of a lane quarter take blocks of 16 columns in turn
-            const float ct = A.cumf[tl];
-            for (int kb = half; kb < 8; kb += 2) {
-                uint32_t w[8];
-                if (kb > 2 * q4 + 1) {
+            // the state before the segment
+            const int ch = DP == 64 ? (tl & 63) : tl;  // my channel; with DP = 64 lanes 64.. repeat 0..63
+            const float *p = a.segs > 1 ? a.seg_state + ((size_t)unit * a.segs + seg) * a.fine * M * d
+                                        : (a.state_in ? a.state_in + (size_t)unit * M * d : nullptr);
+            const bool mine = p && j0 + ch < d;
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) w[e] = 0u;
-                } else {
-                    float v[16];
-                    tmem_ld16(tm + lane_base + T::G + 16 * kb, v);
-                    if (kb < 2 * q4) {  // wholly before my rows: one exponential for the block
-                        const float f = ex2(ct - A.cref[kb]);
-                        tmem_wait_ld();
+            for (int m0 = 0; m0 < MP; m0 += 16) {
+                float v[16];
 #pragma unroll
-                        for (int e = 0; e < 16; e += 4) {
-                            const float4 r = *reinterpret_cast<const float4 *>(A.rs + 16 * kb + e);
-                            v[e] *= f * r.x;
-                            v[e + 1] *= f * r.y;
-                            v[e + 2] *= f * r.z;
-                            v[e + 3] *= f * r.w;
-                        }
-                    } else {
-                        tmem_wait_ld();
-#pragma unroll
-                        for (int e = 0; e < 16; ++e) {
-                            const int s = 16 * kb + e;
-                            const float p = v[e] * ex2(ct - A.uf[s]);
-                            v[e] = s < tl ? p : s == tl ? p + skip : 0.f;
-                        }
-                    }
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) w[e] = pack_bf16(v[2 * e], v[2 * e + 1]);
-                }
-                tmem_st8(tm + lane_base + T::P + 8 * kb, w);
+                for (int e = 0; e < 16; ++e) v[e] = mine && m0 + e < M ? __ldg(p + (size_t)(m0 + e) * d + j0 + ch) : 0.f;
+                tmem_st16(tm + lane_base + TS + m0, v);
             }
+            tmem_wait_st();
         }
-        {
-            // b 2^(S_Q - S_s) D_s and c 2^S_t, in units of 16 bytes of 32 rows: a block of P is worth
-            // four of them, and a warp of lane quarter q has q + 1 blocks
-            constexpr int UNITS = 2 * 4 * (MP / 8), BASE = UNITS / 8 + 6;
-            const int n = BASE - 4 * q4, first = 2 * (BASE * q4 - 2 * q4 * (q4 - 1)) + half * n;
-            // (n is even: two units' loads at a time)
-            for (int k0 = first; k0 < first + n; k0 += 2) {
-                uint4 *at[2], u[2];
-                float f[2];
+        for (int i = 0; i < nch; ++i) {
+            const int c = i & 1;
+            const StepArrays A(arrays + c * SARR);
+            ok = wait(kArr + c, (i >> 1) & 1) && wait(kFullBC + c, (i >> 1) & 1) && wait(kG + c, (i >> 1) & 1);  // G has read b
+            if (named_any(3, 128, !ok)) {
+                ok = false;
+                break;
+            }
+            const float weight = A.wst[k], decay = *A.decay;
+            unsigned char *pb = sm + L::B + c * L::BB;
 #pragma unroll
-                for (int o = 0; o < 2; ++o) {
-                    const int k = k0 + o, r = 32 * (k & 3) + lane, p = (k >> 2) % (MP / 8);
-                    const bool is_c = (k >> 2) >= MP / 8;
-                    f[o] = is_c ? A.et[r] : A.wst[r];
-                    at[o] = reinterpret_cast<uint4 *>(sm + (is_c ? L::C : L::B) + p / 8 * SSLAB + sw_off(r, p % 8));
-                    u[o] = *at[o];
-                }
+            for (int p0 = 0; p0 < MP / 8; p0 += 8) {
+                uint4 u[8];
 #pragma unroll
-                for (int o = 0; o < 2; ++o) {
+                for (int p = 0; p < 8; ++p) u[p] = *reinterpret_cast<uint4 *>(pb + p0 / 8 * SSLAB + sw_off(k, p));
+#pragma unroll
+                for (int p = 0; p < 8; ++p) {
                     float v[8];
-                    Vec16<__nv_bfloat16>::unpack(u[o], v);
+                    Vec16<__nv_bfloat16>::unpack(u[p], v);
 #pragma unroll
-                    for (int x = 0; x < 8; ++x) v[x] *= f[o];
-                    *at[o] = Vec16<__nv_bfloat16>::pack(v);
+                    for (int x = 0; x < 8; ++x) v[x] *= weight;
+                    *reinterpret_cast<uint4 *>(pb + p0 / 8 * SSLAB + sw_off(k, p)) = Vec16<__nv_bfloat16>::pack(v);
+                }
+            }
+            if (i > 0) ok = wait(kState, (i - 1) & 1) && wait(kCX, (i - 1) & 1) && (!L::OUT_OVER_SB || wait(kOut, (i - 1) & 1));
+            if (__any_sync(0xffffffffu, !ok)) {
+                ok = false;
+                break;
+            }
+            tc_fence_after();
+#pragma unroll
+            for (int m0 = 0; m0 < MP; m0 += 32) {
+                const uint32_t at = tm + lane_base + TS + m0;
+                float v[32];
+                tmem_ld16(at, v);
+                tmem_ld16(at + 16, v + 16);
+                tmem_wait_ld();
+                if (tl < DP)
+#pragma unroll
+                    for (int p = 0; p < 4; ++p)
+                        *reinterpret_cast<uint4 *>(sm + L::SB + m0 / 64 * L::SBS + sw_off(tl, m0 % 64 / 8 + p)) = Vec16<__nv_bfloat16>::pack(v + 8 * p);
+#pragma unroll
+                for (int e = 0; e < 32; ++e) v[e] *= decay;
+                tmem_st16(at, v);
+                tmem_st16(at + 16, v + 16);
+            }
+            tmem_wait_st();
+            tc_fence_before();
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bar[kScaled]);
+        }
+    } else if (warp >= 8 && warp < 16) {
+        const int half = (warp - 8) >> 2;
+        const float skip = a.D[h];
+        for (int i = 0; i < nch; ++i) {
+            const int c = i & 1;
+            const StepArrays A(arrays + c * SARR);
+            ok = wait(kArr + c, (i >> 1) & 1) && wait(kG + c, (i >> 1) & 1);
+            if (__any_sync(0xffffffffu, !ok)) {
+                ok = false;
+                break;
+            }
+            tc_fence_after();
+            // row tl, columns 64 half ..: blocks of 16 up to the one that row tl ends in, two at a time
+            const uint32_t at = tm + lane_base + TG + 128 * c + 64 * half;
+            const float ct = A.cumf[tl];
+#pragma unroll
+            for (int k2 = 0; k2 < 4; k2 += 2) {
+                float v[2][16];
+                const int kb2 = 4 * half + k2;  // even, as the last block of a row's pair is odd
+                uint32_t w[2][8];
+                if (kb2 > 2 * q4) {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) w[0][e] = w[1][e] = 0u;
+                } else {
+                    tmem_ld16(at + 16 * k2, v[0]);
+                    tmem_ld16(at + 16 * k2 + 16, v[1]);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        const int kb = kb2 + k;
+                        if (kb2 < 2 * q4) {  // wholly before my rows: one exponential for the block
+                            const float f = ex2(ct - A.cref[kb]);
+                            const ssm_f2 ff = ssm_pack(f, f);
+#pragma unroll
+                            for (int e = 0; e < 16; e += 4) {
+                                const ulonglong2 r = *reinterpret_cast<const ulonglong2 *>(A.rs + 16 * kb + e);
+                                const ssm_f2 lo = ssm_mul(ssm_pack(v[k][e], v[k][e + 1]), ssm_mul(ff, r.x));
+                                const ssm_f2 hi = ssm_mul(ssm_pack(v[k][e + 2], v[k][e + 3]), ssm_mul(ff, r.y));
+                                ssm_unpack(lo, v[k][e], v[k][e + 1]);
+                                ssm_unpack(hi, v[k][e + 2], v[k][e + 3]);
+                            }
+                        } else if (A.span[kb] < 64.f) {
+                            // as above, from the block's end: at most 2^64 too large before, and as much too small behind
+                            const float f = ex2(ct - A.cref[kb]);
+#pragma unroll
+                            for (int e = 0; e < 16; ++e) {
+                                const int s = 16 * kb + e;
+                                const float p = v[k][e] * (f * A.rs[s]);
+                                v[k][e] = s < tl ? p : s == tl ? p + skip : 0.f;
+                            }
+                        } else {
+#pragma unroll
+                            for (int e = 0; e < 16; ++e) {
+                                const int s = 16 * kb + e;
+                                const float p = v[k][e] * ex2(ct - A.uf[s]);
+                                v[k][e] = s < tl ? p : s == tl ? p + skip : 0.f;
+                            }
+                        }
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) w[k][e] = pack_bf16(v[k][2 * e], v[k][2 * e + 1]);
+                    }
+                }
+                tmem_st8(at + 8 * k2, w[0]);
+                tmem_st8(at + 8 * k2 + 8, w[1]);
+            }
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bar[kP + c]);
+        }
+    } else if (warp >= 16) {
+        for (int i = 0; i < nch; ++i) {
+            const int c = i & 1;
+            const uint32_t par = i & 1;
+            const StepArrays A(arrays + c * SARR);
+            ok = wait(kArr + c, (i >> 1) & 1) && wait(kCX, par);
+            if (__any_sync(0xffffffffu, !ok)) {
+                ok = false;
+                break;
+            }
+            tc_fence_after();
+            const uint32_t at = tm + lane_base + TY;
+            const float f = A.et[tl];
+#pragma unroll
+            for (int j = 0; j < DP; j += 32) {
+                float v[32];
+                tmem_ld16(at + j, v);
+                tmem_ld16(at + j + 16, v + 16);
+                tmem_wait_ld();
+#pragma unroll
+                for (int e = 0; e < 32; ++e) v[e] *= f;
+                tmem_st16(at + j, v);
+                tmem_st16(at + j + 16, v + 16);
+            }
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bar[kRows]);
+            ok = wait(kY + c, (i >> 1) & 1);
+            if (tid == 512) bulk_wait_read_all();  // the last output tile has left shared memory
+            if (named_any(2, 128, !ok)) {
+                ok = false;
+                break;
+            }
+            tc_fence_after();
+            unsigned char *out = sm + L::OUT;
+#pragma unroll
+            for (int j = 0; j < DP; j += 32) {
+                float v[32];
+                tmem_ld16(at + j, v);
+                tmem_ld16(at + j + 16, v + 16);
+                tmem_wait_ld();
+                if (j + 32 == DP) {  // the next chunk's c X_0 may go over Y
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&bar[kFreeY]);
+                }
+#pragma unroll
+                for (int p = 0; p < 4; ++p)
+                    *reinterpret_cast<uint4 *>(out + j / 64 * SSLAB + sw_off(tl, j % 64 / 8 + p)) = Vec16<__nv_bfloat16>::pack(v + 8 * p);
+            }
+            fence_proxy_async_smem();
+            named_sync(2, 128);
+            if (tid == 512) {
+#pragma unroll
+                for (int s = 0; s < DP / 64; ++s)
+                    if (j0 + 64 * s < d) tma_store_4d(&tm_y, j0 + 64 * s, h, t_begin + i * SQ, b, out + s * SSLAB);
+                bulk_commit();
+                if (L::OUT_OVER_SB) {
+                    bulk_wait_read_all();
+                    mbar_arrive(&bar[kOut]);
                 }
             }
         }
-        tmem_wait_st();
-        tc_fence_before();
-        fence_proxy_async_smem();
-        __syncthreads();
-        if (warp == 0 && elect_one()) {
-            tc_fence_after();
-            const SmemDesc dx = sw_desc(s0 + L::X, SSLAB);  // [K = s][j]
-            constexpr uint32_t id_p = idesc(128, DP, 1, 1, 0, 1), id_s = idesc(128, DP, 1, 1);
-#pragma unroll
-            for (int k = 0; k < SQ / 16; ++k)
-                mma_f16_t(tm + T::G, tm + T::P + 8 * k, sw_step(dx, k * 2048), id_p, k > 0);
-            const SmemDesc dc = sw_desc(s0 + L::C, 16), ds = sw_desc(s0 + L::SB, 16);
-#pragma unroll
-            for (int k = 0; k < MP / 16; ++k)
-                mma_f16(tm + T::G, sw_step(dc, k / 4 * SSLAB + k % 4 * 32), sw_step(ds, k / 4 * L::SBS + k % 4 * 32),
-                        id_s, 1);
-            mma_commit(&bar[2]);
-            // x^T as A: with DP = 64 its second 64 rows repeat the first
-            const SmemDesc da = sw_desc(s0 + L::X, DP == 64 ? 0 : SSLAB), dh = sw_desc(s0 + L::B, SSLAB);
-            constexpr uint32_t id_x = idesc(128, MP, 1, 1, 1, 1);
-#pragma unroll
-            for (int k = 0; k < SQ / 16; ++k) mma_f16(tm + T::S, sw_step(da, k * 2048), sw_step(dh, k * 2048), id_x, 1);
-            mma_commit(&bar[3]);
-        }
-        __syncwarp();
-        if (i + 1 < nch) {
-            make_arrays(t0 + SQ, par ^ 1);
-            fetch_dt(t0 + 2 * SQ);
-        }
-        ok = mbar_wait(&bar[2], par);
-        tc_fence_after();
-        // y: row tl, half of the channels
-        constexpr int CW = DP / 2;  // channels of a warp
-        unsigned char *out = sm + (DP == 128 && half ? L::OUT1 : L::OUT0);
-        const int p0 = DP == 128 ? 0 : half * 4;
-#pragma unroll
-        for (int blk = 0; blk < CW / 32; ++blk) {
-            float v[32];
-            tmem_ld16(tm + lane_base + T::G + half * CW + 32 * blk, v);
-            tmem_ld16(tm + lane_base + T::G + half * CW + 32 * blk + 16, v + 16);
-            tmem_wait_ld();
-#pragma unroll
-            for (int c = 0; c < 4; ++c)
-                *reinterpret_cast<uint4 *>(out + sw_off(tl, p0 + 4 * blk + c)) = Vec16<__nv_bfloat16>::pack(v + 8 * c);
-        }
-        tc_fence_before();
-        fence_proxy_async_smem();
-        ok = mbar_wait(&bar[3], par) && ok;
-        if (__syncthreads_or(!ok)) break;
-        if (tid == 0) {
-            if (i + 1 < nch) fetch(t0 + SQ);
-#pragma unroll
-            for (int s = 0; s < DP / 64; ++s)
-                if (j0 + 64 * s < d) tma_store_4d(&tm_y, j0 + 64 * s, h, t0, b, sm + (s ? L::OUT1 : L::OUT0));
-            bulk_commit();
-        }
+        if (tid == 512) bulk_wait_all();
     }
-    if (i < nch && tid == 0) {  // a wait ran out
-        report_error(a.err, kErrWaitTimeout);
-        mbar_wait(&bar[0], i & 1);  // the copy of this chunk, if it is still in flight
-    }
-    if (tid == 0) bulk_wait_all();
+    if (!ok) *failed = 1;  // a wait ran out
     tc_fence_before();
     __syncthreads();
-    if (warp == 0) {
+    if (tid == 0 && *failed) report_error(a.err, kErrWaitTimeout);
+    if (warp == 1) {
         tc_fence_after();
-        tmem_dealloc(tm, T::COLS);
+        tmem_dealloc(tm, TCOLS);
     }
 }
 
@@ -400,10 +549,11 @@ __global__ void __launch_bounds__(STH, MP == 64 ? 2 : 1)
     const int seg = id % a.state_segs;
     id /= a.state_segs;
     const int j0 = id % slices * DP, unit = id / slices, b = unit / H, h = unit % H, g = h / (H / a.G);
-    const int t_begin = seg * a.seg, t_end = min(N, t_begin + a.seg), nch = (t_end - t_begin + SQ - 1) / SQ;
+    const int len = a.seg / a.fine, t_begin = seg * len, t_end = min(N, t_begin + len);
+    const int nch = t_end > t_begin ? (t_end - t_begin + SQ - 1) / SQ : 0, parts = a.segs * a.fine;
     const __nv_bfloat16 *gdt = static_cast<const __nv_bfloat16 *>(a.dt) + (size_t)b * N * a.lddt + h;
     const float dt_bias = a.dt_bias[h];
-    const double rate2 = log2_rate(a.a_log[h]);
+    const Rate2 rate(a.a_log[h]);
 
     if ((s0 & 1023u) != 0u) {
         if (tid == 0) report_error(a.err, kErrShape);
@@ -442,7 +592,7 @@ __global__ void __launch_bounds__(STH, MP == 64 ? 2 : 1)
         float delta = 0.f;
         if (start_of(n) + k < t_end) delta = softplus(dt_next + dt_bias);
         long long all;
-        const long long fx = chunk_sum(rate2, delta, k, tot, all);
+        const long long fx = chunk_sum(rate, delta, k, tot, all);
         arrays[(n & 1) * SQ + k] = REV ? (start_of(n) + k < t_end ? ex2_fix(fx + behind) : 0.f) : ex2_fix(all - fx + behind) * delta;
         behind += all;
     };
@@ -450,7 +600,7 @@ __global__ void __launch_bounds__(STH, MP == 64 ? 2 : 1)
     __syncthreads();
     if (tid == 0)
         for (int n = 0; n < L::NB && n < nch; ++n) fetch(n);
-    make_weights(0);
+    if (nch > 0) make_weights(0);  // the last segment may have parts without a position
     fetch_dt(1);
     tc_fence_after();
     const uint32_t tm = *tslot;
@@ -529,8 +679,8 @@ __global__ void __launch_bounds__(STH, MP == 64 ? 2 : 1)
         }
     } else {
         // a single segment's last state is the final state
-        float *out = a.segs == 1 && a.final_state ? a.final_state + (size_t)unit * M * d
-                                                  : a.seg_state + ((size_t)unit * a.segs + seg) * M * d;
+        float *out = parts == 1 && a.final_state ? a.final_state + (size_t)unit * M * d
+                                                 : a.seg_state + ((size_t)unit * parts + seg) * M * d;
         if (tid >= SQ && tid < SQ + 1) arrays[0] = (float)behind * kUnfix;
         __syncthreads();
         const float *in = !REV && seg == 0 && a.state_in ? a.state_in + (size_t)unit * M * d : nullptr;
@@ -543,6 +693,9 @@ __global__ void __launch_bounds__(STH, MP == 64 ? 2 : 1)
                 float v[16];
                 tmem_ld16(tm + lane_base + m0, v);
                 tmem_wait_ld();
+                if (nch == 0)
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) v[e] = 0.f;
                 if (j0 + tl < d)
 #pragma unroll
                     for (int e = 0; e < 16; ++e)
@@ -552,7 +705,7 @@ __global__ void __launch_bounds__(STH, MP == 64 ? 2 : 1)
                         }
             }
         }
-        if (!REV && tid == 0 && j0 == 0 && a.segs > 1) a.seg_log[(size_t)unit * a.segs + seg] = total;
+        if (!REV && tid == 0 && j0 == 0 && parts > 1) a.seg_log[(size_t)unit * parts + seg] = total;
     }
     tc_fence_before();
     __syncthreads();
@@ -562,21 +715,21 @@ __global__ void __launch_bounds__(STH, MP == 64 ? 2 : 1)
     }
 }
 
-// Segment states, in place: seg_state[s] becomes the state before segment s; the final state where
-// it is wanted.  One thread per four state elements.
+// Segment states, in place: seg_state[s] becomes the state before part s; the final state where it
+// is wanted.  One thread per four state elements.
 __global__ void __launch_bounds__(256) ssm_carry_kernel(ScanArgs a) {
     const long long i = (long long)blockIdx.x * 256 + threadIdx.x;
-    const int n = a.M * a.d / 4;
+    const int n = a.M * a.d / 4, parts = a.segs * a.fine;
     const int unit = (int)(i / n), e = (int)(i % n);
     if (unit >= a.B * a.H) return;
-    float4 *p = reinterpret_cast<float4 *>(a.seg_state + (size_t)unit * a.segs * a.M * a.d) + e;
-    const float *lg = a.seg_log + (size_t)unit * a.segs;
+    float4 *p = reinterpret_cast<float4 *>(a.seg_state + (size_t)unit * parts * a.M * a.d) + e;
+    const float *lg = a.seg_log + (size_t)unit * parts;
     float4 X = make_float4(0.f, 0.f, 0.f, 0.f);
-    // the first segment starts from the given state, which its last state holds
+    // the first part starts from the given state, which its last state holds
     float4 start = X;
     if (a.state_in) start = __ldg(reinterpret_cast<const float4 *>(a.state_in + (size_t)unit * a.M * a.d) + e);
     constexpr int K = 8;
-    for (int s0 = 0; s0 < a.segs; s0 += K) {
+    for (int s0 = 0; s0 < parts; s0 += K) {
         float4 v[K];
         float f[K];
 #pragma unroll
@@ -588,8 +741,8 @@ __global__ void __launch_bounds__(256) ssm_carry_kernel(ScanArgs a) {
 #pragma unroll
         for (int k = 0; k < K; ++k) {
             const int s = s0 + k;
-            if (s >= a.segs) break;
-            p[(size_t)s * n] = s == 0 ? start : X;
+            if (s >= parts) break;
+            if (s % a.fine == 0) p[(size_t)s * n] = s == 0 ? start : X;  // a segment starts here
             if (s < a.state_segs) {
                 const float w = ex2(f[k]);
                 X = make_float4(fmaf(w, X.x, v[k].x), fmaf(w, X.y, v[k].y), fmaf(w, X.z, v[k].z), fmaf(w, X.w, v[k].w));
@@ -630,25 +783,31 @@ ida_status ssm_map(CUtensorMap *m, const void *p, int B, int N, int K, int w, lo
     return r == CUDA_SUCCESS ? IDA_OK : fail_with(IDA_ERR_CUDA, "cuTensorMapEncodeTiled failed");
 }
 
-// Segments: the split that the two launches' chunk counts per SM favour.
-void ssm_chunk_segments(int B, int H, int N, int d, int M, int num_sms, int &seg, int &segs) {
+// Segments, and the parts of one whose states the first launch makes: the split with the least time
+// by the launches' passes over the SMs, a chunk taking about 1.2 us in the chunk kernel (one CTA per
+// SM) and 0.9 us in the state kernel (two), a CTA's start 3 us, the extra launches 5 us.
+void ssm_chunk_segments(int B, int H, int N, int d, int M, int num_sms, int &seg, int &segs, int &fine) {
     const int nch = (N + SQ - 1) / SQ, dp = d <= 64 ? 64 : 128;
-    const long long units = (long long)B * H * ((d + dp - 1) / dp), slots = (long long)num_sms * (M <= 64 ? 2 : 1);
+    const long long units = (long long)B * H * ((d + dp - 1) / dp), slots = (M <= 64 ? 2LL : 1LL) * num_sms;
     double best = 0;
-    int pick = 1;
-    for (int s = 1; s <= nch && s <= 64; ++s) {
-        const int per = (nch + s - 1) / s, real = (nch + per - 1) / per;
-        if (real != s) continue;
-        const double main_waves = (double)((units * s + slots - 1) / slots);
-        const double state_waves = s > 1 ? (double)((units * (s - 1) + 2 * num_sms - 1) / (2 * num_sms)) : 0.0;
-        const double cost = main_waves * (per * 3.4 + 3.0) + (s > 1 ? state_waves * (per * 1.5 + 3.0) + 4.0 : 0.0);
-        if (s == 1 || cost < best) {
-            best = cost;
-            pick = s;
+    int pick = 1, pick_fine = 1;
+    for (int s = 1; s <= nch && s <= 256; ++s) {
+        const int per = (nch + s - 1) / s;
+        if ((nch + per - 1) / per != s) continue;
+        const double main = (double)((units * s + num_sms - 1) / num_sms) * (1.2 * per + 3.0);
+        for (int f = 1; f <= (s > 1 ? per : 1); ++f) {
+            if (per % f) continue;
+            const double state = s > 1 ? (double)((units * (s - 1) * f + slots - 1) / slots) * (0.9 * (per / f) + 3.0) + 5.0 : 0.0;
+            if ((s == 1 && f == 1) || main + state < best) {
+                best = main + state;
+                pick = s;
+                pick_fine = f;
+            }
         }
     }
     seg = (nch + pick - 1) / pick * SQ;
     segs = (N + seg - 1) / seg;
+    fine = pick_fine;
 }
 
 template <int DP, int MP, int PARTS, bool REV>
@@ -682,11 +841,11 @@ template <int DP, int MP>
 static ida_status launch_chunk(const ScanArgs &a, const CUtensorMap &mx, const CUtensorMap &mb, const CUtensorMap &mc,
                                const CUtensorMap &my, cudaStream_t st) {
     constexpr int smem = SsmSmem<DP, MP>::TOTAL;
-    static_assert(smem <= (MP == 64 ? 113 : 227) * 1024, "shared memory budget");
+    static_assert(smem <= 227 * 1024, "shared memory budget");
     cudaError_t e = cudaFuncSetAttribute(ssm_chunk_kernel<DP, MP>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return fail_with(IDA_ERR_CUDA, cudaGetErrorString(e));
     const long long units = (long long)a.B * a.H * ((a.d + DP - 1) / DP);
-    if (units * a.segs > 0x7FFFFFFFLL) return fail_with(IDA_ERR_UNSUPPORTED, "too many rows and heads");
+    if (units * a.segs * a.fine > 0x7FFFFFFFLL) return fail_with(IDA_ERR_UNSUPPORTED, "too many rows and heads");
     ida_status s = IDA_OK;
     if (a.state_segs > 0) s = launch_ssm_states(a, a.final_state != nullptr, false, st);
     if (s == IDA_OK && a.segs > 1) {
@@ -695,7 +854,7 @@ static ida_status launch_chunk(const ScanArgs &a, const CUtensorMap &mx, const C
         s = launched("ssm segment sums");
     }
     if (s != IDA_OK) return s;
-    ssm_chunk_kernel<DP, MP><<<(unsigned)(units * a.segs), STH, smem, st>>>(a, mx, mb, mc, my);
+    ssm_chunk_kernel<DP, MP><<<(unsigned)(units * a.segs), CTH, smem, st>>>(a, mx, mb, mc, my);
     return launched("ssm scan");
 }
 

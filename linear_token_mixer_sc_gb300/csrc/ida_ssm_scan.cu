@@ -18,7 +18,7 @@ namespace ida {
 
 ida_status device_error_word(unsigned **err, std::string &why);
 ida_status launch_ssm_chunk(const ScanArgs &a, cudaStream_t st);
-void ssm_chunk_segments(int B, int H, int N, int d, int M, int num_sms, int &seg, int &segs);
+void ssm_chunk_segments(int B, int H, int N, int d, int M, int num_sms, int &seg, int &segs, int &fine);
 
 constexpr int SEQ_T = 16;  // positions per tile
 
@@ -231,12 +231,13 @@ static void seq_segments(int B, int H, int N, int d, int num_sms, int &seg, int 
 }
 
 // The split of a call and the bytes of its segment states.
-static size_t scan_plan(int B, int H, int N, int d, int M, bool chunked, int num_sms, int &seg, int &segs) {
+static size_t scan_plan(int B, int H, int N, int d, int M, bool chunked, int num_sms, int &seg, int &segs, int &fine) {
+    fine = 1;
     if (chunked)
-        ssm_chunk_segments(B, H, N, d, M, num_sms, seg, segs);
+        ssm_chunk_segments(B, H, N, d, M, num_sms, seg, segs, fine);
     else
         seq_segments(B, H, N, d, num_sms, seg, segs);
-    return segs < 2 ? 0 : (size_t)B * H * segs * ((size_t)M * d + 4) * sizeof(float);
+    return segs < 2 ? 0 : (size_t)B * H * segs * fine * ((size_t)M * d + 4) * sizeof(float);
 }
 
 template <typename E, int MT>
@@ -293,8 +294,8 @@ size_t ida_ssm_scan_workspace_bytes(int B, int H, int N, int d, int G, int M, in
     if (cudaGetDevice(&dev) != cudaSuccess ||
         cudaDeviceGetAttribute(&num_sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
         return 0;
-    int seg, segs;
-    return scan_plan(B, H, N, d, M, dtype == IDA_BF16, num_sms, seg, segs);
+    int seg, segs, fine;
+    return scan_plan(B, H, N, d, M, dtype == IDA_BF16, num_sms, seg, segs, fine);
 }
 
 ida_status ida_ssm_scan(const void *x, const void *b, const void *c, const void *dt, const float *a_log,
@@ -330,20 +331,20 @@ ida_status ida_ssm_scan(const void *x, const void *b, const void *c, const void 
         return e == cudaSuccess ? IDA_OK : fail_with(IDA_ERR_CUDA, cudaGetErrorString(e));
     }
     ScanArgs a = {x, b, c, dt, a_log, dt_bias, D, state_in, y, final_state, B, H, N, d, G, M, ldx, ldb, ldc, lddt,
-                  0, 0, 0, nullptr, nullptr, nullptr};
+                  0, 0, 1, 0, nullptr, nullptr, nullptr};
     s = device_error_word(&a.err, why);
     if (s != IDA_OK) return fail_with(s, why);
     const bool chunked = dtype == IDA_BF16;
-    const size_t need = scan_plan(B, H, N, d, M, chunked, num_sms, a.seg, a.segs);
+    const size_t need = scan_plan(B, H, N, d, M, chunked, num_sms, a.seg, a.segs, a.fine);
     if (need > 0 && workspace && workspace_bytes >= need) {
         a.seg_state = static_cast<float *>(workspace);
-        a.seg_log = a.seg_state + (size_t)B * H * a.segs * M * d;
+        a.seg_log = a.seg_state + (size_t)B * H * a.segs * a.fine * M * d;
     } else {
         a.seg = (N + 127) / 128 * 128;
-        a.segs = 1;
+        a.segs = a.fine = 1;
     }
     // the tensor-core kernel takes a final state from segment states, the other one from its own
-    a.state_segs = chunked && final_state ? a.segs : a.segs - 1;
+    a.state_segs = chunked && final_state ? a.segs * a.fine : (a.segs - 1) * a.fine;
     return chunked ? launch_ssm_chunk(a, st) : launch_seq_m<float>(a, st);
 }
 

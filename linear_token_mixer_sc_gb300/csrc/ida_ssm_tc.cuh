@@ -57,23 +57,39 @@ __device__ __forceinline__ float ex2_fix(long long x) {
     return ex2(frac) * ex2((float)(int)(x >> 32));
 }
 
-// Running sum of log2 a over a chunk by 128 threads (four warps, named barrier 1), position k of
-// it in thread k; returns the inclusive sum, and the chunk's in `all`.  fp64 for the rate and its
-// product: an error in the rate would be the same in every position of a head.
-__device__ __forceinline__ double log2_rate(float a_log) { return exp((double)a_log) * 1.4426950408889634; }
-__device__ __forceinline__ long long chunk_sum(double rate2, float delta, int k, long long *tot, long long &all) {
+// The rate e^a_log log2 e in two floats: an error in it would be the same in every position of a
+// head.  (fp64 issues at a small fraction of the fp32 rate on this part: the products below, taken in
+// fp64, were half of a chunk's time.)
+struct Rate2 {
+    float hi, lo;
+    __device__ __forceinline__ explicit Rate2(float a_log) {
+        const double r = exp((double)a_log) * 1.4426950408889634;
+        hi = (float)r;
+        lo = (float)(r - (double)hi);
+    }
+};
+// log2 of exp(-rate delta) in fixed point, from the exact product of the leading parts
+__device__ __forceinline__ long long log2_fix(const Rate2 &rate, float delta) {
+    const float p = rate.hi * delta, e = fmaf(rate.hi, delta, -p) + rate.lo * delta;
+    if (!(p < 1048576.f)) return -(1ll << 52);  // 2^-1048576 is 0
+    return -(__float2ll_rn(p * kFix) + __float2ll_rn(e * kFix));
+}
+
+// Running sum of log2 a over a chunk by 128 threads (four warps, named barrier `id`), position k of
+// it in thread k; returns the inclusive sum, and the chunk's in `all`.
+__device__ __forceinline__ long long chunk_sum(const Rate2 &rate, float delta, int k, long long *tot, long long &all, int id = 1) {
     const int lane = k & 31, w = k >> 5;
-    long long fx = __double2ll_rn(fmax(-rate2 * (double)delta, -1048576.0) * (double)kFix);
+    long long fx = log2_fix(rate, delta);
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
         const long long u = __shfl_up_sync(0xffffffffu, fx, o);
         if (lane >= o) fx += u;
     }
     if (lane == 31) tot[w] = fx;
-    named_sync(1, 128);
+    named_sync(id, 128);
     const long long t1 = tot[0], t2 = t1 + tot[1], t3 = t2 + tot[2];
     all = t3 + tot[3];
-    named_sync(1, 128);  // the totals have been read
+    named_sync(id, 128);  // the totals have been read
     return fx + (w == 0 ? 0 : w == 1 ? t1 : w == 2 ? t2 : t3);
 }
 
