@@ -19,11 +19,11 @@
 // output overlap its neighbours':
 //   warp 0      copies: x, b and c by TMA, two chunks ahead where shared memory allows
 //   warp 1      issues all MMAs
-//   warps 4-7   the step sizes' sums and exponentials of the next chunk
+//   warps 4-7   the step sizes' sums and exponentials, two chunks ahead; half of b scaled in place
 //   warps 8-15  P: thread t of a lane quarter makes row t from row t of G, in G's own place in TMEM
 //               (each half of a row is read and replaced by one warp), an A operand there
 //   warps 16-19 the rows of (c X_0) in Y scaled by 2^S_t before P x is added to them, y out by TMA
-//   warps 20-23 b scaled in place; the state's bf16 copy for Y and its decay in TMEM
+//   warps 20-23 the other half of b; the state's bf16 copy for Y and its decay in TMEM
 // (All stages in one group of 256 threads, two CTAs per SM: 45 us for 4 x 4096 positions of 16
 // heads of 128, 8500 cycles a chunk, most of them waits for the next stage.)
 // The tiles have the 128-byte swizzle that the MMA descriptors name, so one copy serves as a
@@ -57,16 +57,17 @@ enum {
     kFullX = 4,    // [2] x
     kFreeX = 6,    // [2]
     kG = 8,        // [2] G is complete
-    kArr = 10,     // [2] the chunk's arrays are there
-    kP = 12,       // [2] P is complete
-    kY = 14,       // [2] Y is complete
-    kScaled = 16,  // scaled b, the state's bf16 copy and its decay
-    kState = 17,   // the state update is complete
-    kCX = 18,      // c X_0 is complete
-    kRows = 19,    // its rows are scaled
-    kFreeY = 20,   // Y has been read
-    kOut = 21,     // the output tile has left shared memory
-    kBars = 22
+    kP = 10,       // [2] P is complete
+    kY = 12,       // [2] Y is complete
+    kScaled = 14,  // scaled b, the state's bf16 copy and its decay
+    kState = 15,   // the state update is complete
+    kCX = 16,      // c X_0 is complete
+    kRows = 17,    // its rows are scaled
+    kFreeY = 18,   // Y has been read
+    kOut = 19,     // the output tile has left shared memory
+    kArr = 20,     // [4] the chunk's arrays are there (of chunks with the same i % 4)
+    kFreeArr = 24, // [4] and have been used
+    kBars = 28
 };
 
 // Shared memory map; DP, MP: channels and state rows rounded up to 64 or 128.
@@ -83,8 +84,8 @@ struct SsmSmem {
     static constexpr bool OUT_OVER_SB = NX == 1;   // the output tile [DP / 64][128 t][64], where it does not fit beside SB
     static constexpr int OUT = OUT_OVER_SB ? SB : SB + MP / 64 * SBS;
     static constexpr int MISC = OUT + XB;
-    static constexpr int ARR = MISC + 256;         // two chunks' arrays
-    static constexpr int TOT = ARR + 2 * SARR * 4; // 4 64-bit totals
+    static constexpr int ARR = MISC + 256;         // four chunks' arrays
+    static constexpr int TOT = ARR + 4 * SARR * 4; // 4 totals
     static constexpr int TOTAL = TOT + 32;
 };
 // PARTS: bf16 tiles that the scaled b is kept in.  With one, two chunks are in flight.
@@ -133,6 +134,23 @@ __device__ __forceinline__ bool named_any(int id, int n, bool p) {
     return r != 0;
 }
 
+// Half of the 16-byte pieces of row r of b, from piece p0 on, scaled in place.
+template <int MP>
+__device__ __forceinline__ void scale_b(unsigned char *pb, int r, int p0, float weight) {
+    constexpr int N = MP / 16;
+    uint4 u[N];
+#pragma unroll
+    for (int p = 0; p < N; ++p) u[p] = *reinterpret_cast<uint4 *>(pb + (p0 + p) / 8 * SSLAB + sw_off(r, (p0 + p) % 8));
+#pragma unroll
+    for (int p = 0; p < N; ++p) {
+        float v[8];
+        Vec16<__nv_bfloat16>::unpack(u[p], v);
+#pragma unroll
+        for (int x = 0; x < 8; ++x) v[x] *= weight;
+        *reinterpret_cast<uint4 *>(pb + (p0 + p) / 8 * SSLAB + sw_off(r, (p0 + p) % 8)) = Vec16<__nv_bfloat16>::pack(v);
+    }
+}
+
 template <int DP, int MP>
 __global__ void __launch_bounds__(CTH, 1)
     ssm_chunk_kernel(ScanArgs a, const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_b,
@@ -144,7 +162,7 @@ __global__ void __launch_bounds__(CTH, 1)
     uint32_t *tslot = reinterpret_cast<uint32_t *>(sm + L::MISC + 8 * kBars);
     uint32_t *failed = tslot + 1;
     float *arrays = reinterpret_cast<float *>(sm + L::ARR);
-    long long *tot = reinterpret_cast<long long *>(sm + L::TOT);
+    float *tot = reinterpret_cast<float *>(sm + L::TOT);
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
     const int q4 = warp & 3, tl = 32 * q4 + lane;  // the lane quarter of TMEM this warp reaches, and its lane
     const uint32_t lane_base = (uint32_t)(32 * q4) << 16;
@@ -162,7 +180,7 @@ __global__ void __launch_bounds__(CTH, 1)
     }
     if (tid == 0) {
         for (int i = 0; i < kBars; ++i)
-            mbar_init(&bar[i], i == kP || i == kP + 1 ? 8 : i == kArr || i == kArr + 1 || i == kScaled || i == kRows || i == kFreeY ? 4 : 1);
+            mbar_init(&bar[i], i == kP || i == kP + 1 || i == kScaled ? 8 : (i >= kArr && i < kFreeArr) || i == kRows || i == kFreeY ? 4 : 1);
         fence_mbar_init();
         *failed = 0;
         tma_prefetch_desc(&tm_x);
@@ -276,41 +294,64 @@ __global__ void __launch_bounds__(CTH, 1)
     } else if (warp >= 4 && warp < 8) {
         const int k = tid - 128;  // position of the chunk
         const __nv_bfloat16 *gdt = static_cast<const __nv_bfloat16 *>(a.dt) + (size_t)b * N * a.lddt + h;
-        const float dt_bias = a.dt_bias[h];
-        const Rate2 rate(a.a_log[h]);
+        const float dt_bias = a.dt_bias[h], rate2 = expf(a.a_log[h]) * 1.4426950408889634f;
         const auto dt_of = [&](int i) {
             const int p = t_begin + i * SQ + k;
-            return p < t_end ? __bfloat162float(gdt[(size_t)p * a.lddt]) : 0.f;
+            return i < nch && p < t_end ? __bfloat162float(gdt[(size_t)p * a.lddt]) : 0.f;
         };
         float dt_next = dt_of(0);
-        for (int i = 0; i < nch; ++i) {
-            const float dt_now = dt_next;
-            if (i + 1 < nch) dt_next = dt_of(i + 1);
-            if (i >= 2) ok = wait(kY + (i & 1), ((i - 2) >> 1) & 1);  // the arrays of chunk i - 2 have been used
-            if (named_any(1, 128, !ok)) {
-                ok = false;
-                break;
+        // y alone comes of these: fp32 sums within a chunk, and log(1 + e) to 2^-18, are far below the
+        // rounding of P
+        const auto make_arrays = [&](int i) {
+            const float z = dt_next + dt_bias;
+            dt_next = dt_of(i + 1);
+            if (i >= 4) ok = wait(kFreeArr + (i & 3), ((i >> 2) - 1) & 1);
+            const float e = __expf(-fabsf(z));
+            const float l1 = e < 0.03125f ? e * fmaf(e, fmaf(e, 0.33333333f, -0.5f), 1.f) : __logf(1.f + e);
+            const float delta = t_begin + i * SQ + k < t_end ? fmaxf(z, 0.f) + l1 : 0.f;  // behind the end nothing decays or is added
+            float s = fmaxf(-rate2 * delta, -1048576.f);
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const float u = __shfl_up_sync(0xffffffffu, s, o);
+                if (lane >= o) s += u;
             }
-            float delta = 0.f;
-            if (t_begin + i * SQ + k < t_end) delta = softplus(dt_now + dt_bias);  // behind the end nothing decays or is added
-            long long all;
-            const long long fx = chunk_sum(rate, delta, k, tot, all);
-            const StepArrays A(arrays + (i & 1) * SARR);
-            const float s = (float)fx * kUnfix, u = s - log2f(delta);  // D = 0: +inf, and 2^(.. - u) = 0
+            if (lane == 31) tot[q4] = s;
+            if (named_any(1, 128, !ok)) return false;
+            const float w0 = tot[0], w1 = w0 + tot[1], w2 = w1 + tot[2], all = w2 + tot[3];
+            s += q4 == 0 ? 0.f : q4 == 1 ? w0 : q4 == 2 ? w1 : w2;
+            const StepArrays A(arrays + (i & 3) * SARR);
+            const float u = s - __log2f(delta);  // D = 0: +inf, and 2^(.. - u) = 0
             const float ref = __shfl_sync(0xffffffffu, s, lane | 15), first = __shfl_sync(0xffffffffu, s, lane & 16);
             A.cumf[k] = s;
             A.uf[k] = u;
             A.rs[k] = ex2(ref - u);
             A.et[k] = ex2(s);
-            A.wst[k] = ex2((float)(all - fx) * kUnfix) * delta;
+            A.wst[k] = ex2(all - u);
             if ((lane & 15) == 15) {
                 A.cref[k >> 4] = s;
                 A.span[k >> 4] = first - s;
             }
-            if (k == 0) *A.decay = ex2((float)all * kUnfix);
+            if (k == 0) *A.decay = ex2(all);
+            named_sync(1, 128);  // the totals have been read
+            if (lane == 0) mbar_arrive(&bar[kArr + (i & 3)]);
+            return true;
+        };
+        bool go = make_arrays(0);
+        if (go && nch > 1) go = make_arrays(1);
+        for (int i = 0; i < nch && go; ++i) {
+            const int c = i & 1;
+            ok = wait(kFullBC + c, (i >> 1) & 1) && wait(kG + c, (i >> 1) & 1);  // G has read b
+            if (named_any(1, 128, !ok)) {
+                ok = false;
+                break;
+            }
+            scale_b<MP>(sm + L::B + c * L::BB, k, MP / 16, arrays[(i & 3) * SARR + 4 * SQ + k]);
+            fence_proxy_async_smem();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&bar[kArr + (i & 1)]);
+            if (lane == 0) mbar_arrive(&bar[kScaled]);
+            if (i + 2 < nch) go = make_arrays(i + 2);
         }
+        if (!go) ok = false;
     } else if (warp >= 20) {
         const int k = tid - 640;  // row of b
         {
@@ -330,28 +371,14 @@ __global__ void __launch_bounds__(CTH, 1)
         }
         for (int i = 0; i < nch; ++i) {
             const int c = i & 1;
-            const StepArrays A(arrays + c * SARR);
-            ok = wait(kArr + c, (i >> 1) & 1) && wait(kFullBC + c, (i >> 1) & 1) && wait(kG + c, (i >> 1) & 1);  // G has read b
-            if (named_any(3, 128, !ok)) {
+            const StepArrays A(arrays + (i & 3) * SARR);
+            ok = wait(kArr + (i & 3), (i >> 2) & 1) && wait(kFullBC + c, (i >> 1) & 1) && wait(kG + c, (i >> 1) & 1);
+            if (__any_sync(0xffffffffu, !ok)) {
                 ok = false;
                 break;
             }
-            const float weight = A.wst[k], decay = *A.decay;
-            unsigned char *pb = sm + L::B + c * L::BB;
-#pragma unroll
-            for (int p0 = 0; p0 < MP / 8; p0 += 8) {
-                uint4 u[8];
-#pragma unroll
-                for (int p = 0; p < 8; ++p) u[p] = *reinterpret_cast<uint4 *>(pb + p0 / 8 * SSLAB + sw_off(k, p));
-#pragma unroll
-                for (int p = 0; p < 8; ++p) {
-                    float v[8];
-                    Vec16<__nv_bfloat16>::unpack(u[p], v);
-#pragma unroll
-                    for (int x = 0; x < 8; ++x) v[x] *= weight;
-                    *reinterpret_cast<uint4 *>(pb + p0 / 8 * SSLAB + sw_off(k, p)) = Vec16<__nv_bfloat16>::pack(v);
-                }
-            }
+            const float decay = *A.decay;
+            scale_b<MP>(sm + L::B + c * L::BB, k, 0, A.wst[k]);
             if (i > 0) ok = wait(kState, (i - 1) & 1) && wait(kCX, (i - 1) & 1) && (!L::OUT_OVER_SB || wait(kOut, (i - 1) & 1));
             if (__any_sync(0xffffffffu, !ok)) {
                 ok = false;
@@ -385,8 +412,8 @@ __global__ void __launch_bounds__(CTH, 1)
         const float skip = a.D[h];
         for (int i = 0; i < nch; ++i) {
             const int c = i & 1;
-            const StepArrays A(arrays + c * SARR);
-            ok = wait(kArr + c, (i >> 1) & 1) && wait(kG + c, (i >> 1) & 1);
+            const StepArrays A(arrays + (i & 3) * SARR);
+            ok = wait(kArr + (i & 3), (i >> 2) & 1) && wait(kG + c, (i >> 1) & 1);
             if (__any_sync(0xffffffffu, !ok)) {
                 ok = false;
                 break;
@@ -454,8 +481,8 @@ __global__ void __launch_bounds__(CTH, 1)
         for (int i = 0; i < nch; ++i) {
             const int c = i & 1;
             const uint32_t par = i & 1;
-            const StepArrays A(arrays + c * SARR);
-            ok = wait(kArr + c, (i >> 1) & 1) && wait(kCX, par);
+            const StepArrays A(arrays + (i & 3) * SARR);
+            ok = wait(kArr + (i & 3), (i >> 2) & 1) && wait(kCX, par);
             if (__any_sync(0xffffffffu, !ok)) {
                 ok = false;
                 break;
@@ -463,6 +490,7 @@ __global__ void __launch_bounds__(CTH, 1)
             tc_fence_after();
             const uint32_t at = tm + lane_base + TY;
             const float f = A.et[tl];
+            const ssm_f2 ff = ssm_pack(f, f);
 #pragma unroll
             for (int j = 0; j < DP; j += 32) {
                 float v[32];
@@ -470,7 +498,7 @@ __global__ void __launch_bounds__(CTH, 1)
                 tmem_ld16(at + j + 16, v + 16);
                 tmem_wait_ld();
 #pragma unroll
-                for (int e = 0; e < 32; ++e) v[e] *= f;
+                for (int e = 0; e < 32; e += 2) ssm_unpack(ssm_mul(ff, ssm_pack(v[e], v[e + 1])), v[e], v[e + 1]);
                 tmem_st16(at + j, v);
                 tmem_st16(at + j + 16, v + 16);
             }
@@ -479,7 +507,10 @@ __global__ void __launch_bounds__(CTH, 1)
             __syncwarp();
             if (lane == 0) mbar_arrive(&bar[kRows]);
             ok = wait(kY + c, (i >> 1) & 1);
-            if (tid == 512) bulk_wait_read_all();  // the last output tile has left shared memory
+            if (tid == 512) {
+                mbar_arrive(&bar[kFreeArr + (i & 3)]);
+                bulk_wait_read_all();  // the last output tile has left shared memory
+            }
             if (named_any(2, 128, !ok)) {
                 ok = false;
                 break;
