@@ -57,7 +57,8 @@ struct BwdSmem {
     static constexpr int NARR = 7 + 8 + 5 + 8 + 2;
     // <Z, X_0> per warp, 2^S_Q, parameters' parts; sums per warp; sums of K per pair of groups
     static constexpr int RED = ARR + NARR * SQ * 4;
-    static constexpr int TOT = RED + 128 + 32 + 256;
+    static constexpr int RATES = RED + 128 + 32 + 256;  // of 32 heads
+    static constexpr int TOT = RATES + 256;
     static constexpr int TOTAL = TOT + 32;
 };
 
@@ -113,6 +114,7 @@ __global__ void __launch_bounds__(BTH, 1)
     float *gs = xin + 4 * SQ, *es = gs + SQ;  // G and E at s = t
     float *red = reinterpret_cast<float *>(sm + L::RED);
     float *wsum = red + 32, *blk = wsum + 8;  // [8] and [8][8]
+    Rate2 *rates = reinterpret_cast<Rate2 *>(sm + L::RATES);
     long long *tot = reinterpret_cast<long long *>(sm + L::TOT);
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
     const int q4 = warp & 3, wj = warp >> 2, row = 32 * q4 + lane;  // my lane of TMEM: position s or t
@@ -202,13 +204,17 @@ __global__ void __launch_bounds__(BTH, 1)
         const float rate = expf(a.a_log[h]);
         // step sizes and decays of the head, by the first four warps
         if (tid < SQ) {
+            if (((r - r0) & 31) == 0) {  // the rates of the next 32 heads
+                if (warp == 0 && r + lane < r1) rates[lane] = rate2_of(a.a_log[h + lane]);
+                named_sync(1, 128);
+            }
             float delta = 0.f, z = 0.f;
             if (tid < len) {
                 z = __bfloat162float(static_cast<const __nv_bfloat16 *>(a.dt)[((size_t)b * N + t0 + tid) * a.lddt + h]) + a.dt_bias[h];
                 delta = softplus(z);
             }
             long long all;
-            const long long fx = chunk_sum(Rate2(a.a_log[h]), delta, tid, tot, all);
+            const long long fx = chunk_sum(rates[(r - r0) & 31], delta, tid, tot, all);
             const float hi = (float)fx * kUnfix;
             // S at the end of the block of 16 before mine
             const int edge = (lane & 16) - 1;
@@ -627,14 +633,14 @@ static ida_status launch_bwd_tc_d(const BwdTcArgs &ba, cudaStream_t st) {
 ida_status launch_bwd_tc_states(const ScanBwdArgs &a, cudaStream_t st) {
     ScanArgs f = {a.x, a.b, a.c, a.dt, a.a_log, a.dt_bias, a.D, nullptr, nullptr, nullptr, a.B, a.H, a.N, a.d, a.G, a.M,
                   a.ldx, a.ldb, a.ldc, a.lddt, a.chunk, a.chunks, 1, a.chunks, a.state0, a.chunk_log, a.err};
-    ida_status s = launch_ssm_states(f, true, false, st);
+    ida_status s = launch_ssm_chunk_states(f, false, st);
     if (s != IDA_OK) return s;
     f.x = a.dy;
     f.b = a.c;
     f.ldx = (long long)a.H * a.d;
     f.ldb = a.ldc;
     f.seg_state = a.adj;
-    return launch_ssm_states(f, true, true, st);
+    return launch_ssm_chunk_states(f, true, st);
 }
 
 ida_status launch_bwd_tc(const ScanBwdArgs &a, int splits, cudaStream_t st) {

@@ -192,6 +192,7 @@ __global__ void __launch_bounds__(CTH, 1)
         tmem_alloc(tslot, TCOLS);
         tmem_relinquish();
     }
+    dependent_wait();
     __syncthreads();
     tc_fence_after();
     const uint32_t tm = *tslot;
@@ -258,12 +259,6 @@ __global__ void __launch_bounds__(CTH, 1)
                 mma_commit(&bar[kState]);
             }
             __syncwarp();
-            if (i + 1 < nch) {  // in the place of P of chunk i - 1, which the MMAs before have read
-                ok = all_wait(kFullBC + (c ^ 1), ((i + 1) >> 1) & 1);
-                if (!ok) break;
-                if (elect_one()) issue_g(i + 1);
-                __syncwarp();
-            }
             if (i > 0) ok = all_wait(kFreeY, par ^ 1);
             if (!ok) break;
             if (elect_one()) {
@@ -277,6 +272,12 @@ __global__ void __launch_bounds__(CTH, 1)
                 mma_commit(&bar[kFreeBC + c]);
             }
             __syncwarp();
+            if (i + 1 < nch) {  // in the place of P of chunk i - 1, which the MMAs before have read
+                ok = all_wait(kFullBC + (c ^ 1), ((i + 1) >> 1) & 1);
+                if (!ok) break;
+                if (elect_one()) issue_g(i + 1);
+                __syncwarp();
+            }
             ok = all_wait(kRows, par) && all_wait(kP + c, (i >> 1) & 1);
             if (!ok) break;
             if (elect_one()) {
@@ -557,34 +558,42 @@ __global__ void __launch_bounds__(CTH, 1)
     }
 }
 
-// A segment's last state from zero (the first segment's: from state_in) and its log2 decay; a
-// single segment's is the final state.  Chunks from the last to the first.  REV: what a segment
-// passes on of its own adjoint, sum_t a_first .. a_t c_t dy_t^T, from dy and c in the places of x
-// and b; there the sum up to a chunk is needed, so chunks go from the first to the last.
-template <int DP, int MP, int PARTS, bool REV>
+// What the state kernel leaves: a part's last state (from state_in for the first part) and its
+// log2 decay; or every chunk's by itself, or what every chunk passes on of its own adjoint (from dy
+// and c in the places of x and b).
+enum { kPart, kEach, kAdjoint };
+
+// Parts are walked backwards.  Chunks by themselves (of a.seg <= 128 positions each, `per` of a CTA)
+// alternate between two accumulators, so that one is written out while the next is made.
+template <int DP, int MP, int PARTS, int MODE>
 __global__ void __launch_bounds__(STH, MP == 64 ? 2 : 1)
-    ssm_state_kernel(ScanArgs a, const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_b) {
+    ssm_state_kernel(ScanArgs a, int per, const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_b) {
     using L = SsmStateSmem<DP, MP, PARTS>;
     extern __shared__ __align__(1024) unsigned char sm[];
     const uint32_t s0 = smem_u32(sm);
     uint64_t *bar = reinterpret_cast<uint64_t *>(sm + L::MISC);  // 0, 1 copies, 2, 3 MMAs, of each buffer
     uint32_t *tslot = reinterpret_cast<uint32_t *>(sm + L::MISC + 48);
+    Rate2 *rate_s = reinterpret_cast<Rate2 *>(sm + L::MISC + 56);
     float *arrays = reinterpret_cast<float *>(sm + L::ARR);
     long long *tot = reinterpret_cast<long long *>(sm + L::TOT);
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
     const int q4 = warp & 3, half = warp >> 2, tl = 32 * q4 + lane;
     const uint32_t lane_base = (uint32_t)(32 * q4) << 16;
     const int H = a.H, N = a.N, M = a.M, d = a.d;
-    const int slices = (d + DP - 1) / DP;
+    const int slices = (d + DP - 1) / DP, parts = a.segs * a.fine;
+    constexpr bool EACH = MODE != kPart;
+    constexpr uint32_t COLS = EACH ? 2 * MP : MP;
+    const int groups = EACH ? (parts + per - 1) / per : a.state_segs;
     int id = blockIdx.x;
-    const int seg = id % a.state_segs;
-    id /= a.state_segs;
+    const int seg = id % groups;
+    id /= groups;
     const int j0 = id % slices * DP, unit = id / slices, b = unit / H, h = unit % H, g = h / (H / a.G);
-    const int len = a.seg / a.fine, t_begin = seg * len, t_end = min(N, t_begin + len);
-    const int nch = t_end > t_begin ? (t_end - t_begin + SQ - 1) / SQ : 0, parts = a.segs * a.fine;
+    // positions of the CTA, and of a chunk of it
+    const int len = EACH ? a.seg * per : a.seg / a.fine, step = EACH ? a.seg : SQ;
+    const int t_begin = seg * len, t_end = min(N, t_begin + len);
+    const int nch = t_end > t_begin ? (t_end - t_begin + step - 1) / step : 0;
     const __nv_bfloat16 *gdt = static_cast<const __nv_bfloat16 *>(a.dt) + (size_t)b * N * a.lddt + h;
     const float dt_bias = a.dt_bias[h];
-    const Rate2 rate(a.a_log[h]);
 
     if ((s0 & 1023u) != 0u) {
         if (tid == 0) report_error(a.err, kErrShape);
@@ -597,10 +606,10 @@ __global__ void __launch_bounds__(STH, MP == 64 ? 2 : 1)
         tma_prefetch_desc(&tm_b);
     }
     if (warp == 0) {
-        tmem_alloc(tslot, MP);
+        tmem_alloc(tslot, COLS);
         tmem_relinquish();
     }
-    const auto start_of = [&](int n) { return t_begin + (REV ? n : nch - 1 - n) * SQ; };  // the n-th chunk walked
+    const auto start_of = [&](int n) { return t_begin + (EACH ? n : nch - 1 - n) * step; };  // the n-th chunk walked
     const auto fetch = [&](int n) {  // one thread
         const int buf = n % L::NB, t0 = start_of(n);
         mbar_arrive_expect_tx(&bar[buf], (uint32_t)SSLAB * (DP / 64 + MP / 64));
@@ -614,27 +623,62 @@ __global__ void __launch_bounds__(STH, MP == 64 ? 2 : 1)
     float dt_next = 0.f;
     const auto fetch_dt = [&](int n) {
         const int k = tid - SQ, p = start_of(n) + k;
-        if (k >= 0) dt_next = n < nch && p < t_end ? __bfloat162float(gdt[(size_t)p * a.lddt]) : 0.f;
+        if (k >= 0) dt_next = n < nch && k < step && p < t_end ? __bfloat162float(gdt[(size_t)p * a.lddt]) : 0.f;
     };
+    fetch_dt(0);
+    __syncthreads();
+    // the launches behind may take their places now: not before, a CTA of theirs that got this SM's TMEM
+    // ahead of this one would wait for this one
+    dependent_launch();
+    if (tid == 0)
+        for (int n = 0; n < L::NB && n < nch; ++n) fetch(n);
+    if (warp == 4) {
+        const Rate2 r = rate2_of(a.a_log[h]);
+        if (lane == 0) *rate_s = r;
+    }
+    tc_fence_after();
+    const uint32_t tm = *tslot;
     long long behind = 0;  // log2 a summed over the chunks done, in warps 4 .. 7
     const auto make_weights = [&](int n) {
         const int k = tid - SQ;
         if (k < 0) return;
-        float delta = 0.f;
-        if (start_of(n) + k < t_end) delta = softplus(dt_next + dt_bias);
+        const bool in = k < step && start_of(n) + k < t_end;
+        const float delta = in ? softplus(dt_next + dt_bias) : 0.f;
         long long all;
-        const long long fx = chunk_sum(rate, delta, k, tot, all);
-        arrays[(n & 1) * SQ + k] = REV ? (start_of(n) + k < t_end ? ex2_fix(fx + behind) : 0.f) : ex2_fix(all - fx + behind) * delta;
-        behind += all;
+        const long long fx = chunk_sum(*rate_s, delta, k, tot, all);
+        if (MODE == kAdjoint)
+            arrays[(n & 1) * SQ + k] = in ? ex2_fix(fx) : 0.f;
+        else
+            arrays[(n & 1) * SQ + k] = ex2_fix(all - fx + behind) * delta;
+        if (!EACH) behind += all;
+        if (MODE == kEach && k == 0 && j0 == 0) a.seg_log[(size_t)unit * parts + seg * per + n] = (float)all * kUnfix;
     };
-    fetch_dt(0);
-    __syncthreads();
-    if (tid == 0)
-        for (int n = 0; n < L::NB && n < nch; ++n) fetch(n);
+    // the accumulator of chunk n (of the whole part) to memory
+    const auto write_out = [&](int n, float *out, const float *in, float f) {
+        if (DP == 64 && tl >= DP) return;
+        constexpr int MH = MP / 2;
+#pragma unroll
+        for (int blk = 0; blk < MH / 16; ++blk) {
+            const int m0 = half * MH + 16 * blk;
+            float v[16];
+            tmem_ld16(tm + lane_base + (EACH && (n & 1) ? MP : 0) + m0, v);
+            tmem_wait_ld();
+            if (nch == 0)
+#pragma unroll
+                for (int e = 0; e < 16; ++e) v[e] = 0.f;
+            if (j0 + tl < d)
+#pragma unroll
+                for (int e = 0; e < 16; ++e)
+                    if (m0 + e < M) {
+                        const size_t at = (size_t)(m0 + e) * d + j0 + tl;
+                        out[at] = in ? fmaf(f, __ldg(in + at), v[e]) : v[e];
+                    }
+        }
+    };
+    const auto each_out = [&](int n) { return a.seg_state + ((size_t)unit * parts + seg * per + n) * M * d; };
+    named_sync(2, STH);  // the rate
     if (nch > 0) make_weights(0);  // the last segment may have parts without a position
     fetch_dt(1);
-    tc_fence_after();
-    const uint32_t tm = *tslot;
     bool ok = true;
     int n = 0;
     for (; n < nch; ++n) {
@@ -642,7 +686,7 @@ __global__ void __launch_bounds__(STH, MP == 64 ? 2 : 1)
         const uint32_t par = (n / L::NB) & 1;
         ok = mbar_wait(&bar[buf], par) && ok;
         if (__syncthreads_or(!ok)) break;  // the tiles and the weights are there
-        // b 2^(S_end - S_s) D_s: row r, half of the columns
+        // b times its weight: row r, half of the columns
         const int r = tid & 127, p0 = (tid >> 7) * (MP / 16);
         const float w = arrays[(n & 1) * SQ + r];
 #pragma unroll
@@ -671,6 +715,7 @@ __global__ void __launch_bounds__(STH, MP == 64 ? 2 : 1)
             ok = mbar_wait(&bar[2 + (buf ^ 1)], ((n - 1) / 2) & 1);
             if (ok) fetch(n + 1);
         }
+        tc_fence_before();
         __syncthreads();
         if (warp == 0 && elect_one()) {
             tc_fence_after();
@@ -682,7 +727,8 @@ __global__ void __launch_bounds__(STH, MP == 64 ? 2 : 1)
                 const SmemDesc dh = sw_desc(s0 + L::B + buf * L::BB + part * (MP / 64) * SSLAB, SSLAB);
 #pragma unroll
                 for (int k = 0; k < SQ / 16; ++k)
-                    mma_f16(tm, sw_step(da, k * 2048), sw_step(dh, k * 2048), id_x, n > 0 || part < PARTS - 1 || k > 0);
+                    mma_f16(tm + (EACH && (n & 1) ? MP : 0), sw_step(da, k * 2048), sw_step(dh, k * 2048), id_x,
+                            (!EACH && n > 0) || part < PARTS - 1 || k > 0);
             }
             mma_commit(&bar[2 + buf]);
         }
@@ -691,9 +737,14 @@ __global__ void __launch_bounds__(STH, MP == 64 ? 2 : 1)
             make_weights(n + 1);
             fetch_dt(n + 2);
         }
-        if (L::NB == 1 && tid == 0 && n + 1 < nch) {
-            ok = mbar_wait(&bar[2], par);
-            if (ok) fetch(n + 1);
+        if (EACH && n > 0) {  // the chunk before, whose MMAs have completed
+            if (L::NB == 2) ok = mbar_wait(&bar[2 + (buf ^ 1)], ((n - 1) / 2) & 1) && ok;
+            tc_fence_after();
+            write_out(n - 1, each_out(n - 1), nullptr, 0.f);
+        }
+        if (L::NB == 1 && n + 1 < nch) {
+            ok = mbar_wait(&bar[2], par) && ok;
+            if (tid == 0 && ok) fetch(n + 1);
         }
     }
     if (n == nch) {
@@ -708,57 +759,39 @@ __global__ void __launch_bounds__(STH, MP == 64 ? 2 : 1)
             report_error(a.err, kErrWaitTimeout);
             for (int k = 0; k < L::NB && n + k < nch; ++k) mbar_wait(&bar[(n + k) % L::NB], ((n + k) / L::NB) & 1);
         }
+    } else if (EACH) {
+        if (nch > 0) write_out(nch - 1, each_out(nch - 1), nullptr, 0.f);
     } else {
-        // a single segment's last state is the final state
-        float *out = parts == 1 && a.final_state ? a.final_state + (size_t)unit * M * d
-                                                 : a.seg_state + ((size_t)unit * parts + seg) * M * d;
-        if (tid >= SQ && tid < SQ + 1) arrays[0] = (float)behind * kUnfix;
+        // a single part's last state is the final state
+        float *out = parts == 1 ? a.final_state + (size_t)unit * M * d : a.seg_state + ((size_t)unit * parts + seg) * M * d;
+        if (tid == SQ) arrays[0] = (float)behind * kUnfix;
         __syncthreads();
-        const float *in = !REV && seg == 0 && a.state_in ? a.state_in + (size_t)unit * M * d : nullptr;
-        const float total = arrays[0], f = ex2(total);
-        constexpr int MH = MP / 2;
-        if (DP == 128 || tl < DP) {
-#pragma unroll
-            for (int blk = 0; blk < MH / 16; ++blk) {
-                const int m0 = half * MH + 16 * blk;
-                float v[16];
-                tmem_ld16(tm + lane_base + m0, v);
-                tmem_wait_ld();
-                if (nch == 0)
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) v[e] = 0.f;
-                if (j0 + tl < d)
-#pragma unroll
-                    for (int e = 0; e < 16; ++e)
-                        if (m0 + e < M) {
-                            const size_t at = (size_t)(m0 + e) * d + j0 + tl;
-                            out[at] = in ? fmaf(f, __ldg(in + at), v[e]) : v[e];
-                        }
-            }
-        }
-        if (!REV && tid == 0 && j0 == 0 && parts > 1) a.seg_log[(size_t)unit * parts + seg] = total;
+        const float total = arrays[0];
+        write_out(0, out, seg == 0 && a.state_in ? a.state_in + (size_t)unit * M * d : nullptr, ex2(total));
+        if (tid == 0 && j0 == 0 && parts > 1) a.seg_log[(size_t)unit * parts + seg] = total;
     }
     tc_fence_before();
     __syncthreads();
     if (warp == 0) {
         tc_fence_after();
-        tmem_dealloc(tm, MP);
+        tmem_dealloc(tm, COLS);
     }
 }
 
-// Segment states, in place: seg_state[s] becomes the state before part s; the final state where it
-// is wanted.  One thread per four state elements.
-__global__ void __launch_bounds__(256) ssm_carry_kernel(ScanArgs a) {
-    const long long i = (long long)blockIdx.x * 256 + threadIdx.x;
+// Segment states, in place: seg_state[s] becomes the state before part s where a segment starts; the
+// final state where it is wanted.  One thread per four state elements.
+__global__ void __launch_bounds__(128) ssm_carry_kernel(ScanArgs a) {
+    dependent_launch();
+    dependent_wait();
+    const long long i = (long long)blockIdx.x * 128 + threadIdx.x;
     const int n = a.M * a.d / 4, parts = a.segs * a.fine;
     const int unit = (int)(i / n), e = (int)(i % n);
     if (unit >= a.B * a.H) return;
     float4 *p = reinterpret_cast<float4 *>(a.seg_state + (size_t)unit * parts * a.M * a.d) + e;
     const float *lg = a.seg_log + (size_t)unit * parts;
-    float4 X = make_float4(0.f, 0.f, 0.f, 0.f);
     // the first part starts from the given state, which its last state holds
-    float4 start = X;
-    if (a.state_in) start = __ldg(reinterpret_cast<const float4 *>(a.state_in + (size_t)unit * a.M * a.d) + e);
+    float4 X = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (a.state_in) X = __ldg(reinterpret_cast<const float4 *>(a.state_in + (size_t)unit * a.M * a.d) + e);
     constexpr int K = 8;
     for (int s0 = 0; s0 < parts; s0 += K) {
         float4 v[K];
@@ -773,10 +806,10 @@ __global__ void __launch_bounds__(256) ssm_carry_kernel(ScanArgs a) {
         for (int k = 0; k < K; ++k) {
             const int s = s0 + k;
             if (s >= parts) break;
-            if (s % a.fine == 0) p[(size_t)s * n] = s == 0 ? start : X;  // a segment starts here
+            if (s % a.fine == 0) p[(size_t)s * n] = X;  // a segment starts here
             if (s < a.state_segs) {
                 const float w = ex2(f[k]);
-                X = make_float4(fmaf(w, X.x, v[k].x), fmaf(w, X.y, v[k].y), fmaf(w, X.z, v[k].z), fmaf(w, X.w, v[k].w));
+                X = s == 0 ? v[k] : make_float4(fmaf(w, X.x, v[k].x), fmaf(w, X.y, v[k].y), fmaf(w, X.z, v[k].z), fmaf(w, X.w, v[k].w));
             }
         }
     }
@@ -841,7 +874,7 @@ void ssm_chunk_segments(int B, int H, int N, int d, int M, int num_sms, int &seg
     fine = pick_fine;
 }
 
-template <int DP, int MP, int PARTS, bool REV>
+template <int DP, int MP, int PARTS, int MODE>
 static ida_status launch_states(const ScanArgs &a, cudaStream_t st) {
     constexpr int smem = SsmStateSmem<DP, MP, PARTS>::TOTAL;
     static_assert(smem <= (MP == 64 ? 113 : 227) * 1024, "shared memory budget");
@@ -849,23 +882,34 @@ static ida_status launch_states(const ScanArgs &a, cudaStream_t st) {
     ida_status s = ssm_map(&mx, a.x, a.B, a.N, a.H, a.d, a.ldx);
     if (s == IDA_OK) s = ssm_map(&mb, a.b, a.B, a.N, a.G, a.M, a.ldb);
     if (s != IDA_OK) return s;
-    const auto kernel = ssm_state_kernel<DP, MP, PARTS, REV>;
+    const auto kernel = ssm_state_kernel<DP, MP, PARTS, MODE>;
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return fail_with(IDA_ERR_CUDA, cudaGetErrorString(e));
     const long long units = (long long)a.B * a.H * ((a.d + DP - 1) / DP);
-    kernel<<<(unsigned)(units * a.state_segs), STH, smem, st>>>(a, mx, mb);
+    // chunks by themselves: as many of a CTA as leave every SM its two (one where M > 64)
+    const long long slots = MP == 64 ? 304 : 152, chunks = (long long)a.segs * a.fine;
+    const int per = (int)((units * chunks + slots - 1) / slots < chunks ? (units * chunks + slots - 1) / slots : chunks);
+    const long long groups = MODE == kPart ? a.state_segs : (chunks + per - 1) / per;
+    kernel<<<(unsigned)(units * groups), STH, smem, st>>>(a, per, mx, mb);
     return launched("ssm segment states");
 }
 
 template <int DP, int MP>
-static ida_status launch_states_of(const ScanArgs &a, bool exact, bool rev, cudaStream_t st) {
-    if (rev) return launch_states<DP, MP, 3, true>(a, st);
-    return exact ? launch_states<DP, MP, 3, false>(a, st) : launch_states<DP, MP, 1, false>(a, st);
+static ida_status launch_states_of(const ScanArgs &a, bool exact, cudaStream_t st) {
+    return exact ? launch_states<DP, MP, 3, kPart>(a, st) : launch_states<DP, MP, 1, kPart>(a, st);
+}
+ida_status launch_ssm_states(const ScanArgs &a, bool exact, cudaStream_t st) {
+    if (a.d <= 64) return a.M <= 64 ? launch_states_of<64, 64>(a, exact, st) : launch_states_of<64, 128>(a, exact, st);
+    return a.M <= 64 ? launch_states_of<128, 64>(a, exact, st) : launch_states_of<128, 128>(a, exact, st);
 }
 
-ida_status launch_ssm_states(const ScanArgs &a, bool exact, bool rev, cudaStream_t st) {
-    if (a.d <= 64) return a.M <= 64 ? launch_states_of<64, 64>(a, exact, rev, st) : launch_states_of<64, 128>(a, exact, rev, st);
-    return a.M <= 64 ? launch_states_of<128, 64>(a, exact, rev, st) : launch_states_of<128, 128>(a, exact, rev, st);
+template <int DP, int MP>
+static ida_status launch_each_of(const ScanArgs &a, bool rev, cudaStream_t st) {
+    return rev ? launch_states<DP, MP, 3, kAdjoint>(a, st) : launch_states<DP, MP, 3, kEach>(a, st);
+}
+ida_status launch_ssm_chunk_states(const ScanArgs &a, bool rev, cudaStream_t st) {
+    if (a.d <= 64) return a.M <= 64 ? launch_each_of<64, 64>(a, rev, st) : launch_each_of<64, 128>(a, rev, st);
+    return a.M <= 64 ? launch_each_of<128, 64>(a, rev, st) : launch_each_of<128, 128>(a, rev, st);
 }
 
 template <int DP, int MP>
@@ -878,14 +922,18 @@ static ida_status launch_chunk(const ScanArgs &a, const CUtensorMap &mx, const C
     const long long units = (long long)a.B * a.H * ((a.d + DP - 1) / DP);
     if (units * a.segs * a.fine > 0x7FFFFFFFLL) return fail_with(IDA_ERR_UNSUPPORTED, "too many rows and heads");
     ida_status s = IDA_OK;
-    if (a.state_segs > 0) s = launch_ssm_states(a, a.final_state != nullptr, false, st);
-    if (s == IDA_OK && a.segs > 1) {
-        const long long n = (long long)a.B * a.H * (a.M * a.d / 4);
-        ssm_carry_kernel<<<(unsigned)((n + 255) / 256), 256, 0, st>>>(a);
-        s = launched("ssm segment sums");
-    }
+    if (a.state_segs > 0) s = launch_ssm_states(a, a.final_state != nullptr, st);
     if (s != IDA_OK) return s;
-    ssm_chunk_kernel<DP, MP><<<(unsigned)(units * a.segs), CTH, smem, st>>>(a, mx, mb, mc, my);
+    if (a.segs > 1) {
+        const long long n = (long long)a.B * a.H * a.M * a.d / 4;
+        e = launch_dependent(ssm_carry_kernel, dim3((unsigned)((n + 127) / 128)), dim3(128), 0, st, a);
+        if (e != cudaSuccess) return fail_with(IDA_ERR_CUDA, std::string("ssm segment sums launch: ") + cudaGetErrorString(e));
+    }
+    if (a.state_segs > 0)
+        e = launch_dependent(ssm_chunk_kernel<DP, MP>, dim3((unsigned)(units * a.segs)), dim3(CTH), smem, st, a, mx, mb, mc, my);
+    else
+        ssm_chunk_kernel<DP, MP><<<(unsigned)(units * a.segs), CTH, smem, st>>>(a, mx, mb, mc, my);
+    if (e != cudaSuccess) return fail_with(IDA_ERR_CUDA, std::string("ssm scan launch: ") + cudaGetErrorString(e));
     return launched("ssm scan");
 }
 

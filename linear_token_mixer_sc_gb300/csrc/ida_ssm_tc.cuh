@@ -58,16 +58,16 @@ __device__ __forceinline__ float ex2_fix(long long x) {
 }
 
 // The rate e^a_log log2 e in two floats: an error in it would be the same in every position of a
-// head.  (fp64 issues at a small fraction of the fp32 rate on this part: the products below, taken in
-// fp64, were half of a chunk's time.)
+// head.  (fp64 issues at a small fraction of the fp32 rate on this part: one warp makes the rates,
+// a lane each, and no position takes an fp64 product.)
 struct Rate2 {
     float hi, lo;
-    __device__ __forceinline__ explicit Rate2(float a_log) {
-        const double r = exp((double)a_log) * 1.4426950408889634;
-        hi = (float)r;
-        lo = (float)(r - (double)hi);
-    }
 };
+__device__ __forceinline__ Rate2 rate2_of(float a_log) {
+    const double r = exp((double)a_log) * 1.4426950408889634;
+    const float hi = (float)r;
+    return {hi, (float)(r - (double)hi)};
+}
 // log2 of exp(-rate delta) in fixed point, from the exact product of the leading parts
 __device__ __forceinline__ long long log2_fix(const Rate2 &rate, float delta) {
     const float p = rate.hi * delta, e = fmaf(rate.hi, delta, -p) + rate.lo * delta;
@@ -100,9 +100,31 @@ __device__ __forceinline__ long long chunk_sum(const Rate2 &rate, float delta, i
 // behind w and positions behind N are read as zero and not written.
 ida_status ssm_map(CUtensorMap *m, const void *p, int B, int N, int K, int w, long long ld, int rows = SQ);
 
-// Each segment's last state from zero (from state_in for the first), with rev the sum
-// sum_t a_first .. a_t c_t dy_t^T of the adjoint it passes on; a.x, a.b and their strides then are
-// dy's and c's.
-ida_status launch_ssm_states(const ScanArgs &a, bool exact, bool rev, cudaStream_t st);
+// Each part's last state from zero (from state_in for the first), rounded as three bf16 parts of
+// its operands or one.
+ida_status launch_ssm_states(const ScanArgs &a, bool exact, cudaStream_t st);
+
+// Every chunk's (a.seg positions) last state from zero, with rev the sum sum_t a_first .. a_t c_t dy_t^T
+// of the adjoint it passes on; a.x, a.b and their strides then are dy's and c's.
+ida_status launch_ssm_chunk_states(const ScanArgs &a, bool rev, cudaStream_t st);
+
+// A launch that may start while the one before it in the stream ends; its kernel waits (dependent_wait)
+// before it touches memory.
+template <typename... K, typename... A>
+cudaError_t launch_dependent(void (*kernel)(K...), dim3 grid, dim3 block, size_t smem, cudaStream_t st, A... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = block;
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, K(args)...);
+}
+__device__ __forceinline__ void dependent_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void dependent_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
 }  // namespace ida
