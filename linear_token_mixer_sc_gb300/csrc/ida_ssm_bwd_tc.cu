@@ -52,13 +52,13 @@ struct BwdSmem {
     static constexpr int ST = P + (QB > XB ? QB : XB);  // [3] parts of Z, later of X_0
     static constexpr int MISC = ST + 3 * PART;
     static constexpr int ARR = MISC + 64;
-    // S in two floats, 2^S, f, D, z, column factors, column sums of K in 8 parts and row sums in 4 + 1,
-    // the inter-chunk products in 4 parts each, G and E of a position with itself
-    static constexpr int NARR = 7 + 8 + 5 + 8 + 2;
+    // S in two floats, 2^S, f, D and column factors of two heads; column sums of K in 8 parts and row
+    // sums in 4 + 1, the inter-chunk products in 4 parts each, G and E of a position with itself
+    static constexpr int NARR = 2 * 6 + 8 + 5 + 8 + 2;
     // <Z, X_0> per warp, 2^S_Q, parameters' parts; sums per warp; sums of K per pair of groups
     static constexpr int RED = ARR + NARR * SQ * 4;
-    static constexpr int RATES = RED + 128 + 32 + 256;  // of 32 heads
-    static constexpr int TOT = RATES + 256;
+    static constexpr int RATES = RED + 128 + 32 + 256;  // of 64 heads, made 32 at a time
+    static constexpr int TOT = RATES + 512;
     static constexpr int TOTAL = TOT + 32;
 };
 
@@ -105,8 +105,7 @@ __global__ void __launch_bounds__(BTH, 1)
     uint64_t *bar = reinterpret_cast<uint64_t *>(sm + L::MISC);  // 0 b, c; 1 x, dy; 2 E and Z^T b; 3 dx, Z x; 4 the rest
     uint32_t *tslot = reinterpret_cast<uint32_t *>(sm + L::MISC + 48);
     float *arr = reinterpret_cast<float *>(sm + L::ARR);
-    float *Sh = arr, *Sl = Sh + SQ, *et = Sl + SQ, *fs = et + SQ, *dl = fs + SQ, *zz = dl + SQ, *rt = zz + SQ;
-    float *ksum_t = rt + SQ;          // [8 groups of 16][128]: sum over the group's s of K, per t
+    float *ksum_t = arr + 12 * SQ;    // [8 groups of 16][128]: sum over the group's s of K, per t
     float *ksum_s = ksum_t + 8 * SQ;  // [4 warps of a quarter][128]: sum over their t of K / D_s, per s, ...
     float *kown = ksum_s + 4 * SQ;    // [128]: ... and over the t of s's own group
     float *zin = kown + SQ;           // [4][128]: b_s^T Z x_s
@@ -154,12 +153,15 @@ __global__ void __launch_bounds__(BTH, 1)
             tma_load_4d(sm + L::DY + i * L::SLAB, &tm_dy, 64 * i, h, t0, b, &bar[1]);
         }
     };
-    // one state [M][d], its three parts as tiles [m][j]; with `other`, returns my share of <st, other>
-    const auto load_state = [&](const float *st, const float *other) {
+    // one state [M][d]: read and split into its three parts, held in registers until their tiles
+    // [m][j] may be written; with `other`, returns my share of <st, other>
+    constexpr int NI = MP * DP / 8 / BTH;
+    uint4 held[NI][3];
+    const auto read_state = [&](const float *st, const float *other) {
         float dot = 0.f;
 #pragma unroll
-        for (int i = tid; i < MP * DP / 8; i += BTH) {
-            const int m = i / (DP / 8), j = i % (DP / 8) * 8;
+        for (int n = 0; n < NI; ++n) {
+            const int i = tid + n * BTH, m = i / (DP / 8), j = i % (DP / 8) * 8;
             float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
             if (m < M && j < d) {
                 *reinterpret_cast<float4 *>(v) = __ldg(reinterpret_cast<const float4 *>(st + (size_t)m * d + j));
@@ -172,13 +174,47 @@ __global__ void __launch_bounds__(BTH, 1)
                     for (int e = 0; e < 8; ++e) dot = fmaf(u[e], v[e], dot);
                 }
             }
-            uint4 p[3];
-            split3(v, p);
-#pragma unroll
-            for (int k = 0; k < 3; ++k)
-                *reinterpret_cast<uint4 *>(sm + L::ST + k * L::PART + j / 64 * L::PSLAB + sw_off(m, j % 64 / 8)) = p[k];
+            split3(v, held[n]);
         }
         return dot;
+    };
+    const auto write_state = [&]() {
+#pragma unroll
+        for (int n = 0; n < NI; ++n) {
+            const int i = tid + n * BTH, m = i / (DP / 8), j = i % (DP / 8) * 8;
+#pragma unroll
+            for (int k = 0; k < 3; ++k)
+                *reinterpret_cast<uint4 *>(sm + L::ST + k * L::PART + j / 64 * L::PSLAB + sw_off(m, j % 64 / 8)) = held[n][k];
+        }
+    };
+    // step sizes and decays of head g rep + r, by the first four warps, into the arrays of r's parity
+    float dt_next = 0.f;
+    const auto read_dt = [&](int r) {
+        if (tid < len && r < r1)
+            dt_next = __bfloat162float(static_cast<const __nv_bfloat16 *>(a.dt)[((size_t)b * N + t0 + tid) * a.lddt + g * rep + r]) + a.dt_bias[g * rep + r];
+    };
+    const auto make_arrays = [&](int r) {
+        if (tid >= SQ || r >= r1) return;
+        if (((r - r0) & 31) == 0) {  // the rates of the next 32 heads
+            if (warp == 0 && r + lane < r1) rates[((r - r0) & 63) + lane] = rate2_of(a.a_log[g * rep + r + lane]);
+            named_sync(1, 128);
+        }
+        float *Sh = arr + ((r - r0) & 1) * 6 * SQ, *Sl = Sh + SQ, *et = Sl + SQ, *fs = et + SQ, *dl = fs + SQ, *rt = dl + SQ;
+        const float delta = tid < len ? softplus(dt_next) : 0.f;
+        long long all;
+        const long long fx = chunk_sum(rates[(r - r0) & 63], delta, tid, tot, all);
+        const float hi = (float)fx * kUnfix;
+        // S at the end of the block of 16 before mine
+        const int edge = (lane & 16) - 1;
+        long long ref = __shfl_sync(0xffffffffu, fx, edge < 0 ? 0 : edge);
+        if (edge < 0) ref = tid < 32 ? 0 : tid < 64 ? tot[0] : tid < 96 ? tot[0] + tot[1] : tot[0] + tot[1] + tot[2];
+        Sh[tid] = hi;
+        Sl[tid] = (float)(fx - (long long)(hi * kFix)) * kUnfix;
+        et[tid] = ex2_fix(fx);
+        fs[tid] = ex2_fix(all - fx);
+        dl[tid] = delta;
+        rt[tid] = ex2_fix(fx - ref);
+        if (tid == 0) red[16 + 15 * ((r - r0) & 1)] = ex2_fix(all);
     };
     __syncthreads();
     if (tid == 0 && r0 < r1) {
@@ -196,40 +232,17 @@ __global__ void __launch_bounds__(BTH, 1)
     // shared memory, and the lanes that get them are not read
     const bool mine = row < Q;
     bool ok = true;
+    read_dt(r0);
+    make_arrays(r0);
+    read_dt(r0 + 1);
+    if (r0 < r1) read_state(a.adj + ((size_t)(b * H + g * rep + r0) * a.chunks + ch) * M * d, nullptr);
     int r = r0;
     for (; r < r1; ++r) {
         const int h = g * rep + r, unit = b * H + h;
         const uint32_t par = (r - r0) & 1;
         const size_t so = ((size_t)unit * a.chunks + ch) * M * d;
-        const float rate = expf(a.a_log[h]);
-        // step sizes and decays of the head, by the first four warps
-        if (tid < SQ) {
-            if (((r - r0) & 31) == 0) {  // the rates of the next 32 heads
-                if (warp == 0 && r + lane < r1) rates[lane] = rate2_of(a.a_log[h + lane]);
-                named_sync(1, 128);
-            }
-            float delta = 0.f, z = 0.f;
-            if (tid < len) {
-                z = __bfloat162float(static_cast<const __nv_bfloat16 *>(a.dt)[((size_t)b * N + t0 + tid) * a.lddt + h]) + a.dt_bias[h];
-                delta = softplus(z);
-            }
-            long long all;
-            const long long fx = chunk_sum(rates[(r - r0) & 31], delta, tid, tot, all);
-            const float hi = (float)fx * kUnfix;
-            // S at the end of the block of 16 before mine
-            const int edge = (lane & 16) - 1;
-            long long ref = __shfl_sync(0xffffffffu, fx, edge < 0 ? 0 : edge);
-            if (edge < 0) ref = tid < 32 ? 0 : tid < 64 ? tot[0] : tid < 96 ? tot[0] + tot[1] : tot[0] + tot[1] + tot[2];
-            Sh[tid] = hi;
-            Sl[tid] = (float)(fx - (long long)(hi * kFix)) * kUnfix;
-            et[tid] = ex2_fix(fx);
-            fs[tid] = ex2_fix(all - fx);
-            dl[tid] = delta;
-            zz[tid] = z;
-            rt[tid] = ex2_fix(fx - ref);
-            if (tid == 0) red[16] = ex2_fix(all);
-        }
-        load_state(a.adj + so, nullptr);
+        const float *Sh = arr + par * 6 * SQ, *Sl = Sh + SQ, *et = Sl + SQ, *fs = et + SQ, *dl = fs + SQ, *rt = dl + SQ;
+        write_state();  // Z
         fence_proxy_async_smem();
         if (r == r0) ok = mbar_wait(&bar[0], 0) && ok;
         ok = mbar_wait(&bar[1], par) && ok;
@@ -289,14 +302,21 @@ __global__ void __launch_bounds__(BTH, 1)
                     tmem_wait_ld();
                     if (kb >= 2 * q4 + 2) {  // wholly behind my rows: decay to the block's start, then inside it
                         const float f = ex2((Sh[16 * kb - 1] - sh) + (Sl[16 * kb - 1] - sl));
+const ssm_f2 ff = ssm_pack(f, f), dd = ssm_pack(delta, delta);
+                        ssm_f2 sum = 0ull;
 #pragma unroll
-                        for (int e = 0; e < 16; ++e) {
-                            const float w = f * rt[16 * kb + e], we = w * ev[e], k1 = we * gv[e];
-                            ks += k1;
-                            kk[e] = k1 * delta;
-                            gv[e] *= w * delta;
-                            ev[e] = we * delta;
+                        for (int e = 0; e < 16; e += 2) {
+                            const ssm_f2 w = ssm_mul(ff, *reinterpret_cast<const ssm_f2 *>(rt + 16 * kb + e));
+                            const ssm_f2 gg = ssm_pack(gv[e], gv[e + 1]), we = ssm_mul(w, ssm_pack(ev[e], ev[e + 1]));
+                            const ssm_f2 k1 = ssm_mul(we, gg), one = ssm_pack(1.f, 1.f);
+                            sum = ssm_fma(k1, one, sum);
+                            ssm_unpack(ssm_mul(k1, dd), kk[e], kk[e + 1]);
+                            ssm_unpack(ssm_mul(gg, ssm_mul(w, dd)), gv[e], gv[e + 1]);
+                            ssm_unpack(ssm_mul(we, dd), ev[e], ev[e + 1]);
                         }
+                        float lo, hi;
+                        ssm_unpack(sum, lo, hi);
+                        ks += lo + hi;
                     } else {
                         float ko = 0.f;
 #pragma unroll
@@ -366,13 +386,12 @@ __global__ void __launch_bounds__(BTH, 1)
             mma_commit(&bar[3]);
         }
         __syncwarp();
+        const float cross = warp_sum(read_state(a.state0 + so, a.adj + so));
         ok = mbar_wait(&bar[3], par);
         if (__syncthreads_or(!ok)) break;
         tc_fence_after();
-        {  // X_0's parts take the place of Z's
-            const float dot = warp_sum(load_state(a.state0 + so, a.adj + so));
-            if (lane == 0) red[warp] = dot;
-        }
+        if (lane == 0) red[warp] = cross;
+        write_state();  // X_0's parts take the place of Z's
         if (mine) {  // dx out: my row, a quarter of the channels, over P
             constexpr int CW = DP / 4;
 #pragma unroll
@@ -441,6 +460,11 @@ __global__ void __launch_bounds__(BTH, 1)
                 if (64 * s < d) tma_store_4d(&tm_dx, 64 * s, h, t0, b, sm + L::P + s * L::SLAB);
             bulk_commit();
         }
+        if (r + 1 < r1) {  // the next head's arrays and Z
+            make_arrays(r + 1);
+            read_dt(r + 2);
+            read_state(a.adj + so + (size_t)a.chunks * M * d, nullptr);
+        }
         ok = mbar_wait(&bar[4], par);
         if (__syncthreads_or(!ok)) break;
         tc_fence_after();
@@ -470,34 +494,38 @@ __global__ void __launch_bounds__(BTH, 1)
         tmem_wait_st();
         tc_fence_before();
         __syncthreads();
-        // w, dt's gradient and the chunk's parts of the parameters': position tid
-        if (tid < SQ) {
-            const int t = tid, J = t >> 4;
-            if (t < NG * NG) {  // sums of K per pair of groups
-                float v = 0.f;
+        // w, dt's gradient and the chunk's parts of the parameters', by the last four warps
+        if (tid >= BTH - SQ) {
+            const int t = tid - (BTH - SQ), J = t >> 4, wq = t >> 5;
+            float kc[NG], ks = 0.f, zi = 0.f, xi = 0.f, ko = 0.f, gg = 0.f, ee = 0.f, delta = 0.f, f = 0.f, e2 = 0.f;
 #pragma unroll
-                for (int e = 0; e < 16; ++e) v += ksum_t[t / NG * SQ + 16 * (t % NG) + e];
-                blk[t] = v;
-            }
-            float ks = 0.f, zi = 0.f, xi = 0.f, kt = 0.f;  // kt: K of s in earlier groups
-            float ko = 0.f, kd = 0.f;
+            for (int k = 0; k < NG; ++k) kc[k] = 0.f;
             if (t < Q) {
+#pragma unroll
+                for (int k = 0; k < NG; ++k) kc[k] = k <= J ? ksum_t[k * SQ + t] : 0.f;
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
                     ks += ksum_s[k * SQ + t];
                     zi += zin[k * SQ + t];
                     xi += xin[k * SQ + t];
                 }
-#pragma unroll
-                for (int k = 0; k < NG - 1; ++k) kt += k < J ? ksum_t[k * SQ + t] : 0.f;
                 ko = kown[t];
-                kd = ksum_t[J * SQ + t];
+                gg = gs[t];
+                ee = es[t];
+                delta = dl[t];
+                f = fs[t];
+                e2 = et[t];
             }
-            const float delta = dl[t], zf = zi * fs[t];
+            const float rate = rates[(r - r0) & 63].hi * 0.6931471805599453f, zf = zi * f;
+            float kt = 0.f, kd = 0.f;  // K of s in earlier groups, and in mine
+#pragma unroll
+            for (int k = 0; k < NG; ++k) {
+                kt += k < J ? kc[k] : 0.f;
+                kd = k == J ? kc[k] : kd;
+            }
             // over my group, from my position on: K from earlier groups, and inside the group the running
             // difference; before my position: K to later groups.  Over the warp: the inter-chunk terms
-            float su = kt + (kd - delta * ko), sb = delta * ks;
-            float iu = et[t] * xi, ib = delta * zf;
+            float su = kt + (kd - delta * ko), sb = delta * ks, iu = e2 * xi, ib = delta * zf;
             const float own_b = sb, own_ib = ib;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
@@ -510,37 +538,48 @@ __global__ void __launch_bounds__(BTH, 1)
                 if (lane + o < 32) iu += x;
                 if (lane >= o) ib += y;
             }
-            if (lane == 0) wsum[warp] = iu;
-            if (lane == 31) wsum[4 + warp] = ib;
-            named_sync(1, 128);
+            if (lane == 0) wsum[wq] = iu;
+            if (lane == 31) wsum[4 + wq] = ib;
+            // sums of K per pair of groups (s in group k, t in mine)
+#pragma unroll
+            for (int o = 8; o > 0; o >>= 1)
+#pragma unroll
+                for (int k = 0; k < NG; ++k) kc[k] += __shfl_xor_sync(0xffffffffu, kc[k], o);
+            if ((lane & 15) == 0 && t < Q)
+#pragma unroll
+                for (int k = 0; k < NG; ++k) blk[k * 8 + J] = kc[k];
+            named_sync(2, 128);
             float wt = su + (sb - own_b) + (iu + (ib - own_ib));
 #pragma unroll
-            for (int k = 0; k < 4; ++k) wt += k > warp ? wsum[k] : k < warp ? wsum[4 + k] : 0.f;
-            for (int i = 0; i < (J < NG ? J : 0); ++i)  // pairs of groups around mine
-                for (int k = J + 1; k < NG; ++k) wt += blk[NG * i + k];
-            float cross = 0.f;
+            for (int k = 0; k < 4; ++k) wt += k > wq ? wsum[k] : k < wq ? wsum[4 + k] : 0.f;
 #pragma unroll
-            for (int k = 0; k < BTH / 32; ++k) cross += red[k];
-            wt = fmaf(cross, red[16], wt);
+            for (int i = 0; i < NG - 2; ++i)  // pairs of groups around mine
+#pragma unroll
+                for (int k = i + 2; k < NG; ++k) wt += i < J && k > J ? blk[i * 8 + k] : 0.f;
+            float zx = 0.f;
+#pragma unroll
+            for (int k = 0; k < BTH / 32; ++k) zx += red[k];
+            wt = fmaf(zx, red[16 + 15 * par], wt);
             float ga = 0.f, gb = 0.f, gd = 0.f;
             if (t < len) {
-                const float ddt = (ks + ko + gs[t] * es[t] + zf - rate * wt) / (1.f + expf(-zz[t]));
+                // 1 / (1 + e^-z) of D = log(1 + e^z) is 1 - e^-D
+                const float ddt = (ks + ko + gg * ee + zf - rate * wt) * -expm1f(-delta);
                 static_cast<__nv_bfloat16 *>(a.ddt)[((size_t)b * N + t0 + t) * a.ldddt + h] = __float2bfloat16_rn(ddt);
                 ga = -rate * delta * wt;
                 gb = ddt;
-                gd = es[t];
+                gd = ee;
             }
             ga = warp_sum(ga);
             gb = warp_sum(gb);
             gd = warp_sum(gd);
             if (lane == 0) {
-                red[17 + 3 * warp] = ga;
-                red[18 + 3 * warp] = gb;
-                red[19 + 3 * warp] = gd;
+                red[17 + 3 * wq] = ga;
+                red[18 + 3 * wq] = gb;
+                red[19 + 3 * wq] = gd;
             }
-            named_sync(1, 128);
-            if (tid < 3)
-                a.part[((size_t)unit * a.chunks + ch) * 4 + tid] = red[17 + tid] + red[20 + tid] + red[23 + tid] + red[26 + tid];
+            named_sync(2, 128);
+            if (t < 3)
+                a.part[((size_t)unit * a.chunks + ch) * 4 + t] = red[17 + t] + red[20 + t] + red[23 + t] + red[26 + t];
         }
     }
     if (r < r1) {  // a wait ran out

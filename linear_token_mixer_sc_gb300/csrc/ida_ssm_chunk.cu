@@ -563,7 +563,8 @@ __global__ void __launch_bounds__(CTH, 1)
 // and c in the places of x and b).
 enum { kPart, kEach, kAdjoint };
 
-// Parts are walked backwards.  Chunks by themselves (of a.seg <= 128 positions each, `per` of a CTA)
+// Parts are walked backwards.  The MMAs' sums are cut off, not rounded, so over a part's chunks the small
+// bf16 parts of b have an accumulator of their own.  Chunks by themselves (of a.seg <= 128 positions each, `per` of a CTA)
 // alternate between two accumulators, so that one is written out while the next is made.
 template <int DP, int MP, int PARTS, int MODE>
 __global__ void __launch_bounds__(STH, MP == 64 ? 2 : 1)
@@ -582,7 +583,7 @@ __global__ void __launch_bounds__(STH, MP == 64 ? 2 : 1)
     const int H = a.H, N = a.N, M = a.M, d = a.d;
     const int slices = (d + DP - 1) / DP, parts = a.segs * a.fine;
     constexpr bool EACH = MODE != kPart;
-    constexpr uint32_t COLS = EACH ? 2 * MP : MP;
+    constexpr uint32_t COLS = EACH || PARTS > 1 ? 2 * MP : MP;
     const int groups = EACH ? (parts + per - 1) / per : a.state_segs;
     int id = blockIdx.x;
     const int seg = id % groups;
@@ -662,6 +663,13 @@ __global__ void __launch_bounds__(STH, MP == 64 ? 2 : 1)
             const int m0 = half * MH + 16 * blk;
             float v[16];
             tmem_ld16(tm + lane_base + (EACH && (n & 1) ? MP : 0) + m0, v);
+            if (!EACH && PARTS > 1) {
+                float u[16];
+                tmem_ld16(tm + lane_base + MP + m0, u);
+                tmem_wait_ld();
+#pragma unroll
+                for (int e = 0; e < 16; ++e) v[e] += u[e];
+            }
             tmem_wait_ld();
             if (nch == 0)
 #pragma unroll
@@ -727,8 +735,8 @@ __global__ void __launch_bounds__(STH, MP == 64 ? 2 : 1)
                 const SmemDesc dh = sw_desc(s0 + L::B + buf * L::BB + part * (MP / 64) * SSLAB, SSLAB);
 #pragma unroll
                 for (int k = 0; k < SQ / 16; ++k)
-                    mma_f16(tm + (EACH && (n & 1) ? MP : 0), sw_step(da, k * 2048), sw_step(dh, k * 2048), id_x,
-                            (!EACH && n > 0) || part < PARTS - 1 || k > 0);
+                    mma_f16(tm + ((EACH ? (n & 1) : part > 0) ? MP : 0), sw_step(da, k * 2048), sw_step(dh, k * 2048), id_x,
+                            (!EACH && n > 0) || (part < PARTS - 1 && (EACH || part > 0)) || k > 0);
             }
             mma_commit(&bar[2 + buf]);
         }

@@ -263,6 +263,7 @@ GRADS = [
     (1, 90, 2, 32, 2, 32, "f32", False, True), (1, 140, 1, 256, 1, 128, "bf16", False, False),
     (2, 150, 4, 64, 2, 128, "bf16", False, False), (1, 200, 6, 128, 1, 104, "bf16", False, False),
     (1, 260, 3, 16, 3, 72, "bf16", False, True), (1, 300, 5, 64, 1, 16, "bf16", False, False),
+    (1, 20, 70, 8, 1, 16, "bf16", False, False),  # one CTA's heads are more than two batches of rates
 ]
 NAMES = ("x", "b", "c", "dt", "a_log", "dt_bias", "D")
 
