@@ -36,7 +36,7 @@ struct ScanBwdArgs {
     float *adj;      // [B H][chunks][M][d]: a Z of the first position behind each chunk
     float *chunk_log;  // [B H][chunks]: the sum of log2 a over the chunk
     float *db_head, *dc_head;  // [B][N][H][M] per head, or NULL where nothing is left to sum
-    float *part;     // [B H][chunks][4]: the chunk's parts of da_log, ddt_bias, dD
+    float *part;     // [B H][chunks][4] ([4][4] on the tensor cores): the chunk's parts of da_log, ddt_bias, dD
     float *kept;     // [B H][chunks][chunk / 8][M][d]: the states behind its groups of 8 positions (CUDA cores)
     unsigned *err;
 };

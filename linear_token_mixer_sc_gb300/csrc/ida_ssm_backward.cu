@@ -503,14 +503,14 @@ __global__ void __launch_bounds__(256) bwd_group_kernel(ScanBwdArgs s, int n) {
 }
 
 // The head's parameter gradients: its chunks' parts over all rows, 128 interleaved sums.
-__global__ void __launch_bounds__(128) bwd_params_kernel(ScanBwdArgs s) {
+__global__ void __launch_bounds__(128) bwd_params_kernel(ScanBwdArgs s, int per) {  // per: parts of a chunk
     __shared__ float red[4][3];
     const int h = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     float v[3] = {0.f, 0.f, 0.f};
-    const long long n = (long long)s.B * s.chunks;
+    const long long n = (long long)s.B * s.chunks * per;
     for (long long i = threadIdx.x; i < n; i += 128) {
-        const long long b = i / s.chunks, c = i % s.chunks;
-        const float4 u = *reinterpret_cast<const float4 *>(s.part + ((size_t)(b * s.H + h) * s.chunks + c) * 4);
+        const long long b = i / (s.chunks * per), c = i % (s.chunks * per);
+        const float4 u = *reinterpret_cast<const float4 *>(s.part + ((size_t)(b * s.H + h) * s.chunks * per + c) * 4);
         v[0] += u.x;
         v[1] += u.y;
         v[2] += u.z;
@@ -556,7 +556,7 @@ static BwdPlan bwd_plan(int B, int H, int N, int d, int G, int M, int dtype) {
     p.db = p.kept + (p.tc ? 0 : states * (p.chunk / BT));
     p.dc = p.db + heads;
     p.part = p.dc + heads;
-    p.log = p.part + units * p.chunks * 4;
+    p.log = p.part + units * p.chunks * (p.tc ? 16 : 4);
     p.total = p.log + (units * p.chunks + 3) / 4 * 4;
     return p;
 }
@@ -578,14 +578,14 @@ static ida_status launch_bwd_carry(const ScanBwdArgs &s, cudaStream_t st) {
 
 // The sums over a group's parts and over the chunks.
 template <typename E>
-static ida_status launch_bwd_sums(const ScanBwdArgs &s, int parts, cudaStream_t st) {
+static ida_status launch_bwd_sums(const ScanBwdArgs &s, int parts, int per, cudaStream_t st) {
     if (s.db_head) {
         const long long n = ((long long)s.B * s.N * s.G * s.M / 4 + 255) / 256;
         bwd_group_kernel<E><<<dim3((unsigned)n, 2), 256, 0, st>>>(s, parts);
         const ida_status r = launched("ssm group sums");
         if (r != IDA_OK) return r;
     }
-    bwd_params_kernel<<<s.H, 128, 0, st>>>(s);
+    bwd_params_kernel<<<s.H, 128, 0, st>>>(s, per);
     return launched("ssm parameter gradients");
 }
 
@@ -604,7 +604,7 @@ static ida_status launch_bwd(const ScanBwdArgs &s, cudaStream_t st) {
     if (r != IDA_OK) return r;
     bwd_main_kernel<E, MT><<<(unsigned)blocks, cols, smem, st>>>(s);
     r = launched("ssm scan backward");
-    return r == IDA_OK ? launch_bwd_sums<E>(s, s.H / s.G, st) : r;
+    return r == IDA_OK ? launch_bwd_sums<E>(s, s.H / s.G, 1, st) : r;
 }
 
 template <typename E>
@@ -678,7 +678,7 @@ ida_status ida_ssm_scan_backward(const void *x, const void *b, const void *c, co
     s = launch_bwd_tc_states(a, st);
     if (s == IDA_OK) s = launch_bwd_carry(a, st);
     if (s == IDA_OK) s = launch_bwd_tc(a, p.parts, st);
-    return s == IDA_OK ? launch_bwd_sums<__nv_bfloat16>(a, p.parts, st) : s;
+    return s == IDA_OK ? launch_bwd_sums<__nv_bfloat16>(a, p.parts, 4, st) : s;
 }
 
 }  // extern "C"

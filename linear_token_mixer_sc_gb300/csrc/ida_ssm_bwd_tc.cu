@@ -187,34 +187,36 @@ __global__ void __launch_bounds__(BTH, 1)
                 *reinterpret_cast<uint4 *>(sm + L::ST + k * L::PART + j / 64 * L::PSLAB + sw_off(m, j % 64 / 8)) = held[n][k];
         }
     };
-    // step sizes and decays of head g rep + r, by the first four warps, into the arrays of r's parity
+    // step sizes and decays of head g rep + r, by warps 4 .. 7 (warp 0 issues MMAs), into the arrays of r's
+    // parity
+    const int ta = tid - SQ;
     float dt_next = 0.f;
     const auto read_dt = [&](int r) {
-        if (tid < len && r < r1)
-            dt_next = __bfloat162float(static_cast<const __nv_bfloat16 *>(a.dt)[((size_t)b * N + t0 + tid) * a.lddt + g * rep + r]) + a.dt_bias[g * rep + r];
+        if (ta >= 0 && ta < len && r < r1)
+            dt_next = __bfloat162float(static_cast<const __nv_bfloat16 *>(a.dt)[((size_t)b * N + t0 + ta) * a.lddt + g * rep + r]) + a.dt_bias[g * rep + r];
     };
     const auto make_arrays = [&](int r) {
-        if (tid >= SQ || r >= r1) return;
+        if (ta < 0 || ta >= SQ || r >= r1) return;
         if (((r - r0) & 31) == 0) {  // the rates of the next 32 heads
-            if (warp == 0 && r + lane < r1) rates[((r - r0) & 63) + lane] = rate2_of(a.a_log[g * rep + r + lane]);
+            if (warp == 4 && r + lane < r1) rates[((r - r0) & 63) + lane] = rate2_of(a.a_log[g * rep + r + lane]);
             named_sync(1, 128);
         }
         float *Sh = arr + ((r - r0) & 1) * 6 * SQ, *Sl = Sh + SQ, *et = Sl + SQ, *fs = et + SQ, *dl = fs + SQ, *rt = dl + SQ;
-        const float delta = tid < len ? softplus(dt_next) : 0.f;
+        const float delta = ta < len ? softplus(dt_next) : 0.f;
         long long all;
-        const long long fx = chunk_sum(rates[(r - r0) & 63], delta, tid, tot, all);
+        const long long fx = chunk_sum(rates[(r - r0) & 63], delta, ta, tot, all);
         const float hi = (float)fx * kUnfix;
         // S at the end of the block of 16 before mine
         const int edge = (lane & 16) - 1;
         long long ref = __shfl_sync(0xffffffffu, fx, edge < 0 ? 0 : edge);
-        if (edge < 0) ref = tid < 32 ? 0 : tid < 64 ? tot[0] : tid < 96 ? tot[0] + tot[1] : tot[0] + tot[1] + tot[2];
-        Sh[tid] = hi;
-        Sl[tid] = (float)(fx - (long long)(hi * kFix)) * kUnfix;
-        et[tid] = ex2_fix(fx);
-        fs[tid] = ex2_fix(all - fx);
-        dl[tid] = delta;
-        rt[tid] = ex2_fix(fx - ref);
-        if (tid == 0) red[16 + 15 * ((r - r0) & 1)] = ex2_fix(all);
+        if (edge < 0) ref = ta < 32 ? 0 : ta < 64 ? tot[0] : ta < 96 ? tot[0] + tot[1] : tot[0] + tot[1] + tot[2];
+        Sh[ta] = hi;
+        Sl[ta] = (float)(fx - (long long)(hi * kFix)) * kUnfix;
+        et[ta] = ex2_fix(fx);
+        fs[ta] = ex2_fix(all - fx);
+        dl[ta] = delta;
+        rt[ta] = ex2_fix(fx - ref);
+        if (ta == 0) red[16 + 15 * ((r - r0) & 1)] = ex2_fix(all);
     };
     __syncthreads();
     if (tid == 0 && r0 < r1) {
@@ -572,14 +574,8 @@ const ssm_f2 ff = ssm_pack(f, f), dd = ssm_pack(delta, delta);
             ga = warp_sum(ga);
             gb = warp_sum(gb);
             gd = warp_sum(gd);
-            if (lane == 0) {
-                red[17 + 3 * wq] = ga;
-                red[18 + 3 * wq] = gb;
-                red[19 + 3 * wq] = gd;
-            }
-            named_sync(2, 128);
-            if (t < 3)
-                a.part[((size_t)unit * a.chunks + ch) * 4 + t] = red[17 + t] + red[20 + t] + red[23 + t] + red[26 + t];
+            if (lane == 0)
+                *reinterpret_cast<float4 *>(a.part + (((size_t)unit * a.chunks + ch) * 4 + wq) * 4) = make_float4(ga, gb, gd, 0.f);
         }
     }
     if (r < r1) {  // a wait ran out

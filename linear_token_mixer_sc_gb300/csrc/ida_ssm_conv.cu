@@ -10,49 +10,93 @@
 // Both are bound by HBM (about ten operations per element read).  A thread owns four
 // neighbouring channels and walks a strip of positions with the W - 1 rows before the current
 // one in registers, so each row is read once but for the W - 1 rows that two strips share.
-#include "ida_vec.cuh"
+#include <type_traits>
+
+#include "ida_ssm.cuh"
 
 namespace ida {
 
-template <typename E>
-struct Quad;  // 4 neighbouring elements
-template <>
-struct Quad<float> {
-    typedef float4 raw;
-    static __device__ __forceinline__ void unpack(const raw &u, float *x) { x[0] = u.x; x[1] = u.y; x[2] = u.z; x[3] = u.w; }
-    static __device__ __forceinline__ raw pack(const float *x) { return make_float4(x[0], x[1], x[2], x[3]); }
-};
-template <>
-struct Quad<__nv_bfloat16> {
-    typedef uint2 raw;
-    static __device__ __forceinline__ void unpack(const raw &u, float *x) {
-        x[0] = __uint_as_float(u.x << 16);
-        x[1] = __uint_as_float(u.x & 0xFFFF0000u);
-        x[2] = __uint_as_float(u.y << 16);
-        x[3] = __uint_as_float(u.y & 0xFFFF0000u);
+// 2 n neighbouring elements, as n pairs for the packed fp32x2 instructions (the kernels' time is the
+// instructions of an element as much as its bytes)
+template <typename E, int n>
+struct Pairs;
+template <int n>
+struct Pairs<float, n> {
+    typedef typename std::conditional<n == 2, float4, float2>::type raw;
+    static __device__ __forceinline__ void unpack(const raw &u, ssm_f2 (&x)[n]) {
+#pragma unroll
+        for (int i = 0; i < n; ++i) x[i] = ssm_pack((&u.x)[2 * i], (&u.x)[2 * i + 1]);
     }
-    static __device__ __forceinline__ raw pack(const float *x) {
-        const __nv_bfloat162 a = __floats2bfloat162_rn(x[0], x[1]), b = __floats2bfloat162_rn(x[2], x[3]);
-        return make_uint2(*reinterpret_cast<const uint32_t *>(&a), *reinterpret_cast<const uint32_t *>(&b));
+    static __device__ __forceinline__ raw pack(const ssm_f2 (&x)[n]) {
+        raw u;
+#pragma unroll
+        for (int i = 0; i < n; ++i) ssm_unpack(x[i], (&u.x)[2 * i], (&u.x)[2 * i + 1]);
+        return u;
+    }
+};
+template <int n>
+struct Pairs<__nv_bfloat16, n> {
+    typedef typename std::conditional<n == 2, uint2, uint32_t>::type raw;
+    static __device__ __forceinline__ void unpack(const raw &u, ssm_f2 (&x)[n]) {
+#pragma unroll
+        for (int i = 0; i < n; ++i) {
+            const uint32_t w = reinterpret_cast<const uint32_t *>(&u)[i];
+            x[i] = ssm_pack(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+        }
+    }
+    static __device__ __forceinline__ raw pack(const ssm_f2 (&x)[n]) {
+        raw u;
+#pragma unroll
+        for (int i = 0; i < n; ++i) {
+            float lo, hi;
+            ssm_unpack(x[i], lo, hi);
+            const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+            reinterpret_cast<uint32_t *>(&u)[i] = *reinterpret_cast<const uint32_t *>(&h);
+        }
+        return u;
     }
 };
 
-// the W taps of 4 neighbouring channels, tap by tap
-template <int W>
-__device__ __forceinline__ void load_taps(const float *w, float (&t)[W][4]) {
-    float v[4 * W];
+// the W taps of 2 n neighbouring channels, tap by tap
+template <int W, int n>
+__device__ __forceinline__ void load_taps(const float *w, ssm_f2 (&t)[W][n]) {
+    float v[2 * n * W];
 #pragma unroll
-    for (int i = 0; i < W; ++i) {
-        const float4 u = __ldg(reinterpret_cast<const float4 *>(w) + i);
-        v[4 * i] = u.x;
-        v[4 * i + 1] = u.y;
-        v[4 * i + 2] = u.z;
-        v[4 * i + 3] = u.w;
+    for (int i = 0; i < 2 * n * W; i += 2) {
+        const float2 u = __ldg(reinterpret_cast<const float2 *>(w + i));
+        v[i] = u.x;
+        v[i + 1] = u.y;
     }
 #pragma unroll
-    for (int e = 0; e < 4; ++e)
+    for (int i = 0; i < n; ++i)
 #pragma unroll
-        for (int j = 0; j < W; ++j) t[j][e] = v[e * W + j];
+        for (int j = 0; j < W; ++j) t[j][i] = ssm_pack(v[2 * i * W + j], v[(2 * i + 1) * W + j]);
+}
+
+// 1 / (1 + e^-p) by the hardware exponential and reciprocal (2^-21 off)
+__device__ __forceinline__ ssm_f2 fast_sigmoid(ssm_f2 p) {
+    float a, b;
+    ssm_unpack(ssm_mul(p, ssm_pack(-1.4426950408889634f, -1.4426950408889634f)), a, b);
+    asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(a));
+    asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(b));
+    a += 1.f;
+    b += 1.f;
+    asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(a));
+    asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(b));
+    return ssm_pack(a, b);
+}
+// bf16: that is far below the output's rounding
+template <typename E>
+__device__ __forceinline__ ssm_f2 conv_sigmoid(ssm_f2 p);
+template <>
+__device__ __forceinline__ ssm_f2 conv_sigmoid<__nv_bfloat16>(ssm_f2 p) {
+    return fast_sigmoid(p);
+}
+template <>
+__device__ __forceinline__ ssm_f2 conv_sigmoid<float>(ssm_f2 p) {
+    float a, b;
+    ssm_unpack(p, a, b);
+    return ssm_pack(1.f / (1.f + expf(-a)), 1.f / (1.f + expf(-b)));
 }
 
 struct ConvArgs {
@@ -65,26 +109,14 @@ struct ConvArgs {
     int strip, strips;  // positions per strip, strips per row
 };
 
-template <typename E>
-__device__ __forceinline__ float conv_sigmoid(float p);
-// bf16: the hardware exponential and reciprocal, 2^-21 off, are far below the output's rounding
-template <>
-__device__ __forceinline__ float conv_sigmoid<__nv_bfloat16>(float p) {
-    return __fdividef(1.f, 1.f + __expf(-p));
-}
-template <>
-__device__ __forceinline__ float conv_sigmoid<float>(float p) {
-    return 1.f / (1.f + expf(-p));
-}
-
 constexpr int CONV_THREADS = 256;
 constexpr int CONV_BATCH = 8;  // rows whose loads a thread issues together
 
-// Four channels a thread: eight would take 156 registers and leave 8 warps on an SM (94 us for
-// 16384 rows of 2176 channels in bf16).
+// Four channels a thread, two pairs.  (16384 rows of 2176 channels in bf16: eight channels in 156
+// registers, 8 warps an SM, 94 us; four channels in scalar fp32, 21 instructions an element, 41 us.)
 template <typename E, int W>
 __global__ void __launch_bounds__(CONV_THREADS, 3) conv_kernel(ConvArgs a) {
-    using Q = Quad<E>;
+    using Q = Pairs<E, 2>;
     typedef typename Q::raw raw;
     constexpr int H = W > 1 ? W - 1 : 1;
     const int vecs = a.C / 4;
@@ -92,50 +124,48 @@ __global__ void __launch_bounds__(CONV_THREADS, 3) conv_kernel(ConvArgs a) {
     if (item >= (long long)a.B * a.strips * vecs) return;
     const int v = (int)(item % vecs), strip = (int)(item / vecs % a.strips), b = (int)(item / vecs / a.strips);
     const int c0 = v * 4, t0 = strip * a.strip, t1 = min(a.N, t0 + a.strip);
-    const E *x = static_cast<const E *>(a.x) + (size_t)b * a.N * a.ldx + c0;
-    E *out = static_cast<E *>(a.out) + (size_t)b * a.N * a.C + c0;
-    float w[W][4], h[H][4];  // h: the rows before the current one, oldest first
+    const E *x = static_cast<const E *>(a.x) + ((size_t)b * a.N + t0) * a.ldx + c0;
+    E *out = static_cast<E *>(a.out) + ((size_t)b * a.N + t0) * a.C + c0;
+    ssm_f2 w[W][2], h[H][2], bias[2];  // h: the rows before the current one, oldest first
     load_taps<W>(a.w + (size_t)c0 * W, w);
-    const float4 bv = __ldg(reinterpret_cast<const float4 *>(a.bias + c0));
-    const float bias[4] = {bv.x, bv.y, bv.z, bv.w};
+    Pairs<float, 2>::unpack(__ldg(reinterpret_cast<const float4 *>(a.bias + c0)), bias);
 #pragma unroll
     for (int j = 0; j < W - 1; ++j) {
         const int t = t0 - (W - 1) + j;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) h[j][e] = 0.f;
+        h[j][0] = h[j][1] = 0ull;
         if (t >= 0)
-            Q::unpack(__ldg(reinterpret_cast<const raw *>(x + (size_t)t * a.ldx)), h[j]);
+            Q::unpack(__ldg(reinterpret_cast<const raw *>(x - (long long)(W - 1 - j) * a.ldx)), h[j]);
         else if (a.state_in)
-            Quad<float>::unpack(__ldg(reinterpret_cast<const float4 *>(
-                                    a.state_in + ((size_t)b * (W - 1) + (t + W - 1)) * a.C + c0)), h[j]);
+            Pairs<float, 2>::unpack(__ldg(reinterpret_cast<const float4 *>(
+                                        a.state_in + ((size_t)b * (W - 1) + (t + W - 1)) * a.C + c0)), h[j]);
     }
-    for (int tb = t0; tb < t1; tb += CONV_BATCH) {
+    for (int tb = t0; tb < t1; tb += CONV_BATCH, x += CONV_BATCH * a.ldx, out += CONV_BATCH * (long long)a.C) {
         raw u[CONV_BATCH];
 #pragma unroll
         for (int k = 0; k < CONV_BATCH; ++k)
-            if (tb + k < t1) u[k] = __ldg(reinterpret_cast<const raw *>(x + (size_t)(tb + k) * a.ldx));
+            if (tb + k < t1) u[k] = __ldg(reinterpret_cast<const raw *>(x + k * a.ldx));
 #pragma unroll
         for (int k = 0; k < CONV_BATCH; ++k) {
             if (tb + k >= t1) break;
-            float cur[4], o[4];
+            ssm_f2 cur[2], o[2];
             Q::unpack(u[k], cur);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                float p = fmaf(w[W - 1][e], cur[e], bias[e]);
+            for (int e = 0; e < 2; ++e) {
+                ssm_f2 p = ssm_fma(w[W - 1][e], cur[e], bias[e]);
 #pragma unroll
-                for (int j = 0; j < W - 1; ++j) p = fmaf(w[j][e], h[j][e], p);
-                o[e] = p * conv_sigmoid<E>(p);
+                for (int j = 0; j < W - 1; ++j) p = ssm_fma(w[j][e], h[j][e], p);
+                o[e] = ssm_mul(p, conv_sigmoid<E>(p));
 #pragma unroll
                 for (int j = 0; j + 1 < W - 1; ++j) h[j][e] = h[j + 1][e];
                 if (W > 1) h[H - 1][e] = cur[e];
             }
-            __stcs(reinterpret_cast<raw *>(out + (size_t)(tb + k) * a.C), Q::pack(o));
+            __stcs(reinterpret_cast<raw *>(out + k * (long long)a.C), Q::pack(o));
         }
     }
     if (a.final_state && t1 == a.N)
 #pragma unroll
         for (int j = 0; j < W - 1; ++j)
-            *reinterpret_cast<float4 *>(a.final_state + ((size_t)b * (W - 1) + j) * a.C + c0) = Quad<float>::pack(h[j]);
+            *reinterpret_cast<float4 *>(a.final_state + ((size_t)b * (W - 1) + j) * a.C + c0) = Pairs<float, 2>::pack(h[j]);
 }
 
 // ---- backward ------------------------------------------------------------------------------
@@ -152,80 +182,76 @@ struct ConvBwdArgs {
 
 constexpr int CB_STRIPS = 8;  // strips (rows of threads) of a block at a time
 constexpr int CB_BATCH = 4;   // rows whose loads a thread issues together
+constexpr int CN = 4;         // channels of a thread, two pairs
 
-// Block (32 channel quads) x (8 strips), walking the strips of all rows gridDim.x blocks apart with
-// its sums in registers.  A thread walks u = t0 .. t1 + W - 2: it forms g_u from the x window, then
-// dx of position u - (W - 1) from the last W values of g, so the W - 1 positions behind a strip are
-// evaluated twice (their x and dout come from L2).
+// Block (32 x 4 channels) x (8 strips), walking the strips of all rows gridDim.x blocks apart with its
+// sums in registers.  A thread walks u = t0 .. t1 + W - 2: it forms g_u from the x window, then dx of
+// position u - (W - 1) from the last W values of g, so the W - 1 positions behind a strip are evaluated
+// twice (their x and dout come from L2).
 template <typename E, int W>
 __global__ void __launch_bounds__(32 * CB_STRIPS, 2) conv_bwd_kernel(ConvBwdArgs a) {
-    using Q = Quad<E>;
+    using Q = Pairs<E, 2>;
     typedef typename Q::raw raw;
     constexpr int H = W > 1 ? W - 1 : 1;
-    __shared__ float red[CB_STRIPS][W + 1][32 * 4];
-    const int c0 = (blockIdx.y * 32 + threadIdx.x) * 4;
-    float dw[W][4], db[4];
+    __shared__ float red[CB_STRIPS][W + 1][32 * CN];
+    dependent_launch();
+    const int c0 = (blockIdx.y * 32 + threadIdx.x) * CN;
+    ssm_f2 dw[W][2], db[2] = {0ull, 0ull};
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-        db[e] = 0.f;
-#pragma unroll
-        for (int j = 0; j < W; ++j) dw[j][e] = 0.f;
-    }
+    for (int j = 0; j < W; ++j) dw[j][0] = dw[j][1] = 0ull;
     if (c0 < a.C) {
-        float w[W][4];
+        ssm_f2 w[W][2], bias[2];
         load_taps<W>(a.w + (size_t)c0 * W, w);
-        const float4 bv = __ldg(reinterpret_cast<const float4 *>(a.bias + c0));
-        const float bias[4] = {bv.x, bv.y, bv.z, bv.w};
+        Pairs<float, 2>::unpack(__ldg(reinterpret_cast<const float4 *>(a.bias + c0)), bias);
+        const ssm_f2 one = ssm_pack(1.f, 1.f), minus = ssm_pack(-1.f, -1.f);
         for (long long s = (long long)blockIdx.x * CB_STRIPS + threadIdx.y; s < (long long)a.B * a.strips;
              s += (long long)gridDim.x * CB_STRIPS) {
             const int b = (int)(s / a.strips), t0 = (int)(s % a.strips) * a.strip, t1 = min(a.N, t0 + a.strip);
-            const E *x = static_cast<const E *>(a.x) + (size_t)b * a.N * a.ldx + c0;
-            const E *dout = static_cast<const E *>(a.dout) + (size_t)b * a.N * a.C + c0;
-            E *dx = static_cast<E *>(a.dx) + (size_t)b * a.N * a.lddx + c0;
-            float h[H][4], g[H][4];  // the x rows and the g before u
+            const size_t row = (size_t)b * a.N + t0;
+            const E *x = static_cast<const E *>(a.x) + row * a.ldx + c0;
+            const E *dout = static_cast<const E *>(a.dout) + row * a.C + c0;
+            E *dx = static_cast<E *>(a.dx) + row * a.lddx + c0;
+            ssm_f2 h[H][2], g[H][2];  // the x rows and the g before u
 #pragma unroll
             for (int j = 0; j < W - 1; ++j) {
-                const int t = t0 - (W - 1) + j;
-#pragma unroll
-                for (int e = 0; e < 4; ++e) h[j][e] = g[j][e] = 0.f;
-                if (t >= 0) Q::unpack(*reinterpret_cast<const raw *>(x + (size_t)t * a.ldx), h[j]);
+                h[j][0] = h[j][1] = g[j][0] = g[j][1] = 0ull;
+                if (t0 - (W - 1) + j >= 0) Q::unpack(*reinterpret_cast<const raw *>(x - (long long)(W - 1 - j) * a.ldx), h[j]);
             }
-            const int u1 = t1 + W - 1;  // g beyond position N - 1 is zero
-            for (int ub = t0; ub < u1; ub += CB_BATCH) {
+            const int n = t1 - t0, left = a.N - t0;  // positions of the strip, and of the row from it on
+            for (int ub = 0; ub < n + W - 1; ub += CB_BATCH) {  // g beyond the row's end is zero
                 raw rx[CB_BATCH], rd[CB_BATCH];
 #pragma unroll
-                for (int k = 0; k < CB_BATCH; ++k)
-                    if (ub + k < u1 && ub + k < a.N) {
-                        rx[k] = *reinterpret_cast<const raw *>(x + (size_t)(ub + k) * a.ldx);
-                        rd[k] = *reinterpret_cast<const raw *>(dout + (size_t)(ub + k) * a.C);
+                for (int k = 0; k < CB_BATCH; ++k) {
+                    rx[k] = rd[k] = raw();
+                    if (ub + k < n + W - 1 && ub + k < left) {
+                        rx[k] = *reinterpret_cast<const raw *>(x + (ub + k) * a.ldx);
+                        rd[k] = *reinterpret_cast<const raw *>(dout + (ub + k) * (long long)a.C);
                     }
+                }
 #pragma unroll
                 for (int k = 0; k < CB_BATCH; ++k) {
                     const int u = ub + k;
-                    if (u >= u1) break;
-                    float cur[4] = {0.f, 0.f, 0.f, 0.f}, d[4] = {0.f, 0.f, 0.f, 0.f}, o[4];
-                    if (u < a.N) {
-                        Q::unpack(rx[k], cur);
-                        Q::unpack(rd[k], d);
-                    }
-                    const int t = u - (W - 1);
-                    const bool inside = u < t1;  // positions behind the strip are another's to sum
+                    if (u >= n + W - 1) break;
+                    ssm_f2 cur[2], d[2], o[2];
+                    Q::unpack(rx[k], cur);
+                    Q::unpack(rd[k], d);
+                    const bool inside = u < n;  // positions behind the strip are another's to sum
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        float p = fmaf(w[W - 1][e], cur[e], bias[e]);
+                    for (int e = 0; e < 2; ++e) {
+                        ssm_f2 p = ssm_fma(w[W - 1][e], cur[e], bias[e]);
 #pragma unroll
-                        for (int j = 0; j < W - 1; ++j) p = fmaf(w[j][e], h[j][e], p);
-                        // the hardware exponential and reciprocal: 2^-21 of a term, for both types
-                        const float sg = __fdividef(1.f, 1.f + __expf(-p));
-                        const float gu = d[e] * sg * fmaf(p, 1.f - sg, 1.f), gs = inside ? gu : 0.f;
-                        db[e] += gs;
-                        dw[W - 1][e] = fmaf(gs, cur[e], dw[W - 1][e]);
+                        for (int j = 0; j < W - 1; ++j) p = ssm_fma(w[j][e], h[j][e], p);
+                        const ssm_f2 sg = fast_sigmoid(p);  // for both types
+                        const ssm_f2 gu = ssm_mul(ssm_mul(d[e], sg), ssm_fma(p, ssm_fma(sg, minus, one), one));
+                        const ssm_f2 gs = inside ? gu : 0ull;
+                        db[e] = ssm_fma(gs, one, db[e]);
+                        dw[W - 1][e] = ssm_fma(gs, cur[e], dw[W - 1][e]);
 #pragma unroll
-                        for (int j = 0; j < W - 1; ++j) dw[j][e] = fmaf(gs, h[j][e], dw[j][e]);
+                        for (int j = 0; j < W - 1; ++j) dw[j][e] = ssm_fma(gs, h[j][e], dw[j][e]);
                         // g of positions t .. t + W - 1 = u is g[0 ..], gu; w[j] meets g_{t+W-1-j}
-                        o[e] = w[0][e] * gu;
+                        o[e] = ssm_mul(w[0][e], gu);
 #pragma unroll
-                        for (int j = 1; j < W; ++j) o[e] = fmaf(w[j][e], g[W - 1 - j][e], o[e]);
+                        for (int j = 1; j < W; ++j) o[e] = ssm_fma(w[j][e], g[W - 1 - j][e], o[e]);
 #pragma unroll
                         for (int j = 0; j + 1 < W - 1; ++j) {
                             g[j][e] = g[j + 1][e];
@@ -236,20 +262,25 @@ __global__ void __launch_bounds__(32 * CB_STRIPS, 2) conv_bwd_kernel(ConvBwdArgs
                             h[H - 1][e] = cur[e];
                         }
                     }
-                    if (t >= t0) *reinterpret_cast<raw *>(dx + (size_t)t * a.lddx) = Q::pack(o);
+                    if (u >= W - 1) *reinterpret_cast<raw *>(dx + (u - (W - 1)) * a.lddx) = Q::pack(o);
                 }
             }
         }
     }
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
+    for (int e = 0; e < 2; ++e) {
+        float2 v;
 #pragma unroll
-        for (int j = 0; j < W; ++j) red[threadIdx.y][j][threadIdx.x * 4 + e] = dw[j][e];
-        red[threadIdx.y][W][threadIdx.x * 4 + e] = db[e];
+        for (int j = 0; j < W; ++j) {
+            ssm_unpack(dw[j][e], v.x, v.y);
+            *reinterpret_cast<float2 *>(&red[threadIdx.y][j][threadIdx.x * CN + 2 * e]) = v;
+        }
+        ssm_unpack(db[e], v.x, v.y);
+        *reinterpret_cast<float2 *>(&red[threadIdx.y][W][threadIdx.x * CN + 2 * e]) = v;
     }
     __syncthreads();
-    for (int i = threadIdx.y * 32 + threadIdx.x; i < (W + 1) * 32 * 4; i += 32 * CB_STRIPS) {
-        const int j = i / (32 * 4), k = i % (32 * 4), c = blockIdx.y * 32 * 4 + k;
+    for (int i = threadIdx.y * 32 + threadIdx.x; i < (W + 1) * 32 * CN; i += 32 * CB_STRIPS) {
+        const int j = i / (32 * CN), k = i % (32 * CN), c = blockIdx.y * 32 * CN + k;
         if (c >= a.C) continue;
         float v = 0.f;
 #pragma unroll
@@ -262,6 +293,7 @@ __global__ void __launch_bounds__(32 * CB_STRIPS, 2) conv_bwd_kernel(ConvBwdArgs
 __global__ void __launch_bounds__(256) conv_bwd_sum_kernel(const float *part, float *dw, float *dbias, int blocks,
                                                            int C, int W) {
     __shared__ float s[8][33];
+    dependent_wait();
     const int i = blockIdx.x * 32 + threadIdx.x, total = C * (W + 1);
     float v = 0.f;
     if (i < total)
@@ -283,7 +315,7 @@ __global__ void __launch_bounds__(256) conv_bwd_sum_kernel(const float *part, fl
 // sums in registers over all their strips; of the strip lengths 8 .. 64 the one whose longest block
 // walks the fewest positions (W - 1 of each strip are walked twice).
 static int conv_bwd_strip(int B, int N, int C, long long *blocks) {
-    const long long cols = (C / 4 + 31) / 32, most = 304 / cols > 0 ? 304 / cols : 1;
+    const long long cols = (C / CN + 31) / 32, most = 304 / cols > 0 ? 304 / cols : 1;
     int best = 0;
     long long cost = 0;
     for (int strip = 64; strip >= 8; strip /= 2) {
@@ -346,10 +378,17 @@ ida_status ida_ssm_conv(const void *x, const float *conv_w, const float *conv_b,
     }
     ConvArgs a = {x, conv_w, conv_b, state_in, out, final_state, B, N, C, ldx, 0, 0};
     const int vecs = C / 4;
-    // strips of 32 positions read 3 / 32 of the rows twice (from L2); shorter ones, down to a
-    // batch of loads, where 32 would leave SMs with less than 2048 threads
-    a.strip = 32;
-    while (a.strip > CONV_BATCH && (long long)B * ((N + a.strip - 1) / a.strip) * vecs < 2048LL * num_sms) a.strip /= 2;
+    // W - 1 rows of a strip are read twice (from L2), and the last of the passes of three blocks an SM may
+    // be short: of the strip lengths 8 .. 64 the one that makes a thread's passes read the fewest rows
+    long long cost = 0;
+    for (int strip = 64; strip >= CONV_BATCH; strip -= CONV_BATCH) {
+        const long long n = ((long long)B * ((N + strip - 1) / strip) * vecs + CONV_THREADS - 1) / CONV_THREADS;
+        const long long c = (n + 3 * num_sms - 1) / (3 * num_sms) * (strip + W - 1);
+        if (!cost || c < cost) {
+            a.strip = strip;
+            cost = c;
+        }
+    }
     a.strips = (N + a.strip - 1) / a.strip;
     const long long blocks = ((long long)B * a.strips * vecs + CONV_THREADS - 1) / CONV_THREADS;
     if (blocks > 0x7FFFFFFFLL) return fail_with(IDA_ERR_UNSUPPORTED, "too many elements");
@@ -409,7 +448,7 @@ ida_status ida_ssm_conv_backward(const void *x, const void *dout, const float *c
     long long blocks;
     a.strip = conv_bwd_strip(B, N, C, &blocks);
     a.strips = (N + a.strip - 1) / a.strip;
-    const dim3 grid((unsigned)blocks, (unsigned)((C / 4 + 31) / 32)), block(32, CB_STRIPS);
+    const dim3 grid((unsigned)blocks, (unsigned)((C / CN + 31) / 32)), block(32, CB_STRIPS);
 #define IDA_CONV(E)                                                   \
     switch (W) {                                                      \
         case 1: conv_bwd_kernel<E, 1><<<grid, block, 0, st>>>(a); break;  \
@@ -425,8 +464,9 @@ ida_status ida_ssm_conv_backward(const void *x, const void *dout, const float *c
 #undef IDA_CONV
     s = launched("ssm conv backward");
     if (s != IDA_OK) return s;
-    conv_bwd_sum_kernel<<<(unsigned)((C * (W + 1) + 31) / 32), dim3(32, 8), 0, st>>>(a.part, dconv_w, dconv_b,
-                                                                                    (int)blocks, C, W);
+    const cudaError_t e = launch_dependent(conv_bwd_sum_kernel, dim3((unsigned)((C * (W + 1) + 31) / 32)), dim3(32, 8), 0, st,
+                                           a.part, dconv_w, dconv_b, (int)blocks, C, W);
+    if (e != cudaSuccess) return fail_with(IDA_ERR_CUDA, std::string("ssm conv parameter gradients launch: ") + cudaGetErrorString(e));
     return launched("ssm conv parameter gradients");
 }
 

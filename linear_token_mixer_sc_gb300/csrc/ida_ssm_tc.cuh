@@ -108,23 +108,4 @@ ida_status launch_ssm_states(const ScanArgs &a, bool exact, cudaStream_t st);
 // of the adjoint it passes on; a.x, a.b and their strides then are dy's and c's.
 ida_status launch_ssm_chunk_states(const ScanArgs &a, bool rev, cudaStream_t st);
 
-// A launch that may start while the one before it in the stream ends; its kernel waits (dependent_wait)
-// before it touches memory.
-template <typename... K, typename... A>
-cudaError_t launch_dependent(void (*kernel)(K...), dim3 grid, dim3 block, size_t smem, cudaStream_t st, A... args) {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = grid;
-    cfg.blockDim = block;
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = st;
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = at;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kernel, K(args)...);
-}
-__device__ __forceinline__ void dependent_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-__device__ __forceinline__ void dependent_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
-
 }  // namespace ida

@@ -58,6 +58,11 @@ __device__ __forceinline__ void from_float(__nv_bfloat16 *p, float x) { *p = __f
 // log(1 + e^z) without overflow; its derivative is 1 / (1 + e^-z).
 __device__ __forceinline__ float softplus(float z) { return fmaxf(z, 0.f) + log1pf(expf(-fabsf(z))); }
 
+// Programmatic dependent launches (launch_dependent): wait for the launch before in the stream, and let
+// the one behind take its place on the SMs.
+__device__ __forceinline__ void dependent_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void dependent_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
 // ---- host side ---------------------------------------------------------------------------
 
 ida_status fail_with(ida_status s, const std::string &why);
@@ -88,6 +93,22 @@ inline ida_status check_ssm(int H, int d, int G, int M, int dtype) {
     return IDA_OK;
 }
 
+// A launch that may start while the one before it in the stream ends; its kernel waits (dependent_wait)
+// before it touches memory.
+template <typename... K, typename... A>
+cudaError_t launch_dependent(void (*kernel)(K...), dim3 grid, dim3 block, size_t smem, cudaStream_t st, A... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = block;
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, K(args)...);
+}
 inline ida_status launched(const char *what) {
     cudaError_t e = cudaGetLastError();
     return e == cudaSuccess ? IDA_OK : fail_with(IDA_ERR_CUDA, std::string(what) + " launch: " + cudaGetErrorString(e));

@@ -129,8 +129,8 @@ def test_norm_backward(case):
     if dres is not None:
         rx, size = rx + dres.double(), size + dres.double().abs()
     assert worst(g["x"], rx, HALF[dtype] * rx.abs() + 2 * 64 * U32 * size) <= 1
-    # rows add up within a block (rows / 608 of them), then over at most 608 blocks in 8 parts
-    n = 64 + rows // 608 + 608 // 8 + 8
+    # rows add up within a block (rows / 1216 of them), then over at most 1216 blocks in 32 parts
+    n = 64 + rows // 1216 + 1216 // 32 + 8
     assert worst(g["w"], rw, n * U32 * (dy64 * r64 * inv).abs().sum(0)) <= 1
 
 
