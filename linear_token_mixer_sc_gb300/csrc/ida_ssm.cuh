@@ -63,12 +63,6 @@ __device__ __forceinline__ ssm_f2 ssm_mul(ssm_f2 a, ssm_f2 b) {
     return d;
 }
 
-__device__ __forceinline__ void cp_async16(void *smem, const void *gmem, bool ok) {
-    const uint32_t s = static_cast<uint32_t>(__cvta_generic_to_shared(smem));
-    const int n = ok ? 16 : 0;  // 0: the 16 bytes are zero-filled and nothing is read
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(s), "l"(gmem), "r"(n) : "memory");
-}
-__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-__device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_group 0;" ::: "memory"); }
+__device__ __forceinline__ void named_sync(int id, int n) { asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(n) : "memory"); }
 
 }  // namespace ida

@@ -6,8 +6,10 @@
 // so that b and c come from shared memory as 16-byte broadcasts and only y is summed across
 // lanes (three shuffles a position, after which lane l holds column l).  Per position that is
 // three packed operations for two state elements; the fp32 rate of the CUDA cores bounds it.
-// Positions go in tiles of SEQ_T: the next tile's raw rows are copied asynchronously while the
-// present one's, converted to fp32 (b times its step size), are walked.
+// Positions go in tiles of SEQ_T, in two buffers: four helper warps read the next tile's rows, form
+// its step sizes and lay it out (b times its step size) while the others walk the present one.
+// (Converted by the walking warps themselves, 251 positions of 2 heads of 32 x 16 took 54 us, most
+// of it the conversion.)
 //
 // Few (row, head) units do not fill the SMs.  With a workspace a sequence is cut into segments:
 // a first launch leaves each segment's last state from zero, and the second starts every segment
@@ -22,65 +24,107 @@ void ssm_chunk_segments(int B, int H, int N, int d, int M, int num_sms, int &seg
 
 constexpr int SEQ_T = 16;  // positions per tile
 
-// Shared memory of a CTA of `cols` columns.
-template <typename E, int MT>
-struct SeqSmem {
-    static constexpr int QS = MT + 4;      // floats of a quarter row: the four quarters on their own banks
-    static constexpr int MS = 4 * QS;      // floats of a row of b or c
-    __host__ __device__ static size_t raw_bytes(int cols) { return (size_t)SEQ_T * (8 * MT + cols) * sizeof(E); }
-    __host__ __device__ static size_t bytes(int cols) {
-        return raw_bytes(cols) + (size_t)SEQ_T * (2 * MS + cols) * sizeof(float) + 4 * SEQ_T * sizeof(float);
-    }
+constexpr int SEQ_HELP = 128;  // helper threads
+
+// Floats of a tile of `cols` columns: rows of b and c (four quarters on their own banks), of x, decays.
+template <int MT>
+struct SeqTile {
+    static constexpr int QS = MT + 4, MS = 4 * QS;
+    __host__ __device__ static int floats(int cols) { return SEQ_T * (2 * MS + cols + 1); }
 };
 
 // MT: state rows per lane (M <= 4 MT).  STATE: only the segment's last state from zero.
-template <typename E, int MT, bool STATE>
-__global__ void __launch_bounds__(128) scan_seq_kernel(ScanArgs a) {
-    using V = Vec16<E>;
-    using S = SeqSmem<E, MT>;
-    extern __shared__ __align__(16) unsigned char smem[];
+template <int MT, bool STATE>
+__global__ void __launch_bounds__(128 + SEQ_HELP) scan_seq_kernel(ScanArgs a) {
+    using L = SeqTile<MT>;
+    extern __shared__ __align__(16) float sm[];
     const int M = a.M, d = a.d, H = a.H, N = a.N, rep = H / a.G;
-    const int nt = blockDim.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, cols = nt;
+    const int cols = blockDim.x - SEQ_HELP, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int slices = (d + cols - 1) / cols, nseg = STATE ? a.state_segs : a.segs;
     int id = blockIdx.x;
     const int seg = id % nseg;
     id /= nseg;
     const int j0 = id % slices * cols;
     const int unit = id / slices, b = unit / H, h = unit % H, g = h / rep;
-    E *raw = reinterpret_cast<E *>(smem);  // [T][b 4 MT | c 4 MT | x cols]
-    float *fb = reinterpret_cast<float *>(smem + S::raw_bytes(cols)), *fc = fb + SEQ_T * S::MS;
-    float *fx = fc + SEQ_T * S::MS, *fad = fx + SEQ_T * cols;  // fad: decays and step sizes, two tiles' in turn
-    constexpr int RS = 8 * MT;  // raw row: b, c, then x
-    const int rs = RS + cols;
     const int t_begin = seg * a.seg, t_end = min(N, t_begin + a.seg);
-    const E *gb = static_cast<const E *>(a.b) + (size_t)b * N * a.ldb + g * M;
-    const E *gc = static_cast<const E *>(a.c) + (size_t)b * N * a.ldc + g * M;
-    const E *gx = static_cast<const E *>(a.x) + (size_t)b * N * a.ldx + (size_t)h * d + j0;
-    const E *gdt = static_cast<const E *>(a.dt) + (size_t)b * N * a.lddt + h;
-    const float rate = expf(a.a_log[h]), dt_bias = a.dt_bias[h], skip = STATE ? 0.f : a.D[h];
+    const int tile = L::floats(cols);  // [T][MS] b, [T][MS] c, [T][cols] x, [T] decays
 
-    const auto fetch = [&](int t0) {
-        const int vpr = rs / V::n;
-        for (int i = tid; i < SEQ_T * vpr; i += nt) {
-            const int t = i / vpr, e = i % vpr * V::n, p = t0 + t;
-            const E *src = gx;
-            bool ok = p < t_end;
-            if (e < 4 * MT) {
-                ok = ok && e < M;
-                src = gb + (size_t)p * a.ldb + e;
-            } else if (e < RS) {
-                ok = ok && !STATE && e - 4 * MT < M;
-                src = gc + (size_t)p * a.ldc + (e - 4 * MT);
+    if (tid >= cols) {
+        // helpers: a thread keeps its 16-byte column of [b | c | x] and walks the tile's rows
+        const int ht = tid - cols, nb = M / 4, nx = min(cols, d - j0) / 4, vpr = (STATE ? nb : 2 * nb) + nx;
+        const float *dt = static_cast<const float *>(a.dt) + (size_t)b * N * a.lddt + h;
+        const float rate = expf(a.a_log[h]), dt_bias = a.dt_bias[h];
+        const float *src = nullptr;
+        long long ld = 0;
+        int at = 0, rs = 0;  // the column's place in a tile, and its row stride there
+        bool is_b = false;
+        const int step = vpr < SEQ_HELP ? SEQ_HELP / vpr : 1;  // rows the helpers take at a time
+        double log_sum = 0.0;
+        const auto column = [&](int v) {
+            if (v < nb) {
+                is_b = true;
+                src = static_cast<const float *>(a.b) + (size_t)b * N * a.ldb + g * M + 4 * v;
+                ld = a.ldb;
+                at = 4 * v / MT * L::QS + 4 * v % MT;
+                rs = L::MS;
+            } else if (!STATE && v < 2 * nb) {
+                is_b = false;
+                v -= nb;
+                src = static_cast<const float *>(a.c) + (size_t)b * N * a.ldc + g * M + 4 * v;
+                ld = a.ldc;
+                at = SEQ_T * L::MS + 4 * v / MT * L::QS + 4 * v % MT;
+                rs = L::MS;
             } else {
-                ok = ok && j0 + e - RS < d;
-                src = gx + (size_t)p * a.ldx + (e - RS);
+                is_b = false;
+                v -= STATE ? nb : 2 * nb;
+                src = static_cast<const float *>(a.x) + (size_t)b * N * a.ldx + (size_t)h * d + j0 + 4 * v;
+                ld = a.ldx;
+                at = 2 * SEQ_T * L::MS + 4 * v;
+                rs = cols;
             }
-            cp_async16(raw + t * rs + e, ok ? src : gx, ok);
+        };
+        const auto fill = [&](int t0, float *buf) {
+            for (int v = ht % (vpr < SEQ_HELP ? vpr : SEQ_HELP); v < vpr; v += SEQ_HELP) {
+                const int r0 = vpr < SEQ_HELP ? ht / vpr : 0;
+                if (r0 >= step) break;  // spare helpers
+                column(v);
+#pragma unroll 4
+                for (int t = r0; t < SEQ_T; t += step) {
+                    const int p = t0 + t;
+                    float4 u = make_float4(0.f, 0.f, 0.f, 0.f);
+                    if (p < t_end) {
+                        u = __ldg(reinterpret_cast<const float4 *>(src + (size_t)p * ld));
+                        if (is_b) {
+                            const float f = softplus(__ldg(dt + (size_t)p * a.lddt) + dt_bias);
+                            u = make_float4(f * u.x, f * u.y, f * u.z, f * u.w);
+                        }
+                    }
+                    *reinterpret_cast<float4 *>(buf + at + t * rs) = u;
+                }
+            }
+            if (ht < 32) {
+                float la = 0.f;
+                if (ht < SEQ_T && t0 + ht < t_end) la = -rate * softplus(dt[(size_t)(t0 + ht) * a.lddt] + dt_bias);
+                if (ht < SEQ_T) buf[SEQ_T * (2 * L::MS + cols) + ht] = expf(la);  // behind the end nothing decays or is added
+                if (STATE) log_sum += warp_sum(la);
+            }
+        };
+        // columns that no vector fills: rows of b and c behind M, columns of x behind d
+        for (int i = ht; i < 2 * tile; i += SEQ_HELP) sm[i] = 0.f;
+        named_sync(1, SEQ_HELP);
+        fill(t_begin, sm);
+        __syncthreads();
+        int k = 1;
+        for (int t0 = t_begin; t0 < t_end; t0 += SEQ_T, ++k) {
+            if (t0 + SEQ_T < t_end) fill(t0 + SEQ_T, sm + (k & 1) * tile);
+            __syncthreads();
         }
-        cp_async_commit();
-    };
+        if (STATE && ht == 0 && j0 == 0) a.seg_log[(size_t)unit * a.segs + seg] = (float)log_sum;
+        return;
+    }
 
     const int km = lane & 3, jl = warp * 32 + (lane >> 2) * 4;  // my quarter of rows, my first column
+    const float skip = STATE ? 0.f : a.D[h];
     ssm_f2 X[MT / 2][4];
 #pragma unroll
     for (int i = 0; i < MT / 2; ++i)
@@ -109,63 +153,28 @@ __global__ void __launch_bounds__(128) scan_seq_kernel(ScanArgs a) {
             }
         }
     }
-    double log_sum = 0.0;  // thread 0
-
-    fetch(t_begin);
-    for (int t0 = t_begin; t0 < t_end; t0 += SEQ_T) {
-        float *fa = fad + (((t0 - t_begin) / SEQ_T) & 1) * 2 * SEQ_T, *fd = fa + SEQ_T;
-        if (warp == 0) {
-            float la = 0.f;
-            if (lane < SEQ_T) {
-                const int p = t0 + lane;
-                float delta = 0.f;  // behind the end nothing decays or is added
-                if (p < t_end) delta = softplus(to_float(gdt[(size_t)p * a.lddt]) + dt_bias);
-                la = -rate * delta;
-                fd[lane] = delta;
-                fa[lane] = expf(la);
-            }
-            if (STATE) {
-                la = warp_sum(la);
-                log_sum += la;
-            }
-        }
-        cp_async_wait_all();
-        __syncthreads();  // raw rows and step sizes are there, and the walk of the last tile is done
-        for (int i = tid; i < SEQ_T * (rs / V::n); i += nt) {
-            const int t = i / (rs / V::n), e = i % (rs / V::n) * V::n;
-            float v[V::n];
-            V::unpack(*reinterpret_cast<const uint4 *>(raw + t * rs + e), v);
-            float *dst;
-            if (e < RS) {
-                const int m = e < 4 * MT ? e : e - 4 * MT;
-                dst = (e < 4 * MT ? fb : fc) + t * S::MS;
-                const float f = e < 4 * MT ? fd[t] : 1.f;
-#pragma unroll
-                for (int k = 0; k < V::n; ++k) {
-                    const int mk = m + k;
-                    dst[mk / MT * S::QS + mk % MT] = v[k] * f;
-                }
-            } else {
-                dst = fx + t * cols + (e - RS);
-#pragma unroll
-                for (int k = 0; k < V::n; ++k) dst[k] = v[k];
-            }
-        }
-        __syncthreads();
-        if (t0 + SEQ_T < t_end) fetch(t0 + SEQ_T);
-        const int len = min(SEQ_T, t_end - t0);
-        for (int t = 0; t < len; ++t) {
+    const int col = warp * 32 + lane;  // the column whose y I hold after the sum over quarters
+    float *y = static_cast<float *>(a.y) + (((size_t)b * N + t_begin) * H + h) * d + j0 + col;
+    const size_t ys = (size_t)H * d;
+    const bool has = j0 + col < d;
+    __syncthreads();
+    int k = 0;
+    for (int t0 = t_begin; t0 < t_end; t0 += SEQ_T, ++k, y += SEQ_T * ys) {
+        const float *fb = sm + (k & 1) * tile + km * L::QS, *fc = fb + SEQ_T * L::MS;
+        const float *fx = sm + (k & 1) * tile + 2 * SEQ_T * L::MS, *fa = fx + SEQ_T * cols;
+        const int left = t_end - t0;
+#pragma unroll(MT <= 8 ? 4 : 1)
+        for (int t = 0; t < SEQ_T; ++t) {  // positions behind the end change nothing
             const float4 x4 = *reinterpret_cast<const float4 *>(fx + t * cols + jl);
             const float av = fa[t];
             const ssm_f2 aa = ssm_pack(av, av);
             const ssm_f2 xx[4] = {ssm_pack(x4.x, x4.x), ssm_pack(x4.y, x4.y), ssm_pack(x4.z, x4.z), ssm_pack(x4.w, x4.w)};
-            const float *pb = fb + t * S::MS + km * S::QS, *pc = fc + t * S::MS + km * S::QS;
             ssm_f2 acc[4] = {0ull, 0ull, 0ull, 0ull};
 #pragma unroll
             for (int i = 0; i < MT / 2; i += 2) {
-                const ulonglong2 b2 = *reinterpret_cast<const ulonglong2 *>(pb + 2 * i);
+                const ulonglong2 b2 = *reinterpret_cast<const ulonglong2 *>(fb + t * L::MS + 2 * i);
                 ulonglong2 c2;
-                if (!STATE) c2 = *reinterpret_cast<const ulonglong2 *>(pc + 2 * i);
+                if (!STATE) c2 = *reinterpret_cast<const ulonglong2 *>(fc + t * L::MS + 2 * i);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     X[i][j] = ssm_fma(b2.x, xx[j], ssm_mul(aa, X[i][j]));
@@ -177,24 +186,22 @@ __global__ void __launch_bounds__(128) scan_seq_kernel(ScanArgs a) {
                 }
             }
             if (!STATE) {
-                float y[4];
+                float o[4];
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     float lo, hi;
                     ssm_unpack(acc[j], lo, hi);
-                    y[j] = lo + hi;
+                    o[j] = lo + hi;
                 }
                 // sum over the four quarters: lane l ends with column l of the warp
                 const bool up = (lane & 2) != 0, odd = (lane & 1) != 0;
-                const float k0 = (up ? y[2] : y[0]) + __shfl_xor_sync(0xffffffffu, up ? y[0] : y[2], 2);
-                const float k1 = (up ? y[3] : y[1]) + __shfl_xor_sync(0xffffffffu, up ? y[1] : y[3], 2);
-                const float o = (odd ? k1 : k0) + __shfl_xor_sync(0xffffffffu, odd ? k0 : k1, 1);
-                const int col = warp * 32 + lane;
-                if (j0 + col < d)
-                    from_float(static_cast<E *>(a.y) + (((size_t)b * N + t0 + t) * H + h) * d + j0 + col,
-                               fmaf(skip, fx[t * cols + col], o));
+                const float k0 = (up ? o[2] : o[0]) + __shfl_xor_sync(0xffffffffu, up ? o[0] : o[2], 2);
+                const float k1 = (up ? o[3] : o[1]) + __shfl_xor_sync(0xffffffffu, up ? o[1] : o[3], 2);
+                const float v = (odd ? k1 : k0) + __shfl_xor_sync(0xffffffffu, odd ? k0 : k1, 1);
+                if (has && t < left) y[t * ys] = fmaf(skip, fx[t * cols + col], v);
             }
         }
+        __syncthreads();
     }
     float *out = STATE ? a.seg_state + ((size_t)unit * a.segs + seg) * M * d
                        : (a.final_state && seg == a.segs - 1 ? a.final_state + (size_t)unit * M * d : nullptr);
@@ -210,7 +217,6 @@ __global__ void __launch_bounds__(128) scan_seq_kernel(ScanArgs a) {
                 *reinterpret_cast<float4 *>(out + (size_t)(m + 1) * d + j0 + jl) = make_float4(v[0], v[1], v[2], v[3]);
             }
         }
-    if (STATE && tid == 0 && j0 == 0) a.seg_log[(size_t)unit * a.segs + seg] = (float)log_sum;
 }
 
 static int seq_cols(int d) { return d >= 128 ? 128 : (d + 31) / 32 * 32; }
@@ -240,31 +246,30 @@ static size_t scan_plan(int B, int H, int N, int d, int M, bool chunked, int num
     return segs < 2 ? 0 : (size_t)B * H * segs * fine * ((size_t)M * d + 4) * sizeof(float);
 }
 
-template <typename E, int MT>
+template <int MT>
 static ida_status launch_seq(const ScanArgs &a, cudaStream_t st) {
     const int cols = seq_cols(a.d), slices = (a.d + cols - 1) / cols;
-    const size_t smem = SeqSmem<E, MT>::bytes(cols);
+    const size_t smem = 2 * (size_t)SeqTile<MT>::floats(cols) * sizeof(float);
     const long long units = (long long)a.B * a.H * slices;
     if (units * a.segs > 0x7FFFFFFFLL) return fail_with(IDA_ERR_UNSUPPORTED, "too many rows and heads");
-    cudaError_t e = cudaFuncSetAttribute(scan_seq_kernel<E, MT, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    cudaError_t e = cudaFuncSetAttribute(scan_seq_kernel<MT, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e == cudaSuccess)
-        e = cudaFuncSetAttribute(scan_seq_kernel<E, MT, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        e = cudaFuncSetAttribute(scan_seq_kernel<MT, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return fail_with(IDA_ERR_CUDA, cudaGetErrorString(e));
     if (a.state_segs > 0) {
-        scan_seq_kernel<E, MT, true><<<(unsigned)(units * a.state_segs), cols, smem, st>>>(a);
+        scan_seq_kernel<MT, true><<<(unsigned)(units * a.state_segs), cols + SEQ_HELP, smem, st>>>(a);
         const ida_status s = launched("ssm segment states");
         if (s != IDA_OK) return s;
     }
-    scan_seq_kernel<E, MT, false><<<(unsigned)(units * a.segs), cols, smem, st>>>(a);
+    scan_seq_kernel<MT, false><<<(unsigned)(units * a.segs), cols + SEQ_HELP, smem, st>>>(a);
     return launched("ssm scan");
 }
 
-template <typename E>
 static ida_status launch_seq_m(const ScanArgs &a, cudaStream_t st) {
-    if (a.M <= 16) return launch_seq<E, 4>(a, st);
-    if (a.M <= 32) return launch_seq<E, 8>(a, st);
-    if (a.M <= 64) return launch_seq<E, 16>(a, st);
-    return launch_seq<E, 32>(a, st);
+    if (a.M <= 16) return launch_seq<4>(a, st);
+    if (a.M <= 32) return launch_seq<8>(a, st);
+    if (a.M <= 64) return launch_seq<16>(a, st);
+    return launch_seq<32>(a, st);
 }
 
 ida_status check_scan(int B, int H, int N, int d, int G, int M, long long ldx, long long ldb, long long ldc, long long lddt,
@@ -345,7 +350,7 @@ ida_status ida_ssm_scan(const void *x, const void *b, const void *c, const void 
     }
     // the tensor-core kernel takes a final state from segment states, the other one from its own
     a.state_segs = chunked && final_state ? a.segs * a.fine : (a.segs - 1) * a.fine;
-    return chunked ? launch_ssm_chunk(a, st) : launch_seq_m<float>(a, st);
+    return chunked ? launch_ssm_chunk(a, st) : launch_seq_m(a, st);
 }
 
 }  // extern "C"

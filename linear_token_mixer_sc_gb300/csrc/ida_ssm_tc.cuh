@@ -46,8 +46,6 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
     return *reinterpret_cast<const uint32_t *>(&h);
 }
 
-__device__ __forceinline__ void named_sync(int id, int n) { asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(n) : "memory"); }
-
 // log2 of decays in 2^-32 fixed point: their sums and differences are exact
 constexpr float kFix = 4294967296.f, kUnfix = 1.f / 4294967296.f;  // 2^32
 
