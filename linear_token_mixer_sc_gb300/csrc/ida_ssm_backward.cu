@@ -72,6 +72,7 @@ struct ChunkRows {
         const auto fill_bc = [&](const void *src, long long ld, float *dst) {
             const E *p = static_cast<const E *>(src) + row * ld + g * M;
             const int vpr = 4 * MT / V::n;
+#pragma unroll 4
             for (int i = threadIdx.x; i < chunk * vpr; i += blockDim.x) {
                 const int t = i / vpr, m = i % vpr * V::n;
                 float v[V::n];
@@ -86,6 +87,7 @@ struct ChunkRows {
         const auto fill_x = [&](const void *src, size_t at, long long ld, float *dst) {
             const E *p = static_cast<const E *>(src) + at;
             const int vpr = cols / V::n;
+#pragma unroll 4
             for (int i = threadIdx.x; i < chunk * vpr; i += blockDim.x) {
                 const int t = i / vpr, j = i % vpr * V::n;
                 float v[V::n];
@@ -209,8 +211,8 @@ __device__ __forceinline__ float tile_cols(const ssm_f2 (&X)[MT / 2][4], const f
 template <typename E, int MT>
 __global__ void __launch_bounds__(256) bwd_chunk_kernel(ScanBwdArgs s) {
     extern __shared__ __align__(16) float sm[];
-    const int cols = blockDim.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int M = s.M, d = s.d, Q = s.chunk;
+    const int M = s.M, d = s.d, Q = s.chunk, cols = (d + 31) / 32 * 32;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int unit = blockIdx.x / s.chunks, ch = blockIdx.x % s.chunks;
     const bool rev = blockIdx.y != 0;
     ChunkRows<E, MT> r;
@@ -219,6 +221,7 @@ __global__ void __launch_bounds__(256) bwd_chunk_kernel(ScanBwdArgs s) {
     __syncthreads();
     const int km = lane & 3, jl = warp * 32 + (lane >> 2) * 4, ms = BwdRow<MT>::MS, qs = BwdRow<MT>::QS;
     const int len = min(Q, s.N - ch * Q);
+    if (warp < cols / 32) {  // the others have helped to load
     ssm_f2 X[MT / 2][4];
 #pragma unroll
     for (int i = 0; i < MT / 2; ++i)
@@ -248,7 +251,8 @@ __global__ void __launch_bounds__(256) bwd_chunk_kernel(ScanBwdArgs s) {
                 *reinterpret_cast<float4 *>(out + (size_t)(m + 1) * d + jl) = make_float4(v[0], v[1], v[2], v[3]);
             }
         }
-    if (!rev && warp == 0) {
+    }
+    if (!rev && warp == (int)blockDim.x / 32 - 1) {
         float la = 0.f;
         const float rate = expf(s.a_log[unit % s.H]) * 1.4426950408889634f;
         for (int t = lane; t < Q; t += 32) la -= rate * r.delta[t];
@@ -291,8 +295,10 @@ __global__ void __launch_bounds__(256) bwd_carry_kernel(ScanBwdArgs s) {
 template <typename E, int MT>
 __global__ void __launch_bounds__(256) bwd_main_kernel(ScanBwdArgs s) {
     extern __shared__ __align__(16) float sm[];
-    const int cols = blockDim.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, warps = cols / 32;
-    const int M = s.M, d = s.d, Q = s.chunk, H = s.H, N = s.N;
+    const int M = s.M, d = s.d, Q = s.chunk, H = s.H, N = s.N, cols = (d + 31) / 32 * 32;
+    // the first `warps` warps walk the positions, all load and sum
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, warps = cols / 32, all_warps = blockDim.x / 32;
+    const bool walks = warp < warps;
     const int unit = blockIdx.x / s.chunks, ch = blockIdx.x % s.chunks, b = unit / H, h = unit % H;
     const int t0 = ch * Q, len = min(Q, N - t0);
     constexpr int MS = BwdRow<MT>::MS, QS = BwdRow<MT>::QS, MP = 4 * MT;
@@ -364,9 +370,9 @@ __global__ void __launch_bounds__(256) bwd_main_kernel(ScanBwdArgs s) {
             }
         return dot;
     };
-    load_tile(s.state0 + so, false);
+    if (walks) load_tile(s.state0 + so, false);
     __syncthreads();
-    for (int t = warp; t < len; t += warps) {  // the products of a position with itself
+    for (int t = warp; t < len; t += all_warps) {  // the products of a position with itself
         float v = 0.f, u = 0.f;
         for (int j = lane; j < cols; j += 32) v = fmaf(r.x[t * cols + j], r.dy[t * cols + j], v);
         for (int m = lane; m < M; m += 32) {
@@ -386,7 +392,7 @@ __global__ void __launch_bounds__(256) bwd_main_kernel(ScanBwdArgs s) {
     const auto flush_rows = [&](int tb, int nb, bool is_c, float *dots) {
         __syncthreads();
         float *head = is_c ? s.dc_head : s.db_head;
-        for (int tt = warp; tt < nb; tt += warps) {
+        for (int tt = warp; tt < nb; tt += all_warps) {
             const int t = tb + tt;
             const float delta = r.delta[t], self = xdy[t] * delta, f = is_c ? 1.f : delta;
             float dot = 0.f;
@@ -412,28 +418,28 @@ __global__ void __launch_bounds__(256) bwd_main_kernel(ScanBwdArgs s) {
     // forwards: a_t X_{t-1} for dc_t, then X_t
     for (int tb = 0; tb < len; tb += BT) {
         const int nb = min(BT, len - tb);
-        for (int tt = 0; tt < nb; ++tt) {
+        for (int tt = 0; walks && tt < nb; ++tt) {
             const int t = tb + tt;
             tile_scale<MT>(X, r.a[t]);
             tile_rows<MT>(X, *reinterpret_cast<const float4 *>(r.dy + t * cols + jl), lane, rows + (warp * BT + tt) * MP);
             tile_add<MT>(X, r.b + t * MS + km * QS, r.delta[t], *reinterpret_cast<const float4 *>(r.x + t * cols + jl));
         }
         flush_rows(tb, nb, true, pw);
-        if (tb + BT < len) keep_tile(kept + (size_t)(tb / BT) * M * d);
+        if (walks && tb + BT < len) keep_tile(kept + (size_t)(tb / BT) * M * d);
     }
     // w behind a group: <a Z of the next position, X of the last>; here the chunk's last group
-    const float end = warp_sum(load_tile(s.adj + so, true));
-    if (lane == 0) misc[(len - 1) / BT * 8 + warp] = end;
+    const float end = walks ? warp_sum(load_tile(s.adj + so, true)) : 0.f;
+    if (walks && lane == 0) misc[(len - 1) / BT * 8 + warp] = end;
 
     // backwards: a_{t+1} Z_{t+1} for db_t and dx_t, then Z_t
     const float skip = s.D[h];
     for (int tb = (len - 1) / BT * BT; tb >= 0; tb -= BT) {
         const int nb = min(BT, len - tb);
-        if (tb + BT < len) {
+        if (walks && tb + BT < len) {
             const float v = warp_sum(kept_product(kept + (size_t)(tb / BT) * M * d));
             if (lane == 0) misc[tb / BT * 8 + warp] = v;
         }
-        for (int tt = nb - 1; tt >= 0; --tt) {
+        for (int tt = nb - 1; walks && tt >= 0; --tt) {
             const int t = tb + tt;
             tile_rows<MT>(X, *reinterpret_cast<const float4 *>(r.x + t * cols + jl), lane, rows + (warp * BT + tt) * MP);
             const float o = tile_cols<MT>(X, r.b + t * MS + km * QS, lane), gv = r.dy[t * cols + col];
@@ -591,18 +597,19 @@ static ida_status launch_bwd_sums(const ScanBwdArgs &s, int parts, int per, cuda
 
 template <typename E, int MT>
 static ida_status launch_bwd(const ScanBwdArgs &s, cudaStream_t st) {
-    const int cols = bwd_cols(s.d);
+    // narrow heads get warps that help to load and to sum (32 channels: 121 us with one warp, 64 chunks)
+    const int cols = bwd_cols(s.d), threads = cols + 128 < 256 ? cols + 128 : 256;
     const size_t smem = bwd_smem<MT>(cols, s.chunk);
     cudaError_t e = cudaFuncSetAttribute(bwd_chunk_kernel<E, MT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e == cudaSuccess)
         e = cudaFuncSetAttribute(bwd_main_kernel<E, MT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return fail_with(IDA_ERR_CUDA, cudaGetErrorString(e));
     const long long blocks = (long long)s.B * s.H * s.chunks;
-    bwd_chunk_kernel<E, MT><<<dim3((unsigned)blocks, 2), cols, smem, st>>>(s);
+    bwd_chunk_kernel<E, MT><<<dim3((unsigned)blocks, 2), threads, smem, st>>>(s);
     ida_status r = launched("ssm chunk states");
     if (r == IDA_OK) r = launch_bwd_carry(s, st);
     if (r != IDA_OK) return r;
-    bwd_main_kernel<E, MT><<<(unsigned)blocks, cols, smem, st>>>(s);
+    bwd_main_kernel<E, MT><<<(unsigned)blocks, threads, smem, st>>>(s);
     r = launched("ssm scan backward");
     return r == IDA_OK ? launch_bwd_sums<E>(s, s.H / s.G, 1, st) : r;
 }
