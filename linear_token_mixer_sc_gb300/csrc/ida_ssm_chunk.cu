@@ -583,7 +583,12 @@ __global__ void __launch_bounds__(STH, MP == 64 ? 2 : 1)
     const int H = a.H, N = a.N, M = a.M, d = a.d;
     const int slices = (d + DP - 1) / DP, parts = a.segs * a.fine;
     constexpr bool EACH = MODE != kPart;
-    constexpr uint32_t COLS = EACH || PARTS > 1 ? 2 * MP : MP;
+    // TMEM: the small parts have accumulators of their own (see above), so that parts that lie side by side
+    // in shared memory are one MMA's columns (its A tile, x, is what an MMA's time goes to): all three
+    // where they fit 256 columns, which leaves two CTAs an SM, else the high and the middle one
+    constexpr int WIDE = PARTS == 1 ? 1 : MP == 64 && !EACH ? 3 : 2;  // parts of one MMA
+    constexpr int ACC = WIDE * MP;                                    // columns of an accumulator
+    constexpr uint32_t COLS = EACH ? 2 * ACC : ACC > 128 ? 256 : ACC;
     const int groups = EACH ? (parts + per - 1) / per : a.state_segs;
     int id = blockIdx.x;
     const int seg = id % groups;
@@ -662,13 +667,15 @@ __global__ void __launch_bounds__(STH, MP == 64 ? 2 : 1)
         for (int blk = 0; blk < MH / 16; ++blk) {
             const int m0 = half * MH + 16 * blk;
             float v[16];
-            tmem_ld16(tm + lane_base + (EACH && (n & 1) ? MP : 0) + m0, v);
-            if (!EACH && PARTS > 1) {
-                float u[16];
-                tmem_ld16(tm + lane_base + MP + m0, u);
+            const uint32_t at = tm + lane_base + (EACH && (n & 1) ? ACC : 0) + m0;
+            tmem_ld16(at, v);
+            if (WIDE > 1) {
+                float u[16], l[16];
+                tmem_ld16(at + MP, u);
+                if (WIDE > 2) tmem_ld16(at + 2 * MP, l);
                 tmem_wait_ld();
 #pragma unroll
-                for (int e = 0; e < 16; ++e) v[e] += u[e];
+                for (int e = 0; e < 16; ++e) v[e] += WIDE > 2 ? u[e] + l[e] : u[e];
             }
             tmem_wait_ld();
             if (nch == 0)
@@ -729,15 +736,17 @@ __global__ void __launch_bounds__(STH, MP == 64 ? 2 : 1)
             tc_fence_after();
             // x^T as A: with DP = 64 its second 64 rows repeat the first
             const SmemDesc da = sw_desc(s0 + L::X + buf * L::XB, DP == 64 ? 0 : SSLAB);
-            constexpr uint32_t id_x = idesc(128, MP, 1, 1, 1, 1);
+            const SmemDesc dh = sw_desc(s0 + L::B + buf * L::BB, SSLAB);
+            const SmemDesc dl = sw_desc(s0 + L::B + buf * L::BB + WIDE * (MP / 64) * SSLAB, SSLAB);
+            const uint32_t acc = tm + (EACH && (n & 1) ? ACC : 0);
+            constexpr uint32_t id_w = idesc(128, ACC, 1, 1, 1, 1), id_l = idesc(128, MP, 1, 1, 1, 1);
 #pragma unroll
-            for (int part = PARTS - 1; part >= 0; --part) {  // the small parts first: fewer roundings of the large sum
-                const SmemDesc dh = sw_desc(s0 + L::B + buf * L::BB + part * (MP / 64) * SSLAB, SSLAB);
+            for (int k = 0; k < SQ / 16; ++k)
+                mma_f16(acc, sw_step(da, k * 2048), sw_step(dh, k * 2048), id_w, (!EACH && n > 0) || k > 0);
+            if (WIDE < PARTS)  // the low part joins the middle one
 #pragma unroll
                 for (int k = 0; k < SQ / 16; ++k)
-                    mma_f16(tm + ((EACH ? (n & 1) : part > 0) ? MP : 0), sw_step(da, k * 2048), sw_step(dh, k * 2048), id_x,
-                            (!EACH && n > 0) || (part < PARTS - 1 && (EACH || part > 0)) || k > 0);
-            }
+                    mma_f16(acc + MP, sw_step(da, k * 2048), sw_step(dl, k * 2048), id_l, 1);
             mma_commit(&bar[2 + buf]);
         }
         __syncwarp();
