@@ -6,7 +6,7 @@
 // t >= s, f_s = 2^(S_Q - S_s), and the transposed products of positions
 //   G [s][t] = b_s . c_t,   E [s][t] = x_s . dy_t          (MMAs, K = M and K = d)
 // the gradients of ida_ssm_backward.cu's header are
-//   dx_s = D dy_s + D_s (sum_t W G dy_t + f_s Z^T b_s)      P = D_s W G (+ D at s = t) as A, dy as B
+//   dx_s = (D + D_s G_ss) dy_s + D_s (sum_{t > s} W G dy_t + f_s Z^T b_s)     P = D_s W G as A, dy as B
 //   db_s = D_s (sum_t W E c_t + f_s Z x_s)                  R = D_s W E as A, c as B
 //   dc_t = sum_s R b_s + 2^(S_t) X_0 dy_t                   R^T as A (the same tile read MN-major)
 // and, from the fp32 K_st = D_s W G E (t > s, never rounded, never stored) and the inter-chunk
@@ -287,7 +287,7 @@ __global__ void __launch_bounds__(BTH, 1)
         }
         if (mine) {
             // K, P, R: row s, every fourth block of 16 columns t
-            const float sh = Sh[row], sl = Sl[row], delta = dl[row], skip = a.D[h];
+            const float sh = Sh[row], sl = Sl[row], delta = dl[row];
             float ks = 0.f;
 #pragma unroll
             for (int i = 0; i < NG / 4; ++i) {
@@ -333,7 +333,7 @@ const ssm_f2 ff = ssm_pack(f, f), dd = ssm_pack(delta, delta);
                                 es[t] = ev[e];
                                 w = 1.f;
                             }
-                            gv[e] = t >= row ? gv[e] * (w * delta) + (t == row ? skip : 0.f) : 0.f;
+                            gv[e] = t > row ? gv[e] * (w * delta) : 0.f;
                             ev[e] = t >= row ? ev[e] * (w * delta) : 0.f;
                         }
                         if (kb == row >> 4)
@@ -394,14 +394,20 @@ const ssm_f2 ff = ssm_pack(f, f), dd = ssm_pack(delta, delta);
         tc_fence_after();
         if (lane == 0) red[warp] = cross;
         write_state();  // X_0's parts take the place of Z's
-        if (mine) {  // dx out: my row, a quarter of the channels, over P
+        if (mine) {  // dx out: my row, a quarter of the channels, over P; its own dy's term in fp32
             constexpr int CW = DP / 4;
+            const float own = fmaf(dl[row], gs[row], a.D[h]);
 #pragma unroll
             for (int c = 0; c < CW; c += 16) {
                 const int j = wj * CW + c;
-                float v[16];
+                float v[16], u[16];
                 tmem_ld16(tm + lane_base + T::DX + j, v);
+                const unsigned char *py = sm + L::DY + j / 64 * L::SLAB;
+                Vec16<__nv_bfloat16>::unpack(*reinterpret_cast<const uint4 *>(py + sw_off(row, j % 64 / 8)), u);
+                Vec16<__nv_bfloat16>::unpack(*reinterpret_cast<const uint4 *>(py + sw_off(row, j % 64 / 8 + 1)), u + 8);
                 tmem_wait_ld();
+#pragma unroll
+                for (int e = 0; e < 16; ++e) v[e] = fmaf(own, u[e], v[e]);
                 unsigned char *out = sm + L::P + j / 64 * L::SLAB;
                 *reinterpret_cast<uint4 *>(out + sw_off(row, j % 64 / 8)) = Vec16<__nv_bfloat16>::pack(v);
                 *reinterpret_cast<uint4 *>(out + sw_off(row, j % 64 / 8 + 1)) = Vec16<__nv_bfloat16>::pack(v + 8);
