@@ -487,6 +487,8 @@ def _rows(name: str, t: torch.Tensor, shape, dtype, dev: int, lead: int):
 def _work_buffer(given: torch.Tensor | None, nbytes: int, dev: int):
     """(tensor kept alive, address, bytes) of the given workspace or of a new one."""
     if given is None:
+        if not nbytes:
+            return None, None, 0
         given = torch.empty(nbytes, dtype=torch.uint8, device=dev)
     elif given.get_device() != dev or not given.is_contiguous():
         raise ValueError("workspace must be a contiguous tensor on the inputs' CUDA device")
@@ -552,7 +554,7 @@ def ida_ssm_conv_backward(x: torch.Tensor, dout: torch.Tensor, conv_w: torch.Ten
     if dx is None:
         dx = torch.empty((B, N, C), dtype=x.dtype, device=x.device)
     dxp, lddx = _rows("dx", dx, x.shape, x.dtype, dev, 2)
-    dw, db = torch.empty_like(conv_w), torch.empty_like(conv_b)
+    dw, db = (torch.empty(t.shape, dtype=f32, device=x.device) for t in (conv_w, conv_b))
     L = load()
     ws, wsp, n = _work_buffer(workspace, L.ida_ssm_conv_backward_workspace_bytes(B, N, C, W), dev)
     st = L.ida_ssm_conv_backward(xp, dp, wp, bp, dxp, dw.data_ptr(), db.data_ptr(), B, N, C, ldx, lddx, dt, W, wsp, n,
@@ -626,9 +628,10 @@ def ida_ssm_scan_backward(x: torch.Tensor, b: torch.Tensor, c: torch.Tensor, dt:
     st = L.ida_ssm_scan_backward(*ptrs, dyp, p, p + H * d * e, p + (H * d + G * M) * e, ddt.data_ptr(),
                                  pp, pp + 4 * H, pp + 8 * H, *sizes, *strides, C, C, C, H, code, wsp, n, _raw_stream(dev))
     _check(st, "ida_ssm_scan_backward")
-    gx, gb, gc = xbc.split((H * d, G * M, G * M), dim=2)
-    return {"x": gx.view(B, N, H, d), "b": gb.view(B, N, G, M), "c": gc.view(B, N, G, M), "xbc": xbc, "dt": ddt,
-            "a_log": par[0], "dt_bias": par[1], "D": par[2]}
+    da_log, ddt_bias, dD = par.unbind()
+    bc = (B, N, G, M), (N * C, C, M, 1)
+    return {"x": xbc.as_strided((B, N, H, d), (N * C, C, d, 1)), "b": xbc.as_strided(*bc, H * d),
+            "c": xbc.as_strided(*bc, H * d + G * M), "xbc": xbc, "dt": ddt, "a_log": da_log, "dt_bias": ddt_bias, "D": dD}
 
 
 @_placed
@@ -675,7 +678,7 @@ def ida_rmsnorm(x: torch.Tensor, w: torch.Tensor, residual: torch.Tensor | None 
     xp, wp = _dense("x", x, x.shape, x.dtype, dev), _dense("w", w, (D,), torch.float32, dev)
     rp = None if residual is None else _dense("residual", residual, x.shape, x.dtype, dev)
     if residual is not None and res_out is None:
-        res_out = torch.empty_like(x)
+        res_out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
     q = scale = None
     if group:
         if group < 0 or D % group:
@@ -683,7 +686,7 @@ def ida_rmsnorm(x: torch.Tensor, w: torch.Tensor, residual: torch.Tensor | None 
         q = torch.empty(x.shape, dtype=torch.float8_e4m3fn, device=x.device)
         scale = torch.empty((*x.shape[:-1], D // group), dtype=torch.float32, device=x.device)
     elif out is None:
-        out = torch.empty_like(x)
+        out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
     st = load().ida_rmsnorm(xp, rp, wp, None if res_out is None else _dense("res_out", res_out, x.shape, x.dtype, dev),
                             None if out is None else _dense("out", out, x.shape, x.dtype, dev),
                             None if q is None else q.data_ptr(), None if scale is None else scale.data_ptr(),
@@ -705,8 +708,8 @@ def ida_rmsnorm_backward(r: torch.Tensor, w: torch.Tensor, dy: torch.Tensor, dre
     gp = _dense("dy", dy, r.shape, r.dtype, dev)
     sp = None if dres is None else _dense("dres", dres, r.shape, r.dtype, dev)
     if dx is None:
-        dx = torch.empty_like(r)
-    dw = torch.empty_like(w)
+        dx = torch.empty(r.shape, dtype=r.dtype, device=r.device)
+    dw = torch.empty(w.shape, dtype=w.dtype, device=w.device)
     L = load()
     ws, wsp, n = _work_buffer(workspace, L.ida_rmsnorm_backward_workspace_bytes(rows, D) if workspace is None else 0, dev)
     st = L.ida_rmsnorm_backward(rp, wp, gp, sp, _dense("dx", dx, r.shape, r.dtype, dev), dw.data_ptr(), rows, D, eps,

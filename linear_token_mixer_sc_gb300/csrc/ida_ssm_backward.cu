@@ -210,6 +210,7 @@ __device__ __forceinline__ float tile_cols(const ssm_f2 (&X)[MT / 2][4], const f
 // it passes on of its own adjoint, sum_t a_first .. a_t c_t dy_t^T, in adj[c].
 template <typename E, int MT>
 __global__ void __launch_bounds__(256) bwd_chunk_kernel(ScanBwdArgs s) {
+    dependent_launch();
     extern __shared__ __align__(16) float sm[];
     const int M = s.M, d = s.d, Q = s.chunk, cols = (d + 31) / 32 * 32;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -264,6 +265,8 @@ __global__ void __launch_bounds__(256) bwd_chunk_kernel(ScanBwdArgs s) {
 // The running sums over the chunks, in place: state0[c] becomes the state before chunk c, adj[c]
 // what reaches chunk c from behind.  One thread per four state elements.
 __global__ void __launch_bounds__(256) bwd_carry_kernel(ScanBwdArgs s) {
+    dependent_launch();
+    dependent_wait();
     const int unit = blockIdx.y, i = blockIdx.x * 256 + threadIdx.x, n = s.M * s.d / 4;
     if (i >= n) return;
     const bool rev = blockIdx.z != 0;
@@ -294,6 +297,8 @@ __global__ void __launch_bounds__(256) bwd_carry_kernel(ScanBwdArgs s) {
 
 template <typename E, int MT>
 __global__ void __launch_bounds__(256) bwd_main_kernel(ScanBwdArgs s) {
+    dependent_launch();
+    dependent_wait();
     extern __shared__ __align__(16) float sm[];
     const int M = s.M, d = s.d, Q = s.chunk, H = s.H, N = s.N, cols = (d + 31) / 32 * 32;
     // the first `warps` warps walk the positions, all load and sum
@@ -321,8 +326,8 @@ __global__ void __launch_bounds__(256) bwd_main_kernel(ScanBwdArgs s) {
             const int m = km * MT + 2 * i;
             float4 u = make_float4(0.f, 0.f, 0.f, 0.f), v = u;
             if (m < M && jl < d) {
-                u = __ldg(reinterpret_cast<const float4 *>(src + (size_t)m * d + jl));
-                v = __ldg(reinterpret_cast<const float4 *>(src + (size_t)(m + 1) * d + jl));
+                u = __ldcg(reinterpret_cast<const float4 *>(src + (size_t)m * d + jl));
+                v = __ldcg(reinterpret_cast<const float4 *>(src + (size_t)(m + 1) * d + jl));
             }
             if (product) {
                 float x[4], y[4];
@@ -486,6 +491,8 @@ __global__ void __launch_bounds__(256) bwd_main_kernel(ScanBwdArgs s) {
 // thread per four channels.
 template <typename E>
 __global__ void __launch_bounds__(256) bwd_group_kernel(ScanBwdArgs s, int n) {
+    dependent_launch();
+    dependent_wait();
     const int vpr = s.G * s.M / 4;
     const long long i = (long long)blockIdx.x * 256 + threadIdx.x;
     if (i >= (long long)s.B * s.N * vpr) return;
@@ -511,6 +518,7 @@ __global__ void __launch_bounds__(256) bwd_group_kernel(ScanBwdArgs s, int n) {
 // The head's parameter gradients: its chunks' parts over all rows, 128 interleaved sums.
 __global__ void __launch_bounds__(128) bwd_params_kernel(ScanBwdArgs s, int per) {  // per: parts of a chunk
     __shared__ float red[4][3];
+    dependent_wait();
     const int h = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     float v[3] = {0.f, 0.f, 0.f};
     const long long n = (long long)s.B * s.chunks * per;
@@ -575,9 +583,8 @@ static ida_status launch_bwd_carry(const ScanBwdArgs &s, cudaStream_t st) {
         t.adj += (size_t)u0 * s.chunks * s.M * s.d;
         t.chunk_log += (size_t)u0 * s.chunks;
         const int units = s.B * s.H - u0 < 65535 ? s.B * s.H - u0 : 65535;
-        bwd_carry_kernel<<<dim3((s.M * s.d / 4 + 255) / 256, units, 2), 256, 0, st>>>(t);
-        const ida_status r = launched("ssm chunk sums");
-        if (r != IDA_OK) return r;
+        const cudaError_t e = launch_dependent(bwd_carry_kernel, dim3((s.M * s.d / 4 + 255) / 256, units, 2), dim3(256), 0, st, t);
+        if (e != cudaSuccess) return fail_with(IDA_ERR_CUDA, std::string("ssm chunk sums launch: ") + cudaGetErrorString(e));
     }
     return IDA_OK;
 }
@@ -587,12 +594,11 @@ template <typename E>
 static ida_status launch_bwd_sums(const ScanBwdArgs &s, int parts, int per, cudaStream_t st) {
     if (s.db_head) {
         const long long n = ((long long)s.B * s.N * s.G * s.M / 4 + 255) / 256;
-        bwd_group_kernel<E><<<dim3((unsigned)n, 2), 256, 0, st>>>(s, parts);
-        const ida_status r = launched("ssm group sums");
-        if (r != IDA_OK) return r;
+        const cudaError_t e = launch_dependent(bwd_group_kernel<E>, dim3((unsigned)n, 2), dim3(256), 0, st, s, parts);
+        if (e != cudaSuccess) return fail_with(IDA_ERR_CUDA, std::string("ssm group sums launch: ") + cudaGetErrorString(e));
     }
-    bwd_params_kernel<<<s.H, 128, 0, st>>>(s, per);
-    return launched("ssm parameter gradients");
+    const cudaError_t e = launch_dependent(bwd_params_kernel, dim3(s.H), dim3(128), 0, st, s, per);
+    return e == cudaSuccess ? IDA_OK : fail_with(IDA_ERR_CUDA, std::string("ssm parameter gradients launch: ") + cudaGetErrorString(e));
 }
 
 template <typename E, int MT>
@@ -600,18 +606,17 @@ static ida_status launch_bwd(const ScanBwdArgs &s, cudaStream_t st) {
     // narrow heads get warps that help to load and to sum (32 channels: 121 us with one warp, 64 chunks)
     const int cols = bwd_cols(s.d), threads = cols + 128 < 256 ? cols + 128 : 256;
     const size_t smem = bwd_smem<MT>(cols, s.chunk);
-    cudaError_t e = cudaFuncSetAttribute(bwd_chunk_kernel<E, MT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (e == cudaSuccess)
-        e = cudaFuncSetAttribute(bwd_main_kernel<E, MT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    cudaError_t e = allow_smem(bwd_chunk_kernel<E, MT>, smem);
+    if (e == cudaSuccess) e = allow_smem(bwd_main_kernel<E, MT>, smem);
     if (e != cudaSuccess) return fail_with(IDA_ERR_CUDA, cudaGetErrorString(e));
     const long long blocks = (long long)s.B * s.H * s.chunks;
     bwd_chunk_kernel<E, MT><<<dim3((unsigned)blocks, 2), threads, smem, st>>>(s);
     ida_status r = launched("ssm chunk states");
     if (r == IDA_OK) r = launch_bwd_carry(s, st);
     if (r != IDA_OK) return r;
-    bwd_main_kernel<E, MT><<<(unsigned)blocks, threads, smem, st>>>(s);
-    r = launched("ssm scan backward");
-    return r == IDA_OK ? launch_bwd_sums<E>(s, s.H / s.G, 1, st) : r;
+    e = launch_dependent(bwd_main_kernel<E, MT>, dim3((unsigned)blocks), dim3(threads), smem, st, s);
+    if (e != cudaSuccess) return fail_with(IDA_ERR_CUDA, std::string("ssm scan backward launch: ") + cudaGetErrorString(e));
+    return launch_bwd_sums<E>(s, s.H / s.G, 1, st);
 }
 
 template <typename E>

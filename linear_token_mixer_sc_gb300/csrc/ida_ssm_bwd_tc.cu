@@ -164,12 +164,12 @@ __global__ void __launch_bounds__(BTH, 1)
             const int i = tid + n * BTH, m = i / (DP / 8), j = i % (DP / 8) * 8;
             float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
             if (m < M && j < d) {
-                *reinterpret_cast<float4 *>(v) = __ldg(reinterpret_cast<const float4 *>(st + (size_t)m * d + j));
-                *reinterpret_cast<float4 *>(v + 4) = __ldg(reinterpret_cast<const float4 *>(st + (size_t)m * d + j + 4));
+                *reinterpret_cast<float4 *>(v) = __ldcg(reinterpret_cast<const float4 *>(st + (size_t)m * d + j));
+                *reinterpret_cast<float4 *>(v + 4) = __ldcg(reinterpret_cast<const float4 *>(st + (size_t)m * d + j + 4));
                 if (other) {
                     float u[8];
-                    *reinterpret_cast<float4 *>(u) = __ldg(reinterpret_cast<const float4 *>(other + (size_t)m * d + j));
-                    *reinterpret_cast<float4 *>(u + 4) = __ldg(reinterpret_cast<const float4 *>(other + (size_t)m * d + j + 4));
+                    *reinterpret_cast<float4 *>(u) = __ldcg(reinterpret_cast<const float4 *>(other + (size_t)m * d + j));
+                    *reinterpret_cast<float4 *>(u + 4) = __ldcg(reinterpret_cast<const float4 *>(other + (size_t)m * d + j + 4));
 #pragma unroll
                     for (int e = 0; e < 8; ++e) dot = fmaf(u[e], v[e], dot);
                 }
@@ -219,6 +219,8 @@ __global__ void __launch_bounds__(BTH, 1)
         if (ta == 0) red[16 + 15 * ((r - r0) & 1)] = ex2_fix(all);
     };
     __syncthreads();
+    dependent_launch();  // its TMEM is allocated
+    dependent_wait();
     if (tid == 0 && r0 < r1) {
         mbar_arrive_expect_tx(&bar[0], 2 * L::BB);
 #pragma unroll
@@ -666,8 +668,8 @@ static ida_status launch_bwd_tc_d(const BwdTcArgs &ba, cudaStream_t st) {
     if (e != cudaSuccess) return fail_with(IDA_ERR_CUDA, cudaGetErrorString(e));
     const long long ctas = (long long)a.B * a.chunks * a.G * ba.splits;
     if (ctas > 0x7FFFFFFFLL) return fail_with(IDA_ERR_UNSUPPORTED, "too many positions and groups");
-    ssm_bwd_tc_kernel<Q, DP, MP><<<(unsigned)ctas, BTH, smem, st>>>(ba, mx, mdy, mb, mc, mdx);
-    return launched("ssm scan backward");
+    e = launch_dependent(ssm_bwd_tc_kernel<Q, DP, MP>, dim3((unsigned)ctas), dim3(BTH), smem, st, ba, mx, mdy, mb, mc, mdx);
+    return e == cudaSuccess ? IDA_OK : fail_with(IDA_ERR_CUDA, std::string("ssm scan backward launch: ") + cudaGetErrorString(e));
 }
 
 // The chunk states, forwards and backwards, from zero.

@@ -365,7 +365,7 @@ __global__ void __launch_bounds__(CTH, 1)
             for (int m0 = 0; m0 < MP; m0 += 16) {
                 float v[16];
 #pragma unroll
-                for (int e = 0; e < 16; ++e) v[e] = mine && m0 + e < M ? __ldg(p + (size_t)(m0 + e) * d + j0 + ch) : 0.f;
+                for (int e = 0; e < 16; ++e) v[e] = mine && m0 + e < M ? __ldcg(p + (size_t)(m0 + e) * d + j0 + ch) : 0.f;
                 tmem_st16(tm + lane_base + TS + m0, v);
             }
             tmem_wait_st();
@@ -793,6 +793,8 @@ __global__ void __launch_bounds__(STH, MP == 64 ? 2 : 1)
         tc_fence_after();
         tmem_dealloc(tm, COLS);
     }
+    // runs beside the launch before it, which it takes nothing from; what waits for this one waits for both
+    if (MODE == kAdjoint) dependent_wait();
 }
 
 // Segment states, in place: seg_state[s] becomes the state before part s where a segment starts; the
@@ -907,6 +909,10 @@ static ida_status launch_states(const ScanArgs &a, cudaStream_t st) {
     const long long slots = MP == 64 ? 304 : 152, chunks = (long long)a.segs * a.fine;
     const int per = (int)((units * chunks + slots - 1) / slots < chunks ? (units * chunks + slots - 1) / slots : chunks);
     const long long groups = MODE == kPart ? a.state_segs : (chunks + per - 1) / per;
+    if (MODE == kAdjoint) {
+        e = launch_dependent(kernel, dim3((unsigned)(units * groups)), dim3(STH), smem, st, a, per, mx, mb);
+        return e == cudaSuccess ? IDA_OK : fail_with(IDA_ERR_CUDA, std::string("ssm adjoint states launch: ") + cudaGetErrorString(e));
+    }
     kernel<<<(unsigned)(units * groups), STH, smem, st>>>(a, per, mx, mb);
     return launched("ssm segment states");
 }

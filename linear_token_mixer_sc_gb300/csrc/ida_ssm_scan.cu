@@ -38,6 +38,10 @@ template <int MT, bool STATE>
 __global__ void __launch_bounds__(128 + SEQ_HELP) scan_seq_kernel(ScanArgs a) {
     using L = SeqTile<MT>;
     extern __shared__ __align__(16) float sm[];
+    if (STATE)
+        dependent_launch();
+    else
+        dependent_wait();
     const int M = a.M, d = a.d, H = a.H, N = a.N, rep = H / a.G;
     const int cols = blockDim.x - SEQ_HELP, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int slices = (d + cols - 1) / cols, nseg = STATE ? a.state_segs : a.segs;
@@ -143,8 +147,8 @@ __global__ void __launch_bounds__(128 + SEQ_HELP) scan_seq_kernel(ScanArgs a) {
             for (int i = 0; i < MT / 2; ++i) {
                 const int m = km * MT + 2 * i;
                 if (m < M) {
-                    const float4 u = __ldg(reinterpret_cast<const float4 *>(p + (size_t)m * d + j0 + jl));
-                    const float4 v = __ldg(reinterpret_cast<const float4 *>(p + (size_t)(m + 1) * d + j0 + jl));
+                    const float4 u = __ldcg(reinterpret_cast<const float4 *>(p + (size_t)m * d + j0 + jl));
+                    const float4 v = __ldcg(reinterpret_cast<const float4 *>(p + (size_t)(m + 1) * d + j0 + jl));
                     X[i][0] = ssm_fma(X[i][0], ff, ssm_pack(u.x, v.x));
                     X[i][1] = ssm_fma(X[i][1], ff, ssm_pack(u.y, v.y));
                     X[i][2] = ssm_fma(X[i][2], ff, ssm_pack(u.z, v.z));
@@ -252,14 +256,15 @@ static ida_status launch_seq(const ScanArgs &a, cudaStream_t st) {
     const size_t smem = 2 * (size_t)SeqTile<MT>::floats(cols) * sizeof(float);
     const long long units = (long long)a.B * a.H * slices;
     if (units * a.segs > 0x7FFFFFFFLL) return fail_with(IDA_ERR_UNSUPPORTED, "too many rows and heads");
-    cudaError_t e = cudaFuncSetAttribute(scan_seq_kernel<MT, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (e == cudaSuccess)
-        e = cudaFuncSetAttribute(scan_seq_kernel<MT, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    cudaError_t e = allow_smem(scan_seq_kernel<MT, false>, smem);
+    if (e == cudaSuccess) e = allow_smem(scan_seq_kernel<MT, true>, smem);
     if (e != cudaSuccess) return fail_with(IDA_ERR_CUDA, cudaGetErrorString(e));
     if (a.state_segs > 0) {
         scan_seq_kernel<MT, true><<<(unsigned)(units * a.state_segs), cols + SEQ_HELP, smem, st>>>(a);
         const ida_status s = launched("ssm segment states");
         if (s != IDA_OK) return s;
+        e = launch_dependent(scan_seq_kernel<MT, false>, dim3((unsigned)(units * a.segs)), dim3(cols + SEQ_HELP), smem, st, a);
+        return e == cudaSuccess ? IDA_OK : fail_with(IDA_ERR_CUDA, std::string("ssm scan launch: ") + cudaGetErrorString(e));
     }
     scan_seq_kernel<MT, false><<<(unsigned)(units * a.segs), cols + SEQ_HELP, smem, st>>>(a);
     return launched("ssm scan");

@@ -109,6 +109,11 @@ cudaError_t launch_dependent(void (*kernel)(K...), dim3 grid, dim3 block, size_t
     cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, kernel, K(args)...);
 }
+// The attribute that dynamic shared memory above 48 KB needs.
+template <typename F>
+cudaError_t allow_smem(F *kernel, size_t bytes) {
+    return bytes <= 48 * 1024 ? cudaSuccess : cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+}
 inline ida_status launched(const char *what) {
     cudaError_t e = cudaGetLastError();
     return e == cudaSuccess ? IDA_OK : fail_with(IDA_ERR_CUDA, std::string(what) + " launch: " + cudaGetErrorString(e));
