@@ -48,9 +48,9 @@ struct BwdSmem {
     static constexpr int C = B + BB;               // [MP / 64][Q t][64]
     static constexpr int R = C + BB;               // [Q / 64][Q s][64 t]
     static constexpr int P = R + QB;               // [Q / 64][Q s][64 t], later dx [DP / 64][Q s][64]
-    static constexpr int PSLAB = MP * 128, PART = DP / 64 * PSLAB;  // a part of a state [DP / 64][MP m][64]
-    static constexpr int ST = P + (QB > XB ? QB : XB);  // [3] parts of Z, later of X_0
-    static constexpr int MISC = ST + 3 * PART;
+    static constexpr int PSLAB = MP * 128, STS = 3 * PSLAB;  // a state's three parts [DP / 64][3][MP m][64]
+    static constexpr int ST = P + (QB > XB ? QB : XB);  // parts of Z, later of X_0
+    static constexpr int MISC = ST + DP / 64 * STS;
     static constexpr int ARR = MISC + 64;
     // S in two floats, 2^S, f, D and column factors of two heads; column sums of K in 8 parts and row
     // sums in 4 + 1, the inter-chunk products in 4 parts each, G and E of a position with itself
@@ -63,12 +63,16 @@ struct BwdSmem {
 };
 
 // Columns.  With M <= 64 G stays for all heads and the inter-chunk products take E's place; with
-// 64 positions and M > 64 they take G's and E's, and G is made again for every head.
+// 64 positions and M > 64 they take G's and E's, and G is made again for every head.  Parts of a state
+// side by side in shared memory are one MMA's columns, where there is room: all three, or the high and
+// the middle one, which the low one then joins.  An MMA takes as long with 64 columns as with 192
+// (162 us for the three one after the other).
 template <int Q, int DP, int MP>
 struct BwdTmem {
     static constexpr bool KEEP_G = MP == 64;
-    static constexpr uint32_t G = 0, E = KEEP_G ? 128 : 64, DBI = KEEP_G ? 128 : 0, DCI = KEEP_G ? 192 : 0;
-    static constexpr uint32_t DX = KEEP_G ? 256 : 128, DB = KEEP_G ? 384 : 256, DC = KEEP_G ? 448 : 384, COLS = 512;
+    static constexpr int WIDE = MP == 128 ? 1 : DP == 64 ? 3 : 2;  // parts of one MMA
+    static constexpr uint32_t G = 0, E = KEEP_G ? 128 : 64, ZX = KEEP_G ? 128 : 0;
+    static constexpr uint32_t DX = !KEEP_G ? 128 : DP == 64 ? 320 : 256, DB = KEEP_G ? 384 : 256, DC = KEEP_G ? 448 : 384, COLS = 512;
 };
 
 struct BwdTcArgs {
@@ -184,7 +188,7 @@ __global__ void __launch_bounds__(BTH, 1)
             const int i = tid + n * BTH, m = i / (DP / 8), j = i % (DP / 8) * 8;
 #pragma unroll
             for (int k = 0; k < 3; ++k)
-                *reinterpret_cast<uint4 *>(sm + L::ST + k * L::PART + j / 64 * L::PSLAB + sw_off(m, j % 64 / 8)) = held[n][k];
+                *reinterpret_cast<uint4 *>(sm + L::ST + j / 64 * L::STS + k * L::PSLAB + sw_off(m, j % 64 / 8)) = held[n][k];
         }
     };
     // step sizes and decays of head g rep + r, by warps 4 .. 7 (warp 0 issues MMAs), into the arrays of r's
@@ -232,6 +236,38 @@ __global__ void __launch_bounds__(BTH, 1)
     }
     tc_fence_after();
     const uint32_t tm = *tslot;
+    // rows times the state's parts, K = d, by one thread
+    const auto mma_state = [&](SmemDesc rows) {
+        constexpr uint32_t id_w = idesc(128, T::WIDE * MP, 1, 1), id_m = idesc(128, MP, 1, 1);
+#pragma unroll
+        for (int part = T::WIDE > 1 ? 0 : 2; part >= 0; --part) {  // the small parts first: fewer roundings of the large sum
+            const SmemDesc dz = sw_desc(s0 + L::ST + part * L::PSLAB, 16);
+#pragma unroll
+            for (int k = 0; k < DP / 16; ++k)
+                mma_f16(tm + T::ZX, sw_step(rows, k / 4 * L::SLAB + k % 4 * 32), sw_step(dz, k / 4 * L::STS + k % 4 * 32), id_w,
+                        (T::WIDE == 1 && part < 2) || k > 0);
+        }
+        if (T::WIDE == 2) {
+            const SmemDesc dz = sw_desc(s0 + L::ST + 2 * L::PSLAB, 16);
+#pragma unroll
+            for (int k = 0; k < DP / 16; ++k)
+                mma_f16(tm + T::ZX + MP, sw_step(rows, k / 4 * L::SLAB + k % 4 * 32), sw_step(dz, k / 4 * L::STS + k % 4 * 32), id_m, 1);
+        }
+    };
+    // 16 columns of that product, with the tmem_ld16 that the caller has under way
+    const auto read_zx = [&](int m, float (&v)[16]) {
+        const uint32_t at = tm + lane_base + T::ZX + m;
+        tmem_ld16(at, v);
+        if (T::WIDE > 1) {
+            float u[16], l[16];
+            tmem_ld16(at + MP, u);
+            if (T::WIDE > 2) tmem_ld16(at + 2 * MP, l);
+            tmem_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 16; ++e) v[e] += T::WIDE > 2 ? u[e] + l[e] : u[e];
+        }
+        tmem_wait_ld();
+    };
     // 64 positions fill half the lanes: rows 64 .. 127 of the operands are whatever lies behind them in
     // shared memory, and the lanes that get them are not read
     const bool mine = row < Q;
@@ -240,6 +276,98 @@ __global__ void __launch_bounds__(BTH, 1)
     make_arrays(r0);
     read_dt(r0 + 1);
     if (r0 < r1) read_state(a.adj + ((size_t)(b * H + g * rep + r0) * a.chunks + ch) * M * d, nullptr);
+    // w, dt's gradient and the chunk's parts of the parameters', of the head before, by the warps that have
+    // the fewest rows of K to make (the last quarter's).  Their sums are read before the next ones are
+    // written, the rest runs beside the others' rows.
+    struct Sums {
+        float kc[NG], ks, zi, xi, ko, gg, ee, zx;
+    };
+    const auto read_sums = [&]() {
+        const int t = 32 * wj + lane, J = t >> 4;
+        Sums q = {};
+        if (t < Q) {
+#pragma unroll
+            for (int k = 0; k < NG; ++k) q.kc[k] = k <= J ? ksum_t[k * SQ + t] : 0.f;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                q.ks += ksum_s[k * SQ + t];
+                q.zi += zin[k * SQ + t];
+                q.xi += xin[k * SQ + t];
+            }
+            q.ko = kown[t];
+            q.gg = gs[t];
+            q.ee = es[t];
+        }
+#pragma unroll
+        for (int k = 0; k < BTH / 32; ++k) q.zx += red[k];
+        return q;
+    };
+    const auto finish = [&](int r, const Sums &q) {
+        const int h = g * rep + r, unit = b * H + h;
+        const uint32_t par = (r - r0) & 1;
+        const float *et = arr + par * 6 * SQ + 2 * SQ, *fs = et + SQ, *dl = fs + SQ;
+        const int t = 32 * wj + lane, J = t >> 4;
+        float kc[NG];
+#pragma unroll
+        for (int k = 0; k < NG; ++k) kc[k] = q.kc[k];
+        const float ks = q.ks, zi = q.zi, xi = q.xi, ko = q.ko, gg = q.gg, ee = q.ee, zx = q.zx;
+        const float delta = t < Q ? dl[t] : 0.f, f = t < Q ? fs[t] : 0.f, e2 = t < Q ? et[t] : 0.f;
+        const float rate = rates[(r - r0) & 63].hi * 0.6931471805599453f, zf = zi * f;
+        float kt = 0.f, kd = 0.f;  // K of s in earlier groups, and in mine
+#pragma unroll
+        for (int k = 0; k < NG; ++k) {
+            kt += k < J ? kc[k] : 0.f;
+            kd = k == J ? kc[k] : kd;
+        }
+        // over my group, from my position on: K from earlier groups, and inside the group the running
+        // difference; before my position: K to later groups.  Over the warp: the inter-chunk terms
+        float su = kt + (kd - delta * ko), sb = delta * ks, iu = e2 * xi, ib = delta * zf;
+        const float own_b = sb, own_ib = ib;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const float u = __shfl_down_sync(0xffffffffu, su, o), v = __shfl_up_sync(0xffffffffu, sb, o);
+            const float x = __shfl_down_sync(0xffffffffu, iu, o), y = __shfl_up_sync(0xffffffffu, ib, o);
+            if (o < 16) {
+                if ((lane & 15) + o < 16) su += u;
+                if ((lane & 15) >= o) sb += v;
+            }
+            if (lane + o < 32) iu += x;
+            if (lane >= o) ib += y;
+        }
+        if (lane == 0) wsum[wj] = iu;
+        if (lane == 31) wsum[4 + wj] = ib;
+        // sums of K per pair of groups (s in group k, t in mine)
+#pragma unroll
+        for (int o = 8; o > 0; o >>= 1)
+#pragma unroll
+            for (int k = 0; k < NG; ++k) kc[k] += __shfl_xor_sync(0xffffffffu, kc[k], o);
+        if ((lane & 15) == 0 && t < Q)
+#pragma unroll
+            for (int k = 0; k < NG; ++k) blk[k * 8 + J] = kc[k];
+        named_sync(2, 128);
+        float wt = su + (sb - own_b) + (iu + (ib - own_ib));
+#pragma unroll
+        for (int k = 0; k < 4; ++k) wt += k > wj ? wsum[k] : k < wj ? wsum[4 + k] : 0.f;
+#pragma unroll
+        for (int i = 0; i < NG - 2; ++i)  // pairs of groups around mine
+#pragma unroll
+            for (int k = i + 2; k < NG; ++k) wt += i < J && k > J ? blk[i * 8 + k] : 0.f;
+        wt = fmaf(zx, red[16 + 15 * par], wt);
+        float ga = 0.f, gb = 0.f, gd = 0.f;
+        if (t < len) {
+            // 1 / (1 + e^-z) of D = log(1 + e^z) is 1 - e^-D
+            const float ddt = (ks + ko + gg * ee + zf - rate * wt) * -expm1f(-delta);
+            static_cast<__nv_bfloat16 *>(a.ddt)[((size_t)b * N + t0 + t) * a.ldddt + h] = __float2bfloat16_rn(ddt);
+            ga = -rate * delta * wt;
+            gb = ddt;
+            gd = ee;
+        }
+        ga = warp_sum(ga);
+        gb = warp_sum(gb);
+        gd = warp_sum(gd);
+        if (lane == 0)
+            *reinterpret_cast<float4 *>(a.part + (((size_t)unit * a.chunks + ch) * 4 + wj) * 4) = make_float4(ga, gb, gd, 0.f);
+    };
     int r = r0;
     for (; r < r1; ++r) {
         const int h = g * rep + r, unit = b * H + h;
@@ -254,7 +382,7 @@ __global__ void __launch_bounds__(BTH, 1)
         if (warp == 0 && elect_one()) {
             tc_fence_after();
             const SmemDesc dxk = sw_desc(s0 + L::X, 16), dyk = sw_desc(s0 + L::DY, 16);
-            const SmemDesc db = sw_desc(s0 + L::B, 16), dc = sw_desc(s0 + L::C, 16), dz = sw_desc(s0 + L::ST, L::PSLAB);
+            const SmemDesc db = sw_desc(s0 + L::B, 16), dc = sw_desc(s0 + L::C, 16), dz = sw_desc(s0 + L::ST, L::STS);
             constexpr uint32_t id_q = idesc(128, Q, 1, 1), id_x = idesc(128, DP, 1, 1, 0, 1);
 #pragma unroll
             for (int k = 0; k < DP / 16; ++k)
@@ -271,6 +399,8 @@ __global__ void __launch_bounds__(BTH, 1)
         }
         __syncwarp();
         if (tid == 0) bulk_wait_read_all();  // dx of the last head has left P's place
+        Sums last = {};
+        if (r > r0 && q4 == 3) last = read_sums();
         ok = mbar_wait(&bar[2], par);
         if (__syncthreads_or(!ok)) break;
         tc_fence_after();
@@ -287,11 +417,12 @@ __global__ void __launch_bounds__(BTH, 1)
                 tmem_st16(tm + lane_base + T::DX + wj * CW + c, v);
             }
         }
+        if (r > r0 && q4 == 3) finish(r - 1, last);
         if (mine) {
             // K, P, R: row s, every fourth block of 16 columns t
             const float sh = Sh[row], sl = Sl[row], delta = dl[row];
             float ks = 0.f;
-#pragma unroll
+#pragma unroll 1
             for (int i = 0; i < NG / 4; ++i) {
                 const int kb = wj + 4 * i;
                 uint4 pp[2], rr[2];
@@ -306,7 +437,7 @@ __global__ void __launch_bounds__(BTH, 1)
                     tmem_wait_ld();
                     if (kb >= 2 * q4 + 2) {  // wholly behind my rows: decay to the block's start, then inside it
                         const float f = ex2((Sh[16 * kb - 1] - sh) + (Sl[16 * kb - 1] - sl));
-const ssm_f2 ff = ssm_pack(f, f), dd = ssm_pack(delta, delta);
+                        const ssm_f2 ff = ssm_pack(f, f), dd = ssm_pack(delta, delta);
                         ssm_f2 sum = 0ull;
 #pragma unroll
                         for (int e = 0; e < 16; e += 2) {
@@ -322,26 +453,29 @@ const ssm_f2 ff = ssm_pack(f, f), dd = ssm_pack(delta, delta);
                         ssm_unpack(sum, lo, hi);
                         ks += lo + hi;
                     } else {
-                        float ko = 0.f;
+                        // selects, no branches: a warp's rows take different ones (4000 cycles a block with)
+                        float ko = 0.f, go = 0.f, eo = 0.f;
 #pragma unroll
                         for (int e = 0; e < 16; ++e) {
                             const int t = 16 * kb + e;
-                            float w = t > row ? ex2((Sh[t] - sh) + (Sl[t] - sl)) : 0.f;
-                            const float k1 = t > row ? w * ev[e] * gv[e] : 0.f;
+                            const float diff = (Sh[t] - sh) + (Sl[t] - sl);
+                            const float w = ex2(t > row ? diff : -INFINITY), k0 = w * ev[e] * gv[e];
+                            const float k1 = t > row ? k0 : 0.f;
                             ko += k1;
                             kk[e] = k1 * delta;
-                            if (t == row) {
-                                gs[t] = gv[e];
-                                es[t] = ev[e];
-                                w = 1.f;
-                            }
-                            gv[e] = t > row ? gv[e] * (w * delta) : 0.f;
-                            ev[e] = t >= row ? ev[e] * (w * delta) : 0.f;
+                            go = t == row ? gv[e] : go;
+                            eo = t == row ? ev[e] : eo;
+                            const float p = gv[e] * (w * delta), q = ev[e] * ((t == row ? 1.f : w) * delta);
+                            gv[e] = t > row ? p : 0.f;
+                            ev[e] = t >= row ? q : 0.f;
                         }
-                        if (kb == row >> 4)
+                        if (kb == row >> 4) {
                             kown[row] = ko;
-                        else
+                            gs[row] = go;
+                            es[row] = eo;
+                        } else {
                             ks += ko;
+                        }
                     }
                     pp[0] = Vec16<__nv_bfloat16>::pack(gv);
                     pp[1] = Vec16<__nv_bfloat16>::pack(gv + 8);
@@ -375,19 +509,18 @@ const ssm_f2 ff = ssm_pack(f, f), dd = ssm_pack(delta, delta);
         if (warp == 0 && elect_one()) {
             tc_fence_after();
             const SmemDesc dp = sw_desc(s0 + L::P, 16), dyn = sw_desc(s0 + L::DY, L::SLAB), dxk = sw_desc(s0 + L::X, 16);
-            constexpr uint32_t id_x = idesc(128, DP, 1, 1, 0, 1), id_m = idesc(128, MP, 1, 1);
+            constexpr uint32_t id_x = idesc(128, DP, 1, 1, 0, 1), id_c = idesc(128, MP, 1, 1, 1, 1);
 #pragma unroll
             for (int k = 0; k < Q / 16; ++k)
                 mma_f16(tm + T::DX, sw_step(dp, k / 4 * L::SLAB + k % 4 * 32), sw_step(dyn, k * 2048), id_x, 1);
-#pragma unroll
-            for (int part = 2; part >= 0; --part) {  // the small parts first: fewer roundings of the large sum
-                const SmemDesc dz = sw_desc(s0 + L::ST + part * L::PART, 16);
-#pragma unroll
-                for (int k = 0; k < DP / 16; ++k)
-                    mma_f16(tm + T::DBI, sw_step(dxk, k / 4 * L::SLAB + k % 4 * 32),
-                            sw_step(dz, k / 4 * L::PSLAB + k % 4 * 32), id_m, part < 2 || k > 0);
-            }
+            mma_state(dxk);
             mma_commit(&bar[3]);
+            // R^T b into dc, beside what is done with the products before it
+            const SmemDesc drt = sw_desc(s0 + L::R, Q == 64 ? 0 : L::SLAB);  // 64 positions: rows 64.. repeat them
+            const SmemDesc dbn = sw_desc(s0 + L::B, L::SLAB);
+#pragma unroll
+            for (int k = 0; k < Q / 16; ++k)
+                mma_f16(tm + T::DC, sw_step(drt, k * 2048), sw_step(dbn, k * 2048), id_c, r > r0 || k > 0);
         }
         __syncwarp();
         const float cross = warp_sum(read_state(a.state0 + so, a.adj + so));
@@ -422,9 +555,8 @@ const ssm_f2 ff = ssm_pack(f, f), dd = ssm_pack(delta, delta);
             for (int c = 0; c < MW; c += 16) {
                 const int m = MW * wj + c;
                 float v[16], u[16], w[16];
-                tmem_ld16(tm + lane_base + T::DBI + m, v);
                 if (r > r0) tmem_ld16(tm + lane_base + T::DB + m, w);
-                tmem_wait_ld();
+                read_zx(m, v);
                 const unsigned char *pb = sm + L::B + m / 64 * L::SLAB;
                 Vec16<__nv_bfloat16>::unpack(*reinterpret_cast<const uint4 *>(pb + sw_off(row, m % 64 / 8)), u);
                 Vec16<__nv_bfloat16>::unpack(*reinterpret_cast<const uint4 *>(pb + sw_off(row, m % 64 / 8 + 1)), u + 8);
@@ -444,23 +576,12 @@ const ssm_f2 ff = ssm_pack(f, f), dd = ssm_pack(delta, delta);
         if (warp == 0 && elect_one()) {
             tc_fence_after();
             const SmemDesc dyk = sw_desc(s0 + L::DY, 16), dr = sw_desc(s0 + L::R, 16);
-            const SmemDesc drt = sw_desc(s0 + L::R, Q == 64 ? 0 : L::SLAB);  // 64 positions: rows 64.. repeat them
-            const SmemDesc dbn = sw_desc(s0 + L::B, L::SLAB), dcn = sw_desc(s0 + L::C, L::SLAB);
-            constexpr uint32_t id_m = idesc(128, MP, 1, 1), id_b = idesc(128, MP, 1, 1, 0, 1), id_c = idesc(128, MP, 1, 1, 1, 1);
-#pragma unroll
-            for (int part = 2; part >= 0; --part) {
-                const SmemDesc dz = sw_desc(s0 + L::ST + part * L::PART, 16);
-#pragma unroll
-                for (int k = 0; k < DP / 16; ++k)
-                    mma_f16(tm + T::DCI, sw_step(dyk, k / 4 * L::SLAB + k % 4 * 32),
-                            sw_step(dz, k / 4 * L::PSLAB + k % 4 * 32), id_m, part < 2 || k > 0);
-            }
+            const SmemDesc dcn = sw_desc(s0 + L::C, L::SLAB);
+            constexpr uint32_t id_b = idesc(128, MP, 1, 1, 0, 1);
+            mma_state(dyk);
 #pragma unroll
             for (int k = 0; k < Q / 16; ++k)
                 mma_f16(tm + T::DB, sw_step(dr, k / 4 * L::SLAB + k % 4 * 32), sw_step(dcn, k * 2048), id_b, 1);
-#pragma unroll
-            for (int k = 0; k < Q / 16; ++k)
-                mma_f16(tm + T::DC, sw_step(drt, k * 2048), sw_step(dbn, k * 2048), id_c, r > r0 || k > 0);
             mma_commit(&bar[4]);
         }
         __syncwarp();
@@ -486,9 +607,8 @@ const ssm_f2 ff = ssm_pack(f, f), dd = ssm_pack(delta, delta);
             for (int c = 0; c < MW; c += 16) {
                 const int m = MW * wj + c;
                 float v[16], u[16], w[16];
-                tmem_ld16(tm + lane_base + T::DCI + m, v);
                 tmem_ld16(tm + lane_base + T::DC + m, w);
-                tmem_wait_ld();
+                read_zx(m, v);
                 const unsigned char *pc = sm + L::C + m / 64 * L::SLAB;
                 Vec16<__nv_bfloat16>::unpack(*reinterpret_cast<const uint4 *>(pc + sw_off(row, m % 64 / 8)), u);
                 Vec16<__nv_bfloat16>::unpack(*reinterpret_cast<const uint4 *>(pc + sw_off(row, m % 64 / 8 + 1)), u + 8);
@@ -503,88 +623,10 @@ const ssm_f2 ff = ssm_pack(f, f), dd = ssm_pack(delta, delta);
         }
         tmem_wait_st();
         tc_fence_before();
+    }
+    if (r == r1 && r > r0) {
         __syncthreads();
-        // w, dt's gradient and the chunk's parts of the parameters', by the last four warps
-        if (tid >= BTH - SQ) {
-            const int t = tid - (BTH - SQ), J = t >> 4, wq = t >> 5;
-            float kc[NG], ks = 0.f, zi = 0.f, xi = 0.f, ko = 0.f, gg = 0.f, ee = 0.f, delta = 0.f, f = 0.f, e2 = 0.f;
-#pragma unroll
-            for (int k = 0; k < NG; ++k) kc[k] = 0.f;
-            if (t < Q) {
-#pragma unroll
-                for (int k = 0; k < NG; ++k) kc[k] = k <= J ? ksum_t[k * SQ + t] : 0.f;
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    ks += ksum_s[k * SQ + t];
-                    zi += zin[k * SQ + t];
-                    xi += xin[k * SQ + t];
-                }
-                ko = kown[t];
-                gg = gs[t];
-                ee = es[t];
-                delta = dl[t];
-                f = fs[t];
-                e2 = et[t];
-            }
-            const float rate = rates[(r - r0) & 63].hi * 0.6931471805599453f, zf = zi * f;
-            float kt = 0.f, kd = 0.f;  // K of s in earlier groups, and in mine
-#pragma unroll
-            for (int k = 0; k < NG; ++k) {
-                kt += k < J ? kc[k] : 0.f;
-                kd = k == J ? kc[k] : kd;
-            }
-            // over my group, from my position on: K from earlier groups, and inside the group the running
-            // difference; before my position: K to later groups.  Over the warp: the inter-chunk terms
-            float su = kt + (kd - delta * ko), sb = delta * ks, iu = e2 * xi, ib = delta * zf;
-            const float own_b = sb, own_ib = ib;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const float u = __shfl_down_sync(0xffffffffu, su, o), v = __shfl_up_sync(0xffffffffu, sb, o);
-                const float x = __shfl_down_sync(0xffffffffu, iu, o), y = __shfl_up_sync(0xffffffffu, ib, o);
-                if (o < 16) {
-                    if ((lane & 15) + o < 16) su += u;
-                    if ((lane & 15) >= o) sb += v;
-                }
-                if (lane + o < 32) iu += x;
-                if (lane >= o) ib += y;
-            }
-            if (lane == 0) wsum[wq] = iu;
-            if (lane == 31) wsum[4 + wq] = ib;
-            // sums of K per pair of groups (s in group k, t in mine)
-#pragma unroll
-            for (int o = 8; o > 0; o >>= 1)
-#pragma unroll
-                for (int k = 0; k < NG; ++k) kc[k] += __shfl_xor_sync(0xffffffffu, kc[k], o);
-            if ((lane & 15) == 0 && t < Q)
-#pragma unroll
-                for (int k = 0; k < NG; ++k) blk[k * 8 + J] = kc[k];
-            named_sync(2, 128);
-            float wt = su + (sb - own_b) + (iu + (ib - own_ib));
-#pragma unroll
-            for (int k = 0; k < 4; ++k) wt += k > wq ? wsum[k] : k < wq ? wsum[4 + k] : 0.f;
-#pragma unroll
-            for (int i = 0; i < NG - 2; ++i)  // pairs of groups around mine
-#pragma unroll
-                for (int k = i + 2; k < NG; ++k) wt += i < J && k > J ? blk[i * 8 + k] : 0.f;
-            float zx = 0.f;
-#pragma unroll
-            for (int k = 0; k < BTH / 32; ++k) zx += red[k];
-            wt = fmaf(zx, red[16 + 15 * par], wt);
-            float ga = 0.f, gb = 0.f, gd = 0.f;
-            if (t < len) {
-                // 1 / (1 + e^-z) of D = log(1 + e^z) is 1 - e^-D
-                const float ddt = (ks + ko + gg * ee + zf - rate * wt) * -expm1f(-delta);
-                static_cast<__nv_bfloat16 *>(a.ddt)[((size_t)b * N + t0 + t) * a.ldddt + h] = __float2bfloat16_rn(ddt);
-                ga = -rate * delta * wt;
-                gb = ddt;
-                gd = ee;
-            }
-            ga = warp_sum(ga);
-            gb = warp_sum(gb);
-            gd = warp_sum(gd);
-            if (lane == 0)
-                *reinterpret_cast<float4 *>(a.part + (((size_t)unit * a.chunks + ch) * 4 + wq) * 4) = make_float4(ga, gb, gd, 0.f);
-        }
+        if (q4 == 3) finish(r - 1, read_sums());
     }
     if (r < r1) {  // a wait ran out
         if (tid == 0) {
