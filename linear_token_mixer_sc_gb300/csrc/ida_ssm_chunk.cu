@@ -574,7 +574,6 @@ __global__ void __launch_bounds__(STH, MP == 64 ? 2 : 1)
     const uint32_t s0 = smem_u32(sm);
     uint64_t *bar = reinterpret_cast<uint64_t *>(sm + L::MISC);  // 0, 1 copies, 2, 3 MMAs, of each buffer
     uint32_t *tslot = reinterpret_cast<uint32_t *>(sm + L::MISC + 48);
-    Rate2 *rate_s = reinterpret_cast<Rate2 *>(sm + L::MISC + 56);
     float *arrays = reinterpret_cast<float *>(sm + L::ARR);
     long long *tot = reinterpret_cast<long long *>(sm + L::TOT);
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
@@ -594,8 +593,9 @@ __global__ void __launch_bounds__(STH, MP == 64 ? 2 : 1)
     const int seg = id % groups;
     id /= groups;
     const int j0 = id % slices * DP, unit = id / slices, b = unit / H, h = unit % H, g = h / (H / a.G);
-    // positions of the CTA, and of a chunk of it
-    const int len = EACH ? a.seg * per : a.seg / a.fine, step = EACH ? a.seg : SQ;
+    // positions of a chunk (the gradients' chunks have 64 where M > 64), and of the CTA
+    constexpr int step = EACH && MP == 128 ? 64 : SQ;
+    const int len = EACH ? step * per : a.seg / a.fine;
     const int t_begin = seg * len, t_end = min(N, t_begin + len);
     const int nch = t_end > t_begin ? (t_end - t_begin + step - 1) / step : 0;
     const __nv_bfloat16 *gdt = static_cast<const __nv_bfloat16 *>(a.dt) + (size_t)b * N * a.lddt + h;
@@ -618,7 +618,7 @@ __global__ void __launch_bounds__(STH, MP == 64 ? 2 : 1)
     const auto start_of = [&](int n) { return t_begin + (EACH ? n : nch - 1 - n) * step; };  // the n-th chunk walked
     const auto fetch = [&](int n) {  // one thread
         const int buf = n % L::NB, t0 = start_of(n);
-        mbar_arrive_expect_tx(&bar[buf], (uint32_t)SSLAB * (DP / 64 + MP / 64));
+        mbar_arrive_expect_tx(&bar[buf], (uint32_t)(step * 128 * (DP / 64 + MP / 64)));
 #pragma unroll
         for (int i = 0; i < MP / 64; ++i)
             tma_load_4d(sm + L::B + buf * L::BB + i * SSLAB, &tm_b, 64 * i, g, t0, b, &bar[buf]);
@@ -632,16 +632,14 @@ __global__ void __launch_bounds__(STH, MP == 64 ? 2 : 1)
         if (k >= 0) dt_next = n < nch && k < step && p < t_end ? __bfloat162float(gdt[(size_t)p * a.lddt]) : 0.f;
     };
     fetch_dt(0);
+    Rate2 rate = {};
+    if (tid >= SQ) rate = rate2_of(a.a_log[h]);
     __syncthreads();
     // the launches behind may take their places now: not before, a CTA of theirs that got this SM's TMEM
     // ahead of this one would wait for this one
     dependent_launch();
     if (tid == 0)
         for (int n = 0; n < L::NB && n < nch; ++n) fetch(n);
-    if (warp == 4) {
-        const Rate2 r = rate2_of(a.a_log[h]);
-        if (lane == 0) *rate_s = r;
-    }
     tc_fence_after();
     const uint32_t tm = *tslot;
     long long behind = 0;  // log2 a summed over the chunks done, in warps 4 .. 7
@@ -651,7 +649,7 @@ __global__ void __launch_bounds__(STH, MP == 64 ? 2 : 1)
         const bool in = k < step && start_of(n) + k < t_end;
         const float delta = in ? softplus(dt_next + dt_bias) : 0.f;
         long long all;
-        const long long fx = chunk_sum(*rate_s, delta, k, tot, all);
+        const long long fx = chunk_sum(rate, delta, k, tot, all);
         if (MODE == kAdjoint)
             arrays[(n & 1) * SQ + k] = in ? ex2_fix(fx) : 0.f;
         else
@@ -661,11 +659,12 @@ __global__ void __launch_bounds__(STH, MP == 64 ? 2 : 1)
     };
     // the accumulator of chunk n (of the whole part) to memory
     const auto write_out = [&](int n, float *out, const float *in, float f) {
-        if (DP == 64 && tl >= DP) return;
-        constexpr int MH = MP / 2;
+        // with DP = 64 lanes 64.. repeat 0..63 and take half of their columns
+        constexpr int MH = DP == 64 ? MP / 4 : MP / 2;
+        const int part = DP == 64 ? 2 * half + (q4 >> 1) : half, j = DP == 64 ? tl & 63 : tl;
 #pragma unroll
         for (int blk = 0; blk < MH / 16; ++blk) {
-            const int m0 = half * MH + 16 * blk;
+            const int m0 = part * MH + 16 * blk;
             float v[16];
             const uint32_t at = tm + lane_base + (EACH && (n & 1) ? ACC : 0) + m0;
             tmem_ld16(at, v);
@@ -681,17 +680,16 @@ __global__ void __launch_bounds__(STH, MP == 64 ? 2 : 1)
             if (nch == 0)
 #pragma unroll
                 for (int e = 0; e < 16; ++e) v[e] = 0.f;
-            if (j0 + tl < d)
+            if (j0 + j < d)
 #pragma unroll
                 for (int e = 0; e < 16; ++e)
                     if (m0 + e < M) {
-                        const size_t at = (size_t)(m0 + e) * d + j0 + tl;
+                        const size_t at = (size_t)(m0 + e) * d + j0 + j;
                         out[at] = in ? fmaf(f, __ldg(in + at), v[e]) : v[e];
                     }
         }
     };
     const auto each_out = [&](int n) { return a.seg_state + ((size_t)unit * parts + seg * per + n) * M * d; };
-    named_sync(2, STH);  // the rate
     if (nch > 0) make_weights(0);  // the last segment may have parts without a position
     fetch_dt(1);
     bool ok = true;
@@ -741,11 +739,11 @@ __global__ void __launch_bounds__(STH, MP == 64 ? 2 : 1)
             const uint32_t acc = tm + (EACH && (n & 1) ? ACC : 0);
             constexpr uint32_t id_w = idesc(128, ACC, 1, 1, 1, 1), id_l = idesc(128, MP, 1, 1, 1, 1);
 #pragma unroll
-            for (int k = 0; k < SQ / 16; ++k)
+            for (int k = 0; k < step / 16; ++k)
                 mma_f16(acc, sw_step(da, k * 2048), sw_step(dh, k * 2048), id_w, (!EACH && n > 0) || k > 0);
             if (WIDE < PARTS)  // the low part joins the middle one
 #pragma unroll
-                for (int k = 0; k < SQ / 16; ++k)
+                for (int k = 0; k < step / 16; ++k)
                     mma_f16(acc + MP, sw_step(da, k * 2048), sw_step(dl, k * 2048), id_l, 1);
             mma_commit(&bar[2 + buf]);
         }
@@ -898,8 +896,9 @@ static ida_status launch_states(const ScanArgs &a, cudaStream_t st) {
     constexpr int smem = SsmStateSmem<DP, MP, PARTS>::TOTAL;
     static_assert(smem <= (MP == 64 ? 113 : 227) * 1024, "shared memory budget");
     CUtensorMap mx, mb;
-    ida_status s = ssm_map(&mx, a.x, a.B, a.N, a.H, a.d, a.ldx);
-    if (s == IDA_OK) s = ssm_map(&mb, a.b, a.B, a.N, a.G, a.M, a.ldb);
+    constexpr int step = MODE != kPart && MP == 128 ? 64 : SQ;
+    ida_status s = ssm_map(&mx, a.x, a.B, a.N, a.H, a.d, a.ldx, step);
+    if (s == IDA_OK) s = ssm_map(&mb, a.b, a.B, a.N, a.G, a.M, a.ldb, step);
     if (s != IDA_OK) return s;
     const auto kernel = ssm_state_kernel<DP, MP, PARTS, MODE>;
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
