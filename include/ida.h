@@ -393,7 +393,9 @@ IDA_API ida_status ida_rope(void *q, void *k, int B, int N, int H, int R,
  * Supported: d a multiple of 8 up to 256, M a multiple of 8 up to 128, G dividing H, W <= 4,
  * B*H <= 2^24, B*N <= 2^28.  States, sums and gradients of parameters are fp32 for both
  * dtypes.  Non-finite inputs make the outputs of their own row and head (the row and group's
- * heads for b and c) unspecified, earlier positions included; no others.
+ * heads for b and c) unspecified, earlier positions included, and the gradients that sum over
+ * them (of parameters; of the group's b and c); no others.  Outputs that share elements with
+ * inputs are refused; slices of the same wider rows need not.
  */
 
 /*

@@ -666,6 +666,16 @@ ida_status ida_ssm_scan_backward(const void *x, const void *b, const void *c, co
                 return fail_with(IDA_ERR_ARG, "dt and ddt must be aligned pointers");
         if (workspace_bytes < ida_ssm_scan_backward_workspace_bytes(B, H, N, d, G, M, dtype))
             return fail_with(IDA_ERR_ARG, "workspace is smaller than ida_ssm_scan_backward_workspace_bytes");
+        const struct {
+            const void *p;
+            long long ld, w;
+        } rows[] = {{dx, lddx, (long long)H * d}, {db, lddb, (long long)G * M}, {dc, lddc, (long long)G * M}, {ddt, ldddt, H},
+                    {x, ldx, (long long)H * d}, {b, ldb, (long long)G * M}, {c, ldc, (long long)G * M}, {dt, lddt, H},
+                    {dy, (long long)H * d, (long long)H * d}};
+        for (int i = 0; i < 4; ++i)
+            for (int k = i + 1; k < 9; ++k)
+                if (rows_overlap(rows[i].p, rows[i].ld, rows[i].w, rows[k].p, rows[k].ld, rows[k].w, (long long)B * N, dtype))
+                    return fail_with(IDA_ERR_ARG, "the gradients must not overlap one another or the inputs");
     }
     int num_sms = 0;
     std::string why;

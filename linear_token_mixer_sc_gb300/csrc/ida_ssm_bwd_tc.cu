@@ -28,6 +28,12 @@
 // by recursive halving), then the MMAs of dx, the inter-chunk products (read back, scaled by
 // 2^S or f and added into db and dc) and the rest of db and dc.
 //
+// What bounds it: the stages of a head follow one another between block barriers (one CTA of 16 warps an
+// SM: its registers and 175 KB are taken), at 0.34 instructions a cycle and scheduler; tensor pipe 12 %,
+// HBM 15 %.  8 x 2048 positions of 12 heads of 64 x 64: 152 us, 98 of them this kernel's (8 us a head and
+// chunk), 45 the chunk states' and 14 their running sums'.  (The MMAs issued by a 17th warp: 189 us, its
+// threads' share of the registers spills the others'.)
+//
 // Waits are bounded as in ida_ssm_chunk.cu.
 #include "ida_ssm_tc.cuh"
 
@@ -65,8 +71,7 @@ struct BwdSmem {
 // Columns.  With M <= 64 G stays for all heads and the inter-chunk products take E's place; with
 // 64 positions and M > 64 they take G's and E's, and G is made again for every head.  Parts of a state
 // side by side in shared memory are one MMA's columns, where there is room: all three, or the high and
-// the middle one, which the low one then joins.  An MMA takes as long with 64 columns as with 192
-// (162 us for the three one after the other).
+// the middle one, which the low one then joins: 12 and 20 MMAs issued a head instead of 20 and 28.
 template <int Q, int DP, int MP>
 struct BwdTmem {
     static constexpr bool KEEP_G = MP == 64;
@@ -453,7 +458,8 @@ __global__ void __launch_bounds__(BTH, 1)
                         ssm_unpack(sum, lo, hi);
                         ks += lo + hi;
                     } else {
-                        // selects, no branches: a warp's rows take different ones (4000 cycles a block with)
+                        // selects, no branches: a warp's rows take different ones (K, P and R of a head took 5400
+                        // cycles with them, 4600 without)
                         float ko = 0.f, go = 0.f, eo = 0.f;
 #pragma unroll
                         for (int e = 0; e < 16; ++e) {
@@ -673,8 +679,8 @@ __global__ void __launch_bounds__(BTH, 1)
 
 // ---- host side ---------------------------------------------------------------------------
 
-// CTAs that share a group's heads: the fewest passes over the SMs, a head and chunk taking about 4 us
-// and a CTA's start 4 more; the partial rows of a shared group cost their traffic at about 5 TB/s.
+// CTAs that share a group's heads: the fewest passes over the SMs, a head and chunk taking about 7.5 us
+// and a CTA's start 6 more; the partial rows of a shared group cost their traffic at about 5 TB/s.
 int ssm_bwd_tc_chunk(int M) { return M <= 64 ? 128 : 64; }
 int ssm_bwd_tc_splits(int B, int H, int N, int G, int M) {
     const int rep = H / G, q = ssm_bwd_tc_chunk(M);
@@ -684,7 +690,7 @@ int ssm_bwd_tc_splits(int B, int H, int N, int G, int M) {
     for (int s = 1; s <= rep; ++s) {
         const int per = (rep + s - 1) / s;
         if ((rep + per - 1) / per != s) continue;  // some CTA would have no head
-        const double c = (double)((base * s + 151) / 152) * (4.0 * per + 4.0) +
+        const double c = (double)((base * s + 151) / 152) * (7.5 * per + 6.0) +
                          (s > 1 ? 5.0 + 16.0 * (double)B * N * G * s * M / 5e6 : 0.0);
         if (s == 1 || c < cost) {
             best = s;

@@ -365,6 +365,7 @@ ida_status ida_ssm_conv(const void *x, const float *conv_w, const float *conv_b,
             if (!p) return fail_with(IDA_ERR_ARG, "null input or output pointer");
             if (misaligned16(p)) return fail_with(IDA_ERR_ARG, "pointers must be 16-byte aligned");
         }
+        if (rows_overlap(x, ldx, C, out, C, C, (long long)B * N, dtype)) return fail_with(IDA_ERR_ARG, "out must not overlap x");
     }
     int num_sms = 0;
     std::string why;
@@ -433,6 +434,9 @@ ida_status ida_ssm_conv_backward(const void *x, const void *dout, const float *c
         }
         if (workspace_bytes < ida_ssm_conv_backward_workspace_bytes(B, N, C, W))
             return fail_with(IDA_ERR_ARG, "workspace is smaller than ida_ssm_conv_backward_workspace_bytes");
+        const long long n = (long long)B * N;
+        if (rows_overlap(x, ldx, C, dx, lddx, C, n, dtype) || rows_overlap(dout, C, C, dx, lddx, C, n, dtype))
+            return fail_with(IDA_ERR_ARG, "dx must not overlap x or dout");
     }
     int num_sms = 0;
     std::string why;

@@ -329,6 +329,10 @@ ida_status ida_ssm_scan(const void *x, const void *b, const void *c, const void 
         }
         if (!dt || (reinterpret_cast<uintptr_t>(dt) % (dtype == IDA_F32 ? 4 : 2)))
             return fail_with(IDA_ERR_ARG, "dt must be an aligned pointer");
+        const long long n = (long long)B * N, w = (long long)H * d, bc = (long long)G * M;
+        if (rows_overlap(y, w, w, x, ldx, w, n, dtype) || rows_overlap(y, w, w, b, ldb, bc, n, dtype) ||
+            rows_overlap(y, w, w, c, ldc, bc, n, dtype) || rows_overlap(y, w, w, dt, lddt, H, n, dtype))
+            return fail_with(IDA_ERR_ARG, "y must not overlap x, b, c or dt");
     }
     int num_sms = 0;
     std::string why;

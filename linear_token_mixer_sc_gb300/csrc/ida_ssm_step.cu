@@ -190,6 +190,9 @@ extern "C" ida_status ida_ssm_step(const void *xbc, const void *dt, const float 
         return fail_with(IDA_ERR_ARG, "dt must be an aligned pointer");
     if (W > 1 && (!conv_state || misaligned16(conv_state)))
         return fail_with(IDA_ERR_ARG, "conv_state must be a 16-byte aligned pointer");
+    if (rows_overlap(xbc, ldx, C, y, (long long)H * d, (long long)H * d, B, dtype) ||
+        rows_overlap(dt, lddt, H, y, (long long)H * d, (long long)H * d, B, dtype))
+        return fail_with(IDA_ERR_ARG, "y must not overlap xbc or dt");
     int num_sms = 0;
     std::string why;
     s = device_ready(&num_sms, why);

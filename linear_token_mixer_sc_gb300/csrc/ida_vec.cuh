@@ -24,7 +24,6 @@ struct Vec16<float> {
     static __device__ __forceinline__ uint4 pack(const float *x) {
         return make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3]));
     }
-    static __device__ __forceinline__ float round(float x) { return x; }
 };
 
 template <>
@@ -47,7 +46,6 @@ struct Vec16<__nv_bfloat16> {
         }
         return make_uint4(w[0], w[1], w[2], w[3]);
     }
-    static __device__ __forceinline__ float round(float x) { return __bfloat162float(__float2bfloat16_rn(x)); }
 };
 
 __device__ __forceinline__ float to_float(float x) { return x; }
@@ -74,6 +72,16 @@ inline bool misaligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p)
 inline bool overlap(const void *a, size_t na, const void *b, size_t nb) {
     const char *pa = static_cast<const char *>(a), *pb = static_cast<const char *>(b);
     return a && b && pa < pb + nb && pb < pa + na;
+}
+// Whether rows of wa elements, lda apart, share any with rows of wb, ldb apart (slices of the same wider
+// rows do not).
+inline bool rows_overlap(const void *a, long long lda, long long wa, const void *b, long long ldb, long long wb,
+                         long long rows, int dtype) {
+    const long long es = dtype == IDA_F32 ? 4 : 2;
+    if (rows < 1 || !overlap(a, ((rows - 1) * lda + wa) * es, b, ((rows - 1) * ldb + wb) * es)) return false;
+    const long long by = static_cast<const char *>(b) - static_cast<const char *>(a), ld = lda * es;
+    const long long off = (by % ld + ld) % ld;
+    return lda != ldb || off < wa * es || off + wb * es > ld;
 }
 
 // Device set-up of a call whose own arguments have been checked: the number of SMs, and any

@@ -105,6 +105,23 @@ def test_scan_backward_refusals(lib):
         assert binding.ida_ssm_scan_workspace_bytes(1, 4, 4096, 64, 2, 16, 1) == 0
 
 
+def test_outputs_over_inputs_are_refused(lib):
+    b = _Bufs()
+    at = lambda off: ctypes.c_void_p(b.p.value + off)
+    assert _conv(lib, b)() == ARG and "overlap" in binding.ida_last_error()
+    assert _conv(lib, b)(out=at(2 * 32 * 9)) == ARG  # x's last row
+    for off in (0, 2 * 256 * 8, 2 * 256 * 9 - 16):
+        assert _scan(lib, b)(y=at(off)) == ARG and "overlap" in binding.ida_last_error(), off
+    far = at(1 << 24)
+    assert _scan(lib, b)(x=far, y=at(-2 * 256 * 8)) == ARG and "overlap" in binding.ida_last_error()  # y's last row on b, c, dt
+    names = "x dout w bias dx dw db B N C ldx lddx dtype W ws n stream".split()
+    back = _caller(lib.ida_ssm_conv_backward, names, dict(x=b.p, dout=far, w=b.p, bias=b.p, dx=b.p, dw=b.p, db=b.p,
+                                                          B=2, N=5, C=32, ldx=96, lddx=96, dtype=1, W=4, ws=b.p,
+                                                          n=1 << 30, stream=None))
+    for kw in (dict(), dict(dx=far), dict(dx=at(48)), dict(dx=at(2 * 80)), dict(dx=at(2 * 48), lddx=64)):
+        assert back(**kw) == ARG and "overlap" in binding.ida_last_error(), kw
+
+
 def test_step_refusals(lib):
     b = _Bufs()
     names = "xbc dt w cb a bias D tail X y B H d G M ldx lddt dtype W stream".split()

@@ -454,6 +454,20 @@ def test_on_another_stream(name):
         assert torch.equal(a, b)
 
 
+def test_gradients_beside_the_inputs_in_the_same_rows():
+    B, N, H, d, G, M = 2, 150, 4, 32, 2, 16
+    C = H * d + 2 * G * M
+    p = sc.cuda(sc.params(H, C, 4, 3))
+    wide = torch.zeros(B, N, 2 * C, dtype=torch.bfloat16, device="cuda")
+    wide[..., :C] = torch.randn(B, N, C, generator=sc.gen(5)).cuda()
+    dout = torch.randn(B, N, C, generator=sc.gen(6)).bfloat16().cuda()
+    want = binding.ida_ssm_conv_backward(wide[..., :C], dout, p["conv_w"], p["conv_b"])
+    before = wide[..., :C].clone()
+    got = binding.ida_ssm_conv_backward(wide[..., :C], dout, p["conv_w"], p["conv_b"], dx=wide[..., C:])
+    assert torch.equal(got["x"], want["x"]) and torch.equal(wide[..., C:], want["x"])
+    assert torch.equal(wide[..., :C], before) and torch.equal(got["conv_w"], want["conv_w"])
+
+
 def test_outputs_stay_inside_their_rows():
     """Guard bands around y, the final state and the outputs of the step and the convolution."""
     B, N, H, d, G, M, W = 1, 131, 2, 72, 1, 40, 4
