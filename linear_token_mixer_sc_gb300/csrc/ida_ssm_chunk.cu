@@ -426,7 +426,7 @@ __global__ void __launch_bounds__(CTH, 1)
             // row tl, columns 64 half ..: blocks of 16 up to the one that row tl ends in, two at a time
             const uint32_t at = tm + lane_base + TG + 128 * c + 64 * half;
             const float ct = A.cumf[tl];
-#pragma unroll
+#pragma unroll 1
             for (int k2 = 0; k2 < 4; k2 += 2) {
                 float v[2][16];
                 const int kb2 = 4 * half + k2;  // even, as the last block of a row's pair is odd
@@ -495,7 +495,7 @@ __global__ void __launch_bounds__(CTH, 1)
             const uint32_t at = tm + lane_base + TY;
             const float f = A.et[tl];
             const ssm_f2 ff = ssm_pack(f, f);
-#pragma unroll
+#pragma unroll 1
             for (int j = 0; j < DP; j += 32) {
                 float v[32];
                 tmem_ld16(at + j, v);
@@ -521,7 +521,7 @@ __global__ void __launch_bounds__(CTH, 1)
             }
             tc_fence_after();
             unsigned char *out = sm + L::OUT;
-#pragma unroll
+#pragma unroll 1
             for (int j = 0; j < DP; j += 32) {
                 float v[32];
                 tmem_ld16(at + j, v);
