@@ -247,14 +247,14 @@ __global__ void __launch_bounds__(BTH, 1)
 #pragma unroll
         for (int part = T::WIDE > 1 ? 0 : 2; part >= 0; --part) {  // the small parts first: fewer roundings of the large sum
             const SmemDesc dz = sw_desc(s0 + L::ST + part * L::PSLAB, 16);
-#pragma unroll
+#pragma unroll 2
             for (int k = 0; k < DP / 16; ++k)
                 mma_f16(tm + T::ZX, sw_step(rows, k / 4 * L::SLAB + k % 4 * 32), sw_step(dz, k / 4 * L::STS + k % 4 * 32), id_w,
                         (T::WIDE == 1 && part < 2) || k > 0);
         }
         if (T::WIDE == 2) {
             const SmemDesc dz = sw_desc(s0 + L::ST + 2 * L::PSLAB, 16);
-#pragma unroll
+#pragma unroll 2
             for (int k = 0; k < DP / 16; ++k)
                 mma_f16(tm + T::ZX + MP, sw_step(rows, k / 4 * L::SLAB + k % 4 * 32), sw_step(dz, k / 4 * L::STS + k % 4 * 32), id_m, 1);
         }
@@ -389,15 +389,15 @@ __global__ void __launch_bounds__(BTH, 1)
             const SmemDesc dxk = sw_desc(s0 + L::X, 16), dyk = sw_desc(s0 + L::DY, 16);
             const SmemDesc db = sw_desc(s0 + L::B, 16), dc = sw_desc(s0 + L::C, 16), dz = sw_desc(s0 + L::ST, L::STS);
             constexpr uint32_t id_q = idesc(128, Q, 1, 1), id_x = idesc(128, DP, 1, 1, 0, 1);
-#pragma unroll
+#pragma unroll 2
             for (int k = 0; k < DP / 16; ++k)
                 mma_f16(tm + T::E, sw_step(dxk, k / 4 * L::SLAB + k % 4 * 32), sw_step(dyk, k / 4 * L::SLAB + k % 4 * 32), id_q, k > 0);
             if (r == r0 || !T::KEEP_G)
-#pragma unroll
+#pragma unroll 2
                 for (int k = 0; k < MP / 16; ++k)
                     mma_f16(tm + T::G, sw_step(db, k / 4 * L::SLAB + k % 4 * 32), sw_step(dc, k / 4 * L::SLAB + k % 4 * 32), id_q, k > 0);
             // Z^T b: Z's high part [K = m][j] as an MN-major B
-#pragma unroll
+#pragma unroll 2
             for (int k = 0; k < MP / 16; ++k)
                 mma_f16(tm + T::DX, sw_step(db, k / 4 * L::SLAB + k % 4 * 32), sw_step(dz, k * 2048), id_x, k > 0);
             mma_commit(&bar[2]);
@@ -516,7 +516,7 @@ __global__ void __launch_bounds__(BTH, 1)
             tc_fence_after();
             const SmemDesc dp = sw_desc(s0 + L::P, 16), dyn = sw_desc(s0 + L::DY, L::SLAB), dxk = sw_desc(s0 + L::X, 16);
             constexpr uint32_t id_x = idesc(128, DP, 1, 1, 0, 1), id_c = idesc(128, MP, 1, 1, 1, 1);
-#pragma unroll
+#pragma unroll 2
             for (int k = 0; k < Q / 16; ++k)
                 mma_f16(tm + T::DX, sw_step(dp, k / 4 * L::SLAB + k % 4 * 32), sw_step(dyn, k * 2048), id_x, 1);
             mma_state(dxk);
@@ -524,7 +524,7 @@ __global__ void __launch_bounds__(BTH, 1)
             // R^T b into dc, beside what is done with the products before it
             const SmemDesc drt = sw_desc(s0 + L::R, Q == 64 ? 0 : L::SLAB);  // 64 positions: rows 64.. repeat them
             const SmemDesc dbn = sw_desc(s0 + L::B, L::SLAB);
-#pragma unroll
+#pragma unroll 2
             for (int k = 0; k < Q / 16; ++k)
                 mma_f16(tm + T::DC, sw_step(drt, k * 2048), sw_step(dbn, k * 2048), id_c, r > r0 || k > 0);
         }
@@ -585,7 +585,7 @@ __global__ void __launch_bounds__(BTH, 1)
             const SmemDesc dcn = sw_desc(s0 + L::C, L::SLAB);
             constexpr uint32_t id_b = idesc(128, MP, 1, 1, 0, 1);
             mma_state(dyk);
-#pragma unroll
+#pragma unroll 2
             for (int k = 0; k < Q / 16; ++k)
                 mma_f16(tm + T::DB, sw_step(dr, k / 4 * L::SLAB + k % 4 * 32), sw_step(dcn, k * 2048), id_b, 1);
             mma_commit(&bar[4]);

@@ -364,7 +364,7 @@ __global__ void __launch_bounds__(CTH, 1)
             const float *p = a.segs > 1 ? a.seg_state + ((size_t)unit * a.segs + seg) * a.fine * M * d
                                         : (a.state_in ? a.state_in + (size_t)unit * M * d : nullptr);
             const bool mine = p && j0 + ch < d;
-#pragma unroll
+#pragma unroll 1
             for (int m0 = 0; m0 < MP; m0 += 16) {
                 float v[16];
 #pragma unroll
@@ -389,7 +389,7 @@ __global__ void __launch_bounds__(CTH, 1)
                 break;
             }
             tc_fence_after();
-#pragma unroll
+#pragma unroll 1
             for (int m0 = 0; m0 < MP; m0 += 32) {
                 const uint32_t at = tm + lane_base + TS + m0;
                 float v[32];
@@ -427,54 +427,48 @@ __global__ void __launch_bounds__(CTH, 1)
             const uint32_t at = tm + lane_base + TG + 128 * c + 64 * half;
             const float ct = A.cumf[tl];
 #pragma unroll 1
-            for (int k2 = 0; k2 < 4; k2 += 2) {
-                float v[2][16];
-                const int kb2 = 4 * half + k2;  // even, as the last block of a row's pair is odd
-                uint32_t w[2][8];
-                if (kb2 > 2 * q4) {
+            for (int k = 0; k < 4; ++k) {
+                const int kb = 4 * half + k;
+                uint32_t w[8];
+                if (kb > 2 * q4 + 1) {
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) w[0][e] = w[1][e] = 0u;
+                    for (int e = 0; e < 8; ++e) w[e] = 0u;
                 } else {
-                    tmem_ld16(at + 16 * k2, v[0]);
-                    tmem_ld16(at + 16 * k2 + 16, v[1]);
+                    float v[16];
+                    tmem_ld16(at + 16 * k, v);
                     tmem_wait_ld();
+                    if (kb < 2 * q4) {  // wholly before my rows: one exponential for the block
+                        const float f = ex2(ct - A.cref[kb]);
+                        const ssm_f2 ff = ssm_pack(f, f);
 #pragma unroll
-                    for (int k = 0; k < 2; ++k) {
-                        const int kb = kb2 + k;
-                        if (kb2 < 2 * q4) {  // wholly before my rows: one exponential for the block
-                            const float f = ex2(ct - A.cref[kb]);
-                            const ssm_f2 ff = ssm_pack(f, f);
-#pragma unroll
-                            for (int e = 0; e < 16; e += 4) {
-                                const ulonglong2 r = *reinterpret_cast<const ulonglong2 *>(A.rs + 16 * kb + e);
-                                const ssm_f2 lo = ssm_mul(ssm_pack(v[k][e], v[k][e + 1]), ssm_mul(ff, r.x));
-                                const ssm_f2 hi = ssm_mul(ssm_pack(v[k][e + 2], v[k][e + 3]), ssm_mul(ff, r.y));
-                                ssm_unpack(lo, v[k][e], v[k][e + 1]);
-                                ssm_unpack(hi, v[k][e + 2], v[k][e + 3]);
-                            }
-                        } else if (A.span[kb] < 64.f) {
-                            // as above, from the block's end: at most 2^64 too large before, and as much too small behind
-                            const float f = ex2(ct - A.cref[kb]);
-#pragma unroll
-                            for (int e = 0; e < 16; ++e) {
-                                const int s = 16 * kb + e;
-                                const float p = v[k][e] * (f * A.rs[s]);
-                                v[k][e] = s < tl ? p : s == tl ? p + skip : 0.f;
-                            }
-                        } else {
-#pragma unroll
-                            for (int e = 0; e < 16; ++e) {
-                                const int s = 16 * kb + e;
-                                const float p = v[k][e] * ex2(ct - A.uf[s]);
-                                v[k][e] = s < tl ? p : s == tl ? p + skip : 0.f;
-                            }
+                        for (int e = 0; e < 16; e += 4) {
+                            const ulonglong2 r = *reinterpret_cast<const ulonglong2 *>(A.rs + 16 * kb + e);
+                            const ssm_f2 lo = ssm_mul(ssm_pack(v[e], v[e + 1]), ssm_mul(ff, r.x));
+                            const ssm_f2 hi = ssm_mul(ssm_pack(v[e + 2], v[e + 3]), ssm_mul(ff, r.y));
+                            ssm_unpack(lo, v[e], v[e + 1]);
+                            ssm_unpack(hi, v[e + 2], v[e + 3]);
                         }
+                    } else if (A.span[kb] < 64.f) {
+                        // as above, from the block's end: at most 2^64 too large before, and as much too small behind
+                        const float f = ex2(ct - A.cref[kb]);
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) w[k][e] = pack_bf16(v[k][2 * e], v[k][2 * e + 1]);
+                        for (int e = 0; e < 16; ++e) {
+                            const int s = 16 * kb + e;
+                            const float p = v[e] * (f * A.rs[s]);
+                            v[e] = s < tl ? p : s == tl ? p + skip : 0.f;
+                        }
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) {
+                            const int s = 16 * kb + e;
+                            const float p = v[e] * ex2(ct - A.uf[s]);
+                            v[e] = s < tl ? p : s == tl ? p + skip : 0.f;
+                        }
                     }
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) w[e] = pack_bf16(v[2 * e], v[2 * e + 1]);
                 }
-                tmem_st8(at + 8 * k2, w[0]);
-                tmem_st8(at + 8 * k2 + 8, w[1]);
+                tmem_st8(at + 8 * k, w);
             }
             tmem_wait_st();
             tc_fence_before();
