@@ -1,4 +1,5 @@
-"""GB300-native Interdomain Attention token mixer (prefill + recurrent decode).
+"""GB300-native Interdomain Attention token mixer (prefill + recurrent decode), and beside it a
+selective mixer (short convolution, selective scan, one-position step) and the decoder's pre-norm.
 
 The compute path is the CUDA library ``libida.so`` (built from ``csrc/``);
 ``binding`` marshals torch tensors into its C ABI.  Importing this package

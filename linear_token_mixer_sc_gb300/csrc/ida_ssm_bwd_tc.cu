@@ -30,7 +30,7 @@
 //
 // What bounds it: the stages of a head follow one another between block barriers (one CTA of 16 warps an
 // SM: its registers and 175 KB are taken), at 0.34 instructions a cycle and scheduler; tensor pipe 12 %,
-// HBM 15 %.  8 x 2048 positions of 12 heads of 64 x 64: 152 us, 98 of them this kernel's (8 us a head and
+// HBM 15 %.  8 x 2048 positions of 12 heads of 64 x 64: 151 us, 98 of them this kernel's (8 us a head and
 // chunk), 45 the chunk states' and 14 their running sums'.  (The MMAs issued by a 17th warp: 189 us, its
 // threads' share of the registers spills the others'.)
 //

@@ -25,10 +25,11 @@
 //   warps 16-19 the rows of (c X_0) in Y scaled by 2^S_t before P x is added to them, y out by TMA
 //   warps 20-23 the other half of b; the state's bf16 copy for Y and its decay in TMEM
 // What bounds it: the chain c X_0 - scaled rows - P x - state of a chunk, 4600 cycles, of which the MMAs'
-// reads of shared memory are 2300.  4 x 4096 positions of 16 heads of 128 x 64: 38 us, 60 with the segment
-// states before it.  (All stages in one group of 256 threads, two CTAs per SM: 45 us, 8500 cycles a chunk,
+// reads of shared memory are 2300.  4 x 4096 positions of 16 heads of 128 x 64: 34 us, 54 with the segment
+// states before it.  Its warps run different code, so loops stay short: with all of them unrolled (66 KB)
+// they waited for instructions, 60 us.  (All stages in one group of 256 threads, two CTAs per SM: 45 us, 8500 cycles a chunk,
 // most of them waits for the next stage.  D x added in fp32 to the scaled rows, not as a part of P: y's
-// error 1.8e-3 instead of 2.3e-3, 1.7e-3 of which are its own rounding, but 67 us.)
+// error 1.8e-3 instead of 2.3e-3, 1.7e-3 of which are its own rounding, but 58 us.)
 // The tiles have the 128-byte swizzle that the MMA descriptors name, so one copy serves as a
 // K-major operand (b, c in G) and as an MN-major one (x, b in the state update, whose K is the
 // position).  The state stays in TMEM.
@@ -864,9 +865,9 @@ ida_status ssm_map(CUtensorMap *m, const void *p, int B, int N, int K, int w, lo
 // Segments, and the parts of one whose states the first launch makes: the split with the least time
 // by the launches' passes over the SMs, a chunk taking about 1.2 us in the chunk kernel (one CTA per
 // SM) and 0.9 us in the state kernel (two), a CTA's start 3 us, the extra launches 5 us.  Measured, 16
-// heads of 128 x 64: 4 x 4096 positions 59.9 us in 2 segments of 4 parts (its choice), 64.9 of 8, 72.9 of
-// 1, 70.1 in 4 segments, 64.3 in one; 14336 positions with their final state 78.8 us in 19 segments (its
-// choice), 78.4 in 8 of 2 parts, 86.5 in 9, 106.6 in 6.  Parts that fill the SMs several times over are
+// heads of 128 x 64 (the chunk kernel 4 us slower than now): 4 x 4096 positions 59.9 us in 2 segments of 4
+// parts (its choice), 64.9 of 8, 72.9 of 1, 70.1 in 4 segments, 64.3 in one; 14336 positions with their
+// final state 78.8 us in 19 segments (its choice), 78.4 in 8 of 2 parts, 86.5 in 9, 106.6 in 6.  Parts that fill the SMs several times over are
 // not looked at: the search is short for long sequences too.
 void ssm_chunk_segments(int B, int H, int N, int d, int M, int num_sms, int &seg, int &segs, int &fine) {
     const int nch = (N + SQ - 1) / SQ, dp = d <= 64 ? 64 : 128;
