@@ -168,3 +168,23 @@ def test_norm_captured_and_replayed(back):
     _done()
     for a, b in zip(got, ref):
         assert torch.equal(a, b)
+
+
+def test_rows_past_32_bits():
+    rows, D = (1 << 19) + 3, 8192
+    if torch.cuda.mem_get_info()[0] < 64 << 30:
+        pytest.skip("needs 40 GB")
+    g = torch.Generator().manual_seed(5)
+    last = torch.randn(5, D, generator=g).bfloat16().cuda()
+    w = torch.randn(D, generator=g).cuda()
+    x = torch.zeros(rows, D, dtype=torch.bfloat16, device="cuda")
+    x[-5:] = last
+    out, _, _, _ = binding.ida_rmsnorm(x, w)
+    want, _, _, _ = binding.ida_rmsnorm(last, w)
+    assert torch.equal(out[-5:], want) and not out[:-5].any()
+    _, _, q, scale = binding.ida_rmsnorm(x, w, group=128)
+    _, _, wq, ws = binding.ida_rmsnorm(last, w, group=128)
+    assert torch.equal(q[-5:].view(torch.uint8), wq.view(torch.uint8)) and torch.equal(scale[-5:], ws)
+    del q, scale
+    dx = binding.ida_rmsnorm_backward(x, w, out)["x"]
+    assert torch.equal(dx[-5:], binding.ida_rmsnorm_backward(last, w, want)["x"])

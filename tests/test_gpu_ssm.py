@@ -468,6 +468,37 @@ def test_gradients_beside_the_inputs_in_the_same_rows():
     assert torch.equal(wide[..., :C], before) and torch.equal(got["conv_w"], want["conv_w"])
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_rows_past_32_bits(dtype):
+    """Slices of rows 2^26 elements apart, the last ones past element 2^32: the results of dense rows."""
+    B, N, H, d, G, M, ld = 1, 70, 2, 32, 1, 16, 1 << 26
+    C, row = H * d + 2 * G * M, (H * d + 2 * G * M + H + 7) // 8 * 8
+    if torch.cuda.mem_get_info()[0] < 48 << 30:
+        pytest.skip("needs 20 GB")
+    dense = sc.rows(B, N, C, H, dtype, 11).cuda()
+    far = torch.empty(B * N * ld, dtype=dense.dtype, device="cuda").as_strided((B, N, row), (N * ld, ld, 1))
+    far.copy_(dense)
+    p = sc.cuda(sc.params(H, C, 4, 12))
+    dout = torch.randn(B, N, C, generator=sc.gen(13)).to(dense.dtype).cuda()
+    dy = torch.randn(B, N, H, d, generator=sc.gen(14)).to(dense.dtype).cuda()
+
+    def run(rows):
+        x, b, c = sc.split(rows[..., :C], H, d, G, M)
+        dt = rows[..., C:C + H]
+        out = list(binding.ida_ssm_conv(rows[..., :C], p["conv_w"], p["conv_b"], final_state=True))
+        out += binding.ida_ssm_conv_backward(rows[..., :C], dout, p["conv_w"], p["conv_b"]).values()
+        out += binding.ida_ssm_scan(x, b, c, dt, p, final_state=True)
+        out += binding.ida_ssm_scan_backward(x, b, c, dt, p, dy).values()
+        tail, state = torch.zeros(N, 3, C, device="cuda"), torch.zeros(N, H, M, d, device="cuda")
+        return out + [binding.ida_ssm_step(rows[0, :, :C], dt[0], p, tail, state, G), tail, state]
+
+    want, got = run(dense), run(far)
+    assert all(torch.equal(g, w) for g, w in zip(got, want))
+    dx = far[..., :C]
+    g = binding.ida_ssm_conv_backward(dense[..., :C], dout, p["conv_w"], p["conv_b"], dx=dx)
+    assert torch.equal(g["x"], want[2]) and torch.equal(far[..., C:], dense[..., C:])
+
+
 def test_outputs_stay_inside_their_rows():
     """Guard bands around y, the final state and the outputs of the step and the convolution."""
     B, N, H, d, G, M, W = 1, 131, 2, 72, 1, 40, 4
