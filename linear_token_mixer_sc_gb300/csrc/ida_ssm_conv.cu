@@ -110,12 +110,14 @@ struct ConvArgs {
 };
 
 constexpr int CONV_THREADS = 256;
-constexpr int CONV_BATCH = 8;  // rows whose loads a thread issues together
+constexpr int CONV_BATCH = 4;  // rows whose loads a thread issues together
 
 // Four channels a thread, two pairs.  (16384 rows of 2176 channels in bf16: eight channels in 156
-// registers, 8 warps an SM, 94 us; four channels in scalar fp32, 21 instructions an element, 41 us.)
+// registers, 8 warps an SM, 94 us; four channels in scalar fp32, 21 instructions an element, 41 us; packed,
+// three CTAs an SM and 8 rows at a time 32.7; four CTAs and 4 rows 29.8, and 32.1 with the next rows read
+// while the present ones are computed.)
 template <typename E, int W>
-__global__ void __launch_bounds__(CONV_THREADS, 3) conv_kernel(ConvArgs a) {
+__global__ void __launch_bounds__(CONV_THREADS, 4) conv_kernel(ConvArgs a) {
     using Q = Pairs<E, 2>;
     typedef typename Q::raw raw;
     constexpr int H = W > 1 ? W - 1 : 1;
@@ -139,29 +141,30 @@ __global__ void __launch_bounds__(CONV_THREADS, 3) conv_kernel(ConvArgs a) {
             Pairs<float, 2>::unpack(__ldg(reinterpret_cast<const float4 *>(
                                         a.state_in + ((size_t)b * (W - 1) + (t + W - 1)) * a.C + c0)), h[j]);
     }
-    for (int tb = t0; tb < t1; tb += CONV_BATCH, x += CONV_BATCH * a.ldx, out += CONV_BATCH * (long long)a.C) {
+    const auto step = [&](const raw &u, E *o_at) {
+        ssm_f2 cur[2], o[2];
+        Q::unpack(u, cur);
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            ssm_f2 p = ssm_fma(w[W - 1][e], cur[e], bias[e]);
+#pragma unroll
+            for (int j = 0; j < W - 1; ++j) p = ssm_fma(w[j][e], h[j][e], p);
+            o[e] = ssm_mul(p, conv_sigmoid<E>(p));
+#pragma unroll
+            for (int j = 0; j + 1 < W - 1; ++j) h[j][e] = h[j + 1][e];
+            if (W > 1) h[H - 1][e] = cur[e];
+        }
+        __stcs(reinterpret_cast<raw *>(o_at), Q::pack(o));
+    };
+    int tb = t0;
+    for (; tb + CONV_BATCH <= t1; tb += CONV_BATCH, x += CONV_BATCH * a.ldx, out += CONV_BATCH * (long long)a.C) {
         raw u[CONV_BATCH];
 #pragma unroll
-        for (int k = 0; k < CONV_BATCH; ++k)
-            if (tb + k < t1) u[k] = __ldg(reinterpret_cast<const raw *>(x + k * a.ldx));
+        for (int k = 0; k < CONV_BATCH; ++k) u[k] = __ldg(reinterpret_cast<const raw *>(x + k * a.ldx));
 #pragma unroll
-        for (int k = 0; k < CONV_BATCH; ++k) {
-            if (tb + k >= t1) break;
-            ssm_f2 cur[2], o[2];
-            Q::unpack(u[k], cur);
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                ssm_f2 p = ssm_fma(w[W - 1][e], cur[e], bias[e]);
-#pragma unroll
-                for (int j = 0; j < W - 1; ++j) p = ssm_fma(w[j][e], h[j][e], p);
-                o[e] = ssm_mul(p, conv_sigmoid<E>(p));
-#pragma unroll
-                for (int j = 0; j + 1 < W - 1; ++j) h[j][e] = h[j + 1][e];
-                if (W > 1) h[H - 1][e] = cur[e];
-            }
-            __stcs(reinterpret_cast<raw *>(out + k * (long long)a.C), Q::pack(o));
-        }
+        for (int k = 0; k < CONV_BATCH; ++k) step(u[k], out + k * (long long)a.C);
     }
+    for (; tb < t1; ++tb, x += a.ldx, out += a.C) step(__ldg(reinterpret_cast<const raw *>(x)), out);
     if (a.final_state && t1 == a.N)
 #pragma unroll
         for (int j = 0; j < W - 1; ++j)
@@ -187,7 +190,8 @@ constexpr int CN = 4;         // channels of a thread, two pairs
 // Block (32 x 4 channels) x (8 strips), walking the strips of all rows gridDim.x blocks apart with its
 // sums in registers.  A thread walks u = t0 .. t1 + W - 2: it forms g_u from the x window, then dx of
 // position u - (W - 1) from the last W values of g, so the W - 1 positions behind a strip are evaluated
-// twice (their x and dout come from L2).
+// twice (their x and dout come from L2).  The next rows are read as the present ones are taken: 8 x 2048
+// rows of 896 channels in 31.8 us, 35.3 with loads and arithmetic in turn; three CTAs an SM spill, 77 us.
 template <typename E, int W>
 __global__ void __launch_bounds__(32 * CB_STRIPS, 2) conv_bwd_kernel(ConvBwdArgs a) {
     using Q = Pairs<E, 2>;
@@ -218,16 +222,17 @@ __global__ void __launch_bounds__(32 * CB_STRIPS, 2) conv_bwd_kernel(ConvBwdArgs
                 if (t0 - (W - 1) + j >= 0) Q::unpack(*reinterpret_cast<const raw *>(x - (long long)(W - 1 - j) * a.ldx), h[j]);
             }
             const int n = t1 - t0, left = a.N - t0;  // positions of the strip, and of the row from it on
-            for (int ub = 0; ub < n + W - 1; ub += CB_BATCH) {  // g beyond the row's end is zero
-                raw rx[CB_BATCH], rd[CB_BATCH];
-#pragma unroll
-                for (int k = 0; k < CB_BATCH; ++k) {
-                    rx[k] = rd[k] = raw();
-                    if (ub + k < n + W - 1 && ub + k < left) {
-                        rx[k] = *reinterpret_cast<const raw *>(x + (ub + k) * a.ldx);
-                        rd[k] = *reinterpret_cast<const raw *>(dout + (ub + k) * (long long)a.C);
-                    }
+            raw rx[CB_BATCH], rd[CB_BATCH];  // the next rows, on their way
+            const auto read = [&](int k, int u) {  // g beyond the row's end is zero
+                rx[k] = rd[k] = raw();
+                if (u < n + W - 1 && u < left) {
+                    rx[k] = *reinterpret_cast<const raw *>(x + u * a.ldx);
+                    rd[k] = *reinterpret_cast<const raw *>(dout + u * (long long)a.C);
                 }
+            };
+#pragma unroll
+            for (int k = 0; k < CB_BATCH; ++k) read(k, k);
+            for (int ub = 0; ub < n + W - 1; ub += CB_BATCH) {
 #pragma unroll
                 for (int k = 0; k < CB_BATCH; ++k) {
                     const int u = ub + k;
@@ -235,6 +240,7 @@ __global__ void __launch_bounds__(32 * CB_STRIPS, 2) conv_bwd_kernel(ConvBwdArgs
                     ssm_f2 cur[2], d[2], o[2];
                     Q::unpack(rx[k], cur);
                     Q::unpack(rd[k], d);
+                    read(k, u + CB_BATCH);
                     const bool inside = u < n;  // positions behind the strip are another's to sum
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
@@ -379,12 +385,12 @@ ida_status ida_ssm_conv(const void *x, const float *conv_w, const float *conv_b,
     }
     ConvArgs a = {x, conv_w, conv_b, state_in, out, final_state, B, N, C, ldx, 0, 0};
     const int vecs = C / 4;
-    // W - 1 rows of a strip are read twice (from L2), and the last of the passes of three blocks an SM may
-    // be short: of the strip lengths 8 .. 64 the one that makes a thread's passes read the fewest rows
+    // W - 1 rows of a strip are read twice (from L2), and the last of the passes of four blocks an SM may
+    // be short: of the strip lengths up to 64 the one that makes a thread's passes read the fewest rows
     long long cost = 0;
     for (int strip = 64; strip >= CONV_BATCH; strip -= CONV_BATCH) {
         const long long n = ((long long)B * ((N + strip - 1) / strip) * vecs + CONV_THREADS - 1) / CONV_THREADS;
-        const long long c = (n + 3 * num_sms - 1) / (3 * num_sms) * (strip + W - 1);
+        const long long c = (n + 4 * num_sms - 1) / (4 * num_sms) * (strip + W - 1);
         if (!cost || c < cost) {
             a.strip = strip;
             cost = c;
