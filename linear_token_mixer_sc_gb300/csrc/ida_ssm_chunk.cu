@@ -3,8 +3,8 @@
 // Over a chunk of Q = 128 positions, with S_t the sum of log2 a up to position t of it, X_0 the
 // state before it and X_Q the state behind it (see ida_ssm.cuh for the recurrence):
 //   G    [t][s]  = c_t . b_s                                   MMA, K = M
-//   P    [t][s]  = G 2^(S_t - S_s) D_s (s <= t), + D at s = t  CUDA cores, G from TMEM, P to TMEM
-//   Y    [t][j]  = P x + 2^S_t (c_t X_0)                       MMAs, K = Q and K = M
+//   P    [t][s]  = G 2^(S_t - S_s) D_s (s <= t)                CUDA cores, G from TMEM, P to TMEM
+//   Y    [t][j]  = P x + 2^S_t (c_t X_0) + D x_t               MMAs, K = Q and K = M
 //   X_Q^T [j][m] = 2^S_Q X_0^T + x^T (b_s 2^(S_Q - S_s) D_s)   scaled in TMEM, then MMA, K = Q
 // No factor exceeds 1 (but D_s): decays are differences of S taken before the exponential.
 //
@@ -22,14 +22,15 @@
 //   warps 4-7   the step sizes' sums and exponentials, two chunks ahead; half of b scaled in place
 //   warps 8-15  P: thread t of a lane quarter makes row t from row t of G, in G's own place in TMEM
 //               (each half of a row is read and replaced by one warp), an A operand there
-//   warps 16-19 the rows of (c X_0) in Y scaled by 2^S_t before P x is added to them, y out by TMA
-//   warps 20-23 the other half of b; the state's bf16 copy for Y and its decay in TMEM
+//   warps 16-23 the rows of (c X_0) in Y, half a row each, scaled by 2^S_t and D x
+//               added, in fp32, before P x is; y out by TMA
+//   warps 24-27 the other half of b; the state's bf16 copy for Y and its decay in TMEM
 // What bounds it: the chain c X_0 - scaled rows - P x - state of a chunk, 4600 cycles, of which the MMAs'
-// reads of shared memory are 2300.  4 x 4096 positions of 16 heads of 128 x 64: 34 us, 54 with the segment
+// reads of shared memory are 2300.  4 x 4096 positions of 16 heads of 128 x 64: 36 us, 56 with the segment
 // states before it.  Its warps run different code, so loops stay short: with all of them unrolled (66 KB)
-// they waited for instructions, 60 us.  (All stages in one group of 256 threads, two CTAs per SM: 45 us, 8500 cycles a chunk,
-// most of them waits for the next stage.  D x added in fp32 to the scaled rows, not as a part of P: y's
-// error 1.8e-3 instead of 2.3e-3, 1.7e-3 of which are its own rounding, but 58 us.)
+// they waited for instructions, 60 us.  (All stages in one group of 256 threads, two CTAs per SM: 45 us,
+// 8500 cycles a chunk, most of them waits for the next stage.  D as a part of P, rounded with it: 55 us, but y's error is 2.3e-3
+// of its size instead of 1.8e-3, 1.7e-3 of which are its own rounding.  Four warps for the rows: 58 us.)
 // The tiles have the 128-byte swizzle that the MMA descriptors name, so one copy serves as a
 // K-major operand (b, c in G) and as an MN-major one (x, b in the state update, whose K is the
 // position).  The state stays in TMEM.
@@ -52,7 +53,7 @@ namespace ida {
 using namespace tc;
 
 constexpr int STH = 256;   // threads per CTA of the state kernel
-constexpr int CTH = 768;   // threads per CTA of the chunk kernel
+constexpr int CTH = 896;   // threads per CTA of the chunk kernel
 
 // The chunk kernel's mbarriers: those of chunk i, or of chunks i with the same i % 2.
 enum {
@@ -184,7 +185,7 @@ __global__ void __launch_bounds__(CTH, 1)
     }
     if (tid == 0) {
         for (int i = 0; i < kBars; ++i)
-            mbar_init(&bar[i], i == kP || i == kP + 1 || i == kScaled ? 8 : (i >= kArr && i < kFreeArr) || i == kRows || i == kFreeY ? 4 : 1);
+            mbar_init(&bar[i], i == kP || i == kP + 1 || i == kScaled || i == kRows || i == kFreeY ? 8 : i >= kArr && i < kFreeArr ? 4 : 1);
         fence_mbar_init();
         *failed = 0;
         tma_prefetch_desc(&tm_x);
@@ -357,8 +358,8 @@ __global__ void __launch_bounds__(CTH, 1)
             if (i + 2 < nch) go = make_arrays(i + 2);
         }
         if (!go) ok = false;
-    } else if (warp >= 20) {
-        const int k = tid - 640;  // row of b
+    } else if (warp >= 24) {
+        const int k = tid - 768;  // row of b
         {
             // the state before the segment
             const int ch = DP == 64 ? (tl & 63) : tl;  // my channel; with DP = 64 lanes 64.. repeat 0..63
@@ -414,7 +415,6 @@ __global__ void __launch_bounds__(CTH, 1)
         }
     } else if (warp >= 8 && warp < 16) {
         const int half = (warp - 8) >> 2;
-        const float skip = a.D[h];
         for (int i = 0; i < nch; ++i) {
             const int c = i & 1;
             const StepArrays A(arrays + (i & 3) * SARR);
@@ -456,14 +456,14 @@ __global__ void __launch_bounds__(CTH, 1)
                         for (int e = 0; e < 16; ++e) {
                             const int s = 16 * kb + e;
                             const float p = v[e] * (f * A.rs[s]);
-                            v[e] = s < tl ? p : s == tl ? p + skip : 0.f;
+                            v[e] = s <= tl ? p : 0.f;
                         }
                     } else {
 #pragma unroll
                         for (int e = 0; e < 16; ++e) {
                             const int s = 16 * kb + e;
                             const float p = v[e] * ex2(ct - A.uf[s]);
-                            v[e] = s < tl ? p : s == tl ? p + skip : 0.f;
+                            v[e] = s <= tl ? p : 0.f;
                         }
                     }
 #pragma unroll
@@ -477,11 +477,14 @@ __global__ void __launch_bounds__(CTH, 1)
             if (lane == 0) mbar_arrive(&bar[kP + c]);
         }
     } else if (warp >= 16) {
+        const int jb = (warp - 16) >> 2 ? DP / 2 : 0;  // my half of the columns
+        const float skip = a.D[h];
+        const ssm_f2 skip2 = ssm_pack(skip, skip);
         for (int i = 0; i < nch; ++i) {
             const int c = i & 1;
             const uint32_t par = i & 1;
             const StepArrays A(arrays + (i & 3) * SARR);
-            ok = wait(kArr + (i & 3), (i >> 2) & 1) && wait(kCX, par);
+            ok = wait(kArr + (i & 3), (i >> 2) & 1) && wait(kFullX + i % L::NX, (i / L::NX) & 1) && wait(kCX, par);
             if (__any_sync(0xffffffffu, !ok)) {
                 ok = false;
                 break;
@@ -491,13 +494,23 @@ __global__ void __launch_bounds__(CTH, 1)
             const float f = A.et[tl];
             const ssm_f2 ff = ssm_pack(f, f);
 #pragma unroll 1
-            for (int j = 0; j < DP; j += 32) {
+            for (int j = jb; j < jb + DP / 2; j += 32) {
                 float v[32];
                 tmem_ld16(at + j, v);
                 tmem_ld16(at + j + 16, v + 16);
                 tmem_wait_ld();
+                const unsigned char *px = sm + L::X + i % L::NX * L::XB + j / 64 * SSLAB;
 #pragma unroll
-                for (int e = 0; e < 32; e += 2) ssm_unpack(ssm_mul(ff, ssm_pack(v[e], v[e + 1])), v[e], v[e + 1]);
+                for (int p = 0; p < 4; ++p) {
+                    const uint4 xw = *reinterpret_cast<const uint4 *>(px + sw_off(tl, j % 64 / 8 + p));
+                    const uint32_t x2[4] = {xw.x, xw.y, xw.z, xw.w};
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        float *o = v + 8 * p + 2 * k;
+                        const ssm_f2 xf = ssm_pack(__uint_as_float(x2[k] << 16), __uint_as_float(x2[k] & 0xffff0000u));
+                        ssm_unpack(ssm_fma(ff, ssm_pack(o[0], o[1]), ssm_mul(skip2, xf)), o[0], o[1]);
+                    }
+                }
                 tmem_st16(at + j, v);
                 tmem_st16(at + j + 16, v + 16);
             }
@@ -510,19 +523,19 @@ __global__ void __launch_bounds__(CTH, 1)
                 mbar_arrive(&bar[kFreeArr + (i & 3)]);
                 bulk_wait_read_all();  // the last output tile has left shared memory
             }
-            if (named_any(2, 128, !ok)) {
+            if (named_any(2, 256, !ok)) {
                 ok = false;
                 break;
             }
             tc_fence_after();
             unsigned char *out = sm + L::OUT;
 #pragma unroll 1
-            for (int j = 0; j < DP; j += 32) {
+            for (int j = jb; j < jb + DP / 2; j += 32) {
                 float v[32];
                 tmem_ld16(at + j, v);
                 tmem_ld16(at + j + 16, v + 16);
                 tmem_wait_ld();
-                if (j + 32 == DP) {  // the next chunk's c X_0 may go over Y
+                if (j + 32 == jb + DP / 2) {  // the next chunk's c X_0 may go over Y
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&bar[kFreeY]);
@@ -532,7 +545,7 @@ __global__ void __launch_bounds__(CTH, 1)
                     *reinterpret_cast<uint4 *>(out + j / 64 * SSLAB + sw_off(tl, j % 64 / 8 + p)) = Vec16<__nv_bfloat16>::pack(v + 8 * p);
             }
             fence_proxy_async_smem();
-            named_sync(2, 128);
+            named_sync(2, 256);
             if (tid == 512) {
 #pragma unroll
                 for (int s = 0; s < DP / 64; ++s)
