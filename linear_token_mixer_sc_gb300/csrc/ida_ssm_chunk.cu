@@ -6,13 +6,17 @@
 //   P    [t][s]  = G 2^(S_t - S_s) D_s (s <= t)                CUDA cores, G from TMEM, P to TMEM
 //   Y    [t][j]  = P x + 2^S_t (c_t X_0) + D x_t               MMAs, K = Q and K = M
 //   X_Q^T [j][m] = 2^S_Q X_0^T + x^T (b_s 2^(S_Q - S_s) D_s)   scaled in TMEM, then MMA, K = Q
-// No factor exceeds 1 (but D_s): decays are differences of S taken before the exponential.
+// Decays are differences of S taken before the exponential, so no weight but D_s exceeds 1.  (Where a block
+// of 16 positions holds the diagonal, a weight is the product of a factor up to 2^64 and one as small.)
 //
 // Precision.  Everything accumulates in fp32.  P, the X_0 operand and, where only y comes of it, the
 // scaled b are rounded to bf16 (each 2^-9 of a term on average, as y's own rounding); c is not:
 // 2^S_t scales the rows of c X_0.  States that leave the kernel (the final state, and a segment's last state, which the
 // next one starts from) are fp32 results: for them the scaled b is kept as the sum of three bf16
-// tiles, all 24 bits.  S is summed in 2^-32 fixed point: it is exact over any chunk or segment.
+// tiles, all 24 bits, and S is summed in 2^-32 fixed point.  The chunk kernel sums it in two floats, one of
+// them exactly: a position that forgets everything takes nothing from the decays behind it.  (One float
+// and D in it as log2 D: y off by 2e-2 of its terms behind a step size of 1e5, and by 17 times its error bound
+// with rates of e^9 and step sizes of 10; fixed point: 2.46 us a chunk for 2.26.)
 //
 // One CTA per SM walks the chunks of one (row, head, up to 128 channels, segment), its warps in
 // roles that hand chunks on through mbarriers, so that a chunk's copy, MMAs, CUDA-core stages and
@@ -76,7 +80,7 @@ enum {
 };
 
 // Shared memory map; DP, MP: channels and state rows rounded up to 64 or 128.
-constexpr int SARR = 5 * SQ + 32;  // floats of one chunk's arrays (StepArrays)
+constexpr int SARR = 6 * SQ + 32;  // floats of one chunk's arrays (StepArrays)
 template <int DP, int MP>
 struct SsmSmem {
     static constexpr int NX = DP == 128 && MP == 128 ? 1 : 2;  // buffers of x
@@ -110,19 +114,20 @@ struct SsmStateSmem {
 // Y [t][j], the state [j][m] (with DP = 64 lanes 64.. repeat 0..63).
 constexpr uint32_t TG = 0, TY = 256, TS = 384, TCOLS = 512;
 
-// What a chunk's step sizes give, for the positions s of the chunk.
+// What a chunk's step sizes give, for the positions s of the chunk.  S is kept in two floats: a position
+// that forgets everything leaves it large, and the small decays behind it are differences of it.
 struct StepArrays {
-    float *cumf;  // S_s
-    float *uf;    // S_s - log2 D_s
-    float *rs;    // 2^(S at the end of s's block of 16 - uf)
-    float *et;    // 2^S_s
-    float *wst;   // 2^(S_Q - S_s) D_s
-    float *cref;  // S at the end of each block of 16
-    float *span;  // how far S falls from the first to the last position of each block
-    float *decay; // 2^S_Q
+    float *sh, *sl;        // S_s
+    float *delta;          // D_s
+    float *rs;             // 2^(S at the end of s's block of 16 - S_s) D_s
+    float *et;             // 2^S_s
+    float *wst;            // 2^(S_Q - S_s) D_s
+    float *crefh, *crefl;  // S at the end of each block of 16
+    float *span;           // how far S falls from the first to the last position of each block
+    float *decay;          // 2^S_Q
     __device__ __forceinline__ StepArrays(float *p)
-        : cumf(p), uf(p + SQ), rs(p + 2 * SQ), et(p + 3 * SQ), wst(p + 4 * SQ), cref(p + 5 * SQ), span(p + 5 * SQ + 8),
-          decay(p + 5 * SQ + 16) {}
+        : sh(p), sl(p + SQ), delta(p + 2 * SQ), rs(p + 3 * SQ), et(p + 4 * SQ), wst(p + 5 * SQ), crefh(p + 6 * SQ),
+          crefl(p + 6 * SQ + 8), span(p + 6 * SQ + 16), decay(p + 6 * SQ + 24) {}
 };
 
 __device__ __forceinline__ void mbar_arrive(uint64_t *bar) {
@@ -167,7 +172,7 @@ __global__ void __launch_bounds__(CTH, 1)
     uint32_t *tslot = reinterpret_cast<uint32_t *>(sm + L::MISC + 8 * kBars);
     uint32_t *failed = tslot + 1;
     float *arrays = reinterpret_cast<float *>(sm + L::ARR);
-    float *tot = reinterpret_cast<float *>(sm + L::TOT);
+    float2 *tot = reinterpret_cast<float2 *>(sm + L::TOT);
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
     const int q4 = warp & 3, tl = 32 * q4 + lane;  // the lane quarter of TMEM this warp reaches, and its lane
     const uint32_t lane_base = (uint32_t)(32 * q4) << 16;
@@ -300,45 +305,60 @@ __global__ void __launch_bounds__(CTH, 1)
     } else if (warp >= 4 && warp < 8) {
         const int k = tid - 128;  // position of the chunk
         const __nv_bfloat16 *gdt = static_cast<const __nv_bfloat16 *>(a.dt) + (size_t)b * N * a.lddt + h;
-        const float dt_bias = a.dt_bias[h], rate2 = expf(a.a_log[h]) * 1.4426950408889634f;
+        const float dt_bias = a.dt_bias[h];
+        const float rate2 = expf(a.a_log[h]) * 1.4426950408889634f;
         const auto dt_of = [&](int i) {
             const int p = t_begin + i * SQ + k;
             return i < nch && p < t_end ? __bfloat162float(gdt[(size_t)p * a.lddt]) : 0.f;
         };
         float dt_next = dt_of(0);
-        // y alone comes of these: fp32 sums within a chunk, and log(1 + e) to 2^-18, are far below the
-        // rounding of P
         const auto make_arrays = [&](int i) {
-            const float z = dt_next + dt_bias;
+            const float delta = t_begin + i * SQ + k < t_end ? softplus(dt_next + dt_bias) : 0.f;  // behind the end nothing decays or is added
             dt_next = dt_of(i + 1);
             if (i >= 4) ok = wait(kFreeArr + (i & 3), ((i >> 2) - 1) & 1);
-            const float e = __expf(-fabsf(z));
-            const float l1 = e < 0.03125f ? e * fmaf(e, fmaf(e, 0.33333333f, -0.5f), 1.f) : __logf(1.f + e);
-            const float delta = t_begin + i * SQ + k < t_end ? fmaxf(z, 0.f) + l1 : 0.f;  // behind the end nothing decays or is added
-            float s = fmaxf(-rate2 * delta, -1048576.f);
+            // log2 a in two floats, a multiple of 1/64 and the rest, summed apart: the sums of the first are exact
+            // (2^-512 is 0 here, and 128 times 512 has 22 bits of 1/64), those of the rest stay below 1
+            const float p = fminf(rate2 * delta, 512.f), m = (p + 196608.f) - 196608.f;
+            float hi = -m, lo = m - p;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
-                const float u = __shfl_up_sync(0xffffffffu, s, o);
-                if (lane >= o) s += u;
+                const float u = __shfl_up_sync(0xffffffffu, hi, o), v = __shfl_up_sync(0xffffffffu, lo, o);
+                if (lane >= o) {
+                    hi += u;
+                    lo += v;
+                }
             }
-            if (lane == 31) tot[q4] = s;
+            if (lane == 31) tot[q4] = make_float2(hi, lo);
             if (named_any(1, 128, !ok)) return false;
-            const float w0 = tot[0], w1 = w0 + tot[1], w2 = w1 + tot[2], all = w2 + tot[3];
-            s += q4 == 0 ? 0.f : q4 == 1 ? w0 : q4 == 2 ? w1 : w2;
-            const StepArrays A(arrays + (i & 3) * SARR);
-            const float u = s - __log2f(delta);  // D = 0: +inf, and 2^(.. - u) = 0
-            const float ref = __shfl_sync(0xffffffffu, s, lane | 15), first = __shfl_sync(0xffffffffu, s, lane & 16);
-            A.cumf[k] = s;
-            A.uf[k] = u;
-            A.rs[k] = ex2(ref - u);
-            A.et[k] = ex2(s);
-            A.wst[k] = ex2(all - u);
-            if ((lane & 15) == 15) {
-                A.cref[k >> 4] = s;
-                A.span[k >> 4] = first - s;
+            float2 all = make_float2(0.f, 0.f);
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+                if (w == q4) {
+                    hi += all.x;
+                    lo += all.y;
+                }
+                const float2 u = tot[w];
+                all.x += u.x;
+                all.y += u.y;
             }
-            if (k == 0) *A.decay = ex2(all);
             named_sync(1, 128);  // the totals have been read
+            const StepArrays A(arrays + (i & 3) * SARR);
+            const int end = lane | 15;  // of my block of 16
+            const float rh = __shfl_sync(0xffffffffu, hi, end), rl = __shfl_sync(0xffffffffu, lo, end);
+            const float first = __shfl_sync(0xffffffffu, hi, lane & 16);
+            A.sh[k] = hi;
+            A.sl[k] = lo;
+            A.delta[k] = delta;
+            A.rs[k] = ex2((rh - hi) + (rl - lo)) * delta;
+            A.et[k] = ex2(hi + lo);
+            A.wst[k] = ex2((all.x - hi) + (all.y - lo)) * delta;
+            if ((lane & 15) == 15) {
+                A.crefh[k >> 4] = hi;
+                A.crefl[k >> 4] = lo;
+                A.span[k >> 4] = first - hi;
+            }
+            if (k == 0) *A.decay = ex2(all.x + all.y);
+            __syncwarp();
             if (lane == 0) mbar_arrive(&bar[kArr + (i & 3)]);
             return true;
         };
@@ -351,7 +371,7 @@ __global__ void __launch_bounds__(CTH, 1)
                 ok = false;
                 break;
             }
-            scale_b<MP>(sm + L::B + c * L::BB, k, MP / 16, arrays[(i & 3) * SARR + 4 * SQ + k]);
+            scale_b<MP>(sm + L::B + c * L::BB, k, MP / 16, StepArrays(arrays + (i & 3) * SARR).wst[k]);
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(&bar[kScaled]);
@@ -426,7 +446,7 @@ __global__ void __launch_bounds__(CTH, 1)
             tc_fence_after();
             // row tl, columns 64 half ..: blocks of 16 up to the one that row tl ends in, two at a time
             const uint32_t at = tm + lane_base + TG + 128 * c + 64 * half;
-            const float ct = A.cumf[tl];
+            const float ch = A.sh[tl], cl = A.sl[tl];
 #pragma unroll 1
             for (int k = 0; k < 4; ++k) {
                 const int kb = 4 * half + k;
@@ -439,7 +459,7 @@ __global__ void __launch_bounds__(CTH, 1)
                     tmem_ld16(at + 16 * k, v);
                     tmem_wait_ld();
                     if (kb < 2 * q4) {  // wholly before my rows: one exponential for the block
-                        const float f = ex2(ct - A.cref[kb]);
+                        const float f = ex2((ch - A.crefh[kb]) + (cl - A.crefl[kb]));
                         const ssm_f2 ff = ssm_pack(f, f);
 #pragma unroll
                         for (int e = 0; e < 16; e += 4) {
@@ -451,7 +471,7 @@ __global__ void __launch_bounds__(CTH, 1)
                         }
                     } else if (A.span[kb] < 64.f) {
                         // as above, from the block's end: at most 2^64 too large before, and as much too small behind
-                        const float f = ex2(ct - A.cref[kb]);
+                        const float f = ex2((ch - A.crefh[kb]) + (cl - A.crefl[kb]));
 #pragma unroll
                         for (int e = 0; e < 16; ++e) {
                             const int s = 16 * kb + e;
@@ -462,7 +482,7 @@ __global__ void __launch_bounds__(CTH, 1)
 #pragma unroll
                         for (int e = 0; e < 16; ++e) {
                             const int s = 16 * kb + e;
-                            const float p = v[e] * ex2(ct - A.uf[s]);
+                            const float p = v[e] * (ex2((ch - A.sh[s]) + (cl - A.sl[s])) * A.delta[s]);
                             v[e] = s <= tl ? p : 0.f;
                         }
                     }

@@ -1,0 +1,70 @@
+"""The selective mixer at finite inputs far from the usual ones: positions that forget everything.
+
+Bounds as in ``test_gpu_ssm.py`` where nothing else is said.
+"""
+import math
+
+import pytest
+import torch
+
+from linear_token_mixer_sc_gb300 import binding, build
+from tests import ssm_cases as sc
+from tests.ssm_cases import DT, worst
+from tests.test_gpu_ssm import _done, _on_gpu, _scan_bounds, _scan_inputs, _scan_ref
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    build.build()
+    binding.load()
+
+
+def _large_steps(name, N, H):
+    """(changes to the step sizes' inputs, changes to the parameters), by position and head."""
+    at = torch.zeros(N, H)
+    if name == "one step of 1e4 early":
+        at[3] = 1e4
+    elif name == "one step of 1e5 early":
+        at[3] = 1e5
+    elif name == "a step of 300 every 10 positions":
+        at[::10] = 300.0
+    elif name == "steps of 3e8 in one block of 16":
+        at[16:32] = 3e8
+    p = {}
+    if name == "rates of e^7 and steps of 10":
+        p = {"a_log": torch.full((H,), 7.0), "dt_bias": torch.full((H,), 10.0)}
+    elif name == "rates of e^9 and steps of 10":
+        p = {"a_log": torch.full((H,), 9.0), "dt_bias": torch.full((H,), 10.0)}
+    else:
+        p = {"a_log": torch.full((H,), math.log(16.0))}
+    return at, p
+
+
+LARGE = ["one step of 1e4 early", "one step of 1e5 early", "a step of 300 every 10 positions",
+         "steps of 3e8 in one block of 16", "rates of e^7 and steps of 10", "rates of e^9 and steps of 10"]
+
+
+def _large_case(name, dtype, N):
+    case = (1, N, 2, 64, 1, 64, dtype, True, False)
+    B, N, H, d, G, M = case[:6]
+    p, row, s, C = _scan_inputs(*case)
+    at, over = _large_steps(name, N, H)
+    dt = row[0, :, C:C + H].float()
+    row[0, :, C:C + H] = torch.where(at > 0, at, dt).to(DT[dtype])
+    return row, s, C, {**p, **over}, (H, d, G, M)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("name", LARGE)
+def test_scan_after_positions_that_forget(name, dtype):
+    """A position's large decay takes nothing from the accuracy of the weights behind it."""
+    row, s, C, p, shape = _large_case(name, dtype, 200)
+    y, X = binding.ida_ssm_scan(*_on_gpu(row, C, *shape), sc.cuda(p), state_in=s.cuda(), final_state=True)
+    _done()
+    ry, rX = _scan_ref(row, C, *shape, p, s)
+    ya, Xa = _scan_ref(row, C, *shape, p, s, absolute=True)
+    by, bX = _scan_bounds(dtype, 200, ry, ya, Xa)
+    assert worst(X, rX, bX) <= 1
+    assert worst(y, ry, by) <= 1
