@@ -15,8 +15,8 @@
 // next one starts from) are fp32 results: for them the scaled b is kept as the sum of three bf16
 // tiles, all 24 bits, and S is summed in 2^-32 fixed point.  The chunk kernel sums it in two floats, one of
 // them exactly: a position that forgets everything takes nothing from the decays behind it.  (One float
-// and D in it as log2 D: y off by 2e-2 of its terms behind a step size of 1e5, and by 17 times its error bound
-// with rates of e^9 and step sizes of 10; fixed point: 2.46 us a chunk for 2.26.)
+// and D in it as log2 D: y 3.4 times its error bound off behind a step size of 1e5, 17 times with rates
+// of e^9 and step sizes of 10; fixed point: 2.46 us a chunk for 2.26.)
 //
 // One CTA per SM walks the chunks of one (row, head, up to 128 channels, segment), its warps in
 // roles that hand chunks on through mbarriers, so that a chunk's copy, MMAs, CUDA-core stages and
@@ -685,7 +685,7 @@ __global__ void __launch_bounds__(STH, MP == 64 ? 2 : 1)
             arrays[(n & 1) * SQ + k] = in ? ex2_fix(fx) : 0.f;
         else
             arrays[(n & 1) * SQ + k] = ex2_fix(all - fx + behind) * delta;
-        if (!EACH) behind += all;
+        if (!EACH) behind = max(behind + all, kFixLeast);
         if (MODE == kEach && k == 0 && j0 == 0) a.seg_log[(size_t)unit * parts + seg * per + n] = (float)all * kUnfix;
     };
     // the accumulator of chunk n (of the whole part) to memory

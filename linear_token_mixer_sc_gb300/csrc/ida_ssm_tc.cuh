@@ -46,8 +46,11 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
     return *reinterpret_cast<const uint32_t *>(&h);
 }
 
-// log2 of decays in 2^-32 fixed point: their sums and differences are exact
+// log2 of decays in 2^-32 fixed point: their sums and differences are exact.  -2^20 stands for all below
+// it, 2^-1048576 being 0: a position's is limited to it, and so are sums over more than a chunk (2^11 such
+// positions pass 64 bits).
 constexpr float kFix = 4294967296.f, kUnfix = 1.f / 4294967296.f;  // 2^32
+constexpr long long kFixLeast = -(1ll << 52);
 
 // 2^x of such an x <= 0, to the accuracy of the hardware exponential however long the decay
 __device__ __forceinline__ float ex2_fix(long long x) {
@@ -69,7 +72,7 @@ __device__ __forceinline__ Rate2 rate2_of(float a_log) {
 // log2 of exp(-rate delta) in fixed point, from the exact product of the leading parts
 __device__ __forceinline__ long long log2_fix(const Rate2 &rate, float delta) {
     const float p = rate.hi * delta, e = fmaf(rate.hi, delta, -p) + rate.lo * delta;
-    if (!(p < 1048576.f)) return -(1ll << 52);  // 2^-1048576 is 0
+    if (!(p < 1048576.f)) return kFixLeast;
     return -(__float2ll_rn(p * kFix) + __float2ll_rn(e * kFix));
 }
 

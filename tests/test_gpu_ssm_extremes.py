@@ -1,4 +1,5 @@
-"""The selective mixer at finite inputs far from the usual ones: positions that forget everything.
+"""The selective mixer at finite inputs far from the usual ones: positions that forget everything,
+long runs of them.
 
 Bounds as in ``test_gpu_ssm.py`` where nothing else is said.
 """
@@ -66,5 +67,24 @@ def test_scan_after_positions_that_forget(name, dtype):
     ry, rX = _scan_ref(row, C, *shape, p, s)
     ya, Xa = _scan_ref(row, C, *shape, p, s, absolute=True)
     by, bX = _scan_bounds(dtype, 200, ry, ya, Xa)
+    assert worst(X, rX, bX) <= 1
+    assert worst(y, ry, by) <= 1
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("split", [True, False], ids=["workspace", "no workspace"])
+def test_state_behind_a_long_run_of_positions_that_forget(dtype, split):
+    """More than 2048 positions of log2 a below -2^20 each: their sum passes 2^31."""
+    B, N, H, d, G, M = 1, 4500, 1, 8, 1, 8
+    p, row, s, C = _scan_inputs(B, N, H, d, G, M, dtype, True, False)
+    p = {**p, "a_log": torch.full((H,), math.log(16.0))}
+    row[..., C:C + H] = 2e5
+    ws = None if split else torch.empty(0, dtype=torch.uint8, device="cuda")
+    y, X = binding.ida_ssm_scan(*_on_gpu(row, C, H, d, G, M), sc.cuda(p), state_in=s.cuda(), final_state=True,
+                                workspace=ws)
+    _done()
+    ry, rX = _scan_ref(row, C, H, d, G, M, p, s)
+    ya, Xa = _scan_ref(row, C, H, d, G, M, p, s, absolute=True)
+    by, bX = _scan_bounds(dtype, N, ry, ya, Xa)
     assert worst(X, rX, bX) <= 1
     assert worst(y, ry, by) <= 1
