@@ -9,11 +9,13 @@
 // Decays are differences of S taken before the exponential, so no weight but D_s exceeds 1.  (Where a block
 // of 16 positions holds the diagonal, a weight is the product of a factor up to 2^64 and one as small.)
 //
-// Precision.  Everything accumulates in fp32.  P, the X_0 operand and, where only y comes of it, the
-// scaled b are rounded to bf16 (each 2^-9 of a term on average, as y's own rounding); c is not:
-// 2^S_t scales the rows of c X_0.  States that leave the kernel (the final state, and a segment's last state, which the
-// next one starts from) are fp32 results: for them the scaled b is kept as the sum of three bf16
-// tiles, all 24 bits, and S is summed in 2^-32 fixed point.  The chunk kernel sums it in two floats, one of
+// Precision.  Everything accumulates in fp32.  P, the X_0 operand and the chunk kernel's scaled b are
+// rounded to bf16 (each 2^-9 of a term on average, as y's own rounding); c is not: 2^S_t scales the rows
+// of c X_0.  The states that a segment starts from and the final state are fp32 results, so that y is the
+// same whether that one is wanted or not: for them the scaled b is kept as the sum of three bf16 tiles, all
+// 24 bits, and S is summed in 2^-32 fixed point.  (Starting segments from one tile's sums: 55.9 us for 57.6
+// at 4 x 4096, and another y.)
+// The chunk kernel sums it in two floats, one of
 // them exactly: a position that forgets everything takes nothing from the decays behind it.  (One float
 // and D in it as log2 D: y 3.4 times its error bound off behind a step size of 1e5, 17 times with rates
 // of e^9 and step sizes of 10; fixed point: 2.46 us a chunk for 2.26.)
@@ -30,7 +32,7 @@
 //               added, in fp32, before P x is; y out by TMA
 //   warps 24-27 the other half of b; the state's bf16 copy for Y and its decay in TMEM
 // What bounds it: the chain c X_0 - scaled rows - P x - state of a chunk, 4600 cycles, of which the MMAs'
-// reads of shared memory are 2300.  4 x 4096 positions of 16 heads of 128 x 64: 36 us, 56 with the segment
+// reads of shared memory are 2300.  4 x 4096 positions of 16 heads of 128 x 64: 36 us, 57.6 with the segment
 // states before it.  Its warps run different code, so loops stay short: with all of them unrolled (66 KB)
 // they waited for instructions, 60 us.  (All stages in one group of 256 threads, two CTAs per SM: 45 us,
 // 8500 cycles a chunk, most of them waits for the next stage.  D as a part of P, rounded with it: 55 us, but y's error is 2.3e-3
@@ -97,14 +99,12 @@ struct SsmSmem {
     static constexpr int TOT = ARR + 4 * SARR * 4; // 4 totals
     static constexpr int TOTAL = TOT + 32;
 };
-// PARTS: bf16 tiles that the scaled b is kept in.  With one, two chunks are in flight.
-template <int DP, int MP, int PARTS>
+constexpr int PARTS = 3;  // bf16 tiles that the state kernel keeps the scaled b in
+template <int DP, int MP>
 struct SsmStateSmem {
-    static constexpr int NB = PARTS == 1 ? 2 : 1;
-    static constexpr int X = 0;                            // [NB][DP / 64][128 s][64] bf16
-    static constexpr int XB = DP / 64 * SSLAB, BB = MP / 64 * SSLAB * PARTS;
-    static constexpr int B = X + NB * XB;                  // [NB][PARTS][MP / 64][128 s][64]
-    static constexpr int MISC = B + NB * BB;
+    static constexpr int X = 0;                            // [DP / 64][128 s][64] bf16
+    static constexpr int B = X + DP / 64 * SSLAB;          // [PARTS][MP / 64][128 s][64]
+    static constexpr int MISC = B + PARTS * (MP / 64) * SSLAB;
     static constexpr int ARR = MISC + 64;                  // two chunks' weights
     static constexpr int TOT = ARR + 2 * SQ * 4;
     static constexpr int TOTAL = TOT + 32;
@@ -597,13 +597,13 @@ enum { kPart, kEach, kAdjoint };
 // Parts are walked backwards.  The MMAs' sums are cut off, not rounded, so over a part's chunks the small
 // bf16 parts of b have an accumulator of their own.  Chunks by themselves (of a.seg <= 128 positions each, `per` of a CTA)
 // alternate between two accumulators, so that one is written out while the next is made.
-template <int DP, int MP, int PARTS, int MODE>
+template <int DP, int MP, int MODE>
 __global__ void __launch_bounds__(STH, MP == 64 ? 2 : 1)
     ssm_state_kernel(ScanArgs a, int per, const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_b) {
-    using L = SsmStateSmem<DP, MP, PARTS>;
+    using L = SsmStateSmem<DP, MP>;
     extern __shared__ __align__(1024) unsigned char sm[];
     const uint32_t s0 = smem_u32(sm);
-    uint64_t *bar = reinterpret_cast<uint64_t *>(sm + L::MISC);  // 0, 1 copies, 2, 3 MMAs, of each buffer
+    uint64_t *bar = reinterpret_cast<uint64_t *>(sm + L::MISC);  // 0 copies, 1 MMAs
     uint32_t *tslot = reinterpret_cast<uint32_t *>(sm + L::MISC + 48);
     float *arrays = reinterpret_cast<float *>(sm + L::ARR);
     long long *tot = reinterpret_cast<long long *>(sm + L::TOT);
@@ -616,9 +616,9 @@ __global__ void __launch_bounds__(STH, MP == 64 ? 2 : 1)
     // TMEM: the small parts have accumulators of their own (see above), so that parts that lie side by side
     // in shared memory are one MMA's columns (its A tile, x, is what an MMA's time goes to): all three
     // where they fit 256 columns, which leaves two CTAs an SM, else the high and the middle one
-    constexpr int WIDE = PARTS == 1 ? 1 : MP == 64 && !EACH ? 3 : 2;  // parts of one MMA
-    constexpr int ACC = WIDE * MP;                                    // columns of an accumulator
-    constexpr uint32_t COLS = EACH ? 2 * ACC : ACC > 128 ? 256 : ACC;
+    constexpr int WIDE = MP == 64 && !EACH ? 3 : 2;  // parts of one MMA
+    constexpr int ACC = WIDE * MP;                   // columns of an accumulator
+    constexpr uint32_t COLS = EACH ? 2 * ACC : 256;
     const int groups = EACH ? (parts + per - 1) / per : a.state_segs;
     int id = blockIdx.x;
     const int seg = id % groups;
@@ -637,7 +637,7 @@ __global__ void __launch_bounds__(STH, MP == 64 ? 2 : 1)
         return;
     }
     if (tid == 0) {
-        for (int i = 0; i < 4; ++i) mbar_init(&bar[i], 1);
+        for (int i = 0; i < 2; ++i) mbar_init(&bar[i], 1);
         fence_mbar_init();
         tma_prefetch_desc(&tm_x);
         tma_prefetch_desc(&tm_b);
@@ -648,14 +648,12 @@ __global__ void __launch_bounds__(STH, MP == 64 ? 2 : 1)
     }
     const auto start_of = [&](int n) { return t_begin + (EACH ? n : nch - 1 - n) * step; };  // the n-th chunk walked
     const auto fetch = [&](int n) {  // one thread
-        const int buf = n % L::NB, t0 = start_of(n);
-        mbar_arrive_expect_tx(&bar[buf], (uint32_t)(step * 128 * (DP / 64 + MP / 64)));
+        const int t0 = start_of(n);
+        mbar_arrive_expect_tx(&bar[0], (uint32_t)(step * 128 * (DP / 64 + MP / 64)));
 #pragma unroll
-        for (int i = 0; i < MP / 64; ++i)
-            tma_load_4d(sm + L::B + buf * L::BB + i * SSLAB, &tm_b, 64 * i, g, t0, b, &bar[buf]);
+        for (int i = 0; i < MP / 64; ++i) tma_load_4d(sm + L::B + i * SSLAB, &tm_b, 64 * i, g, t0, b, &bar[0]);
 #pragma unroll
-        for (int i = 0; i < DP / 64; ++i)
-            tma_load_4d(sm + L::X + buf * L::XB + i * SSLAB, &tm_x, j0 + 64 * i, h, t0, b, &bar[buf]);
+        for (int i = 0; i < DP / 64; ++i) tma_load_4d(sm + L::X + i * SSLAB, &tm_x, j0 + 64 * i, h, t0, b, &bar[0]);
     };
     float dt_next = 0.f;
     const auto fetch_dt = [&](int n) {
@@ -669,8 +667,7 @@ __global__ void __launch_bounds__(STH, MP == 64 ? 2 : 1)
     // the launches behind may take their places now: not before, a CTA of theirs that got this SM's TMEM
     // ahead of this one would wait for this one
     dependent_launch();
-    if (tid == 0)
-        for (int n = 0; n < L::NB && n < nch; ++n) fetch(n);
+    if (tid == 0 && nch > 0) fetch(0);
     tc_fence_after();
     const uint32_t tm = *tslot;
     long long behind = 0;  // log2 a summed over the chunks done, in warps 4 .. 7
@@ -699,15 +696,12 @@ __global__ void __launch_bounds__(STH, MP == 64 ? 2 : 1)
             float v[16];
             const uint32_t at = tm + lane_base + (EACH && (n & 1) ? ACC : 0) + m0;
             tmem_ld16(at, v);
-            if (WIDE > 1) {
-                float u[16], l[16];
-                tmem_ld16(at + MP, u);
-                if (WIDE > 2) tmem_ld16(at + 2 * MP, l);
-                tmem_wait_ld();
-#pragma unroll
-                for (int e = 0; e < 16; ++e) v[e] += WIDE > 2 ? u[e] + l[e] : u[e];
-            }
+            float u[16], l[16];
+            tmem_ld16(at + MP, u);
+            if (WIDE > 2) tmem_ld16(at + 2 * MP, l);
             tmem_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 16; ++e) v[e] += WIDE > 2 ? u[e] + l[e] : u[e];
             if (nch == 0)
 #pragma unroll
                 for (int e = 0; e < 16; ++e) v[e] = 0.f;
@@ -726,9 +720,8 @@ __global__ void __launch_bounds__(STH, MP == 64 ? 2 : 1)
     bool ok = true;
     int n = 0;
     for (; n < nch; ++n) {
-        const int buf = n % L::NB;
-        const uint32_t par = (n / L::NB) & 1;
-        ok = mbar_wait(&bar[buf], par) && ok;
+        const uint32_t par = n & 1;
+        ok = mbar_wait(&bar[0], par) && ok;
         if (__syncthreads_or(!ok)) break;  // the tiles and the weights are there
         // b times its weight: row r, half of the columns
         const int r = tid & 127, p0 = (tid >> 7) * (MP / 16);
@@ -736,7 +729,7 @@ __global__ void __launch_bounds__(STH, MP == 64 ? 2 : 1)
 #pragma unroll
         for (int k = 0; k < MP / 16; ++k) {
             const int p = p0 + k;
-            unsigned char *at = sm + L::B + buf * L::BB + p / 8 * SSLAB + sw_off(r, p % 8);
+            unsigned char *at = sm + L::B + p / 8 * SSLAB + sw_off(r, p % 8);
             float v[8];
             Vec16<__nv_bfloat16>::unpack(*reinterpret_cast<uint4 *>(at), v);
 #pragma unroll
@@ -754,19 +747,14 @@ __global__ void __launch_bounds__(STH, MP == 64 ? 2 : 1)
             }
         }
         fence_proxy_async_smem();
-        // two buffers: the other one's next copy, once its MMAs, issued before this scaling, have read it
-        if (L::NB == 2 && tid == 0 && n > 0 && n + 1 < nch) {
-            ok = mbar_wait(&bar[2 + (buf ^ 1)], ((n - 1) / 2) & 1);
-            if (ok) fetch(n + 1);
-        }
         tc_fence_before();
         __syncthreads();
         if (warp == 0 && elect_one()) {
             tc_fence_after();
             // x^T as A: with DP = 64 its second 64 rows repeat the first
-            const SmemDesc da = sw_desc(s0 + L::X + buf * L::XB, DP == 64 ? 0 : SSLAB);
-            const SmemDesc dh = sw_desc(s0 + L::B + buf * L::BB, SSLAB);
-            const SmemDesc dl = sw_desc(s0 + L::B + buf * L::BB + WIDE * (MP / 64) * SSLAB, SSLAB);
+            const SmemDesc da = sw_desc(s0 + L::X, DP == 64 ? 0 : SSLAB);
+            const SmemDesc dh = sw_desc(s0 + L::B, SSLAB);
+            const SmemDesc dl = sw_desc(s0 + L::B + WIDE * (MP / 64) * SSLAB, SSLAB);
             const uint32_t acc = tm + (EACH && (n & 1) ? ACC : 0);
             constexpr uint32_t id_w = idesc(128, ACC, 1, 1, 1, 1), id_l = idesc(128, MP, 1, 1, 1, 1);
 #pragma unroll
@@ -776,7 +764,7 @@ __global__ void __launch_bounds__(STH, MP == 64 ? 2 : 1)
 #pragma unroll
                 for (int k = 0; k < step / 16; ++k)
                     mma_f16(acc + MP, sw_step(da, k * 2048), sw_step(dl, k * 2048), id_l, 1);
-            mma_commit(&bar[2 + buf]);
+            mma_commit(&bar[1]);
         }
         __syncwarp();
         if (n + 1 < nch) {
@@ -784,26 +772,20 @@ __global__ void __launch_bounds__(STH, MP == 64 ? 2 : 1)
             fetch_dt(n + 2);
         }
         if (EACH && n > 0) {  // the chunk before, whose MMAs have completed
-            if (L::NB == 2) ok = mbar_wait(&bar[2 + (buf ^ 1)], ((n - 1) / 2) & 1) && ok;
             tc_fence_after();
             write_out(n - 1, each_out(n - 1), nullptr, 0.f);
         }
-        if (L::NB == 1 && n + 1 < nch) {
-            ok = mbar_wait(&bar[2], par) && ok;
+        if (n + 1 < nch) {
+            ok = mbar_wait(&bar[1], par) && ok;
             if (tid == 0 && ok) fetch(n + 1);
         }
     }
-    if (n == nch) {
-        for (int k = 0; k < L::NB && k < nch; ++k) {  // the last MMAs of each buffer
-            const int last = nch - 1 - k;
-            ok = mbar_wait(&bar[2 + last % L::NB], (last / L::NB) & 1) && ok;
-        }
-    }
+    if (n == nch && nch > 0) ok = mbar_wait(&bar[1], (nch - 1) & 1) && ok;  // the last MMAs
     tc_fence_after();
     if (__syncthreads_or(!ok)) {  // a wait ran out
         if (tid == 0) {
             report_error(a.err, kErrWaitTimeout);
-            for (int k = 0; k < L::NB && n + k < nch; ++k) mbar_wait(&bar[(n + k) % L::NB], ((n + k) / L::NB) & 1);
+            if (n < nch) mbar_wait(&bar[0], n & 1);
         }
     } else if (EACH) {
         if (nch > 0) write_out(nch - 1, each_out(nch - 1), nullptr, 0.f);
@@ -896,12 +878,15 @@ ida_status ssm_map(CUtensorMap *m, const void *p, int B, int N, int K, int w, lo
 }
 
 // Segments, and the parts of one whose states the first launch makes: the split with the least time
-// by the launches' passes over the SMs, a chunk taking about 1.2 us in the chunk kernel (one CTA per
-// SM) and 0.9 us in the state kernel (two), a CTA's start 3 us, the extra launches 5 us.  Measured, 16
-// heads of 128 x 64 (the chunk kernel 4 us slower than now): 4 x 4096 positions 59.9 us in 2 segments of 4
-// parts (its choice), 64.9 of 8, 72.9 of 1, 70.1 in 4 segments, 64.3 in one; 14336 positions with their
-// final state 78.8 us in 19 segments (its choice), 78.4 in 8 of 2 parts, 86.5 in 9, 106.6 in 6.  Parts that fill the SMs several times over are
-// not looked at: the search is short for long sequences too.
+// by the launches' passes over the SMs, at 1.2 us a chunk in the chunk kernel (one CTA per SM) and 0.9 us
+// in the state kernel (two), a CTA's start 3 us, the extra launches 5 us.  (Relative costs: a chunk takes
+// longer where the launches fill the SMs.)  Measured against every other split, in us, without and with a
+// final state, its choice first: 4 x 4096 positions of 16 heads of 128 x 64 58.6 and 72.6 in 2 segments of
+// 4 parts, 63.2 and 82.0 of 8, 64.7 and 70.0 of 2, 73.3 and 76.0 in 4 segments, 64.6 and 138.6 in one;
+// 1 x 14336 64.2 and 63.5 in 19 segments, 61.2 and 62.5 in 8 of 2 parts, 66.9 and 67.9 in 7; 1 x 8192 of 24
+// heads of 64 x 128 72.8 and 73.2 in 6, 82.1 and 82.7 in 5; 2 x 4096 of 16 heads of 128 x 128 71.0 and 72.5
+// in 4, 77.5 and 79.1 of 2 parts, 83.4 and 84.6 in 8.  Parts that fill the SMs several times over are not
+// looked at: the search is short for long sequences too.
 void ssm_chunk_segments(int B, int H, int N, int d, int M, int num_sms, int &seg, int &segs, int &fine) {
     const int nch = (N + SQ - 1) / SQ, dp = d <= 64 ? 64 : 128;
     const long long units = (long long)B * H * ((d + dp - 1) / dp), slots = (M <= 64 ? 2LL : 1LL) * num_sms;
@@ -927,16 +912,16 @@ void ssm_chunk_segments(int B, int H, int N, int d, int M, int num_sms, int &seg
     fine = pick_fine;
 }
 
-template <int DP, int MP, int PARTS, int MODE>
+template <int DP, int MP, int MODE>
 static ida_status launch_states(const ScanArgs &a, cudaStream_t st) {
-    constexpr int smem = SsmStateSmem<DP, MP, PARTS>::TOTAL;
+    constexpr int smem = SsmStateSmem<DP, MP>::TOTAL;
     static_assert(smem <= (MP == 64 ? 113 : 227) * 1024, "shared memory budget");
     CUtensorMap mx, mb;
     constexpr int step = MODE != kPart && MP == 128 ? 64 : SQ;
     ida_status s = ssm_map(&mx, a.x, a.B, a.N, a.H, a.d, a.ldx, step);
     if (s == IDA_OK) s = ssm_map(&mb, a.b, a.B, a.N, a.G, a.M, a.ldb, step);
     if (s != IDA_OK) return s;
-    const auto kernel = ssm_state_kernel<DP, MP, PARTS, MODE>;
+    const auto kernel = ssm_state_kernel<DP, MP, MODE>;
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return fail_with(IDA_ERR_CUDA, cudaGetErrorString(e));
     const long long units = (long long)a.B * a.H * ((a.d + DP - 1) / DP);
@@ -952,18 +937,14 @@ static ida_status launch_states(const ScanArgs &a, cudaStream_t st) {
     return launched("ssm segment states");
 }
 
-template <int DP, int MP>
-static ida_status launch_states_of(const ScanArgs &a, bool exact, cudaStream_t st) {
-    return exact ? launch_states<DP, MP, 3, kPart>(a, st) : launch_states<DP, MP, 1, kPart>(a, st);
-}
-ida_status launch_ssm_states(const ScanArgs &a, bool exact, cudaStream_t st) {
-    if (a.d <= 64) return a.M <= 64 ? launch_states_of<64, 64>(a, exact, st) : launch_states_of<64, 128>(a, exact, st);
-    return a.M <= 64 ? launch_states_of<128, 64>(a, exact, st) : launch_states_of<128, 128>(a, exact, st);
+ida_status launch_ssm_states(const ScanArgs &a, cudaStream_t st) {
+    if (a.d <= 64) return a.M <= 64 ? launch_states<64, 64, kPart>(a, st) : launch_states<64, 128, kPart>(a, st);
+    return a.M <= 64 ? launch_states<128, 64, kPart>(a, st) : launch_states<128, 128, kPart>(a, st);
 }
 
 template <int DP, int MP>
 static ida_status launch_each_of(const ScanArgs &a, bool rev, cudaStream_t st) {
-    return rev ? launch_states<DP, MP, 3, kAdjoint>(a, st) : launch_states<DP, MP, 3, kEach>(a, st);
+    return rev ? launch_states<DP, MP, kAdjoint>(a, st) : launch_states<DP, MP, kEach>(a, st);
 }
 ida_status launch_ssm_chunk_states(const ScanArgs &a, bool rev, cudaStream_t st) {
     if (a.d <= 64) return a.M <= 64 ? launch_each_of<64, 64>(a, rev, st) : launch_each_of<64, 128>(a, rev, st);
@@ -980,7 +961,7 @@ static ida_status launch_chunk(const ScanArgs &a, const CUtensorMap &mx, const C
     const long long units = (long long)a.B * a.H * ((a.d + DP - 1) / DP);
     if (units * a.segs * a.fine > 0x7FFFFFFFLL) return fail_with(IDA_ERR_UNSUPPORTED, "too many rows and heads");
     ida_status s = IDA_OK;
-    if (a.state_segs > 0) s = launch_ssm_states(a, a.final_state != nullptr, st);
+    if (a.state_segs > 0) s = launch_ssm_states(a, st);
     if (s != IDA_OK) return s;
     if (a.segs > 1) {
         const long long n = (long long)a.B * a.H * a.M * a.d / 4;

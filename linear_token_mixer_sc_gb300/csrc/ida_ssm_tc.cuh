@@ -101,9 +101,8 @@ __device__ __forceinline__ long long chunk_sum(const Rate2 &rate, float delta, i
 // behind w and positions behind N are read as zero and not written.
 ida_status ssm_map(CUtensorMap *m, const void *p, int B, int N, int K, int w, long long ld, int rows = SQ);
 
-// Each part's last state from zero (from state_in for the first), rounded as three bf16 parts of
-// its operands or one.
-ida_status launch_ssm_states(const ScanArgs &a, bool exact, cudaStream_t st);
+// Each part's last state from zero (from state_in for the first).
+ida_status launch_ssm_states(const ScanArgs &a, cudaStream_t st);
 
 // Every chunk's (a.seg positions) last state from zero, with rev the sum sum_t a_first .. a_t c_t dy_t^T
 // of the adjoint it passes on; a.x, a.b and their strides then are dy's and c's.
