@@ -477,7 +477,8 @@ IDA_API ida_status ida_ssm_step(const void *xbc, const void *dt, const float *co
  *   out       [rows, D] dtype: receives y (NULL allowed when group > 0);
  *   group     0, or the channels that share a scale: 32, 64, 128 (dividing D) or D.  Then
  *             out_e4m3 [rows, D] receives y / scale in e4m3 (round to nearest even, saturating)
- *             and scale [rows, D / group] float max |y| / 448 of the group (1 if all are zero).
+ *             and scale [rows, D / group] float max |y| / 448 of the group (1 if all are zero, rounded
+ *             up where it is subnormal).
  * Supported: 8 <= D <= 8192, D % 8 == 0.  Arithmetic in fp32.
  */
 IDA_API ida_status ida_rmsnorm(const void *x, const void *residual, const float *w, void *res_out, void *out,

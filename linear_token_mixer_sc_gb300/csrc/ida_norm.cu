@@ -6,8 +6,8 @@
 //   r = x + residual (rounded to the stream's type and stored),
 //   y = r / sqrt(mean r^2 + eps) * w,
 // y in the stream's type or in e4m3 with one fp32 scale per group of channels, for a
-// projection in 8 bits:  scale = max |y| / 448 over the group (1 for a group of zeros),
-// q = y / scale.  Backwards, with n = r / rms and g = dy w:
+// projection in 8 bits:  scale = max |y| / 448 over the group (1 for a group of zeros, rounded up
+// where it is subnormal),  q = y / scale.  Backwards, with n = r / rms and g = dy w:
 //   dx = (g - n mean(g n)) / rms + dres,   dw = sum over rows of dy n.
 //
 // Both directions are bound by HBM: every row is read once, held in registers as fp32 through
@@ -20,7 +20,7 @@
 
 namespace ida {
 
-constexpr float kE4M3Max = 448.f;
+constexpr float kE4M3Max = 448.f, kLeastNormal = 0x1p-126f;
 
 struct NormArgs {
     const void *x, *residual;
@@ -129,7 +129,14 @@ __global__ void __launch_bounds__(TPR > 256 ? TPR : 256) rmsnorm_kernel(NormArgs
             for (int o = a.group / V::n / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
         }
         if (!live || v >= vecs) continue;
-        const float sc = top > 0.f ? top / kE4M3Max : 1.f, is = 1.f / sc;
+        float sc = top > 0.f ? top / kE4M3Max : 1.f, up = 1.f;
+        if (sc < kLeastNormal) {  // 1 / sc would overflow, and sc may be 0 or 1.5 times too small
+            sc = __fdiv_ru(top, kE4M3Max);
+            up = 0x1p64f;
+#pragma unroll
+            for (int e = 0; e < V::n; ++e) r[i][e] *= up;
+        }
+        const float is = 1.f / (sc * up);
         uint32_t q[V::n / 4];
 #pragma unroll
         for (int e = 0; e < V::n; e += 4) {
