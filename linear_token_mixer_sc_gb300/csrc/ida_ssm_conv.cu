@@ -85,7 +85,7 @@ __device__ __forceinline__ ssm_f2 fast_sigmoid(ssm_f2 p) {
     asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(b));
     return ssm_pack(a, b);
 }
-// bf16: that is far below the output's rounding
+// bf16: that is far below the rounding of out and dx.  fp32: expf and a division, in both directions
 template <typename E>
 __device__ __forceinline__ ssm_f2 conv_sigmoid(ssm_f2 p);
 template <>
@@ -247,7 +247,7 @@ __global__ void __launch_bounds__(32 * CB_STRIPS, 2) conv_bwd_kernel(ConvBwdArgs
                         ssm_f2 p = ssm_fma(w[W - 1][e], cur[e], bias[e]);
 #pragma unroll
                         for (int j = 0; j < W - 1; ++j) p = ssm_fma(w[j][e], h[j][e], p);
-                        const ssm_f2 sg = fast_sigmoid(p);  // for both types
+                        const ssm_f2 sg = conv_sigmoid<E>(p);
                         const ssm_f2 gu = ssm_mul(ssm_mul(d[e], sg), ssm_fma(p, ssm_fma(sg, minus, one), one));
                         const ssm_f2 gs = inside ? gu : 0ull;
                         db[e] = ssm_fma(gs, one, db[e]);

@@ -1,5 +1,5 @@
-"""The selective mixer at finite inputs far from the usual ones: positions that forget everything,
-long runs of them.
+"""The selective mixer at finite inputs far from the usual ones: positions that forget everything, long
+runs of them, arguments where a sigmoid is small.
 
 Bounds as in ``test_gpu_ssm.py`` where nothing else is said.
 """
@@ -10,7 +10,7 @@ import torch
 
 from linear_token_mixer_sc_gb300 import binding, build
 from tests import ssm_cases as sc
-from tests.ssm_cases import DT, worst
+from tests.ssm_cases import DT, U32, worst
 from tests.test_gpu_ssm import _done, _on_gpu, _scan_bounds, _scan_inputs, _scan_ref
 
 pytestmark = pytest.mark.gpu
@@ -88,3 +88,19 @@ def test_state_behind_a_long_run_of_positions_that_forget(dtype, split):
     by, bX = _scan_bounds(dtype, N, ry, ya, Xa)
     assert worst(X, rX, bX) <= 1
     assert worst(y, ry, by) <= 1
+
+
+def test_fp32_conv_gradients_where_the_sigmoid_is_small():
+    """One tap of 1 and no bias: the convolved value is the input, and each gradient one evaluation of
+    SiLU' = s (1 + p (1 - s)).  e^-p within 2 units (4 u, u = 2^-24), the addition and the division
+    make s good to 6 u; the product's terms then to (6 s + 1) u |p| s + 10 u |SiLU'|."""
+    N, C = 600, 16
+    x = (-30.0 * torch.rand(1, N, C, generator=sc.gen(1))).cuda()
+    w, b = torch.ones(C, 1, device="cuda"), torch.zeros(C, device="cuda")
+    g = binding.ida_ssm_conv_backward(x, torch.ones_like(x), w, b)
+    _done()
+    p = x.cpu().double()
+    sg = torch.sigmoid(p)
+    ref = sg * (1 + p * (1 - sg))
+    bound = U32 * ((6 * sg + 1) * p.abs() * sg + 10 * ref.abs() + sg)
+    assert worst(g["x"], ref, bound) <= 1
