@@ -394,15 +394,15 @@ IDA_API ida_status ida_rope(void *q, void *k, int B, int N, int H, int R,
  * B*H <= 2^24, B*N <= 2^28.  States, sums and gradients of parameters are fp32 for both
  * dtypes.  Non-finite inputs make the outputs of their own row and head (the row and group's
  * heads for b and c) unspecified, earlier positions included, and the gradients that sum over
- * them (of parameters; of the group's b and c); no others.  Outputs that share elements with
- * inputs are refused; slices of the same wider rows need not.
+ * them (of parameters; of the group's b and c); no others.  Outputs (a workspace that is used and
+ * the states that ida_ssm_step updates among them) that share bytes with inputs or with one another are
+ * refused; other slices of the same wider rows do not share any.
  */
 
 /*
  * The convolution with SiLU over N positions of B rows of C channels (C % 8 == 0, any C up to
  * 2^20; the C above for the mixer).  x rows of stride ldx, out [B, N, C] dtype.  state_in
- * (NULL: zero rows) and final_state (NULL: not wanted) must not overlap.  N == 0 hands the
- * state on.
+ * NULL: zero rows; final_state NULL: not wanted.  N == 0 hands the state on.
  */
 IDA_API ida_status ida_ssm_conv(const void *x, const float *conv_w, const float *conv_b, const float *state_in,
                         void *out, float *final_state, int B, int N, int C, long long ldx,
@@ -423,8 +423,8 @@ IDA_API size_t ida_ssm_conv_backward_workspace_bytes(int B, int N, int C, int W)
 
 /*
  * The scan over N positions: x [B, N, H, d] (rows of stride ldx), b and c [B, N, G, M]
- * (strides ldb and ldc), dt [B, N, H] (stride lddt), y [B, N, H, d] dense.  state_in (NULL: zero) and
- * final_state (NULL: not wanted) must not overlap.  workspace as in ida_forward_ws: with at
+ * (strides ldb and ldc), dt [B, N, H] (stride lddt), y [B, N, H, d] dense.  state_in NULL: zero;
+ * final_state NULL: not wanted (y is the same either way).  workspace as in ida_forward_ws: with at
  * least ida_ssm_scan_workspace_bytes(...) bytes a sequence is split across SMs, with less (or
  * NULL) it is not; results differ by rounding only.  N == 0 hands the state on.
  */
@@ -473,7 +473,8 @@ IDA_API ida_status ida_ssm_step(const void *xbc, const void *dt, const float *co
  * summary, "Skalierbare Implementierung", "Architektur").  Per row of D channels:
  *   r = x + residual, rounded to dtype (x itself without one),  y = r / sqrt(mean r^2 + eps) * w.
  *   x, residual (NULL: none) [rows, D] dtype;  w [D] float;
- *   res_out   NULL, or [rows, D] dtype: receives r; may be x or residual itself;
+ *   res_out   NULL, or [rows, D] dtype: receives r; may be x or residual itself (any other
+ *             overlap of outputs with inputs or one another is refused);
  *   out       [rows, D] dtype: receives y (NULL allowed when group > 0);
  *   group     0, or the channels that share a scale: 32, 64, 128 (dividing D) or D.  Then
  *             out_e4m3 [rows, D] receives y / scale in e4m3 (round to nearest even, saturating)
@@ -490,7 +491,7 @@ IDA_API ida_status ida_rmsnorm(const void *x, const void *residual, const float 
  * residual), dy [rows, D], dres NULL or [rows, D] (what reaches r from elsewhere); dx [rows, D]
  * dtype, the gradient of x and of residual alike, dres included; dw [D] float, summed over the
  * rows (zero when rows == 0).  The workspace is required when rows > 0.  dx may be dy or dres
- * itself.  Deterministic.
+ * itself (any other overlap is refused).  Deterministic.
  */
 IDA_API ida_status ida_rmsnorm_backward(const void *r, const float *w, const void *dy, const void *dres, void *dx,
                                 float *dw, int rows, int D, float eps, int dtype, void *workspace,

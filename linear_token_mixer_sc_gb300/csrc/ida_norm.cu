@@ -367,6 +367,15 @@ ida_status ida_rmsnorm(const void *x, const void *residual, const float *w, void
     for (const void *p : ptrs)
         if (misaligned16(p)) return fail_with(IDA_ERR_ARG, "pointers must be 16-byte aligned");
     if (misaligned16(scale)) return fail_with(IDA_ERR_ARG, "scale must be 16-byte aligned");
+    // in place on x or residual: every thread reads its part of a row before it writes it
+    const size_t n = (size_t)rows * D, bytes = n * (dtype == IDA_F32 ? 4 : 2);
+    const bool on_x = res_out == x, on_residual = res_out == residual;
+    const Rows outs[] = {dense("res_out", res_out, bytes), dense("out", out, bytes), dense("out_e4m3", group ? out_e4m3 : nullptr, n),
+                         dense("scale", group ? scale : nullptr, group ? n / group * 4 : 0)};
+    const Rows ins[] = {dense("x", on_x ? nullptr : x, bytes), dense("residual", on_residual ? nullptr : residual, bytes),
+                        dense("w", w, (size_t)D * 4)};
+    s = check_overlaps(outs, ins);
+    if (s != IDA_OK) return s;
     int num_sms = 0;
     std::string why;
     s = device_ready(&num_sms, why);
@@ -401,6 +410,13 @@ ida_status ida_rmsnorm_backward(const void *r, const float *w, const void *dy, c
         if (misaligned16(dres)) return fail_with(IDA_ERR_ARG, "dres must be 16-byte aligned");
         if (workspace_bytes < ida_rmsnorm_backward_workspace_bytes(rows, D))
             return fail_with(IDA_ERR_ARG, "workspace is smaller than ida_rmsnorm_backward_workspace_bytes");
+        const size_t bytes = (size_t)rows * D * (dtype == IDA_F32 ? 4 : 2);
+        const Rows outs[] = {dense("dx", dx, bytes), dense("dw", dw, (size_t)D * 4),
+                             dense("workspace", workspace, ida_rmsnorm_backward_workspace_bytes(rows, D))};
+        const Rows ins[] = {dense("r", r, bytes), dense("dy", dx == dy ? nullptr : dy, bytes),
+                            dense("dres", dx == dres ? nullptr : dres, bytes), dense("w", w, (size_t)D * 4)};
+        s = check_overlaps(outs, ins);
+        if (s != IDA_OK) return s;
     }
     int num_sms = 0;
     std::string why;

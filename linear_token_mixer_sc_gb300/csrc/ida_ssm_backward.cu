@@ -666,17 +666,18 @@ ida_status ida_ssm_scan_backward(const void *x, const void *b, const void *c, co
                 return fail_with(IDA_ERR_ARG, "dt and ddt must be aligned pointers");
         if (workspace_bytes < ida_ssm_scan_backward_workspace_bytes(B, H, N, d, G, M, dtype))
             return fail_with(IDA_ERR_ARG, "workspace is smaller than ida_ssm_scan_backward_workspace_bytes");
-        const struct {
-            const void *p;
-            long long ld, w;
-        } rows[] = {{dx, lddx, (long long)H * d}, {db, lddb, (long long)G * M}, {dc, lddc, (long long)G * M}, {ddt, ldddt, H},
-                    {x, ldx, (long long)H * d}, {b, ldb, (long long)G * M}, {c, ldc, (long long)G * M}, {dt, lddt, H},
-                    {dy, (long long)H * d, (long long)H * d}};
-        for (int i = 0; i < 4; ++i)
-            for (int k = i + 1; k < 9; ++k)
-                if (rows_overlap(rows[i].p, rows[i].ld, rows[i].w, rows[k].p, rows[k].ld, rows[k].w, (long long)B * N, dtype))
-                    return fail_with(IDA_ERR_ARG, "the gradients must not overlap one another or the inputs");
     }
+    const long long n = (long long)B * N, w = (long long)H * d, bc = (long long)G * M;
+    const size_t par = (size_t)H * 4;
+    const Rows outs[] = {rows_of("dx", dx, lddx, w, n, dtype), rows_of("db", db, lddb, bc, n, dtype), rows_of("dc", dc, lddc, bc, n, dtype),
+                         rows_of("ddt", ddt, ldddt, H, n, dtype), dense("da_log", da_log, par), dense("ddt_bias", ddt_bias, par),
+                         dense("dD", dD, par),
+                         dense("workspace", workspace, ida_ssm_scan_backward_workspace_bytes(B, H, N, d, G, M, dtype))};
+    const Rows ins[] = {rows_of("x", x, ldx, w, n, dtype), rows_of("b", b, ldb, bc, n, dtype), rows_of("c", c, ldc, bc, n, dtype),
+                        rows_of("dt", dt, lddt, H, n, dtype), rows_of("dy", dy, w, w, n, dtype), dense("a_log", work ? a_log : nullptr, par),
+                        dense("dt_bias", work ? dt_bias : nullptr, par), dense("D", work ? D : nullptr, par)};
+    s = check_overlaps(outs, ins);
+    if (s != IDA_OK) return s;
     int num_sms = 0;
     std::string why;
     s = device_ready(&num_sms, why);

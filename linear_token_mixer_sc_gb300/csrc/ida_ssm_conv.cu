@@ -363,16 +363,19 @@ ida_status ida_ssm_conv(const void *x, const float *conv_w, const float *conv_b,
     if (B == 0 || (N == 0 && !final_state)) return IDA_OK;
     if (misaligned16(state_in) || misaligned16(final_state))
         return fail_with(IDA_ERR_ARG, "state_in and final_state must be 16-byte aligned");
-    if (overlap(state_in, state_bytes, final_state, state_bytes))
-        return fail_with(IDA_ERR_ARG, "state_in and final_state must not overlap");
     if (N > 0) {
         const void *ptrs[] = {x, conv_w, conv_b, out};
         for (const void *p : ptrs) {
             if (!p) return fail_with(IDA_ERR_ARG, "null input or output pointer");
             if (misaligned16(p)) return fail_with(IDA_ERR_ARG, "pointers must be 16-byte aligned");
         }
-        if (rows_overlap(x, ldx, C, out, C, C, (long long)B * N, dtype)) return fail_with(IDA_ERR_ARG, "out must not overlap x");
     }
+    const long long n = (long long)B * N;
+    const Rows outs[] = {rows_of("out", out, C, C, n, dtype), dense("final_state", final_state, state_bytes)};
+    const Rows ins[] = {rows_of("x", x, ldx, C, n, dtype), dense("conv_w", N > 0 ? conv_w : nullptr, (size_t)C * W * 4),
+                        dense("conv_b", N > 0 ? conv_b : nullptr, (size_t)C * 4), dense("state_in", state_in, state_bytes)};
+    s = check_overlaps(outs, ins);
+    if (s != IDA_OK) return s;
     int num_sms = 0;
     std::string why;
     s = device_ready(&num_sms, why);
@@ -440,10 +443,15 @@ ida_status ida_ssm_conv_backward(const void *x, const void *dout, const float *c
         }
         if (workspace_bytes < ida_ssm_conv_backward_workspace_bytes(B, N, C, W))
             return fail_with(IDA_ERR_ARG, "workspace is smaller than ida_ssm_conv_backward_workspace_bytes");
-        const long long n = (long long)B * N;
-        if (rows_overlap(x, ldx, C, dx, lddx, C, n, dtype) || rows_overlap(dout, C, C, dx, lddx, C, n, dtype))
-            return fail_with(IDA_ERR_ARG, "dx must not overlap x or dout");
     }
+    const long long n = (long long)B * N;
+    const size_t wb = (size_t)C * W * 4, bb = (size_t)C * 4;
+    const Rows outs[] = {rows_of("dx", dx, lddx, C, n, dtype), dense("dconv_w", dconv_w, wb), dense("dconv_b", dconv_b, bb),
+                         dense("workspace", workspace, ida_ssm_conv_backward_workspace_bytes(B, N, C, W))};
+    const Rows ins[] = {rows_of("x", x, ldx, C, n, dtype), rows_of("dout", dout, C, C, n, dtype),
+                        dense("conv_w", work ? conv_w : nullptr, wb), dense("conv_b", work ? conv_b : nullptr, bb)};
+    s = check_overlaps(outs, ins);
+    if (s != IDA_OK) return s;
     int num_sms = 0;
     std::string why;
     s = device_ready(&num_sms, why);

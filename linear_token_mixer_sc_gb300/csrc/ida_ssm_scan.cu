@@ -319,8 +319,6 @@ ida_status ida_ssm_scan(const void *x, const void *b, const void *c, const void 
     const size_t state_bytes = (size_t)B * H * M * d * sizeof(float);
     if (misaligned16(state_in) || misaligned16(final_state) || misaligned16(workspace))
         return fail_with(IDA_ERR_ARG, "state_in, final_state and workspace must be 16-byte aligned");
-    if (overlap(state_in, state_bytes, final_state, state_bytes))
-        return fail_with(IDA_ERR_ARG, "state_in and final_state must not overlap");
     if (N > 0) {
         const void *ptrs[] = {x, b, c, a_log, dt_bias, D, y};
         for (const void *p : ptrs) {
@@ -329,11 +327,19 @@ ida_status ida_ssm_scan(const void *x, const void *b, const void *c, const void 
         }
         if (!dt || (reinterpret_cast<uintptr_t>(dt) % (dtype == IDA_F32 ? 4 : 2)))
             return fail_with(IDA_ERR_ARG, "dt must be an aligned pointer");
-        const long long n = (long long)B * N, w = (long long)H * d, bc = (long long)G * M;
-        if (rows_overlap(y, w, w, x, ldx, w, n, dtype) || rows_overlap(y, w, w, b, ldb, bc, n, dtype) ||
-            rows_overlap(y, w, w, c, ldc, bc, n, dtype) || rows_overlap(y, w, w, dt, lddt, H, n, dtype))
-            return fail_with(IDA_ERR_ARG, "y must not overlap x, b, c or dt");
     }
+    const long long rows = (long long)B * N, w = (long long)H * d, bc = (long long)G * M;
+    const size_t par = N > 0 ? (size_t)H * 4 : 0;
+    const auto refuse_overlaps = [&](size_t workspace_used) {
+        const Rows outs[] = {rows_of("y", y, w, w, rows, dtype), dense("final_state", final_state, state_bytes),
+                             dense("workspace", workspace, workspace_used)};
+        const Rows ins[] = {rows_of("x", x, ldx, w, rows, dtype), rows_of("b", b, ldb, bc, rows, dtype), rows_of("c", c, ldc, bc, rows, dtype),
+                            rows_of("dt", dt, lddt, H, rows, dtype), dense("a_log", a_log, par), dense("dt_bias", dt_bias, par),
+                            dense("D", D, par), dense("state_in", state_in, state_bytes)};
+        return check_overlaps(outs, ins);
+    };
+    s = refuse_overlaps(0);
+    if (s != IDA_OK) return s;
     int num_sms = 0;
     std::string why;
     s = device_ready(&num_sms, why);
@@ -351,6 +357,8 @@ ida_status ida_ssm_scan(const void *x, const void *b, const void *c, const void 
     const bool chunked = dtype == IDA_BF16;
     const size_t need = scan_plan(B, H, N, d, M, chunked, num_sms, a.seg, a.segs, a.fine);
     if (need > 0 && workspace && workspace_bytes >= need) {
+        s = refuse_overlaps(need);
+        if (s != IDA_OK) return s;
         a.seg_state = static_cast<float *>(workspace);
         a.seg_log = a.seg_state + (size_t)B * H * a.segs * a.fine * M * d;
     } else {

@@ -190,9 +190,15 @@ extern "C" ida_status ida_ssm_step(const void *xbc, const void *dt, const float 
         return fail_with(IDA_ERR_ARG, "dt must be an aligned pointer");
     if (W > 1 && (!conv_state || misaligned16(conv_state)))
         return fail_with(IDA_ERR_ARG, "conv_state must be a 16-byte aligned pointer");
-    if (rows_overlap(xbc, ldx, C, y, (long long)H * d, (long long)H * d, B, dtype) ||
-        rows_overlap(dt, lddt, H, y, (long long)H * d, (long long)H * d, B, dtype))
-        return fail_with(IDA_ERR_ARG, "y must not overlap xbc or dt");
+    const long long w = (long long)H * d;
+    const size_t par = (size_t)H * 4;
+    const Rows outs[] = {rows_of("y", y, w, w, B, dtype), dense("conv_state", conv_state, (size_t)B * (W - 1) * C * 4),
+                         dense("state", state, (size_t)B * H * M * d * 4)};
+    const Rows ins[] = {rows_of("xbc", xbc, ldx, C, B, dtype), rows_of("dt", dt, lddt, H, B, dtype),
+                        dense("conv_w", conv_w, (size_t)C * W * 4), dense("conv_b", conv_b, (size_t)C * 4), dense("a_log", a_log, par),
+                        dense("dt_bias", dt_bias, par), dense("D", D, par)};
+    s = check_overlaps(outs, ins);
+    if (s != IDA_OK) return s;
     int num_sms = 0;
     std::string why;
     s = device_ready(&num_sms, why);

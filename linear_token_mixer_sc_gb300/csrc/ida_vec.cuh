@@ -68,20 +68,39 @@ ida_status check_call(int d, int R, int M, int W, int dtype, int flags, int *num
 
 inline bool misaligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) != 0; }
 
-// [a, a + na) and [b, b + nb) share a byte
-inline bool overlap(const void *a, size_t na, const void *b, size_t nb) {
-    const char *pa = static_cast<const char *>(a), *pb = static_cast<const char *>(b);
-    return a && b && pa < pb + nb && pb < pa + na;
-}
-// Whether rows of wa elements, lda apart, share any with rows of wb, ldb apart (slices of the same wider
-// rows do not).
-inline bool rows_overlap(const void *a, long long lda, long long wa, const void *b, long long ldb, long long wb,
-                         long long rows, int dtype) {
+// Rows of a call's tensor in memory: `rows` of w bytes, ld bytes apart.
+struct Rows {
+    const char *name;
+    const void *p;
+    long long ld, w, rows;
+};
+inline Rows rows_of(const char *name, const void *p, long long ld, long long w, long long rows, int dtype) {
     const long long es = dtype == IDA_F32 ? 4 : 2;
-    if (rows < 1 || !overlap(a, ((rows - 1) * lda + wa) * es, b, ((rows - 1) * ldb + wb) * es)) return false;
-    const long long by = static_cast<const char *>(b) - static_cast<const char *>(a), ld = lda * es;
-    const long long off = (by % ld + ld) % ld;
-    return lda != ldb || off < wa * es || off + wb * es > ld;
+    return {name, p, ld * es, w * es, rows};
+}
+inline Rows dense(const char *name, const void *p, size_t bytes) { return {name, p, (long long)bytes, (long long)bytes, 1}; }
+
+// Whether two share a byte (slices of the same wider rows do not; rows at two strides whose ranges meet count
+// as sharing).
+inline bool overlap(const Rows &a, const Rows &b) {
+    if (!a.p || !b.p || a.rows < 1 || b.rows < 1 || a.w < 1 || b.w < 1) return false;
+    const uintptr_t pa = reinterpret_cast<uintptr_t>(a.p), pb = reinterpret_cast<uintptr_t>(b.p);
+    if (pa >= pb + (uintptr_t)((b.rows - 1) * b.ld + b.w) || pb >= pa + (uintptr_t)((a.rows - 1) * a.ld + a.w)) return false;
+    if (a.ld != b.ld || (a.rows == 1 && b.rows == 1)) return true;
+    const long long by = (long long)(pb - pa), off = (by % a.ld + a.ld) % a.ld;
+    return off < a.w || off + b.w > a.ld;
+}
+
+// Outputs share no byte with inputs or one another.
+template <int NO, int NI>
+ida_status check_overlaps(const Rows (&out)[NO], const Rows (&in)[NI]) {
+    for (int i = 0; i < NO; ++i) {
+        for (int k = 0; k < NI; ++k)
+            if (overlap(out[i], in[k])) return fail_with(IDA_ERR_ARG, std::string(out[i].name) + " must not overlap " + in[k].name);
+        for (int k = i + 1; k < NO; ++k)
+            if (overlap(out[i], out[k])) return fail_with(IDA_ERR_ARG, std::string(out[i].name) + " must not overlap " + out[k].name);
+    }
+    return IDA_OK;
 }
 
 // Device set-up of a call whose own arguments have been checked: the number of SMs, and any
