@@ -385,8 +385,8 @@ IDA_API ida_status ida_rope(void *q, void *k, int B, int N, int H, int R,
  * [x (H d) | b (G M) | c (G M)].  Inputs are rows inside wider ones (a slice of a
  * projection's output): position t of row r starts ld elements behind the one before it,
  * (r N + t) ld elements behind the pointer.  x, b, c and the convolution's rows start on
- * 16-byte boundaries and their strides are multiples of 8; dt needs its element's alignment
- * only.  y, out and dout are dense.
+ * 16-byte boundaries and their strides are multiples of 8; dt, ddt and the gradients of
+ * parameters need their element's alignment only.  y, out and dout are dense.
  *   a_log, dt_bias, D  [H] float;  conv_w [C, W] (tap W-1 on the current position),
  *   conv_b [C] float;  scan states [B, H, M, d] float;  conv states [B, W-1, C] float, the
  *   raw rows of the last W-1 positions, oldest first (zero before the first position).

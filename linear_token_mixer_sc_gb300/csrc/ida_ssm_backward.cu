@@ -653,6 +653,8 @@ ida_status ida_ssm_scan_backward(const void *x, const void *b, const void *c, co
     if (s != IDA_OK) return s;
     if (H == 0) return IDA_OK;
     if (!da_log || !ddt_bias || !dD) return fail_with(IDA_ERR_ARG, "null gradient pointer");
+    if (misaligned4(da_log) || misaligned4(ddt_bias) || misaligned4(dD))
+        return fail_with(IDA_ERR_ARG, "da_log, ddt_bias and dD must be 4-byte aligned");
     const bool work = B > 0 && N > 0;
     if (work) {
         const void *ptrs[] = {x, b, c, a_log, dt_bias, D, dy, dx, db, dc, workspace};

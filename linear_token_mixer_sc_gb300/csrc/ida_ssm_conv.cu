@@ -434,6 +434,7 @@ ida_status ida_ssm_conv_backward(const void *x, const void *dout, const float *c
     if (s == IDA_OK) s = check_conv(B, N, C, lddx, dtype, W);
     if (s != IDA_OK) return s;
     if (!dconv_w || !dconv_b) return fail_with(IDA_ERR_ARG, "null gradient pointer");
+    if (misaligned4(dconv_w) || misaligned4(dconv_b)) return fail_with(IDA_ERR_ARG, "dconv_w and dconv_b must be 4-byte aligned");
     const bool work = B > 0 && N > 0;
     if (work) {
         const void *ptrs[] = {x, dout, conv_w, conv_b, dx, workspace};

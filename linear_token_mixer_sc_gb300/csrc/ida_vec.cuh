@@ -67,6 +67,7 @@ ida_status fail_with(ida_status s, const std::string &why);
 ida_status check_call(int d, int R, int M, int W, int dtype, int flags, int *num_sms, std::string &why);
 
 inline bool misaligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) != 0; }
+inline bool misaligned4(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3u) != 0; }
 
 // Rows of a call's tensor in memory: `rows` of w bytes, ld bytes apart.
 struct Rows {
