@@ -422,10 +422,16 @@ def ida_rope(q: torch.Tensor, k: torch.Tensor | None = None, pos0: int = 0, base
 # ---- the selective mixer and the residual pre-norm --------------------------------------------
 
 def _placed(fn):
-    """Run ``fn`` with its first tensor's device and the given stream current, so that what it
-    allocates belongs to the stream its kernels run on."""
+    """Give ``fn`` a keyword ``stream`` (a torch.cuda.Stream; None: the current one), and run it with its
+    first tensor's device and that stream current, so that what it allocates belongs to the stream its
+    kernels run on."""
+    name = fn.__code__.co_varnames[0]
+
     @functools.wraps(fn)
-    def call(first, *args, stream=None, **kw):
+    def call(*args, stream=None, **kw):
+        first = args[0] if args else kw.get(name)
+        if first is None:
+            raise TypeError(f"{fn.__name__}() needs {name}")
         dev = first.get_device()
         if dev < 0:
             raise ValueError(f"{fn.__name__}: expected CUDA tensors")
@@ -433,11 +439,11 @@ def _placed(fn):
             if stream.device_index != dev:
                 raise ValueError(f"{fn.__name__}: the stream is on another device than the tensors")
             with torch.cuda.stream(stream):
-                return fn(first, *args, **kw)
+                return fn(*args, **kw)
         if dev != _current_device():
             with torch.cuda.device(dev):
-                return fn(first, *args, **kw)
-        return fn(first, *args, **kw)
+                return fn(*args, **kw)
+        return fn(*args, **kw)
     return call
 
 

@@ -1,5 +1,5 @@
 """Arguments of the selective mixer and of the pre-norm that no kernel may see: gradients of parameters
-off their element's alignment."""
+off their element's alignment; and how the binding's calls take their arguments."""
 
 import pytest
 import torch
@@ -26,3 +26,37 @@ def test_parameter_gradients_off_their_alignment(lib, name, outputs):
         for off in (1, 2, 3, 6):
             assert _call(lib, name, {**base, k: base[k] + off}) == ARG and "aligned" in binding.ida_last_error(), (k, off)
         assert _call(lib, name, {**base, k: base[k] + 4}) == binding.IDA_ERR_CUDA  # taken, but there is no device
+
+
+def test_the_first_argument_by_its_name(lib):
+    """Refused for what it is (a host tensor), not for how it is given."""
+    x, w, b = torch.zeros(1, 8, 16), torch.zeros(16, 4), torch.zeros(16)
+    p = {k: torch.zeros(1) for k in ("a_log", "dt_bias", "D")}
+    scan = dict(x=x[:, :, None], b=x[:, :, None], c=x[:, :, None], dt=x[..., :1], params=p)
+    calls = [(binding.ida_ssm_conv, dict(x=x, conv_w=w, conv_b=b)),
+             (binding.ida_ssm_conv_backward, dict(x=x, dout=x, conv_w=w, conv_b=b)),
+             (binding.ida_ssm_scan, scan), (binding.ida_ssm_scan_backward, dict(scan, dy=x[:, :, None])),
+             (binding.ida_ssm_step, dict(xbc=x[0], dt=x[0, :, :1], params=p, conv_state=x, state=x, groups=1)),
+             (binding.ida_rmsnorm, dict(x=x, w=b)), (binding.ida_rmsnorm_backward, dict(r=x, w=b, dy=x))]
+    for fn, kw in calls:
+        with pytest.raises(ValueError, match="CUDA"):
+            fn(**kw)
+        first = next(iter(kw))
+        with pytest.raises(ValueError, match="CUDA"):
+            fn(kw[first], **{k: v for k, v in kw.items() if k != first})
+        with pytest.raises(TypeError, match=first):
+            fn()
+
+
+@pytest.mark.gpu
+def test_by_name_and_on_a_stream_given_by_name(lib):
+    x = torch.randn(2, 40, 64, device="cuda").bfloat16()
+    w, b = torch.randn(64, 4, device="cuda"), torch.randn(64, device="cuda")
+    want = binding.ida_ssm_conv(x, w, b)[0]
+    norm = binding.ida_rmsnorm(x, b)[0]
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    got = [binding.ida_ssm_conv(x=x, conv_w=w, conv_b=b)[0], binding.ida_ssm_conv(conv_b=b, x=x, stream=side, conv_w=w)[0]]
+    norms = [binding.ida_rmsnorm(w=b, x=x)[0], binding.ida_rmsnorm(x=x, w=b, stream=side)[0]]
+    torch.cuda.synchronize()
+    assert all(torch.equal(t, want) for t in got) and all(torch.equal(t, norm) for t in norms)
