@@ -454,6 +454,12 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
                       lambda dev: torch.cuda.current_stream(dev).cuda_stream)
 
 
+def _fits(*sizes: int) -> None:
+    """Sizes that the C ABI's ints hold (ctypes would cut off the others' high bits)."""
+    if max(sizes) > 0x7FFFFFFF or min(sizes) < -0x80000000:
+        raise ValueError(f"a size is above 2^31 - 1: {sizes}")
+
+
 def _misfit(name: str, t: torch.Tensor, shape, dtype):
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
@@ -502,18 +508,22 @@ def _work_buffer(given: torch.Tensor | None, nbytes: int, dev: int):
 
 
 def ida_ssm_conv_backward_workspace_bytes(B: int, N: int, C: int, W: int) -> int:
+    _fits(B, N, C, W)
     return int(load().ida_ssm_conv_backward_workspace_bytes(B, N, C, W))
 
 
 def ida_ssm_scan_workspace_bytes(B: int, H: int, N: int, d: int, G: int, M: int, dtype: int) -> int:
+    _fits(B, H, N, d, G, M, dtype)
     return int(load().ida_ssm_scan_workspace_bytes(B, H, N, d, G, M, dtype))
 
 
 def ida_ssm_scan_backward_workspace_bytes(B: int, H: int, N: int, d: int, G: int, M: int, dtype: int) -> int:
+    _fits(B, H, N, d, G, M, dtype)
     return int(load().ida_ssm_scan_backward_workspace_bytes(B, H, N, d, G, M, dtype))
 
 
 def ida_rmsnorm_backward_workspace_bytes(rows: int, D: int) -> int:
+    _fits(rows, D)
     return int(load().ida_rmsnorm_backward_workspace_bytes(rows, D))
 
 
@@ -527,6 +537,7 @@ def ida_ssm_conv(x: torch.Tensor, conv_w: torch.Tensor, conv_b: torch.Tensor, st
     dt, dev = _dtype_code(x), x.get_device()
     B, N, C = x.shape
     W = conv_w.shape[1]
+    _fits(B, N, C, W)
     xp, ldx = _rows("x", x, x.shape, x.dtype, dev, 2)
     if out is None:
         out = torch.empty((B, N, C), dtype=x.dtype, device=x.device)
@@ -553,6 +564,7 @@ def ida_ssm_conv_backward(x: torch.Tensor, dout: torch.Tensor, conv_w: torch.Ten
     dt, dev = _dtype_code(x), x.get_device()
     B, N, C = x.shape
     W = conv_w.shape[1]
+    _fits(B, N, C, W)
     f32 = torch.float32
     xp, ldx = _rows("x", x, x.shape, x.dtype, dev, 2)
     wp, bp = _dense("conv_w", conv_w, (C, W), f32, dev), _dense("conv_b", conv_b, (C,), f32, dev)
@@ -574,6 +586,7 @@ def _scan_inputs(x, b, c, dt, params):
     dev, f32 = x.get_device(), torch.float32
     B, N, H, d = x.shape
     G, M = b.shape[2:]
+    _fits(B, N, H, d, G, M)
     xp, ldx = _rows("x", x, x.shape, x.dtype, dev, 2)
     bp, ldb = _rows("b", b, (B, N, G, M), x.dtype, dev, 2)
     cp, ldc = _rows("c", c, (B, N, G, M), x.dtype, dev, 2)
@@ -652,6 +665,7 @@ def ida_ssm_step(xbc: torch.Tensor, dt: torch.Tensor, params: dict, conv_state: 
     _, H, M, d = state.shape
     conv_w = params["conv_w"]
     W = conv_w.shape[1]
+    _fits(B, H, M, d, W, groups)
     if C != H * d + 2 * groups * M:
         raise ValueError("xbc must have H d + 2 G M channels")
     xp, ldx = _rows("xbc", xbc, (B, C), xbc.dtype, dev, 1)
@@ -681,6 +695,7 @@ def ida_rmsnorm(x: torch.Tensor, w: torch.Tensor, residual: torch.Tensor | None 
     dt, dev = _dtype_code(x), x.get_device()
     D = x.shape[-1]
     rows = x.numel() // D if D else 0
+    _fits(rows, D, group)
     xp, wp = _dense("x", x, x.shape, x.dtype, dev), _dense("w", w, (D,), torch.float32, dev)
     rp = None if residual is None else _dense("residual", residual, x.shape, x.dtype, dev)
     if residual is not None and res_out is None:
@@ -710,6 +725,7 @@ def ida_rmsnorm_backward(r: torch.Tensor, w: torch.Tensor, dy: torch.Tensor, dre
     dt, dev = _dtype_code(r), r.get_device()
     D = r.shape[-1]
     rows = r.numel() // D if D else 0
+    _fits(rows, D)
     rp, wp = _dense("r", r, r.shape, r.dtype, dev), _dense("w", w, (D,), torch.float32, dev)
     gp = _dense("dy", dy, r.shape, r.dtype, dev)
     sp = None if dres is None else _dense("dres", dres, r.shape, r.dtype, dev)

@@ -157,7 +157,7 @@ __global__ void __launch_bounds__(TPR > 256 ? TPR : 256) rmsnorm_kernel(NormArgs
 template <typename E, int TPR, int NV>
 static void launch_norm_nv(const NormArgs &a, cudaStream_t st) {
     constexpr int BT = TPR > 256 ? TPR : 256, RPB = BT / TPR;
-    rmsnorm_kernel<E, TPR, NV><<<(unsigned)((a.rows + RPB - 1) / RPB), BT, 0, st>>>(a);
+    rmsnorm_kernel<E, TPR, NV><<<(unsigned)(((long long)a.rows + RPB - 1) / RPB), BT, 0, st>>>(a);
 }
 
 template <typename E, int TPR>
@@ -316,8 +316,8 @@ __global__ void __launch_bounds__(1024) sum_rows_kernel(const float *part, float
 // (four rows at a time 29.0, 304 blocks 42.7).
 constexpr int NORM_BWD_BLOCKS = 1216;
 static int norm_bwd_blocks(int rows, int rb) {
-    const int want = (rows + rb - 1) / rb;
-    return want < NORM_BWD_BLOCKS ? (want > 0 ? want : 1) : NORM_BWD_BLOCKS;
+    const long long want = ((long long)rows + rb - 1) / rb;
+    return want < NORM_BWD_BLOCKS ? (want > 0 ? (int)want : 1) : NORM_BWD_BLOCKS;
 }
 
 template <typename E>

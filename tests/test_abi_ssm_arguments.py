@@ -1,5 +1,5 @@
 """Arguments of the selective mixer and of the pre-norm that no kernel may see: gradients of parameters
-off their element's alignment; and how the binding's calls take their arguments."""
+off their element's alignment, sizes behind 2^31; and how the binding's calls take their arguments."""
 
 import pytest
 import torch
@@ -60,3 +60,44 @@ def test_by_name_and_on_a_stream_given_by_name(lib):
     norms = [binding.ida_rmsnorm(w=b, x=x)[0], binding.ida_rmsnorm(x=x, w=b, stream=side)[0]]
     torch.cuda.synchronize()
     assert all(torch.equal(t, want) for t in got) and all(torch.equal(t, norm) for t in norms)
+
+
+def test_sizes_behind_31_bits(lib):
+    """Sizes of 2^32 and a few do not pass for the few."""
+    far = (1 << 32) + 5
+    for call in (lambda: binding.ida_ssm_conv_backward_workspace_bytes(2, far, 32, 4),
+                 lambda: binding.ida_ssm_scan_workspace_bytes(1, 4, far, 64, 2, 16, 1),
+                 lambda: binding.ida_ssm_scan_backward_workspace_bytes(far, 4, 9, 64, 2, 16, 1),
+                 lambda: binding.ida_rmsnorm_backward_workspace_bytes(far, 256)):
+        with pytest.raises(ValueError, match="2\\^31"):
+            call()
+
+
+@pytest.mark.gpu
+def test_tensors_with_sizes_behind_31_bits(lib):
+    """Positions and rows that share one stored row, so that nothing large is behind them."""
+    far, f = (1 << 32) + 5, dict(device="cuda")
+    x, w, b = torch.zeros(1, 1, 8, **f).expand(1, far, 8), torch.zeros(8, 4, **f), torch.zeros(8, **f)
+    bc, dt = x.unsqueeze(2), x[..., :1]
+    p = {"a_log": b[:1], "dt_bias": b[:1], "D": b[:1]}
+    for call in (lambda: binding.ida_ssm_conv(x, w, b), lambda: binding.ida_ssm_conv_backward(x, x, w, b),
+                 lambda: binding.ida_ssm_scan(bc, bc, bc, dt, p), lambda: binding.ida_ssm_scan_backward(bc, bc, bc, dt, p, bc),
+                 lambda: binding.ida_ssm_step(x[0], dt[0], {**p, "conv_w": w, "conv_b": b}, w, w[:, :, None, None], 1)):
+        with pytest.raises(ValueError, match="2\\^31"):
+            call()
+
+
+@pytest.mark.gpu
+def test_as_many_rows_as_an_int_counts(lib):
+    """2^31 - 1 rows of 8 channels: the last ones' norms, and a row more is refused."""
+    if torch.cuda.mem_get_info()[0] < 100 << 30:
+        pytest.skip("needs 70 GB")
+    rows = (1 << 31) - 1
+    store = torch.zeros(rows + 1, 8, dtype=torch.bfloat16, device="cuda")
+    x, w = store[:rows], torch.ones(8, device="cuda")
+    x[-3:] = torch.arange(24, device="cuda").view(3, 8) - 7
+    out = binding.ida_rmsnorm(x, w)[0]
+    assert torch.equal(out[-3:], binding.ida_rmsnorm(x[-3:].clone(), w)[0]) and not out[:9].any() and not out[rows - 9:-3].any()
+    del out
+    with pytest.raises(ValueError, match="2\\^31"):
+        binding.ida_rmsnorm(store, w)
