@@ -106,7 +106,7 @@ struct ChunkRows {
             fill_bc(s.c, s.ldc, c);
             fill_x(s.dy, (row * H + h) * d, (long long)H * d, dy);
         }
-        const float rate = expf(s.a_log[h]), bias = s.dt_bias[h];
+        const float rate = scan_rate(s.a_log[h]), bias = s.dt_bias[h];
         for (int t = threadIdx.x; t < chunk; t += blockDim.x) {
             float dl = 0.f, zz = 0.f;
             if (t < left) {
@@ -255,7 +255,7 @@ __global__ void __launch_bounds__(256) bwd_chunk_kernel(ScanBwdArgs s) {
     }
     if (!rev && warp == (int)blockDim.x / 32 - 1) {
         float la = 0.f;
-        const float rate = expf(s.a_log[unit % s.H]) * 1.4426950408889634f;
+        const float rate = scan_rate(s.a_log[unit % s.H]) * 1.4426950408889634f;
         for (int t = lane; t < Q; t += 32) la -= rate * r.delta[t];
         la = warp_sum(la);
         if (lane == 0) s.chunk_log[(size_t)unit * s.chunks + ch] = la;
@@ -458,7 +458,7 @@ __global__ void __launch_bounds__(256) bwd_main_kernel(ScanBwdArgs s) {
     }
     // w, and the gradients of dt and of the head's parameters: one warp, two positions a lane
     if (warp == 0) {
-        const float rate = expf(s.a_log[h]);
+        const float rate = scan_rate(s.a_log[h]);
         float ga = 0.f, gb = 0.f, gd = 0.f;
         for (int base = 0; base < len; base += 32) {
             const int t = base + lane;
@@ -475,7 +475,7 @@ __global__ void __launch_bounds__(256) bwd_main_kernel(ScanBwdArgs s) {
                 const float sig = 1.f / (1.f + expf(-r.z[t]));
                 const float ddt = (fmaf(bc[t], xdy[t], rw[t]) - rate * w) * sig;
                 from_float(static_cast<E *>(s.ddt) + ((size_t)b * N + t0 + t) * s.ldddt + h, ddt);
-                ga -= rate * r.delta[t] * w;
+                ga -= rate * (r.delta[t] * w);  // 0 where w is, whatever the rate
                 gb += ddt;
                 gd += xdy[t];
             }

@@ -363,7 +363,7 @@ __global__ void __launch_bounds__(BTH, 1)
             // 1 / (1 + e^-z) of D = log(1 + e^z) is 1 - e^-D
             const float ddt = (ks + ko + gg * ee + zf - rate * wt) * -expm1f(-delta);
             static_cast<__nv_bfloat16 *>(a.ddt)[((size_t)b * N + t0 + t) * a.ldddt + h] = __float2bfloat16_rn(ddt);
-            ga = -rate * delta * wt;
+            ga = -rate * (delta * wt);  // 0 where wt is, whatever the rate
             gb = ddt;
             gd = ee;
         }

@@ -306,7 +306,7 @@ __global__ void __launch_bounds__(CTH, 1)
         const int k = tid - 128;  // position of the chunk
         const __nv_bfloat16 *gdt = static_cast<const __nv_bfloat16 *>(a.dt) + (size_t)b * N * a.lddt + h;
         const float dt_bias = a.dt_bias[h];
-        const float rate2 = expf(a.a_log[h]) * 1.4426950408889634f;
+        const float rate2 = scan_rate(a.a_log[h]) * 1.4426950408889634f;
         const auto dt_of = [&](int i) {
             const int p = t_begin + i * SQ + k;
             return i < nch && p < t_end ? __bfloat162float(gdt[(size_t)p * a.lddt]) : 0.f;

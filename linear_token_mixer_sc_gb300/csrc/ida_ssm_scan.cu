@@ -57,7 +57,7 @@ __global__ void __launch_bounds__(128 + SEQ_HELP) scan_seq_kernel(ScanArgs a) {
         // helpers: a thread keeps its 16-byte column of [b | c | x] and walks the tile's rows
         const int ht = tid - cols, nb = M / 4, nx = min(cols, d - j0) / 4, vpr = (STATE ? nb : 2 * nb) + nx;
         const float *dt = static_cast<const float *>(a.dt) + (size_t)b * N * a.lddt + h;
-        const float rate = expf(a.a_log[h]), dt_bias = a.dt_bias[h];
+        const float rate = scan_rate(a.a_log[h]), dt_bias = a.dt_bias[h];
         const float *src = nullptr;
         long long ld = 0;
         int at = 0, rs = 0;  // the column's place in a tile, and its row stride there

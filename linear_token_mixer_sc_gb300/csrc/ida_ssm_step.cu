@@ -95,7 +95,7 @@ __global__ void __launch_bounds__(STEP_THREADS, 4) step_kernel(StepArgs a) {
             for (int j = 0; j < W - 1; ++j) tail[(size_t)j * C + c] = rx[j];
         }
         const float delta = softplus(to_float(static_cast<const E *>(a.dt)[(size_t)b * a.lddt + h]) + a.dt_bias[h]);
-        const float decay = expf(-expf(a.a_log[h]) * delta);
+        const float decay = expf(-scan_rate(a.a_log[h]) * delta);
         __syncthreads();
         float y[4] = {0.f, 0.f, 0.f, 0.f};
         if (worker) {

@@ -65,7 +65,7 @@ struct Rate2 {
     float hi, lo;
 };
 __device__ __forceinline__ Rate2 rate2_of(float a_log) {
-    const double r = exp((double)a_log) * 1.4426950408889634;
+    const double e = exp((double)a_log), r = (e > 2e38 ? 2e38 : e) * 1.4426950408889634;
     const float hi = (float)r;
     return {hi, (float)(r - (double)hi)};
 }

@@ -56,6 +56,13 @@ __device__ __forceinline__ void from_float(__nv_bfloat16 *p, float x) { *p = __f
 // log(1 + e^z) without overflow; its derivative is 1 / (1 + e^-z).
 __device__ __forceinline__ float softplus(float z) { return fmaxf(z, 0.f) + log1pf(expf(-fabsf(z))); }
 
+// The rate e^a_log of a head, 2e38 at most: finite, 1 / ln 2 times it too, so that a step of 0 decays
+// nothing.  (At 2e38 a step of 1e-36 decays to 0 already.)
+__device__ __forceinline__ float scan_rate(float a_log) {
+    const float r = expf(a_log);
+    return r > 2e38f ? 2e38f : r;
+}
+
 // Programmatic dependent launches (launch_dependent): wait for the launch before in the stream, and let
 // the one behind take its place on the SMs.
 __device__ __forceinline__ void dependent_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }

@@ -9,9 +9,10 @@ import pytest
 import torch
 
 from linear_token_mixer_sc_gb300 import binding, build
+from oracle import ida_ssm as orc
 from tests import ssm_cases as sc
-from tests.ssm_cases import DT, U32, worst
-from tests.test_gpu_ssm import _done, _on_gpu, _scan_bounds, _scan_inputs, _scan_ref
+from tests.ssm_cases import DT, HALF, U32, worst
+from tests.test_gpu_ssm import NAMES, _done, _on_gpu, _scan_bounds, _scan_inputs, _scan_ref
 
 pytestmark = pytest.mark.gpu
 
@@ -20,6 +21,21 @@ pytestmark = pytest.mark.gpu
 def _lib():
     build.build()
     binding.load()
+
+
+def check_scan_gradients(g, row, C, H, d, G, M, p, dy, dtype="bf16"):
+    x, b, c = (t.contiguous() for t in sc.split(row[..., :C].double(), H, d, G, M))
+    q = sc.to64(p)
+    leaves = [x, b, c, row[..., C:C + H].double(), q["a_log"], q["dt_bias"], q["D"]]
+    ref = orc.grads(lambda *v: orc.scan(*v)[0], leaves, dy.double())
+    size = orc.scan_grad_sizes(*leaves, dy.double())
+    chain = (8 * row.shape[1] + 2 * d + 2 * M + 64) * U32
+    for k, name in enumerate(NAMES):
+        if k < 4:
+            bound = HALF[dtype] * ref[k].abs() + ((3.1 * 2.0 ** -8 if dtype == "bf16" else 0.0) + chain) * size[k]
+        else:
+            bound = ((2.0 ** -15 if dtype == "bf16" else 0.0) + chain) * size[k]
+        assert worst(g[name], ref[k], bound) <= 1, name
 
 
 def _large_steps(name, N, H):
@@ -104,3 +120,55 @@ def test_fp32_conv_gradients_where_the_sigmoid_is_small():
     ref = sg * (1 + p * (1 - sg))
     bound = U32 * ((6 * sg + 1) * p.abs() * sg + 10 * ref.abs() + sg)
     assert worst(g["x"], ref, bound) <= 1
+
+
+def _rates(name, H):
+    """Parameters of heads whose decays are 0 at every step, or 1."""
+    if name == "e^a_log above fp32":
+        return {"a_log": torch.full((H,), 100.0)}
+    if name == "e^a_log just within fp32":
+        return {"a_log": torch.full((H,), 88.5)}
+    return {"a_log": torch.full((H,), 60.0), "dt_bias": torch.full((H,), -60.0)}  # e^a_log times the step about 1
+
+
+RATES = ["e^a_log above fp32", "e^a_log just within fp32", "a large rate and small steps"]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("name", RATES)
+def test_rates_at_the_end_of_the_range(name, dtype):
+    """Finite a_log of any size: a prompt that ends inside a tile, its gradients, a position."""
+    case = (1, 75, 2, 64, 1, 64, dtype, True, False)
+    B, N, H, d, G, M = case[:6]
+    p, row, s, C = _scan_inputs(*case)
+    p = {**p, **_rates(name, H)}
+    dp, args = sc.cuda(p), _on_gpu(row, C, H, d, G, M)
+    y, X = binding.ida_ssm_scan(*args, dp, state_in=s.cuda(), final_state=True)
+    dy = torch.randn(B, N, H, d, generator=sc.gen(11)).to(DT[dtype])
+    g = binding.ida_ssm_scan_backward(*args, dp, dy.cuda())
+    q = {**sc.params(H, C, 4, 9), **p, "conv_w": torch.zeros(C, 4), "conv_b": torch.randn(C, generator=sc.gen(9))}
+    tail, Z = torch.zeros(N, 3, C, device="cuda"), s.cuda().expand(N, -1, -1, -1).contiguous()
+    z = binding.ida_ssm_step(row[0, :, :C].cuda(), row[0, :, C:C + H].cuda(), sc.cuda(q), tail, Z, G)
+    _done()
+    ry, rX = _scan_ref(row, C, H, d, G, M, p, s)
+    ya, Xa = _scan_ref(row, C, H, d, G, M, p, s, absolute=True)
+    by, bX = _scan_bounds(dtype, N, ry, ya, Xa)
+    assert worst(y, ry, by) <= 1
+    assert worst(X, rX, bX) <= 1
+    # the step's convolution is SiLU of the bias, a constant: one more rounding chain before the products
+    rz, _, rZ = orc.step(row[0, :, :C].double(), row[0, :, C:C + H].double(), sc.to64(q),
+                         torch.zeros(N, 3, C, dtype=torch.float64), s.double().expand(N, -1, -1, -1), G)
+    ax, ab, ac = sc.split(orc.conv(torch.zeros(N, 1, C, dtype=torch.float64), sc.to64(q)["conv_w"], sc.to64(q)["conv_b"])[0].abs(),
+                          H, d, G, M)
+    za, Za = orc.scan(ax, ab, ac, row[0, :, None, C:C + H].double(), sc.to64(q)["a_log"], sc.to64(q)["dt_bias"],
+                      sc.to64(q)["D"].abs(), s.double().abs().expand(N, -1, -1, -1))
+    n = (M + 160) * U32
+    # the step is off by (|z| + 10) u of itself, z its rounded argument, and the exponent of the decay E = rate
+    # times step by 5 u more: the decay by a E (|z| + 15) u, which times the state before comes on top
+    arg = row[0, :, C:C + H].double() + q["dt_bias"].double()
+    E = torch.exp(q["a_log"].double()) * orc.step_size(row[0, :, C:C + H].double(), q["dt_bias"].double())
+    far = (torch.exp(-E) * E * (arg.abs() + 15) * U32)[..., None, None] * s.double().abs()
+    zfar = (ac[:, 0].repeat_interleave(H // G, 1)[..., None] * far).sum(2)
+    assert worst(z, rz, HALF[dtype] * rz.abs() + n * za[:, 0] + zfar) <= 1
+    assert worst(Z, rZ, n * Za + far) <= 1
+    check_scan_gradients(g, row, C, H, d, G, M, p, dy, dtype)
