@@ -1,5 +1,6 @@
 """The selective mixer at finite inputs far from the usual ones: positions that forget everything, long
-runs of them, arguments where a sigmoid is small.
+runs of them, rates at the end of fp32, arguments where a sigmoid is small; and its single position to
+fp32 accuracy.
 
 Bounds as in ``test_gpu_ssm.py`` where nothing else is said.
 """
@@ -88,6 +89,16 @@ def test_scan_after_positions_that_forget(name, dtype):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("name", LARGE)
+def test_scan_gradients_after_positions_that_forget(name, dtype):
+    row, _, C, p, shape = _large_case(name, dtype, 140)
+    dy = torch.randn(1, 140, *shape[:2], generator=sc.gen(11)).to(DT[dtype])
+    g = binding.ida_ssm_scan_backward(*_on_gpu(row, C, *shape), sc.cuda(p), dy.cuda())
+    _done()
+    check_scan_gradients(g, row, C, *shape, p, dy, dtype)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("split", [True, False], ids=["workspace", "no workspace"])
 def test_state_behind_a_long_run_of_positions_that_forget(dtype, split):
     """More than 2048 positions of log2 a below -2^20 each: their sum passes 2^31."""
@@ -172,3 +183,52 @@ def test_rates_at_the_end_of_the_range(name, dtype):
     assert worst(z, rz, HALF[dtype] * rz.abs() + n * za[:, 0] + zfar) <= 1
     assert worst(Z, rZ, n * Za + far) <= 1
     check_scan_gradients(g, row, C, H, d, G, M, p, dy, dtype)
+
+
+# (B, H, d, G, M, W, dtype)
+STEPS = [(2, 6, 72, 3, 128, 3, "f32"), (2, 3, 256, 1, 40, 1, "f32"), (3, 5, 128, 5, 64, 4, "f32"),
+         (2, 12, 64, 1, 64, 4, "bf16"), (1, 24, 16, 2, 16, 2, "bf16")]
+
+
+@pytest.mark.parametrize("case", STEPS, ids=str)
+def test_steps_to_fp32_accuracy(case):
+    """Three positions in a row, the error of every value followed through the formulas.  With u =
+    2^-24: expf, log1pf within 2 units (4 u); pre by W + 1 multiply-adds; SiLU's slope is below 1.1
+    and its evaluation is good to 7 u; softplus to u |z| + 10 u of its value."""
+    B, H, d, G, M, W, dtype = case
+    C, rep = H * d + 2 * G * M, H // G
+    p = sc.params(H, C, W, 7)
+    tail = torch.randn(B, W - 1, C, generator=sc.gen(1))
+    X = torch.randn(B, H, M, d, generator=sc.gen(2)) * 0.3
+    dp, dtail, dX = sc.cuda(p), tail.cuda(), X.cuda()
+    q, t64, X64 = sc.to64(p), tail.double(), X.double()
+    eX = torch.zeros_like(X64)
+    rate = torch.exp(q["a_log"])
+    for k in range(3):
+        row = sc.rows(B, 1, C, H, dtype, 40 + k)[:, 0]
+        r = row.cuda()
+        y = binding.ida_ssm_step(r[:, :C], r[:, C:C + H], dp, dtail, dX, G)
+        _done()
+        x64, dt64 = row[:, :C].double(), row[:, C:C + H].double()
+        rows = torch.cat([t64, x64[:, None]], 1)
+        pre_abs = q["conv_b"].abs() + (q["conv_w"].abs().T * rows.abs()).sum(1)
+        act = orc.conv(x64[:, None], q["conv_w"], q["conv_b"], t64)[0][:, 0]
+        ea = 1.1 * (W + 1) * U32 * pre_abs + 7 * U32 * act.abs()
+        (ax, ab, ac), (ex, eb, ec) = ([t.abs() for t in sc.split(v, H, d, G, M)] for v in (act, ea))
+        ab, ac, eb, ec = (t.repeat_interleave(rep, 1)[..., None] for t in (ab, ac, eb, ec))
+        ax, ex = ax[:, :, None], ex[:, :, None]
+        delta = orc.step_size(dt64, q["dt_bias"])
+        ed = U32 * ((dt64 + q["dt_bias"]).abs() + 10 * delta)
+        decay = torch.exp(-rate * delta)
+        edecay = decay * (5 * U32 * rate * delta + rate * ed + 4 * U32)
+        delta, ed, decay, edecay = (t[..., None, None] for t in (delta, ed, decay, edecay))
+        before = X64.abs()
+        ry, t64, X64 = orc.step(x64, dt64, q, t64, X64, G)
+        eX = (decay * eX + edecay * (before + eX) + delta * (ab * ex + eb * ax + eb * ex) +
+              (ed + 3 * U32 * delta) * ab * ax + 2 * U32 * (X64.abs() + decay * before))
+        D = q["D"].abs()[:, None]
+        terms = (ac * X64.abs()).sum(2) + D * ax[:, :, 0]
+        ey = ((ac + ec) * eX + ec * X64.abs()).sum(2) + D * ex[:, :, 0] + (M + 3) * U32 * terms
+        assert worst(y, ry, HALF[dtype] * ry.abs() + ey) <= 1
+        assert worst(dX, X64, eX + U32 * X64.abs()) <= 1
+        assert torch.equal(dtail.cpu().double(), t64)
