@@ -166,7 +166,7 @@ static void launch_norm_tpr(const NormArgs &a, int nv, cudaStream_t st) {
         launch_norm_nv<E, TPR, 1>(a, st);
     else if (nv <= 2)
         launch_norm_nv<E, TPR, 2>(a, st);
-    else
+    else if constexpr (TPR == 512 && Vec16<E>::n == 4)  // fp32 rows of more than 4096 channels
         launch_norm_nv<E, TPR, 4>(a, st);
 }
 
@@ -327,14 +327,14 @@ static int launch_norm_bwd(const NormBwdArgs &a, cudaStream_t st) {
     if (nt <= 512) {
         blocks = norm_bwd_blocks(a.rows, 2);
         rmsnorm_bwd_kernel<E, 1, 2><<<blocks, nt, 0, st>>>(a);
-    } else if (vecs <= 1024) {
+    } else if (vecs <= 1024) {  // all rows of bf16
         nt = ((vecs + 1) / 2 + 31) / 32 * 32;
         blocks = norm_bwd_blocks(a.rows, 2);
         rmsnorm_bwd_kernel<E, 2, 2><<<blocks, nt, 0, st>>>(a);
     } else {
         nt = ((vecs + 3) / 4 + 31) / 32 * 32;
         blocks = norm_bwd_blocks(a.rows, 1);
-        rmsnorm_bwd_kernel<E, 4, 1><<<blocks, nt, 0, st>>>(a);
+        if constexpr (Vec16<E>::n == 4) rmsnorm_bwd_kernel<E, 4, 1><<<blocks, nt, 0, st>>>(a);
     }
     return blocks;
 }
