@@ -392,7 +392,9 @@ IDA_API ida_status ida_rope(void *q, void *k, int B, int N, int H, int R,
  *   raw rows of the last W-1 positions, oldest first (zero before the first position).
  * Supported: d a multiple of 8 up to 256, M a multiple of 8 up to 128, G dividing H, W <= 4,
  * B*H <= 2^24, B*N <= 2^28.  States, sums and gradients of parameters are fp32 for both
- * dtypes.  exp(a_log) counts as 2e38 where it is above.  Non-finite inputs make the outputs of their own row and head (the row and group's
+ * dtypes.  With IDA_BF16 the scan and its gradients (of up to 128 channels) run on the tensor cores:
+ * the weights of pairs of positions, and the states where y and dx come of them, are rounded to
+ * bf16 there.  exp(a_log) counts as 2e38 where it is above.  Non-finite inputs make the outputs of their own row and head (the row and group's
  * heads for b and c) unspecified, earlier positions included, and the gradients that sum over
  * them (of parameters; of the group's b and c); no others.  Outputs (a workspace that is used and
  * the states that ida_ssm_step updates among them) that share bytes with inputs or with one another are

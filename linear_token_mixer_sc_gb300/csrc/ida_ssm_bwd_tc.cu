@@ -20,7 +20,7 @@
 // the MMAs.  What enters w through MMAs is exact in its operands: b, c, x, dy are bf16, X_0 and Z are
 // kept as the sum of three bf16 tiles.
 //
-// Chunks are independent: X_0 and Z of every chunk come from launch_ssm_states (forwards and
+// Chunks are independent: X_0 and Z of every chunk come from launch_ssm_chunk_states (forwards and
 // backwards) and a running sum over the chunks.  One CTA of 512 threads takes the heads of one
 // group (or a part of them) over one chunk: b, c and G once, db and dc added over the heads in TMEM,
 // so that no per-head rows go to memory where a group's heads stay in one CTA.  Per head: E, then

@@ -34,9 +34,10 @@
 // What bounds it: the chain c X_0 - scaled rows - P x - state of a chunk, 4600 cycles, of which the MMAs'
 // reads of shared memory are 2300.  4 x 4096 positions of 16 heads of 128 x 64: 36 us, 57.6 with the segment
 // states before it.  Its warps run different code, so loops stay short: with all of them unrolled (66 KB)
-// they waited for instructions, 60 us.  (All stages in one group of 256 threads, two CTAs per SM: 45 us,
-// 8500 cycles a chunk, most of them waits for the next stage.  D as a part of P, rounded with it: 55 us, but y's error is 2.3e-3
-// of its size instead of 1.8e-3, 1.7e-3 of which are its own rounding.  Four warps for the rows: 58 us.)
+// they waited for instructions, 60 us.  (All stages in one group of 256 threads, two CTAs per SM: 45 us for
+// the 36, 8500 cycles a chunk, most of them waits for the next stage.  When the whole took 56 us: D as a part
+// of P, rounded with it, 55, but y's error is 2.3e-3 of its size instead of 1.8e-3, 1.7e-3 of which are its own
+// rounding; four warps for the rows, 58.)
 // The tiles have the 128-byte swizzle that the MMA descriptors name, so one copy serves as a
 // K-major operand (b, c in G) and as an MN-major one (x, b in the state update, whose K is the
 // position).  The state stays in TMEM.
