@@ -181,3 +181,79 @@ def test_gradients_of_no_positions_are_zero():
         _done()
         assert g["x"].numel() == 0 and h["x"].numel() == 0
         assert not any(t.any() for t in (g["a_log"], g["dt_bias"], g["D"], h["conv_w"], h["conv_b"]))
+
+
+def _problem(dtype, B=3, N=1700, H=4, d=64, G=2, M=64):
+    p, row, s, C = _scan_inputs(B, N, H, d, G, M, dtype, True, False)
+    dy = torch.randn(B, N, H, d, generator=sc.gen(11)).to(sc.DT[dtype]).cuda()
+    return (B, H, N, d, G, M), _on_gpu(row, C, H, d, G, M), sc.cuda(p), s.cuda(), dy
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_what_a_workspace_held_before_does_not_matter(dtype):
+    """Results of split prompts and of gradients with workspaces full of NaN."""
+    sizes, args, p, s, dy = _problem(dtype)
+    code = binding.IDA_BF16 if dtype == "bf16" else binding.IDA_F32
+    n = binding.ida_ssm_scan_workspace_bytes(*sizes, code), binding.ida_ssm_scan_backward_workspace_bytes(*sizes, code)
+    full = [torch.full(((k + 3) // 4,), float("nan"), device="cuda") for k in n]
+    assert n[0] > 0
+    want = list(binding.ida_ssm_scan(*args, p, state_in=s, final_state=True))
+    got = list(binding.ida_ssm_scan(*args, p, state_in=s, final_state=True, workspace=full[0]))
+    full[0].fill_(float("nan"))
+    got.append(binding.ida_ssm_scan(*args, p, state_in=s, workspace=full[0])[0])
+    want.append(want[0])
+    got += binding.ida_ssm_scan_backward(*args, p, dy, workspace=full[1]).values()
+    want += binding.ida_ssm_scan_backward(*args, p, dy).values()
+    x, w, b = dy.flatten(2), torch.ones(256, 4, device="cuda"), torch.ones(256, device="cuda")
+    k = binding.ida_ssm_conv_backward_workspace_bytes(*x.shape, 4)
+    got += binding.ida_ssm_conv_backward(x, x, w, b, workspace=torch.full((k // 4,), float("nan"), device="cuda")).values()
+    want += binding.ida_ssm_conv_backward(x, x, w, b).values()
+    k = binding.ida_rmsnorm_backward_workspace_bytes(x.shape[0] * x.shape[1], 256)
+    got += binding.ida_rmsnorm_backward(x, b, x, workspace=torch.full((k // 4,), float("nan"), device="cuda")).values()
+    want += binding.ida_rmsnorm_backward(x, b, x).values()
+    _done()
+    assert all(torch.equal(a, c) for a, c in zip(got, want))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_two_graphs_that_share_a_workspace(dtype):
+    """A split prompt and gradients captured apart, over the same workspace, replayed in turn."""
+    sizes, args, p, s, dy = _problem(dtype)
+    code = binding.IDA_BF16 if dtype == "bf16" else binding.IDA_F32
+    ws = torch.empty(max(binding.ida_ssm_scan_workspace_bytes(*sizes, code),
+                         binding.ida_ssm_scan_backward_workspace_bytes(*sizes, code)), dtype=torch.uint8, device="cuda")
+    calls = [lambda: list(binding.ida_ssm_scan(*args, p, state_in=s, final_state=True, workspace=ws)),
+             lambda: list(binding.ida_ssm_scan_backward(*args, p, dy, workspace=ws).values())]
+    want = [[t.clone() for t in call()] for call in calls]
+    torch.cuda.synchronize()
+    graphs, got = [torch.cuda.CUDAGraph(), torch.cuda.CUDAGraph()], []
+    for graph, call in zip(graphs, calls):
+        with torch.cuda.graph(graph):
+            got.append(call())
+    for _ in range(3):
+        for outs in got:
+            for t in outs:
+                t.fill_(float("nan"))
+        for graph in graphs:
+            graph.replay()
+        _done()
+        assert all(torch.equal(a, c) for o, w in zip(got, want) for a, c in zip(o, w))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_more_rows_and_heads_than_a_grid_dimension(dtype):
+    """68000 units of two positions: the sums over chunks take two launches."""
+    case = (17000, 2, 4, 8, 2, 8, dtype, True, False)
+    B, N, H, d, G, M = case[:6]
+    p, row, s, C = _scan_inputs(*case)
+    args, dp = _on_gpu(row, C, H, d, G, M), sc.cuda(p)
+    y, X = binding.ida_ssm_scan(*args, dp, state_in=s.cuda(), final_state=True)
+    dy = torch.randn(B, N, H, d, generator=sc.gen(11)).to(sc.DT[dtype])
+    g = binding.ida_ssm_scan_backward(*args, dp, dy.cuda())
+    _done()
+    ry, rX = _scan_ref(row, C, H, d, G, M, p, s)
+    ya, Xa = _scan_ref(row, C, H, d, G, M, p, s, absolute=True)
+    by, bX = _scan_bounds(dtype, N, ry, ya, Xa)
+    assert worst(y, ry, by) <= 1 and worst(X, rX, bX) <= 1
+    # 17000 chunks (four parts each on the tensor cores) are added in 128 interleaved sums
+    check_scan_gradients(g, row, C, H, d, G, M, p, dy, dtype, sums=4 * B // 128 + 8)
