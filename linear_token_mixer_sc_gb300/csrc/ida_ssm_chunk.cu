@@ -14,11 +14,10 @@
 // of c X_0.  The states that a segment starts from and the final state are fp32 results, so that y is the
 // same whether that one is wanted or not: for them the scaled b is kept as the sum of three bf16 tiles, all
 // 24 bits, and S is summed in 2^-32 fixed point.  (Starting segments from one tile's sums: 55.9 us for 57.6
-// at 4 x 4096, and another y.)
-// The chunk kernel sums it in two floats, one of
-// them exactly: a position that forgets everything takes nothing from the decays behind it.  (One float
-// and D in it as log2 D: y 3.4 times its error bound off behind a step size of 1e5, 17 times with rates
-// of e^9 and step sizes of 10; fixed point: 2.46 us a chunk for 2.26.)
+// at 4 x 4096, and another y.)  The chunk kernel sums it in two floats, one of them exactly: a position that
+// forgets everything takes nothing from the decays behind it.  (One float and D in it as log2 D: y 3.4 times
+// its error bound off behind a step size of 1e5, 17 times with rates of e^9 and step sizes of 10; fixed
+// point: 2.46 us a chunk for 2.26.)
 //
 // One CTA per SM walks the chunks of one (row, head, up to 128 channels, segment), its warps in
 // roles that hand chunks on through mbarriers, so that a chunk's copy, MMAs, CUDA-core stages and
@@ -46,7 +45,8 @@
 // (ssm_state_kernel: x and b only) leaves the last states from zero of parts of the segments, a
 // second the states the segments start from, and the final state.  The state kernel walks a part
 // backwards, where the decay from a position to the part's end is known without a look ahead, so its
-// MMAs only accumulate and the copies and the scaling of the next chunk run beside them.
+// MMAs only accumulate and the next chunk's weights are made beside them.  (Its copy waits for them: three
+// tiles of b leave room for one buffer with two CTAs an SM.)
 //
 // Every wait is bounded.  On a timeout the warps of a role leave their loop together (the others
 // run out of waits of their own), the kernel records kErrWaitTimeout, waits (bounded) for its copies
