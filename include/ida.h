@@ -1,6 +1,7 @@
 /*
  * ida.h -- C ABI of the GB300 (sm_103a) Interdomain Attention token mixer, and of the
- * selective mixer and the residual pre-norm that go with it in a decoder.
+ * selective mixer, the residual pre-norm and the gated feed-forward block (with products
+ * in 8 bits) that go with it in a decoder.
  *
  * The operation is the token mixer of "Interdomain Attention: Beyond
  * Token-Level Key-Value Memory" (arXiv 2605.24330) in its scalable form, as
@@ -501,6 +502,78 @@ IDA_API ida_status ida_rmsnorm_backward(const void *r, const float *w, const voi
 
 /* Workspace bytes of ida_rmsnorm_backward (0 for invalid sizes or no rows); host arithmetic. */
 IDA_API size_t ida_rmsnorm_backward_workspace_bytes(int rows, int D);
+
+/*
+ * The decoder's gated feed-forward block, the other half of a layer whose first half is the mixer
+ * ("Interdomain Attention: Beyond Token-Level Key-Value Memory", German technical summary,
+ * "Skalierbare Implementierung", "Architektur": a Llama-style decoder).  Per row of D channels:
+ *   g = x Wg^T,  u = x Wu^T,  h = g / (1 + e^-g) * u,  out = h Wd^T.
+ *   x         rows of D channels, ldx elements apart, 16-byte aligned (ldx a multiple of 8);
+ *   w_gate, w_up [F, D], w_down [D, F] dtype;  out [rows, D] dtype, dense;
+ *   acts      NULL, or [3, rows, F] dtype: receives g, u and h, for ida_ffn_backward;
+ *   workspace at least ida_ffn_workspace_bytes(...) bytes (contents on entry ignored).
+ * Supported: D and F multiples of 8 up to 65536, rows up to 2^28 with rows * max(D, F) <= 2^36.
+ * Sums are fp32.  With IDA_BF16 h is rounded to bf16 between the products; with IDA_F32 the operands of the
+ * products are taken apart into three bf16 parts each, whose products above 2^-24 of the whole are all
+ * taken.  Non-finite inputs make the rows of out that they reach (all of them for a weight) unspecified.
+ * Outputs (the workspace among them) that share bytes with inputs or with one another are refused.
+ */
+IDA_API ida_status ida_ffn(const void *x, const void *w_gate, const void *w_up, const void *w_down, void *out,
+                   void *acts, int rows, int D, int F, long long ldx, int dtype, void *workspace,
+                   size_t workspace_bytes, ida_stream_t stream);
+
+/* Workspace bytes of ida_ffn (0 for invalid sizes or no rows); host arithmetic. */
+IDA_API size_t ida_ffn_workspace_bytes(int rows, int D, int F, int dtype);
+
+/*
+ * Gradients of ida_ffn's out, given what it read, the acts it wrote and dout [rows, D] dense: dx [rows, D] dense,
+ * dw_gate and dw_up [F, D], dw_down [D, F], all in dtype (written, not accumulated; rounded once from fp32
+ * sums over the rows; zero when rows == 0).  With s = 1 / (1 + e^-g):
+ *   dh = dout Wd,  du = dh g s,  dg = dh u s (1 + g (1 - s)),
+ *   dx = dg Wg + du Wu,  dWg = dg^T x,  dWu = du^T x,  dWd = dout^T h.
+ * With IDA_BF16 dg and du are rounded to bf16 between the products.  The workspace is required when rows > 0.
+ * Sums run in a fixed order: deterministic.
+ */
+IDA_API ida_status ida_ffn_backward(const void *x, const void *w_gate, const void *w_up, const void *w_down,
+                            const void *acts, const void *dout, void *dx, void *dw_gate, void *dw_up,
+                            void *dw_down, int rows, int D, int F, long long ldx, int dtype, void *workspace,
+                            size_t workspace_bytes, ida_stream_t stream);
+
+/* Workspace bytes of ida_ffn_backward (0 for invalid sizes or no rows); host arithmetic. */
+IDA_API size_t ida_ffn_backward_workspace_bytes(int rows, int D, int F, int dtype);
+
+/*
+ * Products in 8 bits.  An operand is e4m3 values in rows of K channels, dense, and fp32 scales: of
+ * activations one for each 128 channels of a row, [rows, ceil(K / 128)] (what ida_rmsnorm writes with
+ * group 128), of weights one for each block of 128 x 128, [ceil(N / 128), ceil(K / 128)].  The last block of
+ * either dimension may be short.  A value stands for itself times its scale.
+ *
+ * ida_quant_e4m3 lays such an operand out: x, rows of K channels in dtype, ldx elements apart (16-byte
+ * aligned, ldx a multiple of 8); block_rows 1 (activations) or 128 (weights);  scale = max |x| / 448 of a block
+ * (1 if all are zero, rounded up where it is subnormal),  q = x / scale, to the nearest, ties to even.
+ * Supported: K a multiple of 16 up to 65536, rows up to 2^28 with rows * K <= 2^36 (of every call here).
+ * A NaN becomes a NaN and leaves its block's scale alone; an infinity makes its block unspecified.
+ */
+IDA_API ida_status ida_quant_e4m3(const void *x, void *q, float *scale, int rows, int K, int block_rows,
+                          long long ldx, int dtype, ida_stream_t stream);
+
+/*
+ * out = A B^T, [rows, N] dtype dense, of A (a [rows, K] and the scales of activations) and B (b [N, K]
+ * and the scales of weights).  N a multiple of 8 up to 65536.  Products are exact and summed in fp32: within a
+ * block by the tensor cores, over blocks with their scales in registers.
+ */
+IDA_API ida_status ida_gemm_e4m3(const void *a, const float *a_scale, const void *b, const float *b_scale, void *out,
+                         int rows, int K, int N, int dtype, ida_stream_t stream);
+
+/*
+ * The first half of the feed-forward block in 8 bits: with g and u as ida_gemm_e4m3 of a [rows, D] with
+ * w_gate and w_up [F, D],  h = g / (1 + e^-g) * u,  quantised as activations are by ida_quant_e4m3:
+ * q [rows, F] and scale [rows, ceil(F / 128)], what ida_gemm_e4m3 takes for w_down.  F a multiple of 16
+ * up to 65536.  h is fp32 until it is quantised.
+ */
+IDA_API ida_status ida_glu_e4m3(const void *a, const float *a_scale, const void *w_gate, const float *gate_scale,
+                        const void *w_up, const float *up_scale, void *q, float *scale, int rows, int D, int F,
+                        ida_stream_t stream);
 
 /*
  * Self-test of the failure reporting (no counterpart in the paper: a property

@@ -27,7 +27,9 @@ EXPORTED = ("ida_state_floats", "ida_forward", "ida_forward_ws", "ida_forward_fr
             "ida_forward_ideal", "ida_rope", "ida_forward_host", "ida_forward_host_staging_bytes",
             "ida_ssm_conv", "ida_ssm_conv_backward", "ida_ssm_conv_backward_workspace_bytes", "ida_ssm_scan",
             "ida_ssm_scan_workspace_bytes", "ida_ssm_scan_backward", "ida_ssm_scan_backward_workspace_bytes",
-            "ida_ssm_step", "ida_rmsnorm", "ida_rmsnorm_backward", "ida_rmsnorm_backward_workspace_bytes")
+            "ida_ssm_step", "ida_rmsnorm", "ida_rmsnorm_backward", "ida_rmsnorm_backward_workspace_bytes",
+            "ida_ffn", "ida_ffn_workspace_bytes", "ida_ffn_backward", "ida_ffn_backward_workspace_bytes",
+            "ida_quant_e4m3", "ida_gemm_e4m3", "ida_glu_e4m3")
 
 _lock = threading.Lock()
 _lib = None
@@ -91,11 +93,17 @@ def load() -> ctypes.CDLL:
                     ("ida_ssm_scan_backward", [_vp] * 15 + [_i] * 6 + [ll] * 8 + [_i, _vp, sz, _vp]),
                     ("ida_ssm_step", [_vp] * 10 + [_i] * 5 + [ll] * 2 + [_i] * 2 + [_vp]),
                     ("ida_rmsnorm", [_vp] * 7 + [_i] * 3 + [ctypes.c_float, _i, _vp]),
-                    ("ida_rmsnorm_backward", [_vp] * 6 + [_i] * 2 + [ctypes.c_float, _i, _vp, sz, _vp])):
+                    ("ida_rmsnorm_backward", [_vp] * 6 + [_i] * 2 + [ctypes.c_float, _i, _vp, sz, _vp]),
+                    ("ida_ffn", [_vp] * 6 + [_i] * 3 + [ll, _i, _vp, sz, _vp]),
+                    ("ida_ffn_backward", [_vp] * 10 + [_i] * 3 + [ll, _i, _vp, sz, _vp]),
+                    ("ida_quant_e4m3", [_vp] * 3 + [_i] * 3 + [ll, _i, _vp]),
+                    ("ida_gemm_e4m3", [_vp] * 5 + [_i] * 4 + [_vp]),
+                    ("ida_glu_e4m3", [_vp] * 8 + [_i] * 3 + [_vp])):
                 getattr(L, name).restype = _i
                 getattr(L, name).argtypes = args
             for name, n in (("ida_ssm_conv_backward_workspace_bytes", 4), ("ida_ssm_scan_workspace_bytes", 7),
-                            ("ida_ssm_scan_backward_workspace_bytes", 7), ("ida_rmsnorm_backward_workspace_bytes", 2)):
+                            ("ida_ssm_scan_backward_workspace_bytes", 7), ("ida_rmsnorm_backward_workspace_bytes", 2),
+                            ("ida_ffn_workspace_bytes", 4), ("ida_ffn_backward_workspace_bytes", 4)):
                 getattr(L, name).restype = sz
                 getattr(L, name).argtypes = [_i] * n
             L.ida_selftest_bounded_wait.restype = _i
@@ -738,6 +746,178 @@ def ida_rmsnorm_backward(r: torch.Tensor, w: torch.Tensor, dy: torch.Tensor, dre
                                 dt, wsp, n, _raw_stream(dev))
     _check(st, "ida_rmsnorm_backward")
     return {"x": dx, "w": dw}
+
+
+# ---- the feed-forward block and products in 8 bits --------------------------------------------
+
+def ida_ffn_workspace_bytes(rows: int, D: int, F: int, dtype: int) -> int:
+    _fits(rows, D, F, dtype)
+    return int(load().ida_ffn_workspace_bytes(rows, D, F, dtype))
+
+
+def ida_ffn_backward_workspace_bytes(rows: int, D: int, F: int, dtype: int) -> int:
+    _fits(rows, D, F, dtype)
+    return int(load().ida_ffn_backward_workspace_bytes(rows, D, F, dtype))
+
+
+def _leading(name: str, t: torch.Tensor, dev: int):
+    """(address, row stride, rows) of a tensor of rows: any leading dimensions where it is dense, one or
+    two at one stride where it is a slice of wider rows."""
+    n = t.shape[-1]
+    rows = t.numel() // n if n else 0
+    if t.is_contiguous():
+        return t.data_ptr(), n, rows
+    if t.dim() not in (2, 3):
+        raise ValueError(f"{name} must be contiguous, or rows in one or two dimensions at one stride")
+    return (*_rows(name, t, t.shape, t.dtype, dev, t.dim() - 1), rows)
+
+
+def _ffn_inputs(x, w_gate, w_up, w_down):
+    """Device, addresses, row stride and sizes of the block's inputs."""
+    dev = x.get_device()
+    F, D = w_gate.shape
+    xp, ldx, rows = _leading("x", x, dev)
+    if x.shape[-1] != D:
+        raise ValueError(f"x must have rows of {D} channels, got {x.shape[-1]}")
+    _fits(rows, D, F)
+    ptrs = [xp, _dense("w_gate", w_gate, (F, D), x.dtype, dev), _dense("w_up", w_up, (F, D), x.dtype, dev),
+            _dense("w_down", w_down, (D, F), x.dtype, dev)]
+    return dev, ptrs, ldx, (rows, D, F)
+
+
+@_placed
+def ida_ffn(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor, w_down: torch.Tensor,
+            acts: torch.Tensor | bool | None = None, out: torch.Tensor | None = None,
+            workspace: torch.Tensor | None = None):
+    """Gated feed-forward block, out = (silu(x w_gate^T) * (x w_up^T)) w_down^T, tensors of one dtype.
+    x: rows of D channels (any leading dimensions, or a slice of wider rows), w_gate and w_up [F,D],
+    w_down [D,F].  ``acts``: a [3,...,F] tensor to fill with both factors and their product (what
+    ``ida_ffn_backward`` takes), True to allocate one, or None.  ``workspace``: a tensor of at least
+    ``ida_ffn_workspace_bytes`` bytes (allocated here when None).  Returns (out [...,D], acts)."""
+    code = _dtype_code(x)
+    dev, ptrs, ldx, sizes = _ffn_inputs(x, w_gate, w_up, w_down)
+    rows, D, F = sizes
+    shape = (3, *x.shape[:-1], F)
+    if out is None:
+        out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    if acts is True:
+        acts = torch.empty(shape, dtype=x.dtype, device=x.device)
+    elif acts is False:
+        acts = None
+    L = load()
+    ws, wsp, n = _work_buffer(workspace, L.ida_ffn_workspace_bytes(rows, D, F, code) if workspace is None else 0, dev)
+    st = L.ida_ffn(*ptrs, _dense("out", out, x.shape, x.dtype, dev),
+                   None if acts is None else _dense("acts", acts, shape, x.dtype, dev), *sizes, ldx, code, wsp, n,
+                   _raw_stream(dev))
+    _check(st, "ida_ffn")
+    return out, acts
+
+
+@_placed
+def ida_ffn_backward(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor, w_down: torch.Tensor,
+                     acts: torch.Tensor, dout: torch.Tensor, grads: dict | None = None,
+                     workspace: torch.Tensor | None = None) -> dict:
+    """Gradients of ``ida_ffn``'s out, given its inputs, the ``acts`` it returned and dout [...,D]: dict x,
+    w_gate, w_up, w_down in their tensors' shapes and dtype, written into ``grads`` when given.
+    ``workspace``: a tensor of at least ``ida_ffn_backward_workspace_bytes`` bytes (allocated here when
+    None)."""
+    code = _dtype_code(x)
+    dev, ptrs, ldx, sizes = _ffn_inputs(x, w_gate, w_up, w_down)
+    rows, D, F = sizes
+    ap = _dense("acts", acts, (3, *x.shape[:-1], F), x.dtype, dev)
+    dp = _dense("dout", dout, x.shape, x.dtype, dev)
+    g = grads if grads is not None else {
+        k: torch.empty(t.shape, dtype=x.dtype, device=x.device)
+        for k, t in (("x", x), ("w_gate", w_gate), ("w_up", w_up), ("w_down", w_down))}
+    gp = [_dense(f"grads[{k!r}]", g[k], t.shape, x.dtype, dev)
+          for k, t in (("x", x), ("w_gate", w_gate), ("w_up", w_up), ("w_down", w_down))]
+    L = load()
+    ws, wsp, n = _work_buffer(workspace, L.ida_ffn_backward_workspace_bytes(rows, D, F, code)
+                              if workspace is None else 0, dev)
+    st = L.ida_ffn_backward(*ptrs, ap, dp, *gp, *sizes, ldx, code, wsp, n, _raw_stream(dev))
+    _check(st, "ida_ffn_backward")
+    return g
+
+
+def _operand(name: str, q: torch.Tensor, scale: torch.Tensor, lead, K: int, scales, dev: int):
+    """Addresses of an e4m3 operand [*lead, K] and its scales."""
+    return (_dense(name, q, (*lead, K), torch.float8_e4m3fn, dev),
+            _dense(f"the scales of {name}", scale, scales, torch.float32, dev))
+
+
+@_placed
+def ida_quant_e4m3(x: torch.Tensor, rows: int = 1, q: torch.Tensor | None = None,
+                   scale: torch.Tensor | None = None):
+    """x, rows of K channels (any leading dimensions, or a slice of wider rows; float32 or bfloat16), in e4m3
+    with a float32 scale for 128 channels of each row (``rows`` = 1, for activations) or of each 128 rows
+    (``rows`` = 128, x [N,K], for weights).  Returns (q, scale): q [...,K] in float8_e4m3fn, scale
+    [...,ceil(K/128)] or [ceil(N/128),ceil(K/128)]; x is q times its scale."""
+    code, dev = _dtype_code(x), x.get_device()
+    K = x.shape[-1]
+    if rows == 128 and x.dim() != 2:
+        raise ValueError("blocks of 128 rows are of a tensor [N, K]")
+    xp, ldx, n = _leading("x", x, dev)
+    _fits(n, K, rows)
+    lead = x.shape[:-1] if rows == 1 else ((n + 127) // 128,)
+    shape = (*lead, (K + 127) // 128)
+    if q is None:
+        q = torch.empty(x.shape, dtype=torch.float8_e4m3fn, device=x.device)
+    if scale is None:
+        scale = torch.empty(shape, dtype=torch.float32, device=x.device)
+    st = load().ida_quant_e4m3(xp, _dense("q", q, x.shape, torch.float8_e4m3fn, dev),
+                               _dense("scale", scale, shape, torch.float32, dev), n, K, rows, ldx, code,
+                               _raw_stream(dev))
+    _check(st, "ida_quant_e4m3")
+    return q, scale
+
+
+@_placed
+def ida_gemm_e4m3(a: torch.Tensor, a_scale: torch.Tensor, b: torch.Tensor, b_scale: torch.Tensor,
+                  dtype: torch.dtype = torch.bfloat16, out: torch.Tensor | None = None) -> torch.Tensor:
+    """(a times its scales) (b times its scales)^T: a [...,K] with a_scale [...,ceil(K/128)], as
+    ``ida_rmsnorm`` (group 128), ``ida_glu_e4m3`` and ``ida_quant_e4m3`` make them, b [N,K] with b_scale
+    [ceil(N/128),ceil(K/128)] of ``ida_quant_e4m3`` with 128 rows; contiguous, q's in float8_e4m3fn.
+    Returns out [...,N] in ``dtype`` (bfloat16 or float32; that of ``out`` when given)."""
+    dev = a.get_device()
+    K, lead = a.shape[-1], a.shape[:-1]
+    N, kb = b.shape[0], (K + 127) // 128
+    rows = a.numel() // K if K else 0
+    _fits(rows, K, N)
+    ptrs = [*_operand("a", a, a_scale, lead, K, (*lead, kb), dev),
+            *_operand("b", b, b_scale, (N,), K, ((N + 127) // 128, kb), dev)]
+    if out is None:
+        out = torch.empty((*lead, N), dtype=dtype, device=a.device)
+    code = _dtype_code(out)
+    st = load().ida_gemm_e4m3(*ptrs, _dense("out", out, (*lead, N), out.dtype, dev), rows, K, N, code,
+                              _raw_stream(dev))
+    _check(st, "ida_gemm_e4m3")
+    return out
+
+
+@_placed
+def ida_glu_e4m3(a: torch.Tensor, a_scale: torch.Tensor, w_gate: torch.Tensor, gate_scale: torch.Tensor,
+                 w_up: torch.Tensor, up_scale: torch.Tensor, q: torch.Tensor | None = None,
+                 scale: torch.Tensor | None = None):
+    """First half of the feed-forward block in 8 bits: silu(a w_gate^T) * (a w_up^T) of operands as
+    ``ida_gemm_e4m3`` takes them (a [...,D], w_gate and w_up [F,D]), quantised with a scale for 128
+    channels of each row.  Returns (q [...,F] in float8_e4m3fn, scale [...,ceil(F/128)])."""
+    dev = a.get_device()
+    D, lead = a.shape[-1], a.shape[:-1]
+    F, kb = w_gate.shape[0], (D + 127) // 128
+    rows = a.numel() // D if D else 0
+    _fits(rows, D, F)
+    blocks = (F + 127) // 128
+    ptrs = [*_operand("a", a, a_scale, lead, D, (*lead, kb), dev),
+            *_operand("w_gate", w_gate, gate_scale, (F,), D, (blocks, kb), dev),
+            *_operand("w_up", w_up, up_scale, (F,), D, (blocks, kb), dev)]
+    if q is None:
+        q = torch.empty((*lead, F), dtype=torch.float8_e4m3fn, device=a.device)
+    if scale is None:
+        scale = torch.empty((*lead, blocks), dtype=torch.float32, device=a.device)
+    st = load().ida_glu_e4m3(*ptrs, _dense("q", q, (*lead, F), torch.float8_e4m3fn, dev),
+                             _dense("scale", scale, (*lead, blocks), torch.float32, dev), rows, D, F, _raw_stream(dev))
+    _check(st, "ida_glu_e4m3")
+    return q, scale
 
 
 def ida_selftest_bounded_wait(limit_cycles: int, stream=None) -> None:

@@ -1,0 +1,766 @@
+// ida_gemm.cuh -- matrix products of the feed-forward block on the tensor cores: one persistent
+// kernel over pairs of SMs, with the epilogues that fuse what follows a product.
+//
+// A pair of CTAs (a cluster of two, tcgen05 cta_group::2) owns an output tile of 256 rows x 256
+// columns: each CTA brings its 128 rows of A and half of the 256 columns of B into shared memory by
+// TMA, the even one issues the MMAs for both, and each finds its own 128 rows x 256 columns in its
+// TMEM, where two such accumulators fit, so that one tile's epilogue runs beside the next one's MMAs.
+// A pair tile reads 64 KB for 8.4 MFLOP; with one CTA a tile of 128 x 256 would read 48 KB for half of
+// that, 96 bytes a clock of every SM at the MMA's rate, more than the L2 gives.
+//
+// Warps: 0 loads, 1 issues the MMAs (of the even CTA), the others are the epilogue's.  The direct kind
+// accumulates a whole tile in TMEM.  The others take the accumulator out every `chunk` contraction
+// blocks and add it up in registers, scaled: in e4m3 because each block of 128 has scales of its own,
+// for fp32 inputs (three bf16 parts, six products) because the tensor cores round sums towards zero.
+#pragma once
+
+#include <cuda.h>
+#include <cuda_fp8.h>
+
+#include "ida_vec.cuh"
+#include "tc_sm103.cuh"
+
+namespace ida {
+
+enum { kDirect = 0, kParts = 1, kE4M3 = 2 };          // operands: bf16, three bf16 parts of fp32, e4m3
+enum { kPlain = 0, kGate = 1, kGateBwd = 2 };         // epilogues
+constexpr int GST = 5;                                // stages
+constexpr int GOP = 128 * 128;                        // bytes of an operand of a stage
+constexpr int GSLAB = 32 * 128;                       // bytes of a warp's staged box: 32 rows of 128 bytes
+constexpr int GSTAGING = 64 * 1024;                   // of all epilogue warps
+constexpr int GSMEM = GST * 2 * GOP + GSTAGING + 1024 + 512;
+static_assert(GSMEM <= 227 * 1024, "shared memory budget");
+
+struct GemmSeg {
+    unsigned char a, ap, b, bp;  // maps and parts of one pass over the contraction
+};
+
+struct GemmArgs {
+    CUtensorMap a[3], b[3], o[3], e[2];  // operands, outputs, what the epilogue reads
+    int M[3], N[3];                      // rows and columns of each problem's output
+    int problems, segs, kblocks, chunk;  // kblocks: blocks of 128 bytes along each segment's contraction
+    GemmSeg seg[12];
+    int keep;                            // kGate: store the two factors as well
+    const float *sa, *sb[2];             // kE4M3: scales [M, kblocks] and [ceil(N / 128), kblocks] (one or two of b)
+    float *so;                           // kE4M3 kGate: output scales [M, ceil(N / 128)]
+    unsigned *err;
+};
+
+// ---- what only pairs need ------------------------------------------------------------------
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void cluster_sync_all() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// the address of the even CTA's copy of a shared variable
+__device__ __forceinline__ uint32_t lead_addr(const void *p) {
+    uint32_t r;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(r) : "r"(tc::smem_u32(p)));
+    return r;
+}
+__device__ __forceinline__ void arrive_remote(uint32_t addr) {
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
+}
+__device__ __forceinline__ void arrive_local(uint64_t *bar) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(tc::smem_u32(bar)) : "memory");
+}
+__device__ __forceinline__ bool try_wait_cluster(uint64_t *bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(tc::smem_u32(bar)), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+// Waits of about a second at most; the role that gives up reports it and ends, and the others follow.
+__device__ __forceinline__ bool pair_wait(uint64_t *bar, uint32_t parity, unsigned *err) {
+    if (try_wait_cluster(bar, parity)) return true;
+    const long long t0 = clock64();
+    while (!try_wait_cluster(bar, parity))
+        if (clock64() - t0 > 2000000000LL) {
+            report_error(err, kErrWaitTimeout);
+            return false;
+        }
+    return true;
+}
+__device__ __forceinline__ void pair_load(void *dst, const void *map, int c0, int c1, int c2, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes.cta_group::2 [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
+            tc::smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(bar)
+        : "memory");
+}
+__device__ __forceinline__ void load_3d(void *dst, const void *map, int c0, int c1, int c2, uint64_t *bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
+            tc::smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(tc::smem_u32(bar))
+        : "memory");
+}
+__device__ __forceinline__ void store_3d(const void *map, int c0, int c1, int c2, const void *src) {
+    asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(
+                     reinterpret_cast<uint64_t>(map)),
+                 "r"(c0), "r"(c1), "r"(c2), "r"(tc::smem_u32(src))
+                 : "memory");
+}
+template <int N>
+__device__ __forceinline__ void bulk_wait_read() {
+    asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void pair_commit(uint64_t *bar) {  // to both CTAs' copies of the barrier
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+            tc::smem_u32(bar)),
+        "h"((unsigned short)3)
+        : "memory");
+}
+template <bool E4M3>
+__device__ __forceinline__ void pair_mma(uint32_t d, tc::SmemDesc a, tc::SmemDesc b, uint32_t id, uint32_t acc) {
+    if (E4M3)
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\tmov.b64 da, {%1, %2};\n\tmov.b64 db, {%3, %4};\n\t"
+            "setp.ne.b32 p, %6, 0;\n\ttcgen05.mma.cta_group::2.kind::f8f6f4 [%0], da, db, %5, p;\n\t}" ::"r"(d),
+            "r"(a.lo), "r"(a.hi), "r"(b.lo), "r"(b.hi), "r"(id), "r"(acc)
+            : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\tmov.b64 da, {%1, %2};\n\tmov.b64 db, {%3, %4};\n\t"
+            "setp.ne.b32 p, %6, 0;\n\ttcgen05.mma.cta_group::2.kind::f16 [%0], da, db, %5, p;\n\t}" ::"r"(d),
+            "r"(a.lo), "r"(a.hi), "r"(b.lo), "r"(b.hi), "r"(id), "r"(acc)
+            : "memory");
+}
+// 32 lanes x 32 columns; the values are there after tc::tmem_wait_ld()
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
+        "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+          "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+          "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_use(uint32_t (&r)[32]) {  // keeps uses of r behind the wait
+#pragma unroll
+    for (int i = 0; i < 32; ++i) asm volatile("" : "+r"(r[i]));
+}
+
+// Shared-memory descriptor of a 128-byte-swizzled operand (rows of 128 bytes, 1024 bytes between groups of
+// 8; `lbo` between 64-element slabs of MN-major operands) and the byte offset of 16-byte piece c of row r.
+__device__ __forceinline__ tc::SmemDesc pair_desc(uint32_t addr, uint32_t lbo) {
+    return {((addr >> 4) & 0x3FFFu) | ((lbo >> 4) << 16), (1024u >> 4) | (1u << 14) | (2u << 29)};
+}
+__device__ __forceinline__ int swz128(int r, int c) { return r * 128 + ((c ^ (r & 7)) << 4); }
+
+// ---- the activation --------------------------------------------------------------------------
+
+// 1 / (1 + e^-x): for bf16 results from the hardware's exponential and reciprocal (2^-21), else exactly rounded steps
+template <typename E>
+__device__ __forceinline__ float sigmoid(float x) {
+    if constexpr (sizeof(E) == 4) return 1.f / (1.f + expf(-x));
+    else return __fdividef(1.f, 1.f + __expf(-x));
+}
+
+// ---- tiles -----------------------------------------------------------------------------------
+
+struct GemmTile {
+    int p, row0, col0;  // problem, the pair's first row and column (kGate: of the product's columns)
+};
+constexpr int tile_cols(int epi) { return epi == kGate ? 128 : 256; }
+
+// Tile `t` of the launch: bands of 8 tiles of rows, column by column, so that the pairs that run at one
+// time share rows and columns in the L2.
+__device__ __forceinline__ GemmTile tile_of(const GemmArgs &g, int t, int cols) {
+    GemmTile r;
+    r.p = 0;
+    int tm = (g.M[0] + 255) / 256, tn = (g.N[0] + cols - 1) / cols;
+    while (t >= tm * tn && r.p + 1 < g.problems) {
+        t -= tm * tn;
+        ++r.p;
+        tm = (g.M[r.p] + 255) / 256;
+        tn = (g.N[r.p] + cols - 1) / cols;
+    }
+    const int band = t / (8 * tn), in = t - band * 8 * tn;
+    const int rows = tm - band * 8 < 8 ? tm - band * 8 : 8;
+    r.row0 = (band * 8 + in % rows) * 256;
+    r.col0 = in / rows * cols;
+    return r;
+}
+__device__ __forceinline__ int tiles_of(const GemmArgs &g, int cols) {
+    int n = 0;
+    for (int p = 0; p < g.problems; ++p) n += (g.M[p] + 255) / 256 * ((g.N[p] + cols - 1) / cols);
+    return n;
+}
+
+// ---- the epilogue's staging: a warp's ring of boxes of 32 rows x 128 bytes ----------------------
+
+template <int SLOTS>
+struct Ring {
+    char *base;
+    int lane, next;
+    // a box that no store still reads; `taken`: boxes taken and not yet put
+    template <int TAKEN = 0>
+    __device__ __forceinline__ char *take() {
+        if (lane == 0) bulk_wait_read<SLOTS - 1 - TAKEN>();
+        __syncwarp();
+        char *s = base + next * GSLAB;
+        next = next + 1 == SLOTS ? 0 : next + 1;
+        return s;
+    }
+    __device__ __forceinline__ void put(const char *slab, const void *map, int c0, int c1, int c2, bool inside) {
+        tc::fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+            if (inside) store_3d(map, c0, c1, c2, slab);
+            tc::bulk_commit();
+        }
+    }
+};
+
+// 8 (bf16) or 4 (fp32) values to 16 bytes of a staged box
+template <typename E>
+__device__ __forceinline__ void stage(char *slab, int row, int piece, const float *x) {
+    *reinterpret_cast<uint4 *>(slab + swz128(row, piece)) = Vec16<E>::pack(x);
+}
+
+// ---- the kernel ------------------------------------------------------------------------------
+
+template <int KIND>
+constexpr int gemm_threads() { return KIND == kDirect ? 192 : 320; }
+
+struct GemmBars {
+    uint64_t full[GST], empty[GST], acc_full[2], acc_empty[2], in[8][2];
+    uint32_t tmem;
+};
+
+// What a warp of the epilogue knows of its place
+struct EpiWarp {
+    char *staging;
+    uint64_t *in;   // its barriers for what the epilogue reads
+    int lane, q, half, rank;
+    uint32_t tmem;  // of its lanes
+};
+
+// Direct kind, kPlain: 256 columns in bf16.
+__device__ __forceinline__ void epi_plain(const GemmArgs &g, const EpiWarp &w, Ring<4> &ring, const GemmTile &t, uint32_t acc,
+                                          uint32_t release) {
+    const int row = t.row0 + w.rank * 128 + w.q * 32;
+    char *slab = nullptr;
+#pragma unroll
+    for (int c = 0; c < 8; ++c) {
+        uint32_t r[32];
+        tmem_ld32(acc + c * 32, r);
+        tc::tmem_wait_ld();
+        tmem_use(r);
+        if (c == 7) {
+            tc::tc_fence_before();
+            __syncwarp();
+            if (w.lane == 0) arrive_remote(release);
+        }
+        if (c % 2 == 0) slab = ring.take();
+#pragma unroll
+        for (int k = 0; k < 4; ++k) stage<__nv_bfloat16>(slab, w.lane, c % 2 * 4 + k, reinterpret_cast<const float *>(r) + 8 * k);
+        if (c % 2) ring.put(slab, &g.o[t.p], t.col0 + c / 2 * 64, row, 0, row < g.M[t.p] && t.col0 + c / 2 * 64 < g.N[t.p]);
+    }
+}
+
+// Direct kind, kGate: columns c and 128 + c are the factors of the product's column c.
+__device__ __forceinline__ void epi_gate(const GemmArgs &g, const EpiWarp &w, Ring<4> &ring, const GemmTile &t, uint32_t acc,
+                                         uint32_t release) {
+    using E = __nv_bfloat16;
+    const int row = t.row0 + w.rank * 128 + w.q * 32;
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+        char *sh = ring.take<0>(), *sg = nullptr, *su = nullptr;
+        if (g.keep) {
+            sg = ring.take<1>();
+            su = ring.take<2>();
+        }
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+            uint32_t rg[32], ru[32];
+            tmem_ld32(acc + j * 64 + c * 32, rg);
+            tmem_ld32(acc + 128 + j * 64 + c * 32, ru);
+            tc::tmem_wait_ld();
+            tmem_use(rg);
+            tmem_use(ru);
+            if (j == 1 && c == 1) {
+                tc::tc_fence_before();
+                __syncwarp();
+                if (w.lane == 0) arrive_remote(release);
+            }
+            const float *xg = reinterpret_cast<const float *>(rg), *xu = reinterpret_cast<const float *>(ru);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                float h[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) h[e] = xg[8 * k + e] * sigmoid<E>(xg[8 * k + e]) * xu[8 * k + e];
+                stage<E>(sh, w.lane, c * 4 + k, h);
+                if (g.keep) {
+                    stage<E>(sg, w.lane, c * 4 + k, xg + 8 * k);
+                    stage<E>(su, w.lane, c * 4 + k, xu + 8 * k);
+                }
+            }
+        }
+        const int col = t.col0 + j * 64;
+        const bool inside = row < g.M[0] && col < g.N[0];
+        ring.put(sh, &g.o[0], col, row, 0, inside);
+        if (g.keep) {
+            ring.put(sg, &g.o[1], col, row, 0, inside);
+            ring.put(su, &g.o[2], col, row, 0, inside);
+        }
+    }
+}
+
+// d/dg and d/du of silu(g) u, given the product's gradient
+template <typename E>
+__device__ __forceinline__ void gate_grads(float dh, float &gate, float &up) {
+    const float s = sigmoid<E>(gate), gs = gate * s;
+    const float dg = dh * up * (s + gs * (1.f - s));
+    up = dh * gs;
+    gate = dg;
+}
+
+// Direct kind, kGateBwd: boxes of 64 columns of both factors are read one box ahead (across tiles too),
+// and the gradients written over them.
+struct GateBwd {
+    int n[2];  // uses of either pair of boxes
+    __device__ __forceinline__ static bool inside(const GemmArgs &g, const EpiWarp &w, const GemmTile &t, int j) {
+        return t.row0 + w.rank * 128 + w.q * 32 < g.M[0] && t.col0 + j * 64 < g.N[0];
+    }
+    __device__ __forceinline__ static void ask(const GemmArgs &g, const EpiWarp &w, const GemmTile &t, int j, int set) {
+        if (w.lane != 0 || !inside(g, w, t, j)) return;
+        char *s = w.staging + set * 2 * GSLAB;
+        const int row = t.row0 + w.rank * 128 + w.q * 32, col = t.col0 + j * 64;
+        bulk_wait_read<0>();  // the gradients that lay here have been stored
+        tc::mbar_arrive_expect_tx(&w.in[set], 2 * GSLAB);
+        load_3d(s, &g.e[0], col, row, 0, &w.in[set]);
+        load_3d(s + GSLAB, &g.e[1], col, row, 0, &w.in[set]);
+    }
+    // next: the tile behind this one (col0 < 0: none)
+    __device__ __forceinline__ bool run(const GemmArgs &g, const EpiWarp &w, const GemmTile &t, const GemmTile &next, uint32_t acc,
+                                        uint32_t release) {
+        using E = __nv_bfloat16;
+        const int row = t.row0 + w.rank * 128 + w.q * 32;
+#pragma unroll 1
+        for (int j = 0; j < 4; ++j) {
+            const int set = j & 1;
+            if (j < 3)
+                ask(g, w, t, j + 1, set ^ 1);
+            else if (next.col0 >= 0)
+                ask(g, w, next, 0, set ^ 1);
+            const bool in = inside(g, w, t, j);
+            if (in && !pair_wait(&w.in[set], n[set] & 1, g.err)) return false;
+            n[set] += in;
+            char *sg = w.staging + set * 2 * GSLAB, *su = sg + GSLAB;
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                uint32_t r[32];
+                tmem_ld32(acc + j * 64 + c * 32, r);
+                tc::tmem_wait_ld();
+                tmem_use(r);
+                if (j == 3 && c == 1) {
+                    tc::tc_fence_before();
+                    __syncwarp();
+                    if (w.lane == 0) arrive_remote(release);
+                }
+                if (!in) continue;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    float xg[8], xu[8];
+                    const int at = swz128(w.lane, c * 4 + k);
+                    Vec16<E>::unpack(*reinterpret_cast<const uint4 *>(sg + at), xg);
+                    Vec16<E>::unpack(*reinterpret_cast<const uint4 *>(su + at), xu);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) gate_grads<E>(__uint_as_float(r[8 * k + e]), xg[e], xu[e]);
+                    *reinterpret_cast<uint4 *>(sg + at) = Vec16<E>::pack(xg);
+                    *reinterpret_cast<uint4 *>(su + at) = Vec16<E>::pack(xu);
+                }
+            }
+            tc::fence_proxy_async_smem();
+            __syncwarp();
+            if (in && w.lane == 0) {
+                store_3d(&g.o[0], t.col0 + j * 64, row, 0, sg);
+                store_3d(&g.o[1], t.col0 + j * 64, row, 0, su);
+                tc::bulk_commit();
+            }
+        }
+        return true;
+    }
+};
+
+// The other kinds: a thread's 128 sums of its row, in registers.
+template <int KIND, int EPI>
+__device__ __forceinline__ int sum_col(int half, int c) {  // TMEM column of sums 32 c ..
+    return EPI == kGate ? (c < 2 ? 0 : 128) + half * 64 + c % 2 * 32 : half * 128 + c * 32;
+}
+
+template <int EPI, typename E>
+__device__ __forceinline__ bool epi_sums(const GemmArgs &g, const EpiWarp &w, Ring<2> &ring, const GemmTile &t, float (&x)[128],
+                                         int &uses) {
+    constexpr int BOX = 128 / (int)sizeof(E), PER = 16 / (int)sizeof(E);  // columns of a box, of a piece
+    const int row = t.row0 + w.rank * 128 + w.q * 32;
+    if constexpr (EPI == kPlain) {
+        const int col = t.col0 + w.half * 128;
+#pragma unroll
+        for (int j = 0; j < 128 / BOX; ++j) {
+            char *slab = ring.take();
+#pragma unroll
+            for (int k = 0; k < 8; ++k) stage<E>(slab, w.lane, k, x + j * BOX + k * PER);
+            ring.put(slab, &g.o[t.p], col + j * BOX, row, 0, row < g.M[t.p] && col + j * BOX < g.N[t.p]);
+        }
+    } else if constexpr (EPI == kGate) {
+        const int col = t.col0 + w.half * 64;
+#pragma unroll
+        for (int j = 0; j < 64 / BOX; ++j) {
+            const bool inside = row < g.M[0] && col + j * BOX < g.N[0];
+            if (g.keep) {
+#pragma unroll
+                for (int f = 0; f < 2; ++f) {
+                    char *slab = ring.take();
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) stage<E>(slab, w.lane, k, x + f * 64 + j * BOX + k * PER);
+                    ring.put(slab, &g.o[1 + f], col + j * BOX, row, 0, inside);
+                }
+            }
+#pragma unroll
+            for (int e = 0; e < BOX; ++e) {
+                const float a = x[j * BOX + e];
+                x[j * BOX + e] = a * sigmoid<E>(a) * x[64 + j * BOX + e];
+            }
+            char *slab = ring.take();
+#pragma unroll
+            for (int k = 0; k < 8; ++k) stage<E>(slab, w.lane, k, x + j * BOX + k * PER);
+            ring.put(slab, &g.o[0], col + j * BOX, row, 0, inside);
+        }
+    } else {
+        const int col = t.col0 + w.half * 128;
+        char *sg = w.staging, *su = sg + GSLAB;
+#pragma unroll
+        for (int j = 0; j < 128 / BOX; ++j) {
+            if (row >= g.M[0] || col + j * BOX >= g.N[0]) continue;
+            if (w.lane == 0) {
+                bulk_wait_read<0>();
+                tc::mbar_arrive_expect_tx(w.in, 2 * GSLAB);
+                load_3d(sg, &g.e[0], col + j * BOX, row, 0, w.in);
+                load_3d(su, &g.e[1], col + j * BOX, row, 0, w.in);
+            }
+            if (!pair_wait(w.in, uses & 1, g.err)) return false;
+            ++uses;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                float xg[PER], xu[PER];
+                const int at = swz128(w.lane, k);
+                Vec16<E>::unpack(*reinterpret_cast<const uint4 *>(sg + at), xg);
+                Vec16<E>::unpack(*reinterpret_cast<const uint4 *>(su + at), xu);
+#pragma unroll
+                for (int e = 0; e < PER; ++e) gate_grads<E>(x[j * BOX + k * PER + e], xg[e], xu[e]);
+                *reinterpret_cast<uint4 *>(sg + at) = Vec16<E>::pack(xg);
+                *reinterpret_cast<uint4 *>(su + at) = Vec16<E>::pack(xu);
+            }
+            tc::fence_proxy_async_smem();
+            __syncwarp();
+            if (w.lane == 0) {
+                store_3d(&g.o[0], col + j * BOX, row, 0, sg);
+                store_3d(&g.o[1], col + j * BOX, row, 0, su);
+                tc::bulk_commit();
+            }
+        }
+    }
+    return true;
+}
+
+// A scale of 128 values whose largest magnitude is `top`, and the factors that divide by it: `up` first
+// where 1 / scale alone would overflow.
+__device__ __forceinline__ float e4m3_scale(float top, float &up) {
+    float sc = top > 0.f ? top / 448.f : 1.f;
+    up = 1.f;
+    if (sc < 0x1p-126f) {
+        sc = __fdiv_ru(top, 448.f);
+        up = 0x1p64f;
+    }
+    return sc;
+}
+__device__ __forceinline__ uint32_t e4m3x4(const float *x) {
+    const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(x[0], x[1]), __NV_SATFINITE, __NV_E4M3);
+    const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(x[2], x[3]), __NV_SATFINITE, __NV_E4M3);
+    return lo | hi << 16;
+}
+
+// kE4M3, kGate: the product's 64 columns of a thread, a scale for its row's 128 with the warp of the other half.
+// Each warp's box is 32 rows of 64 bytes (swizzled over 64 bytes); behind it, in the box's second half, lie
+// its rows' maxima for the other warp, which reads them once this one has arrived on its barrier (and
+// before it arrives itself for the next tile, so that two boxes are enough).  n: tiles before this one.
+__device__ __forceinline__ bool epi_gate_e4m3(const GemmArgs &g, const EpiWarp &w, Ring<2> &ring, const GemmTile &t, float (&x)[128],
+                                              int n) {
+    float top = 0.f;
+#pragma unroll
+    for (int e = 0; e < 64; ++e) {
+        x[e] = x[e] * sigmoid<__nv_bfloat16>(x[e]) * x[64 + e];
+        top = fmaxf(top, fabsf(x[e]));
+    }
+    char *slab = ring.take();
+    const int other = w.half ? -4 : 4;  // warps to the other half's
+    reinterpret_cast<float *>(slab + GSLAB / 2)[w.lane] = top;
+    __syncwarp();
+    if (w.lane == 0) arrive_local(w.in + other * 2);
+    if (!pair_wait(w.in, n & 1, g.err)) return false;
+    top = fmaxf(top, reinterpret_cast<const float *>(slab + GSLAB / 2 + other * (GSTAGING / 8))[w.lane]);
+    float up;
+    const float sc = e4m3_scale(top, up), is = 1.f / (sc * up);
+    const int row = t.row0 + w.rank * 128 + w.q * 32, col = t.col0 + w.half * 64;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        uint32_t v[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            float y[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) y[i] = x[16 * k + 4 * e + i] * up * is;
+            v[e] = e4m3x4(y);
+        }
+        *reinterpret_cast<uint4 *>(slab + w.lane * 64 + ((k ^ (w.lane >> 1 & 3)) << 4)) = make_uint4(v[0], v[1], v[2], v[3]);
+    }
+    ring.put(slab, &g.o[0], col, row, 0, row < g.M[0] && col < g.N[0]);
+    if (w.half == 0 && row + w.lane < g.M[0]) g.so[(size_t)(row + w.lane) * ((g.N[0] + 127) / 128) + t.col0 / 128] = sc;
+    return true;
+}
+
+static_assert(sizeof(GemmBars) <= 512, "shared memory budget");
+
+template <int AMN, int BMN, int KIND, int EPI, typename E>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(gemm_threads<KIND>(), 1) gemm_kernel(const __grid_constant__ GemmArgs g) {
+    constexpr bool E8 = KIND == kE4M3;
+    constexpr int EW = KIND == kDirect ? 4 : 8, COLS = tile_cols(EPI), KB = E8 ? 128 : 64;
+    extern __shared__ char raw[];
+    char *sm = raw + ((1024 - (tc::smem_u32(raw) & 1023)) & 1023);
+    char *ops = sm, *staging = sm + GST * 2 * GOP;
+    GemmBars &bar = *reinterpret_cast<GemmBars *>(staging + GSTAGING);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, rank = (int)cluster_rank();
+    const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+    const int tiles = tiles_of(g, COLS), per_tile = g.segs * g.kblocks;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < GST; ++s) {
+            tc::mbar_init(&bar.full[s], 1);
+            tc::mbar_init(&bar.empty[s], 1);
+        }
+        for (int s = 0; s < 2; ++s) {
+            tc::mbar_init(&bar.acc_full[s], 1);
+            tc::mbar_init(&bar.acc_empty[s], 2 * EW);
+        }
+        for (int s = 0; s < 16; ++s) tc::mbar_init(&bar.in[s >> 1][s & 1], 1);
+        tc::fence_mbar_init();
+    }
+    if (warp == 1) {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(tc::smem_u32(&bar.tmem)) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    }
+    dependent_launch();
+    tc::tc_fence_before();
+    __syncthreads();
+    cluster_sync_all();
+    tc::tc_fence_after();
+    const uint32_t tmem = bar.tmem;
+    dependent_wait();
+
+    if (warp == 0) {
+        if (tc::elect_one()) {
+            int it = 0;
+            bool ok = true;
+            for (int t = pair; ok && t < tiles; t += pairs) {
+                const GemmTile tile = tile_of(g, t, COLS);
+                const int row = tile.row0 + rank * 128, col = EPI == kGate ? tile.col0 : tile.col0 + rank * 128;
+                for (int s = 0; ok && s < g.segs; ++s) {
+                    const GemmSeg sg = g.seg[s];
+                    const CUtensorMap *ma = &g.a[tile.p + sg.a], *mb = &g.b[EPI == kGate ? sg.b + rank : tile.p + sg.b];
+                    for (int kb = 0; kb < g.kblocks; ++kb, ++it) {
+                        const int st = it % GST;
+                        if (!(ok = pair_wait(&bar.empty[st], (it / GST & 1) ^ 1, g.err))) break;
+                        if (rank == 0) tc::mbar_arrive_expect_tx(&bar.full[st], 4 * GOP);
+                        char *A = ops + st * 2 * GOP, *B = A + GOP;
+                        const uint32_t full = lead_addr(&bar.full[st]);
+                        if (AMN) {
+                            pair_load(A, ma, row, kb * 64, sg.ap, full);
+                            pair_load(A + GOP / 2, ma, row + 64, kb * 64, sg.ap, full);
+                        } else {
+                            pair_load(A, ma, kb * KB, row, sg.ap, full);
+                        }
+                        if (BMN) {
+                            pair_load(B, mb, col, kb * 64, sg.bp, full);
+                            pair_load(B + GOP / 2, mb, col + 64, kb * 64, sg.bp, full);
+                        } else {
+                            pair_load(B, mb, kb * KB, col, sg.bp, full);
+                        }
+                    }
+                }
+            }
+            // this CTA's shared memory and barriers are in use until its last stages have been read
+            for (int k = it > GST ? it - GST : 0; k < it; ++k) {
+                if (ok)
+                    ok = pair_wait(&bar.empty[k % GST], k / GST & 1, g.err);
+                else if (rank == 0)
+                    pair_wait(&bar.full[k % GST], k / GST & 1, g.err);
+            }
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        if (rank == 0 && tc::elect_one()) {
+            constexpr uint32_t id = tc::idesc(256, 256, E8 ? 0 : 1, E8 ? 0 : 1, AMN, BMN);
+            int it = 0, ch = 0;
+            bool ok = true;
+            const uint32_t ops32 = tc::smem_u32(ops);
+            for (int t = pair; ok && t < tiles; t += pairs) {
+                for (int k0 = 0; ok && k0 < per_tile; k0 += g.chunk, ++ch) {
+                    const int n = per_tile - k0 < g.chunk ? per_tile - k0 : g.chunk, ab = ch & 1;
+                    if (!(ok = pair_wait(&bar.acc_empty[ab], (ch >> 1 & 1) ^ 1, g.err))) break;
+                    tc::tc_fence_after();
+                    for (int j = 0; j < n; ++j, ++it) {
+                        const int st = it % GST;
+                        if (!(ok = pair_wait(&bar.full[st], it / GST & 1, g.err))) break;
+                        tc::tc_fence_after();
+                        const uint32_t A = ops32 + st * 2 * GOP, B = A + GOP;
+                        tc::SmemDesc da = pair_desc(A, AMN ? GOP / 2 : 16), db = pair_desc(B, BMN ? GOP / 2 : 16);
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            tc::SmemDesc a = da, b = db;
+                            a.lo += k * (AMN ? 2048 : 32) >> 4;
+                            b.lo += k * (BMN ? 2048 : 32) >> 4;
+                            pair_mma<E8>(tmem + ab * 256, a, b, id, j > 0 || k > 0);
+                        }
+                        pair_commit(&bar.empty[st]);
+                    }
+                    if (ok) pair_commit(&bar.acc_full[ab]);
+                }
+            }
+        }
+        __syncwarp();
+    } else {
+        EpiWarp w;
+        const int ew = warp - 2;
+        w.lane = lane;
+        w.q = warp & 3;
+        w.half = ew >> 2;
+        w.rank = rank;
+        w.staging = staging + ew * (GSTAGING / EW);
+        w.in = bar.in[ew];
+        w.tmem = tmem + ((uint32_t)(w.q * 32) << 16);
+        int ch = 0;
+        bool ok = true;
+        if constexpr (KIND == kDirect) {
+            Ring<4> ring = {w.staging, lane, 0};
+            GateBwd back = {{0, 0}};
+            if (EPI == kGateBwd && pair < tiles) GateBwd::ask(g, w, tile_of(g, pair, COLS), 0, 0);
+            for (int t = pair; ok && t < tiles; t += pairs, ++ch) {
+                const GemmTile tile = tile_of(g, t, COLS);
+                const int ab = ch & 1;
+                if (!(ok = pair_wait(&bar.acc_full[ab], ch >> 1 & 1, g.err))) break;
+                tc::tc_fence_after();
+                const uint32_t acc = w.tmem + ab * 256, release = lead_addr(&bar.acc_empty[ab]);
+                if constexpr (EPI == kPlain) epi_plain(g, w, ring, tile, acc, release);
+                if constexpr (EPI == kGate) epi_gate(g, w, ring, tile, acc, release);
+                if constexpr (EPI == kGateBwd) {
+                    GemmTile next = {0, 0, -1};
+                    if (t + pairs < tiles) next = tile_of(g, t + pairs, COLS);
+                    ok = back.run(g, w, tile, next, acc, release);
+                }
+            }
+        } else {
+            Ring<2> ring = {w.staging, lane, 0};
+            int uses = 0;
+            for (int t = pair; ok && t < tiles; t += pairs) {
+                const GemmTile tile = tile_of(g, t, COLS);
+                float x[128];
+#pragma unroll
+                for (int e = 0; e < 128; ++e) x[e] = 0.f;
+                const int row = tile.row0 + rank * 128 + w.q * 32 + lane;
+                const float *sa = nullptr, *sb0 = nullptr, *sb1 = nullptr;
+                if constexpr (E8) {
+                    const int blk = tile.col0 / 128 + (EPI == kGate ? 0 : w.half);
+                    if (row < g.M[tile.p]) sa = g.sa + (size_t)row * g.kblocks;
+                    if (blk * 128 < g.N[tile.p]) {
+                        sb0 = g.sb[0] + (size_t)blk * g.kblocks;
+                        if (EPI == kGate) sb1 = g.sb[1] + (size_t)blk * g.kblocks;
+                    }
+                }
+                for (int k0 = 0, i = 0; k0 < per_tile; k0 += g.chunk, ++ch, ++i) {
+                    const int ab = ch & 1;
+                    float m0 = 1.f, m1 = 1.f;
+                    if constexpr (E8) {
+                        const float s = sa ? __ldg(sa + i) : 0.f;
+                        m0 = sb0 ? s * __ldg(sb0 + i) : 0.f;
+                        m1 = EPI == kGate ? (sb1 ? s * __ldg(sb1 + i) : 0.f) : m0;
+                    }
+                    if (!(ok = pair_wait(&bar.acc_full[ab], ch >> 1 & 1, g.err))) break;
+                    tc::tc_fence_after();
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        uint32_t r[32];
+                        tmem_ld32(w.tmem + ab * 256 + sum_col<KIND, EPI>(w.half, c), r);
+                        tc::tmem_wait_ld();
+                        tmem_use(r);
+                        const float m = EPI == kGate && c >= 2 ? m1 : m0;
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) {
+                            const float v = __uint_as_float(r[e]);
+                            x[c * 32 + e] = E8 ? fmaf(v, m, x[c * 32 + e]) : x[c * 32 + e] + v;
+                        }
+                    }
+                    tc::tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) arrive_remote(lead_addr(&bar.acc_empty[ab]));
+                }
+                if (!ok) break;
+                if constexpr (E8 && EPI == kGate)
+                    ok = epi_gate_e4m3(g, w, ring, tile, x, uses++);
+                else
+                    ok = epi_sums<EPI, E>(g, w, ring, tile, x, uses);
+            }
+        }
+        if (lane == 0) bulk_wait_read<0>();  // staging is read until then
+        __syncwarp();
+    }
+    tc::tc_fence_before();
+    __syncthreads();
+    cluster_sync_all();
+    tc::tc_fence_after();
+    if (warp == 1) asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+}
+
+// ---- host side ---------------------------------------------------------------------------------
+
+ida_status device_error_word(unsigned **err, std::string &why);
+
+enum { kMapBf16 = 0, kMapF32 = 1, kMapBytes = 2 };
+// Rows of `inner` elements, ld bytes apart, in `parts` equal parts one behind the other; boxes of box0 x box1
+// elements.  What lies outside is read as zero and not written.
+ida_status gemm_map(CUtensorMap *m, const void *p, int type, long long inner, long long rows, int parts, long long ld, int box0,
+                    int box1);
+
+template <int AMN, int BMN, int KIND, int EPI, typename E>
+ida_status gemm_launch(GemmArgs &g, int num_sms, cudaStream_t st) {
+    const auto kernel = gemm_kernel<AMN, BMN, KIND, EPI, E>;
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, GSMEM);
+    if (e != cudaSuccess) return fail_with(IDA_ERR_CUDA, cudaGetErrorString(e));
+    long long tiles = 0;
+    constexpr int cols = tile_cols(EPI);
+    for (int p = 0; p < g.problems; ++p) tiles += ((long long)g.M[p] + 255) / 256 * (((long long)g.N[p] + cols - 1) / cols);
+    if (KIND == kDirect) g.chunk = g.segs * g.kblocks;
+    const long long pairs = tiles < num_sms / 2 ? tiles : num_sms / 2;
+    e = launch_dependent(kernel, dim3((unsigned)(2 * pairs)), dim3(gemm_threads<KIND>()), GSMEM, st, g);
+    if (e != cudaSuccess) return fail_with(IDA_ERR_CUDA, std::string("matrix product launch: ") + cudaGetErrorString(e));
+    return launched("matrix product");
+}
+
+// The products by operand layout (a_mn, b_mn: the contraction is the outer dimension in memory) and epilogue.
+ida_status gemm_bf16(int a_mn, int b_mn, int epi, GemmArgs &g, int num_sms, cudaStream_t st);
+ida_status gemm_f32(int a_mn, int b_mn, int epi, GemmArgs &g, int num_sms, cudaStream_t st);
+
+}  // namespace ida
