@@ -62,28 +62,19 @@ __device__ __forceinline__ uint32_t lead_addr(const void *p) {
     asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(r) : "r"(tc::smem_u32(p)));
     return r;
 }
+// No data but the accumulator's goes with this arrival, and tcgen05's own fence orders that: a release at the
+// cluster's scope would wait for all of the warp's memory accesses (8-bit gated projection 649 us, now XXX).
 __device__ __forceinline__ void arrive_remote(uint32_t addr) {
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
 }
 __device__ __forceinline__ void arrive_local(uint64_t *bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(tc::smem_u32(bar)) : "memory");
 }
-__device__ __forceinline__ bool try_wait_cluster(uint64_t *bar, uint32_t parity) {
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(tc::smem_u32(bar)), "r"(parity)
-        : "memory");
-    return ok != 0;
-}
 // Waits of about a second at most; the role that gives up reports it and ends, and the others follow.
 __device__ __forceinline__ bool pair_wait(uint64_t *bar, uint32_t parity, unsigned *err) {
-    if (try_wait_cluster(bar, parity)) return true;
+    if (tc::mbar_try_wait(bar, parity)) return true;
     const long long t0 = clock64();
-    while (!try_wait_cluster(bar, parity))
+    while (!tc::mbar_try_wait(bar, parity))
         if (clock64() - t0 > 2000000000LL) {
             report_error(err, kErrWaitTimeout);
             return false;
@@ -150,6 +141,14 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
 __device__ __forceinline__ void tmem_use(uint32_t (&r)[32]) {  // keeps uses of r behind the wait
 #pragma unroll
     for (int i = 0; i < 32; ++i) asm volatile("" : "+r"(r[i]));
+}
+
+// (x0, x1) += (v0, v1) m, two at a time
+__device__ __forceinline__ void add_scaled(float &x0, float &x1, uint32_t v0, uint32_t v1, float m) {
+    asm("{\n\t.reg .b64 x, v, m;\n\tmov.b64 x, {%0, %1};\n\tmov.b64 v, {%2, %3};\n\tmov.b64 m, {%4, %4};\n\t"
+        "fma.rn.f32x2 x, v, m, x;\n\tmov.b64 {%0, %1}, x;\n\t}"
+        : "+f"(x0), "+f"(x1)
+        : "r"(v0), "r"(v1), "f"(m));
 }
 
 // Shared-memory descriptor of a 128-byte-swizzled operand (rows of 128 bytes, 1024 bytes between groups of
@@ -233,7 +232,7 @@ __device__ __forceinline__ void stage(char *slab, int row, int piece, const floa
 // ---- the kernel ------------------------------------------------------------------------------
 
 template <int KIND>
-constexpr int gemm_threads() { return KIND == kDirect ? 192 : 320; }
+constexpr int gemm_threads() { return KIND == kDirect ? 192 : 384; }
 
 struct GemmBars {
     uint64_t full[GST], empty[GST], acc_full[2], acc_empty[2], in[8][2];
@@ -538,7 +537,7 @@ static_assert(sizeof(GemmBars) <= 512, "shared memory budget");
 template <int AMN, int BMN, int KIND, int EPI, typename E>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(gemm_threads<KIND>(), 1) gemm_kernel(const __grid_constant__ GemmArgs g) {
     constexpr bool E8 = KIND == kE4M3;
-    constexpr int EW = KIND == kDirect ? 4 : 8, COLS = tile_cols(EPI), KB = E8 ? 128 : 64;
+    constexpr int EW = KIND == kDirect ? 4 : 8, E0 = KIND == kDirect ? 2 : 4, COLS = tile_cols(EPI), KB = E8 ? 128 : 64;
     extern __shared__ char raw[];
     char *sm = raw + ((1024 - (tc::smem_u32(raw) & 1023)) & 1023);
     char *ops = sm, *staging = sm + GST * 2 * GOP;
@@ -571,8 +570,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(gemm_threads<KIND>()
     const uint32_t tmem = bar.tmem;
     dependent_wait();
 
-    if (warp == 0) {
-        if (tc::elect_one()) {
+    // sums in registers: 168 of them a thread at launch (64512 in all), 64 for the first four warps leave
+    // 216 for the other eight (63488)
+    if (warp < E0) {
+        if (KIND != kDirect) asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+        if (warp == 0 && tc::elect_one()) {
             int it = 0;
             bool ok = true;
             for (int t = pair; ok && t < tiles; t += pairs) {
@@ -610,9 +612,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(gemm_threads<KIND>()
                     pair_wait(&bar.full[k % GST], k / GST & 1, g.err);
             }
         }
-        __syncwarp();
-    } else if (warp == 1) {
-        if (rank == 0 && tc::elect_one()) {
+        if (warp == 1 && rank == 0 && tc::elect_one()) {
             constexpr uint32_t id = tc::idesc(256, 256, E8 ? 0 : 1, E8 ? 0 : 1, AMN, BMN);
             int it = 0, ch = 0;
             bool ok = true;
@@ -643,8 +643,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(gemm_threads<KIND>()
         }
         __syncwarp();
     } else {
+        if (KIND != kDirect) asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
         EpiWarp w;
-        const int ew = warp - 2;
+        const int ew = warp - E0;
         w.lane = lane;
         w.q = warp & 3;
         w.half = ew >> 2;
@@ -690,32 +691,38 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(gemm_threads<KIND>()
                         if (EPI == kGate) sb1 = g.sb[1] + (size_t)blk * g.kblocks;
                     }
                 }
+                // the scales are read a block ahead
+                float na = 0.f, n0 = 0.f, n1 = 0.f;
+                auto scales = [&](int i) {
+                    na = sa ? __ldg(sa + i) : 0.f;
+                    n0 = sb0 ? __ldg(sb0 + i) : 0.f;
+                    if (EPI == kGate) n1 = sb1 ? __ldg(sb1 + i) : 0.f;
+                };
+                if constexpr (E8) scales(0);
                 for (int k0 = 0, i = 0; k0 < per_tile; k0 += g.chunk, ++ch, ++i) {
                     const int ab = ch & 1;
-                    float m0 = 1.f, m1 = 1.f;
-                    if constexpr (E8) {
-                        const float s = sa ? __ldg(sa + i) : 0.f;
-                        m0 = sb0 ? s * __ldg(sb0 + i) : 0.f;
-                        m1 = EPI == kGate ? (sb1 ? s * __ldg(sb1 + i) : 0.f) : m0;
-                    }
+                    const float m0 = E8 ? na * n0 : 1.f, m1 = E8 && EPI == kGate ? na * n1 : m0;
+                    if (E8 && i + 1 < g.kblocks) scales(i + 1);
                     if (!(ok = pair_wait(&bar.acc_full[ab], ch >> 1 & 1, g.err))) break;
                     tc::tc_fence_after();
+                    const uint32_t acc = w.tmem + ab * 256;
+                    uint32_t r[2][32];
+                    tmem_ld32(acc + sum_col<KIND, EPI>(w.half, 0), r[0]);
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        uint32_t r[32];
-                        tmem_ld32(w.tmem + ab * 256 + sum_col<KIND, EPI>(w.half, c), r);
+                    for (int c = 0; c < 4; ++c) {  // the next 32 columns come while these are added
                         tc::tmem_wait_ld();
-                        tmem_use(r);
+                        tmem_use(r[c & 1]);
+                        if (c < 3) {
+                            tmem_ld32(acc + sum_col<KIND, EPI>(w.half, c + 1), r[(c + 1) & 1]);
+                        } else {
+                            tc::tc_fence_before();
+                            __syncwarp();
+                            if (lane == 0) arrive_remote(lead_addr(&bar.acc_empty[ab]));
+                        }
                         const float m = EPI == kGate && c >= 2 ? m1 : m0;
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) {
-                            const float v = __uint_as_float(r[e]);
-                            x[c * 32 + e] = E8 ? fmaf(v, m, x[c * 32 + e]) : x[c * 32 + e] + v;
-                        }
+                        for (int e = 0; e < 32; e += 2) add_scaled(x[c * 32 + e], x[c * 32 + e + 1], r[c & 1][e], r[c & 1][e + 1], m);
                     }
-                    tc::tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) arrive_remote(lead_addr(&bar.acc_empty[ab]));
                 }
                 if (!ok) break;
                 if constexpr (E8 && EPI == kGate)
