@@ -5,6 +5,7 @@
 //   out = sum over blocks k of 128 channels  sa[t, k] sb[n / 128, k] sum of a[t, .] b[n, .] over the block
 //   h = silu(g) u of two such products, quantised again with a scale for 128 channels of each row
 #include "ida_gemm.cuh"
+#include "ida_skinny.cuh"
 
 namespace ida {
 
@@ -203,6 +204,10 @@ ida_status ida_gemm_e4m3(const void *a, const float *a_scale, const void *b, con
     std::string why;
     s = device_ready(&num_sms, why);
     if (s != IDA_OK) return fail_with(s, why);
+    if (rows <= kFewRows) {
+        SkinnyArgs k = {a, K, b, nullptr, out, nullptr, nullptr, a_scale, b_scale, nullptr, nullptr, rows, K, N, dtype == IDA_F32, false};
+        return skinny_product(k, true, num_sms, reinterpret_cast<cudaStream_t>(stream));
+    }
     GemmArgs g = {};
     s = device_error_word(&g.err, why);
     if (s != IDA_OK) return fail_with(s, why);
@@ -237,6 +242,10 @@ ida_status ida_glu_e4m3(const void *a, const float *a_scale, const void *w_gate,
     std::string why;
     s = device_ready(&num_sms, why);
     if (s != IDA_OK) return fail_with(s, why);
+    if (rows <= kFewRows) {
+        SkinnyArgs k = {a, D, w_gate, w_up, q, nullptr, nullptr, a_scale, gate_scale, up_scale, scale, rows, D, F, false, false};
+        return skinny_gate(k, true, reinterpret_cast<cudaStream_t>(stream));
+    }
     GemmArgs g = {};
     s = device_error_word(&g.err, why);
     if (s != IDA_OK) return fail_with(s, why);

@@ -15,6 +15,7 @@
 #include <mutex>
 
 #include "ida_gemm.cuh"
+#include "ida_skinny.cuh"
 
 namespace ida {
 
@@ -228,6 +229,13 @@ ida_status ida_ffn(const void *x, const void *w_gate, const void *w_up, const vo
 
     char *ws = static_cast<char *>(workspace), *ac = static_cast<char *>(acts);
     void *h = ac ? ac + 2 * tf * es : ws + sp.h;
+    if (rows <= kFewRows && dtype == IDA_BF16) {
+        SkinnyArgs a = {x, ldx, w_gate, w_up, h, ac, ac ? ac + tf * es : nullptr, nullptr, nullptr, nullptr, nullptr, rows, D, F, false, false};
+        s = skinny_gate(a, false, st);
+        if (s != IDA_OK) return s;
+        SkinnyArgs b = {h, F, w_down, nullptr, out, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr, rows, F, D, false, true};
+        return skinny_product(b, false, num_sms, st);
+    }
     const int parts = dtype == IDA_BF16 ? 1 : 3;
     Operand X = {x, parts, rows, D, ldx}, Wg = {w_gate, parts, F, D, D}, Wu = {w_up, parts, F, D, D}, Wd = {w_down, parts, D, F, F},
             H = {h, parts, rows, F, F};

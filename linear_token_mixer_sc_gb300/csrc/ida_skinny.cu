@@ -1,0 +1,254 @@
+// ida_skinny.cu -- the feed-forward block's and the 8-bit products for a few rows (decoding), where
+// the weights' bytes bound them.
+//
+// Every weight is read once, 16 bytes a lane straight into the registers of a matrix instruction: the
+// weights are its 16 x K operand, the rows (tokens) its 8 columns, so the tile that tcgen05 would want
+// (128 weights' rows at least, through shared memory) is not needed and the loads of all warps of all SMs
+// are in flight at once.  A quad of lanes reads 64 bytes of a weight's row; the instruction's order of the
+// contraction is any one order that both operands share, so a lane's 16 bytes serve two instructions.
+// The warps of a block share its weights' rows and split the contraction; their sums meet in shared
+// memory, in a fixed order.  The gate's kernel pairs 8 rows of each weight in one instruction, so that both factors of a
+// product come out in the same block.  Few weights' rows are spread over more blocks, 8 to a block.
+#include "ida_gemm.cuh"
+#include "ida_skinny.cuh"
+
+namespace ida {
+
+__device__ __forceinline__ void mma_rows(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1,
+                                         bool e4m3) {
+    if (e4m3)
+        asm("mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+            : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+    else
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+            : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// the value at the same place of the shared memory of CTA `rank` of the cluster
+__device__ __forceinline__ float remote_float(const float *p, int rank) {
+    uint32_t a;
+    float v;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(tc::smem_u32(p)), "r"(rank));
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(a) : "memory");
+    return v;
+}
+
+constexpr int SKW = 8;  // warps of a block
+
+// NT: groups of 8 tokens.  SUB tiles of 16 weights' rows a block, of which a plain product may use 8 (HALVES
+// 1).  GATE: rows 8 .. 15 of a tile are w1's.  E8 && GATE: a cluster of 8 blocks makes the 128 channels of
+// a scale.
+template <bool E8, int NT, int SUB, int HALVES, bool GATE>
+__global__ void __launch_bounds__(SKW * 32) skinny_kernel(SkinnyArgs a) {
+    constexpr int U = 4 / (SUB * HALVES), LD = 8 * NT + 1, ES = E8 ? 1 : 2;
+    constexpr int COLS = SUB * (GATE ? 8 : 8 * HALVES);  // output columns of a block
+    extern __shared__ float red[];  // [SKW][SUB][16][LD]
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3, nw = blockDim.x >> 5;
+    const long long n0 = (long long)blockIdx.x * COLS;
+    const long long kbytes = (long long)a.K * ES;
+    const int chunks = (int)((kbytes + 127) / 128);
+    const char *row[SUB][HALVES];
+#pragma unroll
+    for (int s = 0; s < SUB; ++s)
+#pragma unroll
+        for (int h = 0; h < HALVES; ++h) {
+            long long r = n0 + (GATE ? 8 * s : 8 * HALVES * s + 8 * h) + g;
+            if (r >= a.N) r = a.N - 1;  // not stored
+            row[s][h] = static_cast<const char *>(GATE && h ? a.w1 : a.w0) + r * kbytes;
+        }
+    float acc[SUB][NT][4];
+#pragma unroll
+    for (int s = 0; s < SUB; ++s)
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) acc[s][n][i] = 0.f;
+
+    uint4 w[U][SUB][HALVES][2];
+    auto fetch = [&](int c0) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int c = c0 + u * nw;
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const long long at = (long long)c * 128 + j * 64 + t * 16;
+#pragma unroll
+                for (int s = 0; s < SUB; ++s)
+#pragma unroll
+                    for (int h = 0; h < HALVES; ++h)
+                        w[u][s][h][j] = c < chunks && at < kbytes ? __ldcs(reinterpret_cast<const uint4 *>(row[s][h] + at)) : make_uint4(0, 0, 0, 0);
+            }
+        }
+    };
+    // the launch before makes x: a product that follows the gate's in one call has its weights read meanwhile
+    // (that one waited for all before it), any other call waits first
+    if (!a.weights_ready) dependent_wait();
+    fetch(warp);
+    if (a.weights_ready) dependent_wait();
+    dependent_launch();
+    for (int c0 = warp; c0 < chunks; c0 += U * nw) {
+        if (c0 != warp) fetch(c0);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int c = c0 + u * nw;
+            if (c >= chunks) break;
+            uint4 x[NT][2];
+            float m[NT][2];
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    const long long at = (long long)c * 128 + j * 64 + t * 16;
+                    const int tok = 8 * n + g;
+                    x[n][j] = tok < a.T && at < kbytes
+                                  ? __ldg(reinterpret_cast<const uint4 *>(static_cast<const char *>(a.x) + tok * a.ldx * ES + at))
+                                  : make_uint4(0, 0, 0, 0);
+                    if (E8) m[n][j] = 8 * n + 2 * t + j < a.T ? __ldg(a.sa + (long long)(8 * n + 2 * t + j) * chunks + c) : 0.f;
+                }
+#pragma unroll
+            for (int s = 0; s < SUB; ++s) {
+                float s0 = 1.f, s1 = 1.f;
+                if (E8) {
+                    const long long blk = n0 / 128 * chunks + c;
+                    s0 = __ldg(a.s0 + blk);
+                    s1 = GATE ? __ldg(a.s1 + blk) : s0;
+                }
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    float part[4] = {0.f, 0.f, 0.f, 0.f};
+                    float(&d)[4] = E8 ? part : acc[s][n];
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        const uint4 lo = w[u][s][0][j], hi = HALVES == 2 ? w[u][s][HALVES - 1][j] : make_uint4(0, 0, 0, 0);
+                        mma_rows(d, lo.x, hi.x, lo.y, hi.y, x[n][j].x, x[n][j].y, E8);
+                        mma_rows(d, lo.z, hi.z, lo.w, hi.w, x[n][j].z, x[n][j].w, E8);
+                    }
+                    if (E8) {
+                        acc[s][n][0] = fmaf(part[0], m[n][0] * s0, acc[s][n][0]);
+                        acc[s][n][1] = fmaf(part[1], m[n][1] * s0, acc[s][n][1]);
+                        acc[s][n][2] = fmaf(part[2], m[n][0] * s1, acc[s][n][2]);
+                        acc[s][n][3] = fmaf(part[3], m[n][1] * s1, acc[s][n][3]);
+                    }
+                }
+            }
+        }
+    }
+#pragma unroll
+    for (int s = 0; s < SUB; ++s)
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) red[((warp * SUB + s) * 16 + g + (i >> 1) * 8) * LD + 8 * n + 2 * t + (i & 1)] = acc[s][n][i];
+    __syncthreads();
+    auto sum = [&](int s, int r, int tok) {
+        float v = red[(s * 16 + r) * LD + tok];
+        for (int k = 1; k < nw; ++k) v += red[((k * SUB + s) * 16 + r) * LD + tok];
+        return v;
+    };
+    if constexpr (!GATE) {
+        for (int i = threadIdx.x; i < COLS * a.T; i += blockDim.x) {
+            const int tok = i / COLS, c = i % COLS;
+            if (n0 + c >= a.N) continue;
+            const float v = sum(c / (8 * HALVES), c % (8 * HALVES), tok);
+            const long long at = tok * a.N + n0 + c;
+            if (a.out_f32)
+                static_cast<float *>(a.out)[at] = v;
+            else
+                static_cast<__nv_bfloat16 *>(a.out)[at] = __float2bfloat16_rn(v);
+        }
+    } else if constexpr (!E8) {
+        for (int i = threadIdx.x; i < COLS * a.T; i += blockDim.x) {
+            const int tok = i / COLS, c = i % COLS;
+            const float x = sum(c / 8, c % 8, tok), y = sum(c / 8, 8 + c % 8, tok);
+            const long long at = tok * a.N + n0 + c;
+            static_cast<__nv_bfloat16 *>(a.out)[at] = __float2bfloat16_rn(x * sigmoid<__nv_bfloat16>(x) * y);
+            if (a.out_g) {
+                static_cast<__nv_bfloat16 *>(a.out_g)[at] = __float2bfloat16_rn(x);
+                static_cast<__nv_bfloat16 *>(a.out_u)[at] = __float2bfloat16_rn(y);
+            }
+        }
+    } else {
+        // 16 channels of a row are 16 lanes'; the 8 blocks of a cluster have the 128 of a scale
+        __shared__ float top[8 * NT];
+        const int c = threadIdx.x & 15, rank = (int)cluster_rank();
+        float v[NT * 8 / 16 + (NT == 1)];
+#pragma unroll
+        for (int k = 0; k < NT * 8 / 16 + (NT == 1); ++k) {
+            const int tok = (threadIdx.x >> 4) + 16 * k;
+            v[k] = 0.f;
+            if (tok < a.T && n0 + c < a.N) {
+                const float x = sum(c / 8, c % 8, tok), y = sum(c / 8, 8 + c % 8, tok);
+                v[k] = x * sigmoid<__nv_bfloat16>(x) * y;
+            }
+            float m = fabsf(v[k]);
+#pragma unroll
+            for (int o = 8; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+            if (c == 0 && tok < 8 * NT) top[tok] = m;
+        }
+        cluster_sync_all();
+#pragma unroll
+        for (int k = 0; k < NT * 8 / 16 + (NT == 1); ++k) {
+            const int tok = (threadIdx.x >> 4) + 16 * k;
+            float m = 0.f;
+            if (tok < 8 * NT)
+                for (int r = 0; r < 8; ++r) m = fmaxf(m, remote_float(&top[tok], r));
+            float up;
+            const float sc = e4m3_scale(m, up), is = 1.f / (sc * up);
+            if (tok < a.T && n0 + c < a.N) {
+                const __nv_fp8_storage_t q = __nv_cvt_float_to_fp8(v[k] * up * is, __NV_SATFINITE, __NV_E4M3);
+                static_cast<uint8_t *>(a.out)[tok * (long long)a.N + n0 + c] = q;
+                if (rank == 0 && c == 0) a.so[(long long)tok * ((a.N + 127) / 128) + n0 / 128] = sc;
+            }
+        }
+        cluster_sync_all();  // the maxima have been read
+    }
+}
+
+template <bool E8, int NT, int SUB, int HALVES, bool GATE>
+static ida_status launch_skinny(const SkinnyArgs &a, cudaStream_t st) {
+    constexpr int cols = SUB * (GATE ? 8 : 8 * HALVES);
+    const auto kernel = skinny_kernel<E8, NT, SUB, HALVES, GATE>;
+    const long long chunks = ((long long)a.K * (E8 ? 1 : 2) + 127) / 128;
+    // the 8-bit gate's threads make 16 channels of 16 rows at a time
+    const int warps = E8 && GATE ? SKW : chunks < SKW ? (int)chunks : SKW;
+    const size_t smem = (size_t)warps * SUB * 16 * (8 * NT + 1) * sizeof(float);
+    cudaError_t e = allow_smem(kernel, smem);
+    if (e != cudaSuccess) return fail_with(IDA_ERR_CUDA, cudaGetErrorString(e));
+    cudaLaunchConfig_t cfg = {};
+    const unsigned blocks = (unsigned)((a.N + cols - 1) / cols);
+    cfg.gridDim = dim3(E8 && GATE ? (blocks + 7) / 8 * 8 : blocks);
+    cfg.blockDim = dim3(warps * 32);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute at[2];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    at[1].id = cudaLaunchAttributeClusterDimension;
+    at[1].val.clusterDim.x = 8;
+    at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = E8 && GATE ? 2 : 1;
+    e = cudaLaunchKernelEx(&cfg, kernel, a);
+    if (e != cudaSuccess) return fail_with(IDA_ERR_CUDA, std::string("few rows' product launch: ") + cudaGetErrorString(e));
+    return launched("few rows' product");
+}
+
+template <bool E8, int SUB, int HALVES, bool GATE>
+static ida_status launch_skinny_rows(const SkinnyArgs &a, cudaStream_t st) {
+    if (a.T <= 8) return launch_skinny<E8, 1, SUB, HALVES, GATE>(a, st);
+    if (a.T <= 16) return launch_skinny<E8, 2, SUB, HALVES, GATE>(a, st);
+    return launch_skinny<E8, 4, SUB, HALVES, GATE>(a, st);
+}
+
+ida_status skinny_product(const SkinnyArgs &a, bool e4m3, int num_sms, cudaStream_t st) {
+    // 16 rows of weights to a block where that leaves every SM two of them
+    if (a.N >= 32 * num_sms) return e4m3 ? launch_skinny_rows<true, 1, 2, false>(a, st) : launch_skinny_rows<false, 1, 2, false>(a, st);
+    return e4m3 ? launch_skinny_rows<true, 1, 1, false>(a, st) : launch_skinny_rows<false, 1, 1, false>(a, st);
+}
+ida_status skinny_gate(const SkinnyArgs &a, bool e4m3, cudaStream_t st) {
+    return e4m3 ? launch_skinny_rows<true, 2, 2, true>(a, st) : launch_skinny_rows<false, 1, 2, true>(a, st);
+}
+
+}  // namespace ida

@@ -28,7 +28,7 @@ def _operand(T, K, block_rows, seed):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
-@pytest.mark.parametrize("T,K,N", [(1, 16, 8), (1, 2048, 264), (5, 384, 136), (33, 128, 128), (128, 144, 256), (129, 256, 264), (300, 1040, 72),
+@pytest.mark.parametrize("T,K,N", [(1, 16, 8), (1, 2048, 264), (5, 384, 136), (8, 128, 5000), (9, 2064, 136), (17, 400, 1000), (32, 5632, 72), (33, 128, 128), (128, 144, 256), (129, 256, 264), (300, 1040, 72),
                                    (257, 640, 520), (700, 272, 1000)])
 def test_product(T, K, N, dtype):
     a, sa = _operand(T, K, 1, 3)
@@ -40,7 +40,7 @@ def test_product(T, K, N, dtype):
     assert worst(out, v, e + HALF[dtype] * v.abs()) <= 1
 
 
-@pytest.mark.parametrize("T,D,F", [(1, 16, 16), (1, 2048, 272), (5, 384, 144), (33, 128, 128), (128, 144, 256), (129, 256, 272), (300, 1040, 80),
+@pytest.mark.parametrize("T,D,F", [(1, 16, 16), (1, 2048, 272), (5, 384, 144), (8, 128, 1264), (9, 2064, 144), (16, 144, 128), (17, 400, 1008), (32, 2048, 80), (33, 128, 128), (128, 144, 256), (129, 256, 272), (300, 1040, 80),
                                    (700, 272, 1040)])
 def test_gated_projection(T, D, F):
     a, sa = _operand(T, D, 1, 3)

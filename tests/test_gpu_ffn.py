@@ -9,7 +9,7 @@ from tests.ssm_cases import DT, worst
 pytestmark = pytest.mark.gpu
 
 # rows, channels, hidden channels: one row, tiles that end anywhere, contractions shorter than a block
-SIZES = [(1, 8, 8), (1, 64, 176), (2, 128, 344), (7, 40, 24), (31, 200, 72), (33, 64, 64), (128, 64, 128), (129, 72, 136), (251, 64, 176),
+SIZES = [(1, 8, 8), (1, 64, 176), (2, 128, 344), (7, 40, 24), (8, 2048, 5632), (9, 264, 520), (16, 72, 1000), (31, 200, 72), (33, 64, 64), (128, 64, 128), (129, 72, 136), (251, 64, 176),
          (256, 256, 256), (300, 520, 264), (513, 768, 520), (1000, 136, 1032)]
 
 
