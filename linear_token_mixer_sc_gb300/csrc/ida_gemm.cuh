@@ -24,12 +24,16 @@ namespace ida {
 
 enum { kDirect = 0, kParts = 1, kE4M3 = 2 };          // operands: bf16, three bf16 parts of fp32, e4m3
 enum { kPlain = 0, kGate = 1, kGateBwd = 2 };         // epilogues
-constexpr int GST = 5;                                // stages
+constexpr int GST = 5;                                // stages at most
 constexpr int GOP = 128 * 128;                        // bytes of an operand of a stage
 constexpr int GSLAB = 32 * 128;                       // bytes of a warp's staged box: 32 rows of 128 bytes
 constexpr int GSTAGING = 64 * 1024;                   // of all epilogue warps
-constexpr int GSMEM = GST * 2 * GOP + GSTAGING + 1024 + 512;
-static_assert(GSMEM <= 227 * 1024, "shared memory budget");
+constexpr int gemm_halves(int kind) { return kind == kParts ? 2 : 1; }
+// The gradients of the gate in fp32 stage two boxes for each of sixteen warps, and take two stages less.
+constexpr int gemm_stages(int kind, int epi) { return kind == kParts && epi == kGateBwd ? 3 : GST; }
+constexpr int gemm_staging(int kind, int epi) { return kind == kParts && epi == kGateBwd ? 2 * GSTAGING : GSTAGING; }
+constexpr int gemm_smem(int kind, int epi) { return gemm_stages(kind, epi) * 2 * GOP + gemm_staging(kind, epi) + 1024 + 512; }
+static_assert(gemm_smem(kDirect, kPlain) <= 227 * 1024 && gemm_smem(kParts, kGateBwd) <= 227 * 1024, "shared memory budget");
 
 struct GemmSeg {
     unsigned char a, ap, b, bp;  // maps and parts of one pass over the contraction
@@ -80,6 +84,9 @@ __device__ __forceinline__ bool pair_wait(uint64_t *bar, uint32_t parity, unsign
             return false;
         }
     return true;
+}
+__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, unsigned *err) {  // by a whole warp
+    return __all_sync(0xffffffffu, pair_wait(bar, parity, err));
 }
 __device__ __forceinline__ void pair_load(void *dst, const void *map, int c0, int c1, int c2, uint32_t bar) {
     asm volatile(
@@ -138,9 +145,17 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
           "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
         : "r"(taddr));
 }
-__device__ __forceinline__ void tmem_use(uint32_t (&r)[32]) {  // keeps uses of r behind the wait
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr));
+}
+template <int N>
+__device__ __forceinline__ void tmem_use(uint32_t (&r)[N]) {  // keeps uses of r behind the wait
 #pragma unroll
-    for (int i = 0; i < 32; ++i) asm volatile("" : "+r"(r[i]));
+    for (int i = 0; i < N; ++i) asm volatile("" : "+r"(r[i]));
 }
 
 // (x0, x1) += (v0, v1) m, two at a time
@@ -232,10 +247,10 @@ __device__ __forceinline__ void stage(char *slab, int row, int piece, const floa
 // ---- the kernel ------------------------------------------------------------------------------
 
 template <int KIND>
-constexpr int gemm_threads() { return KIND == kDirect ? 192 : 384; }
+constexpr int gemm_threads() { return KIND == kDirect ? 192 : 640; }
 
 struct GemmBars {
-    uint64_t full[GST], empty[GST], acc_full[2], acc_empty[2], in[8][2];
+    uint64_t full[GST], empty[GST], acc_full[2][2], acc_empty[2][2], in[16][2];
     uint32_t tmem;
 };
 
@@ -243,8 +258,9 @@ struct GemmBars {
 struct EpiWarp {
     char *staging;
     uint64_t *in;   // its barriers for what the epilogue reads
-    int lane, q, half, rank;
-    uint32_t tmem;  // of its lanes
+    int lane, q, rank;
+    int half, part;  // its accumulator (other kinds) and which part of that one's columns
+    uint32_t tmem;   // of its lanes
 };
 
 // Direct kind, kPlain: 256 columns in bf16.
@@ -395,55 +411,54 @@ struct GateBwd {
     }
 };
 
-// The other kinds: a thread's 128 sums of its row, in registers.
+// The other kinds: a thread's 64 sums of its row, in registers.  A tile's accumulator comes in two halves of 128
+// columns, each CTA's first 64 columns of B and its last 64, that are filled and emptied by themselves;
+// two groups of four warps empty a half: kGate, 32 columns of either factor each, otherwise one CTA's 64 each.
 template <int KIND, int EPI>
-__device__ __forceinline__ int sum_col(int half, int c) {  // TMEM column of sums 32 c ..
-    return EPI == kGate ? (c < 2 ? 0 : 128) + half * 64 + c % 2 * 32 : half * 128 + c * 32;
+__device__ __forceinline__ int sum_col(const EpiWarp &w, int c) {  // TMEM column of sums 16 c .., of the half's
+    if (gemm_halves(KIND) == 1)
+        return EPI == kGate ? w.half * 64 + w.part * 32 + c / 2 * 128 + c % 2 * 16 : w.part * 128 + w.half * 64 + c * 16;
+    return EPI == kGate ? w.part * 32 + c / 2 * 64 + c % 2 * 16 : w.part * 64 + c * 16;
 }
 
 template <int EPI, typename E>
-__device__ __forceinline__ bool epi_sums(const GemmArgs &g, const EpiWarp &w, Ring<2> &ring, const GemmTile &t, float (&x)[128],
-                                         int &uses) {
+__device__ __forceinline__ bool epi_sums(const GemmArgs &g, const EpiWarp &w, const GemmTile &t, float (&x)[64], int &uses) {
     constexpr int BOX = 128 / (int)sizeof(E), PER = 16 / (int)sizeof(E);  // columns of a box, of a piece
     const int row = t.row0 + w.rank * 128 + w.q * 32;
+    Ring<1> ring = {w.staging, w.lane, 0};
     if constexpr (EPI == kPlain) {
-        const int col = t.col0 + w.half * 128;
+        const int col = t.col0 + w.part * 128 + w.half * 64;
 #pragma unroll
-        for (int j = 0; j < 128 / BOX; ++j) {
+        for (int j = 0; j < 64 / BOX; ++j) {
             char *slab = ring.take();
 #pragma unroll
             for (int k = 0; k < 8; ++k) stage<E>(slab, w.lane, k, x + j * BOX + k * PER);
             ring.put(slab, &g.o[t.p], col + j * BOX, row, 0, row < g.M[t.p] && col + j * BOX < g.N[t.p]);
         }
     } else if constexpr (EPI == kGate) {
-        const int col = t.col0 + w.half * 64;
+        static_assert(BOX == 32, "fp32");
+        const int col = t.col0 + w.half * 64 + w.part * 32;
+        const bool inside = row < g.M[0] && col < g.N[0];
+        if (g.keep) {
 #pragma unroll
-        for (int j = 0; j < 64 / BOX; ++j) {
-            const bool inside = row < g.M[0] && col + j * BOX < g.N[0];
-            if (g.keep) {
+            for (int f = 0; f < 2; ++f) {
+                char *slab = ring.take();
 #pragma unroll
-                for (int f = 0; f < 2; ++f) {
-                    char *slab = ring.take();
-#pragma unroll
-                    for (int k = 0; k < 8; ++k) stage<E>(slab, w.lane, k, x + f * 64 + j * BOX + k * PER);
-                    ring.put(slab, &g.o[1 + f], col + j * BOX, row, 0, inside);
-                }
+                for (int k = 0; k < 8; ++k) stage<E>(slab, w.lane, k, x + f * 32 + k * PER);
+                ring.put(slab, &g.o[1 + f], col, row, 0, inside);
             }
-#pragma unroll
-            for (int e = 0; e < BOX; ++e) {
-                const float a = x[j * BOX + e];
-                x[j * BOX + e] = a * sigmoid<E>(a) * x[64 + j * BOX + e];
-            }
-            char *slab = ring.take();
-#pragma unroll
-            for (int k = 0; k < 8; ++k) stage<E>(slab, w.lane, k, x + j * BOX + k * PER);
-            ring.put(slab, &g.o[0], col + j * BOX, row, 0, inside);
         }
+#pragma unroll
+        for (int e = 0; e < 32; ++e) x[e] = x[e] * sigmoid<E>(x[e]) * x[32 + e];
+        char *slab = ring.take();
+#pragma unroll
+        for (int k = 0; k < 8; ++k) stage<E>(slab, w.lane, k, x + k * PER);
+        ring.put(slab, &g.o[0], col, row, 0, inside);
     } else {
-        const int col = t.col0 + w.half * 128;
+        const int col = t.col0 + w.part * 128 + w.half * 64;
         char *sg = w.staging, *su = sg + GSLAB;
 #pragma unroll
-        for (int j = 0; j < 128 / BOX; ++j) {
+        for (int j = 0; j < 64 / BOX; ++j) {
             if (row >= g.M[0] || col + j * BOX >= g.N[0]) continue;
             if (w.lane == 0) {
                 bulk_wait_read<0>();
@@ -493,30 +508,34 @@ __device__ __forceinline__ uint32_t e4m3x4(const float *x) {
     return lo | hi << 16;
 }
 
-// kE4M3, kGate: the product's 64 columns of a thread, a scale for its row's 128 with the warp of the other half.
-// Each warp's box is 32 rows of 64 bytes (swizzled over 64 bytes); behind it, in the box's second half, lie
-// its rows' maxima for the other warp, which reads them once this one has arrived on its barrier (and
-// before it arrives itself for the next tile, so that two boxes are enough).  n: tiles before this one.
-__device__ __forceinline__ bool epi_gate_e4m3(const GemmArgs &g, const EpiWarp &w, Ring<2> &ring, const GemmTile &t, float (&x)[128],
-                                              int n) {
+// kE4M3, kGate: the product's 32 columns of a thread, a scale for its row's 128 with the three other warps of those
+// rows.  Each warp's box is 32 rows of 32 bytes (swizzled over 32 bytes); behind it lie its rows' maxima
+// for the other warps, which read them once this one has arrived on their barriers (and before they arrive
+// themselves for the next tile, so that two sets are enough).  n: tiles before this one.
+__device__ __forceinline__ bool epi_gate_e4m3(const GemmArgs &g, const EpiWarp &w, const GemmTile &t, float (&x)[64], int n) {
     float top = 0.f;
 #pragma unroll
-    for (int e = 0; e < 64; ++e) {
-        x[e] = x[e] * sigmoid<__nv_bfloat16>(x[e]) * x[64 + e];
+    for (int e = 0; e < 32; ++e) {
+        x[e] = x[e] * sigmoid<__nv_bfloat16>(x[e]) * x[32 + e];
         top = fmaxf(top, fabsf(x[e]));
     }
+    Ring<1> ring = {w.staging, w.lane, 0};
     char *slab = ring.take();
-    const int other = w.half ? -4 : 4;  // warps to the other half's
-    reinterpret_cast<float *>(slab + GSLAB / 2)[w.lane] = top;
+    const int at = GSLAB / 2 + (n & 1) * 128, own = w.half * 2 + w.part;
+    reinterpret_cast<float *>(slab + at)[w.lane] = top;
     __syncwarp();
-    if (w.lane == 0) arrive_local(w.in + other * 2);
+#pragma unroll
+    for (int k = 1; k < 4; ++k)
+        if (w.lane == 0) arrive_local(w.in + ((own ^ k) - own) * 8);  // 4 warps on: 4 pairs of barriers
     if (!pair_wait(w.in, n & 1, g.err)) return false;
-    top = fmaxf(top, reinterpret_cast<const float *>(slab + GSLAB / 2 + other * (GSTAGING / 8))[w.lane]);
+#pragma unroll
+    for (int k = 1; k < 4; ++k)
+        top = fmaxf(top, reinterpret_cast<const float *>(slab + at + ((own ^ k) - own) * 4 * (GSTAGING / 16))[w.lane]);
     float up;
     const float sc = e4m3_scale(top, up), is = 1.f / (sc * up);
-    const int row = t.row0 + w.rank * 128 + w.q * 32, col = t.col0 + w.half * 64;
+    const int row = t.row0 + w.rank * 128 + w.q * 32, col = t.col0 + w.half * 64 + w.part * 32;
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
+    for (int k = 0; k < 2; ++k) {
         uint32_t v[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
@@ -525,10 +544,10 @@ __device__ __forceinline__ bool epi_gate_e4m3(const GemmArgs &g, const EpiWarp &
             for (int i = 0; i < 4; ++i) y[i] = x[16 * k + 4 * e + i] * up * is;
             v[e] = e4m3x4(y);
         }
-        *reinterpret_cast<uint4 *>(slab + w.lane * 64 + ((k ^ (w.lane >> 1 & 3)) << 4)) = make_uint4(v[0], v[1], v[2], v[3]);
+        *reinterpret_cast<uint4 *>(slab + w.lane * 32 + ((k ^ (w.lane >> 2 & 1)) << 4)) = make_uint4(v[0], v[1], v[2], v[3]);
     }
     ring.put(slab, &g.o[0], col, row, 0, row < g.M[0] && col < g.N[0]);
-    if (w.half == 0 && row + w.lane < g.M[0]) g.so[(size_t)(row + w.lane) * ((g.N[0] + 127) / 128) + t.col0 / 128] = sc;
+    if (own == 0 && row + w.lane < g.M[0]) g.so[(size_t)(row + w.lane) * ((g.N[0] + 127) / 128) + t.col0 / 128] = sc;
     return true;
 }
 
@@ -537,25 +556,26 @@ static_assert(sizeof(GemmBars) <= 512, "shared memory budget");
 template <int AMN, int BMN, int KIND, int EPI, typename E>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(gemm_threads<KIND>(), 1) gemm_kernel(const __grid_constant__ GemmArgs g) {
     constexpr bool E8 = KIND == kE4M3;
-    constexpr int EW = KIND == kDirect ? 4 : 8, E0 = KIND == kDirect ? 2 : 4, COLS = tile_cols(EPI), KB = E8 ? 128 : 64;
+    constexpr int ST = gemm_stages(KIND, EPI), STAGING = gemm_staging(KIND, EPI);
+    constexpr int EW = KIND == kDirect ? 4 : 16, E0 = KIND == kDirect ? 2 : 4, HALVES = gemm_halves(KIND), COLS = tile_cols(EPI), KB = E8 ? 128 : 64;
     extern __shared__ char raw[];
     char *sm = raw + ((1024 - (tc::smem_u32(raw) & 1023)) & 1023);
-    char *ops = sm, *staging = sm + GST * 2 * GOP;
-    GemmBars &bar = *reinterpret_cast<GemmBars *>(staging + GSTAGING);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, rank = (int)cluster_rank();
+    char *ops = sm, *staging = sm + ST * 2 * GOP;
+    GemmBars &bar = *reinterpret_cast<GemmBars *>(staging + STAGING);
+    const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31, rank = (int)cluster_rank();
     const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
     const int tiles = tiles_of(g, COLS), per_tile = g.segs * g.kblocks;
 
     if (threadIdx.x == 0) {
-        for (int s = 0; s < GST; ++s) {
+        for (int s = 0; s < ST; ++s) {
             tc::mbar_init(&bar.full[s], 1);
             tc::mbar_init(&bar.empty[s], 1);
         }
-        for (int s = 0; s < 2; ++s) {
-            tc::mbar_init(&bar.acc_full[s], 1);
-            tc::mbar_init(&bar.acc_empty[s], 2 * EW);
+        for (int s = 0; s < 4; ++s) {
+            tc::mbar_init(&bar.acc_full[s >> 1][s & 1], 1);
+            tc::mbar_init(&bar.acc_empty[s >> 1][s & 1], 2 * EW / HALVES);
         }
-        for (int s = 0; s < 16; ++s) tc::mbar_init(&bar.in[s >> 1][s & 1], 1);
+        for (int s = 0; s < 2 * EW; ++s) tc::mbar_init(&bar.in[s >> 1][s & 1], E8 && EPI == kGate ? 3 : 1);
         tc::fence_mbar_init();
     }
     if (warp == 1) {
@@ -570,12 +590,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(gemm_threads<KIND>()
     const uint32_t tmem = bar.tmem;
     dependent_wait();
 
-    // sums in registers: 168 of them a thread at launch (64512 in all), 64 for the first four warps leave
-    // 216 for the other eight (63488)
+    // sums in registers: 96 of them a thread at launch (61440 in all), 32 for the first four warps leave
+    // 112 for the other sixteen (61440)
     if (warp < E0) {
-        if (KIND != kDirect) asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
-        if (warp == 0 && tc::elect_one()) {
-            int it = 0;
+        if (KIND != kDirect) asm volatile("setmaxnreg.dec.sync.aligned.u32 32;");
+        // These two roles' loops are run by whole warps and their waits end in a vote: the compiler then keeps
+        // addresses and descriptors in uniform registers, where the one lane that issues wants them (moved there for
+        // each instruction they held the MMAs up: 8-bit gated projection XXX).
+        const bool one = tc::elect_one();
+        if (warp == 0) {
+            int st = 0, ph = 1, it = 0;
             bool ok = true;
             for (int t = pair; ok && t < tiles; t += pairs) {
                 const GemmTile tile = tile_of(g, t, COLS);
@@ -583,74 +607,85 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(gemm_threads<KIND>()
                 for (int s = 0; ok && s < g.segs; ++s) {
                     const GemmSeg sg = g.seg[s];
                     const CUtensorMap *ma = &g.a[tile.p + sg.a], *mb = &g.b[EPI == kGate ? sg.b + rank : tile.p + sg.b];
-                    for (int kb = 0; kb < g.kblocks; ++kb, ++it) {
-                        const int st = it % GST;
-                        if (!(ok = pair_wait(&bar.empty[st], (it / GST & 1) ^ 1, g.err))) break;
-                        if (rank == 0) tc::mbar_arrive_expect_tx(&bar.full[st], 4 * GOP);
-                        char *A = ops + st * 2 * GOP, *B = A + GOP;
-                        const uint32_t full = lead_addr(&bar.full[st]);
-                        if (AMN) {
-                            pair_load(A, ma, row, kb * 64, sg.ap, full);
-                            pair_load(A + GOP / 2, ma, row + 64, kb * 64, sg.ap, full);
-                        } else {
-                            pair_load(A, ma, kb * KB, row, sg.ap, full);
+                    for (int kb = 0; kb < g.kblocks; ++kb) {
+                        if (!(ok = warp_wait(&bar.empty[st], ph, g.err))) break;
+                        if (one) {
+                            if (rank == 0) tc::mbar_arrive_expect_tx(&bar.full[st], 4 * GOP);
+                            char *A = ops + st * 2 * GOP, *B = A + GOP;
+                            const uint32_t full = lead_addr(&bar.full[st]);
+                            if (AMN) {
+                                pair_load(A, ma, row, kb * 64, sg.ap, full);
+                                pair_load(A + GOP / 2, ma, row + 64, kb * 64, sg.ap, full);
+                            } else {
+                                pair_load(A, ma, kb * KB, row, sg.ap, full);
+                            }
+                            if (BMN) {
+                                pair_load(B, mb, col, kb * 64, sg.bp, full);
+                                pair_load(B + GOP / 2, mb, col + 64, kb * 64, sg.bp, full);
+                            } else {
+                                pair_load(B, mb, kb * KB, col, sg.bp, full);
+                            }
                         }
-                        if (BMN) {
-                            pair_load(B, mb, col, kb * 64, sg.bp, full);
-                            pair_load(B + GOP / 2, mb, col + 64, kb * 64, sg.bp, full);
-                        } else {
-                            pair_load(B, mb, kb * KB, col, sg.bp, full);
-                        }
+                        ++it;
+                        if (++st == ST) st = 0, ph ^= 1;
                     }
                 }
             }
             // this CTA's shared memory and barriers are in use until its last stages have been read
-            for (int k = it > GST ? it - GST : 0; k < it; ++k) {
+            for (int k = it > ST ? it - ST : 0; k < it; ++k) {
                 if (ok)
-                    ok = pair_wait(&bar.empty[k % GST], k / GST & 1, g.err);
+                    ok = warp_wait(&bar.empty[k % ST], k / ST & 1, g.err);
                 else if (rank == 0)
-                    pair_wait(&bar.full[k % GST], k / GST & 1, g.err);
+                    warp_wait(&bar.full[k % ST], k / ST & 1, g.err);
             }
         }
-        if (warp == 1 && rank == 0 && tc::elect_one()) {
-            constexpr uint32_t id = tc::idesc(256, 256, E8 ? 0 : 1, E8 ? 0 : 1, AMN, BMN);
-            int it = 0, ch = 0;
+        if (warp == 1 && rank == 0) {
+            constexpr uint32_t id = tc::idesc(256, 256 / HALVES, E8 ? 0 : 1, E8 ? 0 : 1, AMN, BMN);
+            int st = 0, ph = 0, ab = 0, aph = 1;
             bool ok = true;
             const uint32_t ops32 = tc::smem_u32(ops);
             for (int t = pair; ok && t < tiles; t += pairs) {
-                for (int k0 = 0; ok && k0 < per_tile; k0 += g.chunk, ++ch) {
-                    const int n = per_tile - k0 < g.chunk ? per_tile - k0 : g.chunk, ab = ch & 1;
-                    if (!(ok = pair_wait(&bar.acc_empty[ab], (ch >> 1 & 1) ^ 1, g.err))) break;
-                    tc::tc_fence_after();
-                    for (int j = 0; j < n; ++j, ++it) {
-                        const int st = it % GST;
-                        if (!(ok = pair_wait(&bar.full[st], it / GST & 1, g.err))) break;
-                        tc::tc_fence_after();
+                for (int k0 = 0; ok && k0 < per_tile; k0 += g.chunk) {
+                    const int n = per_tile - k0 < g.chunk ? per_tile - k0 : g.chunk;
+                    for (int j = 0; ok && j < n; ++j) {
+                        if (!(ok = warp_wait(&bar.full[st], ph, g.err))) break;
                         const uint32_t A = ops32 + st * 2 * GOP, B = A + GOP;
-                        tc::SmemDesc da = pair_desc(A, AMN ? GOP / 2 : 16), db = pair_desc(B, BMN ? GOP / 2 : 16);
+                        const tc::SmemDesc da = pair_desc(A, AMN ? GOP / 2 : 16);
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            tc::SmemDesc a = da, b = db;
-                            a.lo += k * (AMN ? 2048 : 32) >> 4;
-                            b.lo += k * (BMN ? 2048 : 32) >> 4;
-                            pair_mma<E8>(tmem + ab * 256, a, b, id, j > 0 || k > 0);
+                        for (int h = 0; h < HALVES; ++h) {
+                            if (j == 0 && !(ok = warp_wait(&bar.acc_empty[ab][h], aph, g.err))) break;
+                            tc::tc_fence_after();
+                            const tc::SmemDesc db = pair_desc(B + h * (GOP / 2), BMN ? GOP / 2 : 16);
+                            if (one) {
+#pragma unroll
+                                for (int k = 0; k < 4; ++k) {
+                                    tc::SmemDesc a = da, b = db;
+                                    a.lo += k * (AMN ? 2048 : 32) >> 4;
+                                    b.lo += k * (BMN ? 2048 : 32) >> 4;
+                                    pair_mma<E8>(tmem + ab * 256 + h * 128, a, b, id, j > 0 || k > 0);
+                                }
+                                if (h == HALVES - 1) pair_commit(&bar.empty[st]);
+                                if (j == n - 1) pair_commit(&bar.acc_full[ab][h]);
+                            }
                         }
-                        pair_commit(&bar.empty[st]);
+                        if (++st == ST) st = 0, ph ^= 1;
                     }
-                    if (ok) pair_commit(&bar.acc_full[ab]);
+                    ab ^= 1;
+                    aph ^= ab == 0;
                 }
             }
         }
         __syncwarp();
     } else {
-        if (KIND != kDirect) asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
+        if (KIND != kDirect) asm volatile("setmaxnreg.inc.sync.aligned.u32 112;");
         EpiWarp w;
         const int ew = warp - E0;
         w.lane = lane;
         w.q = warp & 3;
-        w.half = ew >> 2;
+        w.half = ew >> 3;
+        w.part = ew >> 2 & 1;
         w.rank = rank;
-        w.staging = staging + ew * (GSTAGING / EW);
+        w.staging = staging + ew * (STAGING / EW);
         w.in = bar.in[ew];
         w.tmem = tmem + ((uint32_t)(w.q * 32) << 16);
         int ch = 0;
@@ -662,9 +697,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(gemm_threads<KIND>()
             for (int t = pair; ok && t < tiles; t += pairs, ++ch) {
                 const GemmTile tile = tile_of(g, t, COLS);
                 const int ab = ch & 1;
-                if (!(ok = pair_wait(&bar.acc_full[ab], ch >> 1 & 1, g.err))) break;
+                if (!(ok = pair_wait(&bar.acc_full[ab][0], ch >> 1 & 1, g.err))) break;
                 tc::tc_fence_after();
-                const uint32_t acc = w.tmem + ab * 256, release = lead_addr(&bar.acc_empty[ab]);
+                const uint32_t acc = w.tmem + ab * 256, release = lead_addr(&bar.acc_empty[ab][0]);
                 if constexpr (EPI == kPlain) epi_plain(g, w, ring, tile, acc, release);
                 if constexpr (EPI == kGate) epi_gate(g, w, ring, tile, acc, release);
                 if constexpr (EPI == kGateBwd) {
@@ -674,17 +709,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(gemm_threads<KIND>()
                 }
             }
         } else {
-            Ring<2> ring = {w.staging, lane, 0};
             int uses = 0;
             for (int t = pair; ok && t < tiles; t += pairs) {
                 const GemmTile tile = tile_of(g, t, COLS);
-                float x[128];
+                float x[64];
 #pragma unroll
-                for (int e = 0; e < 128; ++e) x[e] = 0.f;
-                const int row = tile.row0 + rank * 128 + w.q * 32 + lane;
+                for (int e = 0; e < 64; ++e) x[e] = 0.f;
                 const float *sa = nullptr, *sb0 = nullptr, *sb1 = nullptr;
                 if constexpr (E8) {
-                    const int blk = tile.col0 / 128 + (EPI == kGate ? 0 : w.half);
+                    const int row = tile.row0 + rank * 128 + w.q * 32 + lane;
+                    const int blk = tile.col0 / 128 + (EPI == kGate ? 0 : w.part);
                     if (row < g.M[tile.p]) sa = g.sa + (size_t)row * g.kblocks;
                     if (blk * 128 < g.N[tile.p]) {
                         sb0 = g.sb[0] + (size_t)blk * g.kblocks;
@@ -703,32 +737,32 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(gemm_threads<KIND>()
                     const int ab = ch & 1;
                     const float m0 = E8 ? na * n0 : 1.f, m1 = E8 && EPI == kGate ? na * n1 : m0;
                     if (E8 && i + 1 < g.kblocks) scales(i + 1);
-                    if (!(ok = pair_wait(&bar.acc_full[ab], ch >> 1 & 1, g.err))) break;
+                    if (!(ok = pair_wait(&bar.acc_full[ab][HALVES == 1 ? 0 : w.half], ch >> 1 & 1, g.err))) break;
                     tc::tc_fence_after();
-                    const uint32_t acc = w.tmem + ab * 256;
-                    uint32_t r[2][32];
-                    tmem_ld32(acc + sum_col<KIND, EPI>(w.half, 0), r[0]);
+                    const uint32_t acc = w.tmem + ab * 256 + (HALVES == 1 ? 0 : w.half * 128);
+                    uint32_t r[2][16];
+                    tmem_ld16(acc + sum_col<KIND, EPI>(w, 0), r[0]);
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) {  // the next 32 columns come while these are added
+                    for (int c = 0; c < 4; ++c) {  // the next 16 columns come while these are added
                         tc::tmem_wait_ld();
                         tmem_use(r[c & 1]);
                         if (c < 3) {
-                            tmem_ld32(acc + sum_col<KIND, EPI>(w.half, c + 1), r[(c + 1) & 1]);
+                            tmem_ld16(acc + sum_col<KIND, EPI>(w, c + 1), r[(c + 1) & 1]);
                         } else {
                             tc::tc_fence_before();
                             __syncwarp();
-                            if (lane == 0) arrive_remote(lead_addr(&bar.acc_empty[ab]));
+                            if (lane == 0) arrive_remote(lead_addr(&bar.acc_empty[ab][HALVES == 1 ? 0 : w.half]));
                         }
                         const float m = EPI == kGate && c >= 2 ? m1 : m0;
 #pragma unroll
-                        for (int e = 0; e < 32; e += 2) add_scaled(x[c * 32 + e], x[c * 32 + e + 1], r[c & 1][e], r[c & 1][e + 1], m);
+                        for (int e = 0; e < 16; e += 2) add_scaled(x[c * 16 + e], x[c * 16 + e + 1], r[c & 1][e], r[c & 1][e + 1], m);
                     }
                 }
                 if (!ok) break;
                 if constexpr (E8 && EPI == kGate)
-                    ok = epi_gate_e4m3(g, w, ring, tile, x, uses++);
+                    ok = epi_gate_e4m3(g, w, tile, x, uses++);
                 else
-                    ok = epi_sums<EPI, E>(g, w, ring, tile, x, uses);
+                    ok = epi_sums<EPI, E>(g, w, tile, x, uses);
             }
         }
         if (lane == 0) bulk_wait_read<0>();  // staging is read until then
@@ -754,14 +788,14 @@ ida_status gemm_map(CUtensorMap *m, const void *p, int type, long long inner, lo
 template <int AMN, int BMN, int KIND, int EPI, typename E>
 ida_status gemm_launch(GemmArgs &g, int num_sms, cudaStream_t st) {
     const auto kernel = gemm_kernel<AMN, BMN, KIND, EPI, E>;
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, GSMEM);
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, gemm_smem(KIND, EPI));
     if (e != cudaSuccess) return fail_with(IDA_ERR_CUDA, cudaGetErrorString(e));
     long long tiles = 0;
     constexpr int cols = tile_cols(EPI);
     for (int p = 0; p < g.problems; ++p) tiles += ((long long)g.M[p] + 255) / 256 * (((long long)g.N[p] + cols - 1) / cols);
     if (KIND == kDirect) g.chunk = g.segs * g.kblocks;
     const long long pairs = tiles < num_sms / 2 ? tiles : num_sms / 2;
-    e = launch_dependent(kernel, dim3((unsigned)(2 * pairs)), dim3(gemm_threads<KIND>()), GSMEM, st, g);
+    e = launch_dependent(kernel, dim3((unsigned)(2 * pairs)), dim3(gemm_threads<KIND>()), gemm_smem(KIND, EPI), st, g);
     if (e != cudaSuccess) return fail_with(IDA_ERR_CUDA, std::string("matrix product launch: ") + cudaGetErrorString(e));
     return launched("matrix product");
 }
