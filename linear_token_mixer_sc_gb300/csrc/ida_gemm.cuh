@@ -39,9 +39,24 @@ struct GemmSeg {
     unsigned char a, ap, b, bp;  // maps and parts of one pass over the contraction
 };
 
+// n / d for n < 2^31 without a division (every warp places its own tiles, and divisions took 1100 .. 1700
+// clocks a tile, a tenth of a tile's time in 8 bits): with 2^s >= d and m = 2^32 (2^s - d) / d + 1 rounded
+// down,  n / d = (m n / 2^32 + n) / 2^s.
+struct Divisor {
+    unsigned m, s, d;
+};
+inline Divisor divisor(unsigned d) {
+    unsigned s = 0;
+    while ((1ull << s) < d) ++s;
+    return {(unsigned)(((1ull << 32) * ((1ull << s) - d)) / d + 1), s, d};
+}
+__device__ __forceinline__ int divide(int n, const Divisor &d) { return (int)((__umulhi(d.m, (unsigned)n) + (unsigned)n) >> d.s); }
+
 struct GemmArgs {
     CUtensorMap a[3], b[3], o[3], e[2];  // operands, outputs, what the epilogue reads
     int M[3], N[3];                      // rows and columns of each problem's output
+    int tiles, bands[3], count[3];       // of the launch; whole bands of 8 rows of tiles, and tiles, of each problem
+    Divisor band[3], last[3];            // tiles of such a band, rows of tiles of the last one (1 if there is none)
     int problems, segs, kblocks, chunk;  // kblocks: blocks of 128 bytes along each segment's contraction
     GemmSeg seg[12];
     int keep;                            // kGate: store the two factors as well
@@ -194,22 +209,31 @@ constexpr int tile_cols(int epi) { return epi == kGate ? 128 : 256; }
 __device__ __forceinline__ GemmTile tile_of(const GemmArgs &g, int t, int cols) {
     GemmTile r;
     r.p = 0;
-    int tm = (g.M[0] + 255) / 256, tn = (g.N[0] + cols - 1) / cols;
-    while (t >= tm * tn && r.p + 1 < g.problems) {
-        t -= tm * tn;
-        ++r.p;
-        tm = (g.M[r.p] + 255) / 256;
-        tn = (g.N[r.p] + cols - 1) / cols;
+    while (r.p + 1 < g.problems && t >= g.count[r.p]) t -= g.count[r.p++];
+    const int band = divide(t, g.band[r.p]), in = t - band * (int)g.band[r.p].d;
+    int col, row;
+    if (band < g.bands[r.p]) {
+        col = in >> 3;
+        row = in & 7;
+    } else {
+        col = divide(in, g.last[r.p]);
+        row = in - col * (int)g.last[r.p].d;
     }
-    const int band = t / (8 * tn), in = t - band * 8 * tn;
-    const int rows = tm - band * 8 < 8 ? tm - band * 8 : 8;
-    r.row0 = (band * 8 + in % rows) * 256;
-    r.col0 = in / rows * cols;
+    r.row0 = (band * 8 + row) * 256;
+    r.col0 = col * cols;
     return r;
 }
-__device__ __forceinline__ int tiles_of(const GemmArgs &g, int cols) {
-    int n = 0;
-    for (int p = 0; p < g.problems; ++p) n += (g.M[p] + 255) / 256 * ((g.N[p] + cols - 1) / cols);
+// ... and the sizes that it goes by
+inline long long place_tiles(GemmArgs &g, int cols) {
+    long long n = 0;
+    for (int p = 0; p < g.problems; ++p) {
+        const int tm = (int)(((long long)g.M[p] + 255) / 256), tn = (g.N[p] + cols - 1) / cols;
+        g.bands[p] = tm / 8;
+        g.count[p] = tm * tn;
+        g.band[p] = divisor((unsigned)(8 * tn));
+        g.last[p] = divisor((unsigned)(tm % 8 ? tm % 8 : 1));
+        n += (long long)tm * tn;
+    }
     return n;
 }
 
@@ -564,7 +588,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(gemm_threads<KIND>()
     GemmBars &bar = *reinterpret_cast<GemmBars *>(staging + STAGING);
     const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31, rank = (int)cluster_rank();
     const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
-    const int tiles = tiles_of(g, COLS), per_tile = g.segs * g.kblocks;
+    const int tiles = g.tiles, per_tile = g.segs * g.kblocks;
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < ST; ++s) {
@@ -710,29 +734,32 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(gemm_threads<KIND>()
             }
         } else {
             int uses = 0;
-            for (int t = pair; ok && t < tiles; t += pairs) {
-                const GemmTile tile = tile_of(g, t, COLS);
-                float x[64];
-#pragma unroll
-                for (int e = 0; e < 64; ++e) x[e] = 0.f;
-                const float *sa = nullptr, *sb0 = nullptr, *sb1 = nullptr;
+            GemmTile tile;
+            // the scales are read a block ahead, a tile's first ones before the epilogue of the one before it
+            const float *sa = nullptr, *sb0 = nullptr, *sb1 = nullptr;
+            float na = 0.f, n0 = 0.f, n1 = 0.f;
+            auto scales = [&](int i) {
+                na = sa ? __ldg(sa + i) : 0.f;
+                n0 = sb0 ? __ldg(sb0 + i) : 0.f;
+                if (EPI == kGate) n1 = sb1 ? __ldg(sb1 + i) : 0.f;
+            };
+            auto open = [&](int t) {
+                tile = tile_of(g, t, COLS);
                 if constexpr (E8) {
                     const int row = tile.row0 + rank * 128 + w.q * 32 + lane;
                     const int blk = tile.col0 / 128 + (EPI == kGate ? 0 : w.part);
-                    if (row < g.M[tile.p]) sa = g.sa + (size_t)row * g.kblocks;
-                    if (blk * 128 < g.N[tile.p]) {
-                        sb0 = g.sb[0] + (size_t)blk * g.kblocks;
-                        if (EPI == kGate) sb1 = g.sb[1] + (size_t)blk * g.kblocks;
-                    }
+                    sa = row < g.M[tile.p] ? g.sa + (size_t)row * g.kblocks : nullptr;
+                    const bool in = blk * 128 < g.N[tile.p];
+                    sb0 = in ? g.sb[0] + (size_t)blk * g.kblocks : nullptr;
+                    if (EPI == kGate) sb1 = in ? g.sb[1] + (size_t)blk * g.kblocks : nullptr;
+                    scales(0);
                 }
-                // the scales are read a block ahead
-                float na = 0.f, n0 = 0.f, n1 = 0.f;
-                auto scales = [&](int i) {
-                    na = sa ? __ldg(sa + i) : 0.f;
-                    n0 = sb0 ? __ldg(sb0 + i) : 0.f;
-                    if (EPI == kGate) n1 = sb1 ? __ldg(sb1 + i) : 0.f;
-                };
-                if constexpr (E8) scales(0);
+            };
+            if (pair < tiles) open(pair);
+            for (int t = pair; ok && t < tiles; t += pairs) {
+                float x[64];
+#pragma unroll
+                for (int e = 0; e < 64; ++e) x[e] = 0.f;
                 for (int k0 = 0, i = 0; k0 < per_tile; k0 += g.chunk, ++ch, ++i) {
                     const int ab = ch & 1;
                     const float m0 = E8 ? na * n0 : 1.f, m1 = E8 && EPI == kGate ? na * n1 : m0;
@@ -759,10 +786,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(gemm_threads<KIND>()
                     }
                 }
                 if (!ok) break;
+                const GemmTile done = tile;
+                if (t + pairs < tiles) open(t + pairs);
                 if constexpr (E8 && EPI == kGate)
-                    ok = epi_gate_e4m3(g, w, tile, x, uses++);
+                    ok = epi_gate_e4m3(g, w, done, x, uses++);
                 else
-                    ok = epi_sums<EPI, E>(g, w, tile, x, uses);
+                    ok = epi_sums<EPI, E>(g, w, done, x, uses);
             }
         }
         if (lane == 0) bulk_wait_read<0>();  // staging is read until then
@@ -790,9 +819,9 @@ ida_status gemm_launch(GemmArgs &g, int num_sms, cudaStream_t st) {
     const auto kernel = gemm_kernel<AMN, BMN, KIND, EPI, E>;
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, gemm_smem(KIND, EPI));
     if (e != cudaSuccess) return fail_with(IDA_ERR_CUDA, cudaGetErrorString(e));
-    long long tiles = 0;
-    constexpr int cols = tile_cols(EPI);
-    for (int p = 0; p < g.problems; ++p) tiles += ((long long)g.M[p] + 255) / 256 * (((long long)g.N[p] + cols - 1) / cols);
+    const long long tiles = place_tiles(g, tile_cols(EPI));
+    if (tiles > 0x7FFFFFFFLL) return fail_with(IDA_ERR_UNSUPPORTED, "too many tiles");
+    g.tiles = (int)tiles;
     if (KIND == kDirect) g.chunk = g.segs * g.kblocks;
     const long long pairs = tiles < num_sms / 2 ? tiles : num_sms / 2;
     e = launch_dependent(kernel, dim3((unsigned)(2 * pairs)), dim3(gemm_threads<KIND>()), gemm_smem(KIND, EPI), st, g);
