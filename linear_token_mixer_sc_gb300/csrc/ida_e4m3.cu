@@ -24,106 +24,127 @@ struct QuantArgs {
     float *scale;
     long long ldx;
     int rows, K;
+    Divisor blocks;  // of 128 channels in a row (rows times blocks < 2^30)
 };
 
-// x / sc rounded to e4m3; for scales whose reciprocal overflows both are scaled up first (exactly)
-template <int N>
-__device__ __forceinline__ void quantise(float (&x)[N], float sc, uint32_t (&q)[N / 4]) {
-    float up = 1.f;
-    if (sc < 0x1p-100f) up = 0x1p64f;
-    const float div = sc * up;
-#pragma unroll
-    for (int e = 0; e < N; ++e) x[e] = x[e] * up / div;
-#pragma unroll
-    for (int e = 0; e < N; e += 4) q[e / 4] = e4m3x4(x + e);
-}
+// Quotients by a scale, rounded as a division rounds them, from its reciprocal: with r = 1 / d to the nearest
+// and q within a unit of x / d, q + r (x - d q) in fused steps is x / d to the nearest (Markstein 1990), where
+// no step underflows.  Quotients below 2^-10 are 0 in e4m3, so a scale of 2^-80 and more leaves the residual's
+// bits above 2^-138; smaller ones are multiplied by 2^120 first, and the values with them, exactly.  (Divisions
+// were 10 instructions a value: 4099 rows of 5632 channels took 21 us, now XXX.)
+struct Quotient {
+    float up, d, r;
+    __device__ __forceinline__ explicit Quotient(float sc) {
+        up = sc < 0x1p-80f ? 0x1p120f : 1.f;
+        d = sc * up;
+        r = 1.f / d;
+    }
+    __device__ __forceinline__ float operator()(float x) const {
+        x *= up;
+        const float q = x * r;
+        return fmaf(fmaf(-d, q, x), r, q);
+    }
+};
 __device__ __forceinline__ float quant_scale(float top) {
-    float sc = top > 0.f ? top / 448.f : 1.f;
+    const float sc = top > 0.f ? top / 448.f : 1.f;
     return sc < 0x1p-126f ? __fdiv_ru(top, 448.f) : sc;
 }
 
-// A scale for 128 channels of a row: 16 threads of 8 channels each.
+// 8 channels of a row, as they lie in memory
+template <typename E>
+struct Eight {
+    uint4 v[8 / Vec16<E>::n];
+    __device__ __forceinline__ void load(const E *p, bool live) {
+#pragma unroll
+        for (int i = 0; i < 8 / Vec16<E>::n; ++i) v[i] = live ? __ldcs(reinterpret_cast<const uint4 *>(p) + i) : make_uint4(0, 0, 0, 0);
+    }
+    __device__ __forceinline__ void unpack(float (&x)[8]) const {
+#pragma unroll
+        for (int i = 0; i < 8 / Vec16<E>::n; ++i) Vec16<E>::unpack(v[i], x + i * Vec16<E>::n);
+    }
+    __device__ __forceinline__ float top() const {
+        float x[8], m = 0.f;
+        unpack(x);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) m = fmaxf(m, fabsf(x[e]));
+        return m;
+    }
+    __device__ __forceinline__ uint2 quantised(const Quotient &by) const {
+        float x[8];
+        unpack(x);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] = by(x[e]);
+        return make_uint2(e4m3x4(x), e4m3x4(x + 4));
+    }
+};
+
+// A scale for 128 channels of a row: 16 threads of 8 channels each, four such groups a thread.
+constexpr int QU = 4;
 template <typename E>
 __global__ void __launch_bounds__(256) quant_rows_kernel(QuantArgs a) {
     dependent_launch();
     dependent_wait();
-    const int kb = (a.K + 127) / 128, sub = threadIdx.x & 15;
-    const long long units = (long long)a.rows * kb;
-    // the same number of passes for all threads of a warp: its shuffles are for full warps
-    for (long long base = (long long)blockIdx.x * 16; base < units; base += (long long)gridDim.x * 16) {
-        const long long u = base + (threadIdx.x >> 4);
-        const bool live = u < units;
-        const long long r = live ? u / kb : 0;
-        const int b = live ? (int)(u - r * kb) : 0, c = b * 128 + sub * 8;
-        float x[8] = {};
-        if (live && c < a.K) {
-            const E *src = static_cast<const E *>(a.x) + r * a.ldx + c;
-            Vec16<E>::unpack(__ldcs(reinterpret_cast<const uint4 *>(src)), x);
-            if (Vec16<E>::n == 4) Vec16<E>::unpack(__ldcs(reinterpret_cast<const uint4 *>(src) + 1), x + 8 - Vec16<E>::n);
-        }
-        float top = 0.f;
+    const int sub = threadIdx.x & 15, kb = (int)a.blocks.d;
+    const int units = a.rows * kb, u0 = blockIdx.x * (16 * QU) + (threadIdx.x >> 4);
+    Eight<E> x[QU];
+    long long at[QU];
+    bool live[QU];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(x[e]));
+    for (int i = 0; i < QU; ++i) {
+        const int u = u0 + 16 * i, r = divide(u < units ? u : 0, a.blocks), c = (u - r * kb) * 128 + sub * 8;
+        live[i] = u < units && c < a.K;
+        at[i] = (long long)r * a.K + c;
+        x[i].load(static_cast<const E *>(a.x) + (long long)r * a.ldx + c, live[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < QU; ++i) {
+        float top = x[i].top();
 #pragma unroll
         for (int o = 8; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
         const float sc = quant_scale(top);
-        uint32_t q[2];
-        quantise(x, sc, q);
-        if (live && c < a.K) __stcs(reinterpret_cast<uint2 *>(a.q + r * a.K + c), make_uint2(q[0], q[1]));
-        if (live && sub == 0) a.scale[u] = sc;
+        const uint2 q = x[i].quantised(Quotient(sc));
+        if (live[i]) __stcs(reinterpret_cast<uint2 *>(a.q + at[i]), q);
+        if (sub == 0 && u0 + 16 * i < units) a.scale[u0 + 16 * i] = sc;
     }
 }
 
-// A scale for a block of 128 x 128, a CTA for each: 16 threads of 8 channels by 16 rows, 8 passes.
+// A scale for a block of 128 x 128, a CTA for each: 16 threads of 8 channels by 32 rows, 4 passes.
 template <typename E>
-__global__ void __launch_bounds__(256) quant_blocks_kernel(QuantArgs a) {
-    __shared__ float red[8];
+__global__ void __launch_bounds__(512) quant_blocks_kernel(QuantArgs a) {
+    __shared__ float red[16];
     dependent_launch();
     dependent_wait();
-    const int kb = (a.K + 127) / 128, b = blockIdx.x % kb, c = b * 128 + (threadIdx.x & 15) * 8;
-    const long long r0 = (long long)(blockIdx.x / kb) * 128 + (threadIdx.x >> 4);
-    float x[8][8];
+    const int rb = divide(blockIdx.x, a.blocks), c = (blockIdx.x - rb * (int)a.blocks.d) * 128 + (threadIdx.x & 15) * 8;
+    const long long r0 = (long long)rb * 128 + (threadIdx.x >> 4);
+    Eight<E> x[4];
     float top = 0.f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const long long r = r0 + 16 * i;
-        const bool live = r < a.rows && c < a.K;
+    for (int i = 0; i < 4; ++i) x[i].load(static_cast<const E *>(a.x) + (r0 + 32 * i) * a.ldx + c, r0 + 32 * i < a.rows && c < a.K);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) x[i][e] = 0.f;
-        if (live) {
-            const E *src = static_cast<const E *>(a.x) + r * a.ldx + c;
-            Vec16<E>::unpack(__ldcs(reinterpret_cast<const uint4 *>(src)), x[i]);
-            if (Vec16<E>::n == 4) Vec16<E>::unpack(__ldcs(reinterpret_cast<const uint4 *>(src) + 1), x[i] + 8 - Vec16<E>::n);
-        }
-    }
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-#pragma unroll
-        for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(x[i][e]));
+    for (int i = 0; i < 4; ++i) top = fmaxf(top, x[i].top());
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
     if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = top;
     __syncthreads();
 #pragma unroll
-    for (int i = 0; i < 8; ++i) top = fmaxf(top, red[i]);
+    for (int i = 0; i < 16; ++i) top = fmaxf(top, red[i]);
     const float sc = quant_scale(top);
+    const Quotient by(sc);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const long long r = r0 + 16 * i;
-        uint32_t q[2];
-        quantise(x[i], sc, q);
-        if (r < a.rows && c < a.K) *reinterpret_cast<uint2 *>(a.q + r * a.K + c) = make_uint2(q[0], q[1]);
+    for (int i = 0; i < 4; ++i) {
+        const long long r = r0 + 32 * i;
+        const uint2 q = x[i].quantised(by);
+        if (r < a.rows && c < a.K) *reinterpret_cast<uint2 *>(a.q + r * a.K + c) = q;
     }
     if (threadIdx.x == 0) a.scale[blockIdx.x] = sc;
 }
 
 template <typename E>
-static cudaError_t launch_quant(const QuantArgs &a, int block_rows, int num_sms, cudaStream_t st) {
-    const long long kb = (a.K + 127) / 128;
+static cudaError_t launch_quant(const QuantArgs &a, int block_rows, cudaStream_t st) {
+    const long long kb = a.blocks.d;
     if (block_rows == 128)
-        return launch_dependent(quant_blocks_kernel<E>, dim3((unsigned)(((long long)a.rows + 127) / 128 * kb)), dim3(256), 0, st, a);
-    const long long want = (a.rows * kb + 15) / 16, cap = (long long)num_sms * 32;
-    return launch_dependent(quant_rows_kernel<E>, dim3((unsigned)(want < cap ? want : cap)), dim3(256), 0, st, a);
+        return launch_dependent(quant_blocks_kernel<E>, dim3((unsigned)(((long long)a.rows + 127) / 128 * kb)), dim3(512), 0, st, a);
+    return launch_dependent(quant_rows_kernel<E>, dim3((unsigned)((a.rows * kb + 16 * QU - 1) / (16 * QU))), dim3(256), 0, st, a);
 }
 
 // Sizes of a product: `rows` by N, contracted over K.
@@ -176,9 +197,9 @@ ida_status ida_quant_e4m3(const void *x, void *q, float *scale, int rows, int K,
     std::string why;
     s = device_ready(&num_sms, why);
     if (s != IDA_OK) return fail_with(s, why);
-    const QuantArgs a = {x, static_cast<uint8_t *>(q), scale, ldx, rows, K};
+    const QuantArgs a = {x, static_cast<uint8_t *>(q), scale, ldx, rows, K, divisor((unsigned)blocks_of(K))};
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-    const cudaError_t e = dtype == IDA_F32 ? launch_quant<float>(a, block_rows, num_sms, st) : launch_quant<__nv_bfloat16>(a, block_rows, num_sms, st);
+    const cudaError_t e = dtype == IDA_F32 ? launch_quant<float>(a, block_rows, st) : launch_quant<__nv_bfloat16>(a, block_rows, st);
     if (e != cudaSuccess) return fail_with(IDA_ERR_CUDA, std::string("quantiser launch: ") + cudaGetErrorString(e));
     return launched("quantiser");
 }
