@@ -14,6 +14,7 @@
 // to 2^-16 make up fp32's; h, dg and du are rounded to bf16 between the products otherwise.
 #include <mutex>
 
+#include "ida_ffn_simt.cuh"
 #include "ida_gemm.cuh"
 #include "ida_skinny.cuh"
 
@@ -173,6 +174,11 @@ static ida_status run_gemm(int a_mn, int b_mn, int epi, GemmArgs &g, int dtype, 
     return dtype == IDA_BF16 ? gemm_bf16(a_mn, b_mn, epi, g, num_sms, st) : gemm_f32(a_mn, b_mn, epi, g, num_sms, st);
 }
 
+// fp32 products on the CUDA cores: few rows, or little arithmetic.  Forward and backward, in us, there and on the tensor cores: 251 rows of
+// 64 and 176 channels 6 + 13 and 19 + 40, 512 of 256 and 512 22 + 53 and 34 + 73, 1024 of 256 and 704 (2^27.5) 40 + 92 and 40 + 98,
+// 1024 of 512 and 1024 104 + 209 and 56 + 125.
+static bool on_cuda_cores(long long rows, long long D, long long F) { return rows <= kFewRows || rows * D * F <= (1LL << 27); }
+
 static ida_status check_ffn(int rows, int D, int F, long long ldx, int dtype) {
     if (rows < 0) return fail_with(IDA_ERR_ARG, "rows must be >= 0");
     if (D < 1 || F < 1) return fail_with(IDA_ERR_ARG, "D and F must be >= 1");
@@ -235,6 +241,15 @@ ida_status ida_ffn(const void *x, const void *w_gate, const void *w_up, const vo
         if (s != IDA_OK) return s;
         SkinnyArgs b = {h, F, w_down, nullptr, out, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr, rows, F, D, false, true};
         return skinny_product(b, false, num_sms, st);
+    }
+    if (dtype == IDA_F32 && on_cuda_cores(rows, D, F)) {
+        float *fh = static_cast<float *>(h), *fa = reinterpret_cast<float *>(ac);
+        SimtArgs a = {{static_cast<const float *>(x)}, {static_cast<const float *>(w_gate), static_cast<const float *>(w_up)}, {ldx}, {D},
+                      {fh, fa, fa ? fa + tf : nullptr}, nullptr, nullptr, {rows}, {F}, D, 1, 1};
+        s = ffn_simt(0, 0, kGate, a, st);
+        if (s != IDA_OK) return s;
+        SimtArgs b = {{fh}, {static_cast<const float *>(w_down)}, {F}, {F}, {static_cast<float *>(out)}, nullptr, nullptr, {rows}, {D}, F, 1, 1};
+        return ffn_simt(0, 0, kPlain, b, st);
     }
     const int parts = dtype == IDA_BF16 ? 1 : 3;
     Operand X = {x, parts, rows, D, ldx}, Wg = {w_gate, parts, F, D, D}, Wu = {w_up, parts, F, D, D}, Wd = {w_down, parts, D, F, F},
@@ -323,6 +338,21 @@ ida_status ida_ffn_backward(const void *x, const void *w_gate, const void *w_up,
     char *ws = static_cast<char *>(workspace);
     const char *ac = static_cast<const char *>(acts);
     char *dg = ws + sp.dgu, *du = dg + tf * es;
+    if (dtype == IDA_F32 && on_cuda_cores(rows, D, F)) {
+        const float *fx = static_cast<const float *>(x), *fy = static_cast<const float *>(dout), *fa = reinterpret_cast<const float *>(ac);
+        float *fg = reinterpret_cast<float *>(dg), *fu = reinterpret_cast<float *>(du);
+        SimtArgs a = {{fy}, {static_cast<const float *>(w_down)}, {D}, {F}, {fg, fu}, fa, fa + tf, {rows}, {F}, D, 1, 1};
+        s = ffn_simt(0, 1, kGateBwd, a, st);
+        if (s != IDA_OK) return s;
+        SimtArgs b = {{fg, fu, fy}, {fx, fx, fa + 2 * tf}, {F, F, D}, {ldx, ldx, F},
+                      {static_cast<float *>(dw_gate), static_cast<float *>(dw_up), static_cast<float *>(dw_down)}, nullptr, nullptr,
+                      {F, F, D}, {D, D, F}, rows, 3, 1};
+        s = ffn_simt(1, 1, kPlain, b, st);
+        if (s != IDA_OK) return s;
+        SimtArgs c = {{fg, fu}, {static_cast<const float *>(w_gate), static_cast<const float *>(w_up)}, {F, F}, {D, D},
+                      {static_cast<float *>(dx)}, nullptr, nullptr, {rows}, {D}, F, 1, 2};
+        return ffn_simt(0, 1, kPlain, c, st);
+    }
     const int parts = dtype == IDA_BF16 ? 1 : 3;
     Operand X = {x, parts, rows, D, ldx}, Wg = {w_gate, parts, F, D, D}, Wu = {w_up, parts, F, D, D}, Wd = {w_down, parts, D, F, F},
             H = {ac + 2 * tf * es, parts, rows, F, F}, dY = {dout, parts, rows, D, D}, dG = {dg, parts, rows, F, F},
