@@ -49,7 +49,9 @@ ida_status gemm_map(CUtensorMap *m, const void *p, int type, long long inner, lo
     const CUresult r = fn(m, type == kMapBf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : type == kMapF32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
                                                                                                   : CU_TENSOR_MAP_DATA_TYPE_UINT8,
                           3, const_cast<void *>(p), dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                          box0 * es == 32 ? CU_TENSOR_MAP_SWIZZLE_32B : CU_TENSOR_MAP_SWIZZLE_128B,
+                          box0 * es == 32   ? CU_TENSOR_MAP_SWIZZLE_32B
+                          : box0 * es == 64 ? CU_TENSOR_MAP_SWIZZLE_64B
+                                            : CU_TENSOR_MAP_SWIZZLE_128B,
                           CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS ? IDA_OK : fail_with(IDA_ERR_CUDA, "cuTensorMapEncodeTiled failed");
 }
@@ -152,8 +154,8 @@ static FfnSpace ffn_space(long long T, int D, int F, int dtype, bool backward) {
 static ida_status operand_map(CUtensorMap *m, const Operand &o, int mn) {
     return gemm_map(m, o.p, kMapBf16, o.cols, o.rows, o.parts, o.ld, 64, mn ? 64 : 128);
 }
-static ida_status out_map(CUtensorMap *m, const void *p, int dtype, long long rows, long long cols) {
-    return gemm_map(m, p, dtype == IDA_BF16 ? kMapBf16 : kMapF32, cols, rows, 1, cols, dtype == IDA_BF16 ? 64 : 32, 32);
+static ida_status out_map(CUtensorMap *m, const void *p, int dtype, long long rows, long long cols, int box = 0) {
+    return gemm_map(m, p, dtype == IDA_BF16 ? kMapBf16 : kMapF32, cols, rows, 1, cols, box ? box : dtype == IDA_BF16 ? 64 : 32, 32);
 }
 
 // Passes over the contraction for operands a and b: one in bf16, the six products of parts otherwise, the
@@ -381,10 +383,10 @@ ida_status ida_ffn_backward(const void *x, const void *w_gate, const void *w_up,
     add_segments(g, dtype, 0, 0);
     s = operand_map(&g.a[0], dY, 0);
     if (s == IDA_OK) s = operand_map(&g.b[0], Wd, 1);
-    if (s == IDA_OK) s = out_map(&g.e[0], ac, dtype, rows, F);
-    if (s == IDA_OK) s = out_map(&g.e[1], ac + tf * es, dtype, rows, F);
-    if (s == IDA_OK) s = out_map(&g.o[0], dg, dtype, rows, F);
-    if (s == IDA_OK) s = out_map(&g.o[1], du, dtype, rows, F);
+    if (s == IDA_OK) s = out_map(&g.e[0], ac, dtype, rows, F, 32);
+    if (s == IDA_OK) s = out_map(&g.e[1], ac + tf * es, dtype, rows, F, 32);
+    if (s == IDA_OK) s = out_map(&g.o[0], dg, dtype, rows, F, 32);
+    if (s == IDA_OK) s = out_map(&g.o[1], du, dtype, rows, F, 32);
     if (s == IDA_OK) s = run_gemm(0, 1, kGateBwd, g, dtype, num_sms, st);
     if (s != IDA_OK) return s;
     if (dtype == IDA_F32) {

@@ -270,8 +270,10 @@ __device__ __forceinline__ void stage(char *slab, int row, int piece, const floa
 
 // ---- the kernel ------------------------------------------------------------------------------
 
-template <int KIND>
-constexpr int gemm_threads() { return KIND == kDirect ? 192 : 640; }
+// Warps of the epilogue.  The direct kind's four are enough, but where the gate's gradients read and write boxes
+// (16384 rows of 768 and 2048 channels 61 us with four, 55 with eight; the other epilogues lose 3 % by eight).
+constexpr int gemm_warps(int kind, int epi) { return kind != kDirect ? 16 : epi == kGateBwd ? 8 : 4; }
+constexpr int gemm_threads(int kind, int epi) { return (kind == kDirect ? 64 : 128) + 32 * gemm_warps(kind, epi); }
 
 struct GemmBars {
     uint64_t full[GST], empty[GST], acc_full[2][2], acc_empty[2][2], in[16][2];
@@ -287,6 +289,13 @@ struct EpiWarp {
     uint32_t tmem;   // of its lanes
 };
 
+// The accumulator has been read
+__device__ __forceinline__ void release_acc(const EpiWarp &w, uint32_t release) {
+    tc::tc_fence_before();
+    __syncwarp();
+    if (w.lane == 0) arrive_remote(release);
+}
+
 // Direct kind, kPlain: 256 columns in bf16.
 __device__ __forceinline__ void epi_plain(const GemmArgs &g, const EpiWarp &w, Ring<4> &ring, const GemmTile &t, uint32_t acc,
                                           uint32_t release) {
@@ -298,11 +307,7 @@ __device__ __forceinline__ void epi_plain(const GemmArgs &g, const EpiWarp &w, R
         tmem_ld32(acc + c * 32, r);
         tc::tmem_wait_ld();
         tmem_use(r);
-        if (c == 7) {
-            tc::tc_fence_before();
-            __syncwarp();
-            if (w.lane == 0) arrive_remote(release);
-        }
+        if (c == 7) release_acc(w, release);
         if (c % 2 == 0) slab = ring.take();
 #pragma unroll
         for (int k = 0; k < 4; ++k) stage<__nv_bfloat16>(slab, w.lane, c % 2 * 4 + k, reinterpret_cast<const float *>(r) + 8 * k);
@@ -330,11 +335,7 @@ __device__ __forceinline__ void epi_gate(const GemmArgs &g, const EpiWarp &w, Ri
             tc::tmem_wait_ld();
             tmem_use(rg);
             tmem_use(ru);
-            if (j == 1 && c == 1) {
-                tc::tc_fence_before();
-                __syncwarp();
-                if (w.lane == 0) arrive_remote(release);
-            }
+            if (j == 1 && c == 1) release_acc(w, release);
             const float *xg = reinterpret_cast<const float *>(rg), *xu = reinterpret_cast<const float *>(ru);
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
@@ -367,21 +368,21 @@ __device__ __forceinline__ void gate_grads(float dh, float &gate, float &up) {
     gate = dg;
 }
 
-// Direct kind, kGateBwd: boxes of 64 columns of both factors are read one box ahead (across tiles too),
-// and the gradients written over them.
+// Direct kind, kGateBwd: boxes of 32 columns (swizzled over 64 bytes) of both factors are read one box ahead
+// (across tiles too), and the gradients written over them.
 struct GateBwd {
     int n[2];  // uses of either pair of boxes
     __device__ __forceinline__ static bool inside(const GemmArgs &g, const EpiWarp &w, const GemmTile &t, int j) {
-        return t.row0 + w.rank * 128 + w.q * 32 < g.M[0] && t.col0 + j * 64 < g.N[0];
+        return t.row0 + w.rank * 128 + w.q * 32 < g.M[0] && t.col0 + w.half * 128 + j * 32 < g.N[0];
     }
     __device__ __forceinline__ static void ask(const GemmArgs &g, const EpiWarp &w, const GemmTile &t, int j, int set) {
         if (w.lane != 0 || !inside(g, w, t, j)) return;
-        char *s = w.staging + set * 2 * GSLAB;
-        const int row = t.row0 + w.rank * 128 + w.q * 32, col = t.col0 + j * 64;
+        char *s = w.staging + set * GSLAB;
+        const int row = t.row0 + w.rank * 128 + w.q * 32, col = t.col0 + w.half * 128 + j * 32;
         bulk_wait_read<0>();  // the gradients that lay here have been stored
-        tc::mbar_arrive_expect_tx(&w.in[set], 2 * GSLAB);
+        tc::mbar_arrive_expect_tx(&w.in[set], GSLAB);
         load_3d(s, &g.e[0], col, row, 0, &w.in[set]);
-        load_3d(s + GSLAB, &g.e[1], col, row, 0, &w.in[set]);
+        load_3d(s + GSLAB / 2, &g.e[1], col, row, 0, &w.in[set]);
     }
     // next: the tile behind this one (col0 < 0: none)
     __device__ __forceinline__ bool run(const GemmArgs &g, const EpiWarp &w, const GemmTile &t, const GemmTile &next, uint32_t acc,
@@ -395,39 +396,30 @@ struct GateBwd {
                 ask(g, w, t, j + 1, set ^ 1);
             else if (next.col0 >= 0)
                 ask(g, w, next, 0, set ^ 1);
-            const bool in = inside(g, w, t, j);
-            if (in && !pair_wait(&w.in[set], n[set] & 1, g.err)) return false;
-            n[set] += in;
-            char *sg = w.staging + set * 2 * GSLAB, *su = sg + GSLAB;
+            uint32_t r[32];
+            tmem_ld32(acc + w.half * 128 + j * 32, r);
+            tc::tmem_wait_ld();
+            tmem_use(r);
+            if (j == 3) release_acc(w, release);
+            if (!inside(g, w, t, j)) continue;
+            if (!pair_wait(&w.in[set], n[set]++ & 1, g.err)) return false;
+            char *sg = w.staging + set * GSLAB, *su = sg + GSLAB / 2;
 #pragma unroll
-            for (int c = 0; c < 2; ++c) {
-                uint32_t r[32];
-                tmem_ld32(acc + j * 64 + c * 32, r);
-                tc::tmem_wait_ld();
-                tmem_use(r);
-                if (j == 3 && c == 1) {
-                    tc::tc_fence_before();
-                    __syncwarp();
-                    if (w.lane == 0) arrive_remote(release);
-                }
-                if (!in) continue;
+            for (int k = 0; k < 4; ++k) {
+                float xg[8], xu[8];
+                const int at = w.lane * 64 + ((k ^ (w.lane >> 1 & 3)) << 4);
+                Vec16<E>::unpack(*reinterpret_cast<const uint4 *>(sg + at), xg);
+                Vec16<E>::unpack(*reinterpret_cast<const uint4 *>(su + at), xu);
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    float xg[8], xu[8];
-                    const int at = swz128(w.lane, c * 4 + k);
-                    Vec16<E>::unpack(*reinterpret_cast<const uint4 *>(sg + at), xg);
-                    Vec16<E>::unpack(*reinterpret_cast<const uint4 *>(su + at), xu);
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) gate_grads<E>(__uint_as_float(r[8 * k + e]), xg[e], xu[e]);
-                    *reinterpret_cast<uint4 *>(sg + at) = Vec16<E>::pack(xg);
-                    *reinterpret_cast<uint4 *>(su + at) = Vec16<E>::pack(xu);
-                }
+                for (int e = 0; e < 8; ++e) gate_grads<E>(__uint_as_float(r[8 * k + e]), xg[e], xu[e]);
+                *reinterpret_cast<uint4 *>(sg + at) = Vec16<E>::pack(xg);
+                *reinterpret_cast<uint4 *>(su + at) = Vec16<E>::pack(xu);
             }
             tc::fence_proxy_async_smem();
             __syncwarp();
-            if (in && w.lane == 0) {
-                store_3d(&g.o[0], t.col0 + j * 64, row, 0, sg);
-                store_3d(&g.o[1], t.col0 + j * 64, row, 0, su);
+            if (w.lane == 0) {
+                store_3d(&g.o[0], t.col0 + w.half * 128 + j * 32, row, 0, sg);
+                store_3d(&g.o[1], t.col0 + w.half * 128 + j * 32, row, 0, su);
                 tc::bulk_commit();
             }
         }
@@ -578,10 +570,10 @@ __device__ __forceinline__ bool epi_gate_e4m3(const GemmArgs &g, const EpiWarp &
 static_assert(sizeof(GemmBars) <= 512, "shared memory budget");
 
 template <int AMN, int BMN, int KIND, int EPI, typename E>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(gemm_threads<KIND>(), 1) gemm_kernel(const __grid_constant__ GemmArgs g) {
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(gemm_threads(KIND, EPI), 1) gemm_kernel(const __grid_constant__ GemmArgs g) {
     constexpr bool E8 = KIND == kE4M3;
     constexpr int ST = gemm_stages(KIND, EPI), STAGING = gemm_staging(KIND, EPI);
-    constexpr int EW = KIND == kDirect ? 4 : 16, E0 = KIND == kDirect ? 2 : 4, HALVES = gemm_halves(KIND), COLS = tile_cols(EPI), KB = E8 ? 128 : 64;
+    constexpr int EW = gemm_warps(KIND, EPI), E0 = KIND == kDirect ? 2 : 4, HALVES = gemm_halves(KIND), COLS = tile_cols(EPI), KB = E8 ? 128 : 64;
     extern __shared__ char raw[];
     char *sm = raw + ((1024 - (tc::smem_u32(raw) & 1023)) & 1023);
     char *ops = sm, *staging = sm + ST * 2 * GOP;
@@ -706,7 +698,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(gemm_threads<KIND>()
         const int ew = warp - E0;
         w.lane = lane;
         w.q = warp & 3;
-        w.half = ew >> 3;
+        w.half = KIND == kDirect ? ew >> 2 : ew >> 3;
         w.part = ew >> 2 & 1;
         w.rank = rank;
         w.staging = staging + ew * (STAGING / EW);
@@ -776,9 +768,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(gemm_threads<KIND>()
                         if (c < 3) {
                             tmem_ld16(acc + sum_col<KIND, EPI>(w, c + 1), r[(c + 1) & 1]);
                         } else {
-                            tc::tc_fence_before();
-                            __syncwarp();
-                            if (lane == 0) arrive_remote(lead_addr(&bar.acc_empty[ab][HALVES == 1 ? 0 : w.half]));
+                            release_acc(w, lead_addr(&bar.acc_empty[ab][HALVES == 1 ? 0 : w.half]));
                         }
                         const float m = EPI == kGate && c >= 2 ? m1 : m0;
 #pragma unroll
@@ -824,7 +814,7 @@ ida_status gemm_launch(GemmArgs &g, int num_sms, cudaStream_t st) {
     g.tiles = (int)tiles;
     if (KIND == kDirect) g.chunk = g.segs * g.kblocks;
     const long long pairs = tiles < num_sms / 2 ? tiles : num_sms / 2;
-    e = launch_dependent(kernel, dim3((unsigned)(2 * pairs)), dim3(gemm_threads<KIND>()), gemm_smem(KIND, EPI), st, g);
+    e = launch_dependent(kernel, dim3((unsigned)(2 * pairs)), dim3(gemm_threads(KIND, EPI)), gemm_smem(KIND, EPI), st, g);
     if (e != cudaSuccess) return fail_with(IDA_ERR_CUDA, std::string("matrix product launch: ") + cudaGetErrorString(e));
     return launched("matrix product");
 }

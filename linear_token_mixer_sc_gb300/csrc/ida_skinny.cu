@@ -35,16 +35,18 @@ __device__ __forceinline__ float remote_float(const float *p, int rank) {
     return v;
 }
 
-constexpr int SKW = 8;  // warps of a block
+// Warps of a block and, below, chunks of 128 bytes that a lane has in flight: in bf16 16 warps of two tiles' rows (one row through the
+// block of 2048 and 5632 channels 16.9 us; 8 warps 19.5, of four rows 20.0), in e4m3 8.
+constexpr int skinny_warps(bool e8) { return e8 ? 8 : 16; }
 
 // NT: groups of 8 tokens.  SUB tiles of 16 weights' rows a block, of which a plain product may use 8 (HALVES
 // 1).  GATE: rows 8 .. 15 of a tile are w1's.  E8 && GATE: a cluster of 8 blocks makes the 128 channels of
 // a scale.
 template <bool E8, int NT, int SUB, int HALVES, bool GATE>
-__global__ void __launch_bounds__(SKW * 32) skinny_kernel(SkinnyArgs a) {
-    constexpr int U = 4 / (SUB * HALVES), LD = 8 * NT + 1, ES = E8 ? 1 : 2;
+__global__ void __launch_bounds__(skinny_warps(E8) * 32, E8 ? 1 : 2) skinny_kernel(SkinnyArgs a) {
+    constexpr int U = SUB * HALVES >= 2 ? 1 : 2, LD = 8 * NT + 1, ES = E8 ? 1 : 2;
     constexpr int COLS = SUB * (GATE ? 8 : 8 * HALVES);  // output columns of a block
-    extern __shared__ float red[];  // [SKW][SUB][16][LD]
+    extern __shared__ float red[];  // [warps][SUB][16][LD]
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3, nw = blockDim.x >> 5;
     const long long n0 = (long long)blockIdx.x * COLS;
     const long long kbytes = (long long)a.K * ES;
@@ -212,7 +214,8 @@ static ida_status launch_skinny(const SkinnyArgs &a, cudaStream_t st) {
     const auto kernel = skinny_kernel<E8, NT, SUB, HALVES, GATE>;
     const long long chunks = ((long long)a.K * (E8 ? 1 : 2) + 127) / 128;
     // the 8-bit gate's threads make 16 channels of 16 rows at a time
-    const int warps = E8 && GATE ? SKW : chunks < SKW ? (int)chunks : SKW;
+    constexpr int most = skinny_warps(E8);
+    const int warps = E8 && GATE ? most : chunks < most ? (int)chunks : most;
     const size_t smem = (size_t)warps * SUB * 16 * (8 * NT + 1) * sizeof(float);
     cudaError_t e = allow_smem(kernel, smem);
     if (e != cudaSuccess) return fail_with(IDA_ERR_CUDA, cudaGetErrorString(e));
