@@ -82,7 +82,6 @@ struct Eight {
 constexpr int QU = 4;
 template <typename E>
 __global__ void __launch_bounds__(256) quant_rows_kernel(QuantArgs a) {
-    dependent_launch();
     dependent_wait();
     const int sub = threadIdx.x & 15, kb = (int)a.blocks.d;
     const int units = a.rows * kb, u0 = blockIdx.x * (16 * QU) + (threadIdx.x >> 4);
@@ -112,7 +111,6 @@ __global__ void __launch_bounds__(256) quant_rows_kernel(QuantArgs a) {
 template <typename E>
 __global__ void __launch_bounds__(512) quant_blocks_kernel(QuantArgs a) {
     __shared__ float red[16];
-    dependent_launch();
     dependent_wait();
     const int rb = divide(blockIdx.x, a.blocks), c = (blockIdx.x - rb * (int)a.blocks.d) * 128 + (threadIdx.x & 15) * 8;
     const long long r0 = (long long)rb * 128 + (threadIdx.x >> 4);

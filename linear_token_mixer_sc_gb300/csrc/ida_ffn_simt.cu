@@ -80,8 +80,7 @@ __global__ void __launch_bounds__(256) ffn_simt_kernel(SimtArgs g) {
     const int tm = (g.M[p] + FT - 1) / FT, row0 = b % tm * FT, col0 = b / tm * COLS, M = g.M[p], N = g.N[p];
     const int t = threadIdx.x, group = t >> 6, tx = t & 7, ty = t >> 3 & 7;
     const int per = (g.K + FK - 1) / FK, slabs = g.halves * per;
-    dependent_launch();
-    dependent_wait();
+    dependent_wait();  // (letting the next launch start early, too, fills the SMs with its waiting blocks: 509 rows' gradients 22 us, then 40)
     auto load = [&](int i) {
         if (i < slabs) {
             const int h = i / per, k0 = (i - h * per) * FK;

@@ -89,7 +89,6 @@ __global__ void __launch_bounds__(skinny_warps(E8) * 32, E8 ? 1 : 2) skinny_kern
     if (!a.weights_ready) dependent_wait();
     fetch(warp);
     if (a.weights_ready) dependent_wait();
-    dependent_launch();
     for (int c0 = warp; c0 < chunks; c0 += U * nw) {
         if (c0 != warp) fetch(c0);
 #pragma unroll
@@ -143,6 +142,7 @@ __global__ void __launch_bounds__(skinny_warps(E8) * 32, E8 ? 1 : 2) skinny_kern
         for (int n = 0; n < NT; ++n)
 #pragma unroll
             for (int i = 0; i < 4; ++i) red[((warp * SUB + s) * 16 + g + (i >> 1) * 8) * LD + 8 * n + 2 * t + (i & 1)] = acc[s][n][i];
+    dependent_launch();
     __syncthreads();
     auto sum = [&](int s, int r, int tok) {
         float v = red[(s * 16 + r) * LD + tok];
