@@ -750,11 +750,13 @@ def ida_rmsnorm_backward(r: torch.Tensor, w: torch.Tensor, dy: torch.Tensor, dre
 
 # ---- the feed-forward block and products in 8 bits --------------------------------------------
 
+@functools.lru_cache(maxsize=256)  # host arithmetic on the sizes alone
 def ida_ffn_workspace_bytes(rows: int, D: int, F: int, dtype: int) -> int:
     _fits(rows, D, F, dtype)
     return int(load().ida_ffn_workspace_bytes(rows, D, F, dtype))
 
 
+@functools.lru_cache(maxsize=256)
 def ida_ffn_backward_workspace_bytes(rows: int, D: int, F: int, dtype: int) -> int:
     _fits(rows, D, F, dtype)
     return int(load().ida_ffn_backward_workspace_bytes(rows, D, F, dtype))
@@ -804,9 +806,8 @@ def ida_ffn(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor, w_down: t
         acts = torch.empty(shape, dtype=x.dtype, device=x.device)
     elif acts is False:
         acts = None
-    L = load()
-    ws, wsp, n = _work_buffer(workspace, L.ida_ffn_workspace_bytes(rows, D, F, code) if workspace is None else 0, dev)
-    st = L.ida_ffn(*ptrs, _dense("out", out, x.shape, x.dtype, dev),
+    ws, wsp, n = _work_buffer(workspace, ida_ffn_workspace_bytes(rows, D, F, code) if workspace is None else 0, dev)
+    st = (_lib or load()).ida_ffn(*ptrs, _dense("out", out, x.shape, x.dtype, dev),
                    None if acts is None else _dense("acts", acts, shape, x.dtype, dev), *sizes, ldx, code, wsp, n,
                    _raw_stream(dev))
     _check(st, "ida_ffn")
@@ -831,18 +832,14 @@ def ida_ffn_backward(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor, 
         for k, t in (("x", x), ("w_gate", w_gate), ("w_up", w_up), ("w_down", w_down))}
     gp = [_dense(f"grads[{k!r}]", g[k], t.shape, x.dtype, dev)
           for k, t in (("x", x), ("w_gate", w_gate), ("w_up", w_up), ("w_down", w_down))]
-    L = load()
-    ws, wsp, n = _work_buffer(workspace, L.ida_ffn_backward_workspace_bytes(rows, D, F, code)
+    ws, wsp, n = _work_buffer(workspace, ida_ffn_backward_workspace_bytes(rows, D, F, code)
                               if workspace is None else 0, dev)
-    st = L.ida_ffn_backward(*ptrs, ap, dp, *gp, *sizes, ldx, code, wsp, n, _raw_stream(dev))
+    st = (_lib or load()).ida_ffn_backward(*ptrs, ap, dp, *gp, *sizes, ldx, code, wsp, n, _raw_stream(dev))
     _check(st, "ida_ffn_backward")
     return g
 
 
-def _operand(name: str, q: torch.Tensor, scale: torch.Tensor, lead, K: int, scales, dev: int):
-    """Addresses of an e4m3 operand [*lead, K] and its scales."""
-    return (_dense(name, q, (*lead, K), torch.float8_e4m3fn, dev),
-            _dense(f"the scales of {name}", scale, scales, torch.float32, dev))
+_E4M3 = torch.float8_e4m3fn
 
 
 @_placed
@@ -861,12 +858,12 @@ def ida_quant_e4m3(x: torch.Tensor, rows: int = 1, q: torch.Tensor | None = None
     lead = x.shape[:-1] if rows == 1 else ((n + 127) // 128,)
     shape = (*lead, (K + 127) // 128)
     if q is None:
-        q = torch.empty(x.shape, dtype=torch.float8_e4m3fn, device=x.device)
+        q = torch.empty(x.shape, dtype=_E4M3, device=x.device)
     if scale is None:
         scale = torch.empty(shape, dtype=torch.float32, device=x.device)
-    st = load().ida_quant_e4m3(xp, _dense("q", q, x.shape, torch.float8_e4m3fn, dev),
-                               _dense("scale", scale, shape, torch.float32, dev), n, K, rows, ldx, code,
-                               _raw_stream(dev))
+    st = (_lib or load()).ida_quant_e4m3(xp, _dense("q", q, x.shape, _E4M3, dev),
+                                         _dense("scale", scale, shape, torch.float32, dev), n, K, rows, ldx, code,
+                                         _raw_stream(dev))
     _check(st, "ida_quant_e4m3")
     return q, scale
 
@@ -883,13 +880,15 @@ def ida_gemm_e4m3(a: torch.Tensor, a_scale: torch.Tensor, b: torch.Tensor, b_sca
     N, kb = b.shape[0], (K + 127) // 128
     rows = a.numel() // K if K else 0
     _fits(rows, K, N)
-    ptrs = [*_operand("a", a, a_scale, lead, K, (*lead, kb), dev),
-            *_operand("b", b, b_scale, (N,), K, ((N + 127) // 128, kb), dev)]
+    f32 = torch.float32
+    ptrs = (_dense("a", a, a.shape, _E4M3, dev), _dense("a_scale", a_scale, (*lead, kb), f32, dev),
+            _dense("b", b, (N, K), _E4M3, dev), _dense("b_scale", b_scale, ((N + 127) // 128, kb), f32, dev))
+    shape = (*lead, N)
     if out is None:
-        out = torch.empty((*lead, N), dtype=dtype, device=a.device)
+        out = torch.empty(shape, dtype=dtype, device=a.device)
     code = _dtype_code(out)
-    st = load().ida_gemm_e4m3(*ptrs, _dense("out", out, (*lead, N), out.dtype, dev), rows, K, N, code,
-                              _raw_stream(dev))
+    st = (_lib or load()).ida_gemm_e4m3(*ptrs, _dense("out", out, shape, out.dtype, dev), rows, K, N, code,
+                                        _raw_stream(dev))
     _check(st, "ida_gemm_e4m3")
     return out
 
@@ -907,15 +906,17 @@ def ida_glu_e4m3(a: torch.Tensor, a_scale: torch.Tensor, w_gate: torch.Tensor, g
     rows = a.numel() // D if D else 0
     _fits(rows, D, F)
     blocks = (F + 127) // 128
-    ptrs = [*_operand("a", a, a_scale, lead, D, (*lead, kb), dev),
-            *_operand("w_gate", w_gate, gate_scale, (F,), D, (blocks, kb), dev),
-            *_operand("w_up", w_up, up_scale, (F,), D, (blocks, kb), dev)]
+    f32 = torch.float32
+    ptrs = (_dense("a", a, a.shape, _E4M3, dev), _dense("a_scale", a_scale, (*lead, kb), f32, dev),
+            _dense("w_gate", w_gate, (F, D), _E4M3, dev), _dense("gate_scale", gate_scale, (blocks, kb), f32, dev),
+            _dense("w_up", w_up, (F, D), _E4M3, dev), _dense("up_scale", up_scale, (blocks, kb), f32, dev))
+    qs, ss = (*lead, F), (*lead, blocks)
     if q is None:
-        q = torch.empty((*lead, F), dtype=torch.float8_e4m3fn, device=a.device)
+        q = torch.empty(qs, dtype=_E4M3, device=a.device)
     if scale is None:
-        scale = torch.empty((*lead, blocks), dtype=torch.float32, device=a.device)
-    st = load().ida_glu_e4m3(*ptrs, _dense("q", q, (*lead, F), torch.float8_e4m3fn, dev),
-                             _dense("scale", scale, (*lead, blocks), torch.float32, dev), rows, D, F, _raw_stream(dev))
+        scale = torch.empty(ss, dtype=f32, device=a.device)
+    st = (_lib or load()).ida_glu_e4m3(*ptrs, _dense("q", q, qs, _E4M3, dev), _dense("scale", scale, ss, f32, dev),
+                                       rows, D, F, _raw_stream(dev))
     _check(st, "ida_glu_e4m3")
     return q, scale
 

@@ -223,9 +223,9 @@ ida_status ida_gemm_e4m3(const void *a, const float *a_scale, const void *b, con
     std::string why;
     s = device_ready(&num_sms, why);
     if (s != IDA_OK) return fail_with(s, why);
-    if (rows <= kFewRows) {
+    if (rows <= few_rows(kFewE4M3)) {
         SkinnyArgs k = {a, K, b, nullptr, out, nullptr, nullptr, a_scale, b_scale, nullptr, nullptr, rows, K, N, dtype == IDA_F32, false};
-        return skinny_product(k, true, num_sms, reinterpret_cast<cudaStream_t>(stream));
+        return skinny_product(k, kFewE4M3, num_sms, reinterpret_cast<cudaStream_t>(stream));
     }
     GemmArgs g = {};
     s = device_error_word(&g.err, why);
@@ -234,6 +234,7 @@ ida_status ida_gemm_e4m3(const void *a, const float *a_scale, const void *b, con
     g.M[0] = rows, g.N[0] = N;
     g.kblocks = (int)kb;
     g.sa = a_scale, g.sb[0] = b_scale;
+    g.out[0] = out;
     s = gemm_map(&g.a[0], a, kMapBytes, K, rows, 1, K, 128, 128);
     if (s == IDA_OK) s = gemm_map(&g.b[0], b, kMapBytes, K, N, 1, K, 128, 128);
     if (s == IDA_OK) s = gemm_map(&g.o[0], out, dtype == IDA_BF16 ? kMapBf16 : kMapF32, N, rows, 1, N, dtype == IDA_BF16 ? 64 : 32, 32);
@@ -261,9 +262,9 @@ ida_status ida_glu_e4m3(const void *a, const float *a_scale, const void *w_gate,
     std::string why;
     s = device_ready(&num_sms, why);
     if (s != IDA_OK) return fail_with(s, why);
-    if (rows <= kFewRows) {
+    if (rows <= few_rows(kFewE4M3)) {
         SkinnyArgs k = {a, D, w_gate, w_up, q, nullptr, nullptr, a_scale, gate_scale, up_scale, scale, rows, D, F, false, false};
-        return skinny_gate(k, true, reinterpret_cast<cudaStream_t>(stream));
+        return skinny_gate(k, kFewE4M3, reinterpret_cast<cudaStream_t>(stream));
     }
     GemmArgs g = {};
     s = device_error_word(&g.err, why);

@@ -178,8 +178,8 @@ static ida_status run_gemm(int a_mn, int b_mn, int epi, GemmArgs &g, int dtype, 
 
 // fp32 products on the CUDA cores: few rows, or little arithmetic.  Forward and backward, in us, there and on the tensor cores: 251 rows of
 // 64 and 176 channels 6 + 13 and 19 + 40, 512 of 256 and 512 22 + 53 and 34 + 73, 1024 of 256 and 704 (2^27.5) 40 + 92 and 40 + 98,
-// 1024 of 512 and 1024 104 + 209 and 56 + 125.
-static bool on_cuda_cores(long long rows, long long D, long long F) { return rows <= kFewRows || rows * D * F <= (1LL << 27); }
+// 1024 of 512 and 1024 104 + 209 and 56 + 125; 32 rows of 2048 and 5632 122 + 391 and 267 + 455.
+static bool on_cuda_cores(long long rows, long long D, long long F) { return rows <= 64 || rows * D * F <= (1LL << 27); }
 
 static ida_status check_ffn(int rows, int D, int F, long long ldx, int dtype) {
     if (rows < 0) return fail_with(IDA_ERR_ARG, "rows must be >= 0");
@@ -237,12 +237,13 @@ ida_status ida_ffn(const void *x, const void *w_gate, const void *w_up, const vo
 
     char *ws = static_cast<char *>(workspace), *ac = static_cast<char *>(acts);
     void *h = ac ? ac + 2 * tf * es : ws + sp.h;
-    if (rows <= kFewRows && dtype == IDA_BF16) {
-        SkinnyArgs a = {x, ldx, w_gate, w_up, h, ac, ac ? ac + tf * es : nullptr, nullptr, nullptr, nullptr, nullptr, rows, D, F, false, false};
-        s = skinny_gate(a, false, st);
+    const int type = dtype == IDA_BF16 ? kFewBf16 : kFewF32;
+    if (rows <= few_rows(type)) {
+        SkinnyArgs a = {x, ldx, w_gate, w_up, h, ac, ac ? ac + tf * es : nullptr, nullptr, nullptr, nullptr, nullptr, rows, D, F, dtype == IDA_F32, false};
+        s = skinny_gate(a, type, st);
         if (s != IDA_OK) return s;
-        SkinnyArgs b = {h, F, w_down, nullptr, out, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr, rows, F, D, false, true};
-        return skinny_product(b, false, num_sms, st);
+        SkinnyArgs b = {h, F, w_down, nullptr, out, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr, rows, F, D, dtype == IDA_F32, true};
+        return skinny_product(b, type, num_sms, st);
     }
     if (dtype == IDA_F32 && on_cuda_cores(rows, D, F)) {
         float *fh = static_cast<float *>(h), *fa = reinterpret_cast<float *>(ac);
@@ -293,6 +294,7 @@ ida_status ida_ffn(const void *x, const void *w_gate, const void *w_up, const vo
     add_segments(d, dtype, 0, 0);
     s = operand_map(&d.a[0], H, 0);
     if (s == IDA_OK) s = operand_map(&d.b[0], Wd, 0);
+    d.out[0] = out;
     if (s == IDA_OK) s = out_map(&d.o[0], out, dtype, rows, D);
     if (s == IDA_OK) s = run_gemm(0, 0, kPlain, d, dtype, num_sms, st);
     return s;
@@ -403,6 +405,7 @@ ida_status ida_ffn_backward(const void *x, const void *w_gate, const void *w_up,
     const Operand *wa[3] = {&dG, &dU, &dY}, *wb[3] = {&X, &X, &H};
     for (int p = 0; p < 3; ++p) {
         w.M[p] = (int)wa[p]->cols, w.N[p] = (int)wb[p]->cols;
+        w.out[p] = dw[p];
         if (s == IDA_OK) s = operand_map(&w.a[p], *wa[p], 1);
         if (s == IDA_OK) s = operand_map(&w.b[p], *wb[p], 1);
         if (s == IDA_OK) s = out_map(&w.o[p], dw[p], dtype, w.M[p], w.N[p]);
@@ -419,6 +422,7 @@ ida_status ida_ffn_backward(const void *x, const void *w_gate, const void *w_up,
     if (s == IDA_OK) s = operand_map(&d.a[1], dU, 0);
     if (s == IDA_OK) s = operand_map(&d.b[0], Wg, 1);
     if (s == IDA_OK) s = operand_map(&d.b[1], Wu, 1);
+    d.out[0] = dx;
     if (s == IDA_OK) s = out_map(&d.o[0], dx, dtype, rows, D);
     if (s == IDA_OK) s = run_gemm(0, 1, kPlain, d, dtype, num_sms, st);
     return s;

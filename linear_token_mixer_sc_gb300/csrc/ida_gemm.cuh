@@ -57,6 +57,8 @@ struct GemmArgs {
     int M[3], N[3];                      // rows and columns of each problem's output
     int tiles, bands[3], count[3];       // of the launch; whole bands of 8 rows of tiles, and tiles, of each problem
     Divisor band[3], last[3];            // tiles of such a band, rows of tiles of the last one (1 if there is none)
+    void *out[3];                        // of split products, which store by themselves
+    int split;                           // pairs that share a tile's contraction
     int problems, segs, kblocks, chunk;  // kblocks: blocks of 128 bytes along each segment's contraction
     GemmSeg seg[12];
     int keep;                            // kGate: store the two factors as well
@@ -75,11 +77,17 @@ __device__ __forceinline__ uint32_t cluster_rank() {
 __device__ __forceinline__ void cluster_sync_all() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
-// the address of the even CTA's copy of a shared variable
-__device__ __forceinline__ uint32_t lead_addr(const void *p) {
+// the address of a shared variable of the cluster's CTA `rank`; of the pair's even one
+__device__ __forceinline__ uint32_t cluster_addr(const void *p, int rank) {
     uint32_t r;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(r) : "r"(tc::smem_u32(p)));
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(tc::smem_u32(p)), "r"(rank));
     return r;
+}
+__device__ __forceinline__ uint32_t lead_addr(const void *p) { return cluster_addr(p, (int)cluster_rank() & ~1); }
+__device__ __forceinline__ float4 cluster_float4(uint32_t addr) {
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr) : "memory");
+    return v;
 }
 // No data but the accumulator's goes with this arrival, and tcgen05's own fence orders that: a release at the
 // cluster's scope would wait for all of the warp's memory accesses (8-bit gated projection 649 us, now XXX).
@@ -131,7 +139,7 @@ __device__ __forceinline__ void pair_commit(uint64_t *bar) {  // to both CTAs' c
     asm volatile(
         "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
             tc::smem_u32(bar)),
-        "h"((unsigned short)3)
+        "h"((unsigned short)(3 << (cluster_rank() & ~1)))
         : "memory");
 }
 template <bool E4M3>
@@ -569,8 +577,31 @@ __device__ __forceinline__ bool epi_gate_e4m3(const GemmArgs &g, const EpiWarp &
 
 static_assert(sizeof(GemmBars) <= 512, "shared memory budget");
 
-template <int AMN, int BMN, int KIND, int EPI, typename E>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(gemm_threads(KIND, EPI), 1) gemm_kernel(const __grid_constant__ GemmArgs g) {
+// Split products (kPlain of few tiles and a long contraction): a cluster of `split` pairs makes one tile, each pair a
+// part of the contraction.  Each CTA lays its 128 x 256 fp32 sums where its operands were, [column / 4][row] so
+// that a warp's 16-byte accesses lie side by side, and adds up its share of the columns over the pairs, in
+// their order.  (256 rows of 5632 channels to 2048, eight tiles: XXX us in four parts, XXX in one.)
+template <int EW, typename E>
+__device__ __forceinline__ void add_parts(const GemmArgs &g, const EpiWarp &w, const GemmTile &t, const char *part, int group, int split) {
+    const int r = w.q * 32 + w.lane, row = t.row0 + w.rank * 128 + r, own = (int)cluster_rank() >> 1;
+    const int cols = 256 / split / (EW / 4), c0 = own * (256 / split) + group * cols;
+    if (row >= g.M[t.p]) return;
+    E *out = static_cast<E *>(g.out[t.p]) + (long long)row * g.N[t.p] + t.col0;
+    for (int c = c0; c < c0 + cols && t.col0 + c < g.N[t.p]; c += 8) {
+        float x[8] = {};
+        for (int p = 0; p < split; ++p) {
+            const uint32_t from = cluster_addr(part + (c / 4 * 128 + r) * 16, 2 * p + w.rank);
+            const float4 lo = cluster_float4(from), hi = cluster_float4(from + 128 * 16);
+            x[0] += lo.x, x[1] += lo.y, x[2] += lo.z, x[3] += lo.w;
+            x[4] += hi.x, x[5] += hi.y, x[6] += hi.z, x[7] += hi.w;
+        }
+#pragma unroll
+        for (int k = 0; k < 8; k += Vec16<E>::n) *reinterpret_cast<uint4 *>(out + c + k) = Vec16<E>::pack(x + k);
+    }
+}
+
+template <int AMN, int BMN, int KIND, int EPI, typename E, bool SPLIT>
+__global__ void __launch_bounds__(gemm_threads(KIND, EPI), 1) gemm_kernel(const __grid_constant__ GemmArgs g) {
     constexpr bool E8 = KIND == kE4M3;
     constexpr int ST = gemm_stages(KIND, EPI), STAGING = gemm_staging(KIND, EPI);
     constexpr int EW = gemm_warps(KIND, EPI), E0 = KIND == kDirect ? 2 : 4, HALVES = gemm_halves(KIND), COLS = tile_cols(EPI), KB = E8 ? 128 : 64;
@@ -578,9 +609,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(gemm_threads(KIND, E
     char *sm = raw + ((1024 - (tc::smem_u32(raw) & 1023)) & 1023);
     char *ops = sm, *staging = sm + ST * 2 * GOP;
     GemmBars &bar = *reinterpret_cast<GemmBars *>(staging + STAGING);
-    const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31, rank = (int)cluster_rank();
-    const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
-    const int tiles = g.tiles, per_tile = g.segs * g.kblocks;
+    const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31, rank = (int)cluster_rank() & 1;
+    const int tiles = g.tiles;
+    // a split product's cluster makes one tile, any other pair every so many
+    const int pair = SPLIT ? blockIdx.x / (2 * g.split) : blockIdx.x >> 1, pairs = SPLIT ? tiles : gridDim.x >> 1;
+    const int all = g.segs * g.kblocks, part = SPLIT ? (int)cluster_rank() >> 1 : 0;
+    const int kfirst = SPLIT ? all * part / g.split : 0, per_tile = (SPLIT ? all * (part + 1) / g.split : all) - kfirst;
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < ST; ++s) {
@@ -620,30 +654,33 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(gemm_threads(KIND, E
             for (int t = pair; ok && t < tiles; t += pairs) {
                 const GemmTile tile = tile_of(g, t, COLS);
                 const int row = tile.row0 + rank * 128, col = EPI == kGate ? tile.col0 : tile.col0 + rank * 128;
-                for (int s = 0; ok && s < g.segs; ++s) {
-                    const GemmSeg sg = g.seg[s];
+                int s = SPLIT ? kfirst / g.kblocks : 0, kb = kfirst - s * g.kblocks;
+                GemmSeg sg = g.seg[s];
+                for (int k = 0; k < per_tile; ++k) {
                     const CUtensorMap *ma = &g.a[tile.p + sg.a], *mb = &g.b[EPI == kGate ? sg.b + rank : tile.p + sg.b];
-                    for (int kb = 0; kb < g.kblocks; ++kb) {
-                        if (!(ok = warp_wait(&bar.empty[st], ph, g.err))) break;
-                        if (one) {
-                            if (rank == 0) tc::mbar_arrive_expect_tx(&bar.full[st], 4 * GOP);
-                            char *A = ops + st * 2 * GOP, *B = A + GOP;
-                            const uint32_t full = lead_addr(&bar.full[st]);
-                            if (AMN) {
-                                pair_load(A, ma, row, kb * 64, sg.ap, full);
-                                pair_load(A + GOP / 2, ma, row + 64, kb * 64, sg.ap, full);
-                            } else {
-                                pair_load(A, ma, kb * KB, row, sg.ap, full);
-                            }
-                            if (BMN) {
-                                pair_load(B, mb, col, kb * 64, sg.bp, full);
-                                pair_load(B + GOP / 2, mb, col + 64, kb * 64, sg.bp, full);
-                            } else {
-                                pair_load(B, mb, kb * KB, col, sg.bp, full);
-                            }
+                    if (!(ok = warp_wait(&bar.empty[st], ph, g.err))) break;
+                    if (one) {
+                        if (rank == 0) tc::mbar_arrive_expect_tx(&bar.full[st], 4 * GOP);
+                        char *A = ops + st * 2 * GOP, *B = A + GOP;
+                        const uint32_t full = lead_addr(&bar.full[st]);
+                        if (AMN) {
+                            pair_load(A, ma, row, kb * 64, sg.ap, full);
+                            pair_load(A + GOP / 2, ma, row + 64, kb * 64, sg.ap, full);
+                        } else {
+                            pair_load(A, ma, kb * KB, row, sg.ap, full);
                         }
-                        ++it;
-                        if (++st == ST) st = 0, ph ^= 1;
+                        if (BMN) {
+                            pair_load(B, mb, col, kb * 64, sg.bp, full);
+                            pair_load(B + GOP / 2, mb, col + 64, kb * 64, sg.bp, full);
+                        } else {
+                            pair_load(B, mb, kb * KB, col, sg.bp, full);
+                        }
+                    }
+                    ++it;
+                    if (++st == ST) st = 0, ph ^= 1;
+                    if (++kb == g.kblocks && k + 1 < per_tile) {
+                        kb = 0;
+                        sg = g.seg[++s];
                     }
                 }
             }
@@ -716,7 +753,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(gemm_threads(KIND, E
                 if (!(ok = pair_wait(&bar.acc_full[ab][0], ch >> 1 & 1, g.err))) break;
                 tc::tc_fence_after();
                 const uint32_t acc = w.tmem + ab * 256, release = lead_addr(&bar.acc_empty[ab][0]);
-                if constexpr (EPI == kPlain) epi_plain(g, w, ring, tile, acc, release);
+                if constexpr (SPLIT) {
+#pragma unroll 1
+                    for (int c = 0; c < 256; c += 32) {
+                        uint32_t r[32];
+                        tmem_ld32(acc + c, r);
+                        tc::tmem_wait_ld();
+                        tmem_use(r);
+#pragma unroll
+                        for (int e = 0; e < 32; e += 4)
+                            *reinterpret_cast<uint4 *>(ops + ((c + e) / 4 * 128 + w.q * 32 + lane) * 16) = make_uint4(r[e], r[e + 1], r[e + 2], r[e + 3]);
+                    }
+                } else if constexpr (EPI == kPlain)
+                    epi_plain(g, w, ring, tile, acc, release);
                 if constexpr (EPI == kGate) epi_gate(g, w, ring, tile, acc, release);
                 if constexpr (EPI == kGateBwd) {
                     GemmTile next = {0, 0, -1};
@@ -740,9 +789,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(gemm_threads(KIND, E
                 if constexpr (E8) {
                     const int row = tile.row0 + rank * 128 + w.q * 32 + lane;
                     const int blk = tile.col0 / 128 + (EPI == kGate ? 0 : w.part);
-                    sa = row < g.M[tile.p] ? g.sa + (size_t)row * g.kblocks : nullptr;
+                    sa = row < g.M[tile.p] ? g.sa + (size_t)row * g.kblocks + kfirst : nullptr;
                     const bool in = blk * 128 < g.N[tile.p];
-                    sb0 = in ? g.sb[0] + (size_t)blk * g.kblocks : nullptr;
+                    sb0 = in ? g.sb[0] + (size_t)blk * g.kblocks + kfirst : nullptr;
                     if (EPI == kGate) sb1 = in ? g.sb[1] + (size_t)blk * g.kblocks : nullptr;
                     scales(0);
                 }
@@ -755,7 +804,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(gemm_threads(KIND, E
                 for (int k0 = 0, i = 0; k0 < per_tile; k0 += g.chunk, ++ch, ++i) {
                     const int ab = ch & 1;
                     const float m0 = E8 ? na * n0 : 1.f, m1 = E8 && EPI == kGate ? na * n1 : m0;
-                    if (E8 && i + 1 < g.kblocks) scales(i + 1);
+                    if (E8 && i + 1 < per_tile) scales(i + 1);
                     if (!(ok = pair_wait(&bar.acc_full[ab][HALVES == 1 ? 0 : w.half], ch >> 1 & 1, g.err))) break;
                     tc::tc_fence_after();
                     const uint32_t acc = w.tmem + ab * 256 + (HALVES == 1 ? 0 : w.half * 128);
@@ -778,7 +827,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(gemm_threads(KIND, E
                 if (!ok) break;
                 const GemmTile done = tile;
                 if (t + pairs < tiles) open(t + pairs);
-                if constexpr (E8 && EPI == kGate)
+                if constexpr (SPLIT) {
+#pragma unroll
+                    for (int e = 0; e < 64; e += 4)
+                        *reinterpret_cast<float4 *>(ops + ((w.part * 128 + w.half * 64 + e) / 4 * 128 + w.q * 32 + lane) * 16) =
+                            make_float4(x[e], x[e + 1], x[e + 2], x[e + 3]);
+                } else if constexpr (E8 && EPI == kGate)
                     ok = epi_gate_e4m3(g, w, done, x, uses++);
                 else
                     ok = epi_sums<EPI, E>(g, w, done, x, uses);
@@ -791,6 +845,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(gemm_threads(KIND, E
     __syncthreads();
     cluster_sync_all();
     tc::tc_fence_after();
+    if constexpr (SPLIT) {
+        if (warp >= E0) {
+            EpiWarp w = {};
+            w.lane = lane;
+            w.q = warp & 3;
+            w.rank = rank;
+            add_parts<EW, E>(g, w, tile_of(g, pair, COLS), ops, (warp - E0) >> 2, g.split);
+        }
+        __syncthreads();
+        cluster_sync_all();  // the other pairs have read this one's sums
+    }
     if (warp == 1) asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
 }
 
@@ -804,19 +869,50 @@ enum { kMapBf16 = 0, kMapF32 = 1, kMapBytes = 2 };
 ida_status gemm_map(CUtensorMap *m, const void *p, int type, long long inner, long long rows, int parts, long long ld, int box0,
                     int box1);
 
+// Pairs to a tile: four or two where so many clusters fit the SMs at once (15 of eight CTAs, 36 of four on 152) and
+// each part keeps eight blocks of the contraction.
+inline int split_of(long long tiles, int blocks, int num_sms) {
+    if (tiles * 10 <= num_sms && blocks >= 32) return 4;
+    if (tiles * 9 <= 2 * num_sms && blocks >= 16) return 2;
+    return 1;
+}
+
+template <int AMN, int BMN, int KIND, int EPI, typename E, bool SPLIT>
+ida_status gemm_launch_as(GemmArgs &g, int num_sms, cudaStream_t st) {
+    const auto kernel = gemm_kernel<AMN, BMN, KIND, EPI, E, SPLIT>;
+    constexpr int smem = gemm_smem(KIND, EPI);
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return fail_with(IDA_ERR_CUDA, cudaGetErrorString(e));
+    const long long pairs = SPLIT ? (long long)g.tiles * g.split : g.tiles < num_sms / 2 ? g.tiles : num_sms / 2;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(2 * pairs));
+    cfg.blockDim = dim3(gemm_threads(KIND, EPI));
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute at[2];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    at[1].id = cudaLaunchAttributeClusterDimension;
+    at[1].val.clusterDim.x = SPLIT ? 2 * g.split : 2;
+    at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 2;
+    e = cudaLaunchKernelEx(&cfg, kernel, g);
+    if (e != cudaSuccess) return fail_with(IDA_ERR_CUDA, std::string("matrix product launch: ") + cudaGetErrorString(e));
+    return launched("matrix product");
+}
+
 template <int AMN, int BMN, int KIND, int EPI, typename E>
 ida_status gemm_launch(GemmArgs &g, int num_sms, cudaStream_t st) {
-    const auto kernel = gemm_kernel<AMN, BMN, KIND, EPI, E>;
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, gemm_smem(KIND, EPI));
-    if (e != cudaSuccess) return fail_with(IDA_ERR_CUDA, cudaGetErrorString(e));
     const long long tiles = place_tiles(g, tile_cols(EPI));
     if (tiles > 0x7FFFFFFFLL) return fail_with(IDA_ERR_UNSUPPORTED, "too many tiles");
     g.tiles = (int)tiles;
     if (KIND == kDirect) g.chunk = g.segs * g.kblocks;
-    const long long pairs = tiles < num_sms / 2 ? tiles : num_sms / 2;
-    e = launch_dependent(kernel, dim3((unsigned)(2 * pairs)), dim3(gemm_threads(KIND, EPI)), gemm_smem(KIND, EPI), st, g);
-    if (e != cudaSuccess) return fail_with(IDA_ERR_CUDA, std::string("matrix product launch: ") + cudaGetErrorString(e));
-    return launched("matrix product");
+    if constexpr (EPI == kPlain && KIND != kParts) {
+        g.split = split_of(tiles, g.segs * g.kblocks, num_sms);
+        if (g.split > 1) return gemm_launch_as<AMN, BMN, KIND, EPI, E, true>(g, num_sms, st);
+    }
+    return gemm_launch_as<AMN, BMN, KIND, EPI, E, false>(g, num_sms, st);
 }
 
 // The products by operand layout (a_mn, b_mn: the contraction is the outer dimension in memory) and epilogue.

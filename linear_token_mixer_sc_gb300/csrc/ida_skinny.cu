@@ -39,7 +39,7 @@ __device__ __forceinline__ float remote_float(const float *p, int rank) {
 // block of 2048 and 5632 channels 16.9 us; 8 warps 19.5, of four rows 20.0), in e4m3 8.
 constexpr int skinny_warps(bool e8) { return e8 ? 8 : 16; }
 
-// NT: groups of 8 tokens.  SUB tiles of 16 weights' rows a block, of which a plain product may use 8 (HALVES
+// NT: groups of 8 rows of x (one in e4m3).  SUB tiles of 16 weights' rows a block, of which a plain product may use 8 (HALVES
 // 1).  GATE: rows 8 .. 15 of a tile are w1's.  E8 && GATE: a cluster of 8 blocks makes the 128 channels of
 // a scale.
 template <bool E8, int NT, int SUB, int HALVES, bool GATE>
@@ -173,36 +173,25 @@ __global__ void __launch_bounds__(skinny_warps(E8) * 32, E8 ? 1 : 2) skinny_kern
         }
     } else {
         // 16 channels of a row are 16 lanes'; the 8 blocks of a cluster have the 128 of a scale
-        __shared__ float top[8 * NT];
-        const int c = threadIdx.x & 15, rank = (int)cluster_rank();
-        float v[NT * 8 / 16 + (NT == 1)];
-#pragma unroll
-        for (int k = 0; k < NT * 8 / 16 + (NT == 1); ++k) {
-            const int tok = (threadIdx.x >> 4) + 16 * k;
-            v[k] = 0.f;
-            if (tok < a.T && n0 + c < a.N) {
-                const float x = sum(c / 8, c % 8, tok), y = sum(c / 8, 8 + c % 8, tok);
-                v[k] = x * sigmoid<__nv_bfloat16>(x) * y;
-            }
-            float m = fabsf(v[k]);
-#pragma unroll
-            for (int o = 8; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-            if (c == 0 && tok < 8 * NT) top[tok] = m;
+        __shared__ float top[8];
+        const int c = threadIdx.x & 15, tok = threadIdx.x >> 4;
+        float v = 0.f;
+        if (tok < a.T && n0 + c < a.N) {
+            const float x = sum(c / 8, c % 8, tok), y = sum(c / 8, 8 + c % 8, tok);
+            v = x * sigmoid<__nv_bfloat16>(x) * y;
         }
-        cluster_sync_all();
+        float m = fabsf(v);
 #pragma unroll
-        for (int k = 0; k < NT * 8 / 16 + (NT == 1); ++k) {
-            const int tok = (threadIdx.x >> 4) + 16 * k;
-            float m = 0.f;
-            if (tok < 8 * NT)
-                for (int r = 0; r < 8; ++r) m = fmaxf(m, remote_float(&top[tok], r));
+        for (int o = 8; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+        if (c == 0 && tok < 8) top[tok] = m;
+        cluster_sync_all();
+        if (tok < a.T) {
+            for (int r = 0; r < 8; ++r) m = fmaxf(m, remote_float(&top[tok], r));
             float up;
             const float sc = e4m3_scale(m, up), is = 1.f / (sc * up);
-            if (tok < a.T && n0 + c < a.N) {
-                const __nv_fp8_storage_t q = __nv_cvt_float_to_fp8(v[k] * up * is, __NV_SATFINITE, __NV_E4M3);
-                static_cast<uint8_t *>(a.out)[tok * (long long)a.N + n0 + c] = q;
-                if (rank == 0 && c == 0) a.so[(long long)tok * ((a.N + 127) / 128) + n0 / 128] = sc;
-            }
+            if (n0 + c < a.N)
+                static_cast<uint8_t *>(a.out)[tok * (long long)a.N + n0 + c] = __nv_cvt_float_to_fp8(v * up * is, __NV_SATFINITE, __NV_E4M3);
+            if (cluster_rank() == 0 && c == 0) a.so[(long long)tok * ((a.N + 127) / 128) + n0 / 128] = sc;
         }
         cluster_sync_all();  // the maxima have been read
     }
@@ -213,7 +202,7 @@ static ida_status launch_skinny(const SkinnyArgs &a, cudaStream_t st) {
     constexpr int cols = SUB * (GATE ? 8 : 8 * HALVES);
     const auto kernel = skinny_kernel<E8, NT, SUB, HALVES, GATE>;
     const long long chunks = ((long long)a.K * (E8 ? 1 : 2) + 127) / 128;
-    // the 8-bit gate's threads make 16 channels of 16 rows at a time
+    // the 8-bit gate's threads make 16 channels of up to 8 rows
     constexpr int most = skinny_warps(E8);
     const int warps = E8 && GATE ? most : chunks < most ? (int)chunks : most;
     const size_t smem = (size_t)warps * SUB * 16 * (8 * NT + 1) * sizeof(float);
@@ -238,20 +227,103 @@ static ida_status launch_skinny(const SkinnyArgs &a, cudaStream_t st) {
     return launched("few rows' product");
 }
 
-template <bool E8, int SUB, int HALVES, bool GATE>
-static ida_status launch_skinny_rows(const SkinnyArgs &a, cudaStream_t st) {
-    if (a.T <= 8) return launch_skinny<E8, 1, SUB, HALVES, GATE>(a, st);
-    if (a.T <= 16) return launch_skinny<E8, 2, SUB, HALVES, GATE>(a, st);
-    return launch_skinny<E8, 4, SUB, HALVES, GATE>(a, st);
+// fp32 on the CUDA cores: a block's warps share four rows of weights (two of either factor) and split the
+// contraction, a lane taking four of each 128; every lane has sums for all rows of x.
+template <int NT, bool GATE>
+__global__ void __launch_bounds__(256) skinny_f32_kernel(SkinnyArgs a) {
+    constexpr int U = 2;
+    __shared__ float red[8][4 * NT];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const long long n0 = (long long)blockIdx.x * (GATE ? 2 : 4);
+    const float *row[4];
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+        row[r] = static_cast<const float *>(GATE && r >= 2 ? a.w1 : a.w0) + (n0 + (GATE ? r & 1 : r)) * a.K + lane * 4;
+    const float *x = static_cast<const float *>(a.x) + lane * 4;
+    float acc[4][NT] = {};
+    float4 w[U][4];
+    auto fetch = [&](int k0) {
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const int k = k0 + u * 1024;
+                w[u][r] = k + lane * 4 < a.K ? __ldcs(reinterpret_cast<const float4 *>(row[r] + k)) : make_float4(0.f, 0.f, 0.f, 0.f);
+            }
+    };
+    if (!a.weights_ready) dependent_wait();
+    fetch(warp * 128);
+    if (a.weights_ready) dependent_wait();
+    for (int k0 = warp * 128; k0 < a.K; k0 += U * 1024) {
+        if (k0 != warp * 128) fetch(k0);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int k = k0 + u * 1024;
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
+                float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (t < a.T && k + lane * 4 < a.K) v = __ldg(reinterpret_cast<const float4 *>(x + t * a.ldx + k));
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+                    acc[r][t] = fmaf(w[u][r].w, v.w, fmaf(w[u][r].z, v.z, fmaf(w[u][r].y, v.y, fmaf(w[u][r].x, v.x, acc[r][t]))));
+            }
+        }
+    }
+    dependent_launch();
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+            const float v = warp_sum(acc[r][t]);
+            if (lane == 0) red[warp][r * NT + t] = v;
+        }
+    __syncthreads();
+    auto sum = [&](int i) {
+        float v = red[0][i];
+        for (int k = 1; k < 8; ++k) v += red[k][i];
+        return v;
+    };
+    constexpr int COLS = GATE ? 2 : 4;
+    const int t = threadIdx.x / COLS, c = threadIdx.x % COLS;
+    if (t >= a.T) return;
+    const long long at = t * (long long)a.N + n0 + c;
+    if (GATE) {
+        const float g = sum(c * NT + t), u = sum((2 + c) * NT + t);
+        static_cast<float *>(a.out)[at] = g * sigmoid<float>(g) * u;
+        if (a.out_g) {
+            static_cast<float *>(a.out_g)[at] = g;
+            static_cast<float *>(a.out_u)[at] = u;
+        }
+    } else {
+        static_cast<float *>(a.out)[at] = sum(c * NT + t);
+    }
 }
 
-ida_status skinny_product(const SkinnyArgs &a, bool e4m3, int num_sms, cudaStream_t st) {
-    // 16 rows of weights to a block where that leaves every SM two of them
-    if (a.N >= 32 * num_sms) return e4m3 ? launch_skinny_rows<true, 1, 2, false>(a, st) : launch_skinny_rows<false, 1, 2, false>(a, st);
-    return e4m3 ? launch_skinny_rows<true, 1, 1, false>(a, st) : launch_skinny_rows<false, 1, 1, false>(a, st);
+template <int NT, bool GATE>
+static ida_status launch_f32(const SkinnyArgs &a, cudaStream_t st) {
+    const cudaError_t e = launch_dependent(skinny_f32_kernel<NT, GATE>, dim3((unsigned)(a.N / (GATE ? 2 : 4))), dim3(256), 0, st, a);
+    if (e != cudaSuccess) return fail_with(IDA_ERR_CUDA, std::string("few rows' product launch: ") + cudaGetErrorString(e));
+    return launched("few rows' product");
 }
-ida_status skinny_gate(const SkinnyArgs &a, bool e4m3, cudaStream_t st) {
-    return e4m3 ? launch_skinny_rows<true, 2, 2, true>(a, st) : launch_skinny_rows<false, 1, 2, true>(a, st);
+template <bool GATE>
+static ida_status launch_f32_rows(const SkinnyArgs &a, cudaStream_t st) {
+    return a.T <= 2 ? launch_f32<2, GATE>(a, st) : launch_f32<8, GATE>(a, st);
+}
+
+template <int HALVES, bool GATE>
+static ida_status launch_bf16_rows(const SkinnyArgs &a, cudaStream_t st) {
+    return a.T <= 8 ? launch_skinny<false, 1, 1, HALVES, GATE>(a, st) : launch_skinny<false, 2, 1, HALVES, GATE>(a, st);
+}
+
+ida_status skinny_product(const SkinnyArgs &a, int type, int num_sms, cudaStream_t st) {
+    if (type == kFewF32) return launch_f32_rows<false>(a, st);
+    // 16 rows of weights to a block where that leaves every SM two of them
+    if (a.N >= 32 * num_sms) return type == kFewE4M3 ? launch_skinny<true, 1, 1, 2, false>(a, st) : launch_bf16_rows<2, false>(a, st);
+    return type == kFewE4M3 ? launch_skinny<true, 1, 1, 1, false>(a, st) : launch_bf16_rows<1, false>(a, st);
+}
+ida_status skinny_gate(const SkinnyArgs &a, int type, cudaStream_t st) {
+    if (type == kFewF32) return launch_f32_rows<true>(a, st);
+    return type == kFewE4M3 ? launch_skinny<true, 1, 2, 2, true>(a, st) : launch_bf16_rows<2, true>(a, st);
 }
 
 }  // namespace ida

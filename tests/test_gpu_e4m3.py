@@ -29,7 +29,8 @@ def _operand(T, K, block_rows, seed):
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("T,K,N", [(1, 16, 8), (1, 2048, 264), (5, 384, 136), (8, 128, 5000), (9, 2064, 136), (17, 400, 1000), (32, 5632, 72), (33, 128, 128), (128, 144, 256), (129, 256, 264), (300, 1040, 72),
-                                   (257, 640, 520), (700, 272, 1000)])
+                                   (257, 640, 520), (700, 272, 1000),
+                                   (33, 4112, 264), (300, 2064, 520), (500, 5632, 72), (1300, 4096, 600)])  # the last: contractions shared by pairs of SMs
 def test_product(T, K, N, dtype):
     a, sa = _operand(T, K, 1, 3)
     b, sb = _operand(N, K, 128, 5)
