@@ -97,12 +97,12 @@ __device__ __forceinline__ void arrive_remote(uint32_t addr) {
 __device__ __forceinline__ void arrive_local(uint64_t *bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(tc::smem_u32(bar)) : "memory");
 }
-// Waits of about a second at most; the role that gives up reports it and ends, and the others follow.
+// Waits of about two seconds at most; the role that gives up reports it and ends, and the others follow.
 __device__ __forceinline__ bool pair_wait(uint64_t *bar, uint32_t parity, unsigned *err) {
     if (tc::mbar_try_wait(bar, parity)) return true;
     const long long t0 = clock64();
     while (!tc::mbar_try_wait(bar, parity))
-        if (clock64() - t0 > 2000000000LL) {
+        if (clock64() - t0 > 4000000000LL) {
             report_error(err, kErrWaitTimeout);
             return false;
         }

@@ -12,6 +12,10 @@ import torch
 from tests.ssm_cases import DT, HALF, gen
 
 STEP = 2.0 ** -19
+# What lies below the types' least normal numbers (2^-126 in either) may be lost: the gate's sigmoid s, where 1 / s passes
+# 2^126 (its reciprocal is 0 from there on: an error of 2^-126 at most, times what it multiplies), a rounded value
+# and a product in a sum (2^-126 at most each).
+TINY = 2.0 ** -126
 E4M3 = torch.float8_e4m3fn
 
 
@@ -41,9 +45,9 @@ def forward_ref(x, wg, wu, wd, dtype):
     eg, eu = cd * (x.abs() @ wg.abs().t()), cd * (x.abs() @ wu.abs().t())
     s = g * torch.sigmoid(g)
     h = s * u
-    eh = 1.01 * (1.1 * u.abs() * eg + s.abs() * eu) + (STEP + half) * h.abs()  # |silu'| < 1.1
+    eh = 1.01 * (1.1 * u.abs() * eg + s.abs() * eu) + (STEP + half) * h.abs() + TINY * (1 + (g * u).abs())  # |silu'| < 1.1
     out = h @ wd.t()
-    eo = eh @ wd.abs().t() + sum_err(wg.shape[0], dtype) * (h.abs() @ wd.abs().t()) + half * out.abs()
+    eo = eh @ wd.abs().t() + sum_err(wg.shape[0], dtype) * (h.abs() @ wd.abs().t()) + half * out.abs() + TINY * (1 + wg.shape[0])
     return {"out": (out, eo), "g": (g, eg + half * g.abs()), "u": (u, eu + half * u.abs()), "h": (h, eh)}
 
 
@@ -57,15 +61,15 @@ def backward_ref(x, wg, wu, wd, acts, dy, dtype):
     dh = dy @ wd
     edh = sum_err(wd.shape[0], dtype) * (dy.abs() @ wd.abs())
     du, dg = dh * silu, dh * u * dsilu
-    edu = 1.01 * edh * silu.abs() + (half + STEP) * du.abs()
-    edg = 1.01 * edh * (u * dsilu).abs() + half * dg.abs() + STEP * (dh * u).abs() * (s + (g * s * (1 - s)).abs())
+    edu = 1.01 * edh * silu.abs() + (half + STEP) * du.abs() + TINY * (1 + (dh * g).abs())
+    edg = 1.01 * edh * (u * dsilu).abs() + half * dg.abs() + STEP * (dh * u).abs() * (s + (g * s * (1 - s)).abs()) + TINY * (1 + (dh * u).abs() * (1 + g.abs()))
     c2f, ct = sum_err(2 * F, dtype), sum_err(T, dtype)
     dx = dg @ wg + du @ wu
-    edx = edg @ wg.abs() + edu @ wu.abs() + c2f * (dg.abs() @ wg.abs() + du.abs() @ wu.abs()) + half * dx.abs()
+    edx = edg @ wg.abs() + edu @ wu.abs() + c2f * (dg.abs() @ wg.abs() + du.abs() @ wu.abs()) + half * dx.abs() + TINY * (1 + 2 * F)
     r = {"x": (dx, edx)}
     for name, a, ea, b in (("w_gate", dg, edg, x), ("w_up", du, edu, x), ("w_down", dy, None, h)):
         v = a.t() @ b
-        e = ct * (a.abs().t() @ b.abs()) + half * v.abs()
+        e = ct * (a.abs().t() @ b.abs()) + half * v.abs() + TINY * (1 + T)
         r[name] = (v, e if ea is None else e + ea.t() @ b.abs())
     return r
 
