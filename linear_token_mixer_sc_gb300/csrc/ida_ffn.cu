@@ -130,7 +130,7 @@ static FfnSpace ffn_space(long long T, int D, int F, int dtype, bool backward) {
         return at;
     };
     const size_t es = dtype == IDA_BF16 ? 2 : 4;
-    if (!backward) s.h = take(tf * es);
+    if (!backward) s.h = take(tf * (T <= few_rows(kFewBf16) ? 4 : es));  // (few rows' h is fp32)
     if (backward) s.dgu = take(2 * tf * es);
     if (dtype == IDA_F32) {
         s.xs = take(6 * td);
@@ -239,10 +239,11 @@ ida_status ida_ffn(const void *x, const void *w_gate, const void *w_up, const vo
     void *h = ac ? ac + 2 * tf * es : ws + sp.h;
     const int type = dtype == IDA_BF16 ? kFewBf16 : kFewF32;
     if (rows <= few_rows(type)) {
-        SkinnyArgs a = {x, ldx, w_gate, w_up, h, ac, ac ? ac + tf * es : nullptr, nullptr, nullptr, nullptr, nullptr, rows, D, F, dtype == IDA_F32, false};
+        // of few rows h stays in fp32, in the workspace
+        SkinnyArgs a = {x, ldx, w_gate, w_up, ws + sp.h, acts, nullptr, nullptr, nullptr, nullptr, rows, D, F, true, false};
         s = skinny_gate(a, type, st);
         if (s != IDA_OK) return s;
-        SkinnyArgs b = {h, F, w_down, nullptr, out, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr, rows, F, D, dtype == IDA_F32, true};
+        SkinnyArgs b = {ws + sp.h, F, w_down, nullptr, out, nullptr, nullptr, nullptr, nullptr, nullptr, rows, F, D, dtype == IDA_F32, true};
         return skinny_product(b, type, num_sms, st);
     }
     if (dtype == IDA_F32 && on_cuda_cores(rows, D, F)) {

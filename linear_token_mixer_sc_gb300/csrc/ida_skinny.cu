@@ -42,7 +42,10 @@ constexpr int skinny_warps(bool e8) { return e8 ? 8 : 16; }
 // NT: groups of 8 rows of x (one in e4m3).  SUB tiles of 16 weights' rows a block, of which a plain product may use 8 (HALVES
 // 1).  GATE: rows 8 .. 15 of a tile are w1's.  E8 && GATE: a cluster of 8 blocks makes the 128 channels of
 // a scale.
-template <bool E8, int NT, int SUB, int HALVES, bool GATE>
+// The gate's product in bf16 leaves its block in fp32; the product back takes it so, in two bf16 parts (WIDE), for two
+// instructions each on weights that are there anyway: of few rows the product's own rounding would be
+// seen in the result (one row's error 2.3e-3, now 1.7e-3 of its size, the output's rounding; 0.X us).
+template <bool E8, int NT, int SUB, int HALVES, bool GATE, bool WIDE>
 __global__ void __launch_bounds__(skinny_warps(E8) * 32, E8 ? 1 : 2) skinny_kernel(SkinnyArgs a) {
     constexpr int U = SUB * HALVES >= 2 ? 1 : 2, LD = 8 * NT + 1, ES = E8 ? 1 : 2;
     constexpr int COLS = SUB * (GATE ? 8 : 8 * HALVES);  // output columns of a block
@@ -95,7 +98,7 @@ __global__ void __launch_bounds__(skinny_warps(E8) * 32, E8 ? 1 : 2) skinny_kern
         for (int u = 0; u < U; ++u) {
             const int c = c0 + u * nw;
             if (c >= chunks) break;
-            uint4 x[NT][2];
+            uint4 x[NT][2], rest[NT][2];  // rest: x's second parts (WIDE)
             float m[NT][2];
 #pragma unroll
             for (int n = 0; n < NT; ++n)
@@ -103,9 +106,22 @@ __global__ void __launch_bounds__(skinny_warps(E8) * 32, E8 ? 1 : 2) skinny_kern
                 for (int j = 0; j < 2; ++j) {
                     const long long at = (long long)c * 128 + j * 64 + t * 16;
                     const int tok = 8 * n + g;
-                    x[n][j] = tok < a.T && at < kbytes
-                                  ? __ldg(reinterpret_cast<const uint4 *>(static_cast<const char *>(a.x) + tok * a.ldx * ES + at))
-                                  : make_uint4(0, 0, 0, 0);
+                    const bool in = tok < a.T && at < kbytes;
+                    const char *src = static_cast<const char *>(a.x) + (WIDE ? 2 : 1) * (tok * a.ldx * ES + at);
+                    if (WIDE) {
+                        float v[8] = {}, lo[8];
+                        if (in) {
+                            Vec16<float>::unpack(__ldg(reinterpret_cast<const uint4 *>(src)), v);
+                            Vec16<float>::unpack(__ldg(reinterpret_cast<const uint4 *>(src) + 1), v + 4);
+                        }
+                        x[n][j] = Vec16<__nv_bfloat16>::pack(v);
+                        Vec16<__nv_bfloat16>::unpack(x[n][j], lo);
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) lo[e] = v[e] - lo[e];
+                        rest[n][j] = Vec16<__nv_bfloat16>::pack(lo);
+                    } else {
+                        x[n][j] = in ? __ldg(reinterpret_cast<const uint4 *>(src)) : make_uint4(0, 0, 0, 0);
+                    }
                     if (E8) m[n][j] = 8 * n + 2 * t + j < a.T ? __ldg(a.sa + (long long)(8 * n + 2 * t + j) * chunks + c) : 0.f;
                 }
 #pragma unroll
@@ -125,6 +141,10 @@ __global__ void __launch_bounds__(skinny_warps(E8) * 32, E8 ? 1 : 2) skinny_kern
                         const uint4 lo = w[u][s][0][j], hi = HALVES == 2 ? w[u][s][HALVES - 1][j] : make_uint4(0, 0, 0, 0);
                         mma_rows(d, lo.x, hi.x, lo.y, hi.y, x[n][j].x, x[n][j].y, E8);
                         mma_rows(d, lo.z, hi.z, lo.w, hi.w, x[n][j].z, x[n][j].w, E8);
+                        if (WIDE) {
+                            mma_rows(d, lo.x, hi.x, lo.y, hi.y, rest[n][j].x, rest[n][j].y, E8);
+                            mma_rows(d, lo.z, hi.z, lo.w, hi.w, rest[n][j].z, rest[n][j].w, E8);
+                        }
                     }
                     if (E8) {
                         acc[s][n][0] = fmaf(part[0], m[n][0] * s0, acc[s][n][0]);
@@ -165,10 +185,13 @@ __global__ void __launch_bounds__(skinny_warps(E8) * 32, E8 ? 1 : 2) skinny_kern
             const int tok = i / COLS, c = i % COLS;
             const float x = sum(c / 8, c % 8, tok), y = sum(c / 8, 8 + c % 8, tok);
             const long long at = tok * a.N + n0 + c;
-            static_cast<__nv_bfloat16 *>(a.out)[at] = __float2bfloat16_rn(x * sigmoid<__nv_bfloat16>(x) * y);
-            if (a.out_g) {
-                static_cast<__nv_bfloat16 *>(a.out_g)[at] = __float2bfloat16_rn(x);
-                static_cast<__nv_bfloat16 *>(a.out_u)[at] = __float2bfloat16_rn(y);
+            const float h = x * sigmoid<__nv_bfloat16>(x) * y;
+            static_cast<float *>(a.out)[at] = h;
+            if (a.acts) {
+                const long long part = (long long)a.T * a.N;
+                static_cast<__nv_bfloat16 *>(a.acts)[at] = __float2bfloat16_rn(x);
+                static_cast<__nv_bfloat16 *>(a.acts)[at + part] = __float2bfloat16_rn(y);
+                static_cast<__nv_bfloat16 *>(a.acts)[at + 2 * part] = __float2bfloat16_rn(h);
             }
         }
     } else {
@@ -197,10 +220,10 @@ __global__ void __launch_bounds__(skinny_warps(E8) * 32, E8 ? 1 : 2) skinny_kern
     }
 }
 
-template <bool E8, int NT, int SUB, int HALVES, bool GATE>
+template <bool E8, int NT, int SUB, int HALVES, bool GATE, bool WIDE = !E8 && !GATE>
 static ida_status launch_skinny(const SkinnyArgs &a, cudaStream_t st) {
     constexpr int cols = SUB * (GATE ? 8 : 8 * HALVES);
-    const auto kernel = skinny_kernel<E8, NT, SUB, HALVES, GATE>;
+    const auto kernel = skinny_kernel<E8, NT, SUB, HALVES, GATE, WIDE>;
     const long long chunks = ((long long)a.K * (E8 ? 1 : 2) + 127) / 128;
     // the 8-bit gate's threads make 16 channels of up to 8 rows
     constexpr int most = skinny_warps(E8);
@@ -289,10 +312,13 @@ __global__ void __launch_bounds__(256) skinny_f32_kernel(SkinnyArgs a) {
     const long long at = t * (long long)a.N + n0 + c;
     if (GATE) {
         const float g = sum(c * NT + t), u = sum((2 + c) * NT + t);
-        static_cast<float *>(a.out)[at] = g * sigmoid<float>(g) * u;
-        if (a.out_g) {
-            static_cast<float *>(a.out_g)[at] = g;
-            static_cast<float *>(a.out_u)[at] = u;
+        const float h = g * sigmoid<float>(g) * u;
+        static_cast<float *>(a.out)[at] = h;
+        if (a.acts) {
+            const long long part = (long long)a.T * a.N;
+            static_cast<float *>(a.acts)[at] = g;
+            static_cast<float *>(a.acts)[at + part] = u;
+            static_cast<float *>(a.acts)[at + 2 * part] = h;
         }
     } else {
         static_cast<float *>(a.out)[at] = sum(c * NT + t);

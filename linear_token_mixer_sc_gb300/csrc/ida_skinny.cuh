@@ -13,10 +13,11 @@ constexpr int few_rows(int type) { return type == 0 ? 16 : 8; }
 enum { kFewBf16 = 0, kFewE4M3 = 1, kFewF32 = 2 };
 
 struct SkinnyArgs {
-    const void *x;                  // T rows of K channels, ldx elements apart
+    const void *x;                  // T rows of K channels, ldx elements apart (fp32 for a bf16 product: its block's h)
     long long ldx;
     const void *w0, *w1;            // [N, K]; w1: the gate's other factor
-    void *out, *out_g, *out_u;      // [T, N]; the factors where they are wanted
+    void *out;                      // [T, N]: a product in bf16 or fp32, the gate's in fp32 (e4m3: in e4m3)
+    void *acts;                     // gate: NULL, or [3, T, N]: both factors and their product
     const float *sa, *s0, *s1;      // e4m3: scales of x, w0 and w1
     float *so;                      // e4m3 gate: output scales
     int T, K, N;
