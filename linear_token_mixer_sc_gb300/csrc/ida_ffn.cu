@@ -154,8 +154,9 @@ static FfnSpace ffn_space(long long T, int D, int F, int dtype, bool backward) {
 static ida_status operand_map(CUtensorMap *m, const Operand &o, int mn) {
     return gemm_map(m, o.p, kMapBf16, o.cols, o.rows, o.parts, o.ld, 64, mn ? 64 : 128);
 }
-static ida_status out_map(CUtensorMap *m, const void *p, int dtype, long long rows, long long cols, int box = 0) {
-    return gemm_map(m, p, dtype == IDA_BF16 ? kMapBf16 : kMapF32, cols, rows, 1, cols, box ? box : dtype == IDA_BF16 ? 64 : 32, 32);
+// Boxes of 32 rows and columns of what the gate's gradients read and write
+static ida_status box_map(CUtensorMap *m, const void *p, int dtype, long long rows, long long cols) {
+    return gemm_map(m, p, dtype == IDA_BF16 ? kMapBf16 : kMapF32, cols, rows, 1, cols, 32, 32);
 }
 
 // Passes over the contraction for operands a and b: one in bf16, the six products of parts otherwise, the
@@ -278,9 +279,7 @@ ida_status ida_ffn(const void *x, const void *w_gate, const void *w_up, const vo
     s = operand_map(&g.a[0], X, 0);
     if (s == IDA_OK) s = operand_map(&g.b[0], Wg, 0);
     if (s == IDA_OK) s = operand_map(&g.b[1], Wu, 0);
-    if (s == IDA_OK) s = out_map(&g.o[0], h, dtype, rows, F);
-    if (s == IDA_OK && ac) s = out_map(&g.o[1], ac, dtype, rows, F);
-    if (s == IDA_OK && ac) s = out_map(&g.o[2], ac + tf * es, dtype, rows, F);
+    g.out[0] = h, g.out[1] = ac, g.out[2] = ac ? ac + tf * es : nullptr;
     if (s == IDA_OK) s = run_gemm(0, 0, kGate, g, dtype, num_sms, st);
     if (s != IDA_OK) return s;
     if (dtype == IDA_F32) {
@@ -296,7 +295,6 @@ ida_status ida_ffn(const void *x, const void *w_gate, const void *w_up, const vo
     s = operand_map(&d.a[0], H, 0);
     if (s == IDA_OK) s = operand_map(&d.b[0], Wd, 0);
     d.out[0] = out;
-    if (s == IDA_OK) s = out_map(&d.o[0], out, dtype, rows, D);
     if (s == IDA_OK) s = run_gemm(0, 0, kPlain, d, dtype, num_sms, st);
     return s;
 }
@@ -386,10 +384,10 @@ ida_status ida_ffn_backward(const void *x, const void *w_gate, const void *w_up,
     add_segments(g, dtype, 0, 0);
     s = operand_map(&g.a[0], dY, 0);
     if (s == IDA_OK) s = operand_map(&g.b[0], Wd, 1);
-    if (s == IDA_OK) s = out_map(&g.e[0], ac, dtype, rows, F, 32);
-    if (s == IDA_OK) s = out_map(&g.e[1], ac + tf * es, dtype, rows, F, 32);
-    if (s == IDA_OK) s = out_map(&g.o[0], dg, dtype, rows, F, 32);
-    if (s == IDA_OK) s = out_map(&g.o[1], du, dtype, rows, F, 32);
+    if (s == IDA_OK) s = box_map(&g.e[0], ac, dtype, rows, F);
+    if (s == IDA_OK) s = box_map(&g.e[1], ac + tf * es, dtype, rows, F);
+    if (s == IDA_OK) s = box_map(&g.o[0], dg, dtype, rows, F);
+    if (s == IDA_OK) s = box_map(&g.o[1], du, dtype, rows, F);
     if (s == IDA_OK) s = run_gemm(0, 1, kGateBwd, g, dtype, num_sms, st);
     if (s != IDA_OK) return s;
     if (dtype == IDA_F32) {
@@ -409,7 +407,6 @@ ida_status ida_ffn_backward(const void *x, const void *w_gate, const void *w_up,
         w.out[p] = dw[p];
         if (s == IDA_OK) s = operand_map(&w.a[p], *wa[p], 1);
         if (s == IDA_OK) s = operand_map(&w.b[p], *wb[p], 1);
-        if (s == IDA_OK) s = out_map(&w.o[p], dw[p], dtype, w.M[p], w.N[p]);
     }
     if (s == IDA_OK) s = run_gemm(1, 1, kPlain, w, dtype, num_sms, st);
     if (s != IDA_OK) return s;
@@ -424,7 +421,6 @@ ida_status ida_ffn_backward(const void *x, const void *w_gate, const void *w_up,
     if (s == IDA_OK) s = operand_map(&d.b[0], Wg, 1);
     if (s == IDA_OK) s = operand_map(&d.b[1], Wu, 1);
     d.out[0] = dx;
-    if (s == IDA_OK) s = out_map(&d.o[0], dx, dtype, rows, D);
     if (s == IDA_OK) s = run_gemm(0, 1, kPlain, d, dtype, num_sms, st);
     return s;
 }

@@ -24,16 +24,26 @@ namespace ida {
 
 enum { kDirect = 0, kParts = 1, kE4M3 = 2 };          // operands: bf16, three bf16 parts of fp32, e4m3
 enum { kPlain = 0, kGate = 1, kGateBwd = 2 };         // epilogues
-constexpr int GST = 5;                                // stages at most
 constexpr int GOP = 128 * 128;                        // bytes of an operand of a stage
 constexpr int GSLAB = 32 * 128;                       // bytes of a warp's staged box: 32 rows of 128 bytes
-constexpr int GSTAGING = 64 * 1024;                   // of all epilogue warps
+// Halves of the accumulator that are filled and emptied by themselves: two for fp32's parts.  In e4m3 each MMA
+// of half the columns would read A again, and shared memory cannot feed that (14336 rows' gated projection 307
+// us, 280 with whole ones).
 constexpr int gemm_halves(int kind) { return kind == kParts ? 2 : 1; }
-// The gradients of the gate in fp32 stage two boxes for each of sixteen warps, and take two stages less.
-constexpr int gemm_stages(int kind, int epi) { return kind == kParts && epi == kGateBwd ? 3 : GST; }
-constexpr int gemm_staging(int kind, int epi) { return kind == kParts && epi == kGateBwd ? 2 * GSTAGING : GSTAGING; }
+// Warps of the epilogue.  The direct kind's four are enough, but where the gate's gradients read and write boxes
+// (16384 rows of 768 and 2048 channels 61 us with four, 55 with eight; the other epilogues lose 3 % by eight).
+constexpr int gemm_warps(int kind, int epi) { return kind != kDirect ? 16 : epi == kPlain ? 4 : 8; }
+constexpr int gemm_threads(int kind, int epi) { return (kind == kDirect ? 64 : 128) + 32 * gemm_warps(kind, epi); }
+// Boxes that a warp stages, and the stages that shared memory has left for operands
+constexpr int gemm_boxes(int epi) { return epi == kGateBwd ? 2 : 1; }
+constexpr int gemm_staging(int kind, int epi) { return gemm_warps(kind, epi) * gemm_boxes(epi) * GSLAB; }
+constexpr int gemm_stages(int kind, int epi) {
+    const int n = (227 * 1024 - 1024 - 512 - gemm_staging(kind, epi)) / (2 * GOP);
+    return n < 6 ? n : 6;
+}
 constexpr int gemm_smem(int kind, int epi) { return gemm_stages(kind, epi) * 2 * GOP + gemm_staging(kind, epi) + 1024 + 512; }
-static_assert(gemm_smem(kDirect, kPlain) <= 227 * 1024 && gemm_smem(kParts, kGateBwd) <= 227 * 1024, "shared memory budget");
+constexpr int GST = 6;                                // stages at most
+constexpr int GSTAGING = 16 * GSLAB;                  // of sixteen warps with a box each
 
 struct GemmSeg {
     unsigned char a, ap, b, bp;  // maps and parts of one pass over the contraction
@@ -53,11 +63,11 @@ inline Divisor divisor(unsigned d) {
 __device__ __forceinline__ int divide(int n, const Divisor &d) { return (int)((__umulhi(d.m, (unsigned)n) + (unsigned)n) >> d.s); }
 
 struct GemmArgs {
-    CUtensorMap a[3], b[3], o[3], e[2];  // operands, outputs, what the epilogue reads
+    CUtensorMap a[3], b[3], o[2], e[2];  // operands; boxes that the epilogue writes and reads
     int M[3], N[3];                      // rows and columns of each problem's output
     int tiles, bands[3], count[3];       // of the launch; whole bands of 8 rows of tiles, and tiles, of each problem
     Divisor band[3], last[3];            // tiles of such a band, rows of tiles of the last one (1 if there is none)
-    void *out[3];                        // of split products, which store by themselves
+    void *out[3];                        // outputs: of each problem; kGate: the product and its factors
     int split;                           // pairs that share a tile's contraction
     int problems, segs, kblocks, chunk;  // kblocks: blocks of 128 bytes along each segment's contraction
     GemmSeg seg[12];
@@ -245,30 +255,7 @@ inline long long place_tiles(GemmArgs &g, int cols) {
     return n;
 }
 
-// ---- the epilogue's staging: a warp's ring of boxes of 32 rows x 128 bytes ----------------------
-
-template <int SLOTS>
-struct Ring {
-    char *base;
-    int lane, next;
-    // a box that no store still reads; `taken`: boxes taken and not yet put
-    template <int TAKEN = 0>
-    __device__ __forceinline__ char *take() {
-        if (lane == 0) bulk_wait_read<SLOTS - 1 - TAKEN>();
-        __syncwarp();
-        char *s = base + next * GSLAB;
-        next = next + 1 == SLOTS ? 0 : next + 1;
-        return s;
-    }
-    __device__ __forceinline__ void put(const char *slab, const void *map, int c0, int c1, int c2, bool inside) {
-        tc::fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) {
-            if (inside) store_3d(map, c0, c1, c2, slab);
-            tc::bulk_commit();
-        }
-    }
-};
+// ---- the epilogue's staging: a warp's box of 32 rows x 128 bytes ------------------------------
 
 // 8 (bf16) or 4 (fp32) values to 16 bytes of a staged box
 template <typename E>
@@ -276,12 +263,41 @@ __device__ __forceinline__ void stage(char *slab, int row, int piece, const floa
     *reinterpret_cast<uint4 *>(slab + swz128(row, piece)) = Vec16<E>::pack(x);
 }
 
-// ---- the kernel ------------------------------------------------------------------------------
+// A warp's staged box to rows row .. and columns col .. of out [M, N], 128 bytes of four rows at a time; what lies
+// outside is not written.  Plain stores: the TMA moves some 64 bytes a clock for an SM, what the MMAs' operands
+// take already, and boxes stored by it held loads back (16384 rows of 768 channels, both factors kept, 68 us, now
+// XXX; projected back 38, now XXX).
+template <typename E>
+__device__ __forceinline__ void store_box(const char *slab, void *out, int M, int N, int row, int col, int lane) {
+    constexpr int PER = 16 / (int)sizeof(E);
+    const int r = lane >> 3, p = lane & 7;
+    E *to = static_cast<E *>(out) + (long long)(row + r) * N + col + p * PER;
+    __syncwarp();
+    if (col + p * PER < N) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (row + r + 4 * i < M)
+                __stcs(reinterpret_cast<uint4 *>(to + (long long)(4 * i) * N), *reinterpret_cast<const uint4 *>(slab + swz128(r + 4 * i, p)));
+    }
+    __syncwarp();  // the box may be filled again
+}
 
-// Warps of the epilogue.  The direct kind's four are enough, but where the gate's gradients read and write boxes
-// (16384 rows of 768 and 2048 channels 61 us with four, 55 with eight; the other epilogues lose 3 % by eight).
-constexpr int gemm_warps(int kind, int epi) { return kind != kDirect ? 16 : epi == kGateBwd ? 8 : 4; }
-constexpr int gemm_threads(int kind, int epi) { return (kind == kDirect ? 64 : 128) + 32 * gemm_warps(kind, epi); }
+// A warp's staged box by the TMA: fewer instructions, which counts in e4m3, where the MMAs wait for a tile's end (by
+// plain stores the 8-bit product 66 us and the gated projection 300, by the TMA 61 and 278).
+__device__ __forceinline__ void box_ready(int lane) {  // no box is being read
+    if (lane == 0) bulk_wait_read<0>();
+    __syncwarp();
+}
+__device__ __forceinline__ void send_box(const char *slab, const void *map, bool inside, int row, int col, int lane) {
+    tc::fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0 && inside) {
+        store_3d(map, col, row, 0, slab);
+        tc::bulk_commit();
+    }
+}
+
+// ---- the kernel ------------------------------------------------------------------------------
 
 struct GemmBars {
     uint64_t full[GST], empty[GST], acc_full[2][2], acc_empty[2][2], in[16][2];
@@ -305,10 +321,8 @@ __device__ __forceinline__ void release_acc(const EpiWarp &w, uint32_t release) 
 }
 
 // Direct kind, kPlain: 256 columns in bf16.
-__device__ __forceinline__ void epi_plain(const GemmArgs &g, const EpiWarp &w, Ring<4> &ring, const GemmTile &t, uint32_t acc,
-                                          uint32_t release) {
+__device__ __forceinline__ void epi_plain(const GemmArgs &g, const EpiWarp &w, const GemmTile &t, uint32_t acc, uint32_t release) {
     const int row = t.row0 + w.rank * 128 + w.q * 32;
-    char *slab = nullptr;
 #pragma unroll
     for (int c = 0; c < 8; ++c) {
         uint32_t r[32];
@@ -316,55 +330,40 @@ __device__ __forceinline__ void epi_plain(const GemmArgs &g, const EpiWarp &w, R
         tc::tmem_wait_ld();
         tmem_use(r);
         if (c == 7) release_acc(w, release);
-        if (c % 2 == 0) slab = ring.take();
 #pragma unroll
-        for (int k = 0; k < 4; ++k) stage<__nv_bfloat16>(slab, w.lane, c % 2 * 4 + k, reinterpret_cast<const float *>(r) + 8 * k);
-        if (c % 2) ring.put(slab, &g.o[t.p], t.col0 + c / 2 * 64, row, 0, row < g.M[t.p] && t.col0 + c / 2 * 64 < g.N[t.p]);
+        for (int k = 0; k < 4; ++k) stage<__nv_bfloat16>(w.staging, w.lane, c % 2 * 4 + k, reinterpret_cast<const float *>(r) + 8 * k);
+        if (c % 2) store_box<__nv_bfloat16>(w.staging, g.out[t.p], g.M[t.p], g.N[t.p], row, t.col0 + c / 2 * 64, w.lane);
     }
 }
 
-// Direct kind, kGate: columns c and 128 + c are the factors of the product's column c.
-__device__ __forceinline__ void epi_gate(const GemmArgs &g, const EpiWarp &w, Ring<4> &ring, const GemmTile &t, uint32_t acc,
-                                         uint32_t release) {
+// Direct kind, kGate: columns c and 128 + c are the factors of the product's column c; 64 of them a warp.
+__device__ __forceinline__ void epi_gate(const GemmArgs &g, const EpiWarp &w, const GemmTile &t, uint32_t acc, uint32_t release) {
     using E = __nv_bfloat16;
-    const int row = t.row0 + w.rank * 128 + w.q * 32;
+    const int row = t.row0 + w.rank * 128 + w.q * 32, col = t.col0 + w.half * 64;
+    uint32_t r[4][32];  // 64 of either factor
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-        char *sh = ring.take<0>(), *sg = nullptr, *su = nullptr;
-        if (g.keep) {
-            sg = ring.take<1>();
-            su = ring.take<2>();
-        }
+    for (int c = 0; c < 4; ++c) tmem_ld32(acc + w.half * 64 + c / 2 * 128 + c % 2 * 32, r[c]);
+    tc::tmem_wait_ld();
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-            uint32_t rg[32], ru[32];
-            tmem_ld32(acc + j * 64 + c * 32, rg);
-            tmem_ld32(acc + 128 + j * 64 + c * 32, ru);
-            tc::tmem_wait_ld();
-            tmem_use(rg);
-            tmem_use(ru);
-            if (j == 1 && c == 1) release_acc(w, release);
-            const float *xg = reinterpret_cast<const float *>(rg), *xu = reinterpret_cast<const float *>(ru);
+    for (int c = 0; c < 4; ++c) tmem_use(r[c]);
+    release_acc(w, release);
+    if (g.keep) {
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                float h[8];
+        for (int f = 0; f < 2; ++f) {
 #pragma unroll
-                for (int e = 0; e < 8; ++e) h[e] = xg[8 * k + e] * sigmoid<E>(xg[8 * k + e]) * xu[8 * k + e];
-                stage<E>(sh, w.lane, c * 4 + k, h);
-                if (g.keep) {
-                    stage<E>(sg, w.lane, c * 4 + k, xg + 8 * k);
-                    stage<E>(su, w.lane, c * 4 + k, xu + 8 * k);
-                }
-            }
-        }
-        const int col = t.col0 + j * 64;
-        const bool inside = row < g.M[0] && col < g.N[0];
-        ring.put(sh, &g.o[0], col, row, 0, inside);
-        if (g.keep) {
-            ring.put(sg, &g.o[1], col, row, 0, inside);
-            ring.put(su, &g.o[2], col, row, 0, inside);
+            for (int k = 0; k < 8; ++k) stage<E>(w.staging, w.lane, k, reinterpret_cast<const float *>(r[2 * f + k / 4]) + k % 4 * 8);
+            store_box<E>(w.staging, g.out[1 + f], g.M[0], g.N[0], row, col, w.lane);
         }
     }
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+        const float *xg = reinterpret_cast<const float *>(r[k / 4]) + k % 4 * 8, *xu = reinterpret_cast<const float *>(r[2 + k / 4]) + k % 4 * 8;
+        float h[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) h[e] = xg[e] * sigmoid<E>(xg[e]) * xu[e];
+        stage<E>(w.staging, w.lane, k, h);
+    }
+    store_box<E>(w.staging, g.out[0], g.M[0], g.N[0], row, col, w.lane);
 }
 
 // d/dg and d/du of silu(g) u, given the product's gradient
@@ -445,39 +444,38 @@ __device__ __forceinline__ int sum_col(const EpiWarp &w, int c) {  // TMEM colum
     return EPI == kGate ? w.part * 32 + c / 2 * 64 + c % 2 * 16 : w.part * 64 + c * 16;
 }
 
-template <int EPI, typename E>
+template <int KIND, int EPI, typename E>
 __device__ __forceinline__ bool epi_sums(const GemmArgs &g, const EpiWarp &w, const GemmTile &t, float (&x)[64], int &uses) {
     constexpr int BOX = 128 / (int)sizeof(E), PER = 16 / (int)sizeof(E);  // columns of a box, of a piece
     const int row = t.row0 + w.rank * 128 + w.q * 32;
-    Ring<1> ring = {w.staging, w.lane, 0};
     if constexpr (EPI == kPlain) {
         const int col = t.col0 + w.part * 128 + w.half * 64;
 #pragma unroll
         for (int j = 0; j < 64 / BOX; ++j) {
-            char *slab = ring.take();
+            if (KIND == kE4M3) box_ready(w.lane);
 #pragma unroll
-            for (int k = 0; k < 8; ++k) stage<E>(slab, w.lane, k, x + j * BOX + k * PER);
-            ring.put(slab, &g.o[t.p], col + j * BOX, row, 0, row < g.M[t.p] && col + j * BOX < g.N[t.p]);
+            for (int k = 0; k < 8; ++k) stage<E>(w.staging, w.lane, k, x + j * BOX + k * PER);
+            if (KIND == kE4M3)
+                send_box(w.staging, &g.o[0], row < g.M[0] && col + j * BOX < g.N[0], row, col + j * BOX, w.lane);
+            else
+                store_box<E>(w.staging, g.out[t.p], g.M[t.p], g.N[t.p], row, col + j * BOX, w.lane);
         }
     } else if constexpr (EPI == kGate) {
         static_assert(BOX == 32, "fp32");
         const int col = t.col0 + w.half * 64 + w.part * 32;
-        const bool inside = row < g.M[0] && col < g.N[0];
         if (g.keep) {
 #pragma unroll
             for (int f = 0; f < 2; ++f) {
-                char *slab = ring.take();
 #pragma unroll
-                for (int k = 0; k < 8; ++k) stage<E>(slab, w.lane, k, x + f * 32 + k * PER);
-                ring.put(slab, &g.o[1 + f], col, row, 0, inside);
+                for (int k = 0; k < 8; ++k) stage<E>(w.staging, w.lane, k, x + f * 32 + k * PER);
+                store_box<E>(w.staging, g.out[1 + f], g.M[0], g.N[0], row, col, w.lane);
             }
         }
 #pragma unroll
         for (int e = 0; e < 32; ++e) x[e] = x[e] * sigmoid<E>(x[e]) * x[32 + e];
-        char *slab = ring.take();
 #pragma unroll
-        for (int k = 0; k < 8; ++k) stage<E>(slab, w.lane, k, x + k * PER);
-        ring.put(slab, &g.o[0], col, row, 0, inside);
+        for (int k = 0; k < 8; ++k) stage<E>(w.staging, w.lane, k, x + k * PER);
+        store_box<E>(w.staging, g.out[0], g.M[0], g.N[0], row, col, w.lane);
     } else {
         const int col = t.col0 + w.part * 128 + w.half * 64;
         char *sg = w.staging, *su = sg + GSLAB;
@@ -543,8 +541,8 @@ __device__ __forceinline__ bool epi_gate_e4m3(const GemmArgs &g, const EpiWarp &
         x[e] = x[e] * sigmoid<__nv_bfloat16>(x[e]) * x[32 + e];
         top = fmaxf(top, fabsf(x[e]));
     }
-    Ring<1> ring = {w.staging, w.lane, 0};
-    char *slab = ring.take();
+    char *slab = w.staging;
+    box_ready(w.lane);
     const int at = GSLAB / 2 + (n & 1) * 128, own = w.half * 2 + w.part;
     reinterpret_cast<float *>(slab + at)[w.lane] = top;
     __syncwarp();
@@ -570,7 +568,7 @@ __device__ __forceinline__ bool epi_gate_e4m3(const GemmArgs &g, const EpiWarp &
         }
         *reinterpret_cast<uint4 *>(slab + w.lane * 32 + ((k ^ (w.lane >> 2 & 1)) << 4)) = make_uint4(v[0], v[1], v[2], v[3]);
     }
-    ring.put(slab, &g.o[0], col, row, 0, row < g.M[0] && col < g.N[0]);
+    send_box(slab, &g.o[0], row < g.M[0] && col < g.N[0], row, col, w.lane);
     if (own == 0 && row + w.lane < g.M[0]) g.so[(size_t)(row + w.lane) * ((g.N[0] + 127) / 128) + t.col0 / 128] = sc;
     return true;
 }
@@ -744,7 +742,6 @@ __global__ void __launch_bounds__(gemm_threads(KIND, EPI), 1) gemm_kernel(const 
         int ch = 0;
         bool ok = true;
         if constexpr (KIND == kDirect) {
-            Ring<4> ring = {w.staging, lane, 0};
             GateBwd back = {{0, 0}};
             if (EPI == kGateBwd && pair < tiles) GateBwd::ask(g, w, tile_of(g, pair, COLS), 0, 0);
             for (int t = pair; ok && t < tiles; t += pairs, ++ch) {
@@ -765,8 +762,8 @@ __global__ void __launch_bounds__(gemm_threads(KIND, EPI), 1) gemm_kernel(const 
                             *reinterpret_cast<uint4 *>(ops + ((c + e) / 4 * 128 + w.q * 32 + lane) * 16) = make_uint4(r[e], r[e + 1], r[e + 2], r[e + 3]);
                     }
                 } else if constexpr (EPI == kPlain)
-                    epi_plain(g, w, ring, tile, acc, release);
-                if constexpr (EPI == kGate) epi_gate(g, w, ring, tile, acc, release);
+                    epi_plain(g, w, tile, acc, release);
+                if constexpr (EPI == kGate) epi_gate(g, w, tile, acc, release);
                 if constexpr (EPI == kGateBwd) {
                     GemmTile next = {0, 0, -1};
                     if (t + pairs < tiles) next = tile_of(g, t + pairs, COLS);
@@ -835,10 +832,10 @@ __global__ void __launch_bounds__(gemm_threads(KIND, EPI), 1) gemm_kernel(const 
                 } else if constexpr (E8 && EPI == kGate)
                     ok = epi_gate_e4m3(g, w, done, x, uses++);
                 else
-                    ok = epi_sums<EPI, E>(g, w, done, x, uses);
+                    ok = epi_sums<KIND, EPI, E>(g, w, done, x, uses);
             }
         }
-        if (lane == 0) bulk_wait_read<0>();  // staging is read until then
+        if ((EPI == kGateBwd || E8) && lane == 0) bulk_wait_read<0>();  // staging is read until then
         __syncwarp();
     }
     tc::tc_fence_before();
