@@ -762,6 +762,9 @@ def ida_ffn_backward_workspace_bytes(rows: int, D: int, F: int, dtype: int) -> i
     return int(load().ida_ffn_backward_workspace_bytes(rows, D, F, dtype))
 
 
+_INT = 0x7FFFFFFF
+
+
 def _leading(name: str, t: torch.Tensor, dev: int):
     """(address, row stride, rows) of a tensor of rows: any leading dimensions where it is dense, one or
     two at one stride where it is a slice of wider rows."""
@@ -781,7 +784,8 @@ def _ffn_inputs(x, w_gate, w_up, w_down):
     xp, ldx, rows = _leading("x", x, dev)
     if x.shape[-1] != D:
         raise ValueError(f"x must have rows of {D} channels, got {x.shape[-1]}")
-    _fits(rows, D, F)
+    if rows > _INT or D > _INT or F > _INT:
+        _fits(rows, D, F)
     ptrs = [xp, _dense("w_gate", w_gate, (F, D), x.dtype, dev), _dense("w_up", w_up, (F, D), x.dtype, dev),
             _dense("w_down", w_down, (D, F), x.dtype, dev)]
     return dev, ptrs, ldx, (rows, D, F)
@@ -799,17 +803,21 @@ def ida_ffn(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor, w_down: t
     code = _dtype_code(x)
     dev, ptrs, ldx, sizes = _ffn_inputs(x, w_gate, w_up, w_down)
     rows, D, F = sizes
-    shape = (3, *x.shape[:-1], F)
+    # (what is allocated here needs none of the checks)
+    op = ap = None
     if out is None:
         out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    else:
+        op = _dense("out", out, x.shape, x.dtype, dev)
     if acts is True:
-        acts = torch.empty(shape, dtype=x.dtype, device=x.device)
-    elif acts is False:
+        acts = torch.empty((3, *x.shape[:-1], F), dtype=x.dtype, device=x.device)
+        ap = acts.data_ptr()
+    elif acts is None or acts is False:
         acts = None
+    else:
+        ap = _dense("acts", acts, (3, *x.shape[:-1], F), x.dtype, dev)
     ws, wsp, n = _work_buffer(workspace, ida_ffn_workspace_bytes(rows, D, F, code) if workspace is None else 0, dev)
-    st = (_lib or load()).ida_ffn(*ptrs, _dense("out", out, x.shape, x.dtype, dev),
-                   None if acts is None else _dense("acts", acts, shape, x.dtype, dev), *sizes, ldx, code, wsp, n,
-                   _raw_stream(dev))
+    st = (_lib or load()).ida_ffn(*ptrs, op or out.data_ptr(), ap, *sizes, ldx, code, wsp, n, _raw_stream(dev))
     _check(st, "ida_ffn")
     return out, acts
 
@@ -827,11 +835,13 @@ def ida_ffn_backward(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor, 
     rows, D, F = sizes
     ap = _dense("acts", acts, (3, *x.shape[:-1], F), x.dtype, dev)
     dp = _dense("dout", dout, x.shape, x.dtype, dev)
-    g = grads if grads is not None else {
-        k: torch.empty(t.shape, dtype=x.dtype, device=x.device)
-        for k, t in (("x", x), ("w_gate", w_gate), ("w_up", w_up), ("w_down", w_down))}
-    gp = [_dense(f"grads[{k!r}]", g[k], t.shape, x.dtype, dev)
-          for k, t in (("x", x), ("w_gate", w_gate), ("w_up", w_up), ("w_down", w_down))]
+    like = (("x", x), ("w_gate", w_gate), ("w_up", w_up), ("w_down", w_down))
+    if grads is None:
+        g = {k: torch.empty(t.shape, dtype=x.dtype, device=x.device) for k, t in like}
+        gp = [t.data_ptr() for t in g.values()]
+    else:
+        g = grads
+        gp = [_dense(f"grads[{k!r}]", g[k], t.shape, x.dtype, dev) for k, t in like]
     ws, wsp, n = _work_buffer(workspace, ida_ffn_backward_workspace_bytes(rows, D, F, code)
                               if workspace is None else 0, dev)
     st = (_lib or load()).ida_ffn_backward(*ptrs, ap, dp, *gp, *sizes, ldx, code, wsp, n, _raw_stream(dev))
@@ -857,12 +867,16 @@ def ida_quant_e4m3(x: torch.Tensor, rows: int = 1, q: torch.Tensor | None = None
     _fits(n, K, rows)
     lead = x.shape[:-1] if rows == 1 else ((n + 127) // 128,)
     shape = (*lead, (K + 127) // 128)
+    qp = sp = None
     if q is None:
         q = torch.empty(x.shape, dtype=_E4M3, device=x.device)
+    else:
+        qp = _dense("q", q, x.shape, _E4M3, dev)
     if scale is None:
         scale = torch.empty(shape, dtype=torch.float32, device=x.device)
-    st = (_lib or load()).ida_quant_e4m3(xp, _dense("q", q, x.shape, _E4M3, dev),
-                                         _dense("scale", scale, shape, torch.float32, dev), n, K, rows, ldx, code,
+    else:
+        sp = _dense("scale", scale, shape, torch.float32, dev)
+    st = (_lib or load()).ida_quant_e4m3(xp, qp or q.data_ptr(), sp or scale.data_ptr(), n, K, rows, ldx, code,
                                          _raw_stream(dev))
     _check(st, "ida_quant_e4m3")
     return q, scale
@@ -879,16 +893,18 @@ def ida_gemm_e4m3(a: torch.Tensor, a_scale: torch.Tensor, b: torch.Tensor, b_sca
     K, lead = a.shape[-1], a.shape[:-1]
     N, kb = b.shape[0], (K + 127) // 128
     rows = a.numel() // K if K else 0
-    _fits(rows, K, N)
+    if rows > _INT or K > _INT or N > _INT:
+        _fits(rows, K, N)
     f32 = torch.float32
     ptrs = (_dense("a", a, a.shape, _E4M3, dev), _dense("a_scale", a_scale, (*lead, kb), f32, dev),
             _dense("b", b, (N, K), _E4M3, dev), _dense("b_scale", b_scale, ((N + 127) // 128, kb), f32, dev))
-    shape = (*lead, N)
+    op = None
     if out is None:
-        out = torch.empty(shape, dtype=dtype, device=a.device)
+        out = torch.empty((*lead, N), dtype=dtype, device=a.device)
+    else:
+        op = _dense("out", out, (*lead, N), out.dtype, dev)
     code = _dtype_code(out)
-    st = (_lib or load()).ida_gemm_e4m3(*ptrs, _dense("out", out, shape, out.dtype, dev), rows, K, N, code,
-                                        _raw_stream(dev))
+    st = (_lib or load()).ida_gemm_e4m3(*ptrs, op or out.data_ptr(), rows, K, N, code, _raw_stream(dev))
     _check(st, "ida_gemm_e4m3")
     return out
 
@@ -904,19 +920,23 @@ def ida_glu_e4m3(a: torch.Tensor, a_scale: torch.Tensor, w_gate: torch.Tensor, g
     D, lead = a.shape[-1], a.shape[:-1]
     F, kb = w_gate.shape[0], (D + 127) // 128
     rows = a.numel() // D if D else 0
-    _fits(rows, D, F)
+    if rows > _INT or D > _INT or F > _INT:
+        _fits(rows, D, F)
     blocks = (F + 127) // 128
     f32 = torch.float32
     ptrs = (_dense("a", a, a.shape, _E4M3, dev), _dense("a_scale", a_scale, (*lead, kb), f32, dev),
             _dense("w_gate", w_gate, (F, D), _E4M3, dev), _dense("gate_scale", gate_scale, (blocks, kb), f32, dev),
             _dense("w_up", w_up, (F, D), _E4M3, dev), _dense("up_scale", up_scale, (blocks, kb), f32, dev))
-    qs, ss = (*lead, F), (*lead, blocks)
+    qp = sp = None
     if q is None:
-        q = torch.empty(qs, dtype=_E4M3, device=a.device)
+        q = torch.empty((*lead, F), dtype=_E4M3, device=a.device)
+    else:
+        qp = _dense("q", q, (*lead, F), _E4M3, dev)
     if scale is None:
-        scale = torch.empty(ss, dtype=f32, device=a.device)
-    st = (_lib or load()).ida_glu_e4m3(*ptrs, _dense("q", q, qs, _E4M3, dev), _dense("scale", scale, ss, f32, dev),
-                                       rows, D, F, _raw_stream(dev))
+        scale = torch.empty((*lead, blocks), dtype=f32, device=a.device)
+    else:
+        sp = _dense("scale", scale, (*lead, blocks), f32, dev)
+    st = (_lib or load()).ida_glu_e4m3(*ptrs, qp or q.data_ptr(), sp or scale.data_ptr(), rows, D, F, _raw_stream(dev))
     _check(st, "ida_glu_e4m3")
     return q, scale
 
