@@ -31,7 +31,8 @@ struct QuantArgs {
 // and q within a unit of x / d, q + r (x - d q) in fused steps is x / d to the nearest (Markstein 1990), where
 // no step underflows.  Quotients below 2^-10 are 0 in e4m3, so a scale of 2^-80 and more leaves the residual's
 // bits above 2^-138; smaller ones are multiplied by 2^120 first, and the values with them, exactly.  (Divisions
-// were 10 instructions a value: 4099 rows of 5632 channels took 21 us, now XXX.)
+// were 10 instructions a value: 4099 rows of 5632 channels took 21 us, now 12.3, with four groups a thread
+// instead of one: 68 % of the copy rate, 75 % of the issue rate.)
 struct Quotient {
     float up, d, r;
     __device__ __forceinline__ explicit Quotient(float sc) {
