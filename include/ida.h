@@ -513,7 +513,7 @@ IDA_API size_t ida_rmsnorm_backward_workspace_bytes(int rows, int D);
  *   acts      NULL, or [3, rows, F] dtype: receives g, u and h, for ida_ffn_backward;
  *   workspace at least ida_ffn_workspace_bytes(...) bytes (contents on entry ignored).
  * Supported: D and F multiples of 8 up to 65536, rows up to 2^28 with rows * max(D, F) <= 2^36.
- * Sums are fp32.  With IDA_BF16 h is rounded to bf16 between the products (not of up to 16 rows); with IDA_F32 the operands of the
+ * Sums are fp32.  With IDA_BF16 h is rounded to bf16 between the products (not of up to 8 rows); with IDA_F32 the operands of the
  * products are taken apart into three bf16 parts each, whose products above 2^-24 of the whole are all
  * taken.  Non-finite inputs make the rows of out that they reach (all of them for a weight) unspecified.
  * Outputs (the workspace among them) that share bytes with inputs or with one another are refused.

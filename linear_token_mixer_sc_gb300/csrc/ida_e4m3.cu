@@ -224,7 +224,7 @@ ida_status ida_gemm_e4m3(const void *a, const float *a_scale, const void *b, con
     std::string why;
     s = device_ready(&num_sms, why);
     if (s != IDA_OK) return fail_with(s, why);
-    if (rows <= few_rows(kFewE4M3)) {
+    if (rows <= kFewRows) {
         SkinnyArgs k = {a, K, b, nullptr, out, nullptr, a_scale, b_scale, nullptr, nullptr, rows, K, N, dtype == IDA_F32, false};
         return skinny_product(k, kFewE4M3, num_sms, reinterpret_cast<cudaStream_t>(stream));
     }
@@ -263,7 +263,7 @@ ida_status ida_glu_e4m3(const void *a, const float *a_scale, const void *w_gate,
     std::string why;
     s = device_ready(&num_sms, why);
     if (s != IDA_OK) return fail_with(s, why);
-    if (rows <= few_rows(kFewE4M3)) {
+    if (rows <= kFewRows) {
         SkinnyArgs k = {a, D, w_gate, w_up, q, nullptr, a_scale, gate_scale, up_scale, scale, rows, D, F, false, false};
         return skinny_gate(k, kFewE4M3, reinterpret_cast<cudaStream_t>(stream));
     }

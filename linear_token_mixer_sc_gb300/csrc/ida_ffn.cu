@@ -130,7 +130,7 @@ static FfnSpace ffn_space(long long T, int D, int F, int dtype, bool backward) {
         return at;
     };
     const size_t es = dtype == IDA_BF16 ? 2 : 4;
-    if (!backward) s.h = take(tf * (T <= few_rows(kFewBf16) ? 4 : es));  // (few rows' h is fp32)
+    if (!backward) s.h = take(tf * (T <= kFewRows ? 4 : es));  // (few rows' h: two parts)
     if (backward) s.dgu = take(2 * tf * es);
     if (dtype == IDA_F32) {
         s.xs = take(6 * td);
@@ -239,8 +239,8 @@ ida_status ida_ffn(const void *x, const void *w_gate, const void *w_up, const vo
     char *ws = static_cast<char *>(workspace), *ac = static_cast<char *>(acts);
     void *h = ac ? ac + 2 * tf * es : ws + sp.h;
     const int type = dtype == IDA_BF16 ? kFewBf16 : kFewF32;
-    if (rows <= few_rows(type)) {
-        // of few rows h stays in fp32, in the workspace
+    if (rows <= kFewRows) {
+        // of few rows h stays in two bf16 parts or fp32, in the workspace
         SkinnyArgs a = {x, ldx, w_gate, w_up, ws + sp.h, acts, nullptr, nullptr, nullptr, nullptr, rows, D, F, true, false};
         s = skinny_gate(a, type, st);
         if (s != IDA_OK) return s;

@@ -779,9 +779,9 @@ __global__ void __launch_bounds__(gemm_threads(KIND, EPI), 1) gemm_kernel(const 
             const float *sa = nullptr, *sb0 = nullptr, *sb1 = nullptr;
             float na = 0.f, n0 = 0.f, n1 = 0.f;
             auto scales = [&](int i) {
-                na = sa ? __ldg(sa + i) : 0.f;
-                n0 = sb0 ? __ldg(sb0 + i) : 0.f;
-                if (EPI == kGate) n1 = sb1 ? __ldg(sb1 + i) : 0.f;
+                na = sa ? sa[i] : 0.f;
+                n0 = sb0 ? sb0[i] : 0.f;
+                if (EPI == kGate) n1 = sb1 ? sb1[i] : 0.f;
             };
             auto open = [&](int t) {
                 tile = tile_of(g, t, COLS);

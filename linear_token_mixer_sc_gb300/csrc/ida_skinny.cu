@@ -39,15 +39,16 @@ __device__ __forceinline__ float remote_float(const float *p, int rank) {
 // block of 2048 and 5632 channels 16.9 us; 8 warps 19.5, of four rows 20.0), in e4m3 8.
 constexpr int skinny_warps(bool e8) { return e8 ? 8 : 16; }
 
-// NT: groups of 8 rows of x (one in e4m3).  SUB tiles of 16 weights' rows a block, of which a plain product may use 8 (HALVES
+// SUB tiles of 16 weights' rows a block, of which a plain product may use 8 (HALVES
 // 1).  GATE: rows 8 .. 15 of a tile are w1's.  E8 && GATE: a cluster of 8 blocks makes the 128 channels of
 // a scale.
-// The gate's product in bf16 leaves its block in fp32; the product back takes it so, in two bf16 parts (WIDE), for two
-// instructions each on weights that are there anyway: of few rows the product's own rounding would be
-// seen in the result (one row's error 2.3e-3 of its size, now 1.6e-3, which is the output's rounding; no difference in time).
-template <bool E8, int NT, int SUB, int HALVES, bool GATE, bool WIDE>
+// The gate's product in bf16 leaves its block in two bf16 parts, 16 bits in all, and the product back takes both
+// (WIDE), for two instructions each on weights that are there anyway: of few rows one rounding of the product
+// would be seen in the result (one row's error 2.3e-3 of its size, now 1.6e-3, which is the output's rounding;
+// 0.5 us of 17.4).
+template <bool E8, int SUB, int HALVES, bool GATE, bool WIDE>
 __global__ void __launch_bounds__(skinny_warps(E8) * 32, E8 ? 1 : 2) skinny_kernel(SkinnyArgs a) {
-    constexpr int U = SUB * HALVES >= 2 ? 1 : 2, LD = 8 * NT + 1, ES = E8 ? 1 : 2;
+    constexpr int U = SUB * HALVES >= 2 ? 1 : 2, LD = 9, ES = E8 ? 1 : 2;
     constexpr int COLS = SUB * (GATE ? 8 : 8 * HALVES);  // output columns of a block
     extern __shared__ float red[];  // [warps][SUB][16][LD]
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3, nw = blockDim.x >> 5;
@@ -63,13 +64,11 @@ __global__ void __launch_bounds__(skinny_warps(E8) * 32, E8 ? 1 : 2) skinny_kern
             if (r >= a.N) r = a.N - 1;  // not stored
             row[s][h] = static_cast<const char *>(GATE && h ? a.w1 : a.w0) + r * kbytes;
         }
-    float acc[SUB][NT][4];
+    float acc[SUB][4];
 #pragma unroll
     for (int s = 0; s < SUB; ++s)
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) acc[s][n][i] = 0.f;
+        for (int i = 0; i < 4; ++i) acc[s][i] = 0.f;
 
     uint4 w[U][SUB][HALVES][2];
     auto fetch = [&](int c0) {
@@ -87,8 +86,9 @@ __global__ void __launch_bounds__(skinny_warps(E8) * 32, E8 ? 1 : 2) skinny_kern
             }
         }
     };
-    // the launch before makes x: a product that follows the gate's in one call has its weights read meanwhile
-    // (that one waited for all before it), any other call waits first
+    // The launch before may make any of these inputs (none of their loads is one of read-only data, which might be
+    // moved up before the wait).  A product that follows the gate's in one call has its weights read
+    // meanwhile: that launch let this one start only after it had waited for all before it.
     if (!a.weights_ready) dependent_wait();
     fetch(warp);
     if (a.weights_ready) dependent_wait();
@@ -98,71 +98,47 @@ __global__ void __launch_bounds__(skinny_warps(E8) * 32, E8 ? 1 : 2) skinny_kern
         for (int u = 0; u < U; ++u) {
             const int c = c0 + u * nw;
             if (c >= chunks) break;
-            uint4 x[NT][2], rest[NT][2];  // rest: x's second parts (WIDE)
-            float m[NT][2];
+            uint4 x[2], rest[2];  // rest: x's second parts (WIDE)
+            float m[2];
 #pragma unroll
-            for (int n = 0; n < NT; ++n)
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    const long long at = (long long)c * 128 + j * 64 + t * 16;
-                    const int tok = 8 * n + g;
-                    const bool in = tok < a.T && at < kbytes;
-                    const char *src = static_cast<const char *>(a.x) + (WIDE ? 2 : 1) * (tok * a.ldx * ES + at);
-                    if (WIDE) {
-                        float v[8] = {}, lo[8];
-                        if (in) {
-                            Vec16<float>::unpack(__ldg(reinterpret_cast<const uint4 *>(src)), v);
-                            Vec16<float>::unpack(__ldg(reinterpret_cast<const uint4 *>(src) + 1), v + 4);
-                        }
-                        x[n][j] = Vec16<__nv_bfloat16>::pack(v);
-                        Vec16<__nv_bfloat16>::unpack(x[n][j], lo);
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) lo[e] = v[e] - lo[e];
-                        rest[n][j] = Vec16<__nv_bfloat16>::pack(lo);
-                    } else {
-                        x[n][j] = in ? __ldg(reinterpret_cast<const uint4 *>(src)) : make_uint4(0, 0, 0, 0);
-                    }
-                    if (E8) m[n][j] = 8 * n + 2 * t + j < a.T ? __ldg(a.sa + (long long)(8 * n + 2 * t + j) * chunks + c) : 0.f;
-                }
+            for (int j = 0; j < 2; ++j) {
+                const long long at = (long long)c * 128 + j * 64 + t * 16;
+                const bool in = g < a.T && at < kbytes;
+                const char *src = static_cast<const char *>(a.x) + g * a.ldx * ES + at;
+                x[j] = in ? *reinterpret_cast<const uint4 *>(src) : make_uint4(0, 0, 0, 0);
+                if (WIDE) rest[j] = in ? *reinterpret_cast<const uint4 *>(src + a.T * a.ldx * ES) : make_uint4(0, 0, 0, 0);
+                if (E8) m[j] = 2 * t + j < a.T ? a.sa[(long long)(2 * t + j) * chunks + c] : 0.f;
+            }
+            float s0 = 1.f, s1 = 1.f;
+            if (E8) {
+                const long long blk = n0 / 128 * chunks + c;
+                s0 = a.s0[blk];
+                s1 = GATE ? a.s1[blk] : s0;
+            }
 #pragma unroll
             for (int s = 0; s < SUB; ++s) {
-                float s0 = 1.f, s1 = 1.f;
-                if (E8) {
-                    const long long blk = n0 / 128 * chunks + c;
-                    s0 = __ldg(a.s0 + blk);
-                    s1 = GATE ? __ldg(a.s1 + blk) : s0;
-                }
+                float part[4] = {0.f, 0.f, 0.f, 0.f};
+                float(&d)[4] = E8 ? part : acc[s];
 #pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                    float part[4] = {0.f, 0.f, 0.f, 0.f};
-                    float(&d)[4] = E8 ? part : acc[s][n];
-#pragma unroll
-                    for (int j = 0; j < 2; ++j) {
-                        const uint4 lo = w[u][s][0][j], hi = HALVES == 2 ? w[u][s][HALVES - 1][j] : make_uint4(0, 0, 0, 0);
-                        mma_rows(d, lo.x, hi.x, lo.y, hi.y, x[n][j].x, x[n][j].y, E8);
-                        mma_rows(d, lo.z, hi.z, lo.w, hi.w, x[n][j].z, x[n][j].w, E8);
-                        if (WIDE) {
-                            mma_rows(d, lo.x, hi.x, lo.y, hi.y, rest[n][j].x, rest[n][j].y, E8);
-                            mma_rows(d, lo.z, hi.z, lo.w, hi.w, rest[n][j].z, rest[n][j].w, E8);
-                        }
-                    }
-                    if (E8) {
-                        acc[s][n][0] = fmaf(part[0], m[n][0] * s0, acc[s][n][0]);
-                        acc[s][n][1] = fmaf(part[1], m[n][1] * s0, acc[s][n][1]);
-                        acc[s][n][2] = fmaf(part[2], m[n][0] * s1, acc[s][n][2]);
-                        acc[s][n][3] = fmaf(part[3], m[n][1] * s1, acc[s][n][3]);
+                for (int j = 0; j < 2; ++j) {
+                    const uint4 lo = w[u][s][0][j], hi = HALVES == 2 ? w[u][s][HALVES - 1][j] : make_uint4(0, 0, 0, 0);
+                    mma_rows(d, lo.x, hi.x, lo.y, hi.y, x[j].x, x[j].y, E8);
+                    mma_rows(d, lo.z, hi.z, lo.w, hi.w, x[j].z, x[j].w, E8);
+                    if (WIDE) {
+                        mma_rows(d, lo.x, hi.x, lo.y, hi.y, rest[j].x, rest[j].y, E8);
+                        mma_rows(d, lo.z, hi.z, lo.w, hi.w, rest[j].z, rest[j].w, E8);
                     }
                 }
+                if (E8)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) acc[s][i] = fmaf(part[i], m[i & 1] * (i < 2 ? s0 : s1), acc[s][i]);
             }
         }
     }
 #pragma unroll
     for (int s = 0; s < SUB; ++s)
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) red[((warp * SUB + s) * 16 + g + (i >> 1) * 8) * LD + 8 * n + 2 * t + (i & 1)] = acc[s][n][i];
-    dependent_launch();
+        for (int i = 0; i < 4; ++i) red[((warp * SUB + s) * 16 + g + (i >> 1) * 8) * LD + 2 * t + (i & 1)] = acc[s][i];
     __syncthreads();
     auto sum = [&](int s, int r, int tok) {
         float v = red[(s * 16 + r) * LD + tok];
@@ -186,12 +162,14 @@ __global__ void __launch_bounds__(skinny_warps(E8) * 32, E8 ? 1 : 2) skinny_kern
             const float x = sum(c / 8, c % 8, tok), y = sum(c / 8, 8 + c % 8, tok);
             const long long at = tok * a.N + n0 + c;
             const float h = x * sigmoid<__nv_bfloat16>(x) * y;
-            static_cast<float *>(a.out)[at] = h;
+            const long long part = (long long)a.T * a.N;
+            const __nv_bfloat16 hi = __float2bfloat16_rn(h);
+            static_cast<__nv_bfloat16 *>(a.out)[at] = hi;
+            static_cast<__nv_bfloat16 *>(a.out)[at + part] = __float2bfloat16_rn(h - __bfloat162float(hi));
             if (a.acts) {
-                const long long part = (long long)a.T * a.N;
                 static_cast<__nv_bfloat16 *>(a.acts)[at] = __float2bfloat16_rn(x);
                 static_cast<__nv_bfloat16 *>(a.acts)[at + part] = __float2bfloat16_rn(y);
-                static_cast<__nv_bfloat16 *>(a.acts)[at + 2 * part] = __float2bfloat16_rn(h);
+                static_cast<__nv_bfloat16 *>(a.acts)[at + 2 * part] = hi;
             }
         }
     } else {
@@ -220,15 +198,15 @@ __global__ void __launch_bounds__(skinny_warps(E8) * 32, E8 ? 1 : 2) skinny_kern
     }
 }
 
-template <bool E8, int NT, int SUB, int HALVES, bool GATE, bool WIDE = !E8 && !GATE>
+template <bool E8, int SUB, int HALVES, bool GATE, bool WIDE = !E8 && !GATE>
 static ida_status launch_skinny(const SkinnyArgs &a, cudaStream_t st) {
     constexpr int cols = SUB * (GATE ? 8 : 8 * HALVES);
-    const auto kernel = skinny_kernel<E8, NT, SUB, HALVES, GATE, WIDE>;
+    const auto kernel = skinny_kernel<E8, SUB, HALVES, GATE, WIDE>;
     const long long chunks = ((long long)a.K * (E8 ? 1 : 2) + 127) / 128;
     // the 8-bit gate's threads make 16 channels of up to 8 rows
     constexpr int most = skinny_warps(E8);
     const int warps = E8 && GATE ? most : chunks < most ? (int)chunks : most;
-    const size_t smem = (size_t)warps * SUB * 16 * (8 * NT + 1) * sizeof(float);
+    const size_t smem = (size_t)warps * SUB * 16 * 9 * sizeof(float);
     cudaError_t e = allow_smem(kernel, smem);
     if (e != cudaSuccess) return fail_with(IDA_ERR_CUDA, cudaGetErrorString(e));
     cudaLaunchConfig_t cfg = {};
@@ -285,7 +263,7 @@ __global__ void __launch_bounds__(256) skinny_f32_kernel(SkinnyArgs a) {
 #pragma unroll
             for (int t = 0; t < NT; ++t) {
                 float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-                if (t < a.T && k + lane * 4 < a.K) v = __ldg(reinterpret_cast<const float4 *>(x + t * a.ldx + k));
+                if (t < a.T && k + lane * 4 < a.K) v = *reinterpret_cast<const float4 *>(x + t * a.ldx + k);
 #pragma unroll
                 for (int r = 0; r < 4; ++r)
                     acc[r][t] = fmaf(w[u][r].w, v.w, fmaf(w[u][r].z, v.z, fmaf(w[u][r].y, v.y, fmaf(w[u][r].x, v.x, acc[r][t]))));
@@ -336,20 +314,15 @@ static ida_status launch_f32_rows(const SkinnyArgs &a, cudaStream_t st) {
     return a.T <= 2 ? launch_f32<2, GATE>(a, st) : launch_f32<8, GATE>(a, st);
 }
 
-template <int HALVES, bool GATE>
-static ida_status launch_bf16_rows(const SkinnyArgs &a, cudaStream_t st) {
-    return a.T <= 8 ? launch_skinny<false, 1, 1, HALVES, GATE>(a, st) : launch_skinny<false, 2, 1, HALVES, GATE>(a, st);
-}
-
 ida_status skinny_product(const SkinnyArgs &a, int type, int num_sms, cudaStream_t st) {
     if (type == kFewF32) return launch_f32_rows<false>(a, st);
     // 16 rows of weights to a block where that leaves every SM two of them
-    if (a.N >= 32 * num_sms) return type == kFewE4M3 ? launch_skinny<true, 1, 1, 2, false>(a, st) : launch_bf16_rows<2, false>(a, st);
-    return type == kFewE4M3 ? launch_skinny<true, 1, 1, 1, false>(a, st) : launch_bf16_rows<1, false>(a, st);
+    if (a.N >= 32 * num_sms) return type == kFewE4M3 ? launch_skinny<true, 1, 2, false>(a, st) : launch_skinny<false, 1, 2, false>(a, st);
+    return type == kFewE4M3 ? launch_skinny<true, 1, 1, false>(a, st) : launch_skinny<false, 1, 1, false>(a, st);
 }
 ida_status skinny_gate(const SkinnyArgs &a, int type, cudaStream_t st) {
     if (type == kFewF32) return launch_f32_rows<true>(a, st);
-    return type == kFewE4M3 ? launch_skinny<true, 1, 2, 2, true>(a, st) : launch_bf16_rows<2, true>(a, st);
+    return type == kFewE4M3 ? launch_skinny<true, 2, 2, true>(a, st) : launch_skinny<false, 1, 2, true>(a, st);
 }
 
 }  // namespace ida
