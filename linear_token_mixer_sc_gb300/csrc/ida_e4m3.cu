@@ -278,7 +278,7 @@ ida_status ida_glu_e4m3(const void *a, const float *a_scale, const void *w_gate,
     s = gemm_map(&g.a[0], a, kMapBytes, D, rows, 1, D, 128, 128);
     if (s == IDA_OK) s = gemm_map(&g.b[0], w_gate, kMapBytes, D, F, 1, D, 128, 128);
     if (s == IDA_OK) s = gemm_map(&g.b[1], w_up, kMapBytes, D, F, 1, D, 128, 128);
-    if (s == IDA_OK) s = gemm_map(&g.o[0], q, kMapBytes, F, rows, 1, F, 32, 32);
+    if (s == IDA_OK) s = gemm_map(&g.o[0], q, kMapBytes, F, rows, 1, F, 64, 32);
     if (s == IDA_OK) s = gemm_e4m3(kGate, IDA_BF16, g, num_sms, reinterpret_cast<cudaStream_t>(stream));
     return s;
 }

@@ -49,9 +49,7 @@ ida_status gemm_map(CUtensorMap *m, const void *p, int type, long long inner, lo
     const CUresult r = fn(m, type == kMapBf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : type == kMapF32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
                                                                                                   : CU_TENSOR_MAP_DATA_TYPE_UINT8,
                           3, const_cast<void *>(p), dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                          box0 * es == 32   ? CU_TENSOR_MAP_SWIZZLE_32B
-                          : box0 * es == 64 ? CU_TENSOR_MAP_SWIZZLE_64B
-                                            : CU_TENSOR_MAP_SWIZZLE_128B,
+                          box0 * es == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
                           CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS ? IDA_OK : fail_with(IDA_ERR_CUDA, "cuTensorMapEncodeTiled failed");
 }

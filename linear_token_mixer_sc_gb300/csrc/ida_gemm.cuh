@@ -26,13 +26,12 @@ enum { kDirect = 0, kParts = 1, kE4M3 = 2 };          // operands: bf16, three b
 enum { kPlain = 0, kGate = 1, kGateBwd = 2 };         // epilogues
 constexpr int GOP = 128 * 128;                        // bytes of an operand of a stage
 constexpr int GSLAB = 32 * 128;                       // bytes of a warp's staged box: 32 rows of 128 bytes
-// Halves of the accumulator that are filled and emptied by themselves: two for fp32's parts.  In e4m3 each MMA
-// of half the columns would read A again, and shared memory cannot feed that (14336 rows' gated projection 307
-// us, 280 with whole ones).
-constexpr int gemm_halves(int kind) { return kind == kParts ? 2 : 1; }
 // Warps of the epilogue.  A plain direct product's four are enough and eight lose 3 %; the gate's and its gradients'
-// have work for eight (gradients of 16384 rows of 768 and 2048 channels 61 us with four, 55 with eight).
-constexpr int gemm_warps(int kind, int epi) { return kind != kDirect ? 16 : epi == kPlain ? 4 : 8; }
+// have work for eight (gradients of 16384 rows of 768 and 2048 channels 61 us with four, 55 with eight).  Sums in
+// registers are eight warps', 128 a thread (14336 rows' gated projection in 8 bits 247 us; 280 with sixteen warps and
+// 64, 307 with those and halves of the accumulator released by themselves: an MMA of half the columns reads A
+// again, and shared memory cannot feed that).
+constexpr int gemm_warps(int kind, int epi) { return kind == kDirect && epi == kPlain ? 4 : 8; }
 constexpr int gemm_threads(int kind, int epi) { return (kind == kDirect ? 64 : 128) + 32 * gemm_warps(kind, epi); }
 // Boxes that a warp stages, and the stages that shared memory has left for operands
 constexpr int gemm_boxes(int epi) { return epi == kGateBwd ? 2 : 1; }
@@ -43,7 +42,6 @@ constexpr int gemm_stages(int kind, int epi) {
 }
 constexpr int gemm_smem(int kind, int epi) { return gemm_stages(kind, epi) * 2 * GOP + gemm_staging(kind, epi) + 1024 + 512; }
 constexpr int GST = 6;                                // stages at most
-constexpr int GSTAGING = 16 * GSLAB;                  // of sixteen warps with a box each
 
 struct GemmSeg {
     unsigned char a, ap, b, bp;  // maps and parts of one pass over the contraction
@@ -301,7 +299,7 @@ __device__ __forceinline__ void send_box(const char *slab, const void *map, bool
 // ---- the kernel ------------------------------------------------------------------------------
 
 struct GemmBars {
-    uint64_t full[GST], empty[GST], acc_full[2][2], acc_empty[2][2], in[16][2];
+    uint64_t full[GST], empty[GST], acc_full[2], acc_empty[2], in[8][2];
     uint32_t tmem;
 };
 
@@ -309,9 +307,8 @@ struct GemmBars {
 struct EpiWarp {
     char *staging;
     uint64_t *in;   // its barriers for what the epilogue reads
-    int lane, q, rank;
-    int half, part;  // its accumulator (other kinds) and which part of that one's columns
-    uint32_t tmem;   // of its lanes
+    int lane, q, half, rank;  // 32 rows q, half of the columns, of two
+    uint32_t tmem;            // of its lanes
 };
 
 // The accumulator has been read
@@ -435,24 +432,20 @@ struct GateBwd {
     }
 };
 
-// The other kinds: a thread's 64 sums of its row, in registers.  A tile's accumulator comes in two halves of 128
-// columns, each CTA's first 64 columns of B and its last 64, that are filled and emptied by themselves;
-// two groups of four warps empty a half: kGate, 32 columns of either factor each, otherwise one CTA's 64 each.
-template <int KIND, int EPI>
-__device__ __forceinline__ int sum_col(const EpiWarp &w, int c) {  // TMEM column of sums 16 c .., of the half's
-    if (gemm_halves(KIND) == 1)
-        return EPI == kGate ? w.half * 64 + w.part * 32 + c / 2 * 128 + c % 2 * 16 : w.part * 128 + w.half * 64 + c * 16;
-    return EPI == kGate ? w.part * 32 + c / 2 * 64 + c % 2 * 16 : w.part * 64 + c * 16;
+// The other kinds: a thread's 128 sums of its row, in registers: half of the tile's columns, or (kGate) 64 of either factor.
+template <int EPI>
+__device__ __forceinline__ int sum_col(const EpiWarp &w, int c) {  // TMEM column of sums 16 c ..
+    return EPI == kGate ? w.half * 64 + c / 4 * 128 + c % 4 * 16 : w.half * 128 + c * 16;
 }
 
 template <int KIND, int EPI, typename E>
-__device__ __forceinline__ bool epi_sums(const GemmArgs &g, const EpiWarp &w, const GemmTile &t, float (&x)[64], int &uses) {
+__device__ __forceinline__ bool epi_sums(const GemmArgs &g, const EpiWarp &w, const GemmTile &t, float (&x)[128], int &uses) {
     constexpr int BOX = 128 / (int)sizeof(E), PER = 16 / (int)sizeof(E);  // columns of a box, of a piece
     const int row = t.row0 + w.rank * 128 + w.q * 32;
     if constexpr (EPI == kPlain) {
-        const int col = t.col0 + w.part * 128 + w.half * 64;
+        const int col = t.col0 + w.half * 128;
 #pragma unroll
-        for (int j = 0; j < 64 / BOX; ++j) {
+        for (int j = 0; j < 128 / BOX; ++j) {
             if (KIND == kE4M3) box_ready(w.lane);
 #pragma unroll
             for (int k = 0; k < 8; ++k) stage<E>(w.staging, w.lane, k, x + j * BOX + k * PER);
@@ -462,26 +455,28 @@ __device__ __forceinline__ bool epi_sums(const GemmArgs &g, const EpiWarp &w, co
                 store_box<E>(w.staging, g.out[t.p], g.M[t.p], g.N[t.p], row, col + j * BOX, w.lane);
         }
     } else if constexpr (EPI == kGate) {
-        static_assert(BOX == 32, "fp32");
-        const int col = t.col0 + w.half * 64 + w.part * 32;
-        if (g.keep) {
-#pragma unroll
-            for (int f = 0; f < 2; ++f) {
-#pragma unroll
-                for (int k = 0; k < 8; ++k) stage<E>(w.staging, w.lane, k, x + f * 32 + k * PER);
-                store_box<E>(w.staging, g.out[1 + f], g.M[0], g.N[0], row, col, w.lane);
-            }
-        }
-#pragma unroll
-        for (int e = 0; e < 32; ++e) x[e] = x[e] * sigmoid<E>(x[e]) * x[32 + e];
-#pragma unroll
-        for (int k = 0; k < 8; ++k) stage<E>(w.staging, w.lane, k, x + k * PER);
-        store_box<E>(w.staging, g.out[0], g.M[0], g.N[0], row, col, w.lane);
-    } else {
-        const int col = t.col0 + w.part * 128 + w.half * 64;
-        char *sg = w.staging, *su = sg + GSLAB;
+        const int col = t.col0 + w.half * 64;
 #pragma unroll
         for (int j = 0; j < 64 / BOX; ++j) {
+            if (g.keep) {
+#pragma unroll
+                for (int f = 0; f < 2; ++f) {
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) stage<E>(w.staging, w.lane, k, x + f * 64 + j * BOX + k * PER);
+                    store_box<E>(w.staging, g.out[1 + f], g.M[0], g.N[0], row, col + j * BOX, w.lane);
+                }
+            }
+#pragma unroll
+            for (int e = j * BOX; e < (j + 1) * BOX; ++e) x[e] = x[e] * sigmoid<E>(x[e]) * x[64 + e];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) stage<E>(w.staging, w.lane, k, x + j * BOX + k * PER);
+            store_box<E>(w.staging, g.out[0], g.M[0], g.N[0], row, col + j * BOX, w.lane);
+        }
+    } else {
+        const int col = t.col0 + w.half * 128;
+        char *sg = w.staging, *su = sg + GSLAB;
+#pragma unroll
+        for (int j = 0; j < 128 / BOX; ++j) {
             if (row >= g.M[0] || col + j * BOX >= g.N[0]) continue;
             if (w.lane == 0) {
                 bulk_wait_read<0>();
@@ -531,34 +526,30 @@ __device__ __forceinline__ uint32_t e4m3x4(const float *x) {
     return lo | hi << 16;
 }
 
-// kE4M3, kGate: the product's 32 columns of a thread, a scale for its row's 128 with the three other warps of those
-// rows.  Each warp's box is 32 rows of 32 bytes (swizzled over 32 bytes); behind it lie its rows' maxima
-// for the other warps, which read them once this one has arrived on their barriers (and before they arrive
-// themselves for the next tile, so that two sets are enough).  n: tiles before this one.
-__device__ __forceinline__ bool epi_gate_e4m3(const GemmArgs &g, const EpiWarp &w, const GemmTile &t, float (&x)[64], int n) {
+// kE4M3, kGate: the product's 64 columns of a thread, a scale for its row's 128 with the warp of the other half.
+// Each warp's box is 32 rows of 64 bytes (swizzled over 64 bytes); behind it lie its rows' maxima for the other
+// warp, which reads them once this one has arrived on its barrier (and before it arrives itself for the next
+// tile, so that two sets are enough).  n: tiles before this one.
+__device__ __forceinline__ bool epi_gate_e4m3(const GemmArgs &g, const EpiWarp &w, const GemmTile &t, float (&x)[128], int n) {
     float top = 0.f;
 #pragma unroll
-    for (int e = 0; e < 32; ++e) {
-        x[e] = x[e] * sigmoid<__nv_bfloat16>(x[e]) * x[32 + e];
+    for (int e = 0; e < 64; ++e) {
+        x[e] = x[e] * sigmoid<__nv_bfloat16>(x[e]) * x[64 + e];
         top = fmaxf(top, fabsf(x[e]));
     }
     char *slab = w.staging;
     box_ready(w.lane);
-    const int at = GSLAB / 2 + (n & 1) * 128, own = w.half * 2 + w.part;
+    const int at = GSLAB / 2 + (n & 1) * 128, other = w.half ? -4 : 4;  // warps to the other half's
     reinterpret_cast<float *>(slab + at)[w.lane] = top;
     __syncwarp();
-#pragma unroll
-    for (int k = 1; k < 4; ++k)
-        if (w.lane == 0) arrive_local(w.in + ((own ^ k) - own) * 8);  // 4 warps on: 4 pairs of barriers
+    if (w.lane == 0) arrive_local(w.in + other * 2);
     if (!pair_wait(w.in, n & 1, g.err)) return false;
-#pragma unroll
-    for (int k = 1; k < 4; ++k)
-        top = fmaxf(top, reinterpret_cast<const float *>(slab + at + ((own ^ k) - own) * 4 * (GSTAGING / 16))[w.lane]);
+    top = fmaxf(top, reinterpret_cast<const float *>(slab + at + other * GSLAB)[w.lane]);
     float up;
     const float sc = e4m3_scale(top, up), is = 1.f / (sc * up);
-    const int row = t.row0 + w.rank * 128 + w.q * 32, col = t.col0 + w.half * 64 + w.part * 32;
+    const int row = t.row0 + w.rank * 128 + w.q * 32, col = t.col0 + w.half * 64;
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {
+    for (int k = 0; k < 4; ++k) {
         uint32_t v[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
@@ -567,10 +558,10 @@ __device__ __forceinline__ bool epi_gate_e4m3(const GemmArgs &g, const EpiWarp &
             for (int i = 0; i < 4; ++i) y[i] = x[16 * k + 4 * e + i] * up * is;
             v[e] = e4m3x4(y);
         }
-        *reinterpret_cast<uint4 *>(slab + w.lane * 32 + ((k ^ (w.lane >> 2 & 1)) << 4)) = make_uint4(v[0], v[1], v[2], v[3]);
+        *reinterpret_cast<uint4 *>(slab + w.lane * 64 + ((k ^ (w.lane >> 1 & 3)) << 4)) = make_uint4(v[0], v[1], v[2], v[3]);
     }
     send_box(slab, &g.o[0], row < g.M[0] && col < g.N[0], row, col, w.lane);
-    if (own == 0 && row + w.lane < g.M[0]) g.so[(size_t)(row + w.lane) * ((g.N[0] + 127) / 128) + t.col0 / 128] = sc;
+    if (w.half == 0 && row + w.lane < g.M[0]) g.so[(size_t)(row + w.lane) * ((g.N[0] + 127) / 128) + t.col0 / 128] = sc;
     return true;
 }
 
@@ -603,7 +594,7 @@ template <int AMN, int BMN, int KIND, int EPI, typename E, bool SPLIT>
 __global__ void __launch_bounds__(gemm_threads(KIND, EPI), 1) gemm_kernel(const __grid_constant__ GemmArgs g) {
     constexpr bool E8 = KIND == kE4M3;
     constexpr int ST = gemm_stages(KIND, EPI), STAGING = gemm_staging(KIND, EPI);
-    constexpr int EW = gemm_warps(KIND, EPI), E0 = KIND == kDirect ? 2 : 4, HALVES = gemm_halves(KIND), COLS = tile_cols(EPI), KB = E8 ? 128 : 64;
+    constexpr int EW = gemm_warps(KIND, EPI), E0 = KIND == kDirect ? 2 : 4, COLS = tile_cols(EPI), KB = E8 ? 128 : 64;
     extern __shared__ char raw[];
     char *sm = raw + ((1024 - (tc::smem_u32(raw) & 1023)) & 1023);
     char *ops = sm, *staging = sm + ST * 2 * GOP;
@@ -620,11 +611,11 @@ __global__ void __launch_bounds__(gemm_threads(KIND, EPI), 1) gemm_kernel(const 
             tc::mbar_init(&bar.full[s], 1);
             tc::mbar_init(&bar.empty[s], 1);
         }
-        for (int s = 0; s < 4; ++s) {
-            tc::mbar_init(&bar.acc_full[s >> 1][s & 1], 1);
-            tc::mbar_init(&bar.acc_empty[s >> 1][s & 1], 2 * EW / HALVES);
+        for (int s = 0; s < 2; ++s) {
+            tc::mbar_init(&bar.acc_full[s], 1);
+            tc::mbar_init(&bar.acc_empty[s], 2 * EW);
         }
-        for (int s = 0; s < 2 * EW; ++s) tc::mbar_init(&bar.in[s >> 1][s & 1], E8 && EPI == kGate ? 3 : 1);
+        for (int s = 0; s < 2 * EW; ++s) tc::mbar_init(&bar.in[s >> 1][s & 1], 1);
         tc::fence_mbar_init();
     }
     if (warp == 1) {
@@ -639,10 +630,10 @@ __global__ void __launch_bounds__(gemm_threads(KIND, EPI), 1) gemm_kernel(const 
     const uint32_t tmem = bar.tmem;
     dependent_wait();
 
-    // sums in registers: 96 of them a thread at launch (61440 in all), 32 for the first four warps leave
-    // 112 for the other sixteen (61440)
+    // sums in registers: 168 of them a thread at launch (64512 in all), 40 for the first four warps leave
+    // 232 for the other eight (64512)
     if (warp < E0) {
-        if (KIND != kDirect) asm volatile("setmaxnreg.dec.sync.aligned.u32 32;");
+        if (KIND != kDirect) asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
         // These two roles' loops are run by whole warps and their waits end in a vote: the compiler then keeps
         // addresses and descriptors in uniform registers, where the one lane that issues wants them (moved there for
         // each instruction they held the MMAs up, 950 clocks a block of 512: 14336 rows' gated projection in 8 bits
@@ -693,7 +684,7 @@ __global__ void __launch_bounds__(gemm_threads(KIND, EPI), 1) gemm_kernel(const 
             }
         }
         if (warp == 1 && rank == 0) {
-            constexpr uint32_t id = tc::idesc(256, 256 / HALVES, E8 ? 0 : 1, E8 ? 0 : 1, AMN, BMN);
+            constexpr uint32_t id = tc::idesc(256, 256, E8 ? 0 : 1, E8 ? 0 : 1, AMN, BMN);
             int st = 0, ph = 0, ab = 0, aph = 1;
             bool ok = true;
             const uint32_t ops32 = tc::smem_u32(ops);
@@ -702,24 +693,20 @@ __global__ void __launch_bounds__(gemm_threads(KIND, EPI), 1) gemm_kernel(const 
                     const int n = per_tile - k0 < g.chunk ? per_tile - k0 : g.chunk;
                     for (int j = 0; ok && j < n; ++j) {
                         if (!(ok = warp_wait(&bar.full[st], ph, g.err))) break;
+                        if (j == 0 && !(ok = warp_wait(&bar.acc_empty[ab], aph, g.err))) break;
+                        tc::tc_fence_after();
                         const uint32_t A = ops32 + st * 2 * GOP, B = A + GOP;
-                        const tc::SmemDesc da = pair_desc(A, AMN ? GOP / 2 : 16);
+                        const tc::SmemDesc da = pair_desc(A, AMN ? GOP / 2 : 16), db = pair_desc(B, BMN ? GOP / 2 : 16);
+                        if (one) {
 #pragma unroll
-                        for (int h = 0; h < HALVES; ++h) {
-                            if (j == 0 && !(ok = warp_wait(&bar.acc_empty[ab][h], aph, g.err))) break;
-                            tc::tc_fence_after();
-                            const tc::SmemDesc db = pair_desc(B + h * (GOP / 2), BMN ? GOP / 2 : 16);
-                            if (one) {
-#pragma unroll
-                                for (int k = 0; k < 4; ++k) {
-                                    tc::SmemDesc a = da, b = db;
-                                    a.lo += k * (AMN ? 2048 : 32) >> 4;
-                                    b.lo += k * (BMN ? 2048 : 32) >> 4;
-                                    pair_mma<E8>(tmem + ab * 256 + h * 128, a, b, id, j > 0 || k > 0);
-                                }
-                                if (h == HALVES - 1) pair_commit(&bar.empty[st]);
-                                if (j == n - 1) pair_commit(&bar.acc_full[ab][h]);
+                            for (int k = 0; k < 4; ++k) {
+                                tc::SmemDesc a = da, b = db;
+                                a.lo += k * (AMN ? 2048 : 32) >> 4;
+                                b.lo += k * (BMN ? 2048 : 32) >> 4;
+                                pair_mma<E8>(tmem + ab * 256, a, b, id, j > 0 || k > 0);
                             }
+                            pair_commit(&bar.empty[st]);
+                            if (j == n - 1) pair_commit(&bar.acc_full[ab]);
                         }
                         if (++st == ST) st = 0, ph ^= 1;
                     }
@@ -730,13 +717,12 @@ __global__ void __launch_bounds__(gemm_threads(KIND, EPI), 1) gemm_kernel(const 
         }
         __syncwarp();
     } else {
-        if (KIND != kDirect) asm volatile("setmaxnreg.inc.sync.aligned.u32 112;");
+        if (KIND != kDirect) asm volatile("setmaxnreg.inc.sync.aligned.u32 232;");
         EpiWarp w;
         const int ew = warp - E0;
         w.lane = lane;
         w.q = warp & 3;
-        w.half = KIND == kDirect ? ew >> 2 : ew >> 3;
-        w.part = ew >> 2 & 1;
+        w.half = ew >> 2;
         w.rank = rank;
         w.staging = staging + ew * (STAGING / EW);
         w.in = bar.in[ew];
@@ -749,9 +735,9 @@ __global__ void __launch_bounds__(gemm_threads(KIND, EPI), 1) gemm_kernel(const 
             for (int t = pair; ok && t < tiles; t += pairs, ++ch) {
                 const GemmTile tile = tile_of(g, t, COLS);
                 const int ab = ch & 1;
-                if (!(ok = pair_wait(&bar.acc_full[ab][0], ch >> 1 & 1, g.err))) break;
+                if (!(ok = pair_wait(&bar.acc_full[ab], ch >> 1 & 1, g.err))) break;
                 tc::tc_fence_after();
-                const uint32_t acc = w.tmem + ab * 256, release = lead_addr(&bar.acc_empty[ab][0]);
+                const uint32_t acc = w.tmem + ab * 256, release = lead_addr(&bar.acc_empty[ab]);
                 if constexpr (SPLIT) {
 #pragma unroll 1
                     for (int c = 0; c < 256; c += 32) {
@@ -787,7 +773,7 @@ __global__ void __launch_bounds__(gemm_threads(KIND, EPI), 1) gemm_kernel(const 
                 tile = tile_of(g, t, COLS);
                 if constexpr (E8) {
                     const int row = tile.row0 + rank * 128 + w.q * 32 + lane;
-                    const int blk = tile.col0 / 128 + (EPI == kGate ? 0 : w.part);
+                    const int blk = tile.col0 / 128 + (EPI == kGate ? 0 : w.half);
                     sa = row < g.M[tile.p] ? g.sa + (size_t)row * g.kblocks + kfirst : nullptr;
                     const bool in = blk * 128 < g.N[tile.p];
                     sb0 = in ? g.sb[0] + (size_t)blk * g.kblocks + kfirst : nullptr;
@@ -797,39 +783,52 @@ __global__ void __launch_bounds__(gemm_threads(KIND, EPI), 1) gemm_kernel(const 
             };
             if (pair < tiles) open(pair);
             for (int t = pair; ok && t < tiles; t += pairs) {
-                float x[64];
+                float x[128];
 #pragma unroll
-                for (int e = 0; e < 64; ++e) x[e] = 0.f;
+                for (int e = 0; e < 128; ++e) x[e] = 0.f;
                 for (int k0 = 0, i = 0; k0 < per_tile; k0 += g.chunk, ++ch, ++i) {
                     const int ab = ch & 1;
                     const float m0 = E8 ? na * n0 : 1.f, m1 = E8 && EPI == kGate ? na * n1 : m0;
                     if (E8 && i + 1 < per_tile) scales(i + 1);
-                    if (!(ok = pair_wait(&bar.acc_full[ab][HALVES == 1 ? 0 : w.half], ch >> 1 & 1, g.err))) break;
+                    if (!(ok = pair_wait(&bar.acc_full[ab], ch >> 1 & 1, g.err))) break;
                     tc::tc_fence_after();
-                    const uint32_t acc = w.tmem + ab * 256 + (HALVES == 1 ? 0 : w.half * 128);
-                    uint32_t r[2][16];
-                    tmem_ld16(acc + sum_col<KIND, EPI>(w, 0), r[0]);
+                    const uint32_t acc = w.tmem + ab * 256;
+                    uint32_t r[8][16];
+                    auto fetch = [&](int c) { tmem_ld16(acc + sum_col<EPI>(w, c), r[c]); };
+                    auto add = [&](int c) {
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) {  // the next 16 columns come while these are added
-                        tc::tmem_wait_ld();
-                        tmem_use(r[c & 1]);
-                        if (c < 3) {
-                            tmem_ld16(acc + sum_col<KIND, EPI>(w, c + 1), r[(c + 1) & 1]);
-                        } else {
-                            release_acc(w, lead_addr(&bar.acc_empty[ab][HALVES == 1 ? 0 : w.half]));
-                        }
-                        const float m = EPI == kGate && c >= 2 ? m1 : m0;
+                        for (int e = 0; e < 16; e += 2)
+                            add_scaled(x[c * 16 + e], x[c * 16 + e + 1], r[c][e], r[c][e + 1], EPI == kGate && c >= 4 ? m1 : m0);
+                    };
+                    // half of them; the others come while these are added, into the registers that they leave; and the
+                    // accumulator is released before the last are added
 #pragma unroll
-                        for (int e = 0; e < 16; e += 2) add_scaled(x[c * 16 + e], x[c * 16 + e + 1], r[c & 1][e], r[c & 1][e + 1], m);
-                    }
+                    for (int c = 0; c < 4; ++c) fetch(c);
+                    tc::tmem_wait_ld();
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) tmem_use(r[c]);
+                    fetch(4);
+                    add(0);
+                    add(1);
+                    fetch(5);
+                    fetch(6);
+                    add(2);
+                    add(3);
+                    fetch(7);
+                    tc::tmem_wait_ld();
+#pragma unroll
+                    for (int c = 4; c < 8; ++c) tmem_use(r[c]);
+                    release_acc(w, lead_addr(&bar.acc_empty[ab]));
+#pragma unroll
+                    for (int c = 4; c < 8; ++c) add(c);
                 }
                 if (!ok) break;
                 const GemmTile done = tile;
                 if (t + pairs < tiles) open(t + pairs);
                 if constexpr (SPLIT) {
 #pragma unroll
-                    for (int e = 0; e < 64; e += 4)
-                        *reinterpret_cast<float4 *>(ops + ((w.part * 128 + w.half * 64 + e) / 4 * 128 + w.q * 32 + lane) * 16) =
+                    for (int e = 0; e < 128; e += 4)
+                        *reinterpret_cast<float4 *>(ops + ((w.half * 128 + e) / 4 * 128 + w.q * 32 + lane) * 16) =
                             make_float4(x[e], x[e + 1], x[e + 2], x[e + 3]);
                 } else if constexpr (E8 && EPI == kGate)
                     ok = epi_gate_e4m3(g, w, done, x, uses++);
