@@ -560,7 +560,8 @@ IDA_API ida_status ida_quant_e4m3(const void *x, void *q, float *scale, int rows
 /*
  * out = A B^T, [rows, N] dtype dense, of A (a [rows, K] and the scales of activations) and B (b [N, K]
  * and the scales of weights).  N a multiple of 8 up to 65536.  Products are exact and summed in fp32: within a
- * block by the tensor cores, over blocks with their scales in registers.
+ * block by the tensor cores, over blocks with their scales in registers.  Values and scales that are not finite make
+ * the rows of out (of b: the columns; of ida_glu_e4m3's weights: the groups) that they reach unspecified.
  */
 IDA_API ida_status ida_gemm_e4m3(const void *a, const float *a_scale, const void *b, const float *b_scale, void *out,
                          int rows, int K, int N, int dtype, ida_stream_t stream);

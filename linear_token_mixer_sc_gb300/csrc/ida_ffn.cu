@@ -106,6 +106,12 @@ static ida_status launch_split(const SplitArgs &a, int count, int num_sms, cudaS
 
 static size_t up256(size_t x) { return (x + 255) & ~(size_t)255; }
 
+// fp32 products on the CUDA cores: few rows, or little arithmetic.  Forward and backward, in us, there and on the tensor
+// cores: 251 rows of 64 and 176 channels 6 + 13 and 19 + 40, 512 of 256 and 512 22 + 53 and 34 + 73, 1024 of 256 and 704
+// (2^27.5) 40 + 92 and 40 + 98, 1024 of 512 and 1024 104 + 209 and 56 + 125; 32 rows of 2048 and 5632 122 + 391 and
+// 267 + 455.
+static bool on_cuda_cores(long long rows, long long D, long long F) { return rows <= 64 || rows * D * F <= (1LL << 27); }
+
 // Operands of the products: the caller's own tensors in bf16, their parts in the workspace otherwise.
 struct Operand {
     const void *p;
@@ -115,7 +121,7 @@ struct Operand {
 
 struct FfnSpace {
     size_t h, xs, wg, wu, wd, hs, total;                // forwards
-    size_t dgu, dys, dgs, dus, back;                    // backwards
+    size_t dgu, dys, dgs, dus;                          // backwards
 };
 
 static FfnSpace ffn_space(long long T, int D, int F, int dtype, bool backward) {
@@ -130,7 +136,7 @@ static FfnSpace ffn_space(long long T, int D, int F, int dtype, bool backward) {
     const size_t es = dtype == IDA_BF16 ? 2 : 4;
     if (!backward) s.h = take(tf * (T <= kFewRows ? 4 : es));  // (few rows' h: two parts)
     if (backward) s.dgu = take(2 * tf * es);
-    if (dtype == IDA_F32) {
+    if (dtype == IDA_F32 && !on_cuda_cores(T, D, F)) {
         s.xs = take(6 * td);
         s.wg = take(6 * df);
         s.wu = take(6 * df);
@@ -174,11 +180,6 @@ static ida_status run_gemm(int a_mn, int b_mn, int epi, GemmArgs &g, int dtype, 
     if (s != IDA_OK) return fail_with(s, why);
     return dtype == IDA_BF16 ? gemm_bf16(a_mn, b_mn, epi, g, num_sms, st) : gemm_f32(a_mn, b_mn, epi, g, num_sms, st);
 }
-
-// fp32 products on the CUDA cores: few rows, or little arithmetic.  Forward and backward, in us, there and on the tensor cores: 251 rows of
-// 64 and 176 channels 6 + 13 and 19 + 40, 512 of 256 and 512 22 + 53 and 34 + 73, 1024 of 256 and 704 (2^27.5) 40 + 92 and 40 + 98,
-// 1024 of 512 and 1024 104 + 209 and 56 + 125; 32 rows of 2048 and 5632 122 + 391 and 267 + 455.
-static bool on_cuda_cores(long long rows, long long D, long long F) { return rows <= 64 || rows * D * F <= (1LL << 27); }
 
 static ida_status check_ffn(int rows, int D, int F, long long ldx, int dtype) {
     if (rows < 0) return fail_with(IDA_ERR_ARG, "rows must be >= 0");
