@@ -2,7 +2,7 @@
 products in 8 bits.
 
 Bounds are elementwise, from the roundings that a value passes: HALF for each rounding to the type, STEP
-for the block's activation (hardware exponential and reciprocal), and for a sum of n products a multiple
+for the block's activation, and for a sum of n products a multiple
 of sum |a| |b|: the tensor cores add 16 products (32 in 8 bits) at a time and round the running sum towards zero,
 each by less than 2^-23 of a partial sum, and align the products of a step to its largest with 2^-24 at least."""
 from __future__ import annotations
@@ -11,7 +11,10 @@ import torch
 
 from tests.ssm_cases import DT, HALF, gen
 
-STEP = 2.0 ** -19
+# The activation's own error.  bf16 (and 8 bits): the exponential of a rounded x log2 e, off by |x| 2^-24 of its value and
+# 2^-22, |x| < 88 (where e^-x ends), the reciprocal's 2^-23 and three products: below 2^-17.  fp32: expf within two
+# units, a division and two products: below 2^-20.
+STEP = {"bf16": 2.0 ** -17, "f32": 2.0 ** -20}
 # What lies below the types' least normal numbers (2^-126 in either) may be lost: the gate's sigmoid s, where 1 / s passes
 # 2^126 (its reciprocal is 0 from there on: an error of 2^-126 at most, times what it multiplies), a rounded value
 # and a product in a sum (2^-126 at most each).
@@ -45,7 +48,7 @@ def forward_ref(x, wg, wu, wd, dtype):
     eg, eu = cd * (x.abs() @ wg.abs().t()), cd * (x.abs() @ wu.abs().t())
     s = g * torch.sigmoid(g)
     h = s * u
-    eh = 1.01 * (1.1 * u.abs() * eg + s.abs() * eu) + (STEP + half) * h.abs() + TINY * (1 + (g * u).abs())  # |silu'| < 1.1
+    eh = 1.01 * (1.1 * u.abs() * eg + s.abs() * eu) + (STEP[dtype] + half) * h.abs() + TINY * (1 + (g * u).abs())  # |silu'| < 1.1
     out = h @ wd.t()
     eo = eh @ wd.abs().t() + sum_err(wg.shape[0], dtype) * (h.abs() @ wd.abs().t()) + half * out.abs() + TINY * (1 + wg.shape[0])
     return {"out": (out, eo), "g": (g, eg + half * g.abs()), "u": (u, eu + half * u.abs()), "h": (h, eh)}
@@ -61,8 +64,8 @@ def backward_ref(x, wg, wu, wd, acts, dy, dtype):
     dh = dy @ wd
     edh = sum_err(wd.shape[0], dtype) * (dy.abs() @ wd.abs())
     du, dg = dh * silu, dh * u * dsilu
-    edu = 1.01 * edh * silu.abs() + (half + STEP) * du.abs() + TINY * (1 + (dh * g).abs())
-    edg = 1.01 * edh * (u * dsilu).abs() + half * dg.abs() + STEP * (dh * u).abs() * (s + (g * s * (1 - s)).abs()) + TINY * (1 + (dh * u).abs() * (1 + g.abs()))
+    edu = 1.01 * edh * silu.abs() + (half + STEP[dtype]) * du.abs() + TINY * (1 + (dh * g).abs())
+    edg = 1.01 * edh * (u * dsilu).abs() + half * dg.abs() + STEP[dtype] * (dh * u).abs() * (s + (g * s * (1 - s)).abs()) + TINY * (1 + (dh * u).abs() * (1 + g.abs()))
     c2f, ct = sum_err(2 * F, dtype), sum_err(T, dtype)
     dx = dg @ wg + du @ wu
     edx = edg @ wg.abs() + edu @ wu.abs() + c2f * (dg.abs() @ wg.abs() + du.abs() @ wu.abs()) + half * dx.abs() + TINY * (1 + 2 * F)
@@ -110,4 +113,4 @@ def glu_ref(a, wg, wu):
     (g, eg), (u, eu) = product_ref(a, wg), product_ref(a, wu)
     s = g * torch.sigmoid(g)
     h = s * u
-    return h, 1.01 * (1.1 * u.abs() * eg + s.abs() * eu) + STEP * h.abs()
+    return h, 1.01 * (1.1 * u.abs() * eg + s.abs() * eu) + STEP["bf16"] * h.abs()
