@@ -511,7 +511,8 @@ IDA_API size_t ida_rmsnorm_backward_workspace_bytes(int rows, int D);
  *   x         rows of D channels, ldx elements apart, 16-byte aligned (ldx a multiple of 8);
  *   w_gate, w_up [F, D], w_down [D, F] dtype;  out [rows, D] dtype, dense;
  *   acts      NULL, or [3, rows, F] dtype: receives g, u and h, for ida_ffn_backward;
- *   workspace at least ida_ffn_workspace_bytes(...) bytes (contents on entry ignored).
+ *   workspace at least ida_ffn_workspace_bytes(...) bytes (NULL allowed where that is 0; contents on entry
+ *             ignored).
  * Supported: D and F multiples of 8 up to 65536, rows up to 2^28 with rows * max(D, F) <= 2^36.
  * Sums are fp32.  With IDA_BF16 h is rounded to bf16 between the products (not of up to 8 rows); with IDA_F32 the operands of the
  * products are taken apart into three bf16 parts each, whose products above 2^-24 of the whole are all
@@ -522,8 +523,9 @@ IDA_API ida_status ida_ffn(const void *x, const void *w_gate, const void *w_up, 
                    void *acts, int rows, int D, int F, long long ldx, int dtype, void *workspace,
                    size_t workspace_bytes, ida_stream_t stream);
 
-/* Workspace bytes of ida_ffn (0 for invalid sizes or no rows); host arithmetic. */
-IDA_API size_t ida_ffn_workspace_bytes(int rows, int D, int F, int dtype);
+/* Workspace bytes of ida_ffn, with acts (keep != 0) or without (0 for invalid sizes, no rows, or where it needs
+ * none); host arithmetic. */
+IDA_API size_t ida_ffn_workspace_bytes(int rows, int D, int F, int dtype, int keep);
 
 /*
  * Gradients of ida_ffn's out, given what it read, the acts it wrote and dout [rows, D] dense: dx [rows, D] dense,

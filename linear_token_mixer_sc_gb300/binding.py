@@ -103,7 +103,7 @@ def load() -> ctypes.CDLL:
                 getattr(L, name).argtypes = args
             for name, n in (("ida_ssm_conv_backward_workspace_bytes", 4), ("ida_ssm_scan_workspace_bytes", 7),
                             ("ida_ssm_scan_backward_workspace_bytes", 7), ("ida_rmsnorm_backward_workspace_bytes", 2),
-                            ("ida_ffn_workspace_bytes", 4), ("ida_ffn_backward_workspace_bytes", 4)):
+                            ("ida_ffn_workspace_bytes", 5), ("ida_ffn_backward_workspace_bytes", 4)):
                 getattr(L, name).restype = sz
                 getattr(L, name).argtypes = [_i] * n
             L.ida_selftest_bounded_wait.restype = _i
@@ -751,9 +751,9 @@ def ida_rmsnorm_backward(r: torch.Tensor, w: torch.Tensor, dy: torch.Tensor, dre
 # ---- the feed-forward block and products in 8 bits --------------------------------------------
 
 @functools.lru_cache(maxsize=256)  # host arithmetic on the sizes alone
-def ida_ffn_workspace_bytes(rows: int, D: int, F: int, dtype: int) -> int:
+def ida_ffn_workspace_bytes(rows: int, D: int, F: int, dtype: int, keep: bool = False) -> int:
     _fits(rows, D, F, dtype)
-    return int(load().ida_ffn_workspace_bytes(rows, D, F, dtype))
+    return int(load().ida_ffn_workspace_bytes(rows, D, F, dtype, int(keep)))
 
 
 @functools.lru_cache(maxsize=256)
@@ -816,7 +816,7 @@ def ida_ffn(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor, w_down: t
         acts = None
     else:
         ap = _dense("acts", acts, (3, *x.shape[:-1], F), x.dtype, dev)
-    ws, wsp, n = _work_buffer(workspace, ida_ffn_workspace_bytes(rows, D, F, code) if workspace is None else 0, dev)
+    ws, wsp, n = _work_buffer(workspace, ida_ffn_workspace_bytes(rows, D, F, code, acts is not None) if workspace is None else 0, dev)
     st = (_lib or load()).ida_ffn(*ptrs, op or out.data_ptr(), ap, *sizes, ldx, code, wsp, n, _raw_stream(dev))
     _check(st, "ida_ffn")
     return out, acts

@@ -124,7 +124,8 @@ struct FfnSpace {
     size_t dgu, dys, dgs, dus;                          // backwards
 };
 
-static FfnSpace ffn_space(long long T, int D, int F, int dtype, bool backward) {
+// keep: the caller's acts take h
+static FfnSpace ffn_space(long long T, int D, int F, int dtype, bool backward, bool keep) {
     FfnSpace s = {};
     const size_t td = (size_t)T * D, tf = (size_t)T * F, df = (size_t)D * F;
     size_t off = 0;
@@ -134,7 +135,7 @@ static FfnSpace ffn_space(long long T, int D, int F, int dtype, bool backward) {
         return at;
     };
     const size_t es = dtype == IDA_BF16 ? 2 : 4;
-    if (!backward) s.h = take(tf * (T <= kFewRows ? 4 : es));  // (few rows' h: two parts)
+    if (!backward && (T <= kFewRows || !keep)) s.h = take(tf * (T <= kFewRows ? 4 : es));  // (few rows' h: two parts)
     if (backward) s.dgu = take(2 * tf * es);
     if (dtype == IDA_F32 && !on_cuda_cores(T, D, F)) {
         s.xs = take(6 * td);
@@ -198,14 +199,14 @@ static ida_status check_ffn(int rows, int D, int F, long long ldx, int dtype) {
 
 extern "C" {
 
-size_t ida_ffn_workspace_bytes(int rows, int D, int F, int dtype) {
+size_t ida_ffn_workspace_bytes(int rows, int D, int F, int dtype, int keep) {
     if (rows < 1 || D < 8 || F < 8 || D > 65536 || F > 65536 || (D % 8) || (F % 8) || (dtype != IDA_F32 && dtype != IDA_BF16)) return 0;
-    return ida::ffn_space(rows, D, F, dtype, false).total;
+    return ida::ffn_space(rows, D, F, dtype, false, keep != 0).total;
 }
 
 size_t ida_ffn_backward_workspace_bytes(int rows, int D, int F, int dtype) {
     if (rows < 1 || D < 8 || F < 8 || D > 65536 || F > 65536 || (D % 8) || (F % 8) || (dtype != IDA_F32 && dtype != IDA_BF16)) return 0;
-    return ida::ffn_space(rows, D, F, dtype, true).total;
+    return ida::ffn_space(rows, D, F, dtype, true, true).total;
 }
 
 ida_status ida_ffn(const void *x, const void *w_gate, const void *w_up, const void *w_down, void *out, void *acts, int rows, int D,
@@ -215,16 +216,18 @@ ida_status ida_ffn(const void *x, const void *w_gate, const void *w_up, const vo
     if (s != IDA_OK) return s;
     if (rows == 0) return IDA_OK;
     if (rows == 1) ldx = D;
-    const void *ptrs[] = {x, w_gate, w_up, w_down, out, workspace};
+    const FfnSpace sp = ffn_space(rows, D, F, dtype, false, acts != nullptr);
+    const void *ptrs[] = {x, w_gate, w_up, w_down, out};
     for (const void *p : ptrs) {
-        if (!p) return fail_with(IDA_ERR_ARG, "null input, output or workspace pointer");
+        if (!p) return fail_with(IDA_ERR_ARG, "null input or output pointer");
         if (misaligned16(p)) return fail_with(IDA_ERR_ARG, "pointers must be 16-byte aligned");
     }
     if (misaligned16(acts)) return fail_with(IDA_ERR_ARG, "acts must be 16-byte aligned");
-    const FfnSpace sp = ffn_space(rows, D, F, dtype, false);
+    if (sp.total > 0 && (!workspace || misaligned16(workspace)))
+        return fail_with(IDA_ERR_ARG, "workspace must be a 16-byte aligned pointer");
     if (workspace_bytes < sp.total) return fail_with(IDA_ERR_ARG, "workspace is smaller than ida_ffn_workspace_bytes");
     const size_t es = dtype == IDA_BF16 ? 2 : 4, td = (size_t)rows * D, tf = (size_t)rows * F, df = (size_t)D * F;
-    const Rows outs[] = {dense("out", out, td * es), dense("acts", acts, 3 * tf * es), dense("workspace", workspace, sp.total)};
+    const Rows outs[] = {dense("out", out, td * es), dense("acts", acts, 3 * tf * es), dense("workspace", sp.total ? workspace : nullptr, sp.total)};
     const Rows ins[] = {rows_of("x", x, ldx, D, rows, dtype), dense("w_gate", w_gate, df * es), dense("w_up", w_up, df * es),
                         dense("w_down", w_down, df * es)};
     s = check_overlaps(outs, ins);
@@ -309,7 +312,7 @@ ida_status ida_ffn_backward(const void *x, const void *w_gate, const void *w_up,
     void *dw[] = {dw_gate, dw_up, dw_down};
     for (const void *p : dw)
         if (!p || misaligned16(p)) return fail_with(IDA_ERR_ARG, "weight gradients must be 16-byte aligned pointers");
-    const FfnSpace sp = ffn_space(rows, D, F, dtype, true);
+    const FfnSpace sp = ffn_space(rows, D, F, dtype, true, true);
     if (rows > 0) {
         const void *ptrs[] = {x, w_gate, w_up, w_down, acts, dout, dx, workspace};
         for (const void *p : ptrs) {

@@ -14,6 +14,8 @@ ARG, UNS, OK, CUDA = binding.IDA_ERR_ARG, binding.IDA_ERR_UNSUPPORTED, binding.I
 T, D, F = 300, 256, 384
 X, DF, TF = 2 * T * D, 2 * D * F, 2 * T * F
 KB, FB = D // 128, F // 128
+FEW = 6  # rows of the block's call: of few, the workspace is needed beside acts
+FX, FTF = 2 * FEW * D, 2 * FEW * F
 
 
 @pytest.fixture(scope="module")
@@ -24,8 +26,8 @@ def lib():
 
 # call: (arguments in their order, {output: bytes}, {input: bytes}, the rest by name)
 CALLS = {
-    "ida_ffn": ("x wg wu wd out acts", dict(out=X, acts=3 * TF, ws=None), dict(x=X, wg=DF, wu=DF, wd=DF),
-                dict(rows=T, D=D, F=F, ldx=D, dtype=1, ws="ws", n=1 << 40, stream=None)),
+    "ida_ffn": ("x wg wu wd out acts", dict(out=FX, acts=3 * FTF, ws=None), dict(x=FX, wg=DF, wu=DF, wd=DF),
+                dict(rows=FEW, D=D, F=F, ldx=D, dtype=1, ws="ws", n=1 << 40, stream=None)),
     "ida_ffn_backward": ("x wg wu wd acts dout dx dwg dwu dwd", dict(dx=X, dwg=DF, dwu=DF, dwd=DF, ws=None),
                          dict(x=X, wg=DF, wu=DF, wd=DF, acts=3 * TF, dout=X),
                          dict(rows=T, D=D, F=F, ldx=D, dtype=1, ws="ws", n=1 << 40, stream=None)),
@@ -41,8 +43,8 @@ CALLS = {
 def _sizes(name):
     outs = dict(CALLS[name][1])
     if "ws" in outs:
-        outs["ws"] = {"ida_ffn": binding.ida_ffn_workspace_bytes,
-                      "ida_ffn_backward": binding.ida_ffn_backward_workspace_bytes}[name](T, D, F, 1)
+        outs["ws"] = (binding.ida_ffn_workspace_bytes(FEW, D, F, 1, True) if name == "ida_ffn" else
+                      binding.ida_ffn_backward_workspace_bytes(T, D, F, 1))
     return outs, CALLS[name][2]
 
 
@@ -82,6 +84,9 @@ def test_sizes_and_pointers(lib, name):
             assert _call(lib, name, {**at, k: None}) == ARG, k
         for off in (1, 4, 8):
             assert _call(lib, name, {**at, k: at[k] + off}) == ARG and "aligned" in binding.ida_last_error(), (k, off)
+    if name == "ida_ffn":  # more rows need none beside acts
+        assert _call(lib, name, {**at, "ws": None}, rows=T, n=0) == CUDA
+        assert _call(lib, name, {**at, "ws": None, "acts": None}, rows=T, n=0) == ARG
     if "ws" in at:
         assert _call(lib, name, {**at, "ws": None}) == ARG and _call(lib, name, {**at, "ws": at["ws"] + 4}) == ARG
     assert _call(lib, name, at) == CUDA  # nothing else is wrong with it
@@ -116,6 +121,9 @@ def test_no_rows(lib):
 
 
 def test_workspaces(lib):
+    keep = binding.ida_ffn_workspace_bytes
+    assert keep(300, 256, 384, 1, True) == 0 and keep(300, 256, 384, 0, True) == 0  # acts take the hidden product
+    assert keep(5, 256, 384, 1, True) > 0 and keep(5000, 256, 384, 0, True) > 0  # in two parts; fp32's parts
     for fn in (binding.ida_ffn_workspace_bytes, binding.ida_ffn_backward_workspace_bytes):
         for bad in [(0, 64, 64, 1), (-1, 64, 64, 1), (5, 60, 64, 1), (5, 64, 0, 1), (5, 64, 64, 2), (5, 65544, 64, 1)]:
             assert fn(*bad) == 0
