@@ -1,5 +1,6 @@
 """GB300-native Interdomain Attention token mixer (prefill + recurrent decode), and beside it a
-selective mixer (short convolution, selective scan, one-position step) and the decoder's pre-norm.
+selective mixer (short convolution, selective scan, one-position step), the decoder's pre-norm and its
+gated feed-forward block, with products in 8 bits.
 
 The compute path is the CUDA library ``libida.so`` (built from ``csrc/``);
 ``binding`` marshals torch tensors into its C ABI.  Importing this package
