@@ -3,7 +3,7 @@ streams, captured and replayed, with workspaces of any contents, far and many ro
 import pytest
 import torch
 
-from linear_token_mixer_sc_gb300 import binding
+from linear_token_mixer_sc_gb300 import binding, inputs
 from tests import ffn_cases as fc
 from tests.ssm_cases import DT, HALF, gen, worst
 
@@ -86,6 +86,29 @@ def test_two_calls_at_once():
                     other = two[m]()
                 _done()
                 assert _same(got, want[k][0]) and _same(other, want[m][1])
+
+
+def test_beside_the_mixers_on_another_stream():
+    """The block and the 8-bit products while the mixer's and the selective mixer's prompts run on another stream."""
+    p = binding.params_to_device(inputs.make_params(H=4, R=64, d=64, M=64, W=4, seed=3))
+    qkv = inputs.make_qkv(2, 1024, 4, 64, 64, "bf16", 4, device="cuda")
+    sp = {"a_log": torch.zeros(4, device="cuda"), "dt_bias": torch.full((4,), -4.0, device="cuda"), "D": torch.ones(4, device="cuda")}
+    bc = torch.randn(2, 1024, 1, 64, generator=gen(5)).bfloat16().cuda()
+    dt = torch.randn(2, 1024, 4, generator=gen(6)).bfloat16().cuda()
+
+    def mixers():
+        return [binding.ida_forward(*qkv, p)[0], binding.ida_ssm_scan(qkv[2], bc, bc, dt, sp)[0]]
+
+    calls = _calls(900, "bf16")
+    want, other = {k: [t.clone() for t in calls[k]()] for k in CALLS}, [t.clone() for t in mixers()]
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    for k in CALLS:
+        with torch.cuda.stream(side):
+            mixed = [mixers() for _ in range(3)]
+        got = [calls[k]() for _ in range(3)]
+        _done()
+        assert all(_same(g, want[k]) for g in got) and all(_same(m, other) for m in mixed), k
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
