@@ -290,7 +290,7 @@ ida_status ida_ffn(const void *x, const void *w_gate, const void *w_up, const vo
         if (s != IDA_OK) return s;
     }
     GemmArgs d = {};
-    d.problems = 1;
+    d.problems = d.back = 1;
     d.M[0] = rows, d.N[0] = D;
     d.kblocks = (F + 63) / 64;
     add_segments(d, dtype, 0, 0);
@@ -413,7 +413,7 @@ ida_status ida_ffn_backward(const void *x, const void *w_gate, const void *w_up,
     if (s == IDA_OK) s = run_gemm(1, 1, kPlain, w, dtype, num_sms, st);
     if (s != IDA_OK) return s;
     GemmArgs d = {};  // dx
-    d.problems = 1;
+    d.problems = d.back = 1;
     d.M[0] = rows, d.N[0] = D;
     d.kblocks = (F + 63) / 64;
     add_segments(d, dtype, 0, 0);
