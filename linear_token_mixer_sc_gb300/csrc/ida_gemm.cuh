@@ -914,7 +914,7 @@ ida_status gemm_launch(GemmArgs &g, int num_sms, cudaStream_t st) {
     if (tiles > 0x7FFFFFFFLL) return fail_with(IDA_ERR_UNSUPPORTED, "too many tiles");
     g.tiles = (int)tiles;
     if (KIND == kDirect) g.chunk = g.segs * g.kblocks;
-    if constexpr (EPI == kPlain && KIND != kParts) {
+    if constexpr (EPI == kPlain) {
         g.split = split_of(tiles, g.segs * g.kblocks, num_sms);
         if (g.split > 1) return gemm_launch_as<AMN, BMN, KIND, EPI, E, true>(g, num_sms, st);
     }
