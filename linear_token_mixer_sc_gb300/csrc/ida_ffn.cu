@@ -106,11 +106,13 @@ static ida_status launch_split(const SplitArgs &a, int count, int num_sms, cudaS
 
 static size_t up256(size_t x) { return (x + 255) & ~(size_t)255; }
 
-// fp32 products on the CUDA cores: few rows, or little arithmetic.  Forward and backward, in us, there and on the tensor
-// cores: 251 rows of 64 and 176 channels 6 + 13 and 19 + 40, 512 of 256 and 512 22 + 53 and 34 + 73, 1024 of 256 and 704
-// (2^27.5) 40 + 92 and 40 + 98, 1024 of 512 and 1024 104 + 209 and 56 + 125; 32 rows of 2048 and 5632 122 + 391 and
-// 267 + 455.
-static bool on_cuda_cores(long long rows, long long D, long long F) { return rows <= 64 || rows * D * F <= (1LL << 27); }
+// fp32 products on the CUDA cores: little arithmetic (and backwards no large weights' gradients), or few rows forwards.  Forward and backward, in us, there and on the
+// tensor cores: 512 rows of 256 and 512 channels 19 + 36 and 30 + 57, 251 of 512 and 1024 (2^27) 34 + 65 and 40 + 71, 1024
+// of 256 and 704 (2^27.5) 40 + 80 and 33 + 64; 64 of 768 and 2048 41 + 86 and 55 + 86; 1 of 2048 and 5632 backwards 328
+// and 252, 32 of them 122 + 341 and 164 + 238, 64 157 + 363 and 165 + 241.
+static bool on_cuda_cores(long long rows, long long D, long long F, bool backward) {
+    return backward ? rows * D * F <= (1LL << 27) && D * F <= (1LL << 21) : rows * D * F <= (1LL << 27) || rows <= 64;
+}
 
 // Operands of the products: the caller's own tensors in bf16, their parts in the workspace otherwise.
 struct Operand {
@@ -137,7 +139,7 @@ static FfnSpace ffn_space(long long T, int D, int F, int dtype, bool backward, b
     const size_t es = dtype == IDA_BF16 ? 2 : 4;
     if (!backward && (T <= kFewRows || !keep)) s.h = take(tf * (T <= kFewRows ? 4 : es));  // (few rows' h: two parts)
     if (backward) s.dgu = take(2 * tf * es);
-    if (dtype == IDA_F32 && !on_cuda_cores(T, D, F)) {
+    if (dtype == IDA_F32 && !on_cuda_cores(T, D, F, backward)) {
         s.xs = take(6 * td);
         s.wg = take(6 * df);
         s.wu = take(6 * df);
@@ -249,7 +251,7 @@ ida_status ida_ffn(const void *x, const void *w_gate, const void *w_up, const vo
         SkinnyArgs b = {ws + sp.h, F, w_down, nullptr, out, nullptr, nullptr, nullptr, nullptr, nullptr, rows, F, D, dtype == IDA_F32, true};
         return skinny_product(b, type, num_sms, st);
     }
-    if (dtype == IDA_F32 && on_cuda_cores(rows, D, F)) {
+    if (dtype == IDA_F32 && on_cuda_cores(rows, D, F, false)) {
         float *fh = static_cast<float *>(h), *fa = reinterpret_cast<float *>(ac);
         SimtArgs a = {{static_cast<const float *>(x)}, {static_cast<const float *>(w_gate), static_cast<const float *>(w_up)}, {ldx}, {D},
                       {fh, fa, fa ? fa + tf : nullptr}, nullptr, nullptr, {rows}, {F}, D, 1, 1};
@@ -343,7 +345,7 @@ ida_status ida_ffn_backward(const void *x, const void *w_gate, const void *w_up,
     char *ws = static_cast<char *>(workspace);
     const char *ac = static_cast<const char *>(acts);
     char *dg = ws + sp.dgu, *du = dg + tf * es;
-    if (dtype == IDA_F32 && on_cuda_cores(rows, D, F)) {
+    if (dtype == IDA_F32 && on_cuda_cores(rows, D, F, true)) {
         const float *fx = static_cast<const float *>(x), *fy = static_cast<const float *>(dout), *fa = reinterpret_cast<const float *>(ac);
         float *fg = reinterpret_cast<float *>(dg), *fu = reinterpret_cast<float *>(du);
         SimtArgs a = {{fy}, {static_cast<const float *>(w_down)}, {D}, {F}, {fg, fu}, fa, fa + tf, {rows}, {F}, D, 1, 1};

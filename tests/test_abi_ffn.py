@@ -128,9 +128,9 @@ def test_workspaces(lib):
         for bad in [(0, 64, 64, 1), (-1, 64, 64, 1), (5, 60, 64, 1), (5, 64, 0, 1), (5, 64, 64, 2), (5, 65544, 64, 1)]:
             assert fn(*bad) == 0
         assert 0 < fn(7, 64, 64, 1) <= fn(7, 64, 64, 0) < fn(700, 64, 64, 0) < fn(70000, 64, 64, 0)
-        assert fn(1, 2048, 5632, 0) < 1 << 20  # no parts of weights where no product takes them
         with pytest.raises(ValueError, match="2\\^31"):
             fn(1 << 31, 64, 64, 1)
+    assert keep(1, 2048, 5632, 0) < 1 << 20  # no parts of weights where no product takes them
     assert binding.ida_ffn_workspace_bytes(300, 256, 384, 1) >= 300 * 384 * 2
 
 

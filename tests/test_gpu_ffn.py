@@ -11,7 +11,7 @@ pytestmark = pytest.mark.gpu
 # rows, channels, hidden channels: one row, tiles that end anywhere, contractions shorter than a block
 SIZES = [(1, 8, 8), (1, 64, 176), (2, 128, 344), (7, 40, 24), (8, 2048, 5632), (9, 264, 520), (16, 72, 1000), (31, 200, 72), (33, 64, 64), (128, 64, 128), (129, 72, 136), (251, 64, 176),
          (256, 256, 256), (300, 520, 264), (513, 768, 520), (1000, 136, 1032),
-         (40, 72, 2056), (300, 264, 2304), (1500, 520, 1096), (2100, 64, 72)]  # contractions shared by pairs of SMs
+         (40, 72, 2056), (40, 1024, 3328), (300, 264, 2304), (1500, 520, 1096), (2100, 64, 72)]  # contractions shared by pairs of SMs
 
 
 def _inputs(T, D, F, dtype, seed=0):
