@@ -106,10 +106,11 @@ static ida_status launch_split(const SplitArgs &a, int count, int num_sms, cudaS
 
 static size_t up256(size_t x) { return (x + 255) & ~(size_t)255; }
 
-// fp32 products on the CUDA cores: little arithmetic (and backwards no large weights' gradients), or few rows forwards.  Forward and backward, in us, there and on the
-// tensor cores: 512 rows of 256 and 512 channels 19 + 36 and 30 + 57, 251 of 512 and 1024 (2^27) 34 + 65 and 40 + 71, 1024
-// of 256 and 704 (2^27.5) 40 + 80 and 33 + 64; 64 of 768 and 2048 41 + 86 and 55 + 86; 1 of 2048 and 5632 backwards 328
-// and 252, 32 of them 122 + 341 and 164 + 238, 64 157 + 363 and 165 + 241.
+// fp32 products on the CUDA cores: little arithmetic (and backwards no large weights' gradients), or few rows
+// forwards.  Forward and backward, in us, there and on the tensor cores: 512 rows of 256 and 512 channels 19 + 36 and
+// 30 + 57, 251 of 512 and 1024 (2^27) 34 + 65 and 40 + 71, 1024 of 256 and 704 (2^27.5) 40 + 80 and 33 + 64; 64 of 768
+// and 2048 41 + 86 and 55 + 86; 1 of 2048 and 5632 backwards 328 and 252, 32 of them 122 + 341 and 164 + 238, 64
+// 157 + 363 and 165 + 241.
 static bool on_cuda_cores(long long rows, long long D, long long F, bool backward) {
     return backward ? rows * D * F <= (1LL << 27) && D * F <= (1LL << 21) : rows * D * F <= (1LL << 27) || rows <= 64;
 }
