@@ -537,7 +537,10 @@ __device__ __forceinline__ uint32_t e4m3x4(const float *x) {
 // kE4M3, kGate: the product's 64 columns of a thread, a scale for its row's 128 with the warp of the other half.
 // Each warp's box is 32 rows of 64 bytes (swizzled over 64 bytes); behind it lie its rows' maxima for the other
 // warp, which reads them once this one has arrived on its barrier (and before it arrives itself for the next
-// tile, so that two sets are enough).  n: tiles before this one.
+// tile, so that two sets are enough).  The barriers are two, taken in turn: a warp arrives before it waits, and
+// with one the other might arrive again, for the next tile, before this one has seen that the phase it waits for is
+// over; for tile n + 2 the other arrives behind its wait for n + 1, which ends when this one has waited for n.
+// n: tiles before this one.
 __device__ __forceinline__ bool epi_gate_e4m3(const GemmArgs &g, const EpiWarp &w, const GemmTile &t, float (&x)[128], int n) {
     float top = 0.f;
 #pragma unroll
@@ -550,8 +553,8 @@ __device__ __forceinline__ bool epi_gate_e4m3(const GemmArgs &g, const EpiWarp &
     const int at = GSLAB / 2 + (n & 1) * 128, other = w.half ? -4 : 4;  // warps to the other half's
     reinterpret_cast<float *>(slab + at)[w.lane] = top;
     __syncwarp();
-    if (w.lane == 0) arrive_local(w.in + other * 2);
-    if (!pair_wait(w.in, n & 1, g.err)) return false;
+    if (w.lane == 0) arrive_local(w.in + other * 2 + (n & 1));
+    if (!pair_wait(w.in + (n & 1), n >> 1 & 1, g.err)) return false;
     top = fmaxf(top, reinterpret_cast<const float *>(slab + at + other * GSLAB)[w.lane]);
     float up;
     const float sc = e4m3_scale(top, up), is = 1.f / (sc * up);
