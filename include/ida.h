@@ -514,9 +514,10 @@ IDA_API size_t ida_rmsnorm_backward_workspace_bytes(int rows, int D);
  *   workspace at least ida_ffn_workspace_bytes(...) bytes (NULL allowed where that is 0; contents on entry
  *             ignored).
  * Supported: D and F multiples of 8 up to 65536, rows up to 2^28 with rows * max(D, F) <= 2^36.
- * Sums are fp32.  With IDA_BF16 h is rounded to bf16 between the products (not of up to 8 rows); with IDA_F32 the operands of the
- * products are taken apart into three bf16 parts each, whose products above 2^-24 of the whole are all
- * taken.  Non-finite inputs make the rows of out that they reach (all of them for a weight) unspecified.
+ * Sums are fp32; those of tensor cores are cut off towards zero by up to 2^-23 every 16 elements, over at most 4096
+ * elements (over a row's D channels for g, u and, backwards, dh with IDA_BF16).  With IDA_BF16 h is rounded to bf16
+ * between the products (not of up to 8 rows); with IDA_F32 the operands of the products are taken apart into three
+ * bf16 parts each, whose products above 2^-24 of the whole are all taken.  Non-finite inputs make the rows of out that they reach (all of them for a weight) unspecified.
  * Outputs (the workspace among them) that share bytes with inputs or with one another are refused.
  */
 IDA_API ida_status ida_ffn(const void *x, const void *w_gate, const void *w_up, const void *w_down, void *out,

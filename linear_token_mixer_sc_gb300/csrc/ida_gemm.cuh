@@ -10,8 +10,10 @@
 //
 // Warps: 0 loads, 1 issues the MMAs (of the even CTA), the others are the epilogue's.  The direct kind
 // accumulates a whole tile in TMEM.  The others take the accumulator out every `chunk` contraction
-// blocks and add it up in registers, scaled: in e4m3 because each block of 128 has scales of its own,
-// for fp32 inputs (three bf16 parts, six products) because the tensor cores round sums towards zero.
+// blocks and add it up in registers, scaled in e4m3, where each block of 128 has scales of its own: the
+// tensor cores cut a running sum off, by up to 2^-23 of it every 16 elements and always towards zero, which
+// fp32 inputs (three bf16 parts, six products) show after 512 elements and bf16 results after many rows (weights'
+// gradients of one sign over 2^20 rows came out 1.6e-3 too small).
 #pragma once
 
 #include <cuda.h>
@@ -22,25 +24,24 @@
 
 namespace ida {
 
-enum { kDirect = 0, kParts = 1, kE4M3 = 2 };          // operands: bf16, three bf16 parts of fp32, e4m3
+enum { kDirect = 0, kSums = 1, kE4M3 = 2 };           // bf16 (or parts) summed in TMEM, or in registers by chunks; e4m3
 enum { kPlain = 0, kGate = 1, kGateBwd = 2 };         // epilogues
 constexpr int GOP = 128 * 128;                        // bytes of an operand of a stage
 constexpr int GSLAB = 32 * 128;                       // bytes of a warp's staged box: 32 rows of 128 bytes
-// Warps of the epilogue.  A plain direct product's four are enough and eight lose 3 %; the gate's and its gradients'
-// have work for eight (gradients of 16384 rows of 768 and 2048 channels 61 us with four, 55 with eight).  Sums in
-// registers are eight warps', 128 a thread (14336 rows' gated projection in 8 bits 247 us; 280 with sixteen warps and
-// 64, 307 with those and halves of the accumulator released by themselves: an MMA of half the columns reads A
-// again, and shared memory cannot feed that).
-constexpr int gemm_warps(int kind, int epi) { return kind == kDirect && epi == kPlain ? 4 : 8; }
-constexpr int gemm_threads(int kind, int epi) { return (kind == kDirect ? 64 : 128) + 32 * gemm_warps(kind, epi); }
+// Warps of the epilogue.  The gate's and its gradients' have work for eight (gradients of 16384 rows of 768 and 2048
+// channels 61 us with four, 55 with eight).  Sums in registers are eight warps', 128 a thread (14336 rows' gated
+// projection in 8 bits 247 us; 280 with sixteen warps and 64, 307 with those and halves of the accumulator released by
+// themselves: an MMA of half the columns reads A again, and shared memory cannot feed that).
+constexpr int GEW = 8;
+constexpr int gemm_threads(int kind) { return (kind == kDirect ? 64 : 128) + 32 * GEW; }
 // Boxes that a warp stages, and the stages that shared memory has left for operands
 constexpr int gemm_boxes(int epi) { return epi == kGateBwd ? 2 : 1; }
-constexpr int gemm_staging(int kind, int epi) { return gemm_warps(kind, epi) * gemm_boxes(epi) * GSLAB; }
-constexpr int gemm_stages(int kind, int epi) {
-    const int n = (227 * 1024 - 1024 - 512 - gemm_staging(kind, epi)) / (2 * GOP);
+constexpr int gemm_staging(int epi) { return GEW * gemm_boxes(epi) * GSLAB; }
+constexpr int gemm_stages(int epi) {
+    const int n = (227 * 1024 - 1024 - 512 - gemm_staging(epi)) / (2 * GOP);
     return n < 6 ? n : 6;
 }
-constexpr int gemm_smem(int kind, int epi) { return gemm_stages(kind, epi) * 2 * GOP + gemm_staging(kind, epi) + 1024 + 512; }
+constexpr int gemm_smem(int epi) { return gemm_stages(epi) * 2 * GOP + gemm_staging(epi) + 1024 + 512; }
 constexpr int GST = 6;                                // stages at most
 
 struct GemmSeg {
@@ -326,22 +327,6 @@ __device__ __forceinline__ void release_acc(const EpiWarp &w, uint32_t release) 
     if (w.lane == 0) arrive_remote(release);
 }
 
-// Direct kind, kPlain: 256 columns in bf16.
-__device__ __forceinline__ void epi_plain(const GemmArgs &g, const EpiWarp &w, const GemmTile &t, uint32_t acc, uint32_t release) {
-    const int row = t.row0 + w.rank * 128 + w.q * 32;
-#pragma unroll
-    for (int c = 0; c < 8; ++c) {
-        uint32_t r[32];
-        tmem_ld32(acc + c * 32, r);
-        tc::tmem_wait_ld();
-        tmem_use(r);
-        if (c == 7) release_acc(w, release);
-#pragma unroll
-        for (int k = 0; k < 4; ++k) stage<__nv_bfloat16>(w.staging, w.lane, c % 2 * 4 + k, reinterpret_cast<const float *>(r) + 8 * k);
-        if (c % 2) store_box<__nv_bfloat16>(w.staging, g.out[t.p], g.M[t.p], g.N[t.p], row, t.col0 + c / 2 * 64, w.lane);
-    }
-}
-
 // Direct kind, kGate: columns c and 128 + c are the factors of the product's column c; 64 of them a warp.
 __device__ __forceinline__ void epi_gate(const GemmArgs &g, const EpiWarp &w, const GemmTile &t, uint32_t acc, uint32_t release) {
     using E = __nv_bfloat16;
@@ -582,10 +567,10 @@ static_assert(sizeof(GemmBars) <= 512, "shared memory budget");
 // part of the contraction.  Each CTA lays its 128 x 256 fp32 sums where its operands were, [column / 4][row] so
 // that a warp's 16-byte accesses lie side by side, and adds up its share of the columns over the pairs, in
 // their order.  (256 rows of 5632 channels to 2048, eight tiles: 12 us in four parts, 28 in one.)
-template <int EW, typename E>
+template <typename E>
 __device__ __forceinline__ void add_parts(const GemmArgs &g, const EpiWarp &w, const GemmTile &t, const char *part, int group, int split) {
     const int r = w.q * 32 + w.lane, row = t.row0 + w.rank * 128 + r, own = (int)cluster_rank() >> 1;
-    const int cols = 256 / split / (EW / 4), c0 = own * (256 / split) + group * cols;
+    const int cols = 256 / split / (GEW / 4), c0 = own * (256 / split) + group * cols;
     if (row >= g.M[t.p]) return;
     E *out = static_cast<E *>(g.out[t.p]) + (long long)row * g.N[t.p] + t.col0;
     for (int c = c0; c < c0 + cols && t.col0 + c < g.N[t.p]; c += 8) {
@@ -602,10 +587,10 @@ __device__ __forceinline__ void add_parts(const GemmArgs &g, const EpiWarp &w, c
 }
 
 template <int AMN, int BMN, int KIND, int EPI, typename E, bool SPLIT>
-__global__ void __launch_bounds__(gemm_threads(KIND, EPI), 1) gemm_kernel(const __grid_constant__ GemmArgs g) {
+__global__ void __launch_bounds__(gemm_threads(KIND), 1) gemm_kernel(const __grid_constant__ GemmArgs g) {
     constexpr bool E8 = KIND == kE4M3;
-    constexpr int ST = gemm_stages(KIND, EPI), STAGING = gemm_staging(KIND, EPI);
-    constexpr int EW = gemm_warps(KIND, EPI), E0 = KIND == kDirect ? 2 : 4, COLS = tile_cols(EPI), KB = E8 ? 128 : 64;
+    constexpr int ST = gemm_stages(EPI), STAGING = gemm_staging(EPI);
+    constexpr int EW = GEW, E0 = KIND == kDirect ? 2 : 4, COLS = tile_cols(EPI), KB = E8 ? 128 : 64;
     extern __shared__ char raw[];
     char *sm = raw + ((1024 - (tc::smem_u32(raw) & 1023)) & 1023);
     char *ops = sm, *staging = sm + ST * 2 * GOP;
@@ -749,19 +734,6 @@ __global__ void __launch_bounds__(gemm_threads(KIND, EPI), 1) gemm_kernel(const 
                 if (!(ok = pair_wait(&bar.acc_full[ab], ch >> 1 & 1, g.err))) break;
                 tc::tc_fence_after();
                 const uint32_t acc = w.tmem + ab * 256, release = lead_addr(&bar.acc_empty[ab]);
-                if constexpr (SPLIT) {
-#pragma unroll 1
-                    for (int c = 0; c < 256; c += 32) {
-                        uint32_t r[32];
-                        tmem_ld32(acc + c, r);
-                        tc::tmem_wait_ld();
-                        tmem_use(r);
-#pragma unroll
-                        for (int e = 0; e < 32; e += 4)
-                            *reinterpret_cast<uint4 *>(ops + ((c + e) / 4 * 128 + w.q * 32 + lane) * 16) = make_uint4(r[e], r[e + 1], r[e + 2], r[e + 3]);
-                    }
-                } else if constexpr (EPI == kPlain)
-                    epi_plain(g, w, tile, acc, release);
                 if constexpr (EPI == kGate) epi_gate(g, w, tile, acc, release);
                 if constexpr (EPI == kGateBwd) {
                     GemmTile next = {0, 0, -1};
@@ -860,7 +832,7 @@ __global__ void __launch_bounds__(gemm_threads(KIND, EPI), 1) gemm_kernel(const 
             w.lane = lane;
             w.q = warp & 3;
             w.rank = rank;
-            add_parts<EW, E>(g, w, tile_of(g, pair, COLS), ops, (warp - E0) >> 2, g.split);
+            add_parts<E>(g, w, tile_of(g, pair, COLS), ops, (warp - E0) >> 2, g.split);
         }
         __syncthreads();
         cluster_sync_all();  // the other pairs have read this one's sums
@@ -889,13 +861,13 @@ inline int split_of(long long tiles, int blocks, int num_sms) {
 template <int AMN, int BMN, int KIND, int EPI, typename E, bool SPLIT>
 ida_status gemm_launch_as(GemmArgs &g, int num_sms, cudaStream_t st) {
     const auto kernel = gemm_kernel<AMN, BMN, KIND, EPI, E, SPLIT>;
-    constexpr int smem = gemm_smem(KIND, EPI);
+    constexpr int smem = gemm_smem(EPI);
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return fail_with(IDA_ERR_CUDA, cudaGetErrorString(e));
     const long long pairs = SPLIT ? (long long)g.tiles * g.split : g.tiles < num_sms / 2 ? g.tiles : num_sms / 2;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(2 * pairs));
-    cfg.blockDim = dim3(gemm_threads(KIND, EPI));
+    cfg.blockDim = dim3(gemm_threads(KIND));
     cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
     cudaLaunchAttribute at[2];

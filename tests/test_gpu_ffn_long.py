@@ -1,0 +1,51 @@
+"""Gradients of the feed-forward block's weights over many rows, where a sum's own error counts."""
+import pytest
+import torch
+
+from linear_token_mixer_sc_gb300 import binding
+from tests.ssm_cases import DT
+
+pytestmark = pytest.mark.gpu
+
+
+def _case(T, D, F, dtype, seed=1):
+    """Inputs of one sign, so that every product adds to its sum, in channels of unlike size, so that results lie anywhere
+    between two neighbours of their type; and the weights' gradients in 64 bits."""
+    g = torch.Generator("cuda").manual_seed(seed)
+
+    def positive(rows, cols):
+        size = torch.exp2(2 * torch.rand(cols, generator=g, device="cuda"))
+        return ((0.5 + torch.rand(rows, cols, generator=g, device="cuda")) * size).to(DT[dtype])
+
+    x, dy, wd = positive(T, D), positive(T, D), positive(D, F) / D
+    wg, wu = torch.zeros(2, F, D, dtype=DT[dtype], device="cuda")  # (dx is not looked at)
+    acts = torch.empty(3, T, F, dtype=DT[dtype], device="cuda")
+    for a in acts:
+        a.copy_(positive(T, F))
+    want = {k: 0 for k in ("w_gate", "w_up", "w_down")}
+    for r in range(0, T, 1 << 18):
+        gate, up, h = acts[:, r:r + (1 << 18)].double().unbind()
+        s, y, xr = torch.sigmoid(gate), dy[r:r + (1 << 18)].double(), x[r:r + (1 << 18)].double()
+        dh = y @ wd.double()
+        want["w_gate"] += (dh * up * s * (1 + gate * (1 - s))).t() @ xr
+        want["w_up"] += (dh * gate * s).t() @ xr
+        want["w_down"] += y.t() @ h
+    return (x, wg, wu, wd, acts, dy), want
+
+
+@pytest.mark.parametrize("T,D,F", [(1 << 20, 64, 64), (1 << 18, 1024, 1024), (70001, 200, 328)])
+def test_bf16_sums_over_many_rows(T, D, F):
+    """Sums keep their size however many rows they have.  Tensor cores cut a running sum off by less than 2^-23 of it
+    every 16 rows: of 4096 rows by less than 2^-15, and the sums of 4096 rows each are added in fp32, at most
+    2^-24 of the whole each, 2^-16 for 2^20 rows.  The results' own roundings, 2^-8 each at most, are of either sign:
+    their mean over at least 4096 results is below 6 / sqrt(3 * 4096) 2^-9 (the least step's half is 2^-9 of the value),
+    about 2^-13; so are those of dg and du, over the rows as well."""
+    args, want = _case(T, D, F, "bf16")
+    got = binding.ida_ffn_backward(*args)
+    torch.cuda.synchronize()
+    assert binding.ida_device_error() == 0
+    for k, v in want.items():
+        rel = got[k].double() / v - 1
+        assert abs(float(rel.mean())) <= 2.0 ** -12, k
+        # dg and du are rounded too, each 2^-8 at most; w_down's inputs are given
+        assert float(rel.abs().max()) <= 2.0 ** -8 * (1 if k == "w_down" else 2) + 2.0 ** -14, k
