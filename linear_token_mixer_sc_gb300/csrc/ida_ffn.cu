@@ -106,13 +106,17 @@ static ida_status launch_split(const SplitArgs &a, int count, int num_sms, cudaS
 
 static size_t up256(size_t x) { return (x + 255) & ~(size_t)255; }
 
-// fp32 products on the CUDA cores: little arithmetic (and backwards no large weights' gradients), or few rows
-// forwards.  Forward and backward, in us, there and on the tensor cores: 512 rows of 256 and 512 channels 19 + 36 and
-// 30 + 57, 251 of 512 and 1024 (2^27) 34 + 65 and 40 + 71, 1024 of 256 and 704 (2^27.5) 40 + 80 and 33 + 64; 64 of 768
-// and 2048 41 + 86 and 55 + 86; 1 of 2048 and 5632 backwards 328 and 252, 32 of them 122 + 341 and 164 + 238, 64
-// 157 + 363 and 165 + 241.
+// fp32 products on the CUDA cores: little arithmetic (and backwards no large weights' gradients), or few rows forwards,
+// or backwards few channels, whose gradients have few tiles.  In us, there and on the tensor cores, forward and backward:
+// 512 rows of 256 and 512 channels 19 + 36 and 30 + 57, 251 of 512 and 1024 (2^27) 34 + 65 and 40 + 71, 1024 of 256 and
+// 704 (2^27.5) 40 + 80 and 33 + 64, 1 of 2048 and 5632 backwards 328 and 252, 32 of them 122 + 341 and 164 + 238, 64
+// 157 + 363 and 165 + 241.  Backwards by channels, 64 rows: of 512 and 1024 44 and 62, 1024 and 1408 73 and 85, 768 and
+// 2048 87 and 89, 1024 and 2048 (2^21) 109 and 102, 1024 and 2816 150 and 119 (the same of 8 rows within 5 %; only
+// of 256 and 4096 124 and 97); many rows: 2^22 of 8 and 8 2891 and 31482, 2^18 of 32 and 64 315 and 1938, 2^17 of 128
+// and 128 (2^14) 812 and 1129, 2^14 of them 112 and 166, of 128 and 256 209 and 182.
 static bool on_cuda_cores(long long rows, long long D, long long F, bool backward) {
-    return backward ? rows * D * F <= (1LL << 27) && D * F <= (1LL << 21) : rows * D * F <= (1LL << 27) || rows <= 64;
+    const long long all = rows * D * F;
+    return backward ? (all <= (1LL << 27) && D * F <= (1LL << 21)) || D * F <= (1LL << 14) : all <= (1LL << 27) || rows <= 64;
 }
 
 // Operands of the products: the caller's own tensors in bf16, their parts in the workspace otherwise.
@@ -124,7 +128,7 @@ struct Operand {
 
 struct FfnSpace {
     size_t h, xs, wg, wu, wd, hs, total;                // forwards
-    size_t dgu, dys, dgs, dus;                          // backwards
+    size_t dgu, dys, dgs, dus, dws;                     // backwards
 };
 
 // keep: the caller's acts take h
@@ -151,6 +155,9 @@ static FfnSpace ffn_space(long long T, int D, int F, int dtype, bool backward, b
             s.dgs = take(6 * tf);
             s.dus = take(6 * tf);
         }
+    } else if (dtype == IDA_F32 && backward) {
+        const int n = ffn_simt_parts(T, D, F);
+        if (n > 1) s.dws = take(12 * df * n);
     }
     s.total = off;
     return s;
@@ -255,10 +262,10 @@ ida_status ida_ffn(const void *x, const void *w_gate, const void *w_up, const vo
     if (dtype == IDA_F32 && on_cuda_cores(rows, D, F, false)) {
         float *fh = static_cast<float *>(h), *fa = reinterpret_cast<float *>(ac);
         SimtArgs a = {{static_cast<const float *>(x)}, {static_cast<const float *>(w_gate), static_cast<const float *>(w_up)}, {ldx}, {D},
-                      {fh, fa, fa ? fa + tf : nullptr}, nullptr, nullptr, {rows}, {F}, D, 1, 1};
+                      {fh, fa, fa ? fa + tf : nullptr}, nullptr, nullptr, {rows}, {F}, D, 1, 1, 1, 0};
         s = ffn_simt(0, 0, kGate, a, st);
         if (s != IDA_OK) return s;
-        SimtArgs b = {{fh}, {static_cast<const float *>(w_down)}, {F}, {F}, {static_cast<float *>(out)}, nullptr, nullptr, {rows}, {D}, F, 1, 1};
+        SimtArgs b = {{fh}, {static_cast<const float *>(w_down)}, {F}, {F}, {static_cast<float *>(out)}, nullptr, nullptr, {rows}, {D}, F, 1, 1, 1, 0};
         return ffn_simt(0, 0, kPlain, b, st);
     }
     const int parts = dtype == IDA_BF16 ? 1 : 3;
@@ -349,16 +356,21 @@ ida_status ida_ffn_backward(const void *x, const void *w_gate, const void *w_up,
     if (dtype == IDA_F32 && on_cuda_cores(rows, D, F, true)) {
         const float *fx = static_cast<const float *>(x), *fy = static_cast<const float *>(dout), *fa = reinterpret_cast<const float *>(ac);
         float *fg = reinterpret_cast<float *>(dg), *fu = reinterpret_cast<float *>(du);
-        SimtArgs a = {{fy}, {static_cast<const float *>(w_down)}, {D}, {F}, {fg, fu}, fa, fa + tf, {rows}, {F}, D, 1, 1};
+        SimtArgs a = {{fy}, {static_cast<const float *>(w_down)}, {D}, {F}, {fg, fu}, fa, fa + tf, {rows}, {F}, D, 1, 1, 1, 0};
         s = ffn_simt(0, 1, kGateBwd, a, st);
         if (s != IDA_OK) return s;
-        SimtArgs b = {{fg, fu, fy}, {fx, fx, fa + 2 * tf}, {F, F, D}, {ldx, ldx, F},
-                      {static_cast<float *>(dw_gate), static_cast<float *>(dw_up), static_cast<float *>(dw_down)}, nullptr, nullptr,
-                      {F, F, D}, {D, D, F}, rows, 3, 1};
+        float *const to[3] = {static_cast<float *>(dw_gate), static_cast<float *>(dw_up), static_cast<float *>(dw_down)};
+        float *const sums = reinterpret_cast<float *>(ws + sp.dws);
+        const int n = ffn_simt_parts(rows, D, F);
+        SimtArgs b = {{fg, fu, fy}, {fx, fx, fa + 2 * tf}, {F, F, D}, {ldx, ldx, F}, {to[0], to[1], to[2]}, nullptr, nullptr,
+                      {F, F, D}, {D, D, F}, rows, 3, 1, n, (long long)(3 * df)};
+        if (n > 1)
+            for (int p = 0; p < 3; ++p) b.out[p] = sums + p * df;
         s = ffn_simt(1, 1, kPlain, b, st);
+        if (s == IDA_OK && n > 1) s = ffn_simt_add(sums, to, (long long)df, n, st);
         if (s != IDA_OK) return s;
         SimtArgs c = {{fg, fu}, {static_cast<const float *>(w_gate), static_cast<const float *>(w_up)}, {F, F}, {D, D},
-                      {static_cast<float *>(dx)}, nullptr, nullptr, {rows}, {D}, F, 1, 2};
+                      {static_cast<float *>(dx)}, nullptr, nullptr, {rows}, {D}, F, 1, 2, 1, 0};
         return ffn_simt(0, 1, kPlain, c, st);
     }
     const int parts = dtype == IDA_BF16 ? 1 : 3;

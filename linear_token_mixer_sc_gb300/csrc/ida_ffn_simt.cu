@@ -65,7 +65,8 @@ __device__ __forceinline__ void fetch(float (&v)[4][4], const float *s, int t, i
     }
 }
 
-template <int AMN, int BMN, int EPI>
+// PARTS: a block's part of the contraction is that of blockIdx.y
+template <int AMN, int BMN, int EPI, bool PARTS>
 __global__ void __launch_bounds__(256) ffn_simt_kernel(SimtArgs g) {
     extern __shared__ float4 raw4[];
     float *sm = reinterpret_cast<float *>(raw4);
@@ -79,11 +80,13 @@ __global__ void __launch_bounds__(256) ffn_simt_kernel(SimtArgs g) {
     }
     const int tm = (g.M[p] + FT - 1) / FT, row0 = b % tm * FT, col0 = b / tm * COLS, M = g.M[p], N = g.N[p];
     const int t = threadIdx.x, group = t >> 6, tx = t & 7, ty = t >> 3 & 7;
-    const int per = (g.K + FK - 1) / FK, slabs = g.halves * per;
+    const int per = (g.K + FK - 1) / FK, all = g.halves * per;
+    const int first = PARTS ? (int)((long long)all * blockIdx.y / g.parts) : 0;
+    const int slabs = PARTS ? (int)((long long)all * (blockIdx.y + 1) / g.parts) - first : all;
     dependent_wait();  // (letting the next launch start early, too, fills the SMs with its waiting blocks: 509 rows' gradients 22 us, then 40)
     auto load = [&](int i) {
         if (i < slabs) {
-            const int h = i / per, k0 = (i - h * per) * FK;
+            const int h = (first + i) / per, k0 = (first + i - h * per) * FK;
             float *A = sm + i % FST * 2 * FOP, *B = A + FOP;
             slab<AMN>(A, g.a[p + h], g.lda[p + h], row0, M, k0, g.K, t);
             if (EPI == kGate)
@@ -131,7 +134,7 @@ __global__ void __launch_bounds__(256) ffn_simt_kernel(SimtArgs g) {
     const int row = row0 + place<AMN>(ty, group);
     if (row >= M) return;
     if constexpr (EPI == kPlain) {
-        float *o = g.out[p] + (long long)row * N;
+        float *o = g.out[p] + (PARTS ? blockIdx.y * g.part_floats : 0) + (long long)row * N;
         if (BMN) {
             if (col0 + tx * 4 < N) *reinterpret_cast<float4 *>(o + col0 + tx * 4) = make_float4(v[0], v[1], v[2], v[3]);
         } else {
@@ -164,14 +167,14 @@ __global__ void __launch_bounds__(256) ffn_simt_kernel(SimtArgs g) {
     }
 }
 
-template <int AMN, int BMN, int EPI>
+template <int AMN, int BMN, int EPI, bool PARTS = false>
 static ida_status launch_simt(const SimtArgs &a, cudaStream_t st) {
     constexpr int cols = EPI == kGate ? FT / 2 : FT;
     long long blocks = 0;
     for (int p = 0; p < a.problems; ++p) blocks += (long long)((a.M[p] + FT - 1) / FT) * ((a.N[p] + cols - 1) / cols);
-    const auto kernel = ffn_simt_kernel<AMN, BMN, EPI>;
+    const auto kernel = ffn_simt_kernel<AMN, BMN, EPI, PARTS>;
     cudaError_t e = allow_smem(kernel, FSMEM);
-    if (e == cudaSuccess) e = launch_dependent(kernel, dim3((unsigned)blocks), dim3(256), FSMEM, st, a);
+    if (e == cudaSuccess) e = launch_dependent(kernel, dim3((unsigned)blocks, PARTS ? (unsigned)a.parts : 1), dim3(256), FSMEM, st, a);
     if (e != cudaSuccess) return fail_with(IDA_ERR_CUDA, std::string("fp32 product launch: ") + cudaGetErrorString(e));
     return launched("fp32 product");
 }
@@ -179,9 +182,40 @@ static ida_status launch_simt(const SimtArgs &a, cudaStream_t st) {
 ida_status ffn_simt(int a_mn, int b_mn, int epi, const SimtArgs &a, cudaStream_t st) {
     if (epi == kGate) return launch_simt<0, 0, kGate>(a, st);
     if (epi == kGateBwd) return launch_simt<0, 1, kGateBwd>(a, st);
-    if (a_mn) return launch_simt<1, 1, kPlain>(a, st);
+    if (a_mn) return a.parts > 1 ? launch_simt<1, 1, kPlain, true>(a, st) : launch_simt<1, 1, kPlain>(a, st);
     if (b_mn) return launch_simt<0, 1, kPlain>(a, st);
     return launch_simt<0, 0, kPlain>(a, st);
+}
+
+// One block's slabs run one behind the other, some 0.7 us each, so few tiles over many rows are shared by as many blocks
+// as the SMs hold at once (four each), of at least eight slabs; their sums are added in a launch of its own, in order.
+// (Gradients of 2^21 rows of 8 and 8 channels 24353 us in whole, now 1391; of 16384 of 32 and 64 204 and 31, 2048 of them 32
+// and 15.)  A sum in one thread then has fewer terms, too.
+int ffn_simt_parts(long long T, long long D, long long F) {
+    const long long tiles = 3 * ((D + FT - 1) / FT) * ((F + FT - 1) / FT), slabs = (T + FK - 1) / FK;
+    const long long n = 608 / tiles < slabs / 8 ? 608 / tiles : slabs / 8;
+    return n > 1 ? (int)n : 1;
+}
+
+__global__ void __launch_bounds__(128) simt_add_kernel(const float4 *from, float4 *o0, float4 *o1, float4 *o2, long long n, int parts) {
+    const long long e = (long long)blockIdx.x * 128 + threadIdx.x;  // n: pieces of 4 floats in an output
+    dependent_wait();
+    if (e >= 3 * n) return;
+    float4 s = from[e];
+    for (int k = 1; k < parts; ++k) {
+        const float4 v = from[k * 3 * n + e];
+        s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w;
+    }
+    (e < n ? o0 : e < 2 * n ? o1 : o2)[e % n] = s;
+}
+
+ida_status ffn_simt_add(const float *from, float *const (&out)[3], long long n, int parts, cudaStream_t st) {
+    const long long blocks = (3 * n / 4 + 127) / 128;
+    const cudaError_t e = launch_dependent(simt_add_kernel, dim3((unsigned)blocks), dim3(128), 0, st, reinterpret_cast<const float4 *>(from),
+                                           reinterpret_cast<float4 *>(out[0]), reinterpret_cast<float4 *>(out[1]),
+                                           reinterpret_cast<float4 *>(out[2]), n / 4, parts);
+    if (e != cudaSuccess) return fail_with(IDA_ERR_CUDA, std::string("fp32 sums launch: ") + cudaGetErrorString(e));
+    return launched("fp32 sums");
 }
 
 }  // namespace ida

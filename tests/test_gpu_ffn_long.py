@@ -49,3 +49,37 @@ def test_bf16_sums_over_many_rows(T, D, F):
         assert abs(float(rel.mean())) <= 2.0 ** -12, k
         # dg and du are rounded too, each 2^-8 at most; w_down's inputs are given
         assert float(rel.abs().max()) <= 2.0 ** -8 * (1 if k == "w_down" else 2) + 2.0 ** -14, k
+
+
+@pytest.mark.parametrize("T,D,F", [(1 << 21, 8, 8), (65536, 32, 64), (20003, 72, 136), (1500, 40, 24), (1024, 16, 8), (300000, 128, 128), (30000, 128, 136)])
+def test_fp32_sums_over_many_rows(T, D, F):
+    """Weights' gradients of many rows and few channels, in a workspace of NaN and of no more bytes than asked for.
+    On the CUDA cores a thread's sum has a quarter of a part's rows, of at most 1024 rows or a share of them that takes
+    608 blocks; each addition is off by at most 2^-24 of the sum, and all terms have one sign.  dh is a sum of D
+    products; sigmoid and the products behind it are off by less than 2^-19.  On the tensor cores (the last case) 512 rows
+    are summed at a time, below 2^-18 in 32 steps with their alignments, and those sums in fp32, six times over."""
+    args, want = _case(T, D, F, "f32")
+    n = binding.ida_ffn_backward_workspace_bytes(T, D, F, 0)
+    raw = torch.full((n + 131072,), 255, dtype=torch.uint8, device="cuda")
+    got = binding.ida_ffn_backward(*args, workspace=raw[65536:65536 + n])
+    torch.cuda.synchronize()
+    assert binding.ida_device_error() == 0
+    assert bool((raw[:65536] == 255).all()) and bool((raw[65536 + n:] == 255).all())
+    tiles = 3 * -(-D // 32) * -(-F // 32)
+    terms = max(1024, -(-T * tiles // 608) + 64) / 4 + 608 + D if D * F <= 1 << 14 or T * D * F <= 1 << 27 else T / 512 * 6 + 64
+    for k, v in want.items():
+        rel = (got[k].double() / v - 1).abs()
+        assert float(rel.max()) <= terms * 2.0 ** -24 + 2.0 ** -18, k
+
+
+def test_fp32_gradients_of_few_channels_share_their_rows():
+    """2^21 rows of 8 channels (some 0.4 GB to read and write, 1.4 ms): not three blocks that walk all rows (24 ms)."""
+    args, _ = _case(1 << 21, 8, 8, "f32")
+    binding.ida_ffn_backward(*args)
+    start, end = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+    torch.cuda.synchronize()
+    start.record()
+    binding.ida_ffn_backward(*args)
+    end.record()
+    torch.cuda.synchronize()
+    assert start.elapsed_time(end) <= 8
