@@ -27,30 +27,6 @@ struct QuantArgs {
     Divisor blocks;  // of 128 channels in a row (rows times blocks < 2^30)
 };
 
-// Quotients by a scale, rounded as a division rounds them, from its reciprocal: with r = 1 / d to the nearest
-// and q within a unit of x / d, q + r (x - d q) in fused steps is x / d to the nearest (Markstein 1990), where
-// no step underflows; taken as q - r (d q - x), it keeps a zero's sign.  Quotients below 2^-10 are 0 in e4m3, so a scale of 2^-80 and more leaves the residual's
-// bits above 2^-138; smaller ones are multiplied by 2^120 first, and the values with them, exactly.  (Divisions
-// were 10 instructions a value: 4099 rows of 5632 channels took 21 us, now 12.3, with four groups a thread
-// instead of one: 68 % of the copy rate, 75 % of the issue rate.)
-struct Quotient {
-    float up, d, r;
-    __device__ __forceinline__ explicit Quotient(float sc) {
-        up = sc < 0x1p-80f ? 0x1p120f : 1.f;
-        d = sc * up;
-        r = 1.f / d;
-    }
-    __device__ __forceinline__ float operator()(float x) const {
-        x *= up;
-        const float q = x * r;
-        return fmaf(-r, fmaf(d, q, -x), q);
-    }
-};
-__device__ __forceinline__ float quant_scale(float top) {
-    const float sc = top > 0.f ? top / 448.f : 1.f;
-    return sc < 0x1p-126f ? __fdiv_ru(top, 448.f) : sc;
-}
-
 // 8 channels of a row, as they lie in memory
 template <typename E>
 struct Eight {
@@ -73,9 +49,8 @@ struct Eight {
     __device__ __forceinline__ uint2 quantised(const Quotient &by) const {
         float x[8];
         unpack(x);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) x[e] = by(x[e]);
-        return make_uint2(e4m3x4(x), e4m3x4(x + 4));
+        by.scale_up(x);
+        return make_uint2(by.four(x), by.four(x + 4));
     }
 };
 

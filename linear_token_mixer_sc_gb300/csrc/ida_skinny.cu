@@ -192,10 +192,9 @@ __global__ void __launch_bounds__(skinny_warps(E8) * 32, E8 ? 1 : 2) skinny_kern
         cluster_sync_all();
         if (tok < a.T) {
             for (int r = 0; r < 8; ++r) m = fmaxf(m, remote_float(&top[tok], r));
-            float up;
-            const float sc = e4m3_scale(m, up), is = 1.f / (sc * up);
+            const float sc = quant_scale(m);
             if (n0 + c < a.N)
-                static_cast<uint8_t *>(a.out)[tok * (long long)a.N + n0 + c] = __nv_cvt_float_to_fp8(v * up * is, __NV_SATFINITE, __NV_E4M3);
+                static_cast<uint8_t *>(a.out)[tok * (long long)a.N + n0 + c] = Quotient(sc).one(v);
             if (cluster_rank() == 0 && c == 0) a.so[(long long)tok * ((a.N + 127) / 128) + n0 / 128] = sc;
         }
         cluster_sync_all();  // the maxima have been read

@@ -26,3 +26,30 @@ def test_the_quantiser_keeps_signs(block_rows, dtype):
     q, scale = binding.ida_quant_e4m3(x.cuda(), rows=block_rows)
     want, wscale = fc.quantised(x, block_rows)
     assert torch.equal(scale.cpu(), wscale) and torch.equal(_bits(q), _bits(want))
+
+
+def _gate_exact(T, seed):
+    """Operands whose gates are 64 and more (their sigmoid is 1) and whose products fp32 holds to a rounding each, the same
+    here and there: rows' scales of 12 bits, so that products by e4m3 values often lie at a tie of e4m3 or an fp32 step
+    beside it.  Returns the arguments and h in fp32."""
+    F = 256
+    sa = (1 + torch.randint(0, 1 << 11, (T, 1), generator=gen(seed)) / (1 << 11)).float()
+    a, wg, wu = torch.zeros(T, 16), torch.zeros(F, 16), torch.zeros(F, 16)
+    a[:, 0] = wg[:, 0] = 1
+    v = torch.arange(8, 16) * 2.0 ** torch.randint(-9, 3, (F // 8, 1), generator=gen(seed + 1))
+    v[:, ::2] *= -1
+    wu[:, 0] = v.flatten()
+    wu[0::128, 0], wu[5, 0] = torch.tensor([64.0, 56.0]), 0
+    one = torch.ones(2, 1)
+    h = (64 * sa) * (wu[:, 0] * sa)
+    return [t.cuda() for t in (a.to(fc.E4M3), sa, wg.to(fc.E4M3), 64 * one, wu.to(fc.E4M3), one)], h
+
+
+@pytest.mark.parametrize("T,times", [(8, 100), (3000, 1)])
+def test_the_gate_quantises_as_the_quantiser(T, times):
+    for seed in range(times):
+        args, h = _gate_exact(T, 10 * seed)
+        q, scale = binding.ida_glu_e4m3(*args)
+        want, wscale = binding.ida_quant_e4m3(h.cuda())
+        assert torch.equal(scale, wscale)
+        assert torch.equal(_bits(q), _bits(want)), int((_bits(q) != _bits(want)).sum())
