@@ -167,9 +167,10 @@ __global__ void __launch_bounds__(skinny_warps(E8) * 32, E8 ? 1 : 2) skinny_kern
             const long long at = tok * a.N + n0 + c;
             const float h = x * sigmoid<__nv_bfloat16>(x) * y;
             const long long part = (long long)a.T * a.N;
-            const __nv_bfloat16 hi = __float2bfloat16_rn(h);
-            static_cast<__nv_bfloat16 *>(a.out)[at] = hi;
-            static_cast<__nv_bfloat16 *>(a.out)[at + part] = __float2bfloat16_rn(h - __bfloat162float(hi));
+            // (the first part towards zero where the nearest is not finite)
+            const __nv_bfloat16 hi = __float2bfloat16_rn(h), first = fabsf(h) < 0x1.FFp127f ? hi : __float2bfloat16_rz(h);
+            static_cast<__nv_bfloat16 *>(a.out)[at] = first;
+            static_cast<__nv_bfloat16 *>(a.out)[at + part] = __float2bfloat16_rn(h - __bfloat162float(first));
             if (a.acts) {
                 static_cast<__nv_bfloat16 *>(a.acts)[at] = __float2bfloat16_rn(x);
                 static_cast<__nv_bfloat16 *>(a.acts)[at + part] = __float2bfloat16_rn(y);

@@ -45,3 +45,22 @@ def test_weights_written_just_before_a_call(T, dtype, captured):
     assert binding.ida_device_error() == 0
     for out, w in zip(outs, want):
         assert torch.equal(out, w)
+
+
+@pytest.mark.parametrize("T", [1, 3, 8])
+def test_a_product_beyond_bf16(T):
+    """h = g u between the largest bf16 number and the largest fp32 one, in a call of few rows, which keeps it in two parts."""
+    x, w, wd = torch.zeros(T, 16), torch.zeros(2, 24, 16), torch.zeros(16, 24)
+    x[:, 0] = 1
+    w[0, :, 0], w[1, :, 0], wd[:] = 181 * 2.0 ** 56, 181 * 2.0 ** 57, 2.0 ** -70
+    w[1, 1::2, 0] *= -0.5
+    args = [t.bfloat16().cuda() for t in (x, *w, wd)]
+    out, acts = binding.ida_ffn(*args, acts=True)
+    g, u = (x.double() @ t.double().t() for t in w)
+    h = g * u
+    assert float(h.abs().max()) < torch.finfo(torch.float32).max and not bool(torch.isfinite(h.bfloat16()).all())
+    want = h @ wd.double().t()
+    # two parts leave 2^-16 of each product; the output is rounded
+    bound = 2.0 ** -15 * (h.abs() @ wd.double().abs().t()) + 2.0 ** -8 * want.abs()
+    assert bool(((out.cpu().double() - want).abs() <= bound).all())
+    assert torch.equal(acts[2].cpu(), h.bfloat16())
