@@ -373,11 +373,12 @@ __device__ __forceinline__ void epi_gate(const GemmArgs &g, const EpiWarp &w, co
     store_box<E>(w.staging, g.out[0], g.M[0], g.N[0], row, col, w.lane);
 }
 
-// d/dg and d/du of silu(g) u, given the product's gradient
+// d/dg and d/du of silu(g) u, given the product's gradient (u times the slope first, which is 1.1 at most: dh u may pass
+// fp32 where the slope is 0)
 template <typename E>
 __device__ __forceinline__ void gate_grads(float dh, float &gate, float &up) {
     const float s = sigmoid<E>(gate), gs = gate * s;
-    const float dg = dh * up * (s + gs * (1.f - s));
+    const float dg = dh * (up * (s + gs * (1.f - s)));
     up = dh * gs;
     gate = dg;
 }
