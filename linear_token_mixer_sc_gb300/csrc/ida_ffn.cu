@@ -192,13 +192,22 @@ static ida_status run_gemm(int a_mn, int b_mn, int epi, GemmArgs &g, int dtype, 
     return dtype == IDA_BF16 ? gemm_bf16(a_mn, b_mn, epi, g, num_sms, st) : gemm_f32(a_mn, b_mn, epi, g, num_sms, st);
 }
 
+// Rows of which a call takes no more
+static bool too_many_rows(int rows, int D, int F) { return rows > (1 << 28) || (long long)rows * (D > F ? D : F) > (1LL << 36); }
+
+// Sizes for which a workspace is wanted
+static bool valid_sizes(int rows, int D, int F, int dtype) {
+    return rows > 0 && D > 0 && F > 0 && D <= 65536 && F <= 65536 && D % 8 == 0 && F % 8 == 0 && !too_many_rows(rows, D, F) &&
+           (dtype == IDA_F32 || dtype == IDA_BF16);
+}
+
 static ida_status check_ffn(int rows, int D, int F, long long ldx, int dtype) {
     if (rows < 0) return fail_with(IDA_ERR_ARG, "rows must be >= 0");
     if (D < 1 || F < 1) return fail_with(IDA_ERR_ARG, "D and F must be >= 1");
     if (dtype != IDA_F32 && dtype != IDA_BF16) return fail_with(IDA_ERR_ARG, "dtype must be IDA_F32 or IDA_BF16");
     if (D > 65536 || F > 65536 || (D % 8) || (F % 8))
         return fail_with(IDA_ERR_UNSUPPORTED, "supported: D and F multiples of 8 up to 65536");
-    if (rows > (1 << 28) || (long long)rows * (D > F ? D : F) > (1LL << 36))
+    if (too_many_rows(rows, D, F))
         return fail_with(IDA_ERR_UNSUPPORTED, "rows above 2^28, or rows times D or F above 2^36");
     if (rows > 1 && ldx < D) return fail_with(IDA_ERR_ARG, "ldx must be at least D");
     if (rows > 1 && ((ldx % 8) || ldx > (1LL << 32))) return fail_with(IDA_ERR_UNSUPPORTED, "ldx must be a multiple of 8 up to 2^32");
@@ -210,13 +219,11 @@ static ida_status check_ffn(int rows, int D, int F, long long ldx, int dtype) {
 extern "C" {
 
 size_t ida_ffn_workspace_bytes(int rows, int D, int F, int dtype, int keep) {
-    if (rows < 1 || D < 8 || F < 8 || D > 65536 || F > 65536 || (D % 8) || (F % 8) || (dtype != IDA_F32 && dtype != IDA_BF16)) return 0;
-    return ida::ffn_space(rows, D, F, dtype, false, keep != 0).total;
+    return ida::valid_sizes(rows, D, F, dtype) ? ida::ffn_space(rows, D, F, dtype, false, keep != 0).total : 0;
 }
 
 size_t ida_ffn_backward_workspace_bytes(int rows, int D, int F, int dtype) {
-    if (rows < 1 || D < 8 || F < 8 || D > 65536 || F > 65536 || (D % 8) || (F % 8) || (dtype != IDA_F32 && dtype != IDA_BF16)) return 0;
-    return ida::ffn_space(rows, D, F, dtype, true, true).total;
+    return ida::valid_sizes(rows, D, F, dtype) ? ida::ffn_space(rows, D, F, dtype, true, true).total : 0;
 }
 
 ida_status ida_ffn(const void *x, const void *w_gate, const void *w_up, const void *w_down, void *out, void *acts, int rows, int D,
