@@ -517,7 +517,7 @@ IDA_API size_t ida_rmsnorm_backward_workspace_bytes(int rows, int D);
  * Sums are fp32; those of tensor cores are cut off towards zero by up to 2^-23 every 16 elements, over at most 4096
  * elements (over a row's D channels for g, u and, backwards, dh with IDA_BF16).  With IDA_BF16 h is rounded to bf16
  * between the products (not of up to 8 rows); with IDA_F32 the operands of the products are taken apart into three
- * bf16 parts each, whose products above 2^-24 of the whole are all taken.  Non-finite inputs make the rows of out that they reach (all of them for a weight) unspecified.
+ * bf16 parts each (exactly from 2^-110 on, to 2^-134 below), whose products above 2^-24 of the whole are all taken.  Non-finite inputs make the rows of out that they reach (all of them for a weight) unspecified.
  * Outputs (the workspace among them) that share bytes with inputs or with one another are refused.
  */
 IDA_API ida_status ida_ffn(const void *x, const void *w_gate, const void *w_up, const void *w_down, void *out,
@@ -564,7 +564,8 @@ IDA_API ida_status ida_quant_e4m3(const void *x, void *q, float *scale, int rows
  * out = A B^T, [rows, N] dtype dense, of A (a [rows, K] and the scales of activations) and B (b [N, K]
  * and the scales of weights).  N a multiple of 8 up to 65536.  Products are exact and summed in fp32: within a
  * block by the tensor cores, over blocks with their scales in registers.  Values and scales that are not finite make
- * the rows of out (of b: the columns; of ida_glu_e4m3's weights: the groups) that they reach unspecified.
+ * the rows of out (of b: the columns; of ida_glu_e4m3's weights: the groups) that they reach unspecified; so does a
+ * row's scale times a block's that passes fp32.  (Below 2^-126 that product has the bits that fp32 has left there.)
  */
 IDA_API ida_status ida_gemm_e4m3(const void *a, const float *a_scale, const void *b, const float *b_scale, void *out,
                          int rows, int K, int N, int dtype, ida_stream_t stream);

@@ -10,7 +10,7 @@
 // Forwards two products: the first one's tile holds 128 columns of g and the same 128 of u, and its epilogue
 // makes h of them.  Backwards three: dh's epilogue reads g and u and writes dg and du, dx is one product
 // over both halves of its contraction, and the three weights' gradients are one launch.
-// fp32 operands are taken apart into three bf16 parts (x = a + b + c exactly), whose six products down
+// fp32 operands are taken apart into three bf16 parts (x = a + b + c, exactly from 2^-110 on), whose six products down
 // to 2^-16 make up fp32's; h, dg and du are rounded to bf16 between the products otherwise.
 #include <mutex>
 

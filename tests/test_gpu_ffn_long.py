@@ -83,3 +83,25 @@ def test_fp32_gradients_of_few_channels_share_their_rows():
     end.record()
     torch.cuda.synchronize()
     assert start.elapsed_time(end) <= 8
+
+
+@pytest.mark.parametrize("dtype,T,D,F", [("f32", 20003, 72, 136), ("bf16", 70001, 40, 72)])
+def test_captured_and_on_another_stream(dtype, T, D, F):
+    args, _ = _case(T, D, F, dtype)
+    want = {k: t.clone() for k, t in binding.ida_ffn_backward(*args).items()}
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        got = binding.ida_ffn_backward(*args)
+    side.synchronize()
+    assert all(torch.equal(got[k], w) for k, w in want.items())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = binding.ida_ffn_backward(*args)
+        again = binding.ida_ffn_backward(*args)
+    for _ in range(3):
+        for t in (*got.values(), *again.values()):
+            t.fill_(float("nan"))
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(got[k], w) and torch.equal(again[k], w) for k, w in want.items())
