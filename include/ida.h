@@ -517,7 +517,8 @@ IDA_API size_t ida_rmsnorm_backward_workspace_bytes(int rows, int D);
  * Sums are fp32; those of tensor cores are cut off towards zero by up to 2^-23 every 16 elements, over at most 4096
  * elements (over a row's D channels for g, u and, backwards, dh with IDA_BF16).  With IDA_BF16 h is rounded to bf16
  * between the products (not of up to 8 rows); with IDA_F32 the operands of the products are taken apart into three
- * bf16 parts each (exactly from 2^-110 on, to 2^-134 below), whose products above 2^-24 of the whole are all taken.  Non-finite inputs make the rows of out that they reach (all of them for a weight) unspecified.
+ * bf16 parts each (exactly from 2^-110 on, to 2^-134 below), whose products above 2^-24 of the whole are all taken.
+ * Non-finite inputs make the rows of out that they reach (all of them for a weight) unspecified.
  * Outputs (the workspace among them) that share bytes with inputs or with one another are refused.
  */
 IDA_API ida_status ida_ffn(const void *x, const void *w_gate, const void *w_up, const void *w_down, void *out,
@@ -535,7 +536,7 @@ IDA_API size_t ida_ffn_workspace_bytes(int rows, int D, int F, int dtype, int ke
  *   dh = dout Wd,  du = dh g s,  dg = dh u s (1 + g (1 - s)),
  *   dx = dg Wg + du Wu,  dWg = dg^T x,  dWu = du^T x,  dWd = dout^T h.
  * With IDA_BF16 dg and du are rounded to bf16 between the products.  The workspace is required when rows > 0.
- * Sums run in a fixed order: deterministic.
+ * Sums run in a fixed order: deterministic.  Non-finite inputs make what they reach unspecified.
  */
 IDA_API ida_status ida_ffn_backward(const void *x, const void *w_gate, const void *w_up, const void *w_down,
                             const void *acts, const void *dout, void *dx, void *dw_gate, void *dw_up,

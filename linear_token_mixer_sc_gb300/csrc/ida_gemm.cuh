@@ -373,8 +373,8 @@ __device__ __forceinline__ void epi_gate(const GemmArgs &g, const EpiWarp &w, co
     store_box<E>(w.staging, g.out[0], g.M[0], g.N[0], row, col, w.lane);
 }
 
-// d/dg and d/du of silu(g) u, given the product's gradient (u times the slope first, which is 1.1 at most: dh u may pass
-// fp32 where the slope is 0)
+// d/dg and d/du of silu(g) u, given the product's gradient (u times the slope first, which is 1.1 at most: dh u may
+// pass fp32 where the slope is 0)
 template <typename E>
 __device__ __forceinline__ void gate_grads(float dh, float &gate, float &up) {
     const float s = sigmoid<E>(gate), gs = gate * s;
@@ -442,7 +442,8 @@ struct GateBwd {
     }
 };
 
-// The other kinds: a thread's 128 sums of its row, in registers: half of the tile's columns, or (kGate) 64 of either factor.
+// The other kinds: a thread's 128 sums of its row, in registers: half of the tile's columns, or (kGate) 64 of either
+// factor.
 template <int EPI>
 __device__ __forceinline__ int sum_col(const EpiWarp &w, int c) {  // TMEM column of sums 16 c ..
     return EPI == kGate ? w.half * 64 + c / 4 * 128 + c % 4 * 16 : w.half * 128 + c * 16;
@@ -525,7 +526,8 @@ __device__ __forceinline__ bool epi_sums(const GemmArgs &g, const EpiWarp &w, co
 // bits above 2^-138; smaller ones are multiplied by 2^120 first, and the values with them, exactly.  All of it is negated
 // until the values are in 8 bits: then a zero keeps its sign.  Two at a time.  (With divisions the quantiser of 4099
 // rows of 5632 channels took 21 us, now 13.3, with four groups a thread instead of one.  By the reciprocal alone
-// 14336 rows' gated projection would take 244 us, now 249, but of 768000 values made to lie at ties 8864 went the other way.)
+// 14336 rows' gated projection would take 244 us, now 249, but of 768000 values made to lie at ties 8864 went the
+// other way.)
 struct Quotient {
     float up, d, nr;
     __device__ __forceinline__ explicit Quotient(float sc) {

@@ -6,15 +6,15 @@
 namespace ida {
 
 // Rows up to which a call takes them: the columns of one matrix instruction.  With 2048 and 5632 channels, in us, here
-// and on tcgen05: the block in bf16 of 8 rows 19 and 29 (of 16 rows, by two instructions, 29 and 29); in e4m3 the product
-// back of 8 rows 4.4 and 10, the gate 9.1 and 12 (of 16 rows 15 and 12: the instruction in 8 bits is put together
-// from others on this part).  In fp32, here and by ida_ffn_simt.cu: the block of one row 22 and 117, of 16 rows
-// 147 and 118.
+// and on tcgen05: the block in bf16 of 8 rows 18.9 and 29 (of 16 rows, by two instructions, 29 and 28); in e4m3 the
+// product back of 8 rows 4.7 and 11, the gate 10.7 and 12 (of 16 rows 15 and 12: the instruction in 8 bits is put
+// together from others on this part).  In fp32, here and by ida_ffn_simt.cu: the block of one row 23.5 and 117, of
+// 16 rows 147 and 118.
 constexpr int kFewRows = 8;
 enum { kFewBf16 = 0, kFewE4M3 = 1, kFewF32 = 2 };
 
 struct SkinnyArgs {
-    const void *x;                  // T rows of K channels, ldx elements apart (for a bf16 product two such, its block's h in two parts)
+    const void *x;                  // T rows of K channels, ldx elements apart (of a bf16 product two such: h in two parts)
     long long ldx;
     const void *w0, *w1;            // [N, K]; w1: the gate's other factor
     void *out;                      // [T, N]: a product in bf16 or fp32, the gate's in two parts of bf16, fp32 or e4m3
