@@ -28,7 +28,7 @@ def test_the_quantiser_keeps_signs(block_rows, dtype):
     assert torch.equal(scale.cpu(), wscale) and torch.equal(_bits(q), _bits(want))
 
 
-def _gate_exact(T, seed):
+def _gate_exact(T, seed, size=1.0):
     """Operands whose gates are 64 and more (their sigmoid is 1) and whose products fp32 holds to a rounding each, the same
     here and there: rows' scales of 12 bits, so that products by e4m3 values often lie at a tie of e4m3 or an fp32 step
     beside it.  Returns the arguments and h in fp32."""
@@ -41,8 +41,8 @@ def _gate_exact(T, seed):
     wu[:, 0] = v.flatten()
     wu[0::128, 0], wu[5, 0] = torch.tensor([64.0, 56.0]), 0
     one = torch.ones(2, 1)
-    h = (64 * sa) * (wu[:, 0] * sa)
-    return [t.cuda() for t in (a.to(fc.E4M3), sa, wg.to(fc.E4M3), 64 * one, wu.to(fc.E4M3), one)], h
+    h = (64 * sa) * (wu[:, 0] * (sa * size))
+    return [t.cuda() for t in (a.to(fc.E4M3), sa, wg.to(fc.E4M3), 64 * one, wu.to(fc.E4M3), size * one)], h
 
 
 @pytest.mark.parametrize("T,times", [(8, 100), (3000, 1)])
@@ -53,3 +53,14 @@ def test_the_gate_quantises_as_the_quantiser(T, times):
         want, wscale = binding.ida_quant_e4m3(h.cuda())
         assert torch.equal(scale, wscale)
         assert torch.equal(_bits(q), _bits(want)), int((_bits(q) != _bits(want)).sum())
+
+
+@pytest.mark.parametrize("T", [8, 3000])
+@pytest.mark.parametrize("size", [2.0 ** -100, 2.0 ** -138, 2.0 ** 100])
+def test_the_gate_quantises_products_of_any_size(T, size):
+    """Scales down to subnormal ones: every factor is a rounding of fp32's, here and there."""
+    args, h = _gate_exact(T, 5, size)
+    q, scale = binding.ida_glu_e4m3(*args)
+    want, wscale = binding.ida_quant_e4m3(h.cuda())
+    assert torch.equal(scale, wscale) and bool((scale > 0).all())
+    assert torch.equal(_bits(q), _bits(want))
